@@ -226,6 +226,65 @@ dfa_status dfa_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
                                float scale, void* dQ, void* dK, void* dV, void* workspace,
                                size_t ws_bytes, void* stream);
 
+/* Causal attention with a sliding window of TOKENS and a few first tokens that
+ * stay visible (sinks): a query at position i sees key j iff
+ *   j <= i  and  (j > i - window  or  j < n_sink),
+ * so every query sees itself, window >= S is plain causal attention, and
+ * n_sink = 0 the bare window.  (The local window above moves in whole chunks
+ * and keeps no first tokens.)  Softmax, lse, GQA and layouts as dfa_attn_fwd;
+ * keys outside a query tile's window are neither loaded nor computed.
+ *   window:    >= 1 tokens;  n_sink: 0 .. 128 tokens (more: UNSUPPORTED)
+ * bf16 only (DFA_ERR_UNSUPPORTED for fp32), D in {64, 128}; tensors must be
+ * finite (a NaN or infinity in K or V reaches queries that do not see it).
+ * The forward takes no workspace and is one kernel launch; the backward is
+ * three launches.  Both may be captured in a CUDA graph; two graphs or calls
+ * that can overlap need a backward workspace each.
+ * Reproducibility: O, lse, dK and dV are the same bits on every call; dQ adds
+ * fp32 partials with atomics, as dfa_attn_bwd.
+ * Errors: INVALID_ARG for bad sizes or pointers, WORKSPACE for a workspace
+ * that is missing or too small; nothing is launched then. */
+dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
+                             int S, int D, int window, int n_sink, float scale, void* O, float* lse,
+                             void* stream);
+/* Bytes of workspace the backward needs (0 for sizes it does not take). */
+size_t dfa_attn_bwd_sink_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);
+/* Its backward from the saved O and lse, never re-running the forward:
+ * P_ij = exp(s_ij - lse_i) on the visible pairs, Delta_i = <dO_i, O_i>, and
+ * dQ, dK, dV as dfa_attn_bwd.  workspace: caller-owned, 16-byte aligned. */
+dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const void* O, const float* lse,
+                             const void* dO, dfa_dtype dt, int B, int H, int H_kv, int S, int D, int window,
+                             int n_sink, float scale, void* dQ, void* dK, void* dV, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* 8-bit attention checkpoint: what a layer keeps for its backward besides lse
+ * (DISTFLASHATTN §3.3 keeps the attention's output so that the forward runs
+ * once) in half the memory.  Each group of 32 consecutive elements of the head
+ * dimension shares an exponent e = max(floor(log2 max|x|) - 6, -120); an
+ * element is held as the integer m nearest to x / 2^e (ties to even, |m| <=
+ * 127) and stands for m 2^e, which is a bf16 number.  A group that holds an
+ * infinity or NaN stands for NaN.  1 + 1/32 bytes per element.
+ *   q, O: [B, S, H, D], k, v: [B, S, H_kv, D] dense, bf16 (fp32: UNSUPPORTED)
+ *   ckpt: caller-owned buffer of dfa_ckpt8_size() bytes, 16-byte aligned; its
+ *         layout is the library's own
+ * save and restore are one kernel launch each and may be captured. */
+size_t dfa_ckpt8_size(int B, int H, int H_kv, int S, int D);
+dfa_status dfa_ckpt8_save(const void* q, const void* k, const void* v, const void* O, dfa_dtype dt, int B, int H,
+                          int H_kv, int S, int D, void* ckpt, size_t ckpt_bytes, void* stream);
+dfa_status dfa_ckpt8_restore(const void* ckpt, size_t ckpt_bytes, dfa_dtype dt, int B, int H, int H_kv, int S, int D,
+                             void* q, void* k, void* v, void* O, void* stream);
+
+/* Backward from an 8-bit checkpoint and the saved lse: dfa_attn_bwd_sink on
+ * the values the checkpoint stands for, with the same window and n_sink as
+ * the forward (window >= S, n_sink = 0: plain causal attention, the backward
+ * of dfa_attn_fwd).  lse is the forward's, of the tensors before they were
+ * rounded, so P_ij = exp(s_ij - lse_i) carries the rounding of q and k.
+ * Arguments, errors and reproducibility as dfa_attn_bwd_sink; the workspace
+ * also holds the restored q, k and v for the length of the call. */
+size_t dfa_attn_bwd_ckpt8_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);
+dfa_status dfa_attn_bwd_ckpt8(const void* ckpt, size_t ckpt_bytes, const float* lse, const void* dO, dfa_dtype dt,
+                              int B, int H, int H_kv, int S, int D, int window, int n_sink, float scale, void* dQ,
+                              void* dK, void* dV, void* workspace, size_t ws_bytes, void* stream);
+
 /* dfa_attn_fwd for callers that cannot allocate device memory.  The paper
  * has no counterpart to this entry point.  Some callers cannot call
  * cudaMalloc where they run attention: a plugin whose host framework owns

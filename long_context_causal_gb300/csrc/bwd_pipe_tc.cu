@@ -44,7 +44,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -95,6 +97,9 @@ struct Args {
     const int32_t* wl_items;
     int n_units;
     int n_split, piece_tiles;     // split-kv pieces of each key tile's query range (SPLIT)
+    int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
+    int n_items, n_pieces;        // ... items, of which the first n_pieces * rows are pieces of key tile 0
+    float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
     int* err;
     uint64_t* trace;
     int trace_cap;
@@ -111,6 +116,7 @@ struct Args {
 struct Item {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head; ntiles over the group's heads
     bool down;                      // sweep query tiles from the last one down
+    int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
     // k-th tile of the item: head h of the group, query tile i
     __device__ __forceinline__ void tile(int k, int G, int& h, int& i) const {
         const int len = i1 - i0, r = k % len;
@@ -119,14 +125,43 @@ struct Item {
     }
 };
 
+// SINK: a sliding window of tokens with sinks (n_split unused; no work list).
+// Costs fall along the items -- the pieces of key tile 0, which the sinks make
+// visible to every query, then the key tiles upwards, which see the window's
+// worth of query tiles until the sequence ends -- and the CTAs take them in a
+// snake.  A piece stores its partial dK, dV to a slab of its own, summed in
+// order afterwards, so dK and dV have the same bits on every call.
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a
 // separate instantiation in which the sequence base is 0 and the lengths are
 // the problem's, so it keeps its registers for the tile loop.
-template <bool VARLEN, bool SPLIT>
+template <bool VARLEN, bool SPLIT, bool SINK>
 __device__ __forceinline__ Item decode(const Args& a, int it) {
     Item x;
+    x.slab = -1;
+    if constexpr (SINK) {
+        const int rows = a.B * a.Hkv;
+        x.n_q = a.n_units;
+        if (a.n_pieces > 1 && it < a.n_pieces * rows) {
+            x.slab = it;
+            x.t = 0;
+            x.i0 = it / rows * a.piece_tiles;
+            x.i1 = min(x.i0 + a.piece_tiles, x.n_q);
+        } else {
+            if (a.n_pieces > 1) it -= (a.n_pieces - 1) * rows;   // key tile 0 is done in pieces
+            x.t = it / rows;
+            x.i0 = x.t;
+            // the last query that sees the tile's last key: its position + window - 1
+            x.i1 = x.t == 0 && a.n_sink > 0 ? x.n_q : min((x.t * BT + BT - 1 + a.window - 1) / BT + 1, x.n_q);
+        }
+        const int row = it % rows;
+        x.b = row / a.Hkv;
+        x.g = row % a.Hkv;
+        x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
+        x.down = false;
+        return x;
+    }
     int piece = 0;
     if constexpr (SPLIT) {
         piece = it % a.n_split;
@@ -167,13 +202,15 @@ __device__ __forceinline__ Item decode(const Args& a, int it) {
 // small, cache-resident sequence table where a value is used instead of
 // holding it in registers across the tile loop (the warps here run at the
 // register limit, and a few more live values cost about a tenth of the speed).
+// Value of the CTA's it-th item.
+#define ITEM(it) (SINK ? snake_item(it, blockIdx.x, gridDim.x) : a.wl_items[it])
 #define SEQ_LQ(x) (VARLEN ? a.seq[(x).b + 1] - a.seq[(x).b] : a.Lq)
 #define SEQ_LKV(x) (VARLEN ? a.seq[(x).b + 1] - a.seq[(x).b] : a.Lkv)
 #define SEQ_BASE(x) (VARLEN ? a.seq[(x).b] : 0)
 #define SEQ_PBASE(x) (VARLEN ? a.seq[a.B + 1 + (x).b] : 0)
 #define SEQ_TB(x) (VARLEN ? 0 : (x).b)
 
-template <bool VARLEN, bool SPLIT>
+template <bool VARLEN, bool SPLIT, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const Args a) {
@@ -208,7 +245,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int it_begin = a.wl_offsets[blockIdx.x], it_end = a.wl_offsets[blockIdx.x + 1];
+    const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
+    const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
 
     if (threadIdx.x == 0) {
@@ -261,7 +299,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT>(a, a.wl_items[it]);
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
@@ -364,7 +402,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT>(a, a.wl_items[it]);
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             if (!wait(kv_full, kvi & 1, 0)) break;
             if (!issue_S(n) || !issue_dP(n)) break;
@@ -437,15 +475,24 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT>(a, a.wl_items[it]);
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             const int kvg = x.t * BT + r;
             const bool row_ok = kvg < SEQ_LKV(x);
             // local window: this key is seen by queries below q_hi (chunk-relative);
             // q_hi_tile is the lowest such bound over the tile's keys
-            const int64_t q_hi = a.win_w > 0 ? ((a.kv_off + kvg) / a.win_c + a.win_w) * a.win_c - a.q_off : INT64_MAX;
-            const int64_t q_hi_tile =
-                a.win_w > 0 ? ((a.kv_off + (int64_t)x.t * BT) / a.win_c + a.win_w) * a.win_c - a.q_off : INT64_MAX;
+            // (SINK: by queries below key + window, a sink by all of them)
+            using Pos = std::conditional_t<SINK, int, int64_t>;
+            Pos q_hi, q_hi_tile;
+            if constexpr (SINK) {
+                const int first = x.t == 0 ? a.n_sink : x.t * BT;   // the tile's first key that is no sink
+                q_hi = kvg < a.n_sink ? INT32_MAX : kvg + a.window;
+                q_hi_tile = first >= (x.t + 1) * BT ? INT32_MAX : first + a.window;
+            } else {
+                q_hi = a.win_w > 0 ? ((a.kv_off + kvg) / a.win_c + a.win_w) * a.win_c - a.q_off : INT64_MAX;
+                q_hi_tile =
+                    a.win_w > 0 ? ((a.kv_off + (int64_t)x.t * BT) / a.win_c + a.win_w) * a.win_c - a.q_off : INT64_MAX;
+            }
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int h, i;
                 x.tile(k, G, h, i);
@@ -459,7 +506,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 // Elements outside the causal triangle or the sequence only occur on
                 // the diagonal tile and on ragged edges; elsewhere no mask is applied.
                 const bool full = !(a.causal && i == x.t + a.rel / BT) && (i + 1) * BT <= SEQ_LQ(x) &&
-                                  (int64_t)(i + 1) * BT <= q_hi_tile &&
+                                  (Pos)(i + 1) * BT <= q_hi_tile &&
                                   (x.t + 1) * BT <= SEQ_LKV(x);
                 // ---- phase 1: P^T = exp2(S^T c + nlse2) -> TMEM (bf16) and registers
                 uint32_t u[32], pk[32];
@@ -525,7 +572,18 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int c = half * 2; c < half * 2 + 2; ++c) {
                 uint32_t uv[32], uk[32];
                 tmem_ld32x2(tmem + lane_base + kColDV + c * 32, tmem + lane_base + kColDK + c * 32, uv, uk);
-                if constexpr (SPLIT) {   // a piece's partial: fp32 reductions, other pieces add to the same rows
+                if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
+                    float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
+                    float4* pv = pkk + BT * D / 4;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        pkk[e] = make_float4(a.scale * __uint_as_float(uk[4 * e]), a.scale * __uint_as_float(uk[4 * e + 1]),
+                                             a.scale * __uint_as_float(uk[4 * e + 2]),
+                                             a.scale * __uint_as_float(uk[4 * e + 3]));
+                        pv[e] = make_float4(__uint_as_float(uv[4 * e]), __uint_as_float(uv[4 * e + 1]),
+                                            __uint_as_float(uv[4 * e + 2]), __uint_as_float(uv[4 * e + 3]));
+                    }
+                } else if constexpr (SPLIT) {   // a piece's partial: fp32 reductions, other pieces add to the same rows
                     if (row_ok) {
                         float* pv = static_cast<float*>(a.dV) + orow + c * 32;
                         float* pkk = static_cast<float*>(a.dK) + orow + c * 32;
@@ -597,7 +655,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         uint64_t wt = 0;
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT>(a, a.wl_items[it]);
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             const int s_pbase = SEQ_PBASE(x), s_len = SEQ_LQ(x);   // once per item
             for (int k = 0; k < x.ntiles; ++k, ++n) {
@@ -642,6 +700,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
 }
 
+#undef ITEM
 #undef SEQ_LQ
 #undef SEQ_LKV
 #undef SEQ_BASE
@@ -682,7 +741,9 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
         return fail(DFA_ERR_INVALID_ARG, "split-kv backward pieces need fp32 dK/dV accumulators");
     a.n_split = wl->n_split;
     a.piece_tiles = wl->piece_tiles;
-    auto kern = p.seq ? bwd_pipe_kernel<true, false> : split ? bwd_pipe_kernel<false, true> : bwd_pipe_kernel<false, false>;
+    auto kern = p.seq ? bwd_pipe_kernel<true, false, false>
+                : split ? bwd_pipe_kernel<false, true, false>
+                        : bwd_pipe_kernel<false, false, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return fail(DFA_ERR_CUDA, "bwd_pipe: shared memory attribute");
     // The setmaxnreg split assumes the launch register count; a different
@@ -694,6 +755,40 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
     kern<<<wl->n_workers, kThreads, kSmem, s>>>(mq, mk, mv, mdo, a);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "bwd_pipe launch: %s", cudaGetErrorString(e));
+}
+
+dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                       const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
+                       void* dK, void* dV, cudaStream_t s) {
+    if (p.D != D) return tc_sink_bwd_d64(p, plan, q, k, v, dO, nlse2, delta, S_pad, dq_acc, slabs, dK, dV, s);
+    alignas(64) CUtensorMap mq, mk, mv, mdo;
+    const int64_t qh = (int64_t)p.H * D, kh = (int64_t)p.Hkv * D;
+    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
+        !make_tmap_bshd(&mdo, dO, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.S * kh, kh, D) ||
+        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, p.S * kh, kh, D))
+        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+    Args a{};
+    a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.Lq = a.Lkv = p.S; a.S_pad = S_pad; a.causal = 1;
+    a.acc_rows = p.S;
+    a.scale = p.scale; a.c2 = p.scale * 1.4426950408889634f;
+    a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
+    a.dK = dK; a.dV = dV;
+    a.n_units = plan.n_q;
+    a.window = p.window; a.n_sink = p.n_sink;
+    a.n_items = (int)plan.n_items; a.n_pieces = plan.n_pieces; a.piece_tiles = plan.piece_len;
+    a.slabs = slabs;
+    a.err = device_error_flag();
+    auto kern = bwd_pipe_kernel<false, false, true>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != (int)kLaunchRegs)
+        return fail(DFA_ERR_CUDA, "sink backward: built with %d registers per thread, the register split needs %u",
+                    fa.numRegs, kLaunchRegs);
+    kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, kSmem, s>>>(mq, mk, mv, mdo, a);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace dfa

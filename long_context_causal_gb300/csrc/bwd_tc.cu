@@ -34,7 +34,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -77,6 +79,9 @@ struct BwdArgs {
     const int32_t* wl_offsets;
     const int32_t* wl_items;
     int n_units;                  // key tiles per (batch, kv head)
+    int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
+    int n_items, n_pieces, piece_tiles;   // ... items, of which the first n_pieces * rows are pieces of key tile 0
+    float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
     int* err;
     uint64_t* trace;              // optional per-CTA timeline (nullptr: off)
     int trace_cap;
@@ -93,6 +98,7 @@ struct BwdArgs {
 struct BItem {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head
     bool down;                      // sweep query tiles from the last one down
+    int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
     int base, pbase, len;           // packed batch: first token, first padded row, tokens of the sequence
     // k-th tile of the item: head hh of the group (0..G-1), query tile i
     __device__ __forceinline__ void tile(int k, int& hh, int& i) const {
@@ -104,9 +110,34 @@ struct BItem {
 
 // VARLEN: a packed batch (a.seq set), compiled as its own instantiation so
 // the dense kernel reads its lengths straight from the parameters.
-template <bool VARLEN>
+// SINK: a sliding window of tokens with sinks; items, pieces and their slabs
+// as in bwd_pipe_tc.cu.
+template <bool VARLEN, bool SINK>
 __device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
     BItem x;
+    x.slab = -1;
+    if constexpr (SINK) {
+        const int rows = a.B * a.Hkv;
+        x.n_q = a.n_units;
+        if (a.n_pieces > 1 && it < a.n_pieces * rows) {
+            x.slab = it;
+            x.t = 0;
+            x.i0 = it / rows * a.piece_tiles;
+            x.i1 = min(x.i0 + a.piece_tiles, x.n_q);
+        } else {
+            if (a.n_pieces > 1) it -= (a.n_pieces - 1) * rows;   // key tile 0 is done in pieces
+            x.t = it / rows;
+            x.i0 = x.t;
+            // the last query that sees the tile's last key: its position + window - 1
+            x.i1 = x.t == 0 && a.n_sink > 0 ? x.n_q : min((x.t * BT + BT - 1 + a.window - 1) / BT + 1, x.n_q);
+        }
+        const int row = it % rows;
+        x.b = row / a.Hkv;
+        x.g = row % a.Hkv;
+        x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
+        x.down = false;
+        return x;
+    }
     const int row = it / a.n_units, unit = it % a.n_units;
     x.b = row / a.Hkv;
     x.g = row % a.Hkv;
@@ -134,12 +165,14 @@ __device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
 }
 
 // Sequence geometry of item x (see bdecode).
+// Value of the CTA's it-th item.
+#define ITEM(it) (SINK ? snake_item(it, blockIdx.x, gridDim.x) : a.wl_items[it])
 #define SEQ_LEN(x) (VARLEN ? (x).len : a.S)
 #define SEQ_BASE(x) (VARLEN ? (x).base : 0)
 #define SEQ_PBASE(x) (VARLEN ? (x).pbase : 0)
 #define SEQ_TB(x) (VARLEN ? 0 : (x).b)
 
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -175,7 +208,8 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 21);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int it_begin = a.wl_offsets[blockIdx.x], it_end = a.wl_offsets[blockIdx.x + 1];
+    const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
+    const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
 
     if (threadIdx.x == 0) {
@@ -223,7 +257,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
+            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
             if (lane == 0) {
@@ -306,7 +340,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             __syncwarp();
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
+            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
             if (!wait(kv_full, kvi & 1, 3)) break;
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 const uint32_t s = n & 1, ph = (n >> 1) & 1;
@@ -387,10 +421,13 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
+            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
             const int kvg = x.t * BT + r;                   // global key index of this thread's row
             const bool row_ok = kvg < SEQ_LEN(x);
-            const int64_t q_hi = a.win_w > 0 ? ((int64_t)kvg / a.win_c + a.win_w) * a.win_c : INT64_MAX;
+            using Pos = std::conditional_t<SINK, int, int64_t>;
+            Pos q_hi;   // queries below it see the key (SINK: a sink is seen by all of them)
+            if constexpr (SINK) q_hi = kvg < a.n_sink ? INT32_MAX : kvg + a.window;
+            else q_hi = a.win_w > 0 ? ((int64_t)kvg / a.win_c + a.win_w) * a.win_c : INT64_MAX;
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
                 x.tile(k, hh, i);
@@ -446,7 +483,18 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 uint32_t uv[32], uk[32];
                 tmem_ld32(tmem + lane_base + kColDV + c * 32, uv);
                 tmem_ld32(tmem + lane_base + kColDK + c * 32, uk);
-                if (row_ok) {
+                if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
+                    float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
+                    float4* pv = pkk + BT * D / 4;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        pkk[e] = make_float4(a.scale * __uint_as_float(uk[4 * e]), a.scale * __uint_as_float(uk[4 * e + 1]),
+                                             a.scale * __uint_as_float(uk[4 * e + 2]),
+                                             a.scale * __uint_as_float(uk[4 * e + 3]));
+                        pv[e] = make_float4(__uint_as_float(uv[4 * e]), __uint_as_float(uv[4 * e + 1]),
+                                            __uint_as_float(uv[4 * e + 2]), __uint_as_float(uv[4 * e + 3]));
+                    }
+                } else if (row_ok) {
                     uint4* pv = reinterpret_cast<uint4*>(a.dV + orow + c * 32);
                     uint4* pkk = reinterpret_cast<uint4*>(a.dK + orow + c * 32);
 #pragma unroll
@@ -484,7 +532,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         uint64_t wt = 0;
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
+            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
                 x.tile(k, hh, i);
@@ -535,6 +583,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     if (threadIdx.x == 0) trace_cta(a.trace, a.trace_cap, t_start, it_end - it_begin);
 }
 
+#undef ITEM
 #undef SEQ_LEN
 #undef SEQ_BASE
 #undef SEQ_PBASE
@@ -563,7 +612,7 @@ dfa_status launch(const AttnProblem& p, const void* q, const void* k, const void
     a.wl_offsets = wl->offsets; a.wl_items = wl->items; a.n_units = wl->n_units;
     a.err = device_error_flag();
     a.trace = cta_trace(&a.trace_cap);
-    auto kern = p.seq ? bwd_tc_kernel<D, true> : bwd_tc_kernel<D, false>;
+    auto kern = p.seq ? bwd_tc_kernel<D, true, false> : bwd_tc_kernel<D, false, false>;
     const int smem = BCfg<D>::kSmem;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return fail(DFA_ERR_CUDA, "bwd_tc: shared memory attribute");
@@ -581,6 +630,38 @@ dfa_status tc_bwd(const AttnProblem& p, const void* q, const void* k, const void
     // Head dim 128 takes the two-stream pipelined kernel (bwd_pipe_tc.cu).
     if (p.D == 128) return tc_bwd_pipelined(p, q, k, v, dO, nlse2, delta, S_pad, dq_acc, dK, dV, false, wl, s);
     return launch<64>(p, q, k, v, dO, nlse2, delta, S_pad, dq_acc, dK, dV, wl, s);
+}
+
+dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                           const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc,
+                           float* slabs, void* dK, void* dV, cudaStream_t s) {
+    constexpr int D = 64;
+    alignas(64) CUtensorMap mq, mk, mv, mdo;
+    const int64_t qh = (int64_t)p.H * D, kh = (int64_t)p.Hkv * D;
+    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
+        !make_tmap_bshd(&mdo, dO, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.S * kh, kh, D) ||
+        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, p.S * kh, kh, D))
+        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+    BwdArgs a{};
+    a.acc_rows = p.S;
+    a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.S = p.S; a.S_pad = S_pad; a.causal = 1;
+    a.scale = p.scale; a.c2 = p.scale * 1.4426950408889634f;
+    a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
+    a.dK = static_cast<__nv_bfloat16*>(dK);
+    a.dV = static_cast<__nv_bfloat16*>(dV);
+    a.n_units = plan.n_q;
+    a.window = p.window; a.n_sink = p.n_sink;
+    a.n_items = (int)plan.n_items; a.n_pieces = plan.n_pieces; a.piece_tiles = plan.piece_len;
+    a.slabs = slabs;
+    a.err = device_error_flag();
+    auto kern = bwd_tc_kernel<D, false, true>;
+    const int smem = BCfg<D>::kSmem;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
+    kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, smem, s>>>(mq, mk, mv, mdo, a);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace dfa

@@ -3,6 +3,7 @@
 // No exception crosses this boundary and no device memory is allocated here.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -832,6 +833,185 @@ extern "C" dfa_status dfa_attn_bwd_varlen(const void* q, const void* k, const vo
     st = launch_convert_varlen(n_seq, H, L.T, L.P, D, scale, seq, dq_acc, dQ, s);
     if (st == DFA_OK) count_launch(DFA_KERNEL_CONVERT);
     return st;
+}
+
+// ---------------------------------------------------------------- sliding window of tokens with sinks
+namespace {
+
+struct SinkWs {
+    size_t delta = 0, nlse2 = 0, dq = 0, slabs = 0, qkv[3] = {0, 0, 0}, total = 0;
+    int S_pad = 0;
+};
+
+// Sizes a call is made for; a message and a status for those it is not.
+dfa_status check_sink(dfa_dtype dt, int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale) {
+    dfa_status st;
+    if ((st = check_dtype(dt)) || (st = check_common(B, H, Hkv, D, scale))) return st;
+    if (dt != DFA_BF16) return fail(DFA_ERR_UNSUPPORTED, "windowed attention with sinks takes bf16 tensors only");
+    if (S < 0) return fail(DFA_ERR_INVALID_ARG, "negative sequence length");
+    if (window < 1) return fail(DFA_ERR_INVALID_ARG, "window must be at least one token (got %d)", window);
+    if (n_sink < 0) return fail(DFA_ERR_INVALID_ARG, "n_sink must be >= 0 (got %d)", n_sink);
+    if (n_sink > kMaxSinks)
+        return fail(DFA_ERR_UNSUPPORTED, "n_sink=%d: at most %d tokens can stay visible", n_sink, kMaxSinks);
+    // item counts, tile positions and grid sizes are 32-bit
+    if ((int64_t)B * H > (1 << 24) || (int64_t)B * H * ((S + 127) / 128 + 64) > (1 << 30) || S > (1 << 30))
+        return fail(DFA_ERR_INVALID_ARG, "problem too large (B*H=%lld heads of %d tokens)", (long long)B * H, S);
+    return DFA_OK;
+}
+
+SinkProblem sink_problem(int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale) {
+    SinkProblem p{B, H, Hkv, S, D, std::min(window, S), n_sink, scale};
+    if (p.window >= S) p.n_sink = 0;
+    return p;
+}
+
+SinkWs sink_ws(const SinkProblem& p, bool ckpt) {
+    SinkWs w;
+    const SinkBwdPlan plan = sink_bwd_plan(p);
+    const size_t rows = (size_t)p.B * p.H;
+    size_t off = 0;
+    w.S_pad = (p.S + 127) / 128 * 128;
+    w.delta = off;
+    off = align_up(off + sizeof(float) * rows * w.S_pad);
+    w.nlse2 = off;
+    off = align_up(off + sizeof(float) * rows * w.S_pad);
+    w.dq = off;
+    off = align_up(off + sizeof(float) * rows * p.S * p.D);
+    w.slabs = off;
+    if (plan.n_pieces > 1)
+        off = align_up(off + sizeof(float) * (size_t)plan.n_pieces * p.B * p.Hkv * 2 * 128 * p.D);
+    for (int i = 0; i < 3 && ckpt; ++i) {
+        w.qkv[i] = off;
+        off = align_up(off + 2 * (size_t)p.B * p.S * (i ? p.Hkv : p.H) * p.D);
+    }
+    w.total = off;
+    return w;
+}
+
+// The backward's three launches; ckpt: q, k, v and O come from an 8-bit checkpoint.
+dfa_status sink_bwd(const SinkProblem& p, const void* q, const void* k, const void* v, const void* O, const float* lse,
+                    const void* dO, const void* ckpt, void* dQ, void* dK, void* dV, char* ws, cudaStream_t s) {
+    const SinkWs w = sink_ws(p, ckpt != nullptr);
+    const SinkBwdPlan plan = sink_bwd_plan(p);
+    float* delta = reinterpret_cast<float*>(ws + w.delta);
+    float* nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
+    float* dq = reinterpret_cast<float*>(ws + w.dq);
+    float* slabs = reinterpret_cast<float*>(ws + w.slabs);
+    const Ckpt8Layout L = ckpt8_layout(p.B, p.H, p.Hkv, p.S, p.D);
+    void* qkv[3] = {ws + w.qkv[0], ws + w.qkv[1], ws + w.qkv[2]};
+    dfa_status st;
+    if ((st = launch_sink_prep(p, w.S_pad, O, dO, lse, nlse2, delta, dq, ckpt, &L, qkv, s))) return st;
+    count_launch(DFA_KERNEL_DELTA);
+    if (ckpt) q = qkv[0], k = qkv[1], v = qkv[2];
+    if ((st = tc_sink_bwd(p, plan, q, k, v, dO, nlse2, delta, w.S_pad, dq, slabs, dK, dV, s))) return st;
+    count_launch(DFA_KERNEL_BWD);
+    st = launch_sink_finish(p, plan, dq, slabs, dQ, dK, dV, s);
+    if (st == DFA_OK) count_launch(DFA_KERNEL_CONVERT);
+    return st;
+}
+
+dfa_status check_ws(void* ws, size_t have, size_t need) {
+    if (!ws || have < need) return fail(DFA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
+    if (!aligned16(ws)) return fail(DFA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    return DFA_OK;
+}
+
+bool sink_sizes_ok(int B, int H, int Hkv, int S, int D, int window, int n_sink) {
+    const std::string keep = g_msg;   // a size query does not change dfa_last_error()
+    const bool ok = check_sink(DFA_BF16, B, H, Hkv, S, D, window, n_sink, 1.f) == DFA_OK;
+    snprintf(g_msg, sizeof(g_msg), "%s", keep.c_str());
+    return ok;
+}
+
+}  // namespace
+
+extern "C" dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H,
+                                        int H_kv, int S, int D, int window, int n_sink, float scale, void* O,
+                                        float* lse, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
+    if (st || (int64_t)B * S == 0) return st;
+    if ((st = check_ptrs({q, k, v, O, lse}))) return st;
+    st = tc_sink_fwd(sink_problem(B, H, H_kv, S, D, window, n_sink, scale), q, k, v, O, lse,
+                     static_cast<cudaStream_t>(stream));
+    if (st == DFA_OK) count_launch(DFA_KERNEL_FWD);
+    return st;
+}
+
+extern "C" size_t dfa_attn_bwd_sink_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink) {
+    if (!sink_sizes_ok(B, H, H_kv, S, D, window, n_sink)) return 0;
+    return sink_ws(sink_problem(B, H, H_kv, S, D, window, n_sink, 1.f), false).total;
+}
+
+extern "C" dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const void* O, const float* lse,
+                                        const void* dO, dfa_dtype dt, int B, int H, int H_kv, int S, int D,
+                                        int window, int n_sink, float scale, void* dQ, void* dK, void* dV,
+                                        void* workspace, size_t ws_bytes, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
+    if (st || (int64_t)B * S == 0) return st;
+    const SinkProblem p = sink_problem(B, H, H_kv, S, D, window, n_sink, scale);
+    if ((st = check_ws(workspace, ws_bytes, sink_ws(p, false).total))) return st;
+    if ((st = check_ptrs({q, k, v, O, lse, dO, dQ, dK, dV}))) return st;
+    return sink_bwd(p, q, k, v, O, lse, dO, nullptr, dQ, dK, dV, static_cast<char*>(workspace),
+                    static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- 8-bit attention checkpoints
+static dfa_status check_ckpt(dfa_dtype dt, int B, int H, int H_kv, int S, int D, const void* ckpt, size_t have) {
+    dfa_status st = check_sink(dt, B, H, H_kv, S, D, 1, 0, 1.f);
+    if (st || (int64_t)B * S == 0) return st;
+    const size_t need = ckpt8_layout(B, H, H_kv, S, D).total;
+    if (!ckpt || have < need) return fail(DFA_ERR_INVALID_ARG, "checkpoint of %zu bytes needed, %zu given", need, have);
+    if (!aligned16(ckpt)) return fail(DFA_ERR_INVALID_ARG, "checkpoint is not 16-byte aligned");
+    return DFA_OK;
+}
+
+extern "C" size_t dfa_ckpt8_size(int B, int H, int H_kv, int S, int D) {
+    return sink_sizes_ok(B, H, H_kv, S, D, 1, 0) ? ckpt8_layout(B, H, H_kv, S, D).total : 0;
+}
+
+extern "C" dfa_status dfa_ckpt8_save(const void* q, const void* k, const void* v, const void* O, dfa_dtype dt, int B,
+                                     int H, int H_kv, int S, int D, void* ckpt, size_t ckpt_bytes, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_ckpt(dt, B, H, H_kv, S, D, ckpt, ckpt_bytes);
+    if (st || (int64_t)B * S == 0) return st;
+    if ((st = check_ptrs({q, k, v, O}))) return st;
+    const void* src[4] = {q, k, v, O};
+    st = launch_ckpt8_save(ckpt8_layout(B, H, H_kv, S, D), src, ckpt, static_cast<cudaStream_t>(stream));
+    if (st == DFA_OK) count_launch(DFA_KERNEL_CONVERT);
+    return st;
+}
+
+extern "C" dfa_status dfa_ckpt8_restore(const void* ckpt, size_t ckpt_bytes, dfa_dtype dt, int B, int H, int H_kv,
+                                        int S, int D, void* q, void* k, void* v, void* O, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_ckpt(dt, B, H, H_kv, S, D, ckpt, ckpt_bytes);
+    if (st || (int64_t)B * S == 0) return st;
+    if ((st = check_ptrs({q, k, v, O}))) return st;
+    void* dst[4] = {q, k, v, O};
+    st = launch_ckpt8_restore(ckpt8_layout(B, H, H_kv, S, D), ckpt, dst, static_cast<cudaStream_t>(stream));
+    if (st == DFA_OK) count_launch(DFA_KERNEL_CONVERT);
+    return st;
+}
+
+extern "C" size_t dfa_attn_bwd_ckpt8_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink) {
+    if (!sink_sizes_ok(B, H, H_kv, S, D, window, n_sink)) return 0;
+    return sink_ws(sink_problem(B, H, H_kv, S, D, window, n_sink, 1.f), true).total;
+}
+
+extern "C" dfa_status dfa_attn_bwd_ckpt8(const void* ckpt, size_t ckpt_bytes, const float* lse, const void* dO,
+                                         dfa_dtype dt, int B, int H, int H_kv, int S, int D, int window, int n_sink,
+                                         float scale, void* dQ, void* dK, void* dV, void* workspace, size_t ws_bytes,
+                                         void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
+    if (st || (st = check_ckpt(dt, B, H, H_kv, S, D, ckpt, ckpt_bytes)) || (int64_t)B * S == 0) return st;
+    const SinkProblem p = sink_problem(B, H, H_kv, S, D, window, n_sink, scale);
+    if ((st = check_ws(workspace, ws_bytes, sink_ws(p, true).total))) return st;
+    if ((st = check_ptrs({lse, dO, dQ, dK, dV}))) return st;
+    return sink_bwd(p, nullptr, nullptr, nullptr, nullptr, lse, dO, ckpt, dQ, dK, dV, static_cast<char*>(workspace),
+                    static_cast<cudaStream_t>(stream));
 }
 
 extern "C" void dfa_shutdown(void) {

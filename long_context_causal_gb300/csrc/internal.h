@@ -112,6 +112,66 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
                             float* dq_acc, void* dK, void* dV, bool acc_f32, const WorkList* wl,
                             cudaStream_t s);
 
+// ---- sliding window of tokens with sinks, bf16 (sink_*.cu, bwd_*.cu) ----
+// Row i sees key j iff j <= i and (j > i - window or j < n_sink).  Dense
+// layouts; window is clamped to S, and n_sink is 0 where the window covers
+// every key (sink_problem()).
+struct SinkProblem {
+    int B, H, Hkv, S, D;
+    int window, n_sink;
+    float scale;
+};
+constexpr int kMaxSinks = 128;   // one key tile
+// Backward plan: key tile 0 is seen by every query when there are sinks.  Its
+// query range is then cut into n_pieces pieces of piece_len 128-row query
+// tiles; with more than one, piece p of (batch, kv head) row r writes its
+// partial dK and dV to slab p * rows + r, and the sum of the slabs is key
+// tile 0's gradient (a fixed order, so dK and dV keep their bits).
+struct SinkBwdPlan {
+    int n_q, piece_len, n_pieces;
+    int64_t n_items;
+};
+SinkBwdPlan sink_bwd_plan(const SinkProblem& p);
+
+dfa_status tc_sink_fwd(const SinkProblem& p, const void* q, const void* k, const void* v, void* O, float* lse,
+                       cudaStream_t s);
+// nlse2 and delta as for tc_bwd; dq_acc fp32 [B, H, S, D], zero; slabs fp32
+// [n_pieces * B * Hkv][2][128][D] (dK with scale applied, dV).
+dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                       const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
+                       void* dK, void* dV, cudaStream_t s);
+dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                           const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc,
+                           float* slabs, void* dK, void* dV, cudaStream_t s);
+
+// 8-bit checkpoint sections, in bytes from the start of the buffer: int8
+// payloads of q, k, v, O and their exponent bytes (one for 32 elements).
+struct Ckpt8Layout {
+    size_t data[4], exps[4], total;
+    int64_t n[4];                // elements
+};
+Ckpt8Layout ckpt8_layout(int B, int H, int Hkv, int S, int D);
+dfa_status launch_ckpt8_save(const Ckpt8Layout& L, const void* const src[4], void* ckpt, cudaStream_t s);
+dfa_status launch_ckpt8_restore(const Ckpt8Layout& L, const void* ckpt, void* const dst[4], cudaStream_t s);
+// Before the main backward kernel: nlse2 and Delta [B, H, S_pad] (zero in the
+// padding) and the zeroed dQ accumulator.  With ckpt (an 8-bit checkpoint), O
+// comes from it and its q, k, v are written as bf16 to `qkv`.
+dfa_status launch_sink_prep(const SinkProblem& p, int S_pad, const void* O, const void* dO, const float* lse,
+                            float* nlse2, float* delta, float* dq_acc, const void* ckpt, const Ckpt8Layout* L,
+                            void* const qkv[3], cudaStream_t s);
+// After it: dQ [B, S, H, D] = bf16(scale * dq_acc) and key tile 0's dK, dV
+// from the slabs (plan.n_pieces > 1).
+dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, const float* dq_acc, const float* slabs,
+                              void* dQ, void* dK, void* dV, cudaStream_t s);
+
+// Dealing of items sorted by falling cost to `n` persistent CTAs in a snake
+// (0..n-1, then n-1..0, ...): the k-th item of CTA `cta`, and how many it has.
+__host__ __device__ inline int snake_item(int k, int cta, int n) { return k * n + ((k & 1) ? n - 1 - cta : cta); }
+__host__ __device__ inline int snake_count(int n_items, int cta, int n) {
+    const int full = n_items / n, pos = (full & 1) ? n - 1 - cta : cta;
+    return full + (pos < n_items % n);
+}
+
 int num_sms();
 
 // A sequence of S tokens cut into n_chunks chunks (DISTFLASHATTN §3.1: one

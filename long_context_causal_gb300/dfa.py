@@ -72,6 +72,16 @@ def _load() -> ctypes.CDLL:
         "dfa_attn_fwd_varlen": (i32, [vp, vp, vp, i32, p32, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp]),
         "dfa_attn_bwd_varlen": (i32, [vp, vp, vp, vp, vp, vp, i32, p32, i32, i32, i32, i32, i32, f32,
                                       vp, vp, vp, vp, sz, vp]),
+        "dfa_attn_fwd_sink": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
+        "dfa_attn_bwd_sink_workspace_size": (sz, [i32] * 7),
+        "dfa_attn_bwd_sink": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                    vp, vp, vp, vp, sz, vp]),
+        "dfa_ckpt8_size": (sz, [i32] * 5),
+        "dfa_ckpt8_save": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz, vp]),
+        "dfa_ckpt8_restore": (i32, [vp, sz, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "dfa_attn_bwd_ckpt8_workspace_size": (sz, [i32] * 7),
+        "dfa_attn_bwd_ckpt8": (i32, [vp, sz, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                     vp, vp, vp, vp, sz, vp]),
         "dfa_build_split_worklist": (i64, [i32, i32, i32, i32, i32, i32, p32, p32]),
         "dfa_debug_mma": (i32, [i32, vp, vp, vp, vp]),
         "dfa_debug_cta_trace": (i32, [vp, i32]),
@@ -414,6 +424,146 @@ def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: f
     _check(_lib.dfa_attn_bwd_local(_ptr(q), _ptr(k), _ptr(v), _ptr(O), _ptr(lse), _ptr(dO), _dtype(q),
                                    B, H, Hkv, S, D, int(n_chunks), int(window), scale, _SCHED[sched],
                                    _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
+    return dQ, dK, dV
+
+
+# -------------------------------------------- sliding window of tokens with sinks, 8-bit checkpoints
+def _on_gpu(q, *named):
+    """Every tensor must lie on the current CUDA device: the library launches
+    there, on the pointers it is given."""
+    for t, name in named:
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others, got {t.device}")
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _sizes(q, k, v):
+    """B, S, H, H_kv, D of dense q [B,S,H,D] and k, v [B,S,H_kv,D]."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError(f"q must be [B, S, H, D] and k, v [B, S, H_kv, D], got {tuple(q.shape)}, {tuple(k.shape)}, "
+                         f"{tuple(v.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have the same dtype")
+    B, S, H, D = q.shape
+    return B, S, H, k.shape[2], D
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace for one call, owned by the stream the call runs on: the
+    allocator then reuses it only behind the call's kernels."""
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def _bytes_buf(t, name, device):
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor on {device}")
+    return t
+
+
+def dfa_attn_fwd_sink(q, k, v, window: int, n_sink: int = 0, scale: float | None = None, O=None, lse=None,
+                      stream=None):
+    """Causal forward over a sliding window of `window` tokens and the first
+    `n_sink` ones: returns (O [B,S,H,D], lse fp32 [B,H,S])."""
+    B, S, H, Hkv, D = _sizes(q, k, v)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _dense(t, n)
+    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
+    O = torch.empty_like(q) if O is None else _like(O, "O", q.shape, q.dtype, q.device)
+    lse = (torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None
+           else _like(lse, "lse", (B, H, S), torch.float32, q.device))
+    _check(_lib.dfa_attn_fwd_sink(_ptr(q), _ptr(k), _ptr(v), _dtype(q), B, H, Hkv, S, D, int(window), int(n_sink),
+                                  D ** -0.5 if scale is None else float(scale), _ptr(O), _ptr(lse), _stream(stream)))
+    return O, lse
+
+
+def dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
+    return int(_lib.dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, int(window), int(n_sink)))
+
+
+def _grads(q_shape, k_shape, dtype, device, dQ, dK, dV):
+    out = []
+    for t, name, shape in ((dQ, "dQ", q_shape), (dK, "dK", k_shape), (dV, "dV", k_shape)):
+        out.append(torch.empty(shape, dtype=dtype, device=device) if t is None else _like(t, name, shape, dtype, device))
+    return out
+
+
+def dfa_attn_bwd_sink(q, k, v, O, lse, dO, window: int, n_sink: int = 0, scale: float | None = None, dQ=None,
+                      dK=None, dV=None, workspace_buf=None, stream=None):
+    """Backward of dfa_attn_fwd_sink from the saved (O, lse): returns (dQ, dK, dV)."""
+    B, S, H, Hkv, D = _sizes(q, k, v)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _dense(t, n)
+    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
+    _like(O, "O", q.shape, q.dtype, q.device)
+    _like(dO, "dO", q.shape, q.dtype, q.device)
+    _like(lse, "lse", (B, H, S), torch.float32, q.device)
+    dQ, dK, dV = _grads(q.shape, k.shape, q.dtype, q.device, dQ, dK, dV)
+    ws = (_scratch(dfa_attn_bwd_sink_workspace_size(B, H, Hkv, S, D, window, n_sink), q.device, stream)
+          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", q.device))
+    _check(_lib.dfa_attn_bwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(O), _ptr(lse), _ptr(dO), _dtype(q), B, H, Hkv, S, D,
+                                  int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), _ptr(dQ),
+                                  _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
+    return dQ, dK, dV
+
+
+def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:
+    return int(_lib.dfa_ckpt8_size(B, H, H_kv, S, D))
+
+
+def dfa_ckpt8_save(q, k, v, O, ckpt=None, stream=None):
+    """q, k, v and O of one attention layer in 8 bits: returns the checkpoint
+    (a uint8 tensor of dfa_ckpt8_size bytes)."""
+    B, S, H, Hkv, D = _sizes(q, k, v)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _dense(t, n)
+    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
+    _like(O, "O", q.shape, q.dtype, q.device)
+    ckpt = (torch.empty(dfa_ckpt8_size(B, H, Hkv, S, D), dtype=torch.uint8, device=q.device) if ckpt is None
+            else _bytes_buf(ckpt, "ckpt", q.device))
+    _check(_lib.dfa_ckpt8_save(_ptr(q), _ptr(k), _ptr(v), _ptr(O), _dtype(q), B, H, Hkv, S, D, _ptr(ckpt), ckpt.numel(),
+                               _stream(stream)))
+    return ckpt
+
+
+def dfa_ckpt8_restore(ckpt, B: int, H: int, H_kv: int, S: int, D: int, q=None, k=None, v=None, O=None, stream=None):
+    """The bf16 tensors (q, k, v, O) a checkpoint stands for."""
+    _bytes_buf(ckpt, "ckpt", ckpt.device)
+    _on_gpu(ckpt, (ckpt, "ckpt"))
+    out = []
+    for t, name, heads in ((q, "q", H), (k, "k", H_kv), (v, "v", H_kv), (O, "O", H)):
+        shape = (B, S, heads, D)
+        out.append(torch.empty(shape, dtype=torch.bfloat16, device=ckpt.device) if t is None
+                   else _like(t, name, shape, torch.bfloat16, ckpt.device))
+    _check(_lib.dfa_ckpt8_restore(_ptr(ckpt), ckpt.numel(), DFA_BF16, B, H, H_kv, S, D, *(_ptr(t) for t in out),
+                                  _stream(stream)))
+    return tuple(out)
+
+
+def dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
+    return int(_lib.dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, int(window), int(n_sink)))
+
+
+def dfa_attn_bwd_ckpt8(ckpt, lse, dO, H_kv: int, window: int | None = None, n_sink: int = 0,
+                       scale: float | None = None, dQ=None, dK=None, dV=None, workspace_buf=None, stream=None):
+    """Backward from an 8-bit checkpoint, the saved lse and dO [B,S,H,D], with
+    the forward's window (None: plain causal): returns (dQ, dK, dV)."""
+    B, S, H, D = dO.shape
+    _dense(dO, "dO")
+    _on_gpu(dO, (dO, "dO"), (ckpt, "ckpt"))
+    _bytes_buf(ckpt, "ckpt", dO.device)
+    _like(lse, "lse", (B, H, S), torch.float32, dO.device)
+    window = max(S, 1) if window is None else int(window)
+    dQ, dK, dV = _grads(dO.shape, (B, S, H_kv, D), dO.dtype, dO.device, dQ, dK, dV)
+    ws = (_scratch(dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink), dO.device, stream)
+          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", dO.device))
+    _check(_lib.dfa_attn_bwd_ckpt8(_ptr(ckpt), ckpt.numel(), _ptr(lse), _ptr(dO), _dtype(dO), B, H, H_kv, S, D, window,
+                                   int(n_sink), D ** -0.5 if scale is None else float(scale), _ptr(dQ), _ptr(dK),
+                                   _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
     return dQ, dK, dV
 
 

@@ -1,0 +1,295 @@
+"""Windowed attention with sinks and the 8-bit checkpoints on the GPU, against
+the fp64 reference (oracle/sink.py).
+
+Tolerances are sums over the terms of each element.  With u = 2^-8, half a
+step of bf16 relative to the value:
+  O    the probabilities are rounded once (u times the sum of P |v|) and the
+       result once (u |O|);
+  dV   likewise (P and the result);
+  dQ, dK  P and dS are rounded (2 u times the sum of |dS| |k| or |dS| |q|),
+       the result once;
+and fp32 sums of up to D = 128 products move a score by less than 2^-13 and
+dO.v - Delta by less than 2^-16 of the magnitudes it is the difference of.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_causal_gb300 import dfa
+from long_context_causal_gb300.inputs import make
+from oracle import sink
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U, F, F2 = 2.0 ** -8, 2.0 ** -12, 2.0 ** -16
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, ref, tol, what):
+    bad = ~(np.abs(np64(got) - ref) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, first at {np.argwhere(bad)[0]}, worst {np.nanmax(np.abs(np64(got) - ref) / (tol + 1e-30)):.3g} of the tolerance"
+
+
+def check_fwd(O, lse, q, k, v, window, n_sink, scale=None):
+    Or, lr, size = sink.attn_fwd(np64(q), np64(k), np64(v), window, n_sink, scale)
+    close(O, Or, (U + F) * size + U * np.abs(Or), "O")
+    close(lse, lr, 2 * F, "lse")
+
+
+def check_bwd(grads, q, k, v, O, lse, do, window, n_sink, scale=None):
+    ref = sink.attn_bwd(*(np64(t) for t in (q, k, v, O, lse, do)), window, n_sink, scale)
+    for got, name in zip(grads, ("dQ", "dK", "dV")):
+        r, terms, cancel = ref[name]
+        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + U * np.abs(r) + 1e-30, name)
+
+
+# (B, H, Hkv, S, D, window, n_sink)
+CASES = [
+    (1, 1, 1, 1, 128, 1, 0), (2, 2, 1, 1, 64, 5, 3),
+    (1, 2, 1, 2, 128, 1, 1), (1, 2, 2, 127, 128, 16, 2), (1, 2, 2, 128, 64, 128, 128),
+    (2, 4, 2, 129, 64, 32, 1), (1, 4, 1, 255, 128, 100, 0), (1, 3, 3, 256, 128, 128, 16),
+    (2, 2, 1, 257, 128, 129, 17), (1, 8, 2, 300, 64, 1, 4), (1, 2, 2, 385, 128, 127, 128),
+    (1, 2, 1, 640, 128, 256, 33), (1, 6, 2, 1000, 128, 200, 8), (1, 2, 2, 1000, 64, 1000, 4),
+    (1, 2, 1, 1500, 128, 2000, 0), (3, 2, 2, 513, 64, 130, 127),
+    (1, 4, 2, 2500, 128, 100, 4), (1, 2, 1, 4200, 64, 257, 128), (1, 2, 2, 3100, 128, 1, 1),
+]
+IDS = ["B{}H{}kv{}S{}D{}w{}s{}".format(*c) for c in CASES]
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward(case):
+    B, H, Hkv, S, D, window, n_sink = case
+    q, k, v, _ = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=31)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dfa.dfa_check_errors()
+    check_fwd(O, lse, q, k, v, window, n_sink)
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_backward(case):
+    B, H, Hkv, S, D, window, n_sink = case
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=32)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    grads = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink)
+    dfa.dfa_check_errors()
+    check_bwd(grads, q, k, v, O, lse, do, window, n_sink)
+
+
+def test_sharp_scores_rescale():
+    """Maxima that rise by more than 2^8 along the keys, and sinks above all of them."""
+    q, k, v, do = make(1, 2, 1, 900, 128, torch.bfloat16, device=DEV, seed=33, k_scale=4.0)
+    k[:, :4] *= 3
+    k[:, 400:] *= 2
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, 300, 4, scale=0.2)
+    grads = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, 300, 4, scale=0.2)
+    dfa.dfa_check_errors()
+    # scores reach 200: fp32 moves them by 2^-24 * 200 * a few, far below F
+    check_fwd(O, lse, q, k, v, 300, 4, 0.2)
+    check_bwd(grads, q, k, v, O, lse, do, 300, 4, 0.2)
+
+
+def test_window_over_every_key_is_the_causal_call():
+    q, k, v, do = make(2, 4, 2, 700, 128, torch.bfloat16, device=DEV, seed=34)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, 700, 9)
+    O2, lse2 = dfa.dfa_attn_fwd(q, k, v)
+    torch.testing.assert_close(O.float(), O2.float(), rtol=2 * U, atol=1e-4)
+    torch.testing.assert_close(lse, lse2, rtol=0, atol=1e-5)
+    for a, b in zip(dfa.dfa_attn_bwd_sink(q, k, v, O2, lse2, do, 1 << 30), dfa.dfa_attn_bwd(q, k, v, O2, lse2, do)):
+        err = (a.float() - b.float()).norm() / b.float().norm()
+        assert err <= 3 * U, err     # each side rounds P, dS and the result; far from their worst at once
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_bits_repeat_and_neighbours_stay(D):
+    """O, lse, dK, dV have the same bits on every call, and nothing is written
+    outside the outputs (sequences of a batch end inside a tile)."""
+    B, H, Hkv, S, W, N = 3, 4, 2, 1337, 90, 5
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=35)
+    def framed(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 8192,), 7.0, dtype=dtype, device=DEV)
+        return buf, buf[4096:4096 + n].view(shape)
+    runs = []
+    for _ in range(3):
+        bufs = [framed(q.shape, q.dtype), framed((B, H, S), torch.float32)]
+        dfa.dfa_attn_fwd_sink(q, k, v, W, N, O=bufs[0][1], lse=bufs[1][1])
+        bufs += [framed(q.shape, q.dtype), framed(k.shape, q.dtype), framed(k.shape, q.dtype)]
+        nb = dfa.dfa_attn_bwd_sink_workspace_size(B, H, Hkv, S, D, W, N)
+        ws = torch.full((nb + 4096,), 0xAB, dtype=torch.uint8, device=DEV)   # dirty, with a frame behind
+        dfa.dfa_attn_bwd_sink(q, k, v, bufs[0][1], bufs[1][1], do, W, N, dQ=bufs[2][1], dK=bufs[3][1], dV=bufs[4][1],
+                              workspace_buf=ws[:nb])
+        assert (ws[nb:] == 0xAB).all()
+        for buf, t in bufs:
+            n = t.numel()
+            assert (buf[:4096] == 7).all() and (buf[4096 + n:] == 7).all()
+        runs.append([t.clone() for _, t in bufs])
+    dfa.dfa_check_errors()
+    for r in runs[1:]:
+        for z in (0, 1, 3, 4):
+            assert torch.equal(r[z], runs[0][z])
+        torch.testing.assert_close(r[2].float(), runs[0][2].float(), rtol=2 * U, atol=1e-3)
+
+
+# ------------------------------------------------------------------------------------------------ checkpoints
+@pytest.mark.parametrize("B,H,Hkv,S,D", [(1, 1, 1, 1, 64), (1, 3, 1, 1, 128), (2, 4, 2, 129, 128), (1, 8, 8, 501, 64),
+                                         (3, 6, 3, 77, 128)])
+def test_checkpoint_holds_the_definitions_values(B, H, Hkv, S, D):
+    q, k, v, o = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=41)
+    q *= 10.0 ** torch.randint(-20, 20, (B, S, H, 1), device=DEV, generator=torch.Generator(DEV).manual_seed(1)).float()
+    k[:, 0, 0, :32] = 0
+    v[:, S // 2, 0, 32:40] = 2.0 ** -126       # beside larger elements, and alone with the smallest exponent
+    v[:, -1, -1, 32:] = 2.0 ** -124
+    o[:, 0, 0, 3] = -3.3e38
+    ckpt = dfa.dfa_ckpt8_save(q, k, v, o)
+    assert ckpt.numel() == dfa.dfa_ckpt8_size(B, H, Hkv, S, D)
+    for got, t, name in zip(dfa.dfa_ckpt8_restore(ckpt, B, H, Hkv, S, D), (q, k, v, o), "qkvO"):
+        assert got.dtype == torch.bfloat16 and np.array_equal(np64(got), sink.ckpt8(np64(t))), name
+
+
+def test_checkpoint_of_non_finite_groups():
+    q, k, v, o = make(1, 2, 1, 40, 64, torch.bfloat16, device=DEV, seed=42)
+    q[0, 3, 1, 40], k[0, 5, 0, 0], o[0, 39, 1, 63] = float("inf"), float("nan"), float("-inf")
+    back = dfa.dfa_ckpt8_restore(dfa.dfa_ckpt8_save(q, k, v, o), 1, 2, 1, 40, 64)
+    for got, t in zip(back, (q, k, v, o)):
+        assert np.array_equal(np64(got), sink.ckpt8(np64(t)), equal_nan=True)
+    assert sum(int(t.isnan().sum()) for t in back) == 96
+
+
+def test_checkpoint_stays_inside_its_buffer():
+    B, H, Hkv, S, D = 1, 3, 1, 33, 64
+    q, k, v, o = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=43)
+    n = dfa.dfa_ckpt8_size(B, H, Hkv, S, D)
+    buf = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    a = dfa.dfa_ckpt8_save(q, k, v, o, ckpt=buf[256:256 + n])
+    assert (buf[:256] == 0x5A).all() and (buf[256 + n:] == 0x5A).all()
+    b = dfa.dfa_ckpt8_save(q, k, v, o)
+    for x, y in zip(dfa.dfa_ckpt8_restore(a, B, H, Hkv, S, D), dfa.dfa_ckpt8_restore(b, B, H, Hkv, S, D)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("case", [c for c in CASES if c[3] in (1, 129, 257, 300, 640, 1000, 1500, 2500, 3100)],
+                         ids=lambda c: "B{}H{}kv{}S{}D{}w{}s{}".format(*c))
+def test_backward_from_a_checkpoint(case):
+    """The training step: forward, save, and the backward from what was saved."""
+    B, H, Hkv, S, D, window, n_sink = case
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=44)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    ckpt = dfa.dfa_ckpt8_save(q, k, v, O)
+    held = [torch.from_numpy(sink.ckpt8(np64(t))).to(DEV) for t in (q, k, v, O)]
+    del q, k, v, O
+    n_fwd = dfa.dfa_launch_count("fwd")
+    grads = dfa.dfa_attn_bwd_ckpt8(ckpt, lse, do, Hkv, window, n_sink)
+    dfa.dfa_check_errors()
+    assert dfa.dfa_launch_count("fwd") == n_fwd
+    check_bwd(grads, *held, lse, do, window, n_sink)
+
+
+def test_causal_backward_from_a_checkpoint():
+    """Without a window it is the backward of dfa_attn_fwd, from rounded tensors."""
+    q, k, v, do = make(1, 4, 1, 770, 128, torch.bfloat16, device=DEV, seed=45)
+    O, lse = dfa.dfa_attn_fwd(q, k, v)
+    grads = dfa.dfa_attn_bwd_ckpt8(dfa.dfa_ckpt8_save(q, k, v, O), lse, do, 1)
+    dfa.dfa_check_errors()
+    held = [sink.ckpt8(np64(t)) for t in (q, k, v, O)]
+    check_bwd(grads, *(torch.from_numpy(t) for t in held), lse, do, 770, 0)
+    # and the checkpoint's own rounding, 2^-7 of a group's largest at most, moves the gradients little
+    for a, b in zip(grads, dfa.dfa_attn_bwd(q, k, v, O, lse, do)):
+        assert (a.float() - b.float()).norm() <= 0.05 * b.float().norm()
+
+
+# ------------------------------------------------------------------------------------------------ streams, graphs
+def step(q, k, v, do, W, N, stream=None):
+    Hkv = k.shape[2]
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, W, N, stream=stream)
+    g = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, W, N, stream=stream)
+    ckpt = dfa.dfa_ckpt8_save(q, k, v, O, stream=stream)
+    h = dfa.dfa_attn_bwd_ckpt8(ckpt, lse, do, Hkv, W, N, stream=stream)
+    return (O, lse) + g + h
+
+
+def same_step(a, b):
+    for z, (x, y) in enumerate(zip(a, b)):
+        if z in (2, 5):      # dQ: fp32 atomics
+            torch.testing.assert_close(x.float(), y.float(), rtol=2 * U, atol=2e-3)
+        else:
+            assert torch.equal(x, y), z
+
+
+def test_captured_and_replayed():
+    W, N = 200, 4
+    q, k, v, do = make(1, 4, 2, 1300, 128, torch.bfloat16, device=DEV, seed=51)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):        # captured without an eager call before it
+        out = step(q, k, v, do, W, N)
+    for seed in (52, 53):
+        for t, n in zip((q, k, v, do), make(1, 4, 2, 1300, 128, torch.bfloat16, device=DEV, seed=seed)):
+            t.copy_(n)
+        g.replay()
+        torch.cuda.synchronize()
+        same_step(out, step(q, k, v, do, W, N))
+    dfa.dfa_check_errors()
+
+
+def test_another_stream_and_two_at_once():
+    W, N = 150, 3
+    sets = [make(1, 4, 2, 1100, D, torch.bfloat16, device=DEV, seed=54 + D) for D in (64, 128)]
+    want = [step(*s, W, N) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [step(*s, W, N, stream=st) for s, st in zip(sets, streams)]
+        for st in streams:
+            st.synchronize()
+        for a, b in zip(got, want):
+            same_step(a, b)
+    got = step(*sets[0], W, N, stream=streams[0].cuda_stream)     # a raw handle
+    streams[0].synchronize()
+    same_step(got, want[0])
+
+
+def test_tensors_on_the_wrong_place_are_refused():
+    q, k, v, do = make(1, 2, 1, 64, 64, torch.bfloat16, device=DEV, seed=57)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfa.dfa_attn_fwd_sink(q, k.cpu(), v, 4)
+    with pytest.raises(dfa.DfaError):
+        dfa.dfa_attn_fwd_sink(q.float(), k.float(), v.float(), 4)
+    with pytest.raises(ValueError, match="O must be"):
+        dfa.dfa_attn_fwd_sink(q, k, v, 4, O=torch.empty(1, 63, 2, 64, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError, match="workspace"):
+        dfa.dfa_attn_bwd_sink(q, k, v, q, torch.zeros(1, 2, 64, device=DEV), do, 4, workspace_buf=torch.zeros(9, device=DEV))
+    empty = dfa.dfa_attn_fwd_sink(q[:, :0], k[:, :0], v[:, :0], 4)
+    assert empty[0].shape == (1, 0, 2, 64) and empty[1].shape == (1, 2, 0)
+
+
+def test_offsets_beyond_32_bits():
+    """512K tokens of 32 heads: 2^31 elements in q, and dQ's fp32 accumulator.
+    Rows of the last head and sequence end against the reference on the slice
+    that they see."""
+    B, H, Hkv, S, D, W, N = 1, 32, 8, 524288 + 77, 128, 300, 4
+    g = torch.Generator(DEV).manual_seed(61)
+    q, k, v, do = (torch.empty(B, S, h, D, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for h in (H, Hkv, Hkv, H))
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, W, N)
+    dQ, dK, dV = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, W, N)
+    ckpt = dfa.dfa_ckpt8_save(q, k, v, O)
+    back = dfa.dfa_ckpt8_restore(ckpt, B, H, Hkv, S, D)
+    dfa.dfa_check_errors()
+    for got, t in zip(back, (q, k, v, O)):
+        assert np.array_equal(np64(got[:, -200:, -1]), sink.ckpt8(np64(t[:, -200:, -1])))
+    G = H // Hkv
+    a = S - 1000                          # keys [a, S) and the sinks, queries from a + W - 1 on see no other
+    idx = torch.cat((torch.arange(N, device=DEV), torch.arange(a, S, device=DEV)))
+    hs, gs = slice(H - G, H), slice(Hkv - 1, Hkv)
+    sub = [np64(t[:, idx][:, :, s]) for t, s in ((q, hs), (k, gs), (v, gs), (O, hs))]
+    sd, sl = np64(do[:, idx][:, :, hs]), np64(lse[:, hs][:, :, idx])
+    # in the slice the keys of the sinks come first and the window is the same
+    Or, lr, size = sink.attn_fwd(*sub[:3], W, N)
+    rows = slice(N + W - 1, None)
+    close(O[:, a + W - 1:, hs], Or[:, rows], ((U + F) * size + U * np.abs(Or))[:, rows], "O")
+    close(lse[:, hs, a + W - 1:], lr[:, :, rows], 2 * F, "lse")
+    ref = sink.attn_bwd(*sub, sl, sd, W, N)
+    for got, name in ((dQ[:, a + W - 1:, hs], "dQ"), (dK[:, a + W - 1:, gs], "dK"), (dV[:, a + W - 1:, gs], "dV")):
+        r, terms, cancel = (t[:, rows] for t in ref[name])
+        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + U * np.abs(r) + 1e-30, name)
