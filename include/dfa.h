@@ -256,6 +256,28 @@ dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const 
                              int n_sink, float scale, void* dQ, void* dK, void* dV, void* workspace,
                              size_t ws_bytes, void* stream);
 
+/* The same attention for one new token of each sequence, over a cache:
+ * sequence b holds n = kv_len[b] tokens, its query stands at position n - 1
+ * (its own key and value are in the cache) and sees key j iff j < n and
+ * (j > n - 1 - window or j < n_sink).
+ *   q, O:    [B, H, D] dense, bf16;  lse: fp32 [B, H]
+ *   k, v:    [B, S_max, H_kv, D] with element strides kv_strides = {batch,
+ *            token, head} (shared; NULL: dense), multiples of 8, D contiguous
+ *   kv_len:  DEVICE int32 [B]; read when the kernels run, so a captured call
+ *            follows the lengths.  0: O = 0, lse = -inf.  Values below 0 count
+ *            as 0, above S_max as S_max.
+ *   workspace: >= dfa_attn_decode_sink_workspace_size() bytes, 16-byte
+ *            aligned, contents not preserved; calls that can overlap need one
+ *            each
+ * Cache rows that the query does not see may hold anything, NaN included.
+ * bf16 only, D in {64, 128}, n_sink <= 128, at most 8192 sequences
+ * (UNSUPPORTED otherwise).  Two launches; the same bits on every call. */
+size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D);
+dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
+                                int S_max, int D, const int64_t* kv_strides, const int32_t* kv_len, int window,
+                                int n_sink, float scale, void* O, float* lse, void* workspace, size_t ws_bytes,
+                                void* stream);
+
 /* 8-bit attention checkpoint: what a layer keeps for its backward besides lse
  * (DISTFLASHATTN §3.3 keeps the attention's output so that the forward runs
  * once) in half the memory.  Each group of 32 consecutive elements of the head

@@ -100,6 +100,8 @@ struct Args {
     int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
     int n_items, n_pieces;        // ... items, of which the first n_pieces * rows are pieces of key tile 0
     float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
+    int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers
+    float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
     uint64_t* trace;
     int trace_cap;
@@ -117,6 +119,7 @@ struct Item {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head; ntiles over the group's heads
     bool down;                      // sweep query tiles from the last one down
     int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
+    bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
     // k-th tile of the item: head h of the group, query tile i
     __device__ __forceinline__ void tile(int k, int G, int& h, int& i) const {
         const int len = i1 - i0, r = k % len;
@@ -131,6 +134,20 @@ struct Item {
 // worth of query tiles until the sequence ends -- and the CTAs take them in a
 // snake.  A piece stores its partial dK, dV to a slab of its own, summed in
 // order afterwards, so dK and dV have the same bits on every call.
+//
+// Roundings of the SINK variant.  P is computed times 2^p_shift (the shift is
+// in nlse2, and undone exactly in scale and scale_v).  It is rounded to bf16
+// only as dV's operand; for dS it is kept as fp16, with 11 bits down to
+// 2^(-14 - p_shift) and an error of 2^(-25 - p_shift) below, so that dS =
+// P (dP - Delta) is rounded once (measured: dQ and dK 2.3e-3 off instead of
+// 3.1e-3, at the same registers).
+// The sinks' keys of a trained model share a direction, and since a row's dS
+// sum to nearly zero that direction cancels in dQ = dS K -- but not in the
+// roundings of dS, which it magnifies (128 sinks that hold most of a row's
+// weight: 8.7e-3).  So key tile 0 of a problem with sinks sends dS to dQ as
+// two bf16 numbers, dS and what its rounding lost: once the tensor cores have
+// read the first, the P/dS warps write the second over it and dQ^T adds K^T
+// times that.  One key tile of W / 128 + 2 pays for it.
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a
@@ -140,6 +157,7 @@ template <bool VARLEN, bool SPLIT, bool SINK>
 __device__ __forceinline__ Item decode(const Args& a, int it) {
     Item x;
     x.slab = -1;
+    x.fine = false;
     if constexpr (SINK) {
         const int rows = a.B * a.Hkv;
         x.n_q = a.n_units;
@@ -160,6 +178,7 @@ __device__ __forceinline__ Item decode(const Args& a, int it) {
         x.g = row % a.Hkv;
         x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
         x.down = false;
+        x.fine = x.t == 0 && a.fine0;
         return x;
     }
     int piece = 0;
@@ -241,6 +260,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* kd_full = bars + 16;
     uint64_t* kd_empty = bars + 17;
     uint64_t* done = bars + 18;
+    uint64_t* ds_read = bars + 19;    // SINK: the MMAs that read dS^T of a fine tile are done
+    uint64_t* rest_done = bars + 20;  // SINK: its rest is in place
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
 
@@ -267,6 +288,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         mbar_init(kd_full, 1);
         mbar_init(kd_empty, 2 * BT);
         mbar_init(done, 1);
+        mbar_init(ds_read, 1);
+        mbar_init(rest_done, 2 * BT);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -367,7 +390,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const SDesc dSk = desc(sdS, 16), dSn = desc(sdS, 16384);
         constexpr uint32_t kSlot = kTile >> 4, kRows16 = 2048 >> 4;
         auto kmaj = [](int kk) -> uint32_t { return (uint32_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4); };
-        uint32_t n = 0, kvi = 0;
+        uint32_t n = 0, kvi = 0, fine_n = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, int slot) {
             // Not profiled, even when tracing: any profiling hook in this
@@ -427,7 +450,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int kk = 0; kk < BT / 16; ++kk)
                         mma_ss(tmem + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
                 }
-                commit(dq_full);
+                if (!SINK || !x.fine) commit(dq_full);
                 {   // dK += dS^T Q
                     const SDesc bq = dQn + s * kSlot;
 #pragma unroll
@@ -435,6 +458,15 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         mma_ss(tmem + kColDK, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
                 }
                 commit(&q_empty[s]);
+                if (SINK && x.fine) {   // dQ^T += K^T (what dS^T's rounding lost)
+                    commit(ds_read);
+                    if (!wait(rest_done, fine_n & 1, 3)) break;
+                    ++fine_n;
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ss(tmem + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, 1u);
+                    commit(dq_full);
+                }
                 if (!more) {
                     commit(kd_full);
                     commit(kv_empty);
@@ -466,7 +498,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint32_t tS = tmem + lane_base + kColS + half * 64;
         const uint32_t tdP = tmem + lane_base + kColDP + half * 64;
         uint8_t* blk = sdS + half * 16384;
-        uint32_t n = 0, kvi = 0;
+        uint32_t n = 0, kvi = 0, fine_n = 0;
         bool ok = true;
         uint64_t wt[3] = {0, 0, 0};   // Q/S^T, dK/dV accumulators, dP^T
         auto wait = [&](uint64_t* bar, uint32_t parity, int slot) {
@@ -521,6 +553,19 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                 u[z] = 0xff800000u;
                         }
                     }
+                    if constexpr (SINK) {
+                        uint32_t ph[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + c + e);
+                            ph[e / 2] = exp2_pack_both(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), a.c2, l4.x, l4.y,
+                                                       pk[(c + e) / 2]);
+                            ph[e / 2 + 1] = exp2_pack_both(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]), a.c2, l4.z,
+                                                           l4.w, pk[(c + e) / 2 + 1]);
+                        }
+                        tmem_st16(tS + c / 2, ph);
+                        continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + c + e);
@@ -543,6 +588,23 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t dk[4];
+                        if constexpr (SINK) {
+#pragma unroll
+                            for (int w = 0; w < 8; w += 4) {
+                                const float4 d4 = *reinterpret_cast<const float4*>(dl + c + e + w);
+                                uint32_t &p01 = pk[(c + e + w) / 2], &p23 = pk[(c + e + w) / 2 + 1];
+                                const float2 x01 = ds_pair(p01, __uint_as_float(u[e + w]), __uint_as_float(u[e + w + 1]),
+                                                           d4.x, d4.y);
+                                const float2 x23 = ds_pair(p23, __uint_as_float(u[e + w + 2]),
+                                                           __uint_as_float(u[e + w + 3]), d4.z, d4.w);
+                                dk[w / 2] = pack_bf16(x01.x, x01.y);
+                                dk[w / 2 + 1] = pack_bf16(x23.x, x23.y);
+                                if (x.fine) {   // P is done with: its registers take the rest
+                                    p01 = pack_rest(x01, dk[w / 2]);
+                                    p23 = pack_rest(x23, dk[w / 2 + 1]);
+                                }
+                            }
+                        } else {
 #pragma unroll
                         for (int w = 0; w < 8; w += 4) {
                             const float4 d4 = *reinterpret_cast<const float4*>(dl + c + e + w);
@@ -555,12 +617,23 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             dk[w / 2 + 1] = ds_pack_bf16(p23.x, p23.y, __uint_as_float(u[e + w + 2]),
                                                          __uint_as_float(u[e + w + 3]), d4.z, d4.w);
                         }
+                        }
                         *reinterpret_cast<uint4*>(blk + sw128_offset(r, c + e)) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(ds_done);
+                if (SINK && x.fine) {
+                    if (!wait(ds_read, fine_n & 1, 2)) break;
+                    ++fine_n;
+#pragma unroll
+                    for (int z = 0; z < 64; z += 8)
+                        *reinterpret_cast<uint4*>(blk + sw128_offset(r, z)) =
+                            make_uint4(pk[z / 2], pk[z / 2 + 1], pk[z / 2 + 2], pk[z / 2 + 3]);
+                    fence_proxy_async_smem();
+                    mbar_arrive(rest_done);
+                }
             }
             if (!ok) break;
             // ---- epilogue: dV = acc, dK = scale * acc into [B, Lkv, Hkv, D] (bf16 store,
@@ -572,6 +645,10 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int c = half * 2; c < half * 2 + 2; ++c) {
                 uint32_t uv[32], uk[32];
                 tmem_ld32x2(tmem + lane_base + kColDV + c * 32, tmem + lane_base + kColDK + c * 32, uv, uk);
+                if constexpr (SINK) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
+                }
                 if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
                     float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
                     float4* pv = pkk + BT * D / 4;
@@ -771,7 +848,9 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
     Args a{};
     a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.Lq = a.Lkv = p.S; a.S_pad = S_pad; a.causal = 1;
     a.acc_rows = p.S;
-    a.scale = p.scale; a.c2 = p.scale * 1.4426950408889634f;
+    a.scale_v = 1.f / (1 << p.p_shift);
+    a.scale = p.scale * a.scale_v; a.c2 = p.scale * 1.4426950408889634f;
+    a.fine0 = p.fine;
     a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
     a.dK = dK; a.dV = dV;
     a.n_units = plan.n_q;

@@ -58,7 +58,9 @@ struct BCfg {
     static constexpr int kOffQ = 2 * kTile;            // 2 slots
     static constexpr int kOffDO = 4 * kTile;           // 2 slots
     static constexpr int kOffDS = 6 * kTile;           // 128 x 128 bf16 = 32 KB
-    static constexpr int kOffSide = kOffDS + 32768;    // 2 x kSide
+    // D = 64 only: what the rounding of dS lost (SINK, key tile 0), 32 KB
+    static constexpr int kOffRest = kOffDS + 32768;
+    static constexpr int kOffSide = kOffRest + (D == 64 ? 32768 : 0);   // 2 x kSide
     static constexpr int kOffBar = kOffSide + 2 * kSide;
     static constexpr int kSmem = kOffBar + 256;
 };
@@ -82,6 +84,8 @@ struct BwdArgs {
     int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
     int n_items, n_pieces, piece_tiles;   // ... items, of which the first n_pieces * rows are pieces of key tile 0
     float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
+    int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers (bwd_pipe_tc.cu)
+    float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
     uint64_t* trace;              // optional per-CTA timeline (nullptr: off)
     int trace_cap;
@@ -99,6 +103,7 @@ struct BItem {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head
     bool down;                      // sweep query tiles from the last one down
     int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
+    bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
     int base, pbase, len;           // packed batch: first token, first padded row, tokens of the sequence
     // k-th tile of the item: head hh of the group (0..G-1), query tile i
     __device__ __forceinline__ void tile(int k, int& hh, int& i) const {
@@ -116,6 +121,7 @@ template <bool VARLEN, bool SINK>
 __device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
     BItem x;
     x.slab = -1;
+    x.fine = false;
     if constexpr (SINK) {
         const int rows = a.B * a.Hkv;
         x.n_q = a.n_units;
@@ -136,6 +142,7 @@ __device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
         x.g = row % a.Hkv;
         x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
         x.down = false;
+        x.fine = x.t == 0 && a.fine0;
         return x;
     }
     const int row = it / a.n_units, unit = it % a.n_units;
@@ -324,6 +331,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const uint64_t dQk = sdesc_sw128(smem_u32(sQ), 16, 1024), dQn = sdesc_sw128(smem_u32(sQ), 16384, 1024);
         const uint64_t dOk = sdesc_sw128(smem_u32(sdO), 16, 1024), dOn = sdesc_sw128(smem_u32(sdO), 16384, 1024);
         const uint64_t dSk = sdesc_sw128(smem_u32(sdS), 16, 1024), dSn = sdesc_sw128(smem_u32(sdS), 16384, 1024);
+        const uint64_t dRn = sdesc_sw128(smem_u32(smem + C::kOffRest), 16384, 1024);
         constexpr uint64_t kSlot = C::kTile >> 4, kRows16 = 2048 >> 4;
         auto kmaj = [](int kk) -> uint64_t { return (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4); };
         uint32_t n = 0, kvi = 0;
@@ -388,6 +396,11 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                         for (int kk = 0; kk < BT / 16; ++kk)   // dQ = dS K
                             mma_ss(tmem + kColDP, dSn + kk * kRows16, dKn + kk * kRows16, idQ, kk > 0);
+                        if (SINK && x.fine) {   // dQ += (what dS's rounding lost) K
+#pragma unroll
+                            for (int kk = 0; kk < BT / 16; ++kk)
+                                mma_ss(tmem + kColDP, dRn + kk * kRows16, dKn + kk * kRows16, idQ, 1u);
+                        }
                     }
                 }
                 commit(dq_full);
@@ -460,6 +473,12 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         pk[e / 2 + 1] = pack_bf16(pp[2], pp[3]);
                         dk[e / 2] = pack_bf16(dd[0], dd[1]);
                         dk[e / 2 + 1] = pack_bf16(dd[2], dd[3]);
+                        if (SINK && x.fine) {
+                            const uint2 rest = make_uint2(pack_rest(make_float2(dd[0], dd[1]), dk[e / 2]),
+                                                          pack_rest(make_float2(dd[2], dd[3]), dk[e / 2 + 1]));
+                            *reinterpret_cast<uint2*>(smem + C::kOffRest + (c / 2) * 16384 +
+                                                      sw128_offset(r, (c % 2) * 32 + e)) = rest;
+                        }
                     }
                     tmem_st16(tP + c * 16, pk);
                     uint8_t* blk = sdS + (c / 2) * 16384;
@@ -483,6 +502,10 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 uint32_t uv[32], uk[32];
                 tmem_ld32(tmem + lane_base + kColDV + c * 32, uv);
                 tmem_ld32(tmem + lane_base + kColDK + c * 32, uk);
+                if constexpr (SINK) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
+                }
                 if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
                     float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
                     float4* pv = pkk + BT * D / 4;
@@ -646,7 +669,9 @@ dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const 
     BwdArgs a{};
     a.acc_rows = p.S;
     a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.S = p.S; a.S_pad = S_pad; a.causal = 1;
-    a.scale = p.scale; a.c2 = p.scale * 1.4426950408889634f;
+    a.scale_v = 1.f / (1 << p.p_shift);
+    a.scale = p.scale * a.scale_v; a.c2 = p.scale * 1.4426950408889634f;
+    a.fine0 = p.fine;
     a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
     a.dK = static_cast<__nv_bfloat16*>(dK);
     a.dV = static_cast<__nv_bfloat16*>(dV);

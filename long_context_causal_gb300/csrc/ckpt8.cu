@@ -119,13 +119,14 @@ struct PrepArgs {
     const __nv_bfloat16* O;
     const uint4* dO;
     const float* lse;
+    float p_shift;
     float *nlse2, *delta, *dq_acc;
     const uint8_t* ckpt;
 };
 
 // D / 16 threads take one row (b, i, h) of the padded range i < S_pad: Delta =
-// <dO, O> and -lse log2 e (negated so that a score's base-2 exponent is one
-// fused multiply-add), and the row's zeros in the head-major accumulator.
+// <dO, O> and p_shift - lse log2 e (so that a score's base-2 exponent is
+// one fused multiply-add), and the row's zeros in the head-major accumulator.
 template <int D, bool CKPT>
 __global__ void __launch_bounds__(kThreads)
 prep_kernel(const PrepArgs a, const Tensors t, const Ckpt8Layout L, int64_t n_rows) {
@@ -178,7 +179,7 @@ prep_kernel(const PrepArgs a, const Tensors t, const Ckpt8Layout L, int64_t n_ro
     for (int o = T / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (on && part == 0) {
         a.delta[dst] = acc;
-        a.nlse2[dst] = real ? a.lse[bh * a.S + i] * -1.4426950408889634f : 0.f;
+        a.nlse2[dst] = real ? fmaf(a.lse[bh * a.S + i], -1.4426950408889634f, a.p_shift) : 0.f;
     }
 }
 
@@ -281,7 +282,7 @@ dfa_status launch_sink_prep(const SinkProblem& p, int S_pad, const void* O, cons
     a.H = p.H; a.S = p.S; a.S_pad = S_pad;
     a.O = static_cast<const __nv_bfloat16*>(O);
     a.dO = static_cast<const uint4*>(dO);
-    a.lse = lse; a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
+    a.lse = lse; a.p_shift = (float)p.p_shift; a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
     a.ckpt = static_cast<const uint8_t*>(ckpt);
     const int64_t n_rows = (int64_t)p.B * S_pad * p.H;
     a.row_blocks = blocks_for(n_rows * (p.D / 16));
@@ -309,13 +310,14 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
                               void* dQ, void* dK, void* dV, cudaStream_t s) {
     const int64_t n8 = (int64_t)p.B * p.S * p.H * p.D / 8, dq_blocks = blocks_for(n8);
     const int rows = p.B * p.Hkv;
+    const float scale = p.scale / (1 << p.p_shift);
     const int64_t extra = plan.n_pieces > 1 ? blocks_for((int64_t)rows * 2 * 128 * p.D / 8) : 0;
     const unsigned grid = (unsigned)(dq_blocks + extra);
     if (p.D == 128)
-        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, p.scale, dq_blocks, n8, dq_acc,
+        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n8, dq_acc,
                                                      slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     else
-        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, p.scale, dq_blocks, n8, dq_acc,
+        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n8, dq_acc,
                                                     slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     return launched("windowed backward finish");
 }

@@ -859,8 +859,8 @@ dfa_status check_sink(dfa_dtype dt, int B, int H, int Hkv, int S, int D, int win
     return DFA_OK;
 }
 
-SinkProblem sink_problem(int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale) {
-    SinkProblem p{B, H, Hkv, S, D, std::min(window, S), n_sink, scale};
+SinkProblem sink_problem(int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale, bool ckpt = false) {
+    SinkProblem p{B, H, Hkv, S, D, std::min(window, S), n_sink, scale, n_sink > 0, ckpt ? 8 : 14};
     if (p.window >= S) p.n_sink = 0;
     return p;
 }
@@ -957,6 +957,55 @@ extern "C" dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void
                     static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+dfa_status check_decode(dfa_dtype dt, const DecodeProblem& p) {
+    dfa_status st = check_sink(dt, p.B, p.H, p.Hkv, p.S, p.D, p.window, p.n_sink, p.scale);
+    if (st) return st;
+    if (p.S < 1) return fail(DFA_ERR_INVALID_ARG, "the cache must have room for a token");
+    if (p.B > kMaxDecodeBatch) return fail(DFA_ERR_UNSUPPORTED, "%d sequences: at most %d at once", p.B, kMaxDecodeBatch);
+    const int64_t blocks = (p.H / p.Hkv + 15) / 16;
+    if (p.B * p.Hkv * blocks * decode_tiles(p) > (1 << 30)) return fail(DFA_ERR_INVALID_ARG, "problem too large");
+    return DFA_OK;
+}
+
+DecodeProblem decode_problem(int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale) {
+    return DecodeProblem{B, H, Hkv, S, D, (int64_t)S * Hkv * D, (int64_t)Hkv * D, D, window, n_sink, scale};
+}
+
+}  // namespace
+
+extern "C" size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D) {
+    const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
+    const std::string keep = g_msg;
+    const bool ok = check_decode(DFA_BF16, p) == DFA_OK;
+    snprintf(g_msg, sizeof(g_msg), "%s", keep.c_str());
+    return ok ? decode_workspace(p) : 0;
+}
+
+extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H,
+                                           int H_kv, int S_max, int D, const int64_t* kv_strides,
+                                           const int32_t* kv_len, int window, int n_sink, float scale, void* O,
+                                           float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    g_msg[0] = 0;
+    DecodeProblem p = decode_problem(B, H, H_kv, S_max, D, window, n_sink, scale);
+    dfa_status st = check_decode(dt, p);
+    if (st || B == 0) return st;
+    if (kv_strides) {
+        p.kv_sb = kv_strides[0]; p.kv_ss = kv_strides[1]; p.kv_sh = kv_strides[2];
+        for (int64_t x : {p.kv_sb, p.kv_ss, p.kv_sh})
+            if (x < 0 || x % 8 != 0) return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+    }
+    if ((st = check_ws(workspace, ws_bytes, decode_workspace(p)))) return st;
+    if ((st = check_ptrs({q, k, v, O}))) return st;
+    if (!kv_len || !lse || ((reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(lse)) & 3u))
+        return fail(DFA_ERR_INVALID_ARG, "kv_len and lse must be 4-byte aligned pointers");
+    p.window = std::min(window, S_max);
+    st = sink_decode(p, q, k, v, kv_len, O, lse, workspace, static_cast<cudaStream_t>(stream));
+    if (st == DFA_OK) count_launch(DFA_KERNEL_FWD), count_launch(DFA_KERNEL_MERGE);
+    return st;
+}
+
 // ---------------------------------------------------------------- 8-bit attention checkpoints
 static dfa_status check_ckpt(dfa_dtype dt, int B, int H, int H_kv, int S, int D, const void* ckpt, size_t have) {
     dfa_status st = check_sink(dt, B, H, H_kv, S, D, 1, 0, 1.f);
@@ -1007,7 +1056,7 @@ extern "C" dfa_status dfa_attn_bwd_ckpt8(const void* ckpt, size_t ckpt_bytes, co
     g_msg[0] = 0;
     dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
     if (st || (st = check_ckpt(dt, B, H, H_kv, S, D, ckpt, ckpt_bytes)) || (int64_t)B * S == 0) return st;
-    const SinkProblem p = sink_problem(B, H, H_kv, S, D, window, n_sink, scale);
+    const SinkProblem p = sink_problem(B, H, H_kv, S, D, window, n_sink, scale, true);
     if ((st = check_ws(workspace, ws_bytes, sink_ws(p, true).total))) return st;
     if ((st = check_ptrs({lse, dO, dQ, dK, dV}))) return st;
     return sink_bwd(p, nullptr, nullptr, nullptr, nullptr, lse, dO, ckpt, dQ, dK, dV, static_cast<char*>(workspace),

@@ -526,15 +526,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 // 4-D bf16 tensor map over [B, L, heads, D] (element strides sb, ss, sh; D
-// contiguous) with a {64, 1, 128, 1} box and the 128-byte swizzle.
+// contiguous) with a {64, 1, box_rows, 1} box and the 128-byte swizzle.
 bool make_tmap_bshd(void* map, const void* base, int B, int L, int heads, int D, int64_t sb,
-                    int64_t ss, int64_t sh) {
+                    int64_t ss, int64_t sh, int box_rows) {
     CUtensorMap* m = static_cast<CUtensorMap*>(map);
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(L > 0 ? L : 1), (cuuint64_t)(B > 0 ? B : 1)};
     cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)ss * 2, (cuuint64_t)sb * 2};
-    cuuint32_t box[4] = {64, 1, 128, 1};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     // A stride of a size-1 dimension is never used; keep it valid for the encoder.
     if (heads == 1 && strides[0] == 0) strides[0] = 16;

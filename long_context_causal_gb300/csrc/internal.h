@@ -120,6 +120,13 @@ struct SinkProblem {
     int B, H, Hkv, S, D;
     int window, n_sink;
     float scale;
+    bool fine;      // the caller's n_sink > 0, whatever the window: the backward keeps key tile 0's dS more exactly
+    // The backward holds P times 2^p_shift: nlse2 = p_shift - lse log2 e, and dQ's
+    // accumulator carries the factor to the finishing kernel.  fp16 then keeps 11
+    // bits of a P between 2^(-14 - p_shift) and 2^(16 - p_shift).  From the saved
+    // tensors P <= 1 but for rounding: 14.  From a checkpoint the scores carry the
+    // rounding of q and k, and e to that may stand above 1: 8.
+    int p_shift;
 };
 constexpr int kMaxSinks = 128;   // one key tile
 // Backward plan: key tile 0 is seen by every query when there are sinks.  Its
@@ -135,7 +142,7 @@ SinkBwdPlan sink_bwd_plan(const SinkProblem& p);
 
 dfa_status tc_sink_fwd(const SinkProblem& p, const void* q, const void* k, const void* v, void* O, float* lse,
                        cudaStream_t s);
-// nlse2 and delta as for tc_bwd; dq_acc fp32 [B, H, S, D], zero; slabs fp32
+// delta as for tc_bwd; nlse2 with p_shift added; dq_acc fp32 [B, H, S, D], zero; slabs fp32
 // [n_pieces * B * Hkv][2][128][D] (dK with scale applied, dV).
 dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
                        const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
@@ -143,6 +150,20 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
 dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
                            const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc,
                            float* slabs, void* dK, void* dV, cudaStream_t s);
+
+// Single-token form over a cache: k, v [B, S, Hkv, D] with element strides
+// kv_s*, kv_len int32 [B] on the device.
+struct DecodeProblem {
+    int B, H, Hkv, S, D;
+    int64_t kv_sb, kv_ss, kv_sh;
+    int window, n_sink;
+    float scale;
+};
+constexpr int kMaxDecodeBatch = 8192;   // the kernel sums the lengths up in shared memory
+int64_t decode_tiles(const DecodeProblem& p);      // at most, per (sequence, block of query heads)
+size_t decode_workspace(const DecodeProblem& p);
+dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
+                       void* O, float* lse, void* ws, cudaStream_t s);
 
 // 8-bit checkpoint sections, in bytes from the start of the buffer: int8
 // payloads of q, k, v, O and their exponent bytes (one for 32 elements).
@@ -184,10 +205,10 @@ inline bool chunks_valid(int64_t S, int n_chunks) {
 }
 
 // 4-D bf16 TMA descriptor over a [B, L, heads, D] tensor (element strides sb,
-// ss, sh; D contiguous), box {64, 1, 128, 1}, 128-byte swizzle.  The map is
+// ss, sh; D contiguous), box {64, 1, box_rows, 1}, 128-byte swizzle.  The map is
 // written into `map` (a CUtensorMap, 128 bytes, 64-byte aligned).
 bool make_tmap_bshd(void* map, const void* base, int B, int L, int heads, int D, int64_t sb,
-                    int64_t ss, int64_t sh);
+                    int64_t ss, int64_t sh, int box_rows = 128);
 
 // Per-CTA trace buffer set by dfa_debug_cta_trace (nullptr when off).
 uint64_t* cta_trace(int* capacity);

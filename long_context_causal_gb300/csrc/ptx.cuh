@@ -514,6 +514,46 @@ __device__ __forceinline__ uint32_t exp2_pack_bf16(float s0, float s1, float c, 
     return r;
 }
 
+// As exp2_pack_bf16, and the same two values in fp16 as well (11 bits of
+// mantissa; beyond 65504 they stay there).
+__device__ __forceinline__ uint32_t exp2_pack_both(float s0, float s1, float c, float n0, float n1, uint32_t& half) {
+    uint32_t r;
+    asm("{\n\t.reg .b64 a, b, d;\n\t.reg .f32 lo, hi;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %4};\n\t"
+        "mov.b64 d, {%5, %6};\n\t"
+        "fma.rn.f32x2 a, a, b, d;\n\t"
+        "mov.b64 {lo, hi}, a;\n\t"
+        "ex2.approx.ftz.f32 lo, lo;\n\t"
+        "ex2.approx.ftz.f32 hi, hi;\n\t"
+        "cvt.rn.bf16x2.f32 %0, hi, lo;\n\t"
+        "cvt.rn.satfinite.f16x2.f32 %1, hi, lo;\n\t}"
+        : "=r"(r), "=r"(half)
+        : "f"(s0), "f"(s1), "f"(c), "f"(n0), "f"(n1));
+    return r;
+}
+// p (u - d) of a pair: p in fp16, the rest and the results in fp32.
+__device__ __forceinline__ float2 ds_pair(uint32_t p, float u0, float u1, float d0, float d1) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\t.reg .b16 h0, h1;\n\t.reg .f32 p0, p1;\n\t"
+        "mov.b32 {h0, h1}, %2;\n\t"
+        "cvt.f32.f16 p0, h0;\n\t"
+        "cvt.f32.f16 p1, h1;\n\t"
+        "mov.b64 a, {%3, %4};\n\t"
+        "mov.b64 b, {%5, %6};\n\t"
+        "sub.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 c, {p0, p1};\n\t"
+        "mul.rn.f32x2 a, a, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(p), "f"(u0), "f"(u1), "f"(d0), "f"(d1));
+    return r;
+}
+// What a pair loses in pack_bf16, packed: bf16(x - bf16(x)).
+__device__ __forceinline__ uint32_t pack_rest(float2 x, uint32_t packed) {
+    return pack_bf16(x.x - __uint_as_float(packed << 16), x.y - __uint_as_float(packed & 0xffff0000u));
+}
+
 // Two softmax-gradient entries packed to bf16x2, `lo` = p0 (u0 - d0) and
 // `hi` = p1 (u1 - d1), with the two-lane fp32 instructions of sm_100 and later
 // (sub.f32x2, mul.f32x2): each lane is rounded exactly as the scalar

@@ -76,6 +76,8 @@ def _load() -> ctypes.CDLL:
         "dfa_attn_bwd_sink_workspace_size": (sz, [i32] * 7),
         "dfa_attn_bwd_sink": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                     vp, vp, vp, vp, sz, vp]),
+        "dfa_attn_decode_sink_workspace_size": (sz, [i32] * 4),
+        "dfa_attn_decode_sink": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, p64, vp, i32, i32, f32, vp, vp, vp, sz, vp]),
         "dfa_ckpt8_size": (sz, [i32] * 5),
         "dfa_ckpt8_save": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, sz, vp]),
         "dfa_ckpt8_restore": (i32, [vp, sz, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]),
@@ -509,6 +511,39 @@ def dfa_attn_bwd_sink(q, k, v, O, lse, dO, window: int, n_sink: int = 0, scale: 
                                   int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), _ptr(dQ),
                                   _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
     return dQ, dK, dV
+
+
+def dfa_attn_decode_sink_workspace_size(B, H, H_kv, D) -> int:
+    return int(_lib.dfa_attn_decode_sink_workspace_size(B, H, H_kv, D))
+
+
+def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: float | None = None, O=None, lse=None,
+                         workspace_buf=None, stream=None):
+    """One new token per sequence over a cache: q [B,H,D], k, v [B,S_max,H_kv,D]
+    (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
+    GPU; returns (O [B,H,D], lse fp32 [B,H])."""
+    if q.dim() != 3 or k.dim() != 4 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[2]:
+        raise ValueError(f"q must be [B, H, D] and k, v [B, S_max, H_kv, D], got {tuple(q.shape)}, {tuple(k.shape)}, "
+                         f"{tuple(v.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have the same dtype")
+    ks = k.stride()
+    if ks != v.stride() or ks[3] != 1:
+        raise ValueError("k and v must share their strides, with the head dimension contiguous")
+    B, H, D = q.shape
+    _, S, Hkv, _ = k.shape
+    _dense(q, "q")
+    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
+    _like(kv_len, "kv_len", (B,), torch.int32, q.device)
+    O = torch.empty_like(q) if O is None else _like(O, "O", q.shape, q.dtype, q.device)
+    lse = (torch.empty((B, H), dtype=torch.float32, device=q.device) if lse is None
+           else _like(lse, "lse", (B, H), torch.float32, q.device))
+    ws = (_scratch(dfa_attn_decode_sink_workspace_size(B, H, Hkv, D), q.device, stream) if workspace_buf is None
+          else _bytes_buf(workspace_buf, "workspace_buf", q.device))
+    _check(_lib.dfa_attn_decode_sink(_ptr(q), _ptr(k), _ptr(v), _dtype(q), B, H, Hkv, S, D, (ctypes.c_int64 * 3)(*ks[:3]),
+                                     _ptr(kv_len), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale),
+                                     _ptr(O), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    return O, lse
 
 
 def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:

@@ -49,23 +49,25 @@ def attn_fwd(q, k, v, window, n_sink, scale=None):
 
 
 def attn_bwd(q, k, v, O, lse, dO, window, n_sink, scale=None):
-    """Gradients from the given O and lse: {"dQ": (value, terms, cancel), ...}.
+    """Gradients from the given O and lse: {"dQ": (value, terms, cancel, floor), ...}.
     `terms` sums |dS| |k|, |dS| |q| or P |dO|; `cancel` sums P (|dO| |v|^T +
-    |dO| |O|) |k| (or |q|): what dO v^T - Delta is the difference of (0 for dV)."""
+    |dO| |O|) |k| (or |q|): what dO v^T - Delta is the difference of (0 for dV);
+    `floor` is `cancel` with P = 1 on every visible pair: what an absolute error
+    of P moves the result by."""
     q, k, v, O, lse, dO = (np.asarray(t, dtype=np.float64) for t in (q, k, v, O, lse, dO))
     B, S, H, D = q.shape
     G = H // k.shape[2]
     scale = D ** -0.5 if scale is None else scale
     see = visible(S, window, n_sink)
-    out = {n: tuple(np.zeros_like(t) for _ in range(3)) for n, t in (("dQ", q), ("dK", k), ("dV", v))}
+    out = {n: tuple(np.zeros_like(t) for _ in range(4)) for n, t in (("dQ", q), ("dK", k), ("dV", v))}
     for b in range(B):
         for h in range(H):
             g = h // G
             qh, kh, vh, oh, dh = q[b, :, h], k[b, :, g], v[b, :, g], O[b, :, h], dO[b, :, h]
             p = np.where(see, np.exp(_scores(q[b], k[b], h, scale) - lse[b, h][:, None]), 0.0)
             ds = p * (dh @ vh.T - (dh * oh).sum(1, keepdims=True)) * scale
-            c = p * (np.abs(dh) @ np.abs(vh).T + (np.abs(dh) * np.abs(oh)).sum(1, keepdims=True)) * scale
-            for z, w in enumerate((ds, np.abs(ds), c)):
+            f = see * (np.abs(dh) @ np.abs(vh).T + (np.abs(dh) * np.abs(oh)).sum(1, keepdims=True)) * scale
+            for z, w in enumerate((ds, np.abs(ds), p * f, f)):
                 kk, qq = (kh, qh) if z == 0 else (np.abs(kh), np.abs(qh))
                 out["dQ"][z][b, :, h] += w @ kk
                 out["dK"][z][b, :, g] += w.T @ qq

@@ -8,6 +8,9 @@ step of bf16 relative to the value:
   dV   likewise (P and the result);
   dQ, dK  P and dS are rounded (2 u times the sum of |dS| |k| or |dS| |q|),
        the result once;
+  P of dS is kept in fp16 times 2^14 (2^8 from a checkpoint): 11 bits, more
+       than the above counts, but for P below 2^-28 (2^-22), where it is off by
+       up to half the smallest fp16 number, 2^-25 / 2^14 = 2^-39 (2^-33);
 and fp32 sums of up to D = 128 products move a score by less than 2^-13 and
 dO.v - Delta by less than 2^-16 of the magnitudes it is the difference of.
 """
@@ -39,11 +42,11 @@ def check_fwd(O, lse, q, k, v, window, n_sink, scale=None):
     close(lse, lr, 2 * F, "lse")
 
 
-def check_bwd(grads, q, k, v, O, lse, do, window, n_sink, scale=None):
+def check_bwd(grads, q, k, v, O, lse, do, window, n_sink, scale=None, least=2.0 ** -39):
     ref = sink.attn_bwd(*(np64(t) for t in (q, k, v, O, lse, do)), window, n_sink, scale)
     for got, name in zip(grads, ("dQ", "dK", "dV")):
-        r, terms, cancel = ref[name]
-        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + U * np.abs(r) + 1e-30, name)
+        r, terms, cancel, floor = ref[name]
+        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + least * floor + U * np.abs(r) + 1e-30, name)
 
 
 # (B, H, Hkv, S, D, window, n_sink)
@@ -89,6 +92,37 @@ def test_sharp_scores_rescale():
     # scores reach 200: fp32 moves them by 2^-24 * 200 * a few, far below F
     check_fwd(O, lse, q, k, v, 300, 4, 0.2)
     check_bwd(grads, q, k, v, O, lse, do, 300, 4, 0.2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,window,n_sink", [(900, 40, 128), (300, 1000, 100)])
+def test_sinks_that_share_a_direction(D, S, window, n_sink):
+    """A row's dS sum to nearly zero, so what all keys share cancels in dQ: the
+    roundings of key tile 0's dS must not bring it back.  There P is rounded to
+    fp16 (half a step: 2^-11) and dS held in two bf16 numbers (2^-8 squared);
+    the other tiles round dS to bf16."""
+    B, H, Hkv = 1, 4, 2
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=36)
+    u = torch.randn(Hkv, D, device=DEV, generator=torch.Generator(DEV).manual_seed(37))
+    q += (0.25 * u.repeat_interleave(H // Hkv, 0)).bfloat16()
+    k[:, :n_sink] = (0.1 * k[:, :n_sink] + 3 * u).bfloat16()
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dQ, dK, dV = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink)
+    dfa.dfa_check_errors()
+    args = [np64(t) for t in (q, k, v, O, lse, do)]
+    r, terms, cancel, floor = sink.attn_bwd(*args, window, n_sink)["dQ"]
+    # what key tile 0 adds to the terms
+    first = np.zeros_like(r)
+    see = sink.visible(S, window, n_sink)
+    for h in range(H):
+        g = h // (H // Hkv)
+        qh, kh, vh, oh, dh = (np64(t)[0] for t in (q[:, :, h], k[:, :, g], v[:, :, g], O[:, :, h], do[:, :, h]))
+        p = np.where(see, np.exp(D ** -0.5 * qh @ kh.T - np64(lse)[0, h][:, None]), 0)
+        ds = np.abs(p * (dh @ vh.T - (dh * oh).sum(1, keepdims=True))) * D ** -0.5
+        first[0, :, h] = ds[:, :128] @ np.abs(kh[:128])
+    close(dQ, r, (2.0 ** -11 + 2.0 ** -16) * first + U * (terms - first) + F * terms + F2 * cancel + 2.0 ** -39 * floor
+          + U * np.abs(r) + 1e-30, "dQ")
+    check_bwd((dQ, dK, dV), q, k, v, O, lse, do, window, n_sink)
 
 
 def test_window_over_every_key_is_the_causal_call():
@@ -184,7 +218,7 @@ def test_backward_from_a_checkpoint(case):
     grads = dfa.dfa_attn_bwd_ckpt8(ckpt, lse, do, Hkv, window, n_sink)
     dfa.dfa_check_errors()
     assert dfa.dfa_launch_count("fwd") == n_fwd
-    check_bwd(grads, *held, lse, do, window, n_sink)
+    check_bwd(grads, *held, lse, do, window, n_sink, least=2.0 ** -33)
 
 
 def test_causal_backward_from_a_checkpoint():
@@ -194,10 +228,128 @@ def test_causal_backward_from_a_checkpoint():
     grads = dfa.dfa_attn_bwd_ckpt8(dfa.dfa_ckpt8_save(q, k, v, O), lse, do, 1)
     dfa.dfa_check_errors()
     held = [sink.ckpt8(np64(t)) for t in (q, k, v, O)]
-    check_bwd(grads, *(torch.from_numpy(t) for t in held), lse, do, 770, 0)
+    check_bwd(grads, *(torch.from_numpy(t) for t in held), lse, do, 770, 0, least=2.0 ** -33)
     # and the checkpoint's own rounding, 2^-7 of a group's largest at most, moves the gradients little
     for a, b in zip(grads, dfa.dfa_attn_bwd(q, k, v, O, lse, do)):
         assert (a.float() - b.float()).norm() <= 0.05 * b.float().norm()
+
+
+# ------------------------------------------------------------------------------------------------ single tokens
+# (B, H, Hkv, S_max, D, window, n_sink, lengths)
+DECODE = [
+    (1, 1, 1, 1, 64, 1, 0, [1]),
+    (1, 4, 1, 64, 128, 64, 4, [64]),
+    (3, 4, 2, 100, 128, 1, 1, [0, 1, 100]),
+    (2, 8, 8, 300, 64, 65, 3, [66, 300]),
+    (4, 6, 2, 1000, 128, 128, 128, [129, 256, 257, 1000]),
+    (5, 40, 2, 700, 64, 200, 17, [0, 0, 17, 217, 700]),          # 20 heads to a key/value head: two blocks of 16
+    (2, 33, 1, 500, 128, 1000, 5, [499, 1]),
+    (1, 8, 2, 5000, 128, 5000, 4, [4999]),
+    (1, 2, 1, 9000, 64, 3000, 100, [9000]),
+    (17, 4, 4, 260, 128, 70, 4, [0] * 8 + [260, 3, 70, 71, 74, 75, 138, 139, 200]),
+    (300, 2, 1, 40, 64, 16, 2, [i % 41 for i in range(300)]),
+]
+
+
+def cache(B, S, Hkv, D, lens, window, n_sink, seed, poison=float("nan")):
+    """Keys and values whose rows nobody sees are poisoned."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    k, v = (torch.randn(B, S, Hkv, D, device=DEV, generator=g).bfloat16() for _ in range(2))
+    j, n = torch.arange(S, device=DEV)[None], torch.tensor(lens, device=DEV)[:, None]
+    hidden = ~((j < n) & ((j > n - 1 - window) | (j < n_sink)))
+    for t in (k, v):
+        t[hidden] = poison
+    return k, v, torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+def check_decode(O, lse, q, k, v, lens, window, n_sink):
+    Or, lr, size = sink.decode(np64(q), np64(k), np64(v), lens, window, n_sink)
+    close(O, Or, (U + F) * size + U * np.abs(Or), "O")
+    empty = np.asarray(lens) == 0
+    assert (np64(lse)[empty] == -np.inf).all()
+    close(lse[~torch.from_numpy(empty)], lr[~empty], 2 * F, "lse")
+
+
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: "B{}H{}kv{}S{}D{}w{}s{}".format(*c))
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_decode(case, poison):
+    B, H, Hkv, S, D, window, n_sink, lens = case
+    k, v, n = cache(B, S, Hkv, D, lens, window, n_sink, 71, poison)
+    q = torch.randn(B, H, D, device=DEV, generator=torch.Generator(DEV).manual_seed(72)).bfloat16()
+    ws = torch.full((dfa.dfa_attn_decode_sink_workspace_size(B, H, Hkv, D),), 0xFF, dtype=torch.uint8, device=DEV)
+    O, lse = dfa.dfa_attn_decode_sink(q, k, v, n, window, n_sink, workspace_buf=ws)
+    dfa.dfa_check_errors()
+    check_decode(O, lse, q, k, v, lens, window, n_sink)
+    O2, lse2 = dfa.dfa_attn_decode_sink(q, k, v, n, window, n_sink)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+
+
+def test_decode_strided_cache_and_lengths_out_of_range():
+    B, H, Hkv, S, D = 3, 4, 2, 200, 128
+    g = torch.Generator(DEV).manual_seed(73)
+    both = torch.randn(B, Hkv, S, 2, D + 8, device=DEV, generator=g).bfloat16()     # head-major, k and v interleaved
+    k, v = both[..., 0, :D].transpose(1, 2), both[..., 1, :D].transpose(1, 2)
+    q = torch.randn(B, H, D, device=DEV, generator=g).bfloat16()
+    n = torch.tensor([-4, 150, 999], dtype=torch.int32, device=DEV)
+    O, lse = dfa.dfa_attn_decode_sink(q, k, v, n, 60, 3)
+    dfa.dfa_check_errors()
+    check_decode(O, lse, q, k, v, [0, 150, 200], 60, 3)
+
+
+def test_decode_follows_the_prompt_and_is_captured_once():
+    """A prompt through the forward, then tokens one at a time through one
+    captured call: each row is what the forward gives for the whole sequence."""
+    B, H, Hkv, D, W, N, P, T = 2, 8, 2, 128, 100, 4, 180, 260
+    q, k, v, _ = make(B, H, Hkv, T, D, torch.bfloat16, device=DEV, seed=74)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, W, N)
+    kc, vc = torch.full((2, B, 300, Hkv, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    kc[:, :P], vc[:, :P] = k[:, :P], v[:, :P]
+    qt = torch.empty(B, H, D, dtype=torch.bfloat16, device=DEV)
+    n = torch.full((B,), P, dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, ls = dfa.dfa_attn_decode_sink(qt, kc, vc, n, W, N)
+    for i in range(P, T):
+        kc[:, i], vc[:, i], qt[:] = k[:, i], v[:, i], q[:, i]
+        n.fill_(i + 1)
+        graph.replay()
+        # both sides round P and the result; the terms' magnitudes are below 4 here
+        assert (out.float() - O[:, i].float()).abs().max() <= 4 * U * 4
+        assert (ls - lse[:, :, i]).abs().max() <= 4 * F
+    dfa.dfa_check_errors()
+
+
+def test_decode_on_two_streams():
+    sets = []
+    for z, case in enumerate(DECODE[4:8]):
+        B, H, Hkv, S, D, window, n_sink, lens = case
+        k, v, n = cache(B, S, Hkv, D, lens, window, n_sink, 80 + z)
+        q = torch.randn(B, H, D, device=DEV, generator=torch.Generator(DEV).manual_seed(z)).bfloat16()
+        sets.append((q, k, v, n, window, n_sink))
+    want = [dfa.dfa_attn_decode_sink(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(10):
+        got = [dfa.dfa_attn_decode_sink(*s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_cache_beyond_32_bits():
+    B, H, Hkv, S, D, W, N = 3, 16, 8, 1 << 20, 128, 700, 4
+    g = torch.Generator(DEV).manual_seed(75)
+    k = torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    v = torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    q = torch.randn(B, H, D, device=DEV, generator=g).bfloat16()
+    lens = [S, 5, S - 1]
+    O, lse = dfa.dfa_attn_decode_sink(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), W, N)
+    dfa.dfa_check_errors()
+    for b, n in enumerate(lens):
+        idx = torch.arange(n, device=DEV)
+        idx = idx[(idx > n - 1 - W) | (idx < N)]
+        # the visible rows alone, all of them in the window
+        check_decode(O[b:b + 1], lse[b:b + 1], q[b:b + 1], k[b:b + 1, idx], v[b:b + 1, idx], [idx.numel()], idx.numel(), 0)
 
 
 # ------------------------------------------------------------------------------------------------ streams, graphs
@@ -291,5 +443,5 @@ def test_offsets_beyond_32_bits():
     close(lse[:, hs, a + W - 1:], lr[:, :, rows], 2 * F, "lse")
     ref = sink.attn_bwd(*sub, sl, sd, W, N)
     for got, name in ((dQ[:, a + W - 1:, hs], "dQ"), (dK[:, a + W - 1:, gs], "dK"), (dV[:, a + W - 1:, gs], "dV")):
-        r, terms, cancel = (t[:, rows] for t in ref[name])
-        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + U * np.abs(r) + 1e-30, name)
+        r, terms, cancel, floor = (t[:, rows] for t in ref[name])
+        close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + 2.0 ** -39 * floor + U * np.abs(r) + 1e-30, name)

@@ -213,3 +213,41 @@ def test_the_binding_refuses_tensors_it_must_not_hand_on():
         dfa.dfa_attn_fwd_sink(q, k, k.float(), 4)
     with pytest.raises(ValueError, match="contiguous"):
         dfa.dfa_attn_fwd_sink(q.transpose(1, 2).contiguous().transpose(1, 2), k, k, 4)
+
+
+def decode(**kw):
+    a = dict(q=A, k=A, v=A, dt=1, B=2, H=4, Hkv=2, S=300, D=128, ks=None, n=A, window=64, n_sink=4, scale=0.1, O=A, lse=A, ws=A,
+             wn=1 << 40)
+    a.update(kw)
+    return lib.dfa_attn_decode_sink(*(a[x] for x in ("q", "k", "v", "dt", "B", "H", "Hkv", "S", "D", "ks", "n", "window",
+                                                     "n_sink", "scale", "O", "lse", "ws", "wn")), None)
+
+
+@pytest.mark.parametrize("kw,code", REFUSED + [
+    (dict(S=0), dfa.DFA_ERR_INVALID_ARG), (dict(B=8193), dfa.DFA_ERR_UNSUPPORTED), (dict(n=None), dfa.DFA_ERR_INVALID_ARG),
+    (dict(n=A + 2), dfa.DFA_ERR_INVALID_ARG), (dict(lse=None), dfa.DFA_ERR_INVALID_ARG), (dict(q=MIS), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ks=(ctypes.c_int64 * 3)(300 * 256, 256, 132)), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ks=(ctypes.c_int64 * 3)(300 * 256, -256, 128)), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ws=None), dfa.DFA_ERR_WORKSPACE), (dict(ws=MIS), dfa.DFA_ERR_INVALID_ARG),
+    (dict(wn=dfa.dfa_attn_decode_sink_workspace_size(2, 4, 2, 128) - 1), dfa.DFA_ERR_WORKSPACE)])
+def test_decode_refusals(kw, code):
+    assert decode(**kw) == code and dfa.dfa_last_error()
+
+
+def test_decode_of_no_sequence_and_size_queries():
+    assert decode(B=0, q=None, k=None, v=None, n=None, ws=None, wn=0) == dfa.DFA_OK
+    assert dfa.dfa_attn_decode_sink_workspace_size(8193, 4, 2, 128) == 0
+    assert dfa.dfa_attn_decode_sink_workspace_size(1, 4, 2, 80) == 0
+    assert dfa.dfa_attn_decode_sink_workspace_size(1, 4, 2, 128) > 0
+
+
+def test_the_binding_refuses_decode_tensors():
+    t = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    q, k, n = t(2, 4, 64), t(2, 8, 2, 64), t(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfa.dfa_attn_decode_sink(q, k, k, n, 4)
+    for bad in ((q[:1], k, k), (q, k[0], k[0]), (q, k, t(2, 8, 2, 128)), (t(2, 4, 128), k, k)):
+        with pytest.raises(ValueError, match="must be"):
+            dfa.dfa_attn_decode_sink(*bad, n, 4)
+    with pytest.raises(ValueError, match="strides"):
+        dfa.dfa_attn_decode_sink(q, k, t(2, 2, 8, 64).transpose(1, 2), n, 4)
