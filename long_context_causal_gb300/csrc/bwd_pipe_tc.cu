@@ -859,12 +859,16 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
     a.slabs = slabs;
     a.err = device_error_flag();
     auto kern = bwd_pipe_kernel<false, false, true>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-        return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != (int)kLaunchRegs)
-        return fail(DFA_ERR_CUDA, "sink backward: built with %d registers per thread, the register split needs %u",
-                    fa.numRegs, kLaunchRegs);
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
+        cudaFuncAttributes fa{};   // as in tc_bwd_pipelined
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != (int)kLaunchRegs)
+            return fail(DFA_ERR_CUDA, "sink backward: built with %d registers per thread, the register split needs %u",
+                        fa.numRegs, kLaunchRegs);
+        mark_on_device(seen);
+    }
     kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, kSmem, s>>>(mq, mk, mv, mdo, a);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));

@@ -682,8 +682,12 @@ dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const 
     a.err = device_error_flag();
     auto kern = bwd_tc_kernel<D, false, true>;
     const int smem = BCfg<D>::kSmem;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
+        mark_on_device(seen);
+    }
     kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, smem, s>>>(mq, mk, mv, mdo, a);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));

@@ -39,83 +39,113 @@ __device__ __forceinline__ float exp_scale(uint32_t code) {   // 2^e of an expon
 }
 __device__ __forceinline__ float s8(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
-// Sixteen int8 elements (one 16-byte word) times 2^e.
-__device__ __forceinline__ void dequant16(const uint4& u, float sc, float* x) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight int8 elements times 2^e.
+__device__ __forceinline__ void dequant8(const uint2& u, float sc, float* x) {
 #pragma unroll
-    for (int z = 0; z < 16; ++z) x[z] = s8(w[z / 4], z % 4) * sc;
+    for (int z = 0; z < 8; ++z) x[z] = s8(z < 4 ? u.x : u.y, z & 3) * sc;
 }
 
+// A unit is eight elements: 16 bytes of bf16, 8 of the payload; four units make
+// a group.  A block takes kPer * kThreads consecutive units of one tensor, each
+// thread kPer of them kThreads apart, all loaded before the first is used: a
+// warp's accesses are contiguous on both sides, and 2048 threads of an SM have
+// 64 bytes each in flight.
+constexpr int kPer = 4;
 struct Tensors {
     const void* src[4];
     void* dst[4];
-    int64_t end[4];     // running count of 16-element units
+    int64_t units[4];
+    int end[4];         // running count of the tensors' blocks
 };
-
-// 16 elements of one tensor per thread; two threads make a group.
-__global__ void __launch_bounds__(kThreads)
-save_kernel(const Tensors t, uint8_t* __restrict__ ckpt, const Ckpt8Layout L) {
-    int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const bool on = u < t.end[3];    // the same for both threads of a group: there is an even number of units
-    if (!on) u = u & 1;              // stays for the shuffle, stores nothing
+__device__ __forceinline__ int tensor_of(const Tensors& t, int block, int n) {
     int i = 0;
+    for (int z = 0; z + 1 < n; ++z) i += block >= t.end[z];
+    return i;
+}
+
+__global__ void __launch_bounds__(kThreads)
+save_kernel(const __grid_constant__ Tensors t, uint8_t* __restrict__ ckpt, const __grid_constant__ Ckpt8Layout L) {
+    const int i = tensor_of(t, blockIdx.x, 4);
+    const int64_t u0 = (int64_t)(blockIdx.x - (i ? t.end[i - 1] : 0)) * (kPer * kThreads) + threadIdx.x, n = t.units[i];
+    const uint4* src = static_cast<const uint4*>(t.src[i]);
+    uint8_t* data = ckpt + L.data[i];
+    uint8_t* exps = ckpt + L.exps[i];
+    uint4 in[kPer];
 #pragma unroll
-    for (int z = 0; z < 3; ++z) i += u >= t.end[z];
-    const int64_t at = u - (i ? t.end[i - 1] : 0);
-    const uint4* src = static_cast<const uint4*>(t.src[i]) + 2 * at;
-    const uint4 a = src[0], b = src[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    // The largest magnitude as an integer: the order of the bits without the
-    // sign is the order of the values, and an infinity or NaN is above all.
-    uint32_t big = 0;
-#pragma unroll
-    for (int z = 0; z < 8; ++z) big = max(big, max(w[z] & 0x7fffu, (w[z] >> 16) & 0x7fffu));
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    const uint32_t ex = big >> 7;    // biased exponent of the largest
-    // e + 127 = ex - 6, at least 7
-    const uint32_t code = ex == 255u ? 255u : max((int)ex - 6, 7);
-    const float down = __uint_as_float((254u - code) << 23);   // 2^-e (unused for code 255)
-    uint32_t o[4];
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-        uint32_t r = 0;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const uint32_t v = w[2 * z + y / 2];
-            const int m = __float2int_rn((y & 1 ? bf_hi(v) : bf_lo(v)) * down);
-            r |= (uint32_t)(uint8_t)max(-127, min(127, m)) << (8 * y);
-        }
-        o[z] = code == 255u ? 0u : r;
+    for (int y = 0; y < kPer; ++y) {
+        const int64_t u = u0 + y * kThreads;
+        in[y] = u < n ? src[u] : make_uint4(0, 0, 0, 0);   // whole groups: n is a multiple of 4
     }
-    if (!on) return;
-    *reinterpret_cast<uint4*>(ckpt + L.data[i] + 16 * at) = make_uint4(o[0], o[1], o[2], o[3]);
-    if ((at & 1) == 0) ckpt[L.exps[i] + at / 2] = (uint8_t)code;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+        const int64_t u = u0 + y * kThreads;
+        const uint32_t w[4] = {in[y].x, in[y].y, in[y].z, in[y].w};
+        // The largest magnitude as an integer: the order of the bits without the
+        // sign is the order of the values, and an infinity or NaN is above all.
+        uint32_t big = 0;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) big = max(big, max(w[z] & 0x7fffu, (w[z] >> 16) & 0x7fffu));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const uint32_t ex = big >> 7;    // biased exponent of the largest
+        // e + 127 = ex - 6, at least 7
+        const uint32_t code = ex == 255u ? 255u : max((int)ex - 6, 7);
+        const float down = __uint_as_float((254u - code) << 23);   // 2^-e (unused for code 255)
+        uint32_t o[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t v = w[2 * z + e / 2];
+                const int m = __float2int_rn((e & 1 ? bf_hi(v) : bf_lo(v)) * down);
+                r |= (uint32_t)(uint8_t)max(-127, min(127, m)) << (8 * e);
+            }
+            o[z] = code == 255u ? 0u : r;
+        }
+        if (u < n) {
+            *reinterpret_cast<uint2*>(data + 8 * u) = make_uint2(o[0], o[1]);
+            if ((u & 3) == 0) exps[u / 4] = (uint8_t)code;
+        }
+    }
 }
 
-__device__ __forceinline__ void restore_unit(const uint8_t* ckpt, const Ckpt8Layout& L, int i, int64_t at, uint4* dst) {
-    const uint4 d = *reinterpret_cast<const uint4*>(ckpt + L.data[i] + 16 * at);
-    float x[16];
-    dequant16(d, exp_scale(ckpt[L.exps[i] + at / 2]), x);
-    dst[0] = make_uint4(pack_exact(x[0], x[1]), pack_exact(x[2], x[3]), pack_exact(x[4], x[5]), pack_exact(x[6], x[7]));
-    dst[1] = make_uint4(pack_exact(x[8], x[9]), pack_exact(x[10], x[11]), pack_exact(x[12], x[13]),
-                        pack_exact(x[14], x[15]));
+// kPer units of a thread from the checkpoint's section i to dst.
+__device__ __forceinline__ void restore_units(const uint8_t* ckpt, const Ckpt8Layout& L, int i, int64_t u0, int64_t n,
+                                              uint4* dst) {
+    const uint2* data = reinterpret_cast<const uint2*>(ckpt + L.data[i]);
+    const uint8_t* exps = ckpt + L.exps[i];
+    uint2 in[kPer];
+    uint32_t code[kPer];
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+        const int64_t u = min(u0 + y * kThreads, n - 1);
+        in[y] = data[u];
+        code[y] = exps[u / 4];
+    }
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+        const int64_t u = u0 + y * kThreads;
+        float x[8];
+        dequant8(in[y], exp_scale(code[y]), x);
+        if (u < n)
+            dst[u] = make_uint4(pack_exact(x[0], x[1]), pack_exact(x[2], x[3]), pack_exact(x[4], x[5]),
+                                pack_exact(x[6], x[7]));
+    }
 }
 
 __global__ void __launch_bounds__(kThreads)
-restore_kernel(const Tensors t, const uint8_t* __restrict__ ckpt, const Ckpt8Layout L) {
-    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (u >= t.end[3]) return;
-    int i = 0;
-#pragma unroll
-    for (int z = 0; z < 3; ++z) i += u >= t.end[z];
-    const int64_t at = u - (i ? t.end[i - 1] : 0);
-    restore_unit(ckpt, L, i, at, static_cast<uint4*>(t.dst[i]) + 2 * at);
+restore_kernel(const __grid_constant__ Tensors t, const uint8_t* __restrict__ ckpt,
+               const __grid_constant__ Ckpt8Layout L) {
+    const int i = tensor_of(t, blockIdx.x, 4);
+    restore_units(ckpt, L, i, (int64_t)(blockIdx.x - (i ? t.end[i - 1] : 0)) * (kPer * kThreads) + threadIdx.x, t.units[i],
+                  static_cast<uint4*>(t.dst[i]));
 }
 
 // ---------------------------------------------------------------- before the backward
 struct PrepArgs {
     int H, S, S_pad;
-    int64_t row_blocks;              // blocks that take query rows; the rest restore q, k, v
+    int row_blocks;                  // blocks that take query rows; the rest restore q, k, v
     const __nv_bfloat16* O;
     const uint4* dO;
     const float* lse;
@@ -124,62 +154,83 @@ struct PrepArgs {
     const uint8_t* ckpt;
 };
 
-// D / 16 threads take one row (b, i, h) of the padded range i < S_pad: Delta =
+// D / 8 threads take one row (b, i, h) of the padded range i < S_pad: Delta =
 // <dO, O> and p_shift - lse log2 e (so that a score's base-2 exponent is
 // one fused multiply-add), and the row's zeros in the head-major accumulator.
+// The blocks behind those restore q, k and v.
 template <int D, bool CKPT>
 __global__ void __launch_bounds__(kThreads)
-prep_kernel(const PrepArgs a, const Tensors t, const Ckpt8Layout L, int64_t n_rows) {
-    constexpr int T = D / 16;        // threads per row
-    if (CKPT && blockIdx.x >= a.row_blocks) {
-        const int64_t u = ((int64_t)blockIdx.x - a.row_blocks) * kThreads + threadIdx.x;
-        if (u >= t.end[2]) return;
-        const int i = (u >= t.end[0]) + (u >= t.end[1]);
-        const int64_t at = u - (i ? t.end[i - 1] : 0);
-        restore_unit(a.ckpt, L, i, at, static_cast<uint4*>(t.dst[i]) + 2 * at);
+prep_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Tensors t, const __grid_constant__ Ckpt8Layout L,
+            int n_rows) {
+    constexpr int T = D / 8;         // threads per row
+    if (CKPT && (int)blockIdx.x >= a.row_blocks) {
+        const int block = (int)blockIdx.x - a.row_blocks, i = tensor_of(t, block, 3);
+        restore_units(a.ckpt, L, i, (int64_t)(block - (i ? t.end[i - 1] : 0)) * (kPer * kThreads) + threadIdx.x, t.units[i],
+                      static_cast<uint4*>(t.dst[i]));
         return;
     }
-    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / T;
+    constexpr int R = 2;             // rows per thread, loaded before the first is used
     const int part = threadIdx.x % T;
-    const bool on = row < n_rows;    // threads past the last row stay for the shuffles
-    const int h = (int)(row % a.H);
-    const int64_t bi = row / a.H;
-    const int i = (int)(bi % a.S_pad);
-    const int64_t b = bi / a.S_pad, bh = b * a.H + h, dst = bh * a.S_pad + i;
-    float acc = 0.f;
-    const bool real = on && i < a.S;
-    if (real) {
-        const int64_t at = ((b * a.S + i) * a.H + h) * T + part;   // 16-element unit
-        float o[16];
-        if constexpr (CKPT) {
-            dequant16(*reinterpret_cast<const uint4*>(a.ckpt + L.data[3] + 16 * at),
-                      exp_scale(a.ckpt[L.exps[3] + at / 2]), o);
-        } else {
-            const uint4* p = reinterpret_cast<const uint4*>(a.O) + 2 * at;
-            const uint4 x = p[0], y = p[1];
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    // rows are counted in 32 bits: 2^31 rows of 64 elements would not fit in the memory
+    const uint32_t row0 = blockIdx.x * (uint32_t)(R * kThreads / T) + threadIdx.x / T;
+    uint4 od[R], dd[R];
+    uint32_t code[R];
+    int64_t at[R], dst[R], src[R];
+    bool on[R], real[R];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-                o[2 * z] = bf_lo(w[z]);
-                o[2 * z + 1] = bf_hi(w[z]);
+    for (int y = 0; y < R; ++y) {
+        const uint32_t row = row0 + y * (kThreads / T);
+        on[y] = row < (uint32_t)n_rows;
+        const uint32_t h = row % a.H, bi = row / a.H;
+        const int i = (int)(bi % a.S_pad);
+        const int64_t b = bi / a.S_pad, bh = b * a.H + h;
+        real[y] = on[y] && i < a.S;
+        dst[y] = bh * a.S_pad + i;
+        src[y] = bh * a.S + i;
+        at[y] = ((b * a.S + i) * a.H + h) * T + part;   // unit
+        if (real[y]) {
+            dd[y] = a.dO[at[y]];
+            if constexpr (CKPT) {
+                const uint2 u = reinterpret_cast<const uint2*>(a.ckpt + L.data[3])[at[y]];
+                od[y].x = u.x;
+                od[y].y = u.y;
+                code[y] = a.ckpt[L.exps[3] + at[y] / 4];
+            } else {
+                od[y] = reinterpret_cast<const uint4*>(a.O)[at[y]];
             }
         }
-        const uint4 x = a.dO[2 * at], y = a.dO[2 * at + 1];
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int z = 0; z < 8; ++z) {
-            acc = fmaf(o[2 * z], bf_lo(w[z]), acc);
-            acc = fmaf(o[2 * z + 1], bf_hi(w[z]), acc);
-        }
-        float4* zero = reinterpret_cast<float4*>(a.dq_acc + (bh * a.S + i) * D);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) zero[z * T + part] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int o = T / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (on && part == 0) {
-        a.delta[dst] = acc;
-        a.nlse2[dst] = real ? fmaf(a.lse[bh * a.S + i], -1.4426950408889634f, a.p_shift) : 0.f;
+    for (int y = 0; y < R; ++y) {
+        float acc = 0.f;
+        if (real[y]) {
+            float o[8];
+            if constexpr (CKPT) {
+                dequant8(make_uint2(od[y].x, od[y].y), exp_scale(code[y]), o);
+            } else {
+                const uint32_t w[4] = {od[y].x, od[y].y, od[y].z, od[y].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    o[2 * z] = bf_lo(w[z]);
+                    o[2 * z + 1] = bf_hi(w[z]);
+                }
+            }
+            const uint32_t w[4] = {dd[y].x, dd[y].y, dd[y].z, dd[y].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                acc = fmaf(o[2 * z], bf_lo(w[z]), acc);
+                acc = fmaf(o[2 * z + 1], bf_hi(w[z]), acc);
+            }
+            float4* zero = reinterpret_cast<float4*>(a.dq_acc + src[y] * D);
+            zero[part] = make_float4(0.f, 0.f, 0.f, 0.f);
+            zero[T + part] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (on[y] && part == 0) {
+            a.delta[dst[y]] = acc;
+            a.nlse2[dst[y]] = real[y] ? fmaf(a.lse[src[y]], -1.4426950408889634f, a.p_shift) : 0.f;
+        }
     }
 }
 
@@ -195,21 +246,29 @@ __device__ __forceinline__ uint4 pack8(const float4& a, const float4& b, float c
 // per thread, in the pieces' order.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-finish_kernel(int H, int Hkv, int S, int rows, int n_pieces, float scale, int64_t dq_blocks, int64_t n8,
+finish_kernel(int H, int Hkv, int S, int rows, int n_pieces, float scale, int dq_blocks, int n_rows,
               const float* __restrict__ acc, const float* __restrict__ slabs, uint4* __restrict__ dQ,
               uint4* __restrict__ dK, uint4* __restrict__ dV) {
     constexpr int T = D / 8;
-    if (blockIdx.x < dq_blocks) {
-        const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-        if (x >= n8) return;
-        const int part = (int)(x % T);
-        const int64_t r = x / T;
-        const int h = (int)(r % H);
-        const int64_t bs = r / H;
-        const int s = (int)(bs % S);
-        const int64_t b = bs / S;
-        const float4* src = reinterpret_cast<const float4*>(acc + ((b * H + h) * S + s) * D) + 2 * part;
-        dQ[x] = pack8(src[0], src[1], scale);
+    if ((int)blockIdx.x < dq_blocks) {
+        constexpr int R = 2;         // rows per thread, loaded before the first is used
+        const int part = threadIdx.x % T;
+        const uint32_t row0 = blockIdx.x * (uint32_t)(R * kThreads / T) + threadIdx.x / T;
+        float4 a[R], b[R];
+#pragma unroll
+        for (int y = 0; y < R; ++y) {
+            const uint32_t row = min(row0 + y * (kThreads / T), (uint32_t)n_rows - 1);
+            const uint32_t h = row % H, bs = row / H, s = bs % S;
+            const int64_t bb = bs / S;
+            const float4* src = reinterpret_cast<const float4*>(acc + ((bb * H + h) * S + s) * D) + 2 * part;
+            a[y] = src[0];
+            b[y] = src[1];
+        }
+#pragma unroll
+        for (int y = 0; y < R; ++y) {
+            const uint32_t row = row0 + y * (kThreads / T);
+            if (row < (uint32_t)n_rows) dQ[(int64_t)row * T + part] = pack8(a[y], b[y], scale);
+        }
         return;
     }
     const int64_t x = ((int64_t)blockIdx.x - dq_blocks) * kThreads + threadIdx.x;   // (row, dK or dV, key, part)
@@ -253,25 +312,32 @@ Ckpt8Layout ckpt8_layout(int B, int H, int Hkv, int S, int D) {
     return L;
 }
 
+namespace {
+// Blocks for the first n tensors of a checkpoint; returns how many there are.
+int split_blocks(const Ckpt8Layout& L, int n, Tensors* t) {
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i) {
+        t->units[i] = L.n[i] / 8;
+        blocks += (t->units[i] + kPer * kThreads - 1) / (kPer * kThreads);
+        t->end[i] = (int)blocks;     // B * S * H * D < 2^44 / 8192 elements by the callers' checks
+    }
+    return (int)blocks;
+}
+}  // namespace
+
 dfa_status launch_ckpt8_save(const Ckpt8Layout& L, const void* const src[4], void* ckpt, cudaStream_t s) {
     Tensors t{};
-    int64_t n = 0;
-    for (int i = 0; i < 4; ++i) {
-        t.src[i] = src[i];
-        t.end[i] = n += L.n[i] / 16;
-    }
-    save_kernel<<<(unsigned)blocks_for(n), kThreads, 0, s>>>(t, static_cast<uint8_t*>(ckpt), L);
+    for (int i = 0; i < 4; ++i) t.src[i] = src[i];
+    const int blocks = split_blocks(L, 4, &t);
+    save_kernel<<<blocks, kThreads, 0, s>>>(t, static_cast<uint8_t*>(ckpt), L);
     return launched("checkpoint save");
 }
 
 dfa_status launch_ckpt8_restore(const Ckpt8Layout& L, const void* ckpt, void* const dst[4], cudaStream_t s) {
     Tensors t{};
-    int64_t n = 0;
-    for (int i = 0; i < 4; ++i) {
-        t.dst[i] = dst[i];
-        t.end[i] = n += L.n[i] / 16;
-    }
-    restore_kernel<<<(unsigned)blocks_for(n), kThreads, 0, s>>>(t, static_cast<const uint8_t*>(ckpt), L);
+    for (int i = 0; i < 4; ++i) t.dst[i] = dst[i];
+    const int blocks = split_blocks(L, 4, &t);
+    restore_kernel<<<blocks, kThreads, 0, s>>>(t, static_cast<const uint8_t*>(ckpt), L);
     return launched("checkpoint restore");
 }
 
@@ -284,17 +350,16 @@ dfa_status launch_sink_prep(const SinkProblem& p, int S_pad, const void* O, cons
     a.dO = static_cast<const uint4*>(dO);
     a.lse = lse; a.p_shift = (float)p.p_shift; a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
     a.ckpt = static_cast<const uint8_t*>(ckpt);
-    const int64_t n_rows = (int64_t)p.B * S_pad * p.H;
-    a.row_blocks = blocks_for(n_rows * (p.D / 16));
+    const int n_rows = p.B * S_pad * p.H, per = 2 * kThreads / (p.D / 8);
+    a.row_blocks = (n_rows - 1) / per + 1;
     Tensors t{};
-    int64_t n = 0;
-    if (ckpt)
-        for (int i = 0; i < 3; ++i) {
-            t.dst[i] = qkv[i];
-            t.end[i] = n += L->n[i] / 16;
-        }
+    int more = 0;
+    if (ckpt) {
+        for (int i = 0; i < 3; ++i) t.dst[i] = qkv[i];
+        more = split_blocks(*L, 3, &t);
+    }
+    const unsigned grid = (unsigned)(a.row_blocks + more);
     const Ckpt8Layout none{};
-    const unsigned grid = (unsigned)(a.row_blocks + blocks_for(n));
     const Ckpt8Layout& l = ckpt ? *L : none;
     if (p.D == 128) {
         if (ckpt) prep_kernel<128, true><<<grid, kThreads, 0, s>>>(a, t, l, n_rows);
@@ -308,16 +373,17 @@ dfa_status launch_sink_prep(const SinkProblem& p, int S_pad, const void* O, cons
 
 dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, const float* dq_acc, const float* slabs,
                               void* dQ, void* dK, void* dV, cudaStream_t s) {
-    const int64_t n8 = (int64_t)p.B * p.S * p.H * p.D / 8, dq_blocks = blocks_for(n8);
+    const int n_rows = p.B * p.S * p.H, per = 2 * kThreads / (p.D / 8);
+    const int dq_blocks = (n_rows - 1) / per + 1;
     const int rows = p.B * p.Hkv;
     const float scale = p.scale / (1 << p.p_shift);
     const int64_t extra = plan.n_pieces > 1 ? blocks_for((int64_t)rows * 2 * 128 * p.D / 8) : 0;
     const unsigned grid = (unsigned)(dq_blocks + extra);
     if (p.D == 128)
-        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n8, dq_acc,
+        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n_rows, dq_acc,
                                                      slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     else
-        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n8, dq_acc,
+        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n_rows, dq_acc,
                                                     slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     return launched("windowed backward finish");
 }

@@ -239,6 +239,16 @@ int* device_error_flag() {
     return g_err_ptr[d];
 }
 
+bool first_on_device(std::atomic<uint64_t>& seen) {
+    const int d = current_device();
+    return d < 0 || !(seen.load(std::memory_order_acquire) >> d & 1);
+}
+
+void mark_on_device(std::atomic<uint64_t>& seen) {
+    const int d = current_device();
+    if (d >= 0) seen.fetch_or(1ull << d, std::memory_order_release);
+}
+
 int num_sms() {
     const int d = current_device();
     if (d < 0) return 1;
@@ -853,8 +863,14 @@ dfa_status check_sink(dfa_dtype dt, int B, int H, int Hkv, int S, int D, int win
     if (n_sink < 0) return fail(DFA_ERR_INVALID_ARG, "n_sink must be >= 0 (got %d)", n_sink);
     if (n_sink > kMaxSinks)
         return fail(DFA_ERR_UNSUPPORTED, "n_sink=%d: at most %d tokens can stay visible", n_sink, kMaxSinks);
-    // item counts, tile positions and grid sizes are 32-bit
-    if ((int64_t)B * H > (1 << 24) || (int64_t)B * H * ((S + 127) / 128 + 64) > (1 << 30) || S > (1 << 30))
+    if ((int64_t)B * H > (1 << 24) || S > (1 << 30))
+        return fail(DFA_ERR_INVALID_ARG, "problem too large (B*H=%lld heads of %d tokens)", (long long)B * H, S);
+    return DFA_OK;
+}
+
+// The whole-sequence calls count rows, items and blocks in 32 bits.
+dfa_status check_sink_rows(int B, int H, int S) {
+    if ((int64_t)B * H * ((S + 127) / 128 + 64) > (1 << 24))
         return fail(DFA_ERR_INVALID_ARG, "problem too large (B*H=%lld heads of %d tokens)", (long long)B * H, S);
     return DFA_OK;
 }
@@ -918,7 +934,7 @@ dfa_status check_ws(void* ws, size_t have, size_t need) {
 
 bool sink_sizes_ok(int B, int H, int Hkv, int S, int D, int window, int n_sink) {
     const std::string keep = g_msg;   // a size query does not change dfa_last_error()
-    const bool ok = check_sink(DFA_BF16, B, H, Hkv, S, D, window, n_sink, 1.f) == DFA_OK;
+    const bool ok = !check_sink(DFA_BF16, B, H, Hkv, S, D, window, n_sink, 1.f) && !check_sink_rows(B, H, S);
     snprintf(g_msg, sizeof(g_msg), "%s", keep.c_str());
     return ok;
 }
@@ -930,7 +946,7 @@ extern "C" dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void
                                         float* lse, void* stream) {
     g_msg[0] = 0;
     dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
-    if (st || (int64_t)B * S == 0) return st;
+    if (st || (st = check_sink_rows(B, H, S)) || (int64_t)B * S == 0) return st;
     if ((st = check_ptrs({q, k, v, O, lse}))) return st;
     st = tc_sink_fwd(sink_problem(B, H, H_kv, S, D, window, n_sink, scale), q, k, v, O, lse,
                      static_cast<cudaStream_t>(stream));
@@ -949,7 +965,7 @@ extern "C" dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void
                                         void* workspace, size_t ws_bytes, void* stream) {
     g_msg[0] = 0;
     dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
-    if (st || (int64_t)B * S == 0) return st;
+    if (st || (st = check_sink_rows(B, H, S)) || (int64_t)B * S == 0) return st;
     const SinkProblem p = sink_problem(B, H, H_kv, S, D, window, n_sink, scale);
     if ((st = check_ws(workspace, ws_bytes, sink_ws(p, false).total))) return st;
     if ((st = check_ptrs({q, k, v, O, lse, dO, dQ, dK, dV}))) return st;
@@ -1009,7 +1025,7 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
 // ---------------------------------------------------------------- 8-bit attention checkpoints
 static dfa_status check_ckpt(dfa_dtype dt, int B, int H, int H_kv, int S, int D, const void* ckpt, size_t have) {
     dfa_status st = check_sink(dt, B, H, H_kv, S, D, 1, 0, 1.f);
-    if (st || (int64_t)B * S == 0) return st;
+    if (st || (st = check_sink_rows(B, H, S)) || (int64_t)B * S == 0) return st;
     const size_t need = ckpt8_layout(B, H, H_kv, S, D).total;
     if (!ckpt || have < need) return fail(DFA_ERR_INVALID_ARG, "checkpoint of %zu bytes needed, %zu given", need, have);
     if (!aligned16(ckpt)) return fail(DFA_ERR_INVALID_ARG, "checkpoint is not 16-byte aligned");

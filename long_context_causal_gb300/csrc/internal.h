@@ -2,6 +2,7 @@
 // Not part of the public ABI (that is include/dfa.h).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -194,6 +195,12 @@ __host__ __device__ inline int snake_count(int n_items, int cta, int n) {
 }
 
 int num_sms();
+
+// Settings made once per device and kernel (attribute queries cost a launch a
+// microsecond each): whether the current device is not in `seen` yet, and its
+// entry there.
+bool first_on_device(std::atomic<uint64_t>& seen);
+void mark_on_device(std::atomic<uint64_t>& seen);
 
 // A sequence of S tokens cut into n_chunks chunks (DISTFLASHATTN §3.1: one
 // chunk per worker): every chunk but the last holds ceil(S / n_chunks)

@@ -467,8 +467,14 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     const int64_t tiles = (int64_t)segments * decode_tiles(p);
     const int n = (int)std::min<int64_t>(num_sms(), tiles);
     const int smem = C::kOffPrefix + (int)sizeof(int) * (p.B + 1);
-    if (cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return fail(DFA_ERR_CUDA, "decode: shared memory attribute");
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        constexpr int most = C::kOffPrefix + (int)sizeof(int) * (kMaxDecodeBatch + 1);
+        static_assert(most <= 232448, "shared memory");
+        if (cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "decode: shared memory attribute");
+        mark_on_device(seen);
+    }
     decode_kernel<D><<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));

@@ -473,8 +473,12 @@ dfa_status launch(const SinkProblem& p, const void* q, const void* k, const void
     a.err = device_error_flag();
     const int smem = Cfg<D>::kSmem;
     auto kern = sink_fwd_kernel<D>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return fail(DFA_ERR_CUDA, "sink_fwd: shared memory attribute");
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "sink_fwd: shared memory attribute");
+        mark_on_device(seen);
+    }
     kern<<<std::min(num_sms(), a.n_items), kThreads, smem, s>>>(mq, mk, mv, a);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink_fwd launch: %s", cudaGetErrorString(e));

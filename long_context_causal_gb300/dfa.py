@@ -430,25 +430,42 @@ def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: f
 
 
 # -------------------------------------------- sliding window of tokens with sinks, 8-bit checkpoints
-def _on_gpu(q, *named):
+# A call's checks and allocations are most of what a short problem costs, so
+# these functions take the cheapest accessors there are (pointers as plain
+# ints, devices as their index, the current stream without a Stream object).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _same_gpu(*named) -> int:
     """Every tensor must lie on the current CUDA device: the library launches
-    there, on the pointers it is given."""
-    for t, name in named:
-        if not t.is_cuda or t.device != q.device:
-            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others, got {t.device}")
-    if q.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
+    there, on the pointers it is given.  Returns its index."""
+    d = named[0].get_device()
+    for t in named:
+        if d < 0 or t.get_device() != d:
+            raise ValueError(f"the tensors must be CUDA tensors on one device, got {[str(x.device) for x in named]}")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _on(stream, d: int) -> int:
+    """Handle of the stream a call runs on (None: the current one)."""
+    if stream is None:
+        return _raw_stream(d)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _sizes(q, k, v):
     """B, S, H, H_kv, D of dense q [B,S,H,D] and k, v [B,S,H_kv,D]."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
-        raise ValueError(f"q must be [B, S, H, D] and k, v [B, S, H_kv, D], got {tuple(q.shape)}, {tuple(k.shape)}, "
-                         f"{tuple(v.shape)}")
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or ks != v.shape or ks[0] != qs[0] or ks[1] != qs[1] or ks[3] != qs[3]:
+        raise ValueError(f"q must be [B, S, H, D] and k, v [B, S, H_kv, D], got {tuple(qs)}, {tuple(ks)}, {tuple(v.shape)}")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have the same dtype")
-    B, S, H, D = q.shape
-    return B, S, H, k.shape[2], D
+    _dense(q, "q")
+    _dense(k, "k")
+    _dense(v, "v")
+    return qs[0], qs[1], qs[2], ks[2], qs[3]
 
 
 def _scratch(nbytes, device, stream):
@@ -467,54 +484,48 @@ def _bytes_buf(t, name, device):
     return t
 
 
+def _out(t, name, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _like(t, name, shape, dtype, device)
+
+
 def dfa_attn_fwd_sink(q, k, v, window: int, n_sink: int = 0, scale: float | None = None, O=None, lse=None,
                       stream=None):
     """Causal forward over a sliding window of `window` tokens and the first
     `n_sink` ones: returns (O [B,S,H,D], lse fp32 [B,H,S])."""
     B, S, H, Hkv, D = _sizes(q, k, v)
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _dense(t, n)
-    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
+    d = _same_gpu(q, k, v)
     O = torch.empty_like(q) if O is None else _like(O, "O", q.shape, q.dtype, q.device)
-    lse = (torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None
-           else _like(lse, "lse", (B, H, S), torch.float32, q.device))
-    _check(_lib.dfa_attn_fwd_sink(_ptr(q), _ptr(k), _ptr(v), _dtype(q), B, H, Hkv, S, D, int(window), int(n_sink),
-                                  D ** -0.5 if scale is None else float(scale), _ptr(O), _ptr(lse), _stream(stream)))
+    lse = _out(lse, "lse", (B, H, S), torch.float32, q.device)
+    _check(_lib.dfa_attn_fwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), B, H, Hkv, S, D, window, n_sink,
+                                  D ** -0.5 if scale is None else scale, O.data_ptr(), lse.data_ptr(), _on(stream, d)))
     return O, lse
 
 
 def dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
-    return int(_lib.dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, int(window), int(n_sink)))
-
-
-def _grads(q_shape, k_shape, dtype, device, dQ, dK, dV):
-    out = []
-    for t, name, shape in ((dQ, "dQ", q_shape), (dK, "dK", k_shape), (dV, "dV", k_shape)):
-        out.append(torch.empty(shape, dtype=dtype, device=device) if t is None else _like(t, name, shape, dtype, device))
-    return out
+    return _lib.dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, window, n_sink)
 
 
 def dfa_attn_bwd_sink(q, k, v, O, lse, dO, window: int, n_sink: int = 0, scale: float | None = None, dQ=None,
                       dK=None, dV=None, workspace_buf=None, stream=None):
     """Backward of dfa_attn_fwd_sink from the saved (O, lse): returns (dQ, dK, dV)."""
     B, S, H, Hkv, D = _sizes(q, k, v)
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _dense(t, n)
-    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
-    _like(O, "O", q.shape, q.dtype, q.device)
-    _like(dO, "dO", q.shape, q.dtype, q.device)
-    _like(lse, "lse", (B, H, S), torch.float32, q.device)
-    dQ, dK, dV = _grads(q.shape, k.shape, q.dtype, q.device, dQ, dK, dV)
-    ws = (_scratch(dfa_attn_bwd_sink_workspace_size(B, H, Hkv, S, D, window, n_sink), q.device, stream)
-          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", q.device))
-    _check(_lib.dfa_attn_bwd_sink(_ptr(q), _ptr(k), _ptr(v), _ptr(O), _ptr(lse), _ptr(dO), _dtype(q), B, H, Hkv, S, D,
-                                  int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), _ptr(dQ),
-                                  _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
+    d, dev = _same_gpu(q, k, v), q.device
+    _like(O, "O", q.shape, q.dtype, dev)
+    _like(dO, "dO", q.shape, q.dtype, dev)
+    _like(lse, "lse", (B, H, S), torch.float32, dev)
+    dQ = _out(dQ, "dQ", q.shape, q.dtype, dev)
+    dK = _out(dK, "dK", k.shape, q.dtype, dev)
+    dV = _out(dV, "dV", k.shape, q.dtype, dev)
+    ws = (_scratch(_lib.dfa_attn_bwd_sink_workspace_size(B, H, Hkv, S, D, window, n_sink), dev, stream)
+          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", dev))
+    _check(_lib.dfa_attn_bwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+                                  _dtype(q), B, H, Hkv, S, D, window, n_sink, D ** -0.5 if scale is None else scale,
+                                  dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d)))
     return dQ, dK, dV
 
 
 def dfa_attn_decode_sink_workspace_size(B, H, H_kv, D) -> int:
-    return int(_lib.dfa_attn_decode_sink_workspace_size(B, H, H_kv, D))
+    return _lib.dfa_attn_decode_sink_workspace_size(B, H, H_kv, D)
 
 
 def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: float | None = None, O=None, lse=None,
@@ -522,83 +533,83 @@ def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: f
     """One new token per sequence over a cache: q [B,H,D], k, v [B,S_max,H_kv,D]
     (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
     GPU; returns (O [B,H,D], lse fp32 [B,H])."""
-    if q.dim() != 3 or k.dim() != 4 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[2]:
-        raise ValueError(f"q must be [B, H, D] and k, v [B, S_max, H_kv, D], got {tuple(q.shape)}, {tuple(k.shape)}, "
-                         f"{tuple(v.shape)}")
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 4 or ks != v.shape or ks[0] != qs[0] or ks[3] != qs[2]:
+        raise ValueError(f"q must be [B, H, D] and k, v [B, S_max, H_kv, D], got {tuple(qs)}, {tuple(ks)}, {tuple(v.shape)}")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have the same dtype")
-    ks = k.stride()
-    if ks != v.stride() or ks[3] != 1:
+    st = k.stride()
+    if st != v.stride() or st[3] != 1:
         raise ValueError("k and v must share their strides, with the head dimension contiguous")
-    B, H, D = q.shape
-    _, S, Hkv, _ = k.shape
+    B, H, D = qs
     _dense(q, "q")
-    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
-    _like(kv_len, "kv_len", (B,), torch.int32, q.device)
-    O = torch.empty_like(q) if O is None else _like(O, "O", q.shape, q.dtype, q.device)
-    lse = (torch.empty((B, H), dtype=torch.float32, device=q.device) if lse is None
-           else _like(lse, "lse", (B, H), torch.float32, q.device))
-    ws = (_scratch(dfa_attn_decode_sink_workspace_size(B, H, Hkv, D), q.device, stream) if workspace_buf is None
-          else _bytes_buf(workspace_buf, "workspace_buf", q.device))
-    _check(_lib.dfa_attn_decode_sink(_ptr(q), _ptr(k), _ptr(v), _dtype(q), B, H, Hkv, S, D, (ctypes.c_int64 * 3)(*ks[:3]),
-                                     _ptr(kv_len), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale),
-                                     _ptr(O), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    d, dev = _same_gpu(q, k, v), q.device
+    _like(kv_len, "kv_len", (B,), torch.int32, dev)
+    O = torch.empty_like(q) if O is None else _like(O, "O", qs, q.dtype, dev)
+    lse = _out(lse, "lse", (B, H), torch.float32, dev)
+    ws = (_scratch(_lib.dfa_attn_decode_sink_workspace_size(B, H, ks[2], D), dev, stream) if workspace_buf is None
+          else _bytes_buf(workspace_buf, "workspace_buf", dev))
+    strides = None if k.is_contiguous() else (ctypes.c_int64 * 3)(*st[:3])
+    _check(_lib.dfa_attn_decode_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), B, H, ks[2], ks[1], D, strides,
+                                     kv_len.data_ptr(), window, n_sink, D ** -0.5 if scale is None else scale, O.data_ptr(),
+                                     lse.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d)))
     return O, lse
 
 
 def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:
-    return int(_lib.dfa_ckpt8_size(B, H, H_kv, S, D))
+    return _lib.dfa_ckpt8_size(B, H, H_kv, S, D)
 
 
 def dfa_ckpt8_save(q, k, v, O, ckpt=None, stream=None):
     """q, k, v and O of one attention layer in 8 bits: returns the checkpoint
     (a uint8 tensor of dfa_ckpt8_size bytes)."""
     B, S, H, Hkv, D = _sizes(q, k, v)
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _dense(t, n)
-    _on_gpu(q, (q, "q"), (k, "k"), (v, "v"))
-    _like(O, "O", q.shape, q.dtype, q.device)
-    ckpt = (torch.empty(dfa_ckpt8_size(B, H, Hkv, S, D), dtype=torch.uint8, device=q.device) if ckpt is None
-            else _bytes_buf(ckpt, "ckpt", q.device))
-    _check(_lib.dfa_ckpt8_save(_ptr(q), _ptr(k), _ptr(v), _ptr(O), _dtype(q), B, H, Hkv, S, D, _ptr(ckpt), ckpt.numel(),
-                               _stream(stream)))
+    d, dev = _same_gpu(q, k, v), q.device
+    _like(O, "O", q.shape, q.dtype, dev)
+    ckpt = (torch.empty(_lib.dfa_ckpt8_size(B, H, Hkv, S, D), dtype=torch.uint8, device=dev) if ckpt is None
+            else _bytes_buf(ckpt, "ckpt", dev))
+    _check(_lib.dfa_ckpt8_save(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), _dtype(q), B, H, Hkv, S, D,
+                               ckpt.data_ptr(), ckpt.numel(), _on(stream, d)))
     return ckpt
 
 
 def dfa_ckpt8_restore(ckpt, B: int, H: int, H_kv: int, S: int, D: int, q=None, k=None, v=None, O=None, stream=None):
     """The bf16 tensors (q, k, v, O) a checkpoint stands for."""
-    _bytes_buf(ckpt, "ckpt", ckpt.device)
-    _on_gpu(ckpt, (ckpt, "ckpt"))
-    out = []
-    for t, name, heads in ((q, "q", H), (k, "k", H_kv), (v, "v", H_kv), (O, "O", H)):
-        shape = (B, S, heads, D)
-        out.append(torch.empty(shape, dtype=torch.bfloat16, device=ckpt.device) if t is None
-                   else _like(t, name, shape, torch.bfloat16, ckpt.device))
-    _check(_lib.dfa_ckpt8_restore(_ptr(ckpt), ckpt.numel(), DFA_BF16, B, H, H_kv, S, D, *(_ptr(t) for t in out),
-                                  _stream(stream)))
-    return tuple(out)
+    d, dev, bf = _same_gpu(ckpt), ckpt.device, torch.bfloat16
+    _bytes_buf(ckpt, "ckpt", dev)
+    q = _out(q, "q", (B, S, H, D), bf, dev)
+    k = _out(k, "k", (B, S, H_kv, D), bf, dev)
+    v = _out(v, "v", (B, S, H_kv, D), bf, dev)
+    O = _out(O, "O", (B, S, H, D), bf, dev)
+    _check(_lib.dfa_ckpt8_restore(ckpt.data_ptr(), ckpt.numel(), DFA_BF16, B, H, H_kv, S, D, q.data_ptr(), k.data_ptr(),
+                                  v.data_ptr(), O.data_ptr(), _on(stream, d)))
+    return q, k, v, O
 
 
 def dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
-    return int(_lib.dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, int(window), int(n_sink)))
+    return _lib.dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink)
 
 
 def dfa_attn_bwd_ckpt8(ckpt, lse, dO, H_kv: int, window: int | None = None, n_sink: int = 0,
                        scale: float | None = None, dQ=None, dK=None, dV=None, workspace_buf=None, stream=None):
     """Backward from an 8-bit checkpoint, the saved lse and dO [B,S,H,D], with
     the forward's window (None: plain causal): returns (dQ, dK, dV)."""
+    if dO.dim() != 4:
+        raise ValueError(f"dO must be [B, S, H, D], got {tuple(dO.shape)}")
     B, S, H, D = dO.shape
     _dense(dO, "dO")
-    _on_gpu(dO, (dO, "dO"), (ckpt, "ckpt"))
-    _bytes_buf(ckpt, "ckpt", dO.device)
-    _like(lse, "lse", (B, H, S), torch.float32, dO.device)
-    window = max(S, 1) if window is None else int(window)
-    dQ, dK, dV = _grads(dO.shape, (B, S, H_kv, D), dO.dtype, dO.device, dQ, dK, dV)
-    ws = (_scratch(dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink), dO.device, stream)
-          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", dO.device))
-    _check(_lib.dfa_attn_bwd_ckpt8(_ptr(ckpt), ckpt.numel(), _ptr(lse), _ptr(dO), _dtype(dO), B, H, H_kv, S, D, window,
-                                   int(n_sink), D ** -0.5 if scale is None else float(scale), _ptr(dQ), _ptr(dK),
-                                   _ptr(dV), _ptr(ws), ws.numel(), _stream(stream)))
+    d, dev = _same_gpu(dO, ckpt), dO.device
+    _bytes_buf(ckpt, "ckpt", dev)
+    _like(lse, "lse", (B, H, S), torch.float32, dev)
+    window = max(S, 1) if window is None else window
+    dQ = _out(dQ, "dQ", (B, S, H, D), dO.dtype, dev)
+    dK = _out(dK, "dK", (B, S, H_kv, D), dO.dtype, dev)
+    dV = _out(dV, "dV", (B, S, H_kv, D), dO.dtype, dev)
+    ws = (_scratch(_lib.dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink), dev, stream)
+          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", dev))
+    _check(_lib.dfa_attn_bwd_ckpt8(ckpt.data_ptr(), ckpt.numel(), lse.data_ptr(), dO.data_ptr(), _dtype(dO), B, H, H_kv, S,
+                                   D, window, n_sink, D ** -0.5 if scale is None else scale, dQ.data_ptr(), dK.data_ptr(),
+                                   dV.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d)))
     return dQ, dK, dV
 
 
