@@ -50,6 +50,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "sink_bwd.cuh"
 
 namespace dfa {
 namespace {
@@ -64,8 +65,10 @@ constexpr int kSide = 1024;                        // nlse2[128] + Delta[128] pe
 constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile, kOffDS = 6 * kTile;
 constexpr int kOffSide = kOffDS + 32768;
 constexpr int kOffBar = kOffSide + 2 * kSide;
-constexpr int kSmem = kOffBar + 256;
-static_assert(kSmem <= 232448, "shared memory");
+constexpr int kOffItems = kOffBar + 256;                   // SINK: item records
+constexpr int kSmem = kOffItems;
+constexpr int kSmemSink = kOffItems + kPlanItems * 16;
+static_assert(kSmemSink <= 232448, "shared memory");
 
 constexpr uint32_t kColDV = 0, kColDK = 128, kColS = 256, kColDP = 384;
 
@@ -98,8 +101,8 @@ struct Args {
     int n_units;
     int n_split, piece_tiles;     // split-kv pieces of each key tile's query range (SPLIT)
     int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
-    int n_items, n_pieces;        // ... items, of which the first n_pieces * rows are pieces of key tile 0
-    float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
+    int n_items;                  // ... items (sink_bwd.cuh)
+    float* slabs;                 // ... and the pieces' partial dK, dV
     int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers
     float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
@@ -118,8 +121,9 @@ struct Args {
 struct Item {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head; ntiles over the group's heads
     bool down;                      // sweep query tiles from the last one down
-    int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
+    int slab;                       // SINK: a piece's slab, -1 for a whole list
     bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
+    int off;                        // SINK: first tile of a piece in the key tile's list
     // k-th tile of the item: head h of the group, query tile i
     __device__ __forceinline__ void tile(int k, int G, int& h, int& i) const {
         const int len = i1 - i0, r = k % len;
@@ -128,12 +132,37 @@ struct Item {
     }
 };
 
-// SINK: a sliding window of tokens with sinks (n_split unused; no work list).
-// Costs fall along the items -- the pieces of key tile 0, which the sinks make
-// visible to every query, then the key tiles upwards, which see the window's
-// worth of query tiles until the sequence ends -- and the CTAs take them in a
-// snake.  A piece stores its partial dK, dV to a slab of its own, summed in
-// order afterwards, so dK and dV have the same bits on every call.
+// The tiles of an item one after another: (head, query tile).  SINK steps to
+// the next one; the others divide (their sweeps may run downwards).
+template <bool SINK>
+struct Sweep {
+    int h, i;
+    __device__ __forceinline__ Sweep(const Item& x, int G) {
+        if constexpr (SINK) {
+            const int len = x.i1 - x.i0;
+            h = x.g * G + x.off / len;
+            i = x.i0 + x.off % len;
+        }
+    }
+    __device__ __forceinline__ void next(const Item& x, int G, int k, int& hk, int& ik) {
+        if constexpr (SINK) {
+            hk = h;
+            ik = i;
+            if (++i == x.i1) {
+                i = x.i0;
+                ++h;
+            }
+        } else {
+            x.tile(k, G, hk, ik);
+        }
+    }
+};
+
+// SINK: a sliding window of tokens with sinks; the items are sink_bwd.cuh's, no
+// work list is uploaded.  Costs fall along them -- the pieces of key tile 0,
+// which the sinks make visible to every query, then the key tiles upwards,
+// which see the window's worth of query tiles until the sequence ends -- and
+// the CTAs take them in a snake.
 //
 // Roundings of the SINK variant.  P is computed times 2^p_shift (the shift is
 // in nlse2, and undone exactly in scale and scale_v).  It is rounded to bf16
@@ -153,30 +182,32 @@ struct Item {
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a
 // separate instantiation in which the sequence base is 0 and the lengths are
 // the problem's, so it keeps its registers for the tile loop.
+template <bool SINK>
+using Plan = std::conditional_t<SINK, SinkBwdPlan, int>;   // an unused int elsewhere
+
 template <bool VARLEN, bool SPLIT, bool SINK>
-__device__ __forceinline__ Item decode(const Args& a, int it) {
+__device__ __forceinline__ Item decode(const Args& a, const Plan<SINK>& plan, const int4* s_items, int it) {
     Item x;
     x.slab = -1;
     x.fine = false;
-    if constexpr (SINK) {
-        const int rows = a.B * a.Hkv;
-        x.n_q = a.n_units;
-        if (a.n_pieces > 1 && it < a.n_pieces * rows) {
-            x.slab = it;
-            x.t = 0;
-            x.i0 = it / rows * a.piece_tiles;
-            x.i1 = min(x.i0 + a.piece_tiles, x.n_q);
+    x.off = 0;
+    if constexpr (SINK) {   // `it` counts the CTA's own items
+        SinkItem w;
+        if (plan.cut_all) {
+            const int4 rec = s_items[it];
+            w = SinkItem{rec.x, rec.y, rec.z, rec.w >> 1, (rec.w & 1) != 0};
         } else {
-            if (a.n_pieces > 1) it -= (a.n_pieces - 1) * rows;   // key tile 0 is done in pieces
-            x.t = it / rows;
-            x.i0 = x.t;
-            // the last query that sees the tile's last key: its position + window - 1
-            x.i1 = x.t == 0 && a.n_sink > 0 ? x.n_q : min((x.t * BT + BT - 1 + a.window - 1) / BT + 1, x.n_q);
+            w = sink_item(plan, snake_item(it, blockIdx.x, gridDim.x));
         }
-        const int row = it % rows;
-        x.b = row / a.Hkv;
-        x.g = row % a.Hkv;
-        x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
+        x.t = w.t;
+        x.b = w.row / a.Hkv;
+        x.g = w.row % a.Hkv;
+        x.n_q = plan.n_q;
+        x.i0 = x.t;
+        x.i1 = x.t + sink_range(plan, x.t);
+        x.off = w.off;
+        x.ntiles = w.n;
+        x.slab = w.whole ? -1 : snake_item(it, blockIdx.x, gridDim.x);
         x.down = false;
         x.fine = x.t == 0 && a.fine0;
         return x;
@@ -222,7 +253,7 @@ __device__ __forceinline__ Item decode(const Args& a, int it) {
 // holding it in registers across the tile loop (the warps here run at the
 // register limit, and a few more live values cost about a tenth of the speed).
 // Value of the CTA's it-th item.
-#define ITEM(it) (SINK ? snake_item(it, blockIdx.x, gridDim.x) : a.wl_items[it])
+#define ITEM(it) (SINK ? (it) : a.wl_items[it])
 #define SEQ_LQ(x) (VARLEN ? a.seq[(x).b + 1] - a.seq[(x).b] : a.Lq)
 #define SEQ_LKV(x) (VARLEN ? a.seq[(x).b + 1] - a.seq[(x).b] : a.Lkv)
 #define SEQ_BASE(x) (VARLEN ? a.seq[(x).b] : 0)
@@ -232,7 +263,8 @@ __device__ __forceinline__ Item decode(const Args& a, int it) {
 template <bool VARLEN, bool SPLIT, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const Args a) {
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const Args a,
+              const __grid_constant__ Plan<SINK> plan) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err) atomicExch(a.err, 2);
@@ -269,6 +301,13 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
     const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
+    int4* s_items = reinterpret_cast<int4*>(smem + kOffItems);   // SINK, plan.cut_all: this CTA's items
+    if constexpr (SINK) {
+        if (plan.cut_all && (int)threadIdx.x < it_end) {
+            const SinkItem x = sink_item(plan, snake_item(threadIdx.x, blockIdx.x, gridDim.x));
+            s_items[threadIdx.x] = make_int4(x.t, x.row, x.off, 2 * x.n + x.whole);
+        }
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -322,7 +361,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, plan, s_items, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
@@ -334,9 +373,10 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
             }
             __syncwarp();
+            Sweep<SINK> sweep(x, G);
             for (int k = 0; k < x.ntiles && ok; ++k, ++n) {
                 int h, i;
-                x.tile(k, G, h, i);
+                sweep.next(x, G, k, h, i);
                 const size_t side_off = ((size_t)SEQ_TB(x) * a.H + h) * a.S_pad + SEQ_PBASE(x) + (size_t)i * BT;
                 const uint32_t s = n & 1, ph = ((n >> 1) & 1) ^ 1;
                 if (!wait(&q_empty[s], ph)) break;
@@ -425,7 +465,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, plan, s_items, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             if (!wait(kv_full, kvi & 1, 0)) break;
             if (!issue_S(n) || !issue_dP(n)) break;
@@ -507,7 +547,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, plan, s_items, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             const int kvg = x.t * BT + r;
             const bool row_ok = kvg < SEQ_LKV(x);
@@ -525,9 +565,10 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 q_hi_tile =
                     a.win_w > 0 ? ((a.kv_off + (int64_t)x.t * BT) / a.win_c + a.win_w) * a.win_c - a.q_off : INT64_MAX;
             }
+            Sweep<SINK> sweep(x, G);
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int h, i;
-                x.tile(k, G, h, i);
+                sweep.next(x, G, k, h, i);
                 (void)h;
                 const uint32_t s = n & 1;
                 const int q0 = i * BT + half * 64;
@@ -649,7 +690,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
                 }
-                if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
+                if (SINK && x.slab >= 0) {   // a piece: its own slab of partials
                     float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
                     float4* pv = pkk + BT * D / 4;
 #pragma unroll
@@ -732,12 +773,13 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         uint64_t wt = 0;
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const Item x = decode<VARLEN, SPLIT, SINK>(a, ITEM(it));
+            const Item x = decode<VARLEN, SPLIT, SINK>(a, plan, s_items, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             const int s_pbase = SEQ_PBASE(x), s_len = SEQ_LQ(x);   // once per item
+            Sweep<SINK> sweep(x, G);
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int h, i;
-                x.tile(k, G, h, i);
+                sweep.next(x, G, k, h, i);
                 ok = __all_sync(0xffffffffu, mbar_wait_acc<2>(dq_full, n & 1, abort_flag, a.err, a.trace ? &wt : nullptr));
                 if (!ok) break;
                 tc_fence_after();
@@ -829,7 +871,7 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != (int)kLaunchRegs)
         return fail(DFA_ERR_CUDA, "bwd_pipe: built with %d registers per thread, the register split needs %u",
                     fa.numRegs, kLaunchRegs);
-    kern<<<wl->n_workers, kThreads, kSmem, s>>>(mq, mk, mv, mdo, a);
+    kern<<<wl->n_workers, kThreads, kSmem, s>>>(mq, mk, mv, mdo, a, 0);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "bwd_pipe launch: %s", cudaGetErrorString(e));
 }
@@ -855,13 +897,13 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
     a.dK = dK; a.dV = dV;
     a.n_units = plan.n_q;
     a.window = p.window; a.n_sink = p.n_sink;
-    a.n_items = (int)plan.n_items; a.n_pieces = plan.n_pieces; a.piece_tiles = plan.piece_len;
+    a.n_items = plan.n_items;
     a.slabs = slabs;
     a.err = device_error_flag();
     auto kern = bwd_pipe_kernel<false, false, true>;
     static std::atomic<uint64_t> seen{0};
     if (first_on_device(seen)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemSink) != cudaSuccess)
             return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
         cudaFuncAttributes fa{};   // as in tc_bwd_pipelined
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != (int)kLaunchRegs)
@@ -869,7 +911,7 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
                         fa.numRegs, kLaunchRegs);
         mark_on_device(seen);
     }
-    kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, kSmem, s>>>(mq, mk, mv, mdo, a);
+    kern<<<std::min(num_sms(), plan.n_items), kThreads, kSmemSink, s>>>(mq, mk, mv, mdo, a, plan);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }

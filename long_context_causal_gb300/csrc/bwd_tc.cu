@@ -40,6 +40,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "sink_bwd.cuh"
 
 namespace dfa {
 namespace {
@@ -62,7 +63,8 @@ struct BCfg {
     static constexpr int kOffRest = kOffDS + 32768;
     static constexpr int kOffSide = kOffRest + (D == 64 ? 32768 : 0);   // 2 x kSide
     static constexpr int kOffBar = kOffSide + 2 * kSide;
-    static constexpr int kSmem = kOffBar + 256;
+    static constexpr int kOffItems = kOffBar + 256;                     // SINK: item records
+    static constexpr int kSmem = kOffItems;
 };
 static_assert(BCfg<128>::kSmem <= 232448, "backward shared memory");
 
@@ -82,8 +84,8 @@ struct BwdArgs {
     const int32_t* wl_items;
     int n_units;                  // key tiles per (batch, kv head)
     int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
-    int n_items, n_pieces, piece_tiles;   // ... items, of which the first n_pieces * rows are pieces of key tile 0
-    float* slabs;                 // ... (n_pieces > 1) and their partial dK, dV
+    int n_items;                  // ... items (sink_bwd.cuh)
+    float* slabs;                 // ... and the pieces' partial dK, dV
     int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers (bwd_pipe_tc.cu)
     float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
@@ -102,9 +104,10 @@ struct BwdArgs {
 struct BItem {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head
     bool down;                      // sweep query tiles from the last one down
-    int slab;                       // SINK: slab of a piece of key tile 0, -1 otherwise
+    int slab;                       // SINK: a piece's slab, -1 for a whole list
     bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
     int base, pbase, len;           // packed batch: first token, first padded row, tokens of the sequence
+    int off;                        // SINK: first tile of a piece in the key tile's list
     // k-th tile of the item: head hh of the group (0..G-1), query tile i
     __device__ __forceinline__ void tile(int k, int& hh, int& i) const {
         const int len = i1 - i0, r = k % len;
@@ -113,34 +116,61 @@ struct BItem {
     }
 };
 
+// The tiles of an item one after another: (head of the group, query tile).
+// SINK steps to the next one; the others divide (their sweeps may run downwards).
+template <bool SINK>
+struct Sweep {
+    int hh, i;
+    __device__ __forceinline__ explicit Sweep(const BItem& x) {
+        if constexpr (SINK) {
+            const int len = x.i1 - x.i0;
+            hh = x.off / len;
+            i = x.i0 + x.off % len;
+        }
+    }
+    __device__ __forceinline__ void next(const BItem& x, int k, int& hk, int& ik) {
+        if constexpr (SINK) {
+            hk = hh;
+            ik = i;
+            if (++i == x.i1) {
+                i = x.i0;
+                ++hh;
+            }
+        } else {
+            x.tile(k, hk, ik);
+        }
+    }
+};
+
 // VARLEN: a packed batch (a.seq set), compiled as its own instantiation so
 // the dense kernel reads its lengths straight from the parameters.
-// SINK: a sliding window of tokens with sinks; items, pieces and their slabs
-// as in bwd_pipe_tc.cu.
+// SINK: a sliding window of tokens with sinks; the items are sink_bwd.cuh's.
+template <bool SINK>
+using Plan = std::conditional_t<SINK, SinkBwdPlan, int>;   // an unused int elsewhere
+
 template <bool VARLEN, bool SINK>
-__device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
+__device__ __forceinline__ BItem bdecode(const BwdArgs& a, const Plan<SINK>& plan, const int4* s_items, int it) {
     BItem x;
     x.slab = -1;
     x.fine = false;
-    if constexpr (SINK) {
-        const int rows = a.B * a.Hkv;
-        x.n_q = a.n_units;
-        if (a.n_pieces > 1 && it < a.n_pieces * rows) {
-            x.slab = it;
-            x.t = 0;
-            x.i0 = it / rows * a.piece_tiles;
-            x.i1 = min(x.i0 + a.piece_tiles, x.n_q);
+    x.off = 0;
+    if constexpr (SINK) {   // `it` counts the CTA's own items
+        SinkItem w;
+        if (plan.cut_all) {
+            const int4 rec = s_items[it];
+            w = SinkItem{rec.x, rec.y, rec.z, rec.w >> 1, (rec.w & 1) != 0};
         } else {
-            if (a.n_pieces > 1) it -= (a.n_pieces - 1) * rows;   // key tile 0 is done in pieces
-            x.t = it / rows;
-            x.i0 = x.t;
-            // the last query that sees the tile's last key: its position + window - 1
-            x.i1 = x.t == 0 && a.n_sink > 0 ? x.n_q : min((x.t * BT + BT - 1 + a.window - 1) / BT + 1, x.n_q);
+            w = sink_item(plan, snake_item(it, blockIdx.x, gridDim.x));
         }
-        const int row = it % rows;
-        x.b = row / a.Hkv;
-        x.g = row % a.Hkv;
-        x.ntiles = (a.H / a.Hkv) * (x.i1 - x.i0);
+        x.t = w.t;
+        x.b = w.row / a.Hkv;
+        x.g = w.row % a.Hkv;
+        x.n_q = plan.n_q;
+        x.i0 = x.t;
+        x.i1 = x.t + sink_range(plan, x.t);
+        x.off = w.off;
+        x.ntiles = w.n;
+        x.slab = w.whole ? -1 : snake_item(it, blockIdx.x, gridDim.x);
         x.down = false;
         x.fine = x.t == 0 && a.fine0;
         return x;
@@ -173,7 +203,7 @@ __device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
 
 // Sequence geometry of item x (see bdecode).
 // Value of the CTA's it-th item.
-#define ITEM(it) (SINK ? snake_item(it, blockIdx.x, gridDim.x) : a.wl_items[it])
+#define ITEM(it) (SINK ? (it) : a.wl_items[it])
 #define SEQ_LEN(x) (VARLEN ? (x).len : a.S)
 #define SEQ_BASE(x) (VARLEN ? (x).base : 0)
 #define SEQ_PBASE(x) (VARLEN ? (x).pbase : 0)
@@ -183,7 +213,7 @@ template <int D, bool VARLEN, bool SINK>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
-              const BwdArgs a) {
+              const BwdArgs a, const __grid_constant__ Plan<SINK> plan) {
     using C = BCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {            // the swizzled layouts need a 1 KB aligned base
@@ -218,6 +248,13 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
     const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
+    int4* s_items = reinterpret_cast<int4*>(smem + C::kOffItems);   // SINK, plan.cut_all: this CTA's items
+    if constexpr (SINK) {
+        if (plan.cut_all && (int)threadIdx.x < it_end) {
+            const SinkItem x = sink_item(plan, snake_item(threadIdx.x, blockIdx.x, gridDim.x));
+            s_items[threadIdx.x] = make_int4(x.t, x.row, x.off, 2 * x.n + x.whole);
+        }
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -264,7 +301,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
+            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
             if (lane == 0) {
@@ -275,9 +312,10 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
             }
             __syncwarp();
+            Sweep<SINK> sweep(x);
             for (int k = 0; k < x.ntiles && ok; ++k, ++n) {
                 int hh, i;
-                x.tile(k, hh, i);
+                sweep.next(x, k, hh, i);
                 const int h = x.g * G + hh;
                 const size_t side_off = ((size_t)SEQ_TB(x) * a.H + h) * a.S_pad + SEQ_PBASE(x);
                 const uint32_t s = n & 1, ph = ((n >> 1) & 1) ^ 1;
@@ -348,7 +386,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             __syncwarp();
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
+            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
             if (!wait(kv_full, kvi & 1, 3)) break;
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 const uint32_t s = n & 1, ph = (n >> 1) & 1;
@@ -434,16 +472,17 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
+            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
             const int kvg = x.t * BT + r;                   // global key index of this thread's row
             const bool row_ok = kvg < SEQ_LEN(x);
             using Pos = std::conditional_t<SINK, int, int64_t>;
             Pos q_hi;   // queries below it see the key (SINK: a sink is seen by all of them)
             if constexpr (SINK) q_hi = kvg < a.n_sink ? INT32_MAX : kvg + a.window;
             else q_hi = a.win_w > 0 ? ((int64_t)kvg / a.win_c + a.win_w) * a.win_c : INT64_MAX;
+            Sweep<SINK> sweep(x);
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
-                x.tile(k, hh, i);
+                sweep.next(x, k, hh, i);
                 const uint32_t s = n & 1, ph = (n >> 1) & 1;
                 if (!wait(&q_full[s], ph, 0) || !wait(s_full, n & 1, 0) || !wait(dp_full, n & 1, 0)) break;
                 tc_fence_after();
@@ -506,7 +545,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                     for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
                 }
-                if (SINK && x.slab >= 0) {   // a piece of key tile 0: its own slab of partials
+                if (SINK && x.slab >= 0) {   // a piece: its own slab of partials
                     float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
                     float4* pv = pkk + BT * D / 4;
 #pragma unroll
@@ -555,10 +594,11 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         uint64_t wt = 0;
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, ITEM(it));
+            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
+            Sweep<SINK> sweep(x);
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
-                x.tile(k, hh, i);
+                sweep.next(x, k, hh, i);
                 const int h = x.g * G + hh;
                 ok = __all_sync(0xffffffffu, mbar_wait_acc(dq_full, n & 1, abort_flag, a.err, a.trace ? &wt : nullptr));
                 if (!ok) break;
@@ -639,7 +679,7 @@ dfa_status launch(const AttnProblem& p, const void* q, const void* k, const void
     const int smem = BCfg<D>::kSmem;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return fail(DFA_ERR_CUDA, "bwd_tc: shared memory attribute");
-    kern<<<wl->n_workers, kThreads, smem, s>>>(mq, mk, mv, mdo, a);
+    kern<<<wl->n_workers, kThreads, smem, s>>>(mq, mk, mv, mdo, a, 0);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "bwd_tc launch: %s", cudaGetErrorString(e));
 }
@@ -677,18 +717,18 @@ dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const 
     a.dV = static_cast<__nv_bfloat16*>(dV);
     a.n_units = plan.n_q;
     a.window = p.window; a.n_sink = p.n_sink;
-    a.n_items = (int)plan.n_items; a.n_pieces = plan.n_pieces; a.piece_tiles = plan.piece_len;
+    a.n_items = plan.n_items;
     a.slabs = slabs;
     a.err = device_error_flag();
     auto kern = bwd_tc_kernel<D, false, true>;
-    const int smem = BCfg<D>::kSmem;
+    const int smem = BCfg<D>::kSmem + kPlanItems * 16;
     static std::atomic<uint64_t> seen{0};
     if (first_on_device(seen)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
         mark_on_device(seen);
     }
-    kern<<<std::min<int64_t>(num_sms(), plan.n_items), kThreads, smem, s>>>(mq, mk, mv, mdo, a);
+    kern<<<std::min(num_sms(), plan.n_items), kThreads, smem, s>>>(mq, mk, mv, mdo, a, plan);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }

@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "sink_bwd.cuh"
 
 namespace dfa {
 namespace {
@@ -242,11 +243,11 @@ __device__ __forceinline__ uint4 pack8(const float4& a, const float4& b, float c
 }
 
 // dQ: eight elements of [B, S, H, D] per thread from the head-major
-// accumulator.  The blocks behind those sum key tile 0's slabs, eight elements
-// per thread, in the pieces' order.
+// accumulator.  The blocks behind those sum the slabs of the key tiles whose
+// lists were cut, eight elements per thread, in the pieces' order.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-finish_kernel(int H, int Hkv, int S, int rows, int n_pieces, float scale, int dq_blocks, int n_rows,
+finish_kernel(int H, int Hkv, int S, const __grid_constant__ SinkBwdPlan p, float scale, int dq_blocks, int n_rows,
               const float* __restrict__ acc, const float* __restrict__ slabs, uint4* __restrict__ dQ,
               uint4* __restrict__ dK, uint4* __restrict__ dV) {
     constexpr int T = D / 8;
@@ -271,17 +272,22 @@ finish_kernel(int H, int Hkv, int S, int rows, int n_pieces, float scale, int dq
         }
         return;
     }
-    const int64_t x = ((int64_t)blockIdx.x - dq_blocks) * kThreads + threadIdx.x;   // (row, dK or dV, key, part)
-    if (x >= (int64_t)rows * 2 * 128 * T) return;
-    const int row = (int)(x / (2 * 128 * T)), in = (int)(x % (2 * 128 * T));
+    // (key tile, row, dK or dV, key, eight elements); the tensor and tile are the block's
+    constexpr int kBlocks = 2 * 128 * T / kThreads;
+    const int block = (int)blockIdx.x - dq_blocks, in = block % kBlocks * kThreads + threadIdx.x;
+    const int row = block / kBlocks % p.rows, t = block / kBlocks / p.rows;
+    const int first = p.cut_all ? p.first[t] : 0, pieces = p.cut_all ? p.first[t + 1] - first : p.pieces0;
+    const int key = t * 128 + in / T % 128;
+    if (pieces == 1 || key >= S) return;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
-    for (int p = 0; p < n_pieces; ++p) {
-        const float4* src = reinterpret_cast<const float4*>(slabs + ((int64_t)p * rows + row) * 2 * 128 * D) + 2 * in;
+#pragma unroll 4
+    for (int z = first; z < first + pieces; ++z) {
+        const float4* src = reinterpret_cast<const float4*>(slabs + ((int64_t)z * p.rows + row) * 2 * 128 * D) + 2 * in;
         const float4 u = src[0], w = src[1];
         a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
         c.x += w.x; c.y += w.y; c.z += w.z; c.w += w.w;
     }
-    const int b = row / Hkv, g = row % Hkv, key = in / T % 128;   // S > 128 whenever there are pieces
+    const int b = row / Hkv, g = row % Hkv;
     (in < 128 * T ? dK : dV)[(((int64_t)b * S + key) * Hkv + g) * T + in % T] = pack8(a, c, 1.f);
 }
 
@@ -375,37 +381,82 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
                               void* dQ, void* dK, void* dV, cudaStream_t s) {
     const int n_rows = p.B * p.S * p.H, per = 2 * kThreads / (p.D / 8);
     const int dq_blocks = (n_rows - 1) / per + 1;
-    const int rows = p.B * p.Hkv;
     const float scale = p.scale / (1 << p.p_shift);
-    const int64_t extra = plan.n_pieces > 1 ? blocks_for((int64_t)rows * 2 * 128 * p.D / 8) : 0;
-    const unsigned grid = (unsigned)(dq_blocks + extra);
+    const int tiles = plan.cut_all ? plan.n_q : plan.pieces0 > 1;
+    const unsigned grid = (unsigned)(dq_blocks + tiles * plan.rows * (2 * 128 * (p.D / 8) / kThreads));
     if (p.D == 128)
-        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n_rows, dq_acc,
-                                                     slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
+        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, plan, scale, dq_blocks, n_rows, dq_acc, slabs,
+                                                     (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     else
-        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, rows, plan.n_pieces, scale, dq_blocks, n_rows, dq_acc,
-                                                    slabs, (uint4*)dQ, (uint4*)dK, (uint4*)dV);
+        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, plan, scale, dq_blocks, n_rows, dq_acc, slabs,
+                                                    (uint4*)dQ, (uint4*)dK, (uint4*)dV);
     return launched("windowed backward finish");
 }
 
+// The time of a plan is estimated in query tiles (about 3 us): an item costs
+// its tiles and about two more (loads, pipeline fill, epilogue), the dealing
+// leaves the CTAs half an item apart, and each slab, written and read at the
+// memory's rate, costs the GPU 0.013 of a tile on top of one for the summing.
 SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
     SinkBwdPlan x{};
-    const int64_t rows = (int64_t)p.B * p.Hkv;
+    x.rows = p.B * p.Hkv;
+    x.G = p.H / p.Hkv;
     x.n_q = (p.S + 127) / 128;
-    x.piece_len = x.n_q;
-    x.n_pieces = 1;
+    x.window_tiles = std::min(x.n_q, (p.window + 126) / 128 + 1);   // a tile's last key is seen by window - 1 more queries
+    x.n_sink = p.n_sink;
+    const int sms = num_sms(), longest = x.G * sink_range(x, 0), ordinary = x.G * x.window_tiles;
+    const int tail = std::min(x.n_q, x.window_tiles);               // the last tiles' ranges shrink to 1
+    const double tiles = (double)x.rows * x.G *
+                         (sink_range(x, 0) - x.window_tiles + (double)(x.n_q - tail) * x.window_tiles + tail * (tail + 1.) / 2);
+    x.piece = longest;
+    x.pieces0 = 1;
     if (p.n_sink > 0) {
-        // Pieces about as long as an ordinary key tile's range, so that the snake's
-        // order by cost holds; at least 8 tiles, which pay for the piece's K and V
-        // loads and its 128 KB slab, and at most 64 pieces.
-        const int wlen = std::min(x.n_q, (p.window + 126) / 128 + 1);
-        const int len = std::max(std::max(wlen, 8), (x.n_q + 63) / 64);
-        if (len < x.n_q) {
-            x.piece_len = len;
-            x.n_pieces = (x.n_q + len - 1) / len;
+        // Pieces about as long as an ordinary key tile's list, so that the snake's
+        // order by cost holds; at least 8 query tiles of each head, which pay for the
+        // piece's K and V loads and its slab, and at most 64 pieces.
+        const int len = x.G * std::max(std::max(x.window_tiles, 8), (x.n_q + 63) / 64);
+        if (len < longest) {
+            x.piece = len;
+            x.pieces0 = (longest + len - 1) / len;
         }
     }
-    x.n_items = rows * (x.n_q + x.n_pieces - 1);
+    x.n_items = x.rows * (x.n_q - 1 + x.pieces0);
+    x.n_slabs = x.pieces0 > 1 ? x.pieces0 * x.rows : 0;
+    // Cut every list while the SMs' even share is less than a few of them.
+    if (x.n_q > kPlanTiles || x.piece == 1 || tiles >= 4.0 * sms * x.piece) return x;
+    auto pieces = [&](int len) {
+        int64_t n = 0;
+        for (int t = x.n_q - tail; t < x.n_q; ++t) n += (x.G * (x.n_q - t) + len - 1) / len;
+        n += (int64_t)(x.n_q - tail) * ((ordinary + len - 1) / len);
+        if (x.n_sink > 0) n += (longest + len - 1) / len - (ordinary + len - 1) / len;
+        return n * x.rows;
+    };
+    auto cost = [&](int len, int64_t n, int64_t slabs) {
+        return std::max(len + 2.0, (tiles + 2.0 * n) / sms + (n > sms ? 0.5 * len : 0.0)) + (slabs ? 1 + 0.013 * slabs : 0.0);
+    };
+    const double uncut = cost(x.piece, x.n_items, x.n_slabs);
+    double least = uncut;
+    int best = 0;
+    for (int k = 2, len = 0; k <= 32; ++k) {
+        const int next = (x.piece + k - 1) / k;
+        if (next == len || next < 2) continue;
+        len = next;
+        const int64_t n = pieces(len);
+        if (n > (int64_t)sms * (kPlanItems - 1)) break;
+        const double c = cost(len, n, n);
+        if (c < least) least = c, best = len;
+    }
+    if (best == 0 || least > 0.95 * uncut) return x;
+    x.cut_all = 1;
+    x.piece = best;
+    int n = 0;
+    for (int t = 0; t < x.n_q; ++t) {
+        x.first[t] = (uint16_t)n;
+        n += (x.G * sink_range(x, t) + best - 1) / best;
+    }
+    x.first[x.n_q] = (uint16_t)n;
+    x.pieces0 = x.first[1];
+    x.n_items = x.n_slabs = n * x.rows;
     return x;
 }
 

@@ -894,8 +894,7 @@ SinkWs sink_ws(const SinkProblem& p, bool ckpt) {
     w.dq = off;
     off = align_up(off + sizeof(float) * rows * p.S * p.D);
     w.slabs = off;
-    if (plan.n_pieces > 1)
-        off = align_up(off + sizeof(float) * (size_t)plan.n_pieces * p.B * p.Hkv * 2 * 128 * p.D);
+    off = align_up(off + sizeof(float) * (size_t)plan.n_slabs * 2 * 128 * p.D);
     for (int i = 0; i < 3 && ckpt; ++i) {
         w.qkv[i] = off;
         off = align_up(off + 2 * (size_t)p.B * p.S * (i ? p.Hkv : p.H) * p.D);

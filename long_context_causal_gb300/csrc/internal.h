@@ -130,21 +130,24 @@ struct SinkProblem {
     int p_shift;
 };
 constexpr int kMaxSinks = 128;   // one key tile
-// Backward plan: key tile 0 is seen by every query when there are sinks.  Its
-// query range is then cut into n_pieces pieces of piece_len 128-row query
-// tiles; with more than one, piece p of (batch, kv head) row r writes its
-// partial dK and dV to slab p * rows + r, and the sum of the slabs is key
-// tile 0's gradient (a fixed order, so dK and dV keep their bits).
+// Backward plan (sink_bwd.cuh): the lists of query tiles of the key tiles, cut
+// into pieces.
+constexpr int kPlanTiles = 512;     // key tiles a problem that is cut everywhere may have ...
+constexpr int kPlanItems = 32;      // ... and items per CTA
 struct SinkBwdPlan {
-    int n_q, piece_len, n_pieces;
-    int64_t n_items;
+    int rows, G, n_q;               // B * Hkv, heads per group, tiles of 128 tokens
+    int window_tiles, n_sink;       // query tiles that see an ordinary key tile
+    int piece, pieces0;             // tiles per piece; pieces of key tile 0
+    int cut_all;                    // 1: every list is cut, first[t] is key tile t's first piece
+    int n_items, n_slabs;
+    uint16_t first[kPlanTiles + 1];
 };
 SinkBwdPlan sink_bwd_plan(const SinkProblem& p);
 
 dfa_status tc_sink_fwd(const SinkProblem& p, const void* q, const void* k, const void* v, void* O, float* lse,
                        cudaStream_t s);
 // delta as for tc_bwd; nlse2 with p_shift added; dq_acc fp32 [B, H, S, D], zero; slabs fp32
-// [n_pieces * B * Hkv][2][128][D] (dK with scale applied, dV).
+// [n_slabs][2][128][D] (dK with scale applied, dV), slab i of item i.
 dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
                        const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
                        void* dK, void* dV, cudaStream_t s);
@@ -181,8 +184,8 @@ dfa_status launch_ckpt8_restore(const Ckpt8Layout& L, const void* ckpt, void* co
 dfa_status launch_sink_prep(const SinkProblem& p, int S_pad, const void* O, const void* dO, const float* lse,
                             float* nlse2, float* delta, float* dq_acc, const void* ckpt, const Ckpt8Layout* L,
                             void* const qkv[3], cudaStream_t s);
-// After it: dQ [B, S, H, D] = bf16(scale * dq_acc) and key tile 0's dK, dV
-// from the slabs (plan.n_pieces > 1).
+// After it: dQ [B, S, H, D] = bf16(scale * dq_acc), and dK, dV of the key tiles
+// whose lists were cut from their slabs.
 dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, const float* dq_acc, const float* slabs,
                               void* dQ, void* dK, void* dV, cudaStream_t s);
 
