@@ -1,4 +1,5 @@
-// bwd_pipe_tc.cu -- pipelined tcgen05 causal attention backward, head dim 128.
+// bwd_pipe_tc.cu -- pipelined tcgen05 causal attention backward, head dim 128
+// (and 64 for the windowed variant).
 //
 // Same mathematics and contract as bwd_tc.cu (DISTFLASHATTN §3.3, paperlayer.ai
 // summary of arXiv 2310.03294: the backward reads the saved output and
@@ -59,7 +60,7 @@ using namespace ptx;
 
 constexpr int kThreads = 640;
 constexpr int BT = 128;          // key rows per work item; query rows per tile
-constexpr int D = 128;
+constexpr int D = 128;                             // head dim (tc_bwd_pipelined; the windowed variant takes HD)
 constexpr int kTile = BT * D * 2;                  // 32 KB bf16 tile
 constexpr int kSide = 1024;                        // nlse2[128] + Delta[128] per query tile
 constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile, kOffDS = 6 * kTile;
@@ -101,9 +102,7 @@ struct Args {
     int n_units;
     int n_split, piece_tiles;     // split-kv pieces of each key tile's query range (SPLIT)
     int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
-    int n_items;                  // ... items (sink_bwd.cuh)
-    float* slabs;                 // ... and the pieces' partial dK, dV
-    int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers
+    float* slabs;                 // ... the pieces' partial dK, dV (sink_bwd.cuh)
     float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
     uint64_t* trace;
@@ -122,7 +121,6 @@ struct Item {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head; ntiles over the group's heads
     bool down;                      // sweep query tiles from the last one down
     int slab;                       // SINK: a piece's slab, -1 for a whole list
-    bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
     int off;                        // SINK: first tile of a piece in the key tile's list
     // k-th tile of the item: head h of the group, query tile i
     __device__ __forceinline__ void tile(int k, int G, int& h, int& i) const {
@@ -158,6 +156,18 @@ struct Sweep {
     }
 };
 
+// The k-th item of this CTA: the first plan.fine_ctas CTAs deal the pieces of
+// key tile 0 among themselves, the others the rest.
+__device__ __forceinline__ int cta_item(const SinkBwdPlan& p, int k) {
+    const int f = p.fine_ctas, n0 = f ? p.pieces0 * p.rows : 0;
+    return (int)blockIdx.x < f ? snake_item(k, blockIdx.x, f) : n0 + snake_item(k, blockIdx.x - f, gridDim.x - f);
+}
+__device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
+    const int f = p.fine_ctas, n0 = f ? p.pieces0 * p.rows : 0;
+    return (int)blockIdx.x < f ? snake_count(n0, blockIdx.x, f)
+                               : snake_count(p.n_items - n0, blockIdx.x - f, gridDim.x - f);
+}
+
 // SINK: a sliding window of tokens with sinks; the items are sink_bwd.cuh's, no
 // work list is uploaded.  Costs fall along them -- the pieces of key tile 0,
 // which the sinks make visible to every query, then the key tiles upwards,
@@ -169,14 +179,22 @@ struct Sweep {
 // only as dV's operand; for dS it is kept as fp16, with 11 bits down to
 // 2^(-14 - p_shift) and an error of 2^(-25 - p_shift) below, so that dS =
 // P (dP - Delta) is rounded once (measured: dQ and dK 2.3e-3 off instead of
-// 3.1e-3, at the same registers).
+// 3.1e-3, at the same registers; 2% of the time).
 // The sinks' keys of a trained model share a direction, and since a row's dS
 // sum to nearly zero that direction cancels in dQ = dS K -- but not in the
 // roundings of dS, which it magnifies (128 sinks that hold most of a row's
-// weight: 8.7e-3).  So key tile 0 of a problem with sinks sends dS to dQ as
-// two bf16 numbers, dS and what its rounding lost: once the tensor cores have
-// read the first, the P/dS warps write the second over it and dQ^T adds K^T
-// times that.  One key tile of W / 128 + 2 pays for it.
+// weight: 8.7e-3).  So key tile 0 of a problem with sinks is FINE: its dS goes
+// to dQ as two bf16 numbers, dS and what its rounding lost (the rest), each an
+// MMA.  FINE tiles have CTAs of their own, which run a second copy of the roles:
+// in one copy the extra code slowed every tile by 2%.  The rest's 32 KB of
+// shared memory come from the second dO slot (HD = 128, whose dO ring is then
+// one deep) or from the halves that HD = 64 leaves free in the K and V tiles.
+//
+// HD = 64 keeps the tiles' places, 128-byte rows of 64 elements with the second
+// half of each 32 KB unused; dQ^T stays a 128-row MMA whose upper 64 rows come
+// from whatever follows K's first half and are never read.  Against the
+// single-phase kernel of bwd_tc.cu with the same items (32K tokens, 32/8 heads):
+// 4.85 ms instead of 8.65 at a window of 4096, 14.9 instead of 34.2 causal.
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a
@@ -189,15 +207,14 @@ template <bool VARLEN, bool SPLIT, bool SINK>
 __device__ __forceinline__ Item decode(const Args& a, const Plan<SINK>& plan, const int4* s_items, int it) {
     Item x;
     x.slab = -1;
-    x.fine = false;
     x.off = 0;
     if constexpr (SINK) {   // `it` counts the CTA's own items
         SinkItem w;
-        if (plan.cut_all) {
+        if (cta_items(plan) <= kPlanItems) {
             const int4 rec = s_items[it];
             w = SinkItem{rec.x, rec.y, rec.z, rec.w >> 1, (rec.w & 1) != 0};
         } else {
-            w = sink_item(plan, snake_item(it, blockIdx.x, gridDim.x));
+            w = sink_item(plan, cta_item(plan, it));
         }
         x.t = w.t;
         x.b = w.row / a.Hkv;
@@ -207,9 +224,8 @@ __device__ __forceinline__ Item decode(const Args& a, const Plan<SINK>& plan, co
         x.i1 = x.t + sink_range(plan, x.t);
         x.off = w.off;
         x.ntiles = w.n;
-        x.slab = w.whole ? -1 : snake_item(it, blockIdx.x, gridDim.x);
+        x.slab = w.whole ? -1 : cta_item(plan, it);
         x.down = false;
-        x.fine = x.t == 0 && a.fine0;
         return x;
     }
     int piece = 0;
@@ -260,11 +276,14 @@ __device__ __forceinline__ Item decode(const Args& a, const Plan<SINK>& plan, co
 #define SEQ_PBASE(x) (VARLEN ? a.seq[a.B + 1 + (x).b] : 0)
 #define SEQ_TB(x) (VARLEN ? 0 : (x).b)
 
-template <bool VARLEN, bool SPLIT, bool SINK>
-__global__ void __launch_bounds__(kThreads, 1)
-bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const Args a,
-              const __grid_constant__ Plan<SINK> plan) {
+template <bool VARLEN, bool SPLIT, bool SINK, bool FINE, int HD>
+__device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                     const CUtensorMap& tmdO, const Args& a, const Plan<SINK>& plan) {
+    static_assert(SINK || (!FINE && HD == 128), "only the windowed variant has these");
+    constexpr int kBytes = BT * HD * 2;                   // one tile as loaded
+    constexpr int kDOSlots = FINE && HD == 128 ? 1 : 2;
+    // FINE: the rest of dS^T, two blocks of 64 queries
+    constexpr int kOffRest = HD == 128 ? kOffDO + kTile : kOffK + 16384, kRestStep = HD == 128 ? 16384 : kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && a.err) atomicExch(a.err, 2);
@@ -292,19 +311,19 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* kd_full = bars + 16;
     uint64_t* kd_empty = bars + 17;
     uint64_t* done = bars + 18;
-    uint64_t* ds_read = bars + 19;    // SINK: the MMAs that read dS^T of a fine tile are done
-    uint64_t* rest_done = bars + 20;  // SINK: its rest is in place
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
-    const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
+    int it_end;
+    if constexpr (SINK) it_end = cta_items(plan);
+    else it_end = a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
-    int4* s_items = reinterpret_cast<int4*>(smem + kOffItems);   // SINK, plan.cut_all: this CTA's items
+    int4* s_items = reinterpret_cast<int4*>(smem + kOffItems);   // SINK: this CTA's items, if they are few
     if constexpr (SINK) {
-        if (plan.cut_all && (int)threadIdx.x < it_end) {
-            const SinkItem x = sink_item(plan, snake_item(threadIdx.x, blockIdx.x, gridDim.x));
+        if (it_end <= kPlanItems && (int)threadIdx.x < it_end) {
+            const SinkItem x = sink_item(plan, cta_item(plan, threadIdx.x));
             s_items[threadIdx.x] = make_int4(x.t, x.row, x.off, 2 * x.n + x.whole);
         }
     }
@@ -327,8 +346,6 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         mbar_init(kd_full, 1);
         mbar_init(kd_empty, 2 * BT);
         mbar_init(done, 1);
-        mbar_init(ds_read, 1);
-        mbar_init(rest_done, 2 * BT);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -366,8 +383,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
             if (lane == 0) {
-                mbar_arrive_expect_tx(kv_full, 2 * kTile);
-                for (int blk = 0; blk < 2; ++blk) {
+                mbar_arrive_expect_tx(kv_full, 2 * kBytes);
+                for (int blk = 0; blk < HD / 64; ++blk) {
                     tma_load_4d(sK + blk * 16384, &tmK, kv_full, blk * 64, x.g, SEQ_BASE(x) + x.t * BT, SEQ_TB(x));
                     tma_load_4d(sV + blk * 16384, &tmV, kv_full, blk * 64, x.g, SEQ_BASE(x) + x.t * BT, SEQ_TB(x));
                 }
@@ -379,23 +396,24 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 sweep.next(x, G, k, h, i);
                 const size_t side_off = ((size_t)SEQ_TB(x) * a.H + h) * a.S_pad + SEQ_PBASE(x) + (size_t)i * BT;
                 const uint32_t s = n & 1, ph = ((n >> 1) & 1) ^ 1;
+                const uint32_t sd = n % kDOSlots, phd = ((n / kDOSlots) & 1) ^ 1;
                 if (!wait(&q_empty[s], ph)) break;
                 ++q_issued;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[s], kTile + kSide);
-                    for (int blk = 0; blk < 2; ++blk)
+                    mbar_arrive_expect_tx(&q_full[s], kBytes + kSide);
+                    for (int blk = 0; blk < HD / 64; ++blk)
                         tma_load_4d(sQ + s * kTile + blk * 16384, &tmQ, &q_full[s], blk * 64, h, SEQ_BASE(x) + i * BT,
                                     SEQ_TB(x));
                     bulk_load(sSide + s * kSide, a.nlse2 + side_off, 512, &q_full[s]);
                     bulk_load(sSide + s * kSide + 512, a.delta + side_off, 512, &q_full[s]);
                 }
                 __syncwarp();
-                if (!wait(&do_empty[s], ph)) break;
+                if (!wait(&do_empty[sd], phd)) break;
                 ++do_issued;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&do_full[s], kTile);
-                    for (int blk = 0; blk < 2; ++blk)
-                        tma_load_4d(sdO + s * kTile + blk * 16384, &tmdO, &do_full[s], blk * 64, h,
+                    mbar_arrive_expect_tx(&do_full[sd], kBytes);
+                    for (int blk = 0; blk < HD / 64; ++blk)
+                        tma_load_4d(sdO + sd * kTile + blk * 16384, &tmdO, &do_full[sd], blk * 64, h,
                                     SEQ_BASE(x) + i * BT, SEQ_TB(x));
                 }
                 __syncwarp();
@@ -407,8 +425,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (kv_issued) mbar_wait(kv_full, (kv_issued - 1) & 1, &dummy, nullptr);
             for (uint32_t m = (q_issued >= 2 ? q_issued - 2 : 0); m < q_issued; ++m)
                 mbar_wait(&q_full[m & 1], (m >> 1) & 1, &dummy, nullptr);
-            for (uint32_t m = (do_issued >= 2 ? do_issued - 2 : 0); m < do_issued; ++m)
-                mbar_wait(&do_full[m & 1], (m >> 1) & 1, &dummy, nullptr);
+            for (uint32_t m = (do_issued >= kDOSlots ? do_issued - kDOSlots : 0); m < do_issued; ++m)
+                mbar_wait(&do_full[m % kDOSlots], (m / kDOSlots) & 1, &dummy, nullptr);
         }
         if (lane == 0) {
             trace_count(a.trace, a.trace_cap, 6, n);
@@ -419,7 +437,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // per-thread, and a lone thread keeps the gaps between MMA groups short
         // (the tensor pipe queues little ahead, so every cycle between groups is idle).
         constexpr uint32_t idS = idesc_bf16_f32(BT, BT, false, false);   // S^T, dP^T
-        constexpr uint32_t idKM = idesc_bf16_f32(BT, D, false, true);    // dV, dK: B N-major
+        constexpr uint32_t idKM = idesc_bf16_f32(BT, HD, false, true);   // dV, dK: B N-major
         constexpr uint32_t idQ = idesc_bf16_f32(D, BT, true, true);      // dQ^T: M = head dim
         // Descriptors as SDesc words: moved by 32-bit adds on the low word.
         auto desc = [](const void* p, uint32_t lbo) { return sdesc_words(sdesc_sw128(smem_u32(p), lbo, 1024)); };
@@ -428,9 +446,10 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const SDesc dQk = desc(sQ, 16), dQn = desc(sQ, 16384);
         const SDesc dOk = desc(sdO, 16), dOn = desc(sdO, 16384);
         const SDesc dSk = desc(sdS, 16), dSn = desc(sdS, 16384);
+        const SDesc dRn = desc(smem + kOffRest, kRestStep);
         constexpr uint32_t kSlot = kTile >> 4, kRows16 = 2048 >> 4;
         auto kmaj = [](int kk) -> uint32_t { return (uint32_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4); };
-        uint32_t n = 0, kvi = 0, fine_n = 0;
+        uint32_t n = 0, kvi = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, int slot) {
             // Not profiled, even when tracing: any profiling hook in this
@@ -447,19 +466,19 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             {
                 const SDesc b0 = dQk + s * kSlot;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + kColS, dKk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
+                for (int kk = 0; kk < HD / 16; ++kk) mma_ss(tmem + kColS, dKk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
             }
             commit(s_full);
             return true;
         };
         auto issue_dP = [&](uint32_t m) {  // dP^T(m) = V dO_m^T, over the drained dQ^T(m-1)
-            const uint32_t s = m & 1;
-            if (!wait(&do_full[s], (m >> 1) & 1, 0)) return false;
+            const uint32_t s = m % kDOSlots;
+            if (!wait(&do_full[s], (m / kDOSlots) & 1, 0)) return false;
             if (m > 0 && !wait(dq_free, (m - 1) & 1, 1)) return false;
             {
                 const SDesc b0 = dOk + s * kSlot;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + kColDP, dVk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
+                for (int kk = 0; kk < HD / 16; ++kk) mma_ss(tmem + kColDP, dVk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
             }
             commit(dp_full);
             return true;
@@ -476,13 +495,13 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (!wait(p_done, n & 1, 2)) break;
                 const uint32_t acc0 = k > 0 ? 1u : 0u;
                 {   // dV += P^T dO: P^T of query half h at S + 64h
-                    const SDesc b0 = dOn + s * kSlot;
+                    const SDesc b0 = dOn + n % kDOSlots * kSlot;
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
                         mma_ts(tmem + kColDV, tmem + kColS + kk * 8 + (kk >= 4 ? 32 : 0), b0 + kk * kRows16, idKM,
                                kk > 0 ? 1u : acc0);
                 }
-                commit(&do_empty[s]);
+                commit(&do_empty[n % kDOSlots]);
                 if (more && !issue_S(n + 1)) break;       // S^T columns are free after phase 1
                 if (!wait(ds_done, n & 1, 3)) break;
                 {   // dQ^T = K^T dS^T into the dP^T columns; drained while dK runs
@@ -490,7 +509,12 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int kk = 0; kk < BT / 16; ++kk)
                         mma_ss(tmem + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
                 }
-                if (!SINK || !x.fine) commit(dq_full);
+                if constexpr (FINE) {   // dQ^T += K^T (what dS^T's rounding lost)
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        mma_ss(tmem + kColDP, dKn + kk * kRows16, dRn + kk * kRows16, idQ, 1u);
+                }
+                commit(dq_full);
                 {   // dK += dS^T Q
                     const SDesc bq = dQn + s * kSlot;
 #pragma unroll
@@ -498,15 +522,6 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         mma_ss(tmem + kColDK, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
                 }
                 commit(&q_empty[s]);
-                if (SINK && x.fine) {   // dQ^T += K^T (what dS^T's rounding lost)
-                    commit(ds_read);
-                    if (!wait(rest_done, fine_n & 1, 3)) break;
-                    ++fine_n;
-#pragma unroll
-                    for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(tmem + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, 1u);
-                    commit(dq_full);
-                }
                 if (!more) {
                     commit(kd_full);
                     commit(kv_empty);
@@ -538,7 +553,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint32_t tS = tmem + lane_base + kColS + half * 64;
         const uint32_t tdP = tmem + lane_base + kColDP + half * 64;
         uint8_t* blk = sdS + half * 16384;
-        uint32_t n = 0, kvi = 0, fine_n = 0;
+        uint32_t n = 0, kvi = 0;
         bool ok = true;
         uint64_t wt[3] = {0, 0, 0};   // Q/S^T, dK/dV accumulators, dP^T
         auto wait = [&](uint64_t* bar, uint32_t parity, int slot) {
@@ -633,31 +648,30 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
                             for (int w = 0; w < 8; w += 4) {
                                 const float4 d4 = *reinterpret_cast<const float4*>(dl + c + e + w);
-                                uint32_t &p01 = pk[(c + e + w) / 2], &p23 = pk[(c + e + w) / 2 + 1];
-                                const float2 x01 = ds_pair(p01, __uint_as_float(u[e + w]), __uint_as_float(u[e + w + 1]),
-                                                           d4.x, d4.y);
-                                const float2 x23 = ds_pair(p23, __uint_as_float(u[e + w + 2]),
+                                const float2 x01 = ds_pair(pk[(c + e + w) / 2], __uint_as_float(u[e + w]),
+                                                           __uint_as_float(u[e + w + 1]), d4.x, d4.y);
+                                const float2 x23 = ds_pair(pk[(c + e + w) / 2 + 1], __uint_as_float(u[e + w + 2]),
                                                            __uint_as_float(u[e + w + 3]), d4.z, d4.w);
                                 dk[w / 2] = pack_bf16(x01.x, x01.y);
                                 dk[w / 2 + 1] = pack_bf16(x23.x, x23.y);
-                                if (x.fine) {   // P is done with: its registers take the rest
-                                    p01 = pack_rest(x01, dk[w / 2]);
-                                    p23 = pack_rest(x23, dk[w / 2 + 1]);
-                                }
+                                if constexpr (FINE)
+                                    *reinterpret_cast<uint2*>(smem + kOffRest + half * kRestStep +
+                                                              sw128_offset(r, c + e + w)) =
+                                        make_uint2(pack_rest(x01, dk[w / 2]), pack_rest(x23, dk[w / 2 + 1]));
                             }
                         } else {
 #pragma unroll
-                        for (int w = 0; w < 8; w += 4) {
-                            const float4 d4 = *reinterpret_cast<const float4*>(dl + c + e + w);
-                            const float2 p01 =
-                                __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pk[(c + e + w) / 2]));
-                            const float2 p23 =
-                                __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pk[(c + e + w) / 2 + 1]));
-                            dk[w / 2] = ds_pack_bf16(p01.x, p01.y, __uint_as_float(u[e + w]),
-                                                     __uint_as_float(u[e + w + 1]), d4.x, d4.y);
-                            dk[w / 2 + 1] = ds_pack_bf16(p23.x, p23.y, __uint_as_float(u[e + w + 2]),
-                                                         __uint_as_float(u[e + w + 3]), d4.z, d4.w);
-                        }
+                            for (int w = 0; w < 8; w += 4) {
+                                const float4 d4 = *reinterpret_cast<const float4*>(dl + c + e + w);
+                                const float2 p01 =
+                                    __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pk[(c + e + w) / 2]));
+                                const float2 p23 =
+                                    __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pk[(c + e + w) / 2 + 1]));
+                                dk[w / 2] = ds_pack_bf16(p01.x, p01.y, __uint_as_float(u[e + w]),
+                                                         __uint_as_float(u[e + w + 1]), d4.x, d4.y);
+                                dk[w / 2 + 1] = ds_pack_bf16(p23.x, p23.y, __uint_as_float(u[e + w + 2]),
+                                                             __uint_as_float(u[e + w + 3]), d4.z, d4.w);
+                            }
                         }
                         *reinterpret_cast<uint4*>(blk + sw128_offset(r, c + e)) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
                     }
@@ -665,25 +679,15 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(ds_done);
-                if (SINK && x.fine) {
-                    if (!wait(ds_read, fine_n & 1, 2)) break;
-                    ++fine_n;
-#pragma unroll
-                    for (int z = 0; z < 64; z += 8)
-                        *reinterpret_cast<uint4*>(blk + sw128_offset(r, z)) =
-                            make_uint4(pk[z / 2], pk[z / 2 + 1], pk[z / 2 + 2], pk[z / 2 + 3]);
-                    fence_proxy_async_smem();
-                    mbar_arrive(rest_done);
-                }
             }
             if (!ok) break;
             // ---- epilogue: dV = acc, dK = scale * acc into [B, Lkv, Hkv, D] (bf16 store,
             // or fp32 += for a chunk pair's partial gradients); this half's columns
             if (!wait(kd_full, kvi & 1, 1)) break;
             tc_fence_after();
-            const int64_t orow = (((int64_t)SEQ_TB(x) * a.Lkv + SEQ_BASE(x) + kvg) * a.Hkv + x.g) * D;
+            const int64_t orow = (((int64_t)SEQ_TB(x) * a.Lkv + SEQ_BASE(x) + kvg) * a.Hkv + x.g) * HD;
 #pragma unroll 1
-            for (int c = half * 2; c < half * 2 + 2; ++c) {
+            for (int c = half * (HD / 64); c < (half + 1) * (HD / 64); ++c) {
                 uint32_t uv[32], uk[32];
                 tmem_ld32x2(tmem + lane_base + kColDV + c * 32, tmem + lane_base + kColDK + c * 32, uv, uk);
                 if constexpr (SINK) {
@@ -691,8 +695,8 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
                 }
                 if (SINK && x.slab >= 0) {   // a piece: its own slab of partials
-                    float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
-                    float4* pv = pkk + BT * D / 4;
+                    float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * HD + c * 32);
+                    float4* pv = pkk + BT * HD / 4;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         pkk[e] = make_float4(a.scale * __uint_as_float(uk[4 * e]), a.scale * __uint_as_float(uk[4 * e + 1]),
@@ -790,11 +794,15 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 // four full 128-byte rows.
                 const int m = lane & 3;
                 float* base = a.dq_acc + (((int64_t)SEQ_TB(x) * a.H + h) * (VARLEN ? a.acc_rows : a.Lq) + s_pbase +
-                                          (int64_t)i * BT + m) * D +
+                                          (int64_t)i * BT + m) * HD +
                               (warp % 4) * 32 + (lane >> 2) * 4;
                 const int nq = min(BT, s_len - i * BT) - dg * 64;
                 // This warpgroup's 64 query columns are read at once, then TMEM is
                 // released (relaxed: the arrival must not wait for any reduction).
+                if (HD == 64 && warp % 4 >= 2) {   // TMEM lanes 64-127 hold no head-dim element
+                    mbar_arrive_relaxed(dq_free);
+                    continue;
+                }
                 uint32_t v[64];
                 tmem_ld32x2(tdQ, tdQ + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]),
                             *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
@@ -806,7 +814,7 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                    __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3])};
                     quad_transpose(xq, lane);
                     if (4 * g + m < nq)
-                        red_add_v4(base + (dg * 64 + 4 * g) * D, xq[0], xq[1], xq[2], xq[3]);
+                        red_add_v4(base + (dg * 64 + 4 * g) * HD, xq[0], xq[1], xq[2], xq[3]);
                 }
             }
         }
@@ -817,6 +825,20 @@ bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         tc_fence_before();
         __syncthreads();
     }
+}
+
+template <bool VARLEN, bool SPLIT, bool SINK, int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+bwd_pipe_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                const __grid_constant__ Args a, const __grid_constant__ Plan<SINK> plan) {
+    if constexpr (SINK) {
+        if ((int)blockIdx.x < plan.fine_ctas) {
+            body<VARLEN, SPLIT, SINK, true, HD>(tmQ, tmK, tmV, tmdO, a, plan);
+            return;
+        }
+    }
+    body<VARLEN, SPLIT, SINK, false, HD>(tmQ, tmK, tmV, tmdO, a, plan);
 }
 
 #undef ITEM
@@ -860,9 +882,9 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
         return fail(DFA_ERR_INVALID_ARG, "split-kv backward pieces need fp32 dK/dV accumulators");
     a.n_split = wl->n_split;
     a.piece_tiles = wl->piece_tiles;
-    auto kern = p.seq ? bwd_pipe_kernel<true, false, false>
-                : split ? bwd_pipe_kernel<false, true, false>
-                        : bwd_pipe_kernel<false, false, false>;
+    auto kern = p.seq ? bwd_pipe_kernel<true, false, false, 128>
+                : split ? bwd_pipe_kernel<false, true, false, 128>
+                        : bwd_pipe_kernel<false, false, false, 128>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return fail(DFA_ERR_CUDA, "bwd_pipe: shared memory attribute");
     // The setmaxnreg split assumes the launch register count; a different
@@ -876,31 +898,19 @@ dfa_status tc_bwd_pipelined(const AttnProblem& p, const void* q, const void* k, 
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "bwd_pipe launch: %s", cudaGetErrorString(e));
 }
 
-dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
-                       const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
-                       void* dK, void* dV, cudaStream_t s) {
-    if (p.D != D) return tc_sink_bwd_d64(p, plan, q, k, v, dO, nlse2, delta, S_pad, dq_acc, slabs, dK, dV, s);
+namespace {
+
+template <int HD>
+dfa_status launch_sink(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                       const void* dO, const Args& a, cudaStream_t s) {
     alignas(64) CUtensorMap mq, mk, mv, mdo;
-    const int64_t qh = (int64_t)p.H * D, kh = (int64_t)p.Hkv * D;
-    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
-        !make_tmap_bshd(&mdo, dO, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
-        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.S * kh, kh, D) ||
-        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, p.S * kh, kh, D))
+    const int64_t qh = (int64_t)p.H * HD, kh = (int64_t)p.Hkv * HD;
+    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, HD, p.S * qh, qh, HD) ||
+        !make_tmap_bshd(&mdo, dO, p.B, p.S, p.H, HD, p.S * qh, qh, HD) ||
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, HD, p.S * kh, kh, HD) ||
+        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, HD, p.S * kh, kh, HD))
         return fail(DFA_ERR_CUDA, "tensor map encoding failed");
-    Args a{};
-    a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.Lq = a.Lkv = p.S; a.S_pad = S_pad; a.causal = 1;
-    a.acc_rows = p.S;
-    a.scale_v = 1.f / (1 << p.p_shift);
-    a.scale = p.scale * a.scale_v; a.c2 = p.scale * 1.4426950408889634f;
-    a.fine0 = p.fine;
-    a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
-    a.dK = dK; a.dV = dV;
-    a.n_units = plan.n_q;
-    a.window = p.window; a.n_sink = p.n_sink;
-    a.n_items = plan.n_items;
-    a.slabs = slabs;
-    a.err = device_error_flag();
-    auto kern = bwd_pipe_kernel<false, false, true>;
+    auto kern = bwd_pipe_kernel<false, false, true, HD>;
     static std::atomic<uint64_t> seen{0};
     if (first_on_device(seen)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemSink) != cudaSuccess)
@@ -911,9 +921,28 @@ dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void
                         fa.numRegs, kLaunchRegs);
         mark_on_device(seen);
     }
-    kern<<<std::min(num_sms(), plan.n_items), kThreads, kSmemSink, s>>>(mq, mk, mv, mdo, a, plan);
+    kern<<<plan.grid, kThreads, kSmemSink, s>>>(mq, mk, mv, mdo, a, plan);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
+                       const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
+                       void* dK, void* dV, cudaStream_t s) {
+    Args a{};
+    a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.Lq = a.Lkv = p.S; a.S_pad = S_pad; a.causal = 1;
+    a.acc_rows = p.S;
+    a.scale_v = 1.f / (1 << p.p_shift);
+    a.scale = p.scale * a.scale_v; a.c2 = p.scale * 1.4426950408889634f;
+    a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
+    a.dK = dK; a.dV = dV;
+    a.n_units = plan.n_q;
+    a.window = p.window; a.n_sink = p.n_sink;
+    a.slabs = slabs;
+    a.err = device_error_flag();
+    return p.D == 128 ? launch_sink<128>(p, plan, q, k, v, dO, a, s) : launch_sink<64>(p, plan, q, k, v, dO, a, s);
 }
 
 }  // namespace dfa

@@ -34,13 +34,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
-#include "sink_bwd.cuh"
 
 namespace dfa {
 namespace {
@@ -59,12 +56,9 @@ struct BCfg {
     static constexpr int kOffQ = 2 * kTile;            // 2 slots
     static constexpr int kOffDO = 4 * kTile;           // 2 slots
     static constexpr int kOffDS = 6 * kTile;           // 128 x 128 bf16 = 32 KB
-    // D = 64 only: what the rounding of dS lost (SINK, key tile 0), 32 KB
-    static constexpr int kOffRest = kOffDS + 32768;
-    static constexpr int kOffSide = kOffRest + (D == 64 ? 32768 : 0);   // 2 x kSide
+    static constexpr int kOffSide = kOffDS + 32768;    // 2 x kSide
     static constexpr int kOffBar = kOffSide + 2 * kSide;
-    static constexpr int kOffItems = kOffBar + 256;                     // SINK: item records
-    static constexpr int kSmem = kOffItems;
+    static constexpr int kSmem = kOffBar + 256;
 };
 static_assert(BCfg<128>::kSmem <= 232448, "backward shared memory");
 
@@ -83,11 +77,6 @@ struct BwdArgs {
     const int32_t* wl_offsets;
     const int32_t* wl_items;
     int n_units;                  // key tiles per (batch, kv head)
-    int window, n_sink;           // SINK: the token window and the first keys that stay visible ...
-    int n_items;                  // ... items (sink_bwd.cuh)
-    float* slabs;                 // ... and the pieces' partial dK, dV
-    int fine0;                    // ... key tile 0's dS goes into dQ as two bf16 numbers (bwd_pipe_tc.cu)
-    float scale_v;                // ... 2^-p_shift; scale holds the factor too
     int* err;
     uint64_t* trace;              // optional per-CTA timeline (nullptr: off)
     int trace_cap;
@@ -104,10 +93,7 @@ struct BwdArgs {
 struct BItem {
     int b, g, t, i0, i1, n_q, ntiles;   // query tiles [i0, i1) per head
     bool down;                      // sweep query tiles from the last one down
-    int slab;                       // SINK: a piece's slab, -1 for a whole list
-    bool fine;                      // SINK: dS goes into dQ as two bf16 numbers
     int base, pbase, len;           // packed batch: first token, first padded row, tokens of the sequence
-    int off;                        // SINK: first tile of a piece in the key tile's list
     // k-th tile of the item: head hh of the group (0..G-1), query tile i
     __device__ __forceinline__ void tile(int k, int& hh, int& i) const {
         const int len = i1 - i0, r = k % len;
@@ -116,65 +102,11 @@ struct BItem {
     }
 };
 
-// The tiles of an item one after another: (head of the group, query tile).
-// SINK steps to the next one; the others divide (their sweeps may run downwards).
-template <bool SINK>
-struct Sweep {
-    int hh, i;
-    __device__ __forceinline__ explicit Sweep(const BItem& x) {
-        if constexpr (SINK) {
-            const int len = x.i1 - x.i0;
-            hh = x.off / len;
-            i = x.i0 + x.off % len;
-        }
-    }
-    __device__ __forceinline__ void next(const BItem& x, int k, int& hk, int& ik) {
-        if constexpr (SINK) {
-            hk = hh;
-            ik = i;
-            if (++i == x.i1) {
-                i = x.i0;
-                ++hh;
-            }
-        } else {
-            x.tile(k, hk, ik);
-        }
-    }
-};
-
 // VARLEN: a packed batch (a.seq set), compiled as its own instantiation so
 // the dense kernel reads its lengths straight from the parameters.
-// SINK: a sliding window of tokens with sinks; the items are sink_bwd.cuh's.
-template <bool SINK>
-using Plan = std::conditional_t<SINK, SinkBwdPlan, int>;   // an unused int elsewhere
-
-template <bool VARLEN, bool SINK>
-__device__ __forceinline__ BItem bdecode(const BwdArgs& a, const Plan<SINK>& plan, const int4* s_items, int it) {
+template <bool VARLEN>
+__device__ __forceinline__ BItem bdecode(const BwdArgs& a, int it) {
     BItem x;
-    x.slab = -1;
-    x.fine = false;
-    x.off = 0;
-    if constexpr (SINK) {   // `it` counts the CTA's own items
-        SinkItem w;
-        if (plan.cut_all) {
-            const int4 rec = s_items[it];
-            w = SinkItem{rec.x, rec.y, rec.z, rec.w >> 1, (rec.w & 1) != 0};
-        } else {
-            w = sink_item(plan, snake_item(it, blockIdx.x, gridDim.x));
-        }
-        x.t = w.t;
-        x.b = w.row / a.Hkv;
-        x.g = w.row % a.Hkv;
-        x.n_q = plan.n_q;
-        x.i0 = x.t;
-        x.i1 = x.t + sink_range(plan, x.t);
-        x.off = w.off;
-        x.ntiles = w.n;
-        x.slab = w.whole ? -1 : snake_item(it, blockIdx.x, gridDim.x);
-        x.down = false;
-        x.fine = x.t == 0 && a.fine0;
-        return x;
-    }
     const int row = it / a.n_units, unit = it % a.n_units;
     x.b = row / a.Hkv;
     x.g = row % a.Hkv;
@@ -202,18 +134,16 @@ __device__ __forceinline__ BItem bdecode(const BwdArgs& a, const Plan<SINK>& pla
 }
 
 // Sequence geometry of item x (see bdecode).
-// Value of the CTA's it-th item.
-#define ITEM(it) (SINK ? (it) : a.wl_items[it])
 #define SEQ_LEN(x) (VARLEN ? (x).len : a.S)
 #define SEQ_BASE(x) (VARLEN ? (x).base : 0)
 #define SEQ_PBASE(x) (VARLEN ? (x).pbase : 0)
 #define SEQ_TB(x) (VARLEN ? 0 : (x).b)
 
-template <int D, bool VARLEN, bool SINK>
+template <int D, bool VARLEN>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
-              const BwdArgs a, const __grid_constant__ Plan<SINK> plan) {
+              const BwdArgs a) {
     using C = BCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {            // the swizzled layouts need a 1 KB aligned base
@@ -245,16 +175,8 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 21);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int it_begin = SINK ? 0 : a.wl_offsets[blockIdx.x];
-    const int it_end = SINK ? snake_count(a.n_items, blockIdx.x, gridDim.x) : a.wl_offsets[blockIdx.x + 1];
+    const int it_begin = a.wl_offsets[blockIdx.x], it_end = a.wl_offsets[blockIdx.x + 1];
     const int G = a.H / a.Hkv;
-    int4* s_items = reinterpret_cast<int4*>(smem + C::kOffItems);   // SINK, plan.cut_all: this CTA's items
-    if constexpr (SINK) {
-        if (plan.cut_all && (int)threadIdx.x < it_end) {
-            const SinkItem x = sink_item(plan, snake_item(threadIdx.x, blockIdx.x, gridDim.x));
-            s_items[threadIdx.x] = make_int4(x.t, x.row, x.off, 2 * x.n + x.whole);
-        }
-    }
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -301,7 +223,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
+            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
             if (!wait(kv_empty, (kvi & 1) ^ 1)) break;
             ++kv_issued;
             if (lane == 0) {
@@ -312,10 +234,9 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
             }
             __syncwarp();
-            Sweep<SINK> sweep(x);
             for (int k = 0; k < x.ntiles && ok; ++k, ++n) {
                 int hh, i;
-                sweep.next(x, k, hh, i);
+                x.tile(k, hh, i);
                 const int h = x.g * G + hh;
                 const size_t side_off = ((size_t)SEQ_TB(x) * a.H + h) * a.S_pad + SEQ_PBASE(x);
                 const uint32_t s = n & 1, ph = ((n >> 1) & 1) ^ 1;
@@ -369,7 +290,6 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const uint64_t dQk = sdesc_sw128(smem_u32(sQ), 16, 1024), dQn = sdesc_sw128(smem_u32(sQ), 16384, 1024);
         const uint64_t dOk = sdesc_sw128(smem_u32(sdO), 16, 1024), dOn = sdesc_sw128(smem_u32(sdO), 16384, 1024);
         const uint64_t dSk = sdesc_sw128(smem_u32(sdS), 16, 1024), dSn = sdesc_sw128(smem_u32(sdS), 16384, 1024);
-        const uint64_t dRn = sdesc_sw128(smem_u32(smem + C::kOffRest), 16384, 1024);
         constexpr uint64_t kSlot = C::kTile >> 4, kRows16 = 2048 >> 4;
         auto kmaj = [](int kk) -> uint64_t { return (uint64_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4); };
         uint32_t n = 0, kvi = 0;
@@ -386,7 +306,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             __syncwarp();
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
+            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
             if (!wait(kv_full, kvi & 1, 3)) break;
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 const uint32_t s = n & 1, ph = (n >> 1) & 1;
@@ -434,11 +354,6 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                         for (int kk = 0; kk < BT / 16; ++kk)   // dQ = dS K
                             mma_ss(tmem + kColDP, dSn + kk * kRows16, dKn + kk * kRows16, idQ, kk > 0);
-                        if (SINK && x.fine) {   // dQ += (what dS's rounding lost) K
-#pragma unroll
-                            for (int kk = 0; kk < BT / 16; ++kk)
-                                mma_ss(tmem + kColDP, dRn + kk * kRows16, dKn + kk * kRows16, idQ, 1u);
-                        }
                     }
                 }
                 commit(dq_full);
@@ -472,17 +387,13 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             return ok;
         };
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
+            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
             const int kvg = x.t * BT + r;                   // global key index of this thread's row
             const bool row_ok = kvg < SEQ_LEN(x);
-            using Pos = std::conditional_t<SINK, int, int64_t>;
-            Pos q_hi;   // queries below it see the key (SINK: a sink is seen by all of them)
-            if constexpr (SINK) q_hi = kvg < a.n_sink ? INT32_MAX : kvg + a.window;
-            else q_hi = a.win_w > 0 ? ((int64_t)kvg / a.win_c + a.win_w) * a.win_c : INT64_MAX;
-            Sweep<SINK> sweep(x);
+            const int64_t q_hi = a.win_w > 0 ? ((int64_t)kvg / a.win_c + a.win_w) * a.win_c : INT64_MAX;
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
-                sweep.next(x, k, hh, i);
+                x.tile(k, hh, i);
                 const uint32_t s = n & 1, ph = (n >> 1) & 1;
                 if (!wait(&q_full[s], ph, 0) || !wait(s_full, n & 1, 0) || !wait(dp_full, n & 1, 0)) break;
                 tc_fence_after();
@@ -512,12 +423,6 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         pk[e / 2 + 1] = pack_bf16(pp[2], pp[3]);
                         dk[e / 2] = pack_bf16(dd[0], dd[1]);
                         dk[e / 2 + 1] = pack_bf16(dd[2], dd[3]);
-                        if (SINK && x.fine) {
-                            const uint2 rest = make_uint2(pack_rest(make_float2(dd[0], dd[1]), dk[e / 2]),
-                                                          pack_rest(make_float2(dd[2], dd[3]), dk[e / 2 + 1]));
-                            *reinterpret_cast<uint2*>(smem + C::kOffRest + (c / 2) * 16384 +
-                                                      sw128_offset(r, (c % 2) * 32 + e)) = rest;
-                        }
                     }
                     tmem_st16(tP + c * 16, pk);
                     uint8_t* blk = sdS + (c / 2) * 16384;
@@ -541,22 +446,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 uint32_t uv[32], uk[32];
                 tmem_ld32(tmem + lane_base + kColDV + c * 32, uv);
                 tmem_ld32(tmem + lane_base + kColDK + c * 32, uk);
-                if constexpr (SINK) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
-                }
-                if (SINK && x.slab >= 0) {   // a piece: its own slab of partials
-                    float4* pkk = reinterpret_cast<float4*>(a.slabs + ((int64_t)x.slab * 2 * BT + r) * D + c * 32);
-                    float4* pv = pkk + BT * D / 4;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        pkk[e] = make_float4(a.scale * __uint_as_float(uk[4 * e]), a.scale * __uint_as_float(uk[4 * e + 1]),
-                                             a.scale * __uint_as_float(uk[4 * e + 2]),
-                                             a.scale * __uint_as_float(uk[4 * e + 3]));
-                        pv[e] = make_float4(__uint_as_float(uv[4 * e]), __uint_as_float(uv[4 * e + 1]),
-                                            __uint_as_float(uv[4 * e + 2]), __uint_as_float(uv[4 * e + 3]));
-                    }
-                } else if (row_ok) {
+                if (row_ok) {
                     uint4* pv = reinterpret_cast<uint4*>(a.dV + orow + c * 32);
                     uint4* pkk = reinterpret_cast<uint4*>(a.dK + orow + c * 32);
 #pragma unroll
@@ -594,11 +484,10 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bool ok = true;
         uint64_t wt = 0;
         for (int it = it_begin; it < it_end && ok; ++it) {
-            const BItem x = bdecode<VARLEN, SINK>(a, plan, s_items, ITEM(it));
-            Sweep<SINK> sweep(x);
+            const BItem x = bdecode<VARLEN>(a, a.wl_items[it]);
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int hh, i;
-                sweep.next(x, k, hh, i);
+                x.tile(k, hh, i);
                 const int h = x.g * G + hh;
                 ok = __all_sync(0xffffffffu, mbar_wait_acc(dq_full, n & 1, abort_flag, a.err, a.trace ? &wt : nullptr));
                 if (!ok) break;
@@ -646,7 +535,6 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     if (threadIdx.x == 0) trace_cta(a.trace, a.trace_cap, t_start, it_end - it_begin);
 }
 
-#undef ITEM
 #undef SEQ_LEN
 #undef SEQ_BASE
 #undef SEQ_PBASE
@@ -675,11 +563,11 @@ dfa_status launch(const AttnProblem& p, const void* q, const void* k, const void
     a.wl_offsets = wl->offsets; a.wl_items = wl->items; a.n_units = wl->n_units;
     a.err = device_error_flag();
     a.trace = cta_trace(&a.trace_cap);
-    auto kern = p.seq ? bwd_tc_kernel<D, true, false> : bwd_tc_kernel<D, false, false>;
+    auto kern = p.seq ? bwd_tc_kernel<D, true> : bwd_tc_kernel<D, false>;
     const int smem = BCfg<D>::kSmem;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return fail(DFA_ERR_CUDA, "bwd_tc: shared memory attribute");
-    kern<<<wl->n_workers, kThreads, smem, s>>>(mq, mk, mv, mdo, a, 0);
+    kern<<<wl->n_workers, kThreads, smem, s>>>(mq, mk, mv, mdo, a);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "bwd_tc launch: %s", cudaGetErrorString(e));
 }
@@ -693,44 +581,6 @@ dfa_status tc_bwd(const AttnProblem& p, const void* q, const void* k, const void
     // Head dim 128 takes the two-stream pipelined kernel (bwd_pipe_tc.cu).
     if (p.D == 128) return tc_bwd_pipelined(p, q, k, v, dO, nlse2, delta, S_pad, dq_acc, dK, dV, false, wl, s);
     return launch<64>(p, q, k, v, dO, nlse2, delta, S_pad, dq_acc, dK, dV, wl, s);
-}
-
-dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
-                           const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc,
-                           float* slabs, void* dK, void* dV, cudaStream_t s) {
-    constexpr int D = 64;
-    alignas(64) CUtensorMap mq, mk, mv, mdo;
-    const int64_t qh = (int64_t)p.H * D, kh = (int64_t)p.Hkv * D;
-    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
-        !make_tmap_bshd(&mdo, dO, p.B, p.S, p.H, D, p.S * qh, qh, D) ||
-        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.S * kh, kh, D) ||
-        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, p.S * kh, kh, D))
-        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
-    BwdArgs a{};
-    a.acc_rows = p.S;
-    a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.S = p.S; a.S_pad = S_pad; a.causal = 1;
-    a.scale_v = 1.f / (1 << p.p_shift);
-    a.scale = p.scale * a.scale_v; a.c2 = p.scale * 1.4426950408889634f;
-    a.fine0 = p.fine;
-    a.nlse2 = nlse2; a.delta = delta; a.dq_acc = dq_acc;
-    a.dK = static_cast<__nv_bfloat16*>(dK);
-    a.dV = static_cast<__nv_bfloat16*>(dV);
-    a.n_units = plan.n_q;
-    a.window = p.window; a.n_sink = p.n_sink;
-    a.n_items = plan.n_items;
-    a.slabs = slabs;
-    a.err = device_error_flag();
-    auto kern = bwd_tc_kernel<D, false, true>;
-    const int smem = BCfg<D>::kSmem + kPlanItems * 16;
-    static std::atomic<uint64_t> seen{0};
-    if (first_on_device(seen)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return fail(DFA_ERR_CUDA, "sink backward: shared memory attribute");
-        mark_on_device(seen);
-    }
-    kern<<<std::min(num_sms(), plan.n_items), kThreads, smem, s>>>(mq, mk, mv, mdo, a, plan);
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace dfa

@@ -394,9 +394,13 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
 }
 
 // The time of a plan is estimated in query tiles (about 3 us): an item costs
-// its tiles and about two more (loads, pipeline fill, epilogue), the dealing
-// leaves the CTAs half an item apart, and each slab, written and read at the
-// memory's rate, costs the GPU 0.013 of a tile on top of one for the summing.
+// its tiles (FINE ones kFine each) and about two more (loads, pipeline fill,
+// epilogue); a CTA has up to four items of one size in whole rounds, and more
+// or mixed ones within half an item of the mean; each slab, written and read
+// at the memory's rate, costs the GPU 0.013 of a tile on top of one for the
+// summing.
+constexpr double kFine = 1.4, kItem = 2.0;
+
 SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
     SinkBwdPlan x{};
     x.rows = p.B * p.Hkv;
@@ -406,57 +410,84 @@ SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
     x.n_sink = p.n_sink;
     const int sms = num_sms(), longest = x.G * sink_range(x, 0), ordinary = x.G * x.window_tiles;
     const int tail = std::min(x.n_q, x.window_tiles);               // the last tiles' ranges shrink to 1
-    const double tiles = (double)x.rows * x.G *
-                         (sink_range(x, 0) - x.window_tiles + (double)(x.n_q - tail) * x.window_tiles + tail * (tail + 1.) / 2);
+    const double rest = (double)x.rows * x.G *                      // tiles of the lists behind the first
+                        ((double)(x.n_q - tail) * x.window_tiles + tail * (tail + 1.) / 2 - x.window_tiles);
+    const double tiles = rest + (double)x.rows * longest;
+
+    auto spread = [&](int64_t n, int ctas, int len, double work, bool even) {
+        if (n == 0) return 0.0;
+        if (n <= ctas || (even && n <= 4 * (int64_t)ctas)) return (double)((n + ctas - 1) / ctas) * (len + kItem);
+        return (work + kItem * n) / ctas + 0.5 * len;
+    };
+    // Time of n items of up to len tiles, the first n0 of them key tile 0's, and the CTAs for those.
+    auto time_of = [&](int64_t n, int64_t n0, int len, int len0, bool even, int* fine_ctas) {
+        *fine_ctas = 0;
+        if (!p.fine) return spread(n, sms, len, tiles, even);
+        const double one = kFine * len0 + kItem;
+        if (n <= sms || n == n0) {
+            *fine_ctas = (int)std::min<int64_t>(n0, sms);
+            return std::max((double)((n0 + *fine_ctas - 1) / *fine_ctas) * one, n > n0 ? len + kItem : 0.0);
+        }
+        double least = 1e30;
+        for (int r = 1, f = 0; r <= 256 && f != 1; ++r) {
+            f = (int)((n0 + r - 1) / r);
+            if (f >= sms) continue;
+            const double t = std::max(r * one, spread(n - n0, sms - f, len, rest, even));
+            if (t < least) least = t, *fine_ctas = f;
+            if (r * one > t) break;
+        }
+        return least;
+    };
+
+    auto slab_time = [](int64_t n) { return n ? 1 + 0.013 * n : 0.0; };
+
+    // Key tile 0 alone cut: pieces about as long as an ordinary key tile's list, or
+    // shorter where that ends earlier; 8 tiles pay for the piece's K and V loads and
+    // its slab.
     x.piece = longest;
     x.pieces0 = 1;
-    if (p.n_sink > 0) {
-        // Pieces about as long as an ordinary key tile's list, so that the snake's
-        // order by cost holds; at least 8 query tiles of each head, which pay for the
-        // piece's K and V loads and its slab, and at most 64 pieces.
-        const int len = x.G * std::max(std::max(x.window_tiles, 8), (x.n_q + 63) / 64);
-        if (len < longest) {
-            x.piece = len;
-            x.pieces0 = (longest + len - 1) / len;
-        }
+    double uncut = time_of((int64_t)x.rows * x.n_q, x.rows, std::max(ordinary, 1), longest, false, &x.fine_ctas);
+    for (int k = 0; k < 4 && p.n_sink > 0; ++k) {
+        const int len = std::max(std::max(x.G * std::max(x.window_tiles, 8) >> k, 8), (longest + 255) / 256);
+        const int64_t n0 = (longest + len - 1) / len;
+        if (len >= longest) continue;
+        int f;
+        const double t = time_of(x.rows * (x.n_q - 1 + n0), x.rows * n0, std::max(ordinary, 1), len, false, &f) +
+                         slab_time(x.rows * n0);
+        if (t < uncut) uncut = t, x.piece = len, x.pieces0 = (int)n0, x.fine_ctas = f;
     }
     x.n_items = x.rows * (x.n_q - 1 + x.pieces0);
     x.n_slabs = x.pieces0 > 1 ? x.pieces0 * x.rows : 0;
     // Cut every list while the SMs' even share is less than a few of them.
-    if (x.n_q > kPlanTiles || x.piece == 1 || tiles >= 4.0 * sms * x.piece) return x;
-    auto pieces = [&](int len) {
-        int64_t n = 0;
-        for (int t = x.n_q - tail; t < x.n_q; ++t) n += (x.G * (x.n_q - t) + len - 1) / len;
-        n += (int64_t)(x.n_q - tail) * ((ordinary + len - 1) / len);
-        if (x.n_sink > 0) n += (longest + len - 1) / len - (ordinary + len - 1) / len;
-        return n * x.rows;
-    };
-    auto cost = [&](int len, int64_t n, int64_t slabs) {
-        return std::max(len + 2.0, (tiles + 2.0 * n) / sms + (n > sms ? 0.5 * len : 0.0)) + (slabs ? 1 + 0.013 * slabs : 0.0);
-    };
-    const double uncut = cost(x.piece, x.n_items, x.n_slabs);
-    double least = uncut;
-    int best = 0;
-    for (int k = 2, len = 0; k <= 32; ++k) {
-        const int next = (x.piece + k - 1) / k;
-        if (next == len || next < 2) continue;
-        len = next;
-        const int64_t n = pieces(len);
-        if (n > (int64_t)sms * (kPlanItems - 1)) break;
-        const double c = cost(len, n, n);
-        if (c < least) least = c, best = len;
+    if (x.n_q <= kPlanTiles && longest > 1 && tiles < 4.0 * sms * std::max(x.piece, ordinary)) {
+        double least = 0.95 * uncut;
+        int best = 0, fine = 0;
+        for (int len = 2; len < longest; len += 1 + longest / 64) {
+            const int64_t n0 = (int64_t)x.rows * ((longest + len - 1) / len);
+            int64_t n = 0;
+            for (int t = std::max(x.n_q - tail, 1); t < x.n_q; ++t) n += (x.G * (x.n_q - t) + len - 1) / len;
+            n += (int64_t)std::max(x.n_q - tail - 1, 0) * ((ordinary + len - 1) / len);
+            n = n * x.rows + n0;
+            if (n > (int64_t)sms * kPlanItems) continue;
+            int f;
+            const double t = time_of(n, n0, len, len, true, &f) + slab_time(n);
+            if (t < least) least = t, best = len, fine = f;
+        }
+        if (best > 0) {
+            x.cut_all = 1;
+            x.piece = best;
+            x.fine_ctas = fine;
+            int n = 0;
+            for (int t = 0; t < x.n_q; ++t) {
+                x.first[t] = (uint16_t)n;
+                n += (x.G * sink_range(x, t) + best - 1) / best;
+            }
+            x.first[x.n_q] = (uint16_t)n;
+            x.pieces0 = x.first[1];
+            x.n_items = x.n_slabs = n * x.rows;
+        }
     }
-    if (best == 0 || least > 0.95 * uncut) return x;
-    x.cut_all = 1;
-    x.piece = best;
-    int n = 0;
-    for (int t = 0; t < x.n_q; ++t) {
-        x.first[t] = (uint16_t)n;
-        n += (x.G * sink_range(x, t) + best - 1) / best;
-    }
-    x.first[x.n_q] = (uint16_t)n;
-    x.pieces0 = x.first[1];
-    x.n_items = x.n_slabs = n * x.rows;
+    x.grid = std::min(sms, x.n_items);
     return x;
 }
 

@@ -132,14 +132,15 @@ struct SinkProblem {
 constexpr int kMaxSinks = 128;   // one key tile
 // Backward plan (sink_bwd.cuh): the lists of query tiles of the key tiles, cut
 // into pieces.
-constexpr int kPlanTiles = 512;     // key tiles a problem that is cut everywhere may have ...
-constexpr int kPlanItems = 32;      // ... and items per CTA
+constexpr int kPlanTiles = 512;     // key tiles a problem that is cut everywhere may have
+constexpr int kPlanItems = 32;      // items a CTA keeps as records
 struct SinkBwdPlan {
     int rows, G, n_q;               // B * Hkv, heads per group, tiles of 128 tokens
     int window_tiles, n_sink;       // query tiles that see an ordinary key tile
     int piece, pieces0;             // tiles per piece; pieces of key tile 0
     int cut_all;                    // 1: every list is cut, first[t] is key tile t's first piece
     int n_items, n_slabs;
+    int grid, fine_ctas;            // CTAs; those that take key tile 0, in the finer arithmetic
     uint16_t first[kPlanTiles + 1];
 };
 SinkBwdPlan sink_bwd_plan(const SinkProblem& p);
@@ -151,9 +152,6 @@ dfa_status tc_sink_fwd(const SinkProblem& p, const void* q, const void* k, const
 dfa_status tc_sink_bwd(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
                        const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc, float* slabs,
                        void* dK, void* dV, cudaStream_t s);
-dfa_status tc_sink_bwd_d64(const SinkProblem& p, const SinkBwdPlan& plan, const void* q, const void* k, const void* v,
-                           const void* dO, const float* nlse2, const float* delta, int S_pad, float* dq_acc,
-                           float* slabs, void* dK, void* dV, cudaStream_t s);
 
 // Single-token form over a cache: k, v [B, S, Hkv, D] with element strides
 // kv_s*, kv_len int32 [B] on the device.

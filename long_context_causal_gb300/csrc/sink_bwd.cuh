@@ -1,5 +1,5 @@
 // sink_bwd.cuh -- how the windowed backward's work is cut into items, shared by
-// the head-dim-128 and head-dim-64 kernels and the finishing kernel.
+// the main and the finishing kernel.
 //
 // Per (batch, key/value head) row, key tile t has a list of G * range(t) query
 // tiles: the heads of its group, one after another, each over the query tiles
@@ -11,8 +11,8 @@
 //
 // Items are (piece, row) with the row fastest.  In a large problem only tile 0
 // is cut, and the pieces' order is arithmetic; a problem too small to fill the
-// SMs has every list cut, with a table of the tiles' first pieces (kernel
-// parameter), read once per CTA into records in shared memory.
+// SMs has every list cut, with a table of the tiles' first pieces (a kernel
+// parameter).  A CTA with few items looks them up once, into shared memory.
 #pragma once
 
 #include "internal.h"
