@@ -602,11 +602,19 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                 for (int c = 0; c < 64; c += 32) {
                     tmem_ld32(tS + c, u);
                     if (!full) {   // masked scores become -inf, so exp2 gives exactly 0
+                        if constexpr (SINK) {
+                            const int at = q0 + c;   // queries [kvg, q_hi) of the sequence see the key
+                            const uint32_t see = row_ok ? low_bits(min(q_hi, a.Lq) - at) & ~low_bits(kvg - at) : 0u;
 #pragma unroll
-                        for (int z = 0; z < 32; ++z) {
-                            const int qg = q0 + c + z;
-                            if (!(row_ok && qg < SEQ_LQ(x) && !(a.causal && kvg + a.rel > qg) && qg < q_hi))
-                                u[z] = 0xff800000u;
+                            for (int z = 0; z < 32; ++z)
+                                if (!(see >> z & 1)) u[z] = 0xff800000u;
+                        } else {
+#pragma unroll
+                            for (int z = 0; z < 32; ++z) {
+                                const int qg = q0 + c + z;
+                                if (!(row_ok && qg < SEQ_LQ(x) && !(a.causal && kvg + a.rel > qg) && qg < q_hi))
+                                    u[z] = 0xff800000u;
+                            }
                         }
                     }
                     if constexpr (SINK) {
@@ -644,6 +652,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t dk[4];
+                        [[maybe_unused]] uint32_t rest[4];
                         if constexpr (SINK) {
 #pragma unroll
                             for (int w = 0; w < 8; w += 4) {
@@ -654,11 +663,14 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                                                            __uint_as_float(u[e + w + 3]), d4.z, d4.w);
                                 dk[w / 2] = pack_bf16(x01.x, x01.y);
                                 dk[w / 2 + 1] = pack_bf16(x23.x, x23.y);
-                                if constexpr (FINE)
-                                    *reinterpret_cast<uint2*>(smem + kOffRest + half * kRestStep +
-                                                              sw128_offset(r, c + e + w)) =
-                                        make_uint2(pack_rest(x01, dk[w / 2]), pack_rest(x23, dk[w / 2 + 1]));
+                                if constexpr (FINE) {
+                                    rest[w / 2] = pack_rest(x01, dk[w / 2]);
+                                    rest[w / 2 + 1] = pack_rest(x23, dk[w / 2 + 1]);
+                                }
                             }
+                            if constexpr (FINE)
+                                *reinterpret_cast<uint4*>(smem + kOffRest + half * kRestStep + sw128_offset(r, c + e)) =
+                                    make_uint4(rest[0], rest[1], rest[2], rest[3]);
                         } else {
 #pragma unroll
                             for (int w = 0; w < 8; w += 4) {

@@ -393,13 +393,13 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
     return launched("windowed backward finish");
 }
 
-// The time of a plan is estimated in query tiles (about 3 us): an item costs
-// its tiles (FINE ones kFine each) and about two more (loads, pipeline fill,
+// The time of a plan is estimated in query tiles (about 2.4 us): an item costs
+// its tiles (FINE ones kFine each) and kItem more (loads, pipeline fill,
 // epilogue); a CTA has up to four items of one size in whole rounds, and more
 // or mixed ones within half an item of the mean; each slab, written and read
 // at the memory's rate, costs the GPU 0.013 of a tile on top of one for the
 // summing.
-constexpr double kFine = 1.4, kItem = 2.0;
+constexpr double kFine = 1.9, kItem = 2.5;
 
 SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
     SinkBwdPlan x{};

@@ -481,6 +481,13 @@ __device__ __forceinline__ void setmaxnreg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The low n bits set (none for n <= 0, all for n >= 32): a mask over 32 columns
+// tested bit by bit costs a kernel about one instruction a column, where range
+// comparisons cost three.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // ---------------------------------------------------------------- math
 // Hardware base-2 exponential (MUFU), flush-to-zero; ex2(-inf) = 0.
 __device__ __forceinline__ float ex2(float x) {

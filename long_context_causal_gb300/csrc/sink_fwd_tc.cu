@@ -110,7 +110,10 @@ __device__ __forceinline__ Block decode(const Args& a, int it) {
 // Column c of a tile is visible iff (c >= lo or c < ns) and c < lim.
 struct Mask {
     int lo, lim, ns;
-    __device__ __forceinline__ bool sees(int c) const { return (c >= lo || c < ns) && c < lim; }
+    // bit e: column c + e
+    __device__ __forceinline__ uint32_t bits(int c) const {
+        return (~low_bits(lo - c) | low_bits(ns - c)) & low_bits(lim - c);
+    }
 };
 
 // Row max of the first 32 * chunks scores of this thread's row in TMEM.
@@ -121,10 +124,11 @@ __device__ __forceinline__ float row_max(uint32_t tS, int chunks, Mask k) {
     for (int c = 0; c < chunks; ++c) {
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
+        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             const float x = __uint_as_float(u[e]);
-            m[e & 3] = fmaxf(m[e & 3], (!MASK || k.sees(c * 32 + e)) ? x : -INFINITY);
+            m[e & 3] = fmaxf(m[e & 3], (!MASK || (see >> e & 1)) ? x : -INFINITY);
         }
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -140,14 +144,14 @@ __device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float 
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
         uint32_t pk[16];
+        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const int c0 = c * 32 + 2 * e;
             float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
             float p1 = ex2(fmaf(__uint_as_float(u[2 * e + 1]), c2, -m));
             if (MASK) {
-                p0 = k.sees(c0) ? p0 : 0.f;
-                p1 = k.sees(c0 + 1) ? p1 : 0.f;
+                p0 = see >> (2 * e) & 1 ? p0 : 0.f;
+                p1 = see >> (2 * e + 1) & 1 ? p1 : 0.f;
             }
             acc[e & 3] += p0 + p1;
             pk[e] = pack_bf16(p0, p1);
