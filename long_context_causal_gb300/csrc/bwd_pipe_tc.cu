@@ -362,6 +362,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint64_t t_start = globaltimer();
+    if constexpr (SINK) wait_for_previous_kernel();   // the preparation's rows, zeros and restored tensors
 
     // Every warp of a warpgroup executes its warpgroup's setmaxnreg, and each
     // role's code sits inside the branch that set its budget (code reached
@@ -933,8 +934,7 @@ dfa_status launch_sink(const SinkProblem& p, const SinkBwdPlan& plan, const void
                         fa.numRegs, kLaunchRegs);
         mark_on_device(seen);
     }
-    kern<<<plan.grid, kThreads, kSmemSink, s>>>(mq, mk, mv, mdo, a, plan);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(kern, plan.grid, kThreads, kSmemSink, s, mq, mk, mv, mdo, a, plan);
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink backward launch: %s", cudaGetErrorString(e));
 }
 

@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "ptx.cuh"
 #include "sink_bwd.cuh"
 
 namespace dfa {
@@ -251,6 +252,7 @@ finish_kernel(int H, int Hkv, int S, const __grid_constant__ SinkBwdPlan p, floa
               const float* __restrict__ acc, const float* __restrict__ slabs, uint4* __restrict__ dQ,
               uint4* __restrict__ dK, uint4* __restrict__ dV) {
     constexpr int T = D / 8;
+    ptx::wait_for_previous_kernel();
     if ((int)blockIdx.x < dq_blocks) {
         constexpr int R = 2;         // rows per thread, loaded before the first is used
         const int part = threadIdx.x % T;
@@ -384,13 +386,11 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
     const float scale = p.scale / (1 << p.p_shift);
     const int tiles = plan.cut_all ? plan.n_q : plan.pieces0 > 1;
     const unsigned grid = (unsigned)(dq_blocks + tiles * plan.rows * (2 * 128 * (p.D / 8) / kThreads));
-    if (p.D == 128)
-        finish_kernel<128><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, plan, scale, dq_blocks, n_rows, dq_acc, slabs,
-                                                     (uint4*)dQ, (uint4*)dK, (uint4*)dV);
-    else
-        finish_kernel<64><<<grid, kThreads, 0, s>>>(p.H, p.Hkv, p.S, plan, scale, dq_blocks, n_rows, dq_acc, slabs,
-                                                    (uint4*)dQ, (uint4*)dK, (uint4*)dV);
-    return launched("windowed backward finish");
+    auto kern = p.D == 128 ? finish_kernel<128> : finish_kernel<64>;
+    const cudaError_t e = launch_overlapped(kern, (int)grid, kThreads, 0, s, p.H, p.Hkv, p.S, plan, scale, dq_blocks, n_rows,
+                                            dq_acc, slabs, static_cast<uint4*>(dQ), static_cast<uint4*>(dK),
+                                            static_cast<uint4*>(dV));
+    return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "windowed backward finish launch: %s", cudaGetErrorString(e));
 }
 
 // The time of a plan is estimated in query tiles (about 2.4 us): an item costs

@@ -195,6 +195,24 @@ __host__ __device__ inline int snake_count(int n_items, int cta, int n) {
     return full + (pos < n_items % n);
 }
 
+// Launch whose start may overlap the end of the kernel before it in the stream
+// (1-2 us of a short call); the kernel calls wait_for_previous_kernel() before
+// it touches what that one writes.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 int num_sms();
 
 // Settings made once per device and kernel (attribute queries cost a launch a

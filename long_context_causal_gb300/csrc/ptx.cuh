@@ -259,6 +259,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Waits until the kernel before this one in the stream has finished and its
+// writes are visible; returns at once unless this kernel was launched to
+// overlap that one's end (programmatic stream serialization).
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 // Allocates `ncols` TMEM columns (power of two >= 32); whole warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {

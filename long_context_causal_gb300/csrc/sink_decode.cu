@@ -408,7 +408,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 template <int D>
 __global__ void __launch_bounds__(256)
 join_kernel(const Args a, int grid) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials of the kernel before this one
+    wait_for_previous_kernel();      // its partials
     const int R = a.Hkv * a.HB, b = blockIdx.x / R, r = blockIdx.x % R;
     const int64_t total = a.prefix[a.B], n_ctas = min((int64_t)grid, total);
     const int before = a.prefix[b], tiles = (a.prefix[b + 1] - before) / R;
@@ -478,17 +478,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     decode_kernel<D><<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-    // Launched so that its start overlaps the first kernel's end; it waits for it.
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(segments);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<D>, a, n);
+    e = launch_overlapped(join_kernel<D>, segments, 256, 0, s, a, n);
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
 }
 

@@ -122,9 +122,10 @@ __device__ __forceinline__ float row_max(uint32_t tS, int chunks, Mask k) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
+        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
+        if (MASK && !__any_sync(0xffffffffu, see)) continue;   // no row of the warp sees the 32 columns
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
-        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             const float x = __uint_as_float(u[e]);
@@ -141,10 +142,16 @@ __device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        uint32_t u[32];
-        tmem_ld32(tS + c * 32, u);
         uint32_t pk[16];
         const uint32_t see = MASK ? k.bits(c * 32) : 0u;
+        if (MASK && !__any_sync(0xffffffffu, see)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0;
+            tmem_st16(tS + c * 16, pk);
+            continue;
+        }
+        uint32_t u[32];
+        tmem_ld32(tS + c * 32, u);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
