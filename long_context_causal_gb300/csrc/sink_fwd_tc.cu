@@ -178,12 +178,12 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint8_t* sQ = smem;                                   // 2 tiles
     uint8_t* sKV = smem + C::kQBytes;                     // ring: K and V tiles alternate
     uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + C::kSlots * C::kTileBytes);
-    uint64_t* q_full = bars + 0;
-    uint64_t* q_empty = bars + 1;
-    uint64_t* s_full = bars + 2;          // [2]
-    uint64_t* p_full = bars + 4;          // [2]
-    uint64_t* o_full = bars + 6;          // [2]
-    uint64_t* done = bars + 8;
+    uint64_t* q_full = bars + 0;          // [2], as all of these one per query tile
+    uint64_t* q_empty = bars + 2;
+    uint64_t* s_full = bars + 4;
+    uint64_t* p_full = bars + 6;
+    uint64_t* o_full = bars + 8;
+    uint64_t* done = bars + 10;
     uint64_t* kv_full = bars + 16;        // [kSlots]
     uint64_t* kv_empty = bars + 16 + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
@@ -193,9 +193,9 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int rounds = snake_count(a.n_items, blockIdx.x, gridDim.x);
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
         for (int w = 0; w < 2; ++w) {
+            mbar_init(&q_full[w], 1);
+            mbar_init(&q_empty[w], 1);
             mbar_init(&s_full[w], 1);
             mbar_init(&p_full[w], BM);
             mbar_init(&o_full[w], 1);
@@ -226,17 +226,19 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         for (int r = 0; r < rounds && ok; ++r) {
             const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
-            ok = __all_sync(0xffffffffu, mbar_wait_acc(q_empty, (qi & 1) ^ 1, abort_flag, a.err, nullptr));
-            if (!ok) break;
-            ++qi;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, C::kQBytes);
-                for (int w = 0; w < 2; ++w)
+            for (int w = 0; w < 2 && ok; ++w) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[w], (r & 1) ^ 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                ++qi;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[w], C::kTileBytes);
                     for (int blk = 0; blk < D / 64; ++blk)
-                        tma_load_4d(sQ + w * C::kTileBytes + blk * 16384, &tmQ, q_full, blk * 64, x.h, x.q0 + w * BM,
+                        tma_load_4d(sQ + w * C::kTileBytes + blk * 16384, &tmQ, &q_full[w], blk * 64, x.h, x.q0 + w * BM,
                                     x.b);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
             for (int k = 0; k < x.n && ok; ++k) {
                 const int j = x.tile(k);
                 for (int which = 0; which < 2; ++which, ++ld) {
@@ -261,7 +263,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const uint32_t last = s + C::kSlots * ((ld - 1 - s) / C::kSlots);
                 mbar_wait(&kv_full[s], (last / C::kSlots) & 1, &dummy, nullptr);
             }
-            if (qi > 0) mbar_wait(q_full, (qi - 1) & 1, &dummy, nullptr);
+            for (uint32_t m = qi > 1 ? qi - 2 : 0; m < qi; ++m) mbar_wait(&q_full[m & 1], (m >> 1) & 1, &dummy, nullptr);
         }
     } else if (warp == 1 && lane == 0) {
         // ------------------------------------------------------------ MMA issuer (one thread)
@@ -273,7 +275,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint64_t dKk = sdesc_sw128(smem_u32(sKV), 16, 1024);         // K slots, K-major
         const uint64_t dVn = sdesc_sw128(smem_u32(sKV), 16384, 1024);      // V slots, N-major
         constexpr uint64_t kSlotStep = C::kTileBytes >> 4;
-        uint32_t cons = 0, qi = 0, t[2] = {0, 0};
+        uint32_t cons = 0, t[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = ok && mbar_wait_issuer(bar, parity, abort_flag, a.err);
@@ -305,20 +307,51 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         };
         for (int r = 0; r < rounds && ok; ++r) {
             const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
-            if (!wait(q_full, qi & 1)) break;
-            ++qi;
+            const Band bd[2] = {band(a, x.q0), band(a, x.q0 + BM)};
             uint32_t slotK = cons % C::kSlots;
             if (!wait(&kv_full[slotK], (cons / C::kSlots) & 1)) break;
             ++cons;
-            const Band bd[2] = {band(a, x.q0), band(a, x.q0 + BM)};
             int now[2], first[2] = {1, 1};
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
+                if (!wait(&q_full[w], r & 1)) break;
                 now[w] = bd[w].part(x.tile(0), a.n_sink);
                 if (now[w]) issue_S(w, slotK, now[w] == 1 ? idSink : idS);
+                // The query tile's last product is the one with the band's last tile; its buffer
+                // is then free for the next block's.  A tile past the end has none.
+                if (x.tile(0) >= bd[w].hi) mma_commit(&q_empty[w]);
             }
+            if (!ok) break;
             mma_commit(&kv_empty[slotK]);
-            for (int k = 0; k < x.n && ok; ++k) {
+            // Steps in which both query tiles take both key tiles whole run without looking at the bands.
+            const int hot = bd[0].hi - x.j0 + x.sink0;       // the first query tile's last key tile in the list
+            int k = 0;
+            while (k < x.n) {
+                if (now[0] == 2 && now[1] == 2 && k < hot) {
+                    const uint32_t acc0 = 1u - first[0], acc1 = 1u - first[1];
+                    first[0] = first[1] = 0;
+                    uint32_t a0 = acc0, a1 = acc1;
+                    for (; k < hot; ++k) {
+                        const uint32_t slotV = cons % C::kSlots;
+                        if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
+                        if (!wait(&p_full[0], t[0] & 1)) break;
+                        ++t[0];
+                        issue_PV(0, slotV, a0);
+                        slotK = (cons + 1) % C::kSlots;
+                        if (!wait(&kv_full[slotK], ((cons + 1) / C::kSlots) & 1)) break;
+                        issue_S(0, slotK, idS);
+                        if (!wait(&p_full[1], t[1] & 1)) break;
+                        ++t[1];
+                        issue_PV(1, slotV, a1);
+                        mma_commit(&kv_empty[slotV]);
+                        issue_S(1, slotK, idS);
+                        mma_commit(&kv_empty[slotK]);
+                        cons += 2;
+                        a0 = a1 = 1u;
+                    }
+                    if (!ok) break;
+                    mma_commit(&q_empty[0]);   // its last product is issued; the second query tile has one more
+                }
                 const bool more = k + 1 < x.n;
                 const uint32_t slotV = cons % C::kSlots;
                 if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
@@ -345,14 +378,15 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             have_k = true;
                         }
                         issue_S(w, slotK, next == 1 ? idSink : idS);
+                        if (jn == bd[w].hi) mma_commit(&q_empty[w]);
                     }
                     if (w == 1 && more) mma_commit(&kv_empty[slotK]);
                     now[w] = next;
                 }
+                if (!ok) break;
                 cons += more ? 2 : 1;
+                ++k;
             }
-            if (!ok) break;
-            mma_commit(q_empty);
         }
         // Drain: every MMA this thread issued has finished before TMEM is freed.
         mma_commit(done);
