@@ -281,7 +281,10 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                                      const CUtensorMap& tmdO, const Args& a, const Plan<SINK>& plan) {
     static_assert(SINK || (!FINE && HD == 128), "only the windowed variant has these");
     constexpr int kBytes = BT * HD * 2;                   // one tile as loaded
-    constexpr int kDOSlots = FINE && HD == 128 ? 1 : 2;
+    constexpr int kDOSlots = SINK && HD == 128 ? 1 : 2;
+    constexpr bool kBulk = SINK && !(FINE && HD == 128);  // dQ leaves through shared memory
+    // kBulk: 16 KB for each drain warpgroup
+    constexpr int kOffStage = HD == 128 ? kOffDO + kTile : kOffQ + 16384, kStageStep = HD == 128 ? 16384 : kTile;
     // FINE: the rest of dS^T, two blocks of 64 queries
     constexpr int kOffRest = HD == 128 ? kOffDO + kTile : kOffK + 16384, kRestStep = HD == 128 ? 16384 : kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -794,6 +797,58 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
             const int s_pbase = SEQ_PBASE(x), s_len = SEQ_LQ(x);   // once per item
             Sweep<SINK> sweep(x, G);
+            if constexpr (kBulk) {
+                // The warpgroup writes its query columns as rows of the accumulator to
+                // shared memory (a warp's 32 head-dim elements of one row at a time, no
+                // bank twice), kRows rows at a time, and one thread has the block added
+                // to global memory as a bulk reduction.
+                constexpr int kRows = 16384 / (HD * 4), kWarps = HD / 32;
+                if (HD == 64 && warp % 4 >= kWarps) {   // TMEM lanes 64-127 hold no head-dim element
+                    for (int k = 0; k < x.ntiles && ok; ++k, ++n) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_acc<2>(dq_full, n & 1, abort_flag, a.err, nullptr));
+                        mbar_arrive_relaxed(dq_free);
+                    }
+                    continue;
+                }
+                const bool leader = warp % 4 == 0 && lane == 0;
+                float* stage = reinterpret_cast<float*>(smem + kOffStage + dg * kStageStep);
+                for (int k = 0; k < x.ntiles; ++k, ++n) {
+                    int h, i;
+                    sweep.next(x, G, k, h, i);
+                    ok = __all_sync(0xffffffffu, mbar_wait_acc<2>(dq_full, n & 1, abort_flag, a.err, nullptr));
+                    uint32_t v[64];
+                    if (ok) {
+                        tc_fence_after();
+                        tmem_ld32x2(tdQ, tdQ + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]),
+                                    *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+                        tc_fence_before();
+                        mbar_arrive_relaxed(dq_free);
+                    }
+                    if (leader) bulk_wait_read();        // the block added last has left shared memory
+                    ok = named_bar_and(1 + dg, 32 * kWarps, ok);
+                    if (!ok) break;
+                    const int row0 = i * BT + dg * 64;
+                    float* dst = a.dq_acc + (((int64_t)x.b * a.H + h) * a.Lq + row0) * HD;
+#pragma unroll
+                    for (int part = 0; part < 64 / kRows; ++part) {
+                        if (part > 0) {
+                            if (leader) bulk_wait_read();
+                            named_bar_sync(1 + dg, 32 * kWarps);
+                        }
+#pragma unroll
+                        for (int z = 0; z < kRows; ++z)
+                            stage[z * HD + (warp % 4) * 32 + lane] = __uint_as_float(v[part * kRows + z]);
+                        fence_proxy_async_smem();
+                        named_bar_sync(1 + dg, 32 * kWarps);
+                        const int rows = min(a.Lq - row0 - part * kRows, kRows);
+                        if (leader && rows > 0) {
+                            bulk_reduce_add_f32(dst + part * kRows * HD, stage, rows * HD * 4);
+                            bulk_commit();
+                        }
+                    }
+                }
+                continue;
+            }
             for (int k = 0; k < x.ntiles; ++k, ++n) {
                 int h, i;
                 sweep.next(x, G, k, h, i);
@@ -812,10 +867,6 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                 const int nq = min(BT, s_len - i * BT) - dg * 64;
                 // This warpgroup's 64 query columns are read at once, then TMEM is
                 // released (relaxed: the arrival must not wait for any reduction).
-                if (HD == 64 && warp % 4 >= 2) {   // TMEM lanes 64-127 hold no head-dim element
-                    mbar_arrive_relaxed(dq_free);
-                    continue;
-                }
                 uint32_t v[64];
                 tmem_ld32x2(tdQ, tdQ + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]),
                             *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
@@ -831,6 +882,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                 }
             }
         }
+        if (kBulk) bulk_wait_all();   // shared memory stays until it is read, and the sums are in place
         if (threadIdx.x == 384) {
             trace_count(a.trace, a.trace_cap, 7, n);
             trace_wait(a.trace, a.trace_cap, 7, wt);
