@@ -795,6 +795,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
         for (int it = it_begin; it < it_end && ok; ++it) {
             const Item x = decode<VARLEN, SPLIT, SINK>(a, plan, s_items, ITEM(it));
             if (x.ntiles == 0) continue;   // key tile entirely above the diagonal: nothing to do
+            static_assert(kBulk || HD == 128, "the register reductions below take all 128 lanes for head-dim elements");
             const int s_pbase = SEQ_PBASE(x), s_len = SEQ_LQ(x);   // once per item
             Sweep<SINK> sweep(x, G);
             if constexpr (kBulk) {
@@ -811,39 +812,59 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                     continue;
                 }
                 const bool leader = warp % 4 == 0 && lane == 0;
-                float* stage = reinterpret_cast<float*>(smem + kOffStage + dg * kStageStep);
+                const uint32_t stage = smem_u32(smem + kOffStage + dg * kStageStep) + ((warp % 4) * 32 + lane) * 4;
+                auto add_block = [&](int h, int row) {   // the staged rows, as far as they are the sequence's
+                    fence_proxy_async_smem();
+                    named_bar_sync(1 + dg, 32 * kWarps);
+                    const int rows = min(a.Lq - row, kRows);
+                    if (leader && rows > 0) {
+                        bulk_reduce_add_f32(a.dq_acc + (((int64_t)x.b * a.H + h) * a.Lq + row) * HD,
+                                            smem + kOffStage + dg * kStageStep, rows * HD * 4);
+                        bulk_commit();
+                    }
+                };
                 for (int k = 0; k < x.ntiles; ++k, ++n) {
                     int h, i;
                     sweep.next(x, G, k, h, i);
                     ok = __all_sync(0xffffffffu, mbar_wait_acc<2>(dq_full, n & 1, abort_flag, a.err, nullptr));
-                    uint32_t v[64];
-                    if (ok) {
+                    if constexpr (HD == 64) {            // one block, 32 columns in registers at a time
+                        if (leader) bulk_wait_read();    // the block added last has left shared memory
+                        ok = named_bar_and(1 + dg, 32 * kWarps, ok);
+                        if (!ok) break;
                         tc_fence_after();
-                        tmem_ld32x2(tdQ, tdQ + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]),
-                                    *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-                        tc_fence_before();
-                        mbar_arrive_relaxed(dq_free);
-                    }
-                    if (leader) bulk_wait_read();        // the block added last has left shared memory
-                    ok = named_bar_and(1 + dg, 32 * kWarps, ok);
-                    if (!ok) break;
-                    const int row0 = i * BT + dg * 64;
-                    float* dst = a.dq_acc + (((int64_t)x.b * a.H + h) * a.Lq + row0) * HD;
 #pragma unroll
-                    for (int part = 0; part < 64 / kRows; ++part) {
-                        if (part > 0) {
-                            if (leader) bulk_wait_read();
-                            named_bar_sync(1 + dg, 32 * kWarps);
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t v[32];
+                            tmem_ld32(tdQ + part * 32, v);
+                            if (part == 1) {
+                                tc_fence_before();
+                                mbar_arrive_relaxed(dq_free);
+                            }
+#pragma unroll
+                            for (int z = 0; z < 32; ++z) st_shared_b32(stage + (part * 32 + z) * HD * 4, v[z]);
                         }
+                        add_block(h, i * BT + dg * 64);
+                    } else {                             // all columns in registers, then two blocks
+                        uint32_t v[64];
+                        if (ok) {
+                            tc_fence_after();
+                            tmem_ld32x2(tdQ, tdQ + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]),
+                                        *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+                            tc_fence_before();
+                            mbar_arrive_relaxed(dq_free);
+                        }
+                        if (leader) bulk_wait_read();
+                        ok = named_bar_and(1 + dg, 32 * kWarps, ok);
+                        if (!ok) break;
 #pragma unroll
-                        for (int z = 0; z < kRows; ++z)
-                            stage[z * HD + (warp % 4) * 32 + lane] = __uint_as_float(v[part * kRows + z]);
-                        fence_proxy_async_smem();
-                        named_bar_sync(1 + dg, 32 * kWarps);
-                        const int rows = min(a.Lq - row0 - part * kRows, kRows);
-                        if (leader && rows > 0) {
-                            bulk_reduce_add_f32(dst + part * kRows * HD, stage, rows * HD * 4);
-                            bulk_commit();
+                        for (int part = 0; part < 64 / kRows; ++part) {
+                            if (part > 0) {
+                                if (leader) bulk_wait_read();
+                                named_bar_sync(1 + dg, 32 * kWarps);
+                            }
+#pragma unroll
+                            for (int z = 0; z < kRows; ++z) st_shared_b32(stage + z * HD * 4, v[part * kRows + z]);
+                            add_block(h, i * BT + dg * 64 + part * kRows);
                         }
                     }
                 }

@@ -253,6 +253,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
+__device__ __forceinline__ void st_shared_b32(uint32_t saddr, uint32_t x) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(x) : "memory");
+}
+
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor-core operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
