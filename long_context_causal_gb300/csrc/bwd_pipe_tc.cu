@@ -435,11 +435,22 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
         if (lane == 0) {
             trace_count(a.trace, a.trace_cap, 6, n);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && (SINK || lane == 0)) {
         // ------------------------------------------------------------ MMA issuer
         // One thread: tcgen05.mma / commit / fence and mbarrier waits are all
         // per-thread, and a lone thread keeps the gaps between MMA groups short
         // (the tensor pipe queues little ahead, so every cycle between groups is idle).
+        // SINK: the whole warp runs the role and one lane issues (elect_one).
+        [[maybe_unused]] const uint32_t lead = SINK ? elect_one() : 1u;
+        const uint32_t tm = SINK ? __shfl_sync(0xffffffffu, *tmem_slot, 0) : tmem;
+        auto ss = [&](uint32_t d, SDesc da, SDesc db, uint32_t id, uint32_t acc) {
+            if constexpr (SINK) mma_ss_lead(lead, d, da, db, id, acc);
+            else mma_ss(d, da, db, id, acc);
+        };
+        auto ts = [&](uint32_t d, uint32_t at, SDesc db, uint32_t id, uint32_t acc) {
+            if constexpr (SINK) mma_ts_lead(lead, d, at, db, id, acc);
+            else mma_ts(d, at, db, id, acc);
+        };
         constexpr uint32_t idS = idesc_bf16_f32(BT, BT, false, false);   // S^T, dP^T
         constexpr uint32_t idKM = idesc_bf16_f32(BT, HD, false, true);   // dV, dK: B N-major
         constexpr uint32_t idQ = idesc_bf16_f32(D, BT, true, true);      // dQ^T: M = head dim
@@ -463,14 +474,14 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
             if (ok) tc_fence_after();
             return ok;
         };
-        auto commit = [&](uint64_t* bar) { mma_commit(bar); };
+        auto commit = [&](uint64_t* bar) { if constexpr (SINK) mma_commit_lead(lead, bar); else mma_commit(bar); };
         auto issue_S = [&](uint32_t m) {   // S^T(m) = K Q_m^T
             const uint32_t s = m & 1;
             if (!wait(&q_full[s], (m >> 1) & 1, 0)) return false;
             {
                 const SDesc b0 = dQk + s * kSlot;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) mma_ss(tmem + kColS, dKk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
+                for (int kk = 0; kk < HD / 16; ++kk) ss(tm + kColS, dKk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
             }
             commit(s_full);
             return true;
@@ -482,7 +493,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
             {
                 const SDesc b0 = dOk + s * kSlot;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) mma_ss(tmem + kColDP, dVk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
+                for (int kk = 0; kk < HD / 16; ++kk) ss(tm + kColDP, dVk + kmaj(kk), b0 + kmaj(kk), idS, kk > 0);
             }
             commit(dp_full);
             return true;
@@ -502,7 +513,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                     const SDesc b0 = dOn + n % kDOSlots * kSlot;
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ts(tmem + kColDV, tmem + kColS + kk * 8 + (kk >= 4 ? 32 : 0), b0 + kk * kRows16, idKM,
+                        ts(tm + kColDV, tm + kColS + kk * 8 + (kk >= 4 ? 32 : 0), b0 + kk * kRows16, idKM,
                                kk > 0 ? 1u : acc0);
                 }
                 commit(&do_empty[n % kDOSlots]);
@@ -511,19 +522,19 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                 {   // dQ^T = K^T dS^T into the dP^T columns; drained while dK runs
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(tmem + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
+                        ss(tm + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
                 }
                 if constexpr (FINE) {   // dQ^T += K^T (what dS^T's rounding lost)
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(tmem + kColDP, dKn + kk * kRows16, dRn + kk * kRows16, idQ, 1u);
+                        ss(tm + kColDP, dKn + kk * kRows16, dRn + kk * kRows16, idQ, 1u);
                 }
                 commit(dq_full);
                 {   // dK += dS^T Q
                     const SDesc bq = dQn + s * kSlot;
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        mma_ss(tmem + kColDK, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
+                        ss(tm + kColDK, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
                 }
                 commit(&q_empty[s]);
                 if (!more) {

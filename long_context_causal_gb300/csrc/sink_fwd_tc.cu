@@ -25,7 +25,7 @@
 // there is no workspace, so a call is one launch and can be captured.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer
-// (one thread), warp 2 TMEM owner, warps 4-11 two softmax warpgroups, one
+// (one lane issues), warp 2 TMEM owner, warps 4-11 two softmax warpgroups, one
 // query row per thread.  TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D)
 // O_1 [384,384+D); P_w (bf16 pairs) overwrites the first 64 columns of S_w.
 #include <cuda.h>
@@ -265,8 +265,10 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             for (uint32_t m = qi > 1 ? qi - 2 : 0; m < qi; ++m) mbar_wait(&q_full[m & 1], (m >> 1) & 1, &dummy, nullptr);
         }
-    } else if (warp == 1 && lane == 0) {
-        // ------------------------------------------------------------ MMA issuer (one thread)
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (one lane of a converged warp)
+        const uint32_t lead = elect_one();
+        const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // uniform
         const uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
         const uint32_t idO = idesc_bf16_f32(BM, D, false, true);
         const int ns16 = (a.n_sink + 15) / 16;                              // sink columns / 16
@@ -288,22 +290,22 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-                mma_ss(d, a0 + off, b0 + off, id, kk > 0);
+                mma_ss_lead(lead, d, a0 + off, b0 + off, id, kk > 0);
             }
-            mma_commit(&s_full[w]);
+            mma_commit_lead(lead, &s_full[w]);
         };
         auto issue_PV = [&](int w, uint32_t slot, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
-            mma_ts(d, p, b0, idO, acc);
+            mma_ts_lead(lead, d, p, b0, idO, acc);
 #pragma unroll
-            for (int kk = 1; kk < BN / 16; ++kk) mma_ts(d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
+            for (int kk = 1; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
         };
         auto issue_PV_sink = [&](int w, uint32_t slot, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
 #pragma unroll 1
-            for (int kk = 0; kk < ns16; ++kk) mma_ts(d, p + kk * 8, b0 + kk * (2048 >> 4), idO, kk > 0 ? 1u : acc);
+            for (int kk = 0; kk < ns16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, kk > 0 ? 1u : acc);
         };
         for (int r = 0; r < rounds && ok; ++r) {
             const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
@@ -319,10 +321,10 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (now[w]) issue_S(w, slotK, now[w] == 1 ? idSink : idS);
                 // The query tile's last product is the one with the band's last tile; its buffer
                 // is then free for the next block's.  A tile past the end has none.
-                if (x.tile(0) >= bd[w].hi) mma_commit(&q_empty[w]);
+                if (x.tile(0) >= bd[w].hi) mma_commit_lead(lead, &q_empty[w]);
             }
             if (!ok) break;
-            mma_commit(&kv_empty[slotK]);
+            mma_commit_lead(lead, &kv_empty[slotK]);
             // Steps in which both query tiles take both key tiles whole run without looking at the bands.
             const int hot = bd[0].hi - x.j0 + x.sink0;       // the first query tile's last key tile in the list
             int k = 0;
@@ -343,14 +345,14 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         if (!wait(&p_full[1], t[1] & 1)) break;
                         ++t[1];
                         issue_PV(1, slotV, a1);
-                        mma_commit(&kv_empty[slotV]);
+                        mma_commit_lead(lead, &kv_empty[slotV]);
                         issue_S(1, slotK, idS);
-                        mma_commit(&kv_empty[slotK]);
+                        mma_commit_lead(lead, &kv_empty[slotK]);
                         cons += 2;
                         a0 = a1 = 1u;
                     }
                     if (!ok) break;
-                    mma_commit(&q_empty[0]);   // its last product is issued; the second query tile has one more
+                    mma_commit_lead(lead, &q_empty[0]);   // its last product is issued; the second query tile has one more
                 }
                 const bool more = k + 1 < x.n;
                 const uint32_t slotV = cons % C::kSlots;
@@ -368,19 +370,19 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         else issue_PV_sink(w, slotV, first[w] ? 0u : 1u);
                         first[w] = 0;
                     }
-                    if (w == 1) mma_commit(&kv_empty[slotV]);
+                    if (w == 1) mma_commit_lead(lead, &kv_empty[slotV]);
                     // a query tile takes part in an unbroken run of the list, sinks apart: it has ended
                     // when the tile after this one lies beyond its band
-                    if (now[w] && (!more || jn > bd[w].hi)) mma_commit(&o_full[w]);
+                    if (now[w] && (!more || jn > bd[w].hi)) mma_commit_lead(lead, &o_full[w]);
                     if (next) {
                         if (!have_k) {
                             if (!wait(&kv_full[slotK], ((cons + 1) / C::kSlots) & 1)) break;
                             have_k = true;
                         }
                         issue_S(w, slotK, next == 1 ? idSink : idS);
-                        if (jn == bd[w].hi) mma_commit(&q_empty[w]);
+                        if (jn == bd[w].hi) mma_commit_lead(lead, &q_empty[w]);
                     }
-                    if (w == 1 && more) mma_commit(&kv_empty[slotK]);
+                    if (w == 1 && more) mma_commit_lead(lead, &kv_empty[slotK]);
                     now[w] = next;
                 }
                 if (!ok) break;
@@ -388,8 +390,8 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 ++k;
             }
         }
-        // Drain: every MMA this thread issued has finished before TMEM is freed.
-        mma_commit(done);
+        // Drain: every MMA issued here has finished before TMEM is freed.
+        mma_commit_lead(lead, done);
         int dummy = 0;
         mbar_wait(done, 0, &dummy, a.err);
     } else if (warp >= 4) {
