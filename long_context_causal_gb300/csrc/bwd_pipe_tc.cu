@@ -285,6 +285,11 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
     constexpr bool kBulk = SINK && !(FINE && HD == 128);  // dQ leaves through shared memory
     // kBulk: 16 KB for each drain warpgroup
     constexpr int kOffStage = HD == 128 ? kOffDO + kTile : kOffQ + 16384, kStageStep = HD == 128 ? 16384 : kTile;
+    // HD = 64: dQ^T has columns of its own, so dP^T of the next tile need not wait until it is read out (3.08
+    // instead of 3.36 ms).  dP^T stays behind dQ^T and dK: in front of them or between them, with a second
+    // buffer for dS^T, it took 3.35 and 3.50 ms.
+    constexpr bool kOwnDQ = HD == 64;
+    constexpr uint32_t kColDKt = kOwnDQ ? 64 : kColDK, kColDQ = kOwnDQ ? 128 : kColDP;
     // FINE: the rest of dS^T, two blocks of 64 queries
     constexpr int kOffRest = HD == 128 ? kOffDO + kTile : kOffK + 16384, kRestStep = HD == 128 ? 16384 : kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -489,7 +494,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
         auto issue_dP = [&](uint32_t m) {  // dP^T(m) = V dO_m^T, over the drained dQ^T(m-1)
             const uint32_t s = m % kDOSlots;
             if (!wait(&do_full[s], (m / kDOSlots) & 1, 0)) return false;
-            if (m > 0 && !wait(dq_free, (m - 1) & 1, 1)) return false;
+            if (!kOwnDQ && m > 0 && !wait(dq_free, (m - 1) & 1, 1)) return false;
             {
                 const SDesc b0 = dOk + s * kSlot;
 #pragma unroll
@@ -519,22 +524,23 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                 commit(&do_empty[n % kDOSlots]);
                 if (more && !issue_S(n + 1)) break;       // S^T columns are free after phase 1
                 if (!wait(ds_done, n & 1, 3)) break;
-                {   // dQ^T = K^T dS^T into the dP^T columns; drained while dK runs
+                if (kOwnDQ && n > 0 && !wait(dq_free, (n - 1) & 1, 1)) break;
+                {   // dQ^T = K^T dS^T (over dP^T, or in its own columns); drained while dK runs
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        ss(tm + kColDP, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
+                        ss(tm + kColDQ, dKn + kk * kRows16, dSn + kk * kRows16, idQ, kk > 0);
                 }
                 if constexpr (FINE) {   // dQ^T += K^T (what dS^T's rounding lost)
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        ss(tm + kColDP, dKn + kk * kRows16, dRn + kk * kRows16, idQ, 1u);
+                        ss(tm + kColDQ, dKn + kk * kRows16, dRn + kk * kRows16, idQ, 1u);
                 }
                 commit(dq_full);
                 {   // dK += dS^T Q
                     const SDesc bq = dQn + s * kSlot;
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        ss(tm + kColDK, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
+                        ss(tm + kColDKt, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
                 }
                 commit(&q_empty[s]);
                 if (!more) {
@@ -716,7 +722,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
 #pragma unroll 1
             for (int c = half * (HD / 64); c < (half + 1) * (HD / 64); ++c) {
                 uint32_t uv[32], uk[32];
-                tmem_ld32x2(tmem + lane_base + kColDV + c * 32, tmem + lane_base + kColDK + c * 32, uv, uk);
+                tmem_ld32x2(tmem + lane_base + kColDV + c * 32, tmem + lane_base + kColDKt + c * 32, uv, uk);
                 if constexpr (SINK) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) uv[e] = __float_as_uint(__uint_as_float(uv[e]) * a.scale_v);
@@ -799,7 +805,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
         // TMEM lane = head-dim element of dQ^T; column c = query row i*128 + c.
         // Two warpgroups: warpgroup dg drains query columns [64 dg, 64 dg + 64).
         const int dg = (warp - 12) / 4;
-        const uint32_t tdQ = tmem + ((uint32_t)((warp % 4) * 32) << 16) + kColDP + dg * 64;
+        const uint32_t tdQ = tmem + ((uint32_t)((warp % 4) * 32) << 16) + kColDQ + dg * 64;
         uint32_t n = 0;
         bool ok = true;
         uint64_t wt = 0;
