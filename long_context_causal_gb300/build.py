@@ -2,7 +2,8 @@
 
 Every translation unit under ``csrc/`` is compiled by nvcc in parallel into
 ``_build/`` and linked into ``long_context_causal_gb300/libdfa.so`` with the
-CUDA runtime linked statically.  Set ``DFA_PTXAS_VERBOSE=1`` to print
+CUDA runtime linked statically.  Beside it, ``binding/dfa_torch.cpp`` becomes
+the extension module ``_dfa_torch`` (host code only, against this torch).  Set ``DFA_PTXAS_VERBOSE=1`` to print
 register / shared-memory use per kernel.
 """
 from __future__ import annotations
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(os.path.dirname(PKG), "_build")
 LIB = os.path.join(PKG, "libdfa.so")
+BINDING = os.path.join(PKG, "binding", "dfa_torch.cpp")
+BINDING_LIB = os.path.join(PKG, "_dfa_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -53,7 +56,44 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_LIB):
+        return False
+    t = os.path.getmtime(BINDING_LIB)
+    return all(os.path.getmtime(d) <= t for d in [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_binding() -> str:
+    """The extension module, by the host compiler against the torch that runs."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_LIB + f".tmp{os.getpid()}"
+    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] +
+           ["-isystem" + i for i in include] + [BINDING, "-o", tmp, "-L" + os.path.join(root, "lib")] +
+           ["-l" + x for x in ("torch_python", "torch", "torch_cpu", "c10", "c10_cuda")])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = None if binding_up_to_date() and not force else ex.submit(build_binding)
+        build_library(force, verbose)
+        if binding:
+            binding.result()
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

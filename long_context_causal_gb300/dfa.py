@@ -1,7 +1,8 @@
 """Python binding of libdfa.so (include/dfa.h) -- argument marshalling only.
 
-Each function has the name of the C entry point it calls.  Torch tensors are
-used for device memory and streams: the binding reads their data pointers,
+Each function has the name of the C entry point it calls (those of the windowed
+attention and the checkpoints by way of the extension module _dfa_torch).  Torch
+tensors are used for device memory and streams: the binding reads their data pointers,
 sizes and strides, allocates missing outputs/workspace with torch, passes the
 current CUDA stream, and raises ``DfaError`` on any non-OK status.  All
 arithmetic runs in the library's CUDA kernels; there is no CPU fallback, and
@@ -10,7 +11,6 @@ importing this module fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 
@@ -431,97 +431,38 @@ def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: f
 
 
 # -------------------------------------------- sliding window of tokens with sinks, 8-bit checkpoints
-# A call's checks and allocations are most of what a short problem costs, so
-# these functions take the cheapest accessors there are (pointers as plain
-# ints, devices as their index, the current stream without a Stream object),
-# and only a check that fails looks for what to say.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_device_now = torch._C._cuda_getDevice
-_empty, _empty_like, _F32, _BF16, _U8 = torch.empty, torch.empty_like, torch.float32, torch.bfloat16, torch.uint8
+# Marshalled in C++ (binding/dfa_torch.cpp): reading and checking tensors and
+# allocating outputs from Python costs several times what a short call runs for
+# on the GPU.  The functions there check every tensor and either return the
+# results or the library's status.
+def _load_native():
+    try:
+        from long_context_causal_gb300 import _dfa_torch as native
+    except ImportError as e:
+        raise ImportError("the extension module _dfa_torch is not built for this torch: run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    native.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+        "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
+        "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
+        "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size")))
+    return native
 
 
-def _gpu_of(*named) -> int:
-    """Every tensor must lie on the current CUDA device: the library launches
-    there, on the pointers it is given.  Returns its index."""
-    d = named[0].get_device()
-    for t in named:
-        if d < 0 or t.get_device() != d:
-            raise ValueError(f"the tensors must be CUDA tensors on one device, got {[str(x.device) for x in named]}")
-    if d != _device_now():
-        raise ValueError(f"the tensors are on cuda:{d}, the current device is cuda:{_device_now()}")
-    return d
+_native = _load_native()
 
 
-def _on(stream, d: int) -> int:
-    """Handle of the stream a call runs on (None: the current one)."""
-    if stream is None:
-        return _raw_stream(d)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _sequence(q, k, v):
-    """B, S, H, H_kv, D, device index of dense q [B,S,H,D] and k, v [B,S,H_kv,D]."""
-    qs, ks = q.shape, k.shape
-    if len(qs) != 4 or len(ks) != 4 or ks != v.shape or ks[0] != qs[0] or ks[1] != qs[1] or ks[3] != qs[3]:
-        raise ValueError(f"q must be [B, S, H, D] and k, v [B, S, H_kv, D], got {tuple(qs)}, {tuple(ks)}, {tuple(v.shape)}")
-    dt = q.dtype
-    if k.dtype is not dt or v.dtype is not dt:
-        raise ValueError("q, k and v must have the same dtype")
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
-        raise ValueError("q, k and v must be contiguous (BSHD dense)")
-    d = q.get_device()
-    if d < 0 or k.get_device() != d or v.get_device() != d or d != _device_now():
-        _gpu_of(q, k, v)
-    B, S, H, D = qs
-    return B, S, H, ks[2], D, d
-
-
-def _given(t, name, shape, dtype, d):
-    """A tensor the caller hands over must be dense and of exactly this shape,
-    dtype and device."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != d or not t.is_contiguous():
-        _like(t, name, shape, dtype, torch.device("cuda", d))
-    return t
-
-
-@functools.lru_cache(maxsize=1024)
-def _bytes_for(size, d, *args) -> int:
-    """A size query's answer for device d (it depends on the device and the arguments alone)."""
-    return size(*args)
-
-
-def _dt(t) -> int:
-    return DFA_BF16 if t.dtype is _BF16 else _dtype(t)
-
-
-def _scratch(nbytes, device, stream):
-    """Workspace for one call, owned by the stream the call runs on: the
-    allocator then reuses it only behind the call's kernels."""
-    if stream is None:
-        return _empty(max(nbytes, 16), dtype=_U8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(s):
-        return _empty(max(nbytes, 16), dtype=_U8, device=device)
-
-
-def _bytes_buf(t, name, d):
-    if t.dtype is not _U8 or t.get_device() != d or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 tensor on cuda:{d}")
-    return t
+def _result(r):
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def dfa_attn_fwd_sink(q, k, v, window: int, n_sink: int = 0, scale: float | None = None, O=None, lse=None,
                       stream=None):
     """Causal forward over a sliding window of `window` tokens and the first
-    `n_sink` ones: returns (O [B,S,H,D], lse fp32 [B,H,S])."""
-    B, S, H, Hkv, D, d = _sequence(q, k, v)
-    O = _empty_like(q) if O is None else _given(O, "O", q.shape, q.dtype, d)
-    lse = _empty((B, H, S), dtype=_F32, device=q.device) if lse is None else _given(lse, "lse", (B, H, S), _F32, d)
-    st = _lib.dfa_attn_fwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), B, H, Hkv, S, D, window, n_sink,
-                                D ** -0.5 if scale is None else scale, O.data_ptr(), lse.data_ptr(), _on(stream, d))
-    if st:
-        _check(st)
-    return O, lse
+    `n_sink` ones: q [B,S,H,D], k, v [B,S,H_kv,D] bf16 dense; returns
+    (O [B,S,H,D], lse fp32 [B,H,S])."""
+    return _result(_native.fwd_sink(q, k, v, window, n_sink, scale, O, lse, stream))
 
 
 def dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
@@ -531,22 +472,7 @@ def dfa_attn_bwd_sink_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
 def dfa_attn_bwd_sink(q, k, v, O, lse, dO, window: int, n_sink: int = 0, scale: float | None = None, dQ=None,
                       dK=None, dV=None, workspace_buf=None, stream=None):
     """Backward of dfa_attn_fwd_sink from the saved (O, lse): returns (dQ, dK, dV)."""
-    B, S, H, Hkv, D, d = _sequence(q, k, v)
-    qs, dt = q.shape, q.dtype
-    _given(O, "O", qs, dt, d)
-    _given(dO, "dO", qs, dt, d)
-    _given(lse, "lse", (B, H, S), _F32, d)
-    dQ = _empty_like(q) if dQ is None else _given(dQ, "dQ", qs, dt, d)
-    dK = _empty_like(k) if dK is None else _given(dK, "dK", k.shape, dt, d)
-    dV = _empty_like(k) if dV is None else _given(dV, "dV", k.shape, dt, d)
-    ws = (_scratch(_bytes_for(dfa_attn_bwd_sink_workspace_size, d, B, H, Hkv, S, D, window, n_sink), q.device, stream)
-          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", d))
-    st = _lib.dfa_attn_bwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), lse.data_ptr(), dO.data_ptr(),
-                                _dt(q), B, H, Hkv, S, D, window, n_sink, D ** -0.5 if scale is None else scale,
-                                dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d))
-    if st:
-        _check(st)
-    return dQ, dK, dV
+    return _result(_native.bwd_sink(q, k, v, O, lse, dO, window, n_sink, scale, dQ, dK, dV, workspace_buf, stream))
 
 
 def dfa_attn_decode_sink_workspace_size(B, H, H_kv, D) -> int:
@@ -558,32 +484,7 @@ def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: f
     """One new token per sequence over a cache: q [B,H,D], k, v [B,S_max,H_kv,D]
     (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
     GPU; returns (O [B,H,D], lse fp32 [B,H])."""
-    qs, ks, dt = q.shape, k.shape, q.dtype
-    if len(qs) != 3 or len(ks) != 4 or ks != v.shape or ks[0] != qs[0] or ks[3] != qs[2]:
-        raise ValueError(f"q must be [B, H, D] and k, v [B, S_max, H_kv, D], got {tuple(qs)}, {tuple(ks)}, {tuple(v.shape)}")
-    if k.dtype is not dt or v.dtype is not dt:
-        raise ValueError("q, k and v must have the same dtype")
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous ([B, H, D] dense)")
-    strides = None
-    if not (k.is_contiguous() and v.is_contiguous()):
-        st = k.stride()
-        if st != v.stride() or st[3] != 1:
-            raise ValueError("k and v must share their strides, with the head dimension contiguous")
-        strides = (ctypes.c_int64 * 3)(*st[:3])
-    d = _gpu_of(q, k, v)
-    B, H, D = qs
-    _given(kv_len, "kv_len", (B,), torch.int32, d)
-    O = _empty_like(q) if O is None else _given(O, "O", qs, dt, d)
-    lse = _empty((B, H), dtype=_F32, device=q.device) if lse is None else _given(lse, "lse", (B, H), _F32, d)
-    ws = (_scratch(_bytes_for(dfa_attn_decode_sink_workspace_size, d, B, H, ks[2], D), q.device, stream) if workspace_buf is None
-          else _bytes_buf(workspace_buf, "workspace_buf", d))
-    st = _lib.dfa_attn_decode_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), B, H, ks[2], ks[1], D, strides,
-                                   kv_len.data_ptr(), window, n_sink, D ** -0.5 if scale is None else scale, O.data_ptr(),
-                                   lse.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d))
-    if st:
-        _check(st)
-    return O, lse
+    return _result(_native.decode_sink(q, k, v, kv_len, window, n_sink, scale, O, lse, workspace_buf, stream))
 
 
 def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:
@@ -593,31 +494,12 @@ def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:
 def dfa_ckpt8_save(q, k, v, O, ckpt=None, stream=None):
     """q, k, v and O of one attention layer in 8 bits: returns the checkpoint
     (a uint8 tensor of dfa_ckpt8_size bytes)."""
-    B, S, H, Hkv, D, d = _sequence(q, k, v)
-    _given(O, "O", q.shape, q.dtype, d)
-    ckpt = (_empty(_bytes_for(dfa_ckpt8_size, d, B, H, Hkv, S, D), dtype=_U8, device=q.device) if ckpt is None
-            else _bytes_buf(ckpt, "ckpt", d))
-    st = _lib.dfa_ckpt8_save(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), _dt(q), B, H, Hkv, S, D,
-                             ckpt.data_ptr(), ckpt.numel(), _on(stream, d))
-    if st:
-        _check(st)
-    return ckpt
+    return _result(_native.ckpt8_save(q, k, v, O, ckpt, stream))
 
 
 def dfa_ckpt8_restore(ckpt, B: int, H: int, H_kv: int, S: int, D: int, q=None, k=None, v=None, O=None, stream=None):
     """The bf16 tensors (q, k, v, O) a checkpoint stands for."""
-    d, dev = _gpu_of(ckpt), ckpt.device
-    _bytes_buf(ckpt, "ckpt", d)
-    qs, ks = (B, S, H, D), (B, S, H_kv, D)
-    q = _empty(qs, dtype=_BF16, device=dev) if q is None else _given(q, "q", qs, _BF16, d)
-    k = _empty(ks, dtype=_BF16, device=dev) if k is None else _given(k, "k", ks, _BF16, d)
-    v = _empty_like(k) if v is None else _given(v, "v", ks, _BF16, d)
-    O = _empty_like(q) if O is None else _given(O, "O", qs, _BF16, d)
-    st = _lib.dfa_ckpt8_restore(ckpt.data_ptr(), ckpt.numel(), DFA_BF16, B, H, H_kv, S, D, q.data_ptr(), k.data_ptr(),
-                                v.data_ptr(), O.data_ptr(), _on(stream, d))
-    if st:
-        _check(st)
-    return q, k, v, O
+    return _result(_native.ckpt8_restore(ckpt, B, H, H_kv, S, D, q, k, v, O, stream))
 
 
 def dfa_attn_bwd_ckpt8_workspace_size(B, H, H_kv, S, D, window, n_sink) -> int:
@@ -628,26 +510,7 @@ def dfa_attn_bwd_ckpt8(ckpt, lse, dO, H_kv: int, window: int | None = None, n_si
                        scale: float | None = None, dQ=None, dK=None, dV=None, workspace_buf=None, stream=None):
     """Backward from an 8-bit checkpoint, the saved lse and dO [B,S,H,D], with
     the forward's window (None: plain causal): returns (dQ, dK, dV)."""
-    qs, dt = dO.shape, dO.dtype
-    if len(qs) != 4 or not dO.is_contiguous():
-        raise ValueError(f"dO must be a contiguous [B, S, H, D] tensor, got {tuple(qs)}")
-    B, S, H, D = qs
-    ks = (B, S, H_kv, D)
-    d = _gpu_of(dO, ckpt)
-    _bytes_buf(ckpt, "ckpt", d)
-    _given(lse, "lse", (B, H, S), _F32, d)
-    window = max(S, 1) if window is None else window
-    dQ = _empty_like(dO) if dQ is None else _given(dQ, "dQ", qs, dt, d)
-    dK = _empty(ks, dtype=dt, device=dO.device) if dK is None else _given(dK, "dK", ks, dt, d)
-    dV = _empty(ks, dtype=dt, device=dO.device) if dV is None else _given(dV, "dV", ks, dt, d)
-    ws = (_scratch(_bytes_for(dfa_attn_bwd_ckpt8_workspace_size, d, B, H, H_kv, S, D, window, n_sink), dO.device, stream)
-          if workspace_buf is None else _bytes_buf(workspace_buf, "workspace_buf", d))
-    st = _lib.dfa_attn_bwd_ckpt8(ckpt.data_ptr(), ckpt.numel(), lse.data_ptr(), dO.data_ptr(), _dt(dO), B, H, H_kv, S, D,
-                                 window, n_sink, D ** -0.5 if scale is None else scale, dQ.data_ptr(), dK.data_ptr(),
-                                 dV.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, d))
-    if st:
-        _check(st)
-    return dQ, dK, dV
+    return _result(_native.bwd_ckpt8(ckpt, lse, dO, H_kv, window, n_sink, scale, dQ, dK, dV, workspace_buf, stream))
 
 
 def dfa_debug_mma(form: int, A, B, C=None, stream=None):
