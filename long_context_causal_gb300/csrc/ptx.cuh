@@ -218,10 +218,11 @@ __device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, 
 // 4 x 4 transpose inside each quad of lanes (lanes 4q..4q+3): on entry lane
 // 4q+j holds x[m] = element (j, m) of its quad's block, on exit lane 4q+m holds
 // x[j] = element (j, m).  Four shuffles.
-__device__ __forceinline__ void quad_transpose(float (&x)[4], int lane) {
+template <typename T>
+__device__ __forceinline__ void quad_transpose(T (&x)[4], int lane) {
     const bool o1 = lane & 1, o2 = lane & 2;
-    float r0 = __shfl_xor_sync(0xffffffffu, o1 ? x[0] : x[1], 1);
-    float r1 = __shfl_xor_sync(0xffffffffu, o1 ? x[2] : x[3], 1);
+    T r0 = __shfl_xor_sync(0xffffffffu, o1 ? x[0] : x[1], 1);
+    T r1 = __shfl_xor_sync(0xffffffffu, o1 ? x[2] : x[3], 1);
     if (o1) { x[0] = r0; x[2] = r1; } else { x[1] = r0; x[3] = r1; }
     r0 = __shfl_xor_sync(0xffffffffu, o2 ? x[0] : x[2], 2);
     r1 = __shfl_xor_sync(0xffffffffu, o2 ? x[1] : x[3], 2);

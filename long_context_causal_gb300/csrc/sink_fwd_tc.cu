@@ -18,16 +18,28 @@
 // W / 128 + 1 tiles, not W / 128 + 2.  The sink tile's MMAs are as wide as the
 // sinks, rounded up to 16 columns: N = 4 costs an eighth of a tile.
 //
+// What bounds it.  A query tile's steps form a chain: S (550 cycles at D = 128),
+// the softmax of its row (1600), two barriers (500), P V (550, of which half
+// runs under the softmax).  The two chains of a CTA overlap, and the tensor
+// cores work for 2200 of a step's 2800 cycles.  A block's ends -- masked tiles,
+// the sink tile's step, the epilogue -- cost another 4 us of chain, so the lists
+// of a CTA's blocks run on into one another (issuer), a 32-column piece of a
+// masked tile pays for its mask only if some of its elements are masked (Mask),
+// and the output leaves in 64-byte pieces.  Measured, 32K tokens, 32 heads of 8 kv
+// heads, 4 sinks: window 4096 1425 us (D = 128; 1460 TFLOP/s, 77% of the cuBLAS
+// rate), window 1024 530; D = 64 1278 and 480.
+//
 // Schedule.  No work list: costs never fall from a block to the next one of
 // its head, so the blocks in the order last to first of all heads are sorted
 // by cost, and dealing them to the persistent CTAs in a snake (0..n-1, then
 // n-1..0, ...) balances them to within one block.  Nothing is uploaded and
 // there is no workspace, so a call is one launch and can be captured.
 //
-// Roles (384 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer
-// (one lane issues), warp 2 TMEM owner, warps 4-11 two softmax warpgroups, one
-// query row per thread.  TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D)
-// O_1 [384,384+D); P_w (bf16 pairs) overwrites the first 64 columns of S_w.
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer of K and V, warp 1 MMA
+// issuer (one lane issues), warp 2 TMEM owner, warp 3 TMA producer of Q, warps 4-11
+// two softmax warpgroups, one query row per thread.  TMEM columns: S_0 [0,128)
+// S_1 [128,256) O_0 [256,256+D) O_1 [384,384+D); P_w (bf16 pairs) overwrites the
+// first 64 columns of S_w.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,19 +61,35 @@ constexpr int BN = 128;            // key rows per tile
 constexpr int kBlockRows = 2 * BM;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kMinusInf = 0xff800000u;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O only when the max grows by > 2^8
 
 template <int D>
 struct Cfg {
     static constexpr int kTileBytes = BN * D * 2;
     static constexpr int kSlots = D == 128 ? 4 : 6;            // K/V ring depth
+    static constexpr bool kHalves = D == 128;                  // P is handed over in two halves (rule at p_half)
     static constexpr int kQBytes = 2 * kTileBytes;
     static constexpr int kSmem = kQBytes + kSlots * kTileBytes + 1024 /*barriers*/ + 1024 /*align*/;
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(l-1) < d <= 2^l and
+// m = floor(2^(31 + l) / d) + 1, m d exceeds 2^(31 + l) by at most d <= 2^l, so
+// n m / 2^(31 + l) exceeds n / d by less than 1 / d (Granlund and Montgomery 1994).
+// A block's start divides five times; the divisions took 1700 cycles of it.
+struct Divider {
+    uint32_t d, m, shift;
+    Divider(int x = 1) : d((uint32_t)x), shift(31) {
+        while ((uint64_t{1} << (shift - 31)) < d) ++shift;
+        m = (uint32_t)((uint64_t{1} << shift) / d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((uint64_t)(uint32_t)n * m >> shift); }
+};
+
 struct Args {
-    int rows;              // B * H
-    int H, G, S;           // G = H / H_kv
+    Divider rows;          // B * H
+    Divider H, G;          // G = H / H_kv
+    int S;
     int window, n_sink;    // window <= S; n_sink <= 128, 0 when the window covers every key
     int n_units, n_items;  // 256-row blocks per head; rows * n_units
     float scale_log2;      // scale * log2(e)
@@ -70,46 +98,53 @@ struct Args {
     int* err;
 };
 
-// Band of the 128-row query tile whose first row is f: key tiles [lo, hi], none if f is past the end.
-struct Band {
-    int lo, hi;
-    // How the tile takes part in key tile j: 0 not at all, 1 the sink columns only, 2 the whole tile.
-    __device__ __forceinline__ int part(int j, int n_sink) const {
-        if (j > hi) return 0;
-        if (j >= lo) return 2;
-        return j == 0 && n_sink > 0 ? 1 : 0;
-    }
-};
-__device__ __forceinline__ Band band(const Args& a, int f) {
-    return Band{max(f - a.window + 1, 0) / BN, f < a.S ? f / BN : -1};
-}
-
+// A block's list of key tiles: the sink tile, when the window has moved off it, then the band.
 struct Block {
     int b, h, g, q0;
     int j0;                // first key tile of the band
     int n;                 // key tiles in the list
-    int sink0;             // 1: the list starts with tile 0 as a sink tile
+    int lead;              // 1: the list starts with tile 0 as a sink tile
     // k-th key tile of the list
-    __device__ __forceinline__ int tile(int k) const { return (sink0 && k == 0) ? 0 : j0 + k - sink0; }
+    __device__ __forceinline__ int tile(int k) const { return lead && k == 0 ? 0 : j0 + k - lead; }
 };
 
 __device__ __forceinline__ Block decode(const Args& a, int it) {
     Block x;
-    const int row = it % a.rows, unit = a.n_units - 1 - it / a.rows;
-    x.b = row / a.H;
-    x.h = row % a.H;
-    x.g = x.h / a.G;
+    const int u = a.rows.div(it), row = it - u * (int)a.rows.d, unit = a.n_units - 1 - u;
+    x.b = a.H.div(row);
+    x.h = row - x.b * (int)a.H.d;
+    x.g = a.G.div(x.h);
     x.q0 = unit * kBlockRows;
-    const Band lo = band(a, x.q0), hi = band(a, x.q0 + BM);
-    x.j0 = lo.lo;
-    x.sink0 = a.n_sink > 0 && x.j0 > 0;
-    x.n = max(lo.hi, hi.hi) - x.j0 + 1 + x.sink0;
+    x.j0 = max(x.q0 - a.window + 1, 0) / BN;
+    const bool two = x.q0 + BM < a.S;                     // the second query tile has rows
+    x.lead = a.n_sink > 0 && x.j0 > 0;
+    x.n = x.lead + (x.q0 / BN + two - x.j0 + 1);
     return x;
+}
+
+// How a block's query tile takes part in its list: in the band's positions
+// [b0, b1], none if b1 < 0, and in the first one's sink columns if its own band
+// starts behind that tile.
+struct Run {
+    int b0, b1;
+    int sink;              // 0, or -1: no sink tile
+    // 0 not at all, 1 the sink columns only, 2 the whole tile.
+    __device__ __forceinline__ int part(int k) const { return k == sink ? 1 : (k >= b0 && k <= b1) ? 2 : 0; }
+};
+__device__ __forceinline__ Run run(const Args& a, const Block& x, int w) {
+    const int f = x.q0 + w * BM;
+    if (f >= a.S) return Run{0, -1, -1};                  // no rows
+    const int lo = max(f - a.window + 1, 0) / BN, at = x.lead - x.j0;
+    return Run{lo + at, f / BN + at, a.n_sink > 0 && lo > 0 ? 0 : -1};
 }
 
 // Column c of a tile is visible iff (c >= lo or c < ns) and c < lim.
 struct Mask {
     int lo, lim, ns;
+    int lo0, lim0, more;   // lo and lim of the warp's first row; its last row's are `more` larger
+    // The warp's rows and columns [c, c + 32): none visible, all visible.
+    __device__ __forceinline__ bool none(int c) const { return lim0 + more <= c || (lo0 >= c + 32 && ns <= c); }
+    __device__ __forceinline__ bool all(int c) const { return lo0 + more <= c && lim0 >= c + 32; }
     // bit e: column c + e
     __device__ __forceinline__ uint32_t bits(int c) const {
         return (~low_bits(lo - c) | low_bits(ns - c)) & low_bits(lim - c);
@@ -122,49 +157,65 @@ __device__ __forceinline__ float row_max(uint32_t tS, int chunks, Mask k) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
-        if (MASK && !__any_sync(0xffffffffu, see)) continue;   // no row of the warp sees the 32 columns
+        if (MASK && k.none(c * 32)) continue;
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
+        if (MASK && !k.all(c * 32)) {
+            const uint32_t see = k.bits(c * 32);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float x = __uint_as_float(u[e]);
-            m[e & 3] = fmaxf(m[e & 3], (!MASK || (see >> e & 1)) ? x : -INFINITY);
+            for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(u[e]));
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// The warp's P so far is in TMEM.  Arrivals of whole warps or of their threads
+// (32K tokens, window 4096: D = 128 1425 us with warps' and 1454 with threads', D = 64 1297
+// and 1278).
+template <bool WARP>
+__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
+    tmem_st_wait();
+    tc_fence_before();
+    if (WARP) __syncwarp();
+    if (!WARP || lane == 0) mbar_arrive(bar);
+}
+
 // P = exp2(s * c2 - m) of the same columns, written as bf16 pairs over S (behind
-// the columns still to be read).  Returns the row sum of the unrounded P.
-template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float c2, float m) {
+// the columns still to be read); `half` is told when 64 columns are there.
+// Returns the row sum of the unrounded P.
+template <bool MASK, bool HALVES>
+__device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float c2, float m, uint64_t* half, int lane) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         uint32_t pk[16];
-        const uint32_t see = MASK ? k.bits(c * 32) : 0u;
-        if (MASK && !__any_sync(0xffffffffu, see)) {
+        if (MASK && k.none(c * 32)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = 0;
             tmem_st16(tS + c * 16, pk);
+            if (HALVES && c == 1) hand_over<HALVES>(half, lane);
             continue;
         }
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
+        if (MASK && !k.all(c * 32)) {
+            const uint32_t see = k.bits(c * 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
-            float p1 = ex2(fmaf(__uint_as_float(u[2 * e + 1]), c2, -m));
-            if (MASK) {
-                p0 = see >> (2 * e) & 1 ? p0 : 0.f;
-                p1 = see >> (2 * e + 1) & 1 ? p1 : 0.f;
-            }
+            const float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
+            const float p1 = ex2(fmaf(__uint_as_float(u[2 * e + 1]), c2, -m));
             acc[e & 3] += p0 + p1;
             pk[e] = pack_bf16(p0, p1);
         }
         tmem_st16(tS + c * 16, pk);
+        if (HALVES && c == 1) hand_over<HALVES>(half, lane);
     }
+    if (HALVES && chunks == 1) hand_over<HALVES>(half, lane);
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -181,9 +232,13 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* q_full = bars + 0;          // [2], as all of these one per query tile
     uint64_t* q_empty = bars + 2;
     uint64_t* s_full = bars + 4;
-    uint64_t* p_full = bars + 6;
-    uint64_t* o_full = bars + 8;
-    uint64_t* done = bars + 10;
+    // The first 64 columns of P: the product with V starts on them while the softmax works on
+    // the others (32K tokens, window 4096, D = 128: 1452 us, without it 1474; at D = 64 the
+    // product is short and the second wait costs more than it gives: 1297, with it 1338).
+    uint64_t* p_half = bars + 8;
+    uint64_t* p_full = bars + 10;
+    uint64_t* o_full = bars + 12;
+    uint64_t* done = bars + 14;
     uint64_t* kv_full = bars + 16;        // [kSlots]
     uint64_t* kv_empty = bars + 16 + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
@@ -197,7 +252,8 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&q_full[w], 1);
             mbar_init(&q_empty[w], 1);
             mbar_init(&s_full[w], 1);
-            mbar_init(&p_full[w], BM);
+            mbar_init(&p_half[w], 4);
+            mbar_init(&p_full[w], C::kHalves ? 4 : BM);
             mbar_init(&o_full[w], 1);
         }
         mbar_init(done, 1);
@@ -221,24 +277,11 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
-        uint32_t ld = 0, qi = 0;
+        // ------------------------------------------------------------ TMA producer of K and V
+        uint32_t ld = 0;
         bool ok = true;
         for (int r = 0; r < rounds && ok; ++r) {
             const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
-            for (int w = 0; w < 2 && ok; ++w) {
-                ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[w], (r & 1) ^ 1, abort_flag, a.err, nullptr));
-                if (!ok) break;
-                ++qi;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[w], C::kTileBytes);
-                    for (int blk = 0; blk < D / 64; ++blk)
-                        tma_load_4d(sQ + w * C::kTileBytes + blk * 16384, &tmQ, &q_full[w], blk * 64, x.h, x.q0 + w * BM,
-                                    x.b);
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
             for (int k = 0; k < x.n && ok; ++k) {
                 const int j = x.tile(k);
                 for (int which = 0; which < 2; ++which, ++ld) {
@@ -263,6 +306,29 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const uint32_t last = s + C::kSlots * ((ld - 1 - s) / C::kSlots);
                 mbar_wait(&kv_full[s], (last / C::kSlots) & 1, &dummy, nullptr);
             }
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ TMA producer of Q: a warp of its own, for
+        // the other one would not load the next block's first keys before a query tile's buffer is free
+        uint32_t qi = 0;
+        bool ok = true;
+        for (int r = 0; r < rounds && ok; ++r) {
+            const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
+            for (int w = 0; w < 2 && ok; ++w) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[w], (r & 1) ^ 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                ++qi;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[w], C::kTileBytes);
+                    for (int blk = 0; blk < D / 64; ++blk)
+                        tma_load_4d(sQ + w * C::kTileBytes + blk * 16384, &tmQ, &q_full[w], blk * 64, x.h, x.q0 + w * BM,
+                                    x.b);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) {
+            int dummy = 0;
             for (uint32_t m = qi > 1 ? qi - 2 : 0; m < qi; ++m) mbar_wait(&q_full[m & 1], (m >> 1) & 1, &dummy, nullptr);
         }
     } else if (warp == 1) {
@@ -294,100 +360,119 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             mma_commit_lead(lead, &s_full[w]);
         };
-        auto issue_PV = [&](int w, uint32_t slot, uint32_t acc) {
+        // O_w += P_w V, the first half of the keys as soon as their P is there
+        auto issue_PV = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
+            if (!wait(C::kHalves ? &p_half[w] : &p_full[w], par)) return;
             mma_ts_lead(lead, d, p, b0, idO, acc);
 #pragma unroll
-            for (int kk = 1; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
+            for (int kk = 1; kk < BN / 32; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
+            if (C::kHalves && !wait(&p_full[w], par)) return;
+#pragma unroll
+            for (int kk = BN / 32; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
         };
-        auto issue_PV_sink = [&](int w, uint32_t slot, uint32_t acc) {
+        auto issue_PV_sink = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
+            if (C::kHalves && !wait(&p_half[w], par)) return;
+            if (!wait(&p_full[w], par)) return;
 #pragma unroll 1
             for (int kk = 0; kk < ns16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, kk > 0 ? 1u : acc);
         };
-        for (int r = 0; r < rounds && ok; ++r) {
-            const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
-            const Band bd[2] = {band(a, x.q0), band(a, x.q0 + BM)};
-            uint32_t slotK = cons % C::kSlots;
-            if (!wait(&kv_full[slotK], (cons / C::kSlots) & 1)) break;
-            ++cons;
-            int now[2], first[2] = {1, 1};
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (!wait(&q_full[w], r & 1)) break;
-                now[w] = bd[w].part(x.tile(0), a.n_sink);
-                if (now[w]) issue_S(w, slotK, now[w] == 1 ? idSink : idS);
-                // The query tile's last product is the one with the band's last tile; its buffer
-                // is then free for the next block's.  A tile past the end has none.
-                if (x.tile(0) >= bd[w].hi) mma_commit_lead(lead, &q_empty[w]);
-            }
-            if (!ok) break;
-            mma_commit_lead(lead, &kv_empty[slotK]);
+        // The blocks' lists run on into one another: at a block's last key tile the next block's
+        // first S is issued where its next S would be, so that neither warpgroup waits for the
+        // other one's end or for its own epilogue.  Block -1 is empty.
+        uint32_t now[2] = {0, 0}, first[2] = {1, 1};
+        Block x{}, y{};
+        Run u0{0, -1, -1}, u1 = u0, v0 = u0, v1 = u0;
+        if (rounds > 0) {
+            y = decode(a, snake_item(0, blockIdx.x, gridDim.x));
+            v0 = run(a, y, 0);
+            v1 = run(a, y, 1);
+        }
+        int k = -1, r = -1;
+        for (;;) {
             // Steps in which both query tiles take both key tiles whole run without looking at the bands.
-            const int hot = bd[0].hi - x.j0 + x.sink0;       // the first query tile's last key tile in the list
-            int k = 0;
-            while (k < x.n) {
-                if (now[0] == 2 && now[1] == 2 && k < hot) {
-                    const uint32_t acc0 = 1u - first[0], acc1 = 1u - first[1];
-                    first[0] = first[1] = 0;
-                    uint32_t a0 = acc0, a1 = acc1;
-                    for (; k < hot; ++k) {
-                        const uint32_t slotV = cons % C::kSlots;
-                        if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
-                        if (!wait(&p_full[0], t[0] & 1)) break;
-                        ++t[0];
-                        issue_PV(0, slotV, a0);
-                        slotK = (cons + 1) % C::kSlots;
-                        if (!wait(&kv_full[slotK], ((cons + 1) / C::kSlots) & 1)) break;
-                        issue_S(0, slotK, idS);
-                        if (!wait(&p_full[1], t[1] & 1)) break;
-                        ++t[1];
-                        issue_PV(1, slotV, a1);
-                        mma_commit_lead(lead, &kv_empty[slotV]);
-                        issue_S(1, slotK, idS);
-                        mma_commit_lead(lead, &kv_empty[slotK]);
-                        cons += 2;
-                        a0 = a1 = 1u;
-                    }
+            const int hot = u0.b1;
+            if (now[0] == 2 && now[1] == 2 && k < hot) {
+                uint32_t a0 = 1u - first[0], a1 = 1u - first[1];
+                first[0] = first[1] = 0;
+                for (; k < hot; ++k) {
+                    const uint32_t slotV = cons % C::kSlots;
+                    if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
+                    issue_PV(0, slotV, t[0]++ & 1, a0);
                     if (!ok) break;
-                    mma_commit_lead(lead, &q_empty[0]);   // its last product is issued; the second query tile has one more
-                }
-                const bool more = k + 1 < x.n;
-                const uint32_t slotV = cons % C::kSlots;
-                if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
-                slotK = (cons + 1) % C::kSlots;
-                bool have_k = false;
-                const int jn = x.tile(k + 1);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int next = more ? bd[w].part(jn, a.n_sink) : 0;
-                    if (now[w]) {
-                        if (!wait(&p_full[w], t[w] & 1)) break;
-                        ++t[w];
-                        if (now[w] == 2) issue_PV(w, slotV, first[w] ? 0u : 1u);
-                        else issue_PV_sink(w, slotV, first[w] ? 0u : 1u);
-                        first[w] = 0;
-                    }
-                    if (w == 1) mma_commit_lead(lead, &kv_empty[slotV]);
-                    // a query tile takes part in an unbroken run of the list, sinks apart: it has ended
-                    // when the tile after this one lies beyond its band
-                    if (now[w] && (!more || jn > bd[w].hi)) mma_commit_lead(lead, &o_full[w]);
-                    if (next) {
-                        if (!have_k) {
-                            if (!wait(&kv_full[slotK], ((cons + 1) / C::kSlots) & 1)) break;
-                            have_k = true;
-                        }
-                        issue_S(w, slotK, next == 1 ? idSink : idS);
-                        if (jn == bd[w].hi) mma_commit_lead(lead, &q_empty[w]);
-                    }
-                    if (w == 1 && more) mma_commit_lead(lead, &kv_empty[slotK]);
-                    now[w] = next;
+                    const uint32_t slotK = (cons + 1) % C::kSlots;
+                    if (!wait(&kv_full[slotK], ((cons + 1) / C::kSlots) & 1)) break;
+                    issue_S(0, slotK, idS);
+                    issue_PV(1, slotV, t[1]++ & 1, a1);
+                    if (!ok) break;
+                    mma_commit_lead(lead, &kv_empty[slotV]);
+                    issue_S(1, slotK, idS);
+                    mma_commit_lead(lead, &kv_empty[slotK]);
+                    cons += 2;
+                    a0 = a1 = 1u;
                 }
                 if (!ok) break;
-                cons += more ? 2 : 1;
-                ++k;
+                mma_commit_lead(lead, &q_empty[0]);   // its last product is issued; the second query tile has one more
+            }
+            const bool end = k + 1 == x.n, more = !end || r + 1 < rounds;
+            const int kn = end ? 0 : k + 1, rn = end ? r + 1 : r;
+            const uint32_t slotV = cons % C::kSlots;
+            if (k >= 0) {
+                if (!wait(&kv_full[slotV], (cons / C::kSlots) & 1)) break;
+                ++cons;
+            }
+            const uint32_t slotK = cons % C::kSlots;
+            bool have_k = false;
+            // a query tile that skips this key tile goes first: it does not wait for the other one
+            const int swap = now[1] == 0 && now[0] != 0;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int w = i ^ swap;
+                if (w ? now[1] : now[0]) {
+                    const uint32_t acc = 1u - (w ? first[1] : first[0]), par = (w ? t[1] : t[0]) & 1;
+                    if ((w ? now[1] : now[0]) == 2) issue_PV(w, slotV, par, acc);
+                    else issue_PV_sink(w, slotV, par, acc);
+                    if (!ok) break;
+                    if (w) ++t[1];
+                    else ++t[0];
+                    if (w) first[1] = 0;
+                    else first[0] = 0;
+                    if (k == (w ? u1.b1 : u0.b1)) mma_commit_lead(lead, &o_full[w]);
+                }
+                if (i == 1 && k >= 0) mma_commit_lead(lead, &kv_empty[slotV]);
+                if (!more) continue;
+                // S of the next key tile
+                const Run u = end ? (w ? v1 : v0) : (w ? u1 : u0);
+                if (kn == 0 && !wait(&q_full[w], rn & 1)) break;
+                const int part = u.part(kn);
+                if (part) {
+                    if (!have_k && !wait(&kv_full[slotK], (cons / C::kSlots) & 1)) break;
+                    have_k = true;
+                    issue_S(w, slotK, part == 1 ? idSink : idS);
+                }
+                if (w) now[1] = part;
+                else now[0] = part;
+                // behind the query tile's last product its buffer is free for the next block's
+                if (kn == max(u.b1, 0)) mma_commit_lead(lead, &q_empty[w]);
+            }
+            if (!ok || !more) break;
+            mma_commit_lead(lead, &kv_empty[slotK]);
+            ++cons;
+            k = kn;
+            if (end) {
+                r = rn;
+                x = y;
+                u0 = v0;
+                u1 = v1;
+                first[0] = first[1] = 1;
+                if (r + 1 < rounds) {
+                    y = decode(a, snake_item(r + 1, blockIdx.x, gridDim.x));
+                    v0 = run(a, y, 0);
+                    v1 = run(a, y, 1);
+                }
             }
         }
         // Drain: every MMA issued here has finished before TMEM is freed.
@@ -404,33 +489,40 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float c2 = a.scale_log2;
         uint32_t t = 0, qi = 0;
         bool ok = true;
-        for (int rd = 0; rd < rounds && ok; ++rd) {
-            const Block x = decode(a, snake_item(rd, blockIdx.x, gridDim.x));
+        Block x = decode(a, snake_item(0, blockIdx.x, gridDim.x)), y = x;
+        for (int rd = 0; rd < rounds && ok; ++rd, x = y) {
             const int f = x.q0 + w * BM, row = f + r;
-            if (f >= a.S) continue;                   // no row of the sequence in this tile
-            const Band bd = band(a, f);
+            if (f >= a.S) {                           // no row of the sequence in this tile
+                if (rd + 1 < rounds) y = decode(a, snake_item(rd + 1, blockIdx.x, gridDim.x));
+                continue;
+            }
+            const Run u = run(a, x, w);
+            const int row0 = __shfl_sync(0xffffffffu, row, 0);
             const int lo_row = row - a.window + 1, lo_last = f + BM - a.window;   // lowest visible keys
             float m_run = -INFINITY, l = 0.f;
             bool started = false;
             for (int k = 0; k < x.n; ++k) {
-                const int j = x.tile(k), part = bd.part(j, a.n_sink);
+                const int j = x.tile(k), part = u.part(k);
                 if (!part) continue;
                 ok = __all_sync(0xffffffffu, mbar_wait_acc(&s_full[w], t & 1, abort_flag, a.err, nullptr));
                 if (!ok) break;
                 ++t;
                 tc_fence_after();
                 const int kv0 = j * BN;
-                Mask mk{0, BN, 0};
+                Mask mk{0, BN, 0, 0, BN, 0};
                 int chunks = BN / 32;
                 bool masked = true;
                 if (part == 1) {
-                    mk.lim = a.n_sink;
+                    mk.lim = mk.lim0 = a.n_sink;
                     chunks = (a.n_sink + 31) / 32;
                 } else {
                     masked = kv0 + BN > f || kv0 < lo_last;   // the diagonal tile (and the ragged end) or the window's edge
                     if (masked) {
-                        mk.lo = max(lo_row - kv0, 0);
-                        mk.lim = min(row - kv0 + 1, BN);
+                        mk.lo = lo_row - kv0;
+                        mk.lim = row - kv0 + 1;
+                        mk.lo0 = row0 - a.window + 1 - kv0;
+                        mk.lim0 = row0 + 1 - kv0;
+                        mk.more = 31;
                         mk.ns = j == 0 ? a.n_sink : 0;
                     }
                 }
@@ -461,38 +553,40 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
                 started = true;
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                l += masked ? row_exp<true>(tS, chunks, mk, c2, m_use) : row_exp<false>(tS, chunks, mk, c2, m_use);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&p_full[w]);
+                l += masked ? row_exp<true, C::kHalves>(tS, chunks, mk, c2, m_use, &p_half[w], lane)
+                            : row_exp<false, C::kHalves>(tS, chunks, mk, c2, m_use, &p_half[w], lane);
+                hand_over<C::kHalves>(&p_full[w], lane);
             }
             if (!ok) break;
             // ---- epilogue: O = O_acc / l, lse = ln(sum exp(s)); every row sees itself, so l > 0
+            if (rd + 1 < rounds) y = decode(a, snake_item(rd + 1, blockIdx.x, gridDim.x));
             ok = __all_sync(0xffffffffu, mbar_wait_acc(&o_full[w], qi & 1, abort_flag, a.err, nullptr));
             if (!ok) break;
             tc_fence_after();
             ++qi;
             const bool valid = row < a.S;
             const float inv = 1.f / l;
-            uint4* dst = reinterpret_cast<uint4*>(a.O + (((int64_t)x.b * a.S + row) * a.H + x.h) * D);
-#pragma unroll
+            // A lane holds a row: stored as it stands, every 16 bytes would go to a line of their own.
+            // Four lanes exchange theirs and each store writes 64 contiguous bytes of eight rows.
+            const int row4 = row & ~3;
+            uint4* dst = reinterpret_cast<uint4*>(a.O + (((int64_t)x.b * a.S + row4) * a.H.d + x.h) * D) + (lane & 3);
+            const int64_t step = (int64_t)a.H.d * (D / 8);
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t u[32];
                 tmem_ld32(tO + c * 32, u);
-                if (valid) {
+                uint32_t o[4][4];                         // [word][16 bytes of the row's 64]
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint4 o;
-                        o.x = pack_bf16(__uint_as_float(u[8 * e + 0]) * inv, __uint_as_float(u[8 * e + 1]) * inv);
-                        o.y = pack_bf16(__uint_as_float(u[8 * e + 2]) * inv, __uint_as_float(u[8 * e + 3]) * inv);
-                        o.z = pack_bf16(__uint_as_float(u[8 * e + 4]) * inv, __uint_as_float(u[8 * e + 5]) * inv);
-                        o.w = pack_bf16(__uint_as_float(u[8 * e + 6]) * inv, __uint_as_float(u[8 * e + 7]) * inv);
-                        dst[c * 4 + e] = o;
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    o[e % 4][e / 4] = pack_bf16(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) quad_transpose(o[e], lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (row4 + e < a.S) dst[c * 4 + e * step] = make_uint4(o[0][e], o[1][e], o[2][e], o[3][e]);
             }
             tc_fence_before();
-            if (valid) a.lse[((int64_t)x.b * a.H + x.h) * a.S + row] = (m_run + __log2f(l)) * kLn2;
+            if (valid) a.lse[((int64_t)x.b * (int)a.H.d + x.h) * a.S + row] = (m_run + __log2f(l)) * kLn2;
         }
     }
     tc_fence_before();
@@ -505,16 +599,17 @@ template <int D>
 dfa_status launch(const SinkProblem& p, const void* q, const void* k, const void* v, void* O, float* lse,
                   cudaStream_t s) {
     CUtensorMap mq, mk, mv;
+    const int64_t kv_sb = (int64_t)p.S * p.Hkv * D, kv_ss = (int64_t)p.Hkv * D;
     if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, (int64_t)p.S * p.H * D, (int64_t)p.H * D, D) ||
-        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, (int64_t)p.S * p.Hkv * D, (int64_t)p.Hkv * D, D) ||
-        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, (int64_t)p.S * p.Hkv * D, (int64_t)p.Hkv * D, D))
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, kv_sb, kv_ss, D) ||
+        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, kv_sb, kv_ss, D))
         return fail(DFA_ERR_CUDA, "tensor map encoding failed");
     Args a{};
-    a.rows = p.B * p.H;
-    a.H = p.H; a.G = p.H / p.Hkv; a.S = p.S;
+    a.rows = Divider(p.B * p.H);
+    a.H = Divider(p.H); a.G = Divider(p.H / p.Hkv); a.S = p.S;
     a.window = p.window; a.n_sink = p.n_sink;
     a.n_units = (p.S + kBlockRows - 1) / kBlockRows;
-    a.n_items = a.rows * a.n_units;
+    a.n_items = p.B * p.H * a.n_units;
     a.scale_log2 = p.scale * kLog2e;
     a.O = static_cast<__nv_bfloat16*>(O); a.lse = lse;
     a.err = device_error_flag();
