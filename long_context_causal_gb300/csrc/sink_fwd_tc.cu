@@ -33,7 +33,13 @@
 // its head, so the blocks in the order last to first of all heads are sorted
 // by cost, and dealing them to the persistent CTAs in a snake (0..n-1, then
 // n-1..0, ...) balances them to within one block.  Nothing is uploaded and
-// there is no workspace, so a call is one launch and can be captured.
+// there is no workspace, so a call is one launch and can be captured.  With few
+// blocks a block would leave most SMs without work: then the blocks, or those
+// behind the last full round, are shared by clusters of two or four CTAs, each
+// with a piece of the key list, and joined through distributed shared memory
+// (make_plan weighs the shorter lists against the join: 1500 tokens of 8 heads,
+// D = 128, causal: 21.5 us, whole blocks 24.2; 4000 tokens 44 and 55; 16000 tokens
+// of one head 71 and 193; 700 tokens of 4 heads stay whole, 14.9 and 16.9).
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer of K and V, warp 1 MMA
 // issuer (one lane issues), warp 2 TMEM owner, warp 3 TMA producer of Q, warps 4-11
@@ -92,6 +98,7 @@ struct Args {
     int S;
     int window, n_sink;    // window <= S; n_sink <= 128, 0 when the window covers every key
     int n_units, n_items;  // 256-row blocks per head; rows * n_units
+    int n_whole, log_p;    // SPLIT: the first n_whole blocks are whole CTAs', the others of clusters of 2^log_p
     float scale_log2;      // scale * log2(e)
     __nv_bfloat16* O;      // [B, S, H, D]
     float* lse;            // [B, H, S]
@@ -104,8 +111,10 @@ struct Block {
     int j0;                // first key tile of the band
     int n;                 // key tiles in the list
     int lead;              // 1: the list starts with tile 0 as a sink tile
+    int from;              // n tiles from here on are this CTA's piece of a split block's list
+    bool split;
     // k-th key tile of the list
-    __device__ __forceinline__ int tile(int k) const { return lead && k == 0 ? 0 : j0 + k - lead; }
+    __device__ __forceinline__ int tile(int k) const { return lead && k + from == 0 ? 0 : j0 + k + from - lead; }
 };
 
 __device__ __forceinline__ Block decode(const Args& a, int it) {
@@ -119,23 +128,61 @@ __device__ __forceinline__ Block decode(const Args& a, int it) {
     const bool two = x.q0 + BM < a.S;                     // the second query tile has rows
     x.lead = a.n_sink > 0 && x.j0 > 0;
     x.n = x.lead + (x.q0 / BN + two - x.j0 + 1);
+    x.from = 0;
+    x.split = false;
     return x;
 }
 
+// A CTA's blocks in order: first whole ones, then (SPLIT) its pieces of the
+// blocks that its cluster shares, which may be empty.
+template <bool SPLIT>
+struct Deal {
+    const Args& a;
+    int n_whole, rank, cluster, n_clusters, rounds;
+    __device__ __forceinline__ explicit Deal(const Args& args) : a(args), rank(0), cluster(0), n_clusters(0) {
+        rounds = n_whole = snake_count(SPLIT ? a.n_whole : a.n_items, blockIdx.x, gridDim.x);
+        if (SPLIT) {
+            rank = blockIdx.x & ((1 << a.log_p) - 1);
+            cluster = blockIdx.x >> a.log_p;
+            n_clusters = gridDim.x >> a.log_p;
+            rounds += snake_count(a.n_items - a.n_whole, cluster, n_clusters);
+        }
+    }
+    __device__ __forceinline__ Block operator()(int i) const {
+        if (!SPLIT || i < n_whole) return decode(a, snake_item(i, blockIdx.x, gridDim.x));
+        Block x = decode(a, a.n_whole + snake_item(i - n_whole, cluster, n_clusters));
+        x.from = x.n * rank >> a.log_p;
+        x.n = (x.n * (rank + 1) >> a.log_p) - x.from;
+        x.split = true;
+        return x;
+    }
+};
+
 // How a block's query tile takes part in its list: in the band's positions
-// [b0, b1], none if b1 < 0, and in the first one's sink columns if its own band
+// [b0, b1], none if b1 < b0, and in the first one's sink columns if its own band
 // starts behind that tile.
 struct Run {
     int b0, b1;
     int sink;              // 0, or -1: no sink tile
+    int piece_last;        // split blocks: the last position that it takes part in, -1: none
+    template <bool SPLIT>
+    __device__ __forceinline__ int last() const { return SPLIT ? piece_last : b1; }
     // 0 not at all, 1 the sink columns only, 2 the whole tile.
     __device__ __forceinline__ int part(int k) const { return k == sink ? 1 : (k >= b0 && k <= b1) ? 2 : 0; }
 };
+template <bool SPLIT>
 __device__ __forceinline__ Run run(const Args& a, const Block& x, int w) {
     const int f = x.q0 + w * BM;
-    if (f >= a.S) return Run{0, -1, -1};                  // no rows
+    if (f >= a.S) return Run{0, -1, -1, -1};              // no rows
     const int lo = max(f - a.window + 1, 0) / BN, at = x.lead - x.j0;
-    return Run{lo + at, f / BN + at, a.n_sink > 0 && lo > 0 ? 0 : -1};
+    Run u{lo + at, f / BN + at, a.n_sink > 0 && lo > 0 ? 0 : -1, f / BN + at};
+    if (SPLIT && x.split) {
+        u.b0 = max(u.b0 - x.from, 0);
+        u.b1 = min(u.b1 - x.from, x.n - 1);
+        if (x.from > 0 || x.n == 0) u.sink = -1;
+        u.piece_last = u.b1 >= u.b0 ? u.b1 : u.sink;
+    }
+    return u;
 }
 
 // Column c of a tile is visible iff (c >= lo or c < ns) and c < lim.
@@ -219,7 +266,104 @@ __device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float 
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
+// A softmax thread's part in joining a split block: row `row` of 256, whose
+// unnormalised output over this CTA's piece is in TMEM at tO (if `some`), with
+// reference maximum m and sum l.  o: the row's output, null if it is past the
+// end.  Out of line, so that its registers are not the softmax loop's.
 template <int D>
+__device__ __noinline__ bool join(int log_p, int rank, uint32_t phase, int row, int lane, bool some, float m, float l,
+                                  uint32_t tO, uint8_t* buf, uint64_t* ready, uint64_t* landed,
+                                  volatile int* abort_flag, int* err, __nv_bfloat16* o, float* lse) {
+    const int P = 1 << log_p, per_log = (D == 128 ? 5 : 4) - log_p, per = 1 << per_log;   // 16-byte groups per CTA
+    const uint32_t ring = smem_u32(buf), slot = per * 4096;
+    if (lane == 0)
+        for (int d = 0; d < P; ++d)
+            if (d != rank) cluster_arrive(smem_u32(ready), d);
+    if (!__all_sync(0xffffffffu, mbar_wait_acc(ready, phase, abort_flag, err, nullptr))) return false;
+    fence_cluster();
+    // [sender][group][row] in the ring of the CTA that finishes the group
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        const int at = c * 4, d = at >> per_log;
+        if (d == rank) continue;
+        uint32_t u[16];
+        if (some) {
+            tmem_ld16_async(tO + c * 16, u);
+            tmem_wait_ld16(u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = 0;
+        }
+        const uint32_t dst = map_to_rank(ring + rank * slot + ((at & (per - 1)) * 256 + row) * 16, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            st_cluster_v4(dst + e * 4096, make_float4(__uint_as_float(u[4 * e]), __uint_as_float(u[4 * e + 1]),
+                                                      __uint_as_float(u[4 * e + 2]), __uint_as_float(u[4 * e + 3])));
+    }
+    // maxima and sums: in the slot that the receiver's own output does not need
+    for (int d = 0; d < P; ++d)
+        if (d != rank) st_cluster_v2(map_to_rank(ring + d * slot + (rank * 256 + row) * 8, d), make_float2(m, l));
+    __syncwarp();
+    if (lane == 0)
+        for (int d = 0; d < P; ++d)
+            if (d != rank) cluster_arrive(smem_u32(landed), d);
+    if (!__all_sync(0xffffffffu, mbar_wait_acc(landed, phase, abort_flag, err, nullptr))) return false;
+    fence_cluster();
+    const float2* stat = reinterpret_cast<const float2*>(buf + rank * slot) + row;
+    float top = m, sum = 0.f;
+    for (int d = 0; d < P; ++d)
+        if (d != rank) top = fmaxf(top, stat[d * 256].x);
+    for (int d = 0; d < P; ++d) {
+        const float2 z = d == rank ? make_float2(m, l) : stat[d * 256];
+        sum += ex2(z.x - top) * z.y;                  // no visible key in the piece: 0 * 0
+    }
+    const float inv = 1.f / sum;
+#pragma unroll 1
+    for (int g = 0; g < per; g += 4) {
+        float acc[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+        for (int d = 0; d < P; ++d) {
+            if (d == rank) {
+                if (!some) continue;
+                const float f = ex2(m - top) * inv;
+                uint32_t u[16];
+                tmem_ld16_async(tO + (rank * per + g) * 4, u);
+                tmem_wait_ld16(u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[e] = fmaf(f, __uint_as_float(u[e]), acc[e]);
+            } else {
+                const float f = ex2(stat[d * 256].x - top) * inv;
+                const float4* src = reinterpret_cast<const float4*>(buf + d * slot) + g * 256 + row;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 v = src[e * 256];
+                    acc[4 * e + 0] = fmaf(f, v.x, acc[4 * e + 0]);
+                    acc[4 * e + 1] = fmaf(f, v.y, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(f, v.z, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(f, v.w, acc[4 * e + 3]);
+                }
+            }
+        }
+        if (o) {
+            uint4* dst = reinterpret_cast<uint4*>(o + (rank * per + g) * 4);
+            dst[0] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
+                                pack_bf16(acc[6], acc[7]));
+            dst[1] = make_uint4(pack_bf16(acc[8], acc[9]), pack_bf16(acc[10], acc[11]), pack_bf16(acc[12], acc[13]),
+                                pack_bf16(acc[14], acc[15]));
+        }
+    }
+    tc_fence_before();
+    if (o && rank == 0) *lse = (top + __log2f(sum)) * kLn2;
+    return true;
+}
+
+// SPLIT: launched in clusters of 2^log_p CTAs.  For the last blocks each CTA of a
+// cluster takes a piece of the block's key list; then every CTA sends the others
+// its unnormalised output (the columns that they finish), maxima and sums through
+// distributed shared memory, into the ring that the pieces' tiles have left, and
+// finishes D / 2^log_p columns of the 256 rows, pieces in the order of the keys.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const Args a) {
@@ -239,13 +383,18 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* p_full = bars + 10;
     uint64_t* o_full = bars + 12;
     uint64_t* done = bars + 14;
+    // SPLIT: the other CTAs' rings may be written; what they sent is here; it has been used
+    uint64_t* ready = bars + 34;
+    uint64_t* landed = bars + 35;
+    uint64_t* merged = bars + 36;
     uint64_t* kv_full = bars + 16;        // [kSlots]
     uint64_t* kv_empty = bars + 16 + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 33);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rounds = snake_count(a.n_items, blockIdx.x, gridDim.x);
+    const Deal<SPLIT> deal(a);
+    const int rounds = deal.rounds, P = SPLIT ? 1 << a.log_p : 1;
 
     if (threadIdx.x == 0) {
         for (int w = 0; w < 2; ++w) {
@@ -257,6 +406,11 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&o_full[w], 1);
         }
         mbar_init(done, 1);
+        if (SPLIT) {
+            mbar_init(ready, (P - 1) * 8);
+            mbar_init(landed, (P - 1) * 8);
+            mbar_init(merged, 8);
+        }
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -273,6 +427,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
+    if (SPLIT) cluster_sync();      // every CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -281,7 +436,12 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         uint32_t ld = 0;
         bool ok = true;
         for (int r = 0; r < rounds && ok; ++r) {
-            const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
+            const Block x = deal(r);
+            // the ring carries the outputs of a split block until they are joined
+            if (SPLIT && r > deal.n_whole) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(merged, (r - deal.n_whole - 1) & 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+            }
             for (int k = 0; k < x.n && ok; ++k) {
                 const int j = x.tile(k);
                 for (int which = 0; which < 2; ++which, ++ld) {
@@ -313,9 +473,10 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         uint32_t qi = 0;
         bool ok = true;
         for (int r = 0; r < rounds && ok; ++r) {
-            const Block x = decode(a, snake_item(r, blockIdx.x, gridDim.x));
+            const Block x = deal(r);
+            if (SPLIT && x.n == 0) continue;
             for (int w = 0; w < 2 && ok; ++w) {
-                ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[w], (r & 1) ^ 1, abort_flag, a.err, nullptr));
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[w], ((qi >> 1) & 1) ^ 1, abort_flag, a.err, nullptr));
                 if (!ok) break;
                 ++qi;
                 if (lane == 0) {
@@ -385,13 +546,20 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // other one's end or for its own epilogue.  Block -1 is empty.
         uint32_t now[2] = {0, 0}, first[2] = {1, 1};
         Block x{}, y{};
-        Run u0{0, -1, -1}, u1 = u0, v0 = u0, v1 = u0;
-        if (rounds > 0) {
-            y = decode(a, snake_item(0, blockIdx.x, gridDim.x));
-            v0 = run(a, y, 0);
-            v1 = run(a, y, 1);
-        }
-        int k = -1, r = -1;
+        Run u0{0, -1, -1, -1}, u1 = u0, v0 = u0, v1 = u0;
+        int k = -1, r = -1, dealt = 0;
+        // y: the next block that has key tiles
+        auto fetch = [&]() {
+            while (dealt < rounds) {
+                y = deal(dealt++);
+                if (SPLIT && y.n == 0) continue;
+                v0 = run<SPLIT>(a, y, 0);
+                v1 = run<SPLIT>(a, y, 1);
+                return true;
+            }
+            return false;
+        };
+        bool have_y = fetch();
         for (;;) {
             // Steps in which both query tiles take both key tiles whole run without looking at the bands.
             const int hot = u0.b1;
@@ -415,9 +583,12 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     a0 = a1 = 1u;
                 }
                 if (!ok) break;
-                mma_commit_lead(lead, &q_empty[0]);   // its last product is issued; the second query tile has one more
+                // The first query tile's last product is issued; the second one's band goes one tile
+                // further, unless a piece ends here.
+                mma_commit_lead(lead, &q_empty[0]);
+                if (SPLIT && u1.piece_last == hot) mma_commit_lead(lead, &q_empty[1]);
             }
-            const bool end = k + 1 == x.n, more = !end || r + 1 < rounds;
+            const bool end = k + 1 == x.n, more = !end || (SPLIT ? have_y : r + 1 < rounds);
             const int kn = end ? 0 : k + 1, rn = end ? r + 1 : r;
             const uint32_t slotV = cons % C::kSlots;
             if (k >= 0) {
@@ -428,10 +599,13 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             bool have_k = false;
             // a query tile that skips this key tile goes first: it does not wait for the other one
             const int swap = now[1] == 0 && now[0] != 0;
+            // The ring takes the next piece's keys only behind the join of the split block before it,
+            // which waits for this block's products: those first.
+            const bool apart = SPLIT && end && have_y && dealt - 1 > deal.n_whole;
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                const int w = i ^ swap;
-                if (w ? now[1] : now[0]) {
+            for (int i = 0; i < (apart ? 4 : 2); ++i) {
+                const int w = (i & 1) ^ swap;
+                if (i < 2 && (w ? now[1] : now[0])) {
                     const uint32_t acc = 1u - (w ? first[1] : first[0]), par = (w ? t[1] : t[0]) & 1;
                     if ((w ? now[1] : now[0]) == 2) issue_PV(w, slotV, par, acc);
                     else issue_PV_sink(w, slotV, par, acc);
@@ -440,10 +614,10 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     else ++t[0];
                     if (w) first[1] = 0;
                     else first[0] = 0;
-                    if (k == (w ? u1.b1 : u0.b1)) mma_commit_lead(lead, &o_full[w]);
+                    if (k == (w ? u1 : u0).template last<SPLIT>()) mma_commit_lead(lead, &o_full[w]);
                 }
                 if (i == 1 && k >= 0) mma_commit_lead(lead, &kv_empty[slotV]);
-                if (!more) continue;
+                if (!more || (apart && i < 2)) continue;
                 // S of the next key tile
                 const Run u = end ? (w ? v1 : v0) : (w ? u1 : u0);
                 if (kn == 0 && !wait(&q_full[w], rn & 1)) break;
@@ -456,7 +630,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (w) now[1] = part;
                 else now[0] = part;
                 // behind the query tile's last product its buffer is free for the next block's
-                if (kn == max(u.b1, 0)) mma_commit_lead(lead, &q_empty[w]);
+                if (kn == max(u.template last<SPLIT>(), 0)) mma_commit_lead(lead, &q_empty[w]);
             }
             if (!ok || !more) break;
             mma_commit_lead(lead, &kv_empty[slotK]);
@@ -468,11 +642,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 u0 = v0;
                 u1 = v1;
                 first[0] = first[1] = 1;
-                if (r + 1 < rounds) {
-                    y = decode(a, snake_item(r + 1, blockIdx.x, gridDim.x));
-                    v0 = run(a, y, 0);
-                    v1 = run(a, y, 1);
-                }
+                have_y = fetch();
             }
         }
         // Drain: every MMA issued here has finished before TMEM is freed.
@@ -489,14 +659,14 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float c2 = a.scale_log2;
         uint32_t t = 0, qi = 0;
         bool ok = true;
-        Block x = decode(a, snake_item(0, blockIdx.x, gridDim.x)), y = x;
+        Block x = deal(0), y = x;
         for (int rd = 0; rd < rounds && ok; ++rd, x = y) {
             const int f = x.q0 + w * BM, row = f + r;
-            if (f >= a.S) {                           // no row of the sequence in this tile
-                if (rd + 1 < rounds) y = decode(a, snake_item(rd + 1, blockIdx.x, gridDim.x));
+            const Run u = run<SPLIT>(a, x, w);
+            if (u.template last<SPLIT>() < 0 && !(SPLIT && x.split)) {             // no row of the sequence in this tile
+                if (rd + 1 < rounds) y = deal(rd + 1);
                 continue;
             }
-            const Run u = run(a, x, w);
             const int row0 = __shfl_sync(0xffffffffu, row, 0);
             const int lo_row = row - a.window + 1, lo_last = f + BM - a.window;   // lowest visible keys
             float m_run = -INFINITY, l = 0.f;
@@ -559,12 +729,25 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             if (!ok) break;
             // ---- epilogue: O = O_acc / l, lse = ln(sum exp(s)); every row sees itself, so l > 0
-            if (rd + 1 < rounds) y = decode(a, snake_item(rd + 1, blockIdx.x, gridDim.x));
-            ok = __all_sync(0xffffffffu, mbar_wait_acc(&o_full[w], qi & 1, abort_flag, a.err, nullptr));
-            if (!ok) break;
-            tc_fence_after();
-            ++qi;
+            if (rd + 1 < rounds) y = deal(rd + 1);
+            if (!SPLIT || started) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(&o_full[w], qi & 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                tc_fence_after();
+                ++qi;
+            }
             const bool valid = row < a.S;
+            if (SPLIT && x.split) {
+                ok = join<D>(a.log_p, deal.rank, (rd - deal.n_whole) & 1, w * BM + r, lane, started, m_run, l, tO, sKV, ready,
+                             landed, abort_flag, a.err,
+                             valid ? a.O + (((int64_t)x.b * a.S + row) * a.H.d + x.h) * D : nullptr,
+                             a.lse + ((int64_t)x.b * (int)a.H.d + x.h) * a.S + row);
+                if (!ok) break;
+                fence_proxy_async_smem();             // the next loads into the ring come behind its reads
+                __syncwarp();
+                if (lane == 0) mbar_arrive(merged);
+                continue;
+            }
             const float inv = 1.f / l;
             // A lane holds a row: stored as it stands, every 16 bytes would go to a line of their own.
             // Four lanes exchange theirs and each store writes 64 contiguous bytes of eight rows.
@@ -591,8 +774,70 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
+    if (SPLIT) cluster_sync();      // no CTA leaves while another one may still write to it
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// How a problem's blocks are dealt: whole ones first, the others split over
+// clusters of 2^log_p CTAs.
+struct Plan {
+    int log_p, n_whole, grid;
+};
+
+// Costs in steps of a key tile (1.4 us at D = 128): kBlockSteps for a block's
+// ends, kJoinSteps for joining the pieces of one (5 us).
+constexpr int kBlockSteps = 3, kJoinSteps = 4;
+
+cudaLaunchConfig_t cluster_config(int grid, int cluster, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+Plan make_plan(const Args& a, int sms, int clusters4) {
+    Plan best{0, a.n_items, std::min(sms, a.n_items)};
+    const int rows = (int)a.rows.d;
+    auto tiles = [&](int it) {
+        const int q0 = (a.n_units - 1 - it / rows) * kBlockRows, j0 = std::max(q0 - a.window + 1, 0) / BN;
+        return (a.n_sink > 0 && j0 > 0) + q0 / BN + (q0 + BM < a.S) - j0 + 1;
+    };
+    // With many blocks per CTA the deal is even enough; short lists are not worth a join.
+    const int longest = tiles(0);
+    if (a.n_items > 2 * sms || longest - (longest + 3) / 4 <= kJoinSteps) return best;
+    int load[1024], least = 1 << 30;
+    for (int log_p = 0; log_p < 3; ++log_p) {
+        const int n = log_p == 0 ? sms : log_p == 1 ? sms / 2 : clusters4, grid = n << log_p;
+        if (grid < 1 || grid > 1024) continue;
+        for (int whole = log_p == 0 ? a.n_items : 0; whole <= a.n_items; whole += grid) {
+            std::fill(load, load + grid, 0);
+            for (int i = 0, c = 0, step = 1; i < whole; ++i) {
+                load[c] += tiles(i) + kBlockSteps;
+                if ((step > 0 ? c == grid - 1 : c == 0)) step = -step;
+                else c += step;
+            }
+            for (int i = whole, c = 0, step = 1; i < a.n_items; ++i) {
+                const int cost = ((tiles(i) + (1 << log_p) - 1) >> log_p) + kBlockSteps + kJoinSteps;
+                for (int e = 0; e < 1 << log_p; ++e) load[(c << log_p) + e] += cost;
+                if ((step > 0 ? c == n - 1 : c == 0)) step = -step;
+                else c += step;
+            }
+            const int most = *std::max_element(load, load + grid);
+            if (most < least) {
+                least = most;
+                if (log_p > 0) best = Plan{log_p, whole, whole > 0 ? grid : std::min(n, a.n_items) << log_p};
+            }
+        }
+    }
+    return best;
 }
 
 template <int D>
@@ -614,15 +859,33 @@ dfa_status launch(const SinkProblem& p, const void* q, const void* k, const void
     a.O = static_cast<__nv_bfloat16*>(O); a.lse = lse;
     a.err = device_error_flag();
     const int smem = Cfg<D>::kSmem;
-    auto kern = sink_fwd_kernel<D>;
     static std::atomic<uint64_t> seen{0};
+    static std::atomic<int> clusters4{0};            // clusters of four that run at a time
+    auto whole = sink_fwd_kernel<D, false>;
+    auto split = sink_fwd_kernel<D, true>;
     if (first_on_device(seen)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return fail(DFA_ERR_CUDA, "sink_fwd: shared memory attribute");
+        int n = 0;
+        cudaLaunchAttribute at[1];
+        const cudaLaunchConfig_t cfg = cluster_config(4, 4, smem, s, at);
+        if (cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, split, &cfg) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "sink_fwd: kernel attributes");
+        clusters4.store(n);
         mark_on_device(seen);
     }
-    kern<<<std::min(num_sms(), a.n_items), kThreads, smem, s>>>(mq, mk, mv, a);
-    cudaError_t e = cudaGetLastError();
+    const Plan plan = make_plan(a, num_sms(), clusters4.load());
+    a.log_p = plan.log_p;
+    a.n_whole = plan.n_whole;
+    cudaError_t e;
+    if (plan.log_p == 0) {
+        whole<<<plan.grid, kThreads, smem, s>>>(mq, mk, mv, a);
+        e = cudaGetLastError();
+    } else {
+        cudaLaunchAttribute at[1];
+        const cudaLaunchConfig_t cfg = cluster_config(plan.grid, 1 << plan.log_p, smem, s, at);
+        e = cudaLaunchKernelEx(&cfg, split, mq, mk, mv, a);
+    }
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "sink_fwd launch: %s", cudaGetErrorString(e));
 }
 

@@ -81,6 +81,46 @@ def test_backward(case):
     check_bwd(grads, q, k, v, O, lse, do, window, n_sink)
 
 
+def rows_fwd(q, k, v, window, n_sink):
+    """O, lse and sum_j p_j |v_j| in 64 bits, rows in blocks that read only the keys they can see."""
+    B, S, H, D = q.shape
+    out = [torch.empty(B, S, H, D, dtype=torch.float64, device=q.device) for _ in range(2)]
+    lse = torch.empty(B, H, S, dtype=torch.float64, device=q.device)
+    for a in range(0, S, 1024):
+        b = min(a + 1024, S)
+        lo = max(a - window + 1, 0)
+        cols = torch.cat([torch.arange(0, min(n_sink, lo), device=q.device), torch.arange(lo, b, device=q.device)])
+        rows = torch.arange(a, b, device=q.device)[:, None]
+        see = (cols <= rows) & ((cols > rows - window) | (cols < n_sink))
+        for h in range(H):
+            kh, vh = (t[:, cols, h * k.shape[2] // H].double() for t in (k, v))
+            s = (q[:, a:b, h].double() @ kh.transpose(1, 2) * D ** -0.5).masked_fill(~see, float("-inf"))
+            lse[:, h, a:b] = torch.logsumexp(s, -1)
+            p = torch.exp(s - lse[:, h, a:b, None])
+            out[0][:, a:b, h], out[1][:, a:b, h] = p @ vh, p @ vh.abs()
+    return out[0], lse, out[1]
+
+
+# Few blocks, or a last round that is not full: blocks whose key lists several CTAs share, in pieces that hold no key
+# of a query tile, the sinks alone, or nothing; query tiles past the end; whole blocks before shared ones.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,S,window,n_sink", [
+    (1, 1, 1, 1100, 2000, 0), (1, 1, 1, 2000, 2000, 0), (1, 1, 1, 3001, 2500, 128), (2, 3, 3, 1111, 900, 17),
+    (1, 8, 2, 1500, 1500, 0), (1, 2, 1, 2200, 1400, 5), (1, 8, 4, 2300, 1500, 33), (1, 2, 2, 2817, 2817, 0),
+    (1, 8, 2, 4000, 4000, 0), (1, 4, 2, 12000, 2000, 1), (1, 1, 1, 20000, 700, 128),
+])
+def test_blocks_shared_by_several_ctas(B, H, Hkv, S, window, n_sink, D):
+    q, k, v, _ = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=71)
+    k[:, :200] *= 3                       # the pieces' maxima differ
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    again = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dfa.dfa_check_errors()
+    Or, lr, size = rows_fwd(q, k, v, window, n_sink)
+    close(O, np64(Or), (U + F) * np64(size) + U * np.abs(np64(Or)), "O")
+    close(lse, np64(lr), 2 * F, "lse")
+    assert torch.equal(O, again[0]) and torch.equal(lse, again[1])
+
+
 def test_sharp_scores_rescale():
     """Maxima that rise by more than 2^8 along the keys, and sinks above all of them."""
     q, k, v, do = make(1, 2, 1, 900, 128, torch.bfloat16, device=DEV, seed=33, k_scale=4.0)
