@@ -199,9 +199,9 @@ __host__ __device__ inline int snake_count(int n_items, int cta, int n) {
 // (1-2 us of a short call); the kernel calls wait_for_previous_kernel() before
 // it touches what that one writes.
 template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
