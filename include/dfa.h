@@ -299,7 +299,8 @@ dfa_status dfa_ckpt8_restore(const void* ckpt, size_t ckpt_bytes, dfa_dtype dt, 
  * the values the checkpoint stands for, with the same window and n_sink as
  * the forward (window >= S, n_sink = 0: plain causal attention, the backward
  * of dfa_attn_fwd).  lse is the forward's, of the tensors before they were
- * rounded, so P_ij = exp(s_ij - lse_i) carries the rounding of q and k.
+ * rounded, so P_ij = exp(s_ij - lse_i) carries the rounding of q and k and can
+ * exceed 1; above 255 (a score that the rounding moved by 5.5) it counts as 255.
  * Arguments, errors and reproducibility as dfa_attn_bwd_sink; the workspace
  * also holds the restored q, k and v for the length of the call. */
 size_t dfa_attn_bwd_ckpt8_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);

@@ -51,6 +51,18 @@ struct TypeErr {
 };
 struct Raised {};   // a Python error is set
 
+// The library call and the allocations may block (a full launch queue, a
+// cudaMalloc): other Python threads run meanwhile, as with ctypes.
+struct NoGil {
+    PyThreadState* save = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(save); }
+};
+template <typename F, typename... A>
+dfa_status without_gil(F entry, A... args) {
+    const NoGil released;
+    return entry(args...);
+}
+
 std::string shape_of(const at::Tensor& t) {
     std::string s = "(";
     for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
@@ -111,6 +123,7 @@ at::Tensor given(PyObject* o, const char* name, at::IntArrayRef shape, at::Scala
 
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
     if (o != Py_None) return given(o, name, shape, type, dev);
+    const NoGil released;
     return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 
@@ -145,6 +158,7 @@ at::Tensor bytes(PyObject* o, const char* name, size_t n, const at::Device& dev,
     }
     const auto opt = at::TensorOptions().dtype(at::kByte).device(dev);
     const int64_t size = n ? (int64_t)n : 16;
+    const NoGil released;
     if (!s.other) return at::empty({size}, opt);
     c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s.handle), dev.index()));
     return at::empty({size}, opt);
@@ -186,9 +200,10 @@ PyObject* fwd(PyObject* const* a) {
     at::Tensor O = output(a[6], "O", q.sizes(), q.scalar_type(), dev);
     at::Tensor lse = output(a[7], "lse", {z.B, z.H, z.S}, at::kFloat, dev);
     const Stream s = stream_of(a[8], d);
-    const dfa_status st = g.fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), z.B, z.H, z.Hkv, z.S, z.D,
-                                number(a[3], "window"), number(a[4], "n_sink"), scale_of(a[5], z.D), O.data_ptr(),
-                                static_cast<float*>(lse.data_ptr()), s.handle);
+    const int window = number(a[3], "window"), n_sink = number(a[4], "n_sink");
+    const dfa_status st = without_gil(g.fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), z.B, z.H, z.Hkv, z.S,
+                                      z.D, window, n_sink, scale_of(a[5], z.D), O.data_ptr(),
+                                      static_cast<float*>(lse.data_ptr()), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
 }
 
@@ -208,10 +223,10 @@ PyObject* bwd(PyObject* const* a) {
     const Stream s = stream_of(a[13], d);
     const at::Tensor ws = bytes(a[12], "workspace_buf",
                                 a[12] == Py_None ? g.bwd_bytes(z.B, z.H, z.Hkv, z.S, z.D, window, n_sink) : 0, dev, s);
-    const dfa_status st = g.bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(),
-                                static_cast<const float*>(lse.data_ptr()), dO.data_ptr(), dtype_of(q), z.B, z.H, z.Hkv, z.S,
-                                z.D, window, n_sink, scale_of(a[8], z.D), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-                                ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    const dfa_status st = without_gil(g.bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(),
+                                      static_cast<const float*>(lse.data_ptr()), dO.data_ptr(), dtype_of(q), z.B, z.H,
+                                      z.Hkv, z.S, z.D, window, n_sink, scale_of(a[8], z.D), dQ.data_ptr(), dK.data_ptr(),
+                                      dV.data_ptr(), ws.data_ptr(), (size_t)ws.numel(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(dQ), std::move(dK), std::move(dV)});
 }
 
@@ -234,10 +249,10 @@ PyObject* decode(PyObject* const* a) {
     const Stream s = stream_of(a[10], d);
     const at::Tensor ws = bytes(a[9], "workspace_buf", a[9] == Py_None ? g.decode_bytes(B, H, Hkv, D) : 0, dev, s);
     const int64_t strides[3] = {k.stride(0), k.stride(1), k.stride(2)};
-    const dfa_status st = g.decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), B, H, Hkv, S, D, strides,
-                                   static_cast<const int32_t*>(len.data_ptr()), number(a[4], "window"),
-                                   number(a[5], "n_sink"), scale_of(a[6], D), O.data_ptr(),
-                                   static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    const dfa_status st = without_gil(g.decode, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), B, H, Hkv, S, D,
+                                      static_cast<const int64_t*>(strides), static_cast<const int32_t*>(len.data_ptr()),
+                                      number(a[4], "window"), number(a[5], "n_sink"), scale_of(a[6], D), O.data_ptr(),
+                                      static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
 }
 
@@ -248,12 +263,11 @@ PyObject* save(PyObject* const* a) {
     const at::Device dev = q.device();
     const at::Tensor O = given(a[3], "O", q.sizes(), q.scalar_type(), dev);
     // An output: the caller's stream or the current one, as the other outputs.
-    at::Tensor ckpt = a[4] == Py_None
-                          ? at::empty({(int64_t)g.ckpt_bytes(z.B, z.H, z.Hkv, z.S, z.D)}, at::TensorOptions().dtype(at::kByte).device(dev))
-                          : bytes(a[4], "ckpt", 0, dev, Stream{});
+    at::Tensor ckpt = a[4] == Py_None ? output(Py_None, "ckpt", {(int64_t)g.ckpt_bytes(z.B, z.H, z.Hkv, z.S, z.D)}, at::kByte, dev)
+                                      : bytes(a[4], "ckpt", 0, dev, Stream{});
     const Stream s = stream_of(a[5], d);
-    const dfa_status st = g.save(q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), dtype_of(q), z.B, z.H, z.Hkv, z.S,
-                                 z.D, ckpt.data_ptr(), (size_t)ckpt.numel(), s.handle);
+    const dfa_status st = without_gil(g.save, q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), dtype_of(q), z.B, z.H,
+                                      z.Hkv, z.S, z.D, ckpt.data_ptr(), (size_t)ckpt.numel(), s.handle);
     return st ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(ckpt));
 }
 
@@ -270,8 +284,8 @@ PyObject* restore(PyObject* const* a) {
     at::Tensor v = output(a[8], "v", {B, S, Hkv, D}, at::kBFloat16, dev);
     at::Tensor O = output(a[9], "O", {B, S, H, D}, at::kBFloat16, dev);
     const Stream s = stream_of(a[10], d);
-    const dfa_status st = g.restore(ckpt.data_ptr(), (size_t)ckpt.numel(), DFA_BF16, B, H, Hkv, S, D, q.data_ptr(),
-                                    k.data_ptr(), v.data_ptr(), O.data_ptr(), s.handle);
+    const dfa_status st = without_gil(g.restore, ckpt.data_ptr(), (size_t)ckpt.numel(), DFA_BF16, B, H, Hkv, S, D,
+                                      q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(q), std::move(k), std::move(v), std::move(O)});
 }
 
@@ -293,9 +307,10 @@ PyObject* bwd_ckpt(PyObject* const* a) {
     const Stream s = stream_of(a[11], d);
     const at::Tensor ws = bytes(a[10], "workspace_buf",
                                 a[10] == Py_None ? g.bwd_ckpt_bytes(B, H, Hkv, S, D, window, n_sink) : 0, dev, s);
-    const dfa_status st = g.bwd_ckpt(ckpt.data_ptr(), (size_t)ckpt.numel(), static_cast<const float*>(lse.data_ptr()),
-                                     dO.data_ptr(), dtype_of(dO), B, H, Hkv, S, D, window, n_sink, scale_of(a[6], D),
-                                     dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    const dfa_status st = without_gil(g.bwd_ckpt, ckpt.data_ptr(), (size_t)ckpt.numel(),
+                                      static_cast<const float*>(lse.data_ptr()), dO.data_ptr(), dtype_of(dO), B, H, Hkv, S, D,
+                                      window, n_sink, scale_of(a[6], D), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+                                      ws.data_ptr(), (size_t)ws.numel(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(dQ), std::move(dK), std::move(dV)});
 }
 

@@ -932,9 +932,10 @@ dfa_status check_ws(void* ws, size_t have, size_t need) {
 }
 
 bool sink_sizes_ok(int B, int H, int Hkv, int S, int D, int window, int n_sink) {
-    const std::string keep = g_msg;   // a size query does not change dfa_last_error()
+    char keep[sizeof(g_msg)];         // a size query does not change dfa_last_error()
+    memcpy(keep, g_msg, sizeof(g_msg));
     const bool ok = !check_sink(DFA_BF16, B, H, Hkv, S, D, window, n_sink, 1.f) && !check_sink_rows(B, H, S);
-    snprintf(g_msg, sizeof(g_msg), "%s", keep.c_str());
+    memcpy(g_msg, keep, sizeof(g_msg));
     return ok;
 }
 
@@ -992,9 +993,10 @@ DecodeProblem decode_problem(int B, int H, int Hkv, int S, int D, int window, in
 
 extern "C" size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D) {
     const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
-    const std::string keep = g_msg;
+    char keep[sizeof(g_msg)];
+    memcpy(keep, g_msg, sizeof(g_msg));
     const bool ok = check_decode(DFA_BF16, p) == DFA_OK;
-    snprintf(g_msg, sizeof(g_msg), "%s", keep.c_str());
+    memcpy(g_msg, keep, sizeof(g_msg));
     return ok ? decode_workspace(p) : 0;
 }
 

@@ -456,6 +456,58 @@ def test_tensors_on_the_wrong_place_are_refused():
     assert empty[0].shape == (1, 0, 2, 64) and empty[1].shape == (1, 2, 0)
 
 
+def test_numbers_out_of_range_are_refused():
+    q, k, v, do = make(1, 2, 1, 64, 64, torch.bfloat16, device=DEV, seed=58)
+    lens = torch.full((1,), 64, dtype=torch.int32, device=DEV)
+    for bad in (1 << 31, -(1 << 31) - 1, 1 << 40):
+        with pytest.raises(ValueError, match="32-bit"):
+            dfa.dfa_attn_fwd_sink(q, k, v, bad)
+        with pytest.raises(ValueError, match="32-bit"):
+            dfa.dfa_attn_decode_sink(q[:, 0].contiguous(), k, v, lens, 4, bad)
+    with pytest.raises(OverflowError):
+        dfa.dfa_attn_fwd_sink(q, k, v, 1 << 70)
+    for bad in (1.5, None, "4"):
+        with pytest.raises(TypeError):
+            dfa.dfa_attn_fwd_sink(q, k, v, bad)
+    for window, n_sink in ((0, 0), (-3, 0), (4, -1), (4, 129)):
+        with pytest.raises(dfa.DfaError):
+            dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    for scale in (0.0, -1.0, float("nan"), 1e300):
+        with pytest.raises(dfa.DfaError):
+            dfa.dfa_attn_fwd_sink(q, k, v, 4, scale=scale)
+    with pytest.raises(TypeError):
+        dfa.dfa_attn_fwd_sink(q, k, [1, 2], 4)
+    with pytest.raises(AttributeError):
+        dfa.dfa_attn_fwd_sink(q, k, v, 4, stream="none")
+
+
+def test_calls_from_several_threads():
+    """Each thread on a stream of its own; the calls let other threads run."""
+    import threading
+    cases = [(1, 4, 2, 700, 64, 100, 4), (1, 2, 2, 1500, 128, 1500, 0), (2, 8, 2, 300, 128, 40, 1), (1, 1, 1, 2500, 64, 900, 17)]
+    data = [make(*c[:5], torch.bfloat16, device=DEV, seed=80 + i) for i, c in enumerate(cases)]
+    want = [step(*d, *c[5:]) for d, c in zip(data, cases)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    same_step(step(*data[i], *cases[i][5:]), want[i])
+        except BaseException as e:       # shown by the test, not lost with the thread
+            failed.append((cases[i], e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    dfa.dfa_check_errors()
+    assert not failed, failed
+
+
 def test_offsets_beyond_32_bits():
     """512K tokens of 32 heads: 2^31 elements in q, and dQ's fp32 accumulator.
     Rows of the last head and sequence end against the reference on the slice
