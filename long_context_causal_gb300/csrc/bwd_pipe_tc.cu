@@ -192,9 +192,20 @@ __device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
 //
 // HD = 64 keeps the tiles' places, 128-byte rows of 64 elements with the second
 // half of each 32 KB unused; dQ^T stays a 128-row MMA whose upper 64 rows come
-// from whatever follows K's first half and are never read.  Against the
-// single-phase kernel of bwd_tc.cu with the same items (32K tokens, 32/8 heads):
-// 4.85 ms instead of 8.65 at a window of 4096, 14.9 instead of 34.2 causal.
+// from whatever follows K's first half and are never read.  At 32K tokens, 32
+// heads of 8 kv heads and a window of 4096 the single-phase kernel of bwd_tc.cu
+// took 8.65 ms on the same items, the two phases alone 4.85, with what follows 2.89.
+//
+// What bounds the variant, on the same problem.  The P/dS warps and the drain
+// share the LSU data pipe, which was busy 78% of the time while dQ left as
+// reductions from registers: now the drain writes blocks to shared memory and the
+// copy engine adds them (kBulk; D = 128 5.08 -> 4.21 ms, one dO slot instead of two
+// for the room).  The MMA role runs as a converged warp of which one lane issues,
+// so that descriptors sit in uniform registers (D = 64 3.69 -> 3.36).  D = 128 now
+// takes 4.15 ms (1230 TFLOP/s, 65% of the cuBLAS rate): 0.5 ms are the memory
+// traffic of the preparing and finishing kernels and the ends of the lists, and a
+// step of 128 x 128 takes 2.05 us, 1.45 of them MMAs; the rest is the chain
+// S -> P -> dS -> dQ of one tile, of which TMEM holds one and a half at a time.
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a

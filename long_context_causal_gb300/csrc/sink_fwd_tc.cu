@@ -19,15 +19,16 @@
 // sinks, rounded up to 16 columns: N = 4 costs an eighth of a tile.
 //
 // What bounds it.  A query tile's steps form a chain: S (550 cycles at D = 128),
-// the softmax of its row (1600), two barriers (500), P V (550, of which half
-// runs under the softmax).  The two chains of a CTA overlap, and the tensor
-// cores work for 2200 of a step's 2800 cycles.  A block's ends -- masked tiles,
-// the sink tile's step, the epilogue -- cost another 4 us of chain, so the lists
-// of a CTA's blocks run on into one another (issuer), a 32-column piece of a
-// masked tile pays for its mask only if some of its elements are masked (Mask),
-// and the output leaves in 64-byte pieces.  Measured, 32K tokens, 32 heads of 8 kv
-// heads, 4 sinks: window 4096 1425 us (D = 128; 1460 TFLOP/s, 77% of the cuBLAS
-// rate), window 1024 530; D = 64 1278 and 480.
+// the softmax of its row (1400), barriers (500), P V (550, of which three quarters
+// run under the softmax).  The two chains of a CTA overlap, and the tensor cores
+// work for 2200 of a step's 2600 cycles (moving exponentials to the FMA pipe gained
+// nothing: it is the chain, not MUFU).  A block's ends -- masked tiles, the sink tile's
+// step, the epilogue -- cost another 4 us of chain, so the lists of a CTA's blocks
+// run on into one another (issuer), a 32-column piece of a masked tile pays for its
+// mask only if some of its elements are masked (Mask), and the output leaves in
+// 64-byte pieces.  Measured, 32K tokens, 32 heads of 8 kv heads, 4 sinks: window 4096
+// 1341 us (D = 128; 1540 TFLOP/s, 81% of the cuBLAS rate), window 1024 512; D = 64
+// 1176 and 455; without sinks, window 128 181 and window 1 105 (D = 128).
 //
 // Schedule.  No work list: costs never fall from a block to the next one of
 // its head, so the blocks in the order last to first of all heads are sorted
@@ -68,13 +69,13 @@ constexpr int kBlockRows = 2 * BM;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kMinusInf = 0xff800000u;
+constexpr int kMost = 6;           // steps of 16 keys in the first part of P that is handed over
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O only when the max grows by > 2^8
 
 template <int D>
 struct Cfg {
     static constexpr int kTileBytes = BN * D * 2;
     static constexpr int kSlots = D == 128 ? 4 : 6;            // K/V ring depth
-    static constexpr bool kHalves = D == 128;                  // P is handed over in two halves (rule at p_half)
     static constexpr int kQBytes = 2 * kTileBytes;
     static constexpr int kSmem = kQBytes + kSlots * kTileBytes + 1024 /*barriers*/ + 1024 /*align*/;
 };
@@ -198,71 +199,112 @@ struct Mask {
     }
 };
 
-// Row max of the first 32 * chunks scores of this thread's row in TMEM.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t tS, int chunks, Mask k) {
+// The warp's P so far is in TMEM.
+__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void max32(float (&m)[4], const uint32_t (&u)[32]) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(u[e]));
+}
+// P = exp2(s * c2 - m) of 32 columns as bf16 pairs to tP; acc: sums of the unrounded P.
+__device__ __forceinline__ void exp32(float (&acc)[4], const uint32_t (&u)[32], float c2, float m, uint32_t tP) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
+        const float p1 = ex2(fmaf(__uint_as_float(u[2 * e + 1]), c2, -m));
+        acc[e & 3] += p0 + p1;
+        pk[e] = pack_bf16(p0, p1);
+    }
+    tmem_st16(tP, pk);
+}
+
+// A tile that every row of the block sees whole: row max of this thread's 128
+// scores in TMEM.  Each piece's load runs under the arithmetic of the one before
+// it (here and in row_exp: 32K tokens, window 4096 1433 -> 1343 us).
+__device__ __forceinline__ float row_max(uint32_t tS) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    uint32_t a[32], b[32];
+    tmem_ld32_async(tS, a);
+    tmem_wait_ld32(a);
+    tmem_ld32_async(tS + 32, b);
+    max32(m, a);
+    tmem_wait_ld32(b);
+    tmem_ld32_async(tS + 64, a);
+    max32(m, b);
+    tmem_wait_ld32(a);
+    tmem_ld32_async(tS + 96, b);
+    max32(m, a);
+    tmem_wait_ld32(b);
+    max32(m, b);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Its P, written as bf16 pairs over S (behind the columns still to be read);
+// `most` is told when 96 columns are there.  Returns the row sum of the unrounded P.
+__device__ __forceinline__ float row_exp(uint32_t tS, float c2, float m, uint64_t* most, int lane) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t a[32], b[32];
+    tmem_ld32_async(tS, a);
+    tmem_wait_ld32(a);
+    tmem_ld32_async(tS + 32, b);
+    exp32(acc, a, c2, m, tS);
+    tmem_wait_ld32(b);
+    tmem_ld32_async(tS + 64, a);
+    exp32(acc, b, c2, m, tS + 16);
+    tmem_wait_ld32(a);
+    tmem_ld32_async(tS + 96, b);
+    exp32(acc, a, c2, m, tS + 32);
+    hand_over(most, lane);
+    tmem_wait_ld32(b);
+    exp32(acc, b, c2, m, tS + 48);
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+// The same two for the first 32 * chunks columns under a mask.
+__device__ __forceinline__ float row_max_masked(uint32_t tS, int chunks, const Mask& k) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        if (MASK && k.none(c * 32)) continue;
+        if (k.none(c * 32)) continue;
         uint32_t u[32];
         tmem_ld32(tS + c * 32, u);
-        if (MASK && !k.all(c * 32)) {
+        if (!k.all(c * 32)) {
             const uint32_t see = k.bits(c * 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(u[e]));
+        max32(m, u);
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-
-// The warp's P so far is in TMEM.  Arrivals of whole warps or of their threads
-// (32K tokens, window 4096: D = 128 1425 us with warps' and 1454 with threads', D = 64 1297
-// and 1278).
-template <bool WARP>
-__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
-    tmem_st_wait();
-    tc_fence_before();
-    if (WARP) __syncwarp();
-    if (!WARP || lane == 0) mbar_arrive(bar);
-}
-
-// P = exp2(s * c2 - m) of the same columns, written as bf16 pairs over S (behind
-// the columns still to be read); `half` is told when 64 columns are there.
-// Returns the row sum of the unrounded P.
-template <bool MASK, bool HALVES>
-__device__ __forceinline__ float row_exp(uint32_t tS, int chunks, Mask k, float c2, float m, uint64_t* half, int lane) {
+__device__ __forceinline__ float row_exp_masked(uint32_t tS, int chunks, const Mask& k, float c2, float m, uint64_t* most,
+                                                int lane) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        uint32_t pk[16];
-        if (MASK && k.none(c * 32)) {
+        if (k.none(c * 32)) {
+            uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = 0;
             tmem_st16(tS + c * 16, pk);
-            if (HALVES && c == 1) hand_over<HALVES>(half, lane);
-            continue;
-        }
-        uint32_t u[32];
-        tmem_ld32(tS + c * 32, u);
-        if (MASK && !k.all(c * 32)) {
-            const uint32_t see = k.bits(c * 32);
+        } else {
+            uint32_t u[32];
+            tmem_ld32(tS + c * 32, u);
+            if (!k.all(c * 32)) {
+                const uint32_t see = k.bits(c * 32);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
+                for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
+            }
+            exp32(acc, u, c2, m, tS + c * 16);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(u[2 * e]), c2, -m));
-            const float p1 = ex2(fmaf(__uint_as_float(u[2 * e + 1]), c2, -m));
-            acc[e & 3] += p0 + p1;
-            pk[e] = pack_bf16(p0, p1);
-        }
-        tmem_st16(tS + c * 16, pk);
-        if (HALVES && c == 1) hand_over<HALVES>(half, lane);
+        if (c == 2) hand_over(most, lane);
     }
-    if (HALVES && chunks == 1) hand_over<HALVES>(half, lane);
+    if (chunks < 3) hand_over(most, lane);
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -376,10 +418,10 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* q_full = bars + 0;          // [2], as all of these one per query tile
     uint64_t* q_empty = bars + 2;
     uint64_t* s_full = bars + 4;
-    // The first 64 columns of P: the product with V starts on them while the softmax works on
-    // the others (32K tokens, window 4096, D = 128: 1452 us, without it 1474; at D = 64 the
-    // product is short and the second wait costs more than it gives: 1297, with it 1338).
-    uint64_t* p_half = bars + 8;
+    // The first 96 columns of P: the product with V starts on them while the softmax works on
+    // the others (32K tokens, window 4096: D = 128 1341 us; 1345 with 64 columns, 1403 with 32,
+    // 1391 without; D = 64 1176, without 1230).
+    uint64_t* p_most = bars + 8;
     uint64_t* p_full = bars + 10;
     uint64_t* o_full = bars + 12;
     uint64_t* done = bars + 14;
@@ -401,8 +443,8 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&q_full[w], 1);
             mbar_init(&q_empty[w], 1);
             mbar_init(&s_full[w], 1);
-            mbar_init(&p_half[w], 4);
-            mbar_init(&p_full[w], C::kHalves ? 4 : BM);
+            mbar_init(&p_most[w], 4);
+            mbar_init(&p_full[w], 4);
             mbar_init(&o_full[w], 1);
         }
         mbar_init(done, 1);
@@ -521,23 +563,22 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             mma_commit_lead(lead, &s_full[w]);
         };
-        // O_w += P_w V, the first half of the keys as soon as their P is there
+        // O_w += P_w V, most of the keys as soon as their P is there
         auto issue_PV = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
-            if (!wait(C::kHalves ? &p_half[w] : &p_full[w], par)) return;
+            if (!wait(&p_most[w], par)) return;
             mma_ts_lead(lead, d, p, b0, idO, acc);
 #pragma unroll
-            for (int kk = 1; kk < BN / 32; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
-            if (C::kHalves && !wait(&p_full[w], par)) return;
+            for (int kk = 1; kk < kMost; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
+            if (!wait(&p_full[w], par)) return;
 #pragma unroll
-            for (int kk = BN / 32; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
+            for (int kk = kMost; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
         };
         auto issue_PV_sink = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
-            if (C::kHalves && !wait(&p_half[w], par)) return;
-            if (!wait(&p_full[w], par)) return;
+            if (!wait(&p_most[w], par) || !wait(&p_full[w], par)) return;
 #pragma unroll 1
             for (int kk = 0; kk < ns16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, kk > 0 ? 1u : acc);
         };
@@ -696,7 +737,7 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         mk.ns = j == 0 ? a.n_sink : 0;
                     }
                 }
-                const float mx = masked ? row_max<true>(tS, chunks, mk) : row_max<false>(tS, chunks, mk);
+                const float mx = masked ? row_max_masked(tS, chunks, mk) : row_max(tS);
                 const float mx2 = mx * c2;
                 // Lazy rescale: this row's reference max moves only when the tile max
                 // exceeds it by more than 2^8; tcgen05.ld/st are warp-collective, so O is
@@ -723,9 +764,9 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
                 started = true;
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                l += masked ? row_exp<true, C::kHalves>(tS, chunks, mk, c2, m_use, &p_half[w], lane)
-                            : row_exp<false, C::kHalves>(tS, chunks, mk, c2, m_use, &p_half[w], lane);
-                hand_over<C::kHalves>(&p_full[w], lane);
+                l += masked ? row_exp_masked(tS, chunks, mk, c2, m_use, &p_most[w], lane)
+                            : row_exp(tS, c2, m_use, &p_most[w], lane);
+                hand_over(&p_full[w], lane);
             }
             if (!ok) break;
             // ---- epilogue: O = O_acc / l, lse = ln(sum exp(s)); every row sees itself, so l > 0
