@@ -196,16 +196,19 @@ __device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
 // heads of 8 kv heads and a window of 4096 the single-phase kernel of bwd_tc.cu
 // took 8.65 ms on the same items, the two phases alone 4.85, with what follows 2.89.
 //
-// What bounds the variant, on the same problem.  The P/dS warps and the drain
-// share the LSU data pipe, which was busy 78% of the time while dQ left as
-// reductions from registers: now the drain writes blocks to shared memory and the
-// copy engine adds them (kBulk; D = 128 5.08 -> 4.21 ms, one dO slot instead of two
-// for the room).  The MMA role runs as a converged warp of which one lane issues,
-// so that descriptors sit in uniform registers (D = 64 3.69 -> 3.36).  D = 128 now
-// takes 4.15 ms (1230 TFLOP/s, 65% of the cuBLAS rate): 0.5 ms are the memory
-// traffic of the preparing and finishing kernels and the ends of the lists, and a
-// step of 128 x 128 takes 2.05 us, 1.45 of them MMAs; the rest is the chain
-// S -> P -> dS -> dQ of one tile, of which TMEM holds one and a half at a time.
+// What bounds the variant, on the same problem: shared memory.  A step of 128 x 128
+// at D = 128 reads 64 KB for each of the four products whose operands both lie there
+// (128 bytes per cycle: all of its bandwidth while they run) and 32 KB for dV,
+// writes 32 KB of dS and 64 KB of dQ, which are read once more, and takes in 64 KB
+// of Q and dO: 512 KB, 4100 cycles, and a step takes 3900 (2.05 us).  So what cut
+// that traffic or the LSU's part of it counted -- dQ leaving as bulk reductions of
+// blocks in shared memory (kBulk: 5.08 -> 4.21 ms, one dO slot instead of two for the
+// room) -- and shorter chains did not: P or dS handed over in parts, TMEM loads under
+// arithmetic, polling, other orders.  At D = 64 the MMA role matters too: it runs as
+// a converged warp of which one lane issues, so that descriptors sit in uniform
+// registers (3.69 -> 3.36 ms).  D = 128 takes 4.15 ms (1240 TFLOP/s, 65% of the cuBLAS
+// rate), of which 0.5 are the preparing and finishing kernels' memory traffic and
+// the ends of the lists.
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a

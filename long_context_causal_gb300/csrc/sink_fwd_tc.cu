@@ -24,11 +24,11 @@
 // work for 2200 of a step's 2600 cycles (moving exponentials to the FMA pipe gained
 // nothing: it is the chain, not MUFU).  A block's ends -- masked tiles, the sink tile's
 // step, the epilogue -- cost another 4 us of chain, so the lists of a CTA's blocks
-// run on into one another (issuer), a 32-column piece of a masked tile pays for its
-// mask only if some of its elements are masked (Mask), and the output leaves in
-// 64-byte pieces.  Measured, 32K tokens, 32 heads of 8 kv heads, 4 sinks: window 4096
-// 1341 us (D = 128; 1540 TFLOP/s, 81% of the cuBLAS rate), window 1024 512; D = 64
-// 1176 and 455; without sinks, window 128 181 and window 1 105 (D = 128).
+// run on into one another (issuer), 32-column pieces of a masked tile that no row
+// sees are skipped (Mask), and the output leaves in 64-byte pieces.  Measured back
+// to back, 32K tokens, 32 heads of 8 kv heads, 4 sinks: window 4096 1332 us (D = 128;
+// 1550 TFLOP/s, 81% of the cuBLAS rate), window 1024 511; D = 64 1169 and 451; without
+// sinks, window 128 180 and window 1 105 (D = 128; 100 at the memory's rate).
 //
 // Schedule.  No work list: costs never fall from a block to the next one of
 // its head, so the blocks in the order last to first of all heads are sorted
@@ -295,11 +295,9 @@ __device__ __forceinline__ float row_exp_masked(uint32_t tS, int chunks, const M
         } else {
             uint32_t u[32];
             tmem_ld32(tS + c * 32, u);
-            if (!k.all(c * 32)) {
-                const uint32_t see = k.bits(c * 32);
+            const uint32_t see = k.bits(c * 32);          // a branch around it, as above, costs more than it saves
 #pragma unroll
-                for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
-            }
+            for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
             exp32(acc, u, c2, m, tS + c * 16);
         }
         if (c == 2) hand_over(most, lane);
