@@ -581,6 +581,31 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // ---------------------------------------------------------------- math
+// Two fp32 numbers in a register pair, and the instructions that take two pairs.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ float sum_f32x2(uint64_t x) {
+    const float2 r = unpack_f32x2(x);
+    return r.x + r.y;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // Hardware base-2 exponential (MUFU), flush-to-zero; ex2(-inf) = 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
