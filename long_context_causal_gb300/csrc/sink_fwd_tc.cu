@@ -19,16 +19,17 @@
 // sinks, rounded up to 16 columns: N = 4 costs an eighth of a tile.
 //
 // What bounds it.  A query tile's steps form a chain: S (550 cycles at D = 128),
-// the softmax of its row (1400), barriers (500), P V (550, of which three quarters
+// the softmax of its row (1350), barriers (500), P V (550, of which three quarters
 // run under the softmax).  The two chains of a CTA overlap, and the tensor cores
-// work for 2200 of a step's 2600 cycles (moving exponentials to the FMA pipe gained
-// nothing: it is the chain, not MUFU).  A block's ends -- masked tiles, the sink tile's
-// step, the epilogue -- cost another 4 us of chain, so the lists of a CTA's blocks
-// run on into one another (issuer), 32-column pieces of a masked tile that no row
-// sees are skipped (Mask), and the output leaves in 64-byte pieces.  Measured back
-// to back, 32K tokens, 32 heads of 8 kv heads, 4 sinks: window 4096 1332 us (D = 128;
-// 1550 TFLOP/s, 81% of the cuBLAS rate), window 1024 511; D = 64 1169 and 451; without
-// sinks, window 128 180 and window 1 105 (D = 128; 100 at the memory's rate).
+// work for 2200 of a step's 2550 cycles.  The softmax is bound by issue and
+// latency, not by MUFU: exponentials moved to the FMA pipe made it slower.  A
+// block's ends -- masked tiles, the sink tile's step, the epilogue -- cost another
+// 4 us of chain, so the lists of a CTA's blocks run on into one another (issuer),
+// 32-column pieces of a masked tile that no row sees are skipped (Mask), and the
+// output leaves in 64-byte pieces.  Measured back to back, 32K tokens, 32 heads of
+// 8 kv heads, 4 sinks: window 4096 1320 us (D = 128; 1560 TFLOP/s, 82% of the cuBLAS
+// rate), window 1024 499; D = 64 1160 and 443; without sinks, window 128 175 and
+// window 1 105 (D = 128; 100 at the memory's rate).
 //
 // Schedule.  No work list: costs never fall from a block to the next one of
 // its head, so the blocks in the order last to first of all heads are sorted
@@ -75,7 +76,8 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O only when t
 template <int D>
 struct Cfg {
     static constexpr int kTileBytes = BN * D * 2;
-    static constexpr int kSlots = D == 128 ? 4 : 6;            // K/V ring depth
+    static constexpr int kSlots = 4;                           // K/V ring depth (6 and 8 gain nothing at D = 64)
+    static constexpr bool kTwice = D == 128;                   // P is handed over in two parts (rule at p_most)
     static constexpr int kQBytes = 2 * kTileBytes;
     static constexpr int kSmem = kQBytes + kSlots * kTileBytes + 1024 /*barriers*/ + 1024 /*align*/;
 };
@@ -213,8 +215,8 @@ __device__ __forceinline__ void max32(float (&m)[4], const uint32_t (&u)[32]) {
 }
 // P = exp2(s * c2 - m) of 32 columns as bf16 pairs to tP; acc: sums of the unrounded P
 // of the even and of the odd columns.  Two columns per instruction where there is one:
-// the softmax warps are bound by issue (32K tokens, D = 128: window 4096 1342 -> 1322 us,
-// 128 180 -> 175; D = 64 1170 -> 1200 and 164 -> 160).
+// the softmax warps are bound by issue (32K tokens, D = 128: window 4096 1342 -> 1320 us,
+// 128 180 -> 175; D = 64 1170 -> 1160 and 164 -> 156).
 __device__ __forceinline__ void exp32(uint64_t& acc, const uint32_t (&u)[32], float c2, float m, uint32_t tP) {
     uint32_t pk[16];
     const uint64_t cc = pack_f32x2(c2, c2), mm = pack_f32x2(-m, -m);
@@ -251,6 +253,7 @@ __device__ __forceinline__ float row_max(uint32_t tS) {
 }
 // Its P, written as bf16 pairs over S (behind the columns still to be read);
 // `most` is told when 96 columns are there.  Returns the row sum of the unrounded P.
+template <bool TWICE>
 __device__ __forceinline__ float row_exp(uint32_t tS, float c2, float m, uint64_t* most, int lane) {
     uint64_t acc = pack_f32x2(0.f, 0.f);
     uint32_t a[32], b[32];
@@ -264,7 +267,7 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float c2, float m, uint64_
     tmem_wait_ld32(a);
     tmem_ld32_async(tS + 96, b);
     exp32(acc, a, c2, m, tS + 32);
-    hand_over(most, lane);
+    if (TWICE) hand_over(most, lane);
     tmem_wait_ld32(b);
     exp32(acc, b, c2, m, tS + 48);
     return sum_f32x2(acc);
@@ -287,6 +290,7 @@ __device__ __forceinline__ float row_max_masked(uint32_t tS, int chunks, const M
     }
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
+template <bool TWICE>
 __device__ __forceinline__ float row_exp_masked(uint32_t tS, int chunks, const Mask& k, float c2, float m, uint64_t* most,
                                                 int lane) {
     uint64_t acc = pack_f32x2(0.f, 0.f);
@@ -305,9 +309,9 @@ __device__ __forceinline__ float row_exp_masked(uint32_t tS, int chunks, const M
             for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : kMinusInf;   // P = 0: the scale is positive
             exp32(acc, u, c2, m, tS + c * 16);
         }
-        if (c == 2) hand_over(most, lane);
+        if (TWICE && c == 2) hand_over(most, lane);
     }
-    if (chunks < 3) hand_over(most, lane);
+    if (TWICE && chunks < 3) hand_over(most, lane);
     return sum_f32x2(acc);
 }
 
@@ -422,8 +426,9 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* q_empty = bars + 2;
     uint64_t* s_full = bars + 4;
     // The first 96 columns of P: the product with V starts on them while the softmax works on
-    // the others (32K tokens, window 4096: D = 128 1341 us; 1345 with 64 columns, 1403 with 32,
-    // 1391 without; D = 64 1176, without 1230).
+    // the others (32K tokens, D = 128, window 4096 1320 us, 1342 without; 5003 tokens, window
+    // 1000 82.7 and 84.7; with 64 columns 1300 and 84.5).  At D = 64 the product is half as
+    // long and the second wait costs more than it gives: 1204 us, 1160 without.
     uint64_t* p_most = bars + 8;
     uint64_t* p_full = bars + 10;
     uint64_t* o_full = bars + 12;
@@ -570,18 +575,18 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         auto issue_PV = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
-            if (!wait(&p_most[w], par)) return;
+            if (!wait(C::kTwice ? &p_most[w] : &p_full[w], par)) return;
             mma_ts_lead(lead, d, p, b0, idO, acc);
 #pragma unroll
             for (int kk = 1; kk < kMost; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
-            if (!wait(&p_full[w], par)) return;
+            if (C::kTwice && !wait(&p_full[w], par)) return;
 #pragma unroll
             for (int kk = kMost; kk < BN / 16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, 1u);
         };
         auto issue_PV_sink = [&](int w, uint32_t slot, uint32_t par, uint32_t acc) {
             const uint64_t b0 = dVn + slot * kSlotStep;
             const uint32_t d = tmem + 256 + w * 128, p = tmem + w * 128;
-            if (!wait(&p_most[w], par) || !wait(&p_full[w], par)) return;
+            if ((C::kTwice && !wait(&p_most[w], par)) || !wait(&p_full[w], par)) return;
 #pragma unroll 1
             for (int kk = 0; kk < ns16; ++kk) mma_ts_lead(lead, d, p + kk * 8, b0 + kk * (2048 >> 4), idO, kk > 0 ? 1u : acc);
         };
@@ -767,8 +772,8 @@ sink_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
                 started = true;
                 const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                l += masked ? row_exp_masked(tS, chunks, mk, c2, m_use, &p_most[w], lane)
-                            : row_exp(tS, c2, m_use, &p_most[w], lane);
+                l += masked ? row_exp_masked<C::kTwice>(tS, chunks, mk, c2, m_use, &p_most[w], lane)
+                            : row_exp<C::kTwice>(tS, c2, m_use, &p_most[w], lane);
                 hand_over(&p_full[w], lane);
             }
             if (!ok) break;
