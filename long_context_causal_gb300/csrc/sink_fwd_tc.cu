@@ -21,9 +21,11 @@
 // What bounds it.  A query tile's steps form a chain: S (550 cycles at D = 128),
 // the softmax of its row (1350), barriers (500), P V (550, of which three quarters
 // run under the softmax).  The two chains of a CTA overlap, and the tensor cores
-// work for 2200 of a step's 2550 cycles.  The softmax is bound by issue and
-// latency, not by MUFU: exponentials moved to the FMA pipe made it slower.  A
-// block's ends -- masked tiles, the sink tile's step, the epilogue -- cost another
+// work for 2200 of a step's 2550 cycles.  The softmax is bound by latency (two
+// warps on a sub-partition; issue slots 41% busy, MUFU 33%): exponentials moved to
+// the FMA pipe made it slower, fewer instructions and loads under arithmetic
+// faster.  A block's ends -- masked tiles, the sink tile's step, the epilogue --
+// cost another
 // 4 us of chain, so the lists of a CTA's blocks run on into one another (issuer),
 // 32-column pieces of a masked tile that no row sees are skipped (Mask), and the
 // output leaves in 64-byte pieces.  Measured back to back, 32K tokens, 32 heads of
@@ -215,7 +217,7 @@ __device__ __forceinline__ void max32(float (&m)[4], const uint32_t (&u)[32]) {
 }
 // P = exp2(s * c2 - m) of 32 columns as bf16 pairs to tP; acc: sums of the unrounded P
 // of the even and of the odd columns.  Two columns per instruction where there is one:
-// the softmax warps are bound by issue (32K tokens, D = 128: window 4096 1342 -> 1320 us,
+// the softmax warps' instructions are on the chain (32K tokens, D = 128: window 4096 1342 -> 1320 us,
 // 128 180 -> 175; D = 64 1170 -> 1160 and 164 -> 156).
 __device__ __forceinline__ void exp32(uint64_t& acc, const uint32_t (&u)[32], float c2, float m, uint32_t tP) {
     uint32_t pk[16];
