@@ -24,9 +24,10 @@
 // work for 2200 of a step's 2550 cycles.  The softmax is bound by latency (two
 // warps on a sub-partition; issue slots 41% busy, MUFU 33%): exponentials moved to
 // the FMA pipe made it slower, fewer instructions and loads under arithmetic
-// faster.  A block's ends -- masked tiles, the sink tile's step, the epilogue --
-// cost another
-// 4 us of chain, so the lists of a CTA's blocks run on into one another (issuer),
+// faster; two threads a row (four softmax warpgroups, maxima exchanged) took 1724 us
+// for 1312: too few registers, and five warps beside the issuing one.  A block's
+// ends -- masked tiles, the sink tile's step, the epilogue -- cost another 4 us of
+// chain, so the lists of a CTA's blocks run on into one another (issuer),
 // 32-column pieces of a masked tile that no row sees are skipped (Mask), and the
 // output leaves in 64-byte pieces.  Measured back to back, 32K tokens, 32 heads of
 // 8 kv heads, 4 sinks: window 4096 1320 us (D = 128; 1560 TFLOP/s, 82% of the cuBLAS

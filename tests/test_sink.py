@@ -425,6 +425,42 @@ def test_captured_and_replayed():
     dfa.dfa_check_errors()
 
 
+FIRST = """
+import torch
+from long_context_causal_gb300 import dfa
+from long_context_causal_gb300.inputs import make
+q, k, v, do = make(1, 1, 1, 2000, 64, torch.bfloat16, device="cuda", seed=90)
+lens = torch.full((1,), 1999, dtype=torch.int32, device="cuda")
+q1 = q[:, 1998].contiguous()
+
+def chain():
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, 2000)             # blocks shared by clusters
+    O2, lse2 = dfa.dfa_attn_fwd_sink(q, k, v, 40, 3)
+    kept = dfa.dfa_ckpt8_save(q, k, v, O2)
+    return (O, lse, O2, lse2, kept) + dfa.dfa_attn_bwd_ckpt8(kept, lse2, do, 1, 40, 3)[1:] + \\
+        dfa.dfa_attn_decode_sink(q1, k, v, lens, 40, 3)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = chain()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, chain()))
+dfa.dfa_check_errors()
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """What a kernel sets up once per device may be set up while a stream is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_another_stream_and_two_at_once():
     W, N = 150, 3
     sets = [make(1, 4, 2, 1100, D, torch.bfloat16, device=DEV, seed=54 + D) for D in (64, 128)]
