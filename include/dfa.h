@@ -271,7 +271,7 @@ dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const 
  *            each
  * Cache rows that the query does not see may hold anything, NaN included.
  * bf16 only, D in {64, 128}, n_sink <= 128, at most 8192 sequences
- * (UNSUPPORTED otherwise).  Two launches; the same bits on every call. */
+ * (UNSUPPORTED otherwise).  One or two launches; the same bits on every call. */
 size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D);
 dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
                                 int S_max, int D, const int64_t* kv_strides, const int32_t* kv_len, int window,

@@ -1018,9 +1018,7 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
     if (!kv_len || !lse || ((reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(lse)) & 3u))
         return fail(DFA_ERR_INVALID_ARG, "kv_len and lse must be 4-byte aligned pointers");
     p.window = std::min(window, S_max);
-    st = sink_decode(p, q, k, v, kv_len, O, lse, workspace, static_cast<cudaStream_t>(stream));
-    if (st == DFA_OK) count_launch(DFA_KERNEL_FWD), count_launch(DFA_KERNEL_MERGE);
-    return st;
+    return sink_decode(p, q, k, v, kv_len, O, lse, workspace, static_cast<cudaStream_t>(stream));
 }
 
 // ---------------------------------------------------------------- 8-bit attention checkpoints

@@ -15,6 +15,11 @@
 // sum, unnormalised output), at most two per CTA, which a second kernel joins
 // in the order of the keys.  No atomics: the same bits on every call.
 //
+// Few short segments (CLUSTER; rule at launch()): a cluster of eight CTAs takes a
+// segment, an eighth of its tiles each, and joins the parts through distributed
+// shared memory: one launch instead of two (1 sequence of 1501 tokens, 32 heads of 8
+// kv heads, window 1024: 5.6 us, by the two kernels 7.1; calls in a stream 8.2 and 9.6).
+//
 // Per CTA: one producer warp streams K and V tiles by TMA into a ring; eight
 // consumer warps in two groups take the tiles in turn, each warp 16 keys of
 // its tile.  S = Q K^T and O += P V run as m16n8k16 bf16 MMAs on registers,
@@ -45,6 +50,8 @@ constexpr int KT = 64;                         // keys per tile
 constexpr int MH = 16;                         // query heads per segment (MMA M)
 constexpr int kConsumers = 8;                  // warps; two groups of four
 constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kCluster = 8;                    // CTAs of a segment's cluster
+constexpr int kClusterTiles = 8 * kCluster;    // segments of more tiles are spread over all SMs (rule at launch())
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -141,7 +148,7 @@ __device__ __forceinline__ void next_segment(const Args& a, Cursor& c) {
     }
 }
 
-template <int D>
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
     using C = Cfg<D>;
@@ -171,36 +178,47 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         tma_prefetch_desc(&tmV);
         prefix[0] = 0;
     }
-    // Tiles before each sequence, all segments counted.
-    const int R = a.Hkv * a.HB;
-    int carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + (int)threadIdx.x;
-        int x = b < a.B ? seen(a, b).tiles * R : 0;
+    Cursor c;
+    int begin, end;
+    const int R = a.Hkv * a.HB, rank = blockIdx.x % kCluster;
+    if constexpr (CLUSTER) {
+        const int segment = blockIdx.x / kCluster;
+        c.b = segment / R;
+        c.r = segment % R;
+        c.s = seen(a, c.b);
+        begin = c.k = c.s.tiles * rank / kCluster;
+        end = c.s.tiles * (rank + 1) / kCluster;
+        __syncthreads();
+    } else {
+        // Tiles before each sequence, all segments counted.
+        int carry = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + (int)threadIdx.x;
+            int x = b < a.B ? seen(a, b).tiles * R : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) s_scan[warp] = x;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) x += s_scan[w];
+            if (b < a.B) prefix[b + 1] = carry + x;
+            int all = 0;
+            for (int w = 0; w < kThreads / 32; ++w) all += s_scan[w];
+            carry += all;
+            __syncthreads();
         }
-        if (lane == 31) s_scan[warp] = x;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) x += s_scan[w];
-        if (b < a.B) prefix[b + 1] = carry + x;
-        int all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) all += s_scan[w];
-        carry += all;
-        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
+        const int total = prefix[a.B];
+        const int n_ctas = min((int)gridDim.x, total);   // every one of them has a tile
+        if ((int)blockIdx.x >= n_ctas) return;
+        begin = (int)((int64_t)total * blockIdx.x / n_ctas);
+        end = (int)((int64_t)total * (blockIdx.x + 1) / n_ctas);
+        c = find(a, prefix, begin);
     }
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
-    const int total = prefix[a.B];
-    const int n_ctas = min((int)gridDim.x, total);   // every one of them has a tile
-    if ((int)blockIdx.x >= n_ctas) return;
-    const int begin = (int)((int64_t)total * blockIdx.x / n_ctas);
-    const int end = (int)((int64_t)total * (blockIdx.x + 1) / n_ctas);
-    Cursor c = find(a, prefix, begin);
-
     if (warp == kConsumers) {
         // ------------------------------------------------------------ TMA producer
         bool ok = true;
@@ -229,6 +247,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             for (int i = max(x - begin - C::kStages, 0); i < x - begin; ++i)
                 mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, &dummy, nullptr);
         }
+        __syncwarp();
+        if constexpr (CLUSTER) {
+            cluster_sync();
+            cluster_sync();
+        }
         return;
     }
     // ---------------------------------------------------------------- consumers
@@ -239,6 +262,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     const int g = lane / 4, t = lane % 4, grp = warp / 4, w16 = (warp % 4) * 16;
     const int rn = (g >> 1) | ((g & 1) << 2);
     bool ok = true;
+    float4 mine[2];                      // CLUSTER: this CTA's part of at most two groups of four dims
+    float2 mine_ml[2];
+    mine_ml[0] = mine_ml[1] = make_float2(-INFINITY, 0.f);
+    mine[0] = mine[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x = begin; x < end && ok;) {
         // One segment, or the part of it in this CTA's range.
         const int k0 = c.k, k1 = min(c.s.tiles, k0 + end - x);
@@ -387,7 +414,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            if (whole) {
+            if constexpr (CLUSTER) {
+                const bool second = y >= kConsumers * 32;
+                mine[second] = acc;
+                mine_ml[second] = make_float2(m, l);
+            } else if (whole) {
                 const float inv = 1.f / l;
                 const int64_t row = (int64_t)c.b * a.H + h0 + h;
                 *reinterpret_cast<uint2*>(a.O + row * D + d) =
@@ -399,15 +430,62 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 2) + D) = make_float2(m, l);
             }
         }
+        if constexpr (CLUSTER) break;
         named_bar_sync(1, kConsumers * 32);  // the merge buffer is read before the next segment fills it
         if (x < end) next_segment(a, c);
+    }
+    if constexpr (CLUSTER) {
+        // Parts [rank][head][D + 4] (unnormalised output, maximum, sum) in rank 0's ring, which it no longer needs.
+        const int h0 = c.r / a.HB * a.G + c.r % a.HB * MH, nh = min(a.G - c.r % a.HB * MH, MH);
+        constexpr int kRow = D + 4;
+        static_assert(kCluster * MH * kRow * 4 <= C::kOffMerge, "parts");
+        __syncwarp();
+        cluster_sync();
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int y = threadIdx.x + z * kConsumers * 32, h = y / (D / 4), d = y % (D / 4) * 4;
+            if (h >= nh) continue;
+            const uint32_t dst = map_to_rank(smem_u32(smem) + (uint32_t)((rank * MH + h) * kRow + d) * 4, 0);
+            st_cluster_v4(dst, mine[z]);
+            if (d == 0) st_cluster_v2(dst + D * 4, mine_ml[z]);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (rank != 0) return;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int y = threadIdx.x + z * kConsumers * 32, h = y / (D / 4), d = y % (D / 4) * 4;
+            if (h >= nh) continue;
+            const float* part = reinterpret_cast<const float*>(smem) + h * kRow;
+            float m = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < kCluster; ++p) m = fmaxf(m, part[p * MH * kRow + D]);
+#pragma unroll
+            for (int p = 0; p < kCluster; ++p) {
+                const float* q = part + p * MH * kRow;
+                if (q[D] == -INFINITY && q[D + 1] == 0.f) continue;   // a part without keys
+                const float f = ex2(q[D] - m);
+                const float4 v = *reinterpret_cast<const float4*>(q + d);
+                l = fmaf(f, q[D + 1], l);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;          // no tiles: an empty sequence
+            const int64_t row = (int64_t)c.b * a.H + h0 + h;
+            *reinterpret_cast<uint2*>(a.O + row * D + d) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        }
     }
 }
 
 // Joins a segment's partials: blocks (segment, 256 pairs of dims of its heads),
 // one thread per pair.  Eight partials are loaded at a time, so that a segment cut
 // into many waits for memory a few times and not once per piece (one sequence of
-// 1501 tokens, 8 segments of 17 pieces: the step takes 7.2 us, 9.3 with one at a time).
+// 1501 tokens, 8 segments of 17 pieces: the step takes 7.1 us, 9.3 with one at a time).
 constexpr int kJoinThreads = 256, kJoinAhead = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -458,9 +536,9 @@ join_kernel(const Args a, int grid) {
         }
     }
     const int64_t row = (int64_t)b * a.H + h0 + h;
-    const float inv = l > 0.f ? 1.f / l : 0.f;   // no tiles: an empty sequence
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no tiles: an empty sequence
     *reinterpret_cast<uint32_t*>(a.O + row * D + d) = pack_bf16(acc.x * inv, acc.y * inv);
-    if (d == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -489,19 +567,49 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     const int n = (int)std::min<int64_t>(num_sms(), tiles);
     const int smem = C::kOffPrefix + (int)sizeof(int) * (p.B + 1);
     static std::atomic<uint64_t> seen{0};
+    static std::atomic<int> clusters{0};             // that run at a time
+    auto spread = decode_kernel<D, false>;
+    auto clustered = decode_kernel<D, true>;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)kCluster);
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = C::kOffPrefix + 16;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     if (first_on_device(seen)) {
         constexpr int most = C::kOffPrefix + (int)sizeof(int) * (kMaxDecodeBatch + 1);
         static_assert(most <= 232448, "shared memory");
-        if (cudaFuncSetAttribute(decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-            return fail(DFA_ERR_CUDA, "decode: shared memory attribute");
+        int k = 0;
+        if (cudaFuncSetAttribute(spread, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+            cudaFuncSetAttribute(clustered, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&k, clustered, &cfg) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "decode: kernel attributes");
+        clusters.store(k);
         mark_on_device(seen);
     }
-    decode_kernel<D><<<n, kThreads, smem, s>>>(mk, mv, a);
+    // One round of clusters, each with tiles enough for its share of the SMs: 4096 keys of 8 kv
+    // heads 8.2 us, spread over all SMs 8.9; 8192 keys 12.1 and 10.8; 262 keys 4.2 and 6.0.
+    if (segments <= clusters.load() && decode_tiles(p) <= kClusterTiles) {
+        cfg.gridDim = dim3((unsigned)(segments * kCluster));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mk, mv, a);
+        if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+        count_launch(DFA_KERNEL_FWD);
+        return DFA_OK;
+    }
+    spread<<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
     e = launch_overlapped(join_kernel<D>, dim3(segments, (std::min(a.G, MH) * (D / 2) + kJoinThreads - 1) / kJoinThreads),
                           kJoinThreads, 0, s, a, n);
-    return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_FWD);
+    count_launch(DFA_KERNEL_MERGE);
+    return DFA_OK;
 }
 
 }  // namespace

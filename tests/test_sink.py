@@ -288,6 +288,9 @@ DECODE = [
     (1, 2, 1, 9000, 64, 3000, 100, [9000]),
     (17, 4, 4, 260, 128, 70, 4, [0] * 8 + [260, 3, 70, 71, 74, 75, 138, 139, 200]),
     (300, 2, 1, 40, 64, 16, 2, [i % 41 for i in range(300)]),
+    (2, 32, 2, 600, 128, 500, 3, [599, 0]),                       # 16 heads to a key/value head
+    (1, 16, 8, 4096, 128, 4096, 0, [4096]), (1, 16, 8, 4200, 128, 4160, 0, [4190]),   # 64 and 65 tiles a segment
+    (15, 2, 1, 130, 64, 100, 1, list(range(0, 130, 9))), (16, 2, 1, 130, 64, 100, 1, list(range(0, 130, 9)) + [130]),
 ]
 
 
