@@ -185,7 +185,9 @@ __device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
 // roundings of dS, which it magnifies (128 sinks that hold most of a row's
 // weight: 8.7e-3).  So key tile 0 of a problem with sinks is FINE: its dS goes
 // to dQ as two bf16 numbers, dS and what its rounding lost (the rest), each an
-// MMA.  FINE tiles have CTAs of their own, which run a second copy of the roles:
+// MMA.  dV of its keys, the longest sums of all, takes P the same way: with P
+// rounded once an element of a sink's dV, whose terms cancelled, was off by half of
+// dV's rms (5013 tokens, causal, 1 sink; 0.02 of it now, at no cost).  FINE tiles have CTAs of their own, which run a second copy of the roles:
 // in one copy the extra code slowed every tile by 2%.  The rest's 32 KB of
 // shared memory come from the second dO slot (HD = 128, whose dO ring is then
 // one deep) or from the halves that HD = 64 leaves free in the K and V tiles.
@@ -534,6 +536,11 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                     for (int kk = 0; kk < BT / 16; ++kk)
                         ts(tm + kColDV, tm + kColS + kk * 8 + (kk >= 4 ? 32 : 0), b0 + kk * kRows16, idKM,
                                kk > 0 ? 1u : acc0);
+                    if constexpr (FINE) {   // and what P^T's rounding lost, behind it in each half
+#pragma unroll
+                        for (int kk = 0; kk < BT / 16; ++kk)
+                            ts(tm + kColDV, tm + kColS + 32 + kk * 8 + (kk >= 4 ? 32 : 0), b0 + kk * kRows16, idKM, 1u);
+                    }
                 }
                 commit(&do_empty[n % kDOSlots]);
                 if (more && !issue_S(n + 1)) break;       // S^T columns are free after phase 1
@@ -633,9 +640,11 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
                                   (x.t + 1) * BT <= SEQ_LKV(x);
                 // ---- phase 1: P^T = exp2(S^T c + nlse2) -> TMEM (bf16) and registers
                 uint32_t u[32], pk[32];
+                [[maybe_unused]] uint32_t lost[16];   // FINE: what P^T's rounding to bf16 lost
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     tmem_ld32(tS + c, u);
+                    if (FINE && c > 0) tmem_st16(tS + 32, lost);   // all of S^T is in registers
                     if (!full) {   // masked scores become -inf, so exp2 gives exactly 0
                         if constexpr (SINK) {
                             const int at = q0 + c;   // queries [kvg, q_hi) of the sequence see the key
@@ -657,12 +666,26 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + c + e);
+                            if constexpr (FINE) {
+                                const float2 x01 = make_float2(ex2(fmaf(__uint_as_float(u[e]), a.c2, l4.x)),
+                                                               ex2(fmaf(__uint_as_float(u[e + 1]), a.c2, l4.y)));
+                                const float2 x23 = make_float2(ex2(fmaf(__uint_as_float(u[e + 2]), a.c2, l4.z)),
+                                                               ex2(fmaf(__uint_as_float(u[e + 3]), a.c2, l4.w)));
+                                ph[e / 2] = pack_bf16(x01.x, x01.y);
+                                ph[e / 2 + 1] = pack_bf16(x23.x, x23.y);
+                                lost[e / 2] = pack_rest(x01, ph[e / 2]);
+                                lost[e / 2 + 1] = pack_rest(x23, ph[e / 2 + 1]);
+                                pk[(c + e) / 2] = pack_f16_sat(x01.x, x01.y);
+                                pk[(c + e) / 2 + 1] = pack_f16_sat(x23.x, x23.y);
+                                continue;
+                            }
                             ph[e / 2] = exp2_pack_both(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), a.c2, l4.x, l4.y,
                                                        pk[(c + e) / 2]);
                             ph[e / 2 + 1] = exp2_pack_both(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]), a.c2, l4.z,
                                                            l4.w, pk[(c + e) / 2 + 1]);
                         }
                         tmem_st16(tS + c / 2, ph);
+                        if (FINE && c > 0) tmem_st16(tS + 48, lost);
                         continue;
                     }
 #pragma unroll

@@ -674,6 +674,11 @@ __device__ __forceinline__ float2 ds_pair(uint32_t p, float u0, float u1, float 
     return r;
 }
 // What a pair loses in pack_bf16, packed: bf16(x - bf16(x)).
+__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_rest(float2 x, uint32_t packed) {
     return pack_bf16(x.x - __uint_as_float(packed << 16), x.y - __uint_as_float(packed & 0xffff0000u));
 }

@@ -165,6 +165,24 @@ def test_sinks_that_share_a_direction(D, S, window, n_sink):
     check_bwd((dQ, dK, dV), q, k, v, O, lse, do, window, n_sink)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,window", [(6, 100), (40, 100), (200, 30)])
+def test_dv_of_the_sinks_tile(D, S, window):
+    """The keys of tile 0 of a problem with sinks: their dV sums over the most queries, and P comes to it in two
+    bf16 numbers (2^-8 squared), so that an element whose terms cancel is not off by their rounding."""
+    B, H, Hkv, n_sink = 2, 4, 2, 1
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=38)
+    u = torch.randn(Hkv, D, device=DEV, generator=torch.Generator(DEV).manual_seed(39))
+    q += (0.25 * u.repeat_interleave(H // Hkv, 0)).bfloat16()
+    k[:, :n_sink] = (0.3 * k[:, :n_sink] + 1.5 * u).bfloat16()
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dV = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink)[2]
+    dfa.dfa_check_errors()
+    r, terms, cancel, floor = sink.attn_bwd(*(np64(t) for t in (q, k, v, O, lse, do)), window, n_sink)["dV"]
+    tol = (2.0 ** -16 + F) * terms + F2 * cancel + 2.0 ** -39 * floor + U * np.abs(r) + 1e-30
+    close(dV[:, :128], r[:, :128], tol[:, :128], "dV")
+
+
 def test_window_over_every_key_is_the_causal_call():
     q, k, v, do = make(2, 4, 2, 700, 128, torch.bfloat16, device=DEV, seed=34)
     O, lse = dfa.dfa_attn_fwd_sink(q, k, v, 700, 9)
