@@ -246,7 +246,7 @@ dfa_status dfa_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
 dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
                              int S, int D, int window, int n_sink, float scale, void* O, float* lse,
                              void* stream);
-/* Bytes of workspace the backward needs (0 for sizes it does not take). */
+/* Bytes of workspace the backward needs (0 for sizes it does not take and for empty batches). */
 size_t dfa_attn_bwd_sink_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);
 /* Its backward from the saved O and lse, never re-running the forward:
  * P_ij = exp(s_ij - lse_i) on the visible pairs, Delta_i = <dO_i, O_i>, and

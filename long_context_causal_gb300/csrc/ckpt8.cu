@@ -408,6 +408,7 @@ SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
     x.n_q = (p.S + 127) / 128;
     x.window_tiles = std::min(x.n_q, (p.window + 126) / 128 + 1);   // a tile's last key is seen by window - 1 more queries
     x.n_sink = p.n_sink;
+    if (x.rows == 0 || x.n_q == 0) return x;                        // an empty batch: no items
     const int sms = num_sms(), longest = x.G * sink_range(x, 0), ordinary = x.G * x.window_tiles;
     const int tail = std::min(x.n_q, x.window_tiles);               // the last tiles' ranges shrink to 1
     const double rest = (double)x.rows * x.G *                      // tiles of the lists behind the first

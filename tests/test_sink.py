@@ -513,6 +513,24 @@ def test_tensors_on_the_wrong_place_are_refused():
     assert empty[0].shape == (1, 0, 2, 64) and empty[1].shape == (1, 2, 0)
 
 
+@pytest.mark.parametrize("n_sink", [0, 4])
+@pytest.mark.parametrize("B,S", [(0, 300), (2, 0)])
+def test_empty_batches(B, S, n_sink):
+    H, Hkv, D, W = 4, 2, 64, 100
+    q, do = (torch.empty(B, S, H, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v = (torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, W, n_sink)
+    ckpt = dfa.dfa_ckpt8_save(q, k, v, O)
+    for grads in (dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, W, n_sink), dfa.dfa_attn_bwd_ckpt8(ckpt, lse, do, Hkv, W, n_sink)):
+        assert [t.shape for t in grads] == [q.shape, k.shape, k.shape]
+    assert [t.shape for t in dfa.dfa_ckpt8_restore(ckpt, B, H, Hkv, S, D)] == [q.shape, k.shape, k.shape, q.shape]
+    if B == 0:
+        n = torch.empty(0, dtype=torch.int32, device=DEV)
+        O, lse = dfa.dfa_attn_decode_sink(torch.empty(0, H, D, dtype=torch.bfloat16, device=DEV), k, v, n, W, n_sink)
+        assert O.shape == (0, H, D) and lse.shape == (0, H)
+    dfa.dfa_check_errors()
+
+
 def test_numbers_out_of_range_are_refused():
     q, k, v, do = make(1, 2, 1, 64, 64, torch.bfloat16, device=DEV, seed=58)
     lens = torch.full((1,), 64, dtype=torch.int32, device=DEV)

@@ -197,6 +197,13 @@ def test_size_queries_refuse_quietly():
     assert 0 < a <= b
 
 
+@pytest.mark.parametrize("n_sink", [0, 4])
+@pytest.mark.parametrize("B,S", [(0, 300), (0, 0), (2, 0)])
+def test_an_empty_batch_needs_no_workspace(B, S, n_sink):
+    assert dfa.dfa_attn_bwd_sink_workspace_size(B, 4, 2, S, 128, 64, n_sink) == 0
+    assert dfa.dfa_attn_bwd_ckpt8_workspace_size(B, 4, 2, S, 64, 64, n_sink) == 0
+
+
 def test_the_binding_refuses_tensors_it_must_not_hand_on():
     t = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
     q, k, lse = t(1, 8, 4, 64), t(1, 8, 2, 64), t(1, 4, 8, dtype=torch.float32)
