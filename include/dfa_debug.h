@@ -53,6 +53,13 @@ dfa_status dfa_debug_cta_trace(uint64_t* buf, int capacity);
  * (device, 2 ints) is given, out[w] = 1 if warp w's wait completed, else 0. */
 dfa_status dfa_debug_wait_timeout(int* out, void* stream);
 
+/* Host only: how dfa_attn_bwd_sink deals its work on a GPU with n_sms SMs.
+ * plan[0] CTAs, [1] those of them that take key tile 0 in the finer arithmetic
+ * (0 without sinks), [2] items, [3] items of key tile 0, [4] query tiles per
+ * piece, [5] 1 if every list is cut, [6] slabs, [7] rows (B * H_kv). */
+dfa_status dfa_debug_sink_bwd_plan(int B, int H, int H_kv, int S, int D, int window, int n_sink, int n_sms,
+                                   int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -401,15 +401,16 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
 // summing.
 constexpr double kFine = 1.9, kItem = 2.5;
 
-SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
+SinkBwdPlan sink_bwd_plan(const SinkProblem& p, int sms) {
     SinkBwdPlan x{};
+    sms = std::max(sms, 2);          // key tile 0 has CTAs of its own
     x.rows = p.B * p.Hkv;
     x.G = p.H / p.Hkv;
     x.n_q = (p.S + 127) / 128;
     x.window_tiles = std::min(x.n_q, (p.window + 126) / 128 + 1);   // a tile's last key is seen by window - 1 more queries
     x.n_sink = p.n_sink;
     if (x.rows == 0 || x.n_q == 0) return x;                        // an empty batch: no items
-    const int sms = num_sms(), longest = x.G * sink_range(x, 0), ordinary = x.G * x.window_tiles;
+    const int longest = x.G * sink_range(x, 0), ordinary = x.G * x.window_tiles;
     const int tail = std::min(x.n_q, x.window_tiles);               // the last tiles' ranges shrink to 1
     const double rest = (double)x.rows * x.G *                      // tiles of the lists behind the first
                         ((double)(x.n_q - tail) * x.window_tiles + tail * (tail + 1.) / 2 - x.window_tiles);
@@ -429,13 +430,14 @@ SinkBwdPlan sink_bwd_plan(const SinkProblem& p) {
             *fine_ctas = (int)std::min<int64_t>(n0, sms);
             return std::max((double)((n0 + *fine_ctas - 1) / *fine_ctas) * one, n > n0 ? len + kItem : 0.0);
         }
+        // Key tile 0 in r rounds of f CTAs, from the most CTAs down until those are what takes longest.
         double least = 1e30;
-        for (int r = 1, f = 0; r <= 256 && f != 1; ++r) {
+        for (int f = sms - 1; f > 0; --f) {
+            const int64_t r = (n0 + f - 1) / f;
             f = (int)((n0 + r - 1) / r);
-            if (f >= sms) continue;
             const double t = std::max(r * one, spread(n - n0, sms - f, len, rest, even));
             if (t < least) least = t, *fine_ctas = f;
-            if (r * one > t) break;
+            if (r * one >= t) break;
         }
         return least;
     };

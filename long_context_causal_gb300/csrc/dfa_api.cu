@@ -15,6 +15,7 @@
 #include <tuple>
 #include <vector>
 
+#include "../../include/dfa_debug.h"
 #include "internal.h"
 
 namespace dfa {
@@ -883,7 +884,7 @@ SinkProblem sink_problem(int B, int H, int Hkv, int S, int D, int window, int n_
 
 SinkWs sink_ws(const SinkProblem& p, bool ckpt) {
     SinkWs w;
-    const SinkBwdPlan plan = sink_bwd_plan(p);
+    const SinkBwdPlan plan = sink_bwd_plan(p, num_sms());
     const size_t rows = (size_t)p.B * p.H;
     size_t off = 0;
     w.S_pad = (p.S + 127) / 128 * 128;
@@ -907,7 +908,7 @@ SinkWs sink_ws(const SinkProblem& p, bool ckpt) {
 dfa_status sink_bwd(const SinkProblem& p, const void* q, const void* k, const void* v, const void* O, const float* lse,
                     const void* dO, const void* ckpt, void* dQ, void* dK, void* dV, char* ws, cudaStream_t s) {
     const SinkWs w = sink_ws(p, ckpt != nullptr);
-    const SinkBwdPlan plan = sink_bwd_plan(p);
+    const SinkBwdPlan plan = sink_bwd_plan(p, num_sms());
     float* delta = reinterpret_cast<float*>(ws + w.delta);
     float* nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
     float* dq = reinterpret_cast<float*>(ws + w.dq);
@@ -957,6 +958,18 @@ extern "C" dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void
 extern "C" size_t dfa_attn_bwd_sink_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink) {
     if (!sink_sizes_ok(B, H, H_kv, S, D, window, n_sink)) return 0;
     return sink_ws(sink_problem(B, H, H_kv, S, D, window, n_sink, 1.f), false).total;
+}
+
+extern "C" dfa_status dfa_debug_sink_bwd_plan(int B, int H, int H_kv, int S, int D, int window, int n_sink, int n_sms,
+                                              int32_t* plan) {
+    g_msg[0] = 0;
+    dfa_status st = check_sink(DFA_BF16, B, H, H_kv, S, D, window, n_sink, 1.f);
+    if (st || (st = check_sink_rows(B, H, S))) return st;
+    if (!plan || n_sms < 1) return fail(DFA_ERR_INVALID_ARG, "a plan needs a result and at least one SM");
+    const SinkBwdPlan x = sink_bwd_plan(sink_problem(B, H, H_kv, S, D, window, n_sink, 1.f), n_sms);
+    const int32_t out[8] = {x.grid, x.fine_ctas, x.n_items, x.pieces0 * x.rows, x.piece, x.cut_all, x.n_slabs, x.rows};
+    memcpy(plan, out, sizeof(out));
+    return DFA_OK;
 }
 
 extern "C" dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const void* O, const float* lse,

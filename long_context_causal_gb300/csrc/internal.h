@@ -143,7 +143,7 @@ struct SinkBwdPlan {
     int grid, fine_ctas;            // CTAs; those that take key tile 0, in the finer arithmetic
     uint16_t first[kPlanTiles + 1];
 };
-SinkBwdPlan sink_bwd_plan(const SinkProblem& p);
+SinkBwdPlan sink_bwd_plan(const SinkProblem& p, int sms);   // for a GPU with `sms` SMs
 
 dfa_status tc_sink_fwd(const SinkProblem& p, const void* q, const void* k, const void* v, void* O, float* lse,
                        cudaStream_t s);

@@ -89,6 +89,7 @@ def _load() -> ctypes.CDLL:
         "dfa_debug_mma": (i32, [i32, vp, vp, vp, vp]),
         "dfa_debug_cta_trace": (i32, [vp, i32]),
         "dfa_debug_wait_timeout": (i32, [vp, vp]),
+        "dfa_debug_sink_bwd_plan": (i32, [i32] * 8 + [p32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -538,6 +539,13 @@ def dfa_debug_wait_timeout(out=None, stream=None):
     """Launches the bounded-wait timeout kernel (out: optional int32 CUDA tensor of 2)."""
     _check(_lib.dfa_debug_wait_timeout(_ptr(out), _stream(stream)))
     return out
+
+
+def dfa_debug_sink_bwd_plan(B: int, H: int, H_kv: int, S: int, D: int, window: int, n_sink: int, n_sms: int) -> dict:
+    """Host-only: how dfa_attn_bwd_sink deals its work (include/dfa_debug.h)."""
+    plan = (ctypes.c_int32 * 8)()
+    _check(_lib.dfa_debug_sink_bwd_plan(B, H, H_kv, S, D, window, n_sink, n_sms, plan))
+    return dict(zip(("ctas", "fine_ctas", "items", "items0", "piece", "cut_all", "slabs", "rows"), plan))
 
 
 def dfa_check_errors(stream=None):

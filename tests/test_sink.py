@@ -183,6 +183,24 @@ def test_dv_of_the_sinks_tile(D, S, window):
     close(dV[:, :128], r[:, :128], tol[:, :128], "dV")
 
 
+def test_dv_of_the_sinks_tile_in_a_large_batch():
+    """As above with more lists of key tile 0 (40000) than 256 rounds of CTAs take: the arithmetic is the same."""
+    B, H, Hkv, S, D, window, n_sink = 5000, 8, 8, 130, 64, 100, 1
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=38)
+    u = torch.randn(Hkv, D, device=DEV, generator=torch.Generator(DEV).manual_seed(39))
+    q += (0.25 * u).bfloat16()
+    k[:, :n_sink] = (0.3 * k[:, :n_sink] + 1.5 * u).bfloat16()
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dQ, dK, dV = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink)
+    dfa.dfa_check_errors()
+    some = [0, 1, 2499, 4999]
+    args = [t[some] for t in (q, k, v, O, lse, do)]
+    check_bwd([t[some] for t in (dQ, dK, dV)], *args, window, n_sink)
+    r, terms, cancel, floor = sink.attn_bwd(*(np64(t) for t in args), window, n_sink)["dV"]
+    tol = (2.0 ** -16 + F) * terms + F2 * cancel + 2.0 ** -39 * floor + U * np.abs(r) + 1e-30
+    close(dV[some][:, :128], r[:, :128], tol[:, :128], "dV")
+
+
 def test_window_over_every_key_is_the_causal_call():
     q, k, v, do = make(2, 4, 2, 700, 128, torch.bfloat16, device=DEV, seed=34)
     O, lse = dfa.dfa_attn_fwd_sink(q, k, v, 700, 9)

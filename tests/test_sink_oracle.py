@@ -204,6 +204,29 @@ def test_an_empty_batch_needs_no_workspace(B, S, n_sink):
     assert dfa.dfa_attn_bwd_ckpt8_workspace_size(B, 4, 2, S, 64, 64, n_sink) == 0
 
 
+@pytest.mark.parametrize("n_sms", [1, 16, 152])
+@pytest.mark.parametrize("B,H,Hkv,S,D,window,n_sink", [
+    (1, 1, 1, 1, 64, 1, 1), (1, 8, 2, 1500, 128, 1500, 4), (2, 8, 4, 777, 64, 200, 8), (1, 32, 8, 32768, 128, 4096, 4),
+    # more key tiles 0 than rounds were once looked at: 40000 of them, lists of one and of two tiles and longer
+    (5000, 8, 8, 200, 128, 200, 4), (5000, 8, 8, 200, 128, 100, 4), (2400, 16, 16, 300, 128, 100, 4), (8000, 16, 8, 147, 64, 21, 128),
+    (2071, 16, 2, 16205, 128, 14, 33), (6000, 16, 16, 129, 64, 1, 1),
+])
+def test_the_sinks_tile_always_has_ctas_of_its_own(B, H, Hkv, S, D, window, n_sink, n_sms):
+    """The finer arithmetic of key tile 0 does not depend on how large the batch is."""
+    p = dfa.dfa_debug_sink_bwd_plan(B, H, Hkv, S, D, window, n_sink, n_sms)
+    assert p["rows"] == B * Hkv and p["items0"] >= p["rows"]
+    assert 1 <= p["fine_ctas"] <= min(p["ctas"], p["items0"]) and p["ctas"] <= max(n_sms, 2)
+    assert (p["ctas"] > p["fine_ctas"]) == (p["items"] > p["items0"])        # someone takes the others
+    assert dfa.dfa_debug_sink_bwd_plan(B, H, Hkv, S, D, window, 0, n_sms)["fine_ctas"] == 0
+
+
+def test_plan_refusals():
+    plan = (ctypes.c_int32 * 8)()
+    for bad in ((1, 4, 2, 300, 96, 64, 4, 152), (1, 4, 2, 300, 64, 0, 4, 152), (1, 4, 2, 300, 64, 64, 4, 0)):
+        assert lib.dfa_debug_sink_bwd_plan(*bad, plan) != dfa.DFA_OK and dfa.dfa_last_error()
+    assert lib.dfa_debug_sink_bwd_plan(1, 4, 2, 300, 64, 64, 4, 152, None) == dfa.DFA_ERR_INVALID_ARG
+
+
 def test_the_binding_refuses_tensors_it_must_not_hand_on():
     t = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
     q, k, lse = t(1, 8, 4, 64), t(1, 8, 2, 64), t(1, 4, 8, dtype=torch.float32)
