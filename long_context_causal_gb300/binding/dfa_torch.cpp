@@ -121,18 +121,13 @@ at::Tensor given(PyObject* o, const char* name, at::IntArrayRef shape, at::Scala
     return t;
 }
 
-at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
-    if (o != Py_None) return given(o, name, shape, type, dev);
-    const NoGil released;
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-}
-
 struct Stream {
     void* handle;
     bool other;      // not the current one
 };
 Stream stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return Stream{c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(), false};
+    void* const now = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+    if (o == Py_None) return Stream{now, false};
     PyObject* n = nullptr;
     if (PyLong_Check(o)) {
         n = o;
@@ -144,11 +139,44 @@ Stream stream_of(PyObject* o, int dev) {
     void* h = PyLong_AsVoidPtr(n);
     Py_DECREF(n);
     if (PyErr_Occurred()) throw Raised{};
-    return Stream{h, true};
+    return Stream{h, h != now};
 }
 
-// A caller's byte buffer, or one for this call alone, owned by the stream the
-// call runs on: the allocator then reuses it only behind the call's kernels.
+c10::cuda::CUDAStream torch_stream(const Stream& s, const at::Device& dev) {
+    return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s.handle), dev.index());
+}
+
+// A new tensor is owned by the stream the call runs on: the allocator hands out
+// its memory again only behind the call's kernels, and took it from no work that
+// another stream has still to do.
+at::Tensor allocate(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev, const Stream& s) {
+    const auto opt = at::TensorOptions().dtype(type).device(dev);
+    const NoGil released;
+    if (!s.other) return at::empty(shape, opt);
+    c10::cuda::CUDAStreamGuard guard(torch_stream(s, dev));
+    return at::empty(shape, opt);
+}
+
+// An output made here is the caller's, who uses it on the current stream: that
+// is waited for as well before its memory is handed out again.
+at::Tensor result(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev, const Stream& s) {
+    at::Tensor t = allocate(shape, type, dev, s);
+    if (s.other) t.record_stream(c10::cuda::getCurrentCUDAStream(dev.index()));
+    return t;
+}
+at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev,
+                  const Stream& s) {
+    return o == Py_None ? result(shape, type, dev, s) : given(o, name, shape, type, dev);
+}
+
+// The caller may drop a tensor as soon as the call returns, and another stream
+// than its own may still use it then.
+void hold(const Stream& s, std::initializer_list<const at::Tensor*> ts) {
+    if (!s.other) return;
+    for (const at::Tensor* t : ts) t->record_stream(torch_stream(s, t->device()));
+}
+
+// A caller's byte buffer, or one for this call.
 at::Tensor bytes(PyObject* o, const char* name, size_t n, const at::Device& dev, const Stream& s) {
     if (o != Py_None) {
         const at::Tensor& t = tensor(o, name);
@@ -156,12 +184,7 @@ at::Tensor bytes(PyObject* o, const char* name, size_t n, const at::Device& dev,
             throw ValueErr{std::string(name) + " must be a contiguous uint8 tensor on " + dev.str()};
         return t;
     }
-    const auto opt = at::TensorOptions().dtype(at::kByte).device(dev);
-    const int64_t size = n ? (int64_t)n : 16;
-    const NoGil released;
-    if (!s.other) return at::empty({size}, opt);
-    c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s.handle), dev.index()));
-    return at::empty({size}, opt);
+    return allocate({n ? (int64_t)n : 16}, at::kByte, dev, s);
 }
 
 struct Sequence {
@@ -197,9 +220,10 @@ PyObject* fwd(PyObject* const* a) {
     const Sequence z = sequence(q, k, v);
     const int d = on_gpu({&q, &k, &v});
     const at::Device dev = q.device();
-    at::Tensor O = output(a[6], "O", q.sizes(), q.scalar_type(), dev);
-    at::Tensor lse = output(a[7], "lse", {z.B, z.H, z.S}, at::kFloat, dev);
     const Stream s = stream_of(a[8], d);
+    at::Tensor O = output(a[6], "O", q.sizes(), q.scalar_type(), dev, s);
+    at::Tensor lse = output(a[7], "lse", {z.B, z.H, z.S}, at::kFloat, dev, s);
+    hold(s, {&q, &k, &v, &O, &lse});
     const int window = number(a[3], "window"), n_sink = number(a[4], "n_sink");
     const dfa_status st = without_gil(g.fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), z.B, z.H, z.Hkv, z.S,
                                       z.D, window, n_sink, scale_of(a[5], z.D), O.data_ptr(),
@@ -217,12 +241,13 @@ PyObject* bwd(PyObject* const* a) {
     const at::Tensor lse = given(a[4], "lse", {z.B, z.H, z.S}, at::kFloat, dev);
     const at::Tensor dO = given(a[5], "dO", q.sizes(), type, dev);
     const int window = number(a[6], "window"), n_sink = number(a[7], "n_sink");
-    at::Tensor dQ = output(a[9], "dQ", q.sizes(), type, dev);
-    at::Tensor dK = output(a[10], "dK", k.sizes(), type, dev);
-    at::Tensor dV = output(a[11], "dV", k.sizes(), type, dev);
     const Stream s = stream_of(a[13], d);
+    at::Tensor dQ = output(a[9], "dQ", q.sizes(), type, dev, s);
+    at::Tensor dK = output(a[10], "dK", k.sizes(), type, dev, s);
+    at::Tensor dV = output(a[11], "dV", k.sizes(), type, dev, s);
     const at::Tensor ws = bytes(a[12], "workspace_buf",
                                 a[12] == Py_None ? g.bwd_bytes(z.B, z.H, z.Hkv, z.S, z.D, window, n_sink) : 0, dev, s);
+    hold(s, {&q, &k, &v, &O, &lse, &dO, &dQ, &dK, &dV, &ws});
     const dfa_status st = without_gil(g.bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(),
                                       static_cast<const float*>(lse.data_ptr()), dO.data_ptr(), dtype_of(q), z.B, z.H,
                                       z.Hkv, z.S, z.D, window, n_sink, scale_of(a[8], z.D), dQ.data_ptr(), dK.data_ptr(),
@@ -244,10 +269,11 @@ PyObject* decode(PyObject* const* a) {
     const at::Device dev = q.device();
     const int B = small(q.size(0)), H = small(q.size(1)), D = small(q.size(2)), S = small(k.size(1)), Hkv = small(k.size(2));
     const at::Tensor len = given(a[3], "kv_len", {B}, at::kInt, dev);
-    at::Tensor O = output(a[7], "O", q.sizes(), q.scalar_type(), dev);
-    at::Tensor lse = output(a[8], "lse", {B, H}, at::kFloat, dev);
     const Stream s = stream_of(a[10], d);
+    at::Tensor O = output(a[7], "O", q.sizes(), q.scalar_type(), dev, s);
+    at::Tensor lse = output(a[8], "lse", {B, H}, at::kFloat, dev, s);
     const at::Tensor ws = bytes(a[9], "workspace_buf", a[9] == Py_None ? g.decode_bytes(B, H, Hkv, D) : 0, dev, s);
+    hold(s, {&q, &k, &v, &len, &O, &lse, &ws});
     const int64_t strides[3] = {k.stride(0), k.stride(1), k.stride(2)};
     const dfa_status st = without_gil(g.decode, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), B, H, Hkv, S, D,
                                       static_cast<const int64_t*>(strides), static_cast<const int32_t*>(len.data_ptr()),
@@ -262,10 +288,10 @@ PyObject* save(PyObject* const* a) {
     const int d = on_gpu({&q, &k, &v});
     const at::Device dev = q.device();
     const at::Tensor O = given(a[3], "O", q.sizes(), q.scalar_type(), dev);
-    // An output: the caller's stream or the current one, as the other outputs.
-    at::Tensor ckpt = a[4] == Py_None ? output(Py_None, "ckpt", {(int64_t)g.ckpt_bytes(z.B, z.H, z.Hkv, z.S, z.D)}, at::kByte, dev)
-                                      : bytes(a[4], "ckpt", 0, dev, Stream{});
     const Stream s = stream_of(a[5], d);
+    at::Tensor ckpt = a[4] == Py_None ? result({(int64_t)g.ckpt_bytes(z.B, z.H, z.Hkv, z.S, z.D)}, at::kByte, dev, s)
+                                      : bytes(a[4], "ckpt", 0, dev, s);
+    hold(s, {&q, &k, &v, &O, &ckpt});
     const dfa_status st = without_gil(g.save, q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), dtype_of(q), z.B, z.H,
                                       z.Hkv, z.S, z.D, ckpt.data_ptr(), (size_t)ckpt.numel(), s.handle);
     return st ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(ckpt));
@@ -275,15 +301,16 @@ PyObject* restore(PyObject* const* a) {
     const at::Tensor& given_ckpt = tensor(a[0], "ckpt");
     const int d = on_gpu({&given_ckpt});
     const at::Device dev = given_ckpt.device();
-    const at::Tensor ckpt = bytes(a[0], "ckpt", 0, dev, Stream{});
+    const Stream s = stream_of(a[10], d);
+    const at::Tensor ckpt = bytes(a[0], "ckpt", 0, dev, s);
     const int B = number(a[1], "B"), H = number(a[2], "H"), Hkv = number(a[3], "H_kv"), S = number(a[4], "S"),
               D = number(a[5], "D");
     if (B < 0 || H < 0 || Hkv < 0 || S < 0 || D < 0) throw ValueErr{"sizes must not be negative"};
-    at::Tensor q = output(a[6], "q", {B, S, H, D}, at::kBFloat16, dev);
-    at::Tensor k = output(a[7], "k", {B, S, Hkv, D}, at::kBFloat16, dev);
-    at::Tensor v = output(a[8], "v", {B, S, Hkv, D}, at::kBFloat16, dev);
-    at::Tensor O = output(a[9], "O", {B, S, H, D}, at::kBFloat16, dev);
-    const Stream s = stream_of(a[10], d);
+    at::Tensor q = output(a[6], "q", {B, S, H, D}, at::kBFloat16, dev, s);
+    at::Tensor k = output(a[7], "k", {B, S, Hkv, D}, at::kBFloat16, dev, s);
+    at::Tensor v = output(a[8], "v", {B, S, Hkv, D}, at::kBFloat16, dev, s);
+    at::Tensor O = output(a[9], "O", {B, S, H, D}, at::kBFloat16, dev, s);
+    hold(s, {&ckpt, &q, &k, &v, &O});
     const dfa_status st = without_gil(g.restore, ckpt.data_ptr(), (size_t)ckpt.numel(), DFA_BF16, B, H, Hkv, S, D,
                                       q.data_ptr(), k.data_ptr(), v.data_ptr(), O.data_ptr(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(q), std::move(k), std::move(v), std::move(O)});
@@ -295,18 +322,19 @@ PyObject* bwd_ckpt(PyObject* const* a) {
         throw ValueErr{"dO must be a contiguous [B, S, H, D] tensor, got " + shape_of(dO)};
     const int d = on_gpu({&dO, &ck});
     const at::Device dev = dO.device();
-    const at::Tensor ckpt = bytes(a[0], "ckpt", 0, dev, Stream{});
+    const Stream s = stream_of(a[11], d);
+    const at::Tensor ckpt = bytes(a[0], "ckpt", 0, dev, s);
     const int B = small(dO.size(0)), S = small(dO.size(1)), H = small(dO.size(2)), D = small(dO.size(3));
     const int Hkv = number(a[3], "H_kv");
     if (Hkv < 0) throw ValueErr{"H_kv must not be negative"};
     const at::Tensor lse = given(a[1], "lse", {B, H, S}, at::kFloat, dev);
     const int window = a[4] == Py_None ? std::max(S, 1) : number(a[4], "window"), n_sink = number(a[5], "n_sink");
-    at::Tensor dQ = output(a[7], "dQ", dO.sizes(), dO.scalar_type(), dev);
-    at::Tensor dK = output(a[8], "dK", {B, S, Hkv, D}, dO.scalar_type(), dev);
-    at::Tensor dV = output(a[9], "dV", {B, S, Hkv, D}, dO.scalar_type(), dev);
-    const Stream s = stream_of(a[11], d);
+    at::Tensor dQ = output(a[7], "dQ", dO.sizes(), dO.scalar_type(), dev, s);
+    at::Tensor dK = output(a[8], "dK", {B, S, Hkv, D}, dO.scalar_type(), dev, s);
+    at::Tensor dV = output(a[9], "dV", {B, S, Hkv, D}, dO.scalar_type(), dev, s);
     const at::Tensor ws = bytes(a[10], "workspace_buf",
                                 a[10] == Py_None ? g.bwd_ckpt_bytes(B, H, Hkv, S, D, window, n_sink) : 0, dev, s);
+    hold(s, {&ckpt, &lse, &dO, &dQ, &dK, &dV, &ws});
     const dfa_status st = without_gil(g.bwd_ckpt, ckpt.data_ptr(), (size_t)ckpt.numel(),
                                       static_cast<const float*>(lse.data_ptr()), dO.data_ptr(), dtype_of(dO), B, H, Hkv, S, D,
                                       window, n_sink, scale_of(a[6], D), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),

@@ -435,7 +435,10 @@ def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: f
 # Marshalled in C++ (binding/dfa_torch.cpp): reading and checking tensors and
 # allocating outputs from Python costs several times what a short call runs for
 # on the GPU.  The functions there check every tensor and either return the
-# results or the library's status.
+# results or the library's status.  With `stream`, outputs and workspaces are
+# allocated on that stream and every tensor of the call is recorded on it, so
+# the caller may drop them before the stream has come that far; as with any
+# stream, it is for the caller to have it wait for what the inputs come from.
 def _load_native():
     try:
         from long_context_causal_gb300 import _dfa_torch as native

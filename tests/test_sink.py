@@ -517,6 +517,60 @@ def test_another_stream_and_two_at_once():
     same_step(got, want[0])
 
 
+DELAY = 40_000_000      # cycles, about 20 ms: longer than what the host does meanwhile
+
+
+def test_memory_of_calls_on_another_stream():
+    """A call on another stream may not write memory that the current one has still to write, nor read or leave
+    memory that the current one takes again when the caller drops a tensor."""
+    W, N, Hkv = 150, 3, 2
+    q, k, v, do = make(1, 4, Hkv, 1100, 64, torch.bfloat16, device=DEV, seed=59)
+    lens, q1 = torch.full((1,), 900, dtype=torch.int32, device=DEV), q[:, 899].contiguous()
+
+    def chain(stream=None):
+        out = step(q, k, v, do, W, N, stream=stream)
+        ckpt = dfa.dfa_ckpt8_save(q, k, v, out[0], stream=stream)
+        return out + dfa.dfa_ckpt8_restore(ckpt, 1, 4, Hkv, 1100, 64, stream=stream) + \
+            dfa.dfa_attn_decode_sink(q1, k, v, lens, W, N, stream=stream)
+
+    want, now, s = chain(), torch.cuda.current_stream(), torch.cuda.Stream()
+    other = q.flip(1).contiguous()
+    for _ in range(3):
+        # outputs: blocks of their sizes that the current stream is about to fill
+        torch.cuda.synchronize()
+        blocks = [torch.empty_like(t) for t in want]
+        torch.cuda._sleep(DELAY)
+        for t in blocks:
+            t.fill_(7)
+        del blocks
+        got = chain(s)
+        torch.cuda.synchronize()
+        same_step(got[:8], want[:8])
+        assert all(torch.equal(a, b) for a, b in zip(got[8:], want[8:]))
+        # inputs that are dropped while the other stream has still to read them
+        ckpt = dfa.dfa_ckpt8_save(q, k, v, want[0])
+        rest = [t.clone() for t in (want[1], do)]
+        s.wait_stream(now)
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(DELAY)
+        got = dfa.dfa_attn_bwd_ckpt8(ckpt, *rest, Hkv, W, N, stream=s)
+        sizes = [torch.empty_like(t, device="meta") for t in (ckpt, *rest)]
+        del ckpt, rest
+        blocks = [torch.full_like(t, 1, device=DEV) for t in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(got[1], want[6]) and torch.equal(got[2], want[7])
+        # an output that is dropped while the current stream has still to read it
+        O, lse = dfa.dfa_attn_fwd_sink(q, k, v, W, N, stream=s)
+        s.synchronize()
+        torch.cuda._sleep(DELAY)
+        seen = O.clone()
+        del O, lse
+        dfa.dfa_attn_fwd_sink(other, k, v, W, N, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(seen, want[0])
+    dfa.dfa_check_errors()
+
+
 def test_tensors_on_the_wrong_place_are_refused():
     q, k, v, do = make(1, 2, 1, 64, 64, torch.bfloat16, device=DEV, seed=57)
     with pytest.raises(ValueError, match="CUDA"):
