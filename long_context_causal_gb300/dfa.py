@@ -11,6 +11,8 @@ importing this module fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import re
 
@@ -128,6 +130,42 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _on_its_stream(call):
+    """A call on another stream than the current one allocates (and zeroes) its
+    outputs and workspace on that stream, and its tensors are recorded there:
+    their memory is handed out again only behind the call's kernels, even if the
+    caller drops them at once.  An output made here is recorded on the current
+    stream as well, where the caller uses it."""
+    sig = inspect.signature(call)
+    at = list(sig.parameters).index("stream")
+
+    @functools.wraps(call)
+    def wrapped(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        now = torch.cuda.current_stream()
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        if stream.cuda_stream == now.cuda_stream:
+            return call(*args, **kw)
+        bound = sig.bind(*args, **kw)
+        if "cu_seqlens" in bound.arguments:      # offsets on the GPU are read on the current stream
+            bound.arguments["cu_seqlens"] = _cu_host(bound.arguments["cu_seqlens"])
+        with torch.cuda.stream(stream):
+            out = call(*bound.args, **bound.kwargs)
+        given = [t for t in bound.arguments.values() if isinstance(t, torch.Tensor)]
+        for t in given:
+            if t.is_cuda:
+                t.record_stream(stream)
+        for t in out:
+            if not any(t is g for g in given):
+                t.record_stream(now)
+        return out
+
+    return wrapped
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return DFA_F32
@@ -166,6 +204,7 @@ def _inputs(q, k, v, *rest):
 
 
 # ---------------------------------------------------------------- entry points
+@_on_its_stream
 def dfa_chunk_attn_fwd(q, k, v, q_offset: int = 0, kv_offset: int = 0, causal: bool = True,
                        scale: float | None = None, O_partial=None, lse=None, stream=None):
     """One chunk step: returns (O_partial fp32 [B,Lq,H,D], lse fp32 [B,H,Lq])."""
@@ -195,6 +234,7 @@ def dfa_chunk_bwd_workspace_size(B, H, H_kv, Lq, Lkv, D) -> int:
     return int(_lib.dfa_chunk_bwd_workspace_size(B, H, H_kv, Lq, Lkv, D))
 
 
+@_on_its_stream
 def dfa_chunk_attn_bwd(q, k, v, O, lse, dO, q_offset: int = 0, kv_offset: int = 0, causal: bool = True,
                        scale: float | None = None, dQ_acc=None, dK_acc=None, dV_acc=None,
                        workspace_buf=None, stream=None):
@@ -227,6 +267,7 @@ def dfa_chunk_attn_bwd(q, k, v, O, lse, dO, q_offset: int = 0, kv_offset: int = 
     return dQ_acc, dK_acc, dV_acc
 
 
+@_on_its_stream
 def dfa_merge_partials(O_a, lse_a, O_b, lse_b, O_out=None, lse_out=None, stream=None):
     """Rescale-and-merge; O_out/lse_out may alias the inputs."""
     B, L, H, D = O_a.shape
@@ -254,6 +295,7 @@ def workspace(B, H, H_kv, S, D, n_chunks, bwd, device="cuda"):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def dfa_attn_fwd(q, k, v, n_chunks: int = 1, causal: bool = True, scale: float | None = None,
                  sched="balanced", O=None, lse=None, workspace_buf=None, stream=None):
     """Whole-sequence forward: returns (O [B,S,H,D] in q's dtype, lse fp32 [B,H,S])."""
@@ -303,6 +345,7 @@ def varlen_workspace(cu_seqlens, H, H_kv, D, bwd, device="cuda"):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def dfa_attn_fwd_varlen(q, k, v, cu_seqlens, causal: bool = True, scale: float | None = None, O=None, lse=None,
                         workspace_buf=None, stream=None):
     """Packed batch forward: q [T,H,D], k, v [T,H_kv,D]; returns (O [T,H,D], lse fp32 [H,T])."""
@@ -324,6 +367,7 @@ def dfa_attn_fwd_varlen(q, k, v, cu_seqlens, causal: bool = True, scale: float |
     return O, lse
 
 
+@_on_its_stream
 def dfa_attn_bwd_varlen(q, k, v, O, lse, dO, cu_seqlens, causal: bool = True, scale: float | None = None,
                         dQ=None, dK=None, dV=None, workspace_buf=None, stream=None):
     """Packed batch backward from the saved (O, lse): returns (dQ, dK, dV)."""
@@ -348,6 +392,7 @@ def dfa_attn_bwd_varlen(q, k, v, O, lse, dO, cu_seqlens, causal: bool = True, sc
     return dQ, dK, dV
 
 
+@_on_its_stream
 def dfa_attn_fwd_noalloc(q, k, v, O, lse, n_chunks: int = 1, causal: bool = True,
                          scale: float | None = None, sched="balanced", stream=None):
     """dfa_attn_fwd without a workspace: writes the caller's O and lse, allocates nothing."""
@@ -365,6 +410,7 @@ def dfa_attn_fwd_noalloc(q, k, v, O, lse, n_chunks: int = 1, causal: bool = True
     return O, lse
 
 
+@_on_its_stream
 def dfa_attn_bwd(q, k, v, O, lse, dO, n_chunks: int = 1, causal: bool = True,
                  scale: float | None = None, sched="balanced", dQ=None, dK=None, dV=None,
                  workspace_buf=None, stream=None):
@@ -388,6 +434,7 @@ def dfa_attn_bwd(q, k, v, O, lse, dO, n_chunks: int = 1, causal: bool = True,
     return dQ, dK, dV
 
 
+@_on_its_stream
 def dfa_attn_fwd_local(q, k, v, n_chunks: int, window: int, scale: float | None = None, sched="balanced",
                        O=None, lse=None, workspace_buf=None, stream=None):
     """Causal forward restricted to a local window of `window` chunks
@@ -409,6 +456,7 @@ def dfa_attn_fwd_local(q, k, v, n_chunks: int, window: int, scale: float | None 
     return O, lse
 
 
+@_on_its_stream
 def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: float | None = None,
                        sched="balanced", dQ=None, dK=None, dV=None, workspace_buf=None, stream=None):
     """Backward of dfa_attn_fwd_local from the saved (O, lse): returns (dQ, dK, dV)."""
