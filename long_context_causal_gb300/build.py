@@ -21,6 +21,7 @@ BUILD = os.path.join(os.path.dirname(PKG), "_build")
 LIB = os.path.join(PKG, "libdfa.so")
 BINDING = os.path.join(PKG, "binding", "dfa_torch.cpp")
 BINDING_LIB = os.path.join(PKG, "_dfa_torch.so")
+BINDING_KEY = os.path.join(BUILD, "dfa_torch.key")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -56,15 +57,8 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING_LIB):
-        return False
-    t = os.path.getmtime(BINDING_LIB)
-    return all(os.path.getmtime(d) <= t for d in [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")))
-
-
-def build_binding() -> str:
-    """The extension module, by the host compiler against the torch that runs."""
+def _binding_command() -> list[str]:
+    """The host compiler's command against the torch that runs, without the output."""
     import sysconfig
 
     import torch
@@ -72,15 +66,42 @@ def build_binding() -> str:
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] +
+            ["-isystem" + i for i in include] + [BINDING, "-L" + os.path.join(root, "lib")] +
+            ["-l" + x for x in ("torch_python", "torch", "torch_cpu", "c10", "c10_cuda")])
+
+
+def _binding_key() -> str:
+    """What the module is built against: it fits no other torch or Python."""
+    import sys
+
+    import torch
+    return "\n".join([f"torch {torch.__version__}", f"python {sys.version}", *_binding_command()])
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_LIB) or not os.path.exists(BINDING_KEY):
+        return False
+    t = os.path.getmtime(BINDING_LIB)
+    if any(os.path.getmtime(d) > t for d in [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return False
+    with open(BINDING_KEY) as f:
+        return f.read() == _binding_key()
+
+
+def build_binding() -> str:
+    """The extension module, and beside the objects what it was built against."""
     tmp = BINDING_LIB + f".tmp{os.getpid()}"
-    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] +
-           ["-isystem" + i for i in include] + [BINDING, "-o", tmp, "-L" + os.path.join(root, "lib")] +
-           ["-l" + x for x in ("torch_python", "torch", "torch_cpu", "c10", "c10_cuda")])
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = subprocess.run(_binding_command() + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(BINDING)}:\n{r.stdout}\n{r.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(BINDING_KEY):
+        os.remove(BINDING_KEY)
     os.replace(tmp, BINDING_LIB)
+    with open(BINDING_KEY, "w") as f:
+        f.write(_binding_key())
     return BINDING_LIB
 
 

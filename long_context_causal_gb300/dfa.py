@@ -487,20 +487,25 @@ def dfa_attn_bwd_local(q, k, v, O, lse, dO, n_chunks: int, window: int, scale: f
 # allocated on that stream and every tensor of the call is recorded on it, so
 # the caller may drop them before the stream has come that far; as with any
 # stream, it is for the caller to have it wait for what the inputs come from.
-def _load_native():
-    try:
-        from long_context_causal_gb300 import _dfa_torch as native
-    except ImportError as e:
-        raise ImportError("the extension module _dfa_torch is not built for this torch: run "
-                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
-    native.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
-        "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
-        "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
-        "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size")))
-    return native
+class _Native:
+    """The extension module, loaded by the first call that needs it: the entry
+    points that go through ctypes do not depend on it."""
+
+    def __getattr__(self, name):
+        try:
+            from long_context_causal_gb300 import _dfa_torch as native
+        except ImportError as e:
+            raise ImportError("the extension module _dfa_torch is not built for this torch: run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        native.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+            "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
+            "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
+            "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size")))
+        vars(self).update((n, f) for n, f in vars(native).items() if not n.startswith("__"))
+        return getattr(native, name)
 
 
-_native = _load_native()
+_native = _Native()
 
 
 def _result(r):
