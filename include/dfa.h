@@ -250,7 +250,10 @@ dfa_status dfa_attn_fwd_sink(const void* q, const void* k, const void* v, dfa_dt
 size_t dfa_attn_bwd_sink_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);
 /* Its backward from the saved O and lse, never re-running the forward:
  * P_ij = exp(s_ij - lse_i) on the visible pairs, Delta_i = <dO_i, O_i>, and
- * dQ, dK, dV as dfa_attn_bwd.  workspace: caller-owned, 16-byte aligned. */
+ * dQ, dK, dV as dfa_attn_bwd.  lse is the forward's of these q and k, with
+ * which P <= 1 but for rounding: for dQ and dK, P is held in fp16 and counts as
+ * at most 65504 / 2^14 (3.998), whatever a smaller lse makes of it; dV takes it
+ * as it is.  workspace: caller-owned, 16-byte aligned. */
 dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const void* O, const float* lse,
                              const void* dO, dfa_dtype dt, int B, int H, int H_kv, int S, int D, int window,
                              int n_sink, float scale, void* dQ, void* dK, void* dV, void* workspace,
@@ -300,7 +303,8 @@ dfa_status dfa_ckpt8_restore(const void* ckpt, size_t ckpt_bytes, dfa_dtype dt, 
  * the forward (window >= S, n_sink = 0: plain causal attention, the backward
  * of dfa_attn_fwd).  lse is the forward's, of the tensors before they were
  * rounded, so P_ij = exp(s_ij - lse_i) carries the rounding of q and k and can
- * exceed 1; above 255 (a score that the rounding moved by 5.5) it counts as 255.
+ * exceed 1; for dQ and dK it counts as at most 65504 / 2^8 (255.9, a score that
+ * the rounding moved by 5.5), dV takes it as it is.
  * Arguments, errors and reproducibility as dfa_attn_bwd_sink; the workspace
  * also holds the restored q, k and v for the length of the call. */
 size_t dfa_attn_bwd_ckpt8_workspace_size(int B, int H, int H_kv, int S, int D, int window, int n_sink);

@@ -48,12 +48,13 @@ def attn_fwd(q, k, v, window, n_sink, scale=None):
     return O, lse, size
 
 
-def attn_bwd(q, k, v, O, lse, dO, window, n_sink, scale=None):
+def attn_bwd(q, k, v, O, lse, dO, window, n_sink, scale=None, most=np.inf):
     """Gradients from the given O and lse: {"dQ": (value, terms, cancel, floor), ...}.
     `terms` sums |dS| |k|, |dS| |q| or P |dO|; `cancel` sums P (|dO| |v|^T +
     |dO| |O|) |k| (or |q|): what dO v^T - Delta is the difference of (0 for dV);
     `floor` is `cancel` with P = 1 on every visible pair: what an absolute error
-    of P moves the result by."""
+    of P moves the result by.  `most`: what P counts as at most in dS (with the
+    forward's lse it is 1 at most)."""
     q, k, v, O, lse, dO = (np.asarray(t, dtype=np.float64) for t in (q, k, v, O, lse, dO))
     B, S, H, D = q.shape
     G = H // k.shape[2]
@@ -65,14 +66,15 @@ def attn_bwd(q, k, v, O, lse, dO, window, n_sink, scale=None):
             g = h // G
             qh, kh, vh, oh, dh = q[b, :, h], k[b, :, g], v[b, :, g], O[b, :, h], dO[b, :, h]
             p = np.where(see, np.exp(_scores(q[b], k[b], h, scale) - lse[b, h][:, None]), 0.0)
+            pv, p = p, np.minimum(p, most)
             ds = p * (dh @ vh.T - (dh * oh).sum(1, keepdims=True)) * scale
             f = see * (np.abs(dh) @ np.abs(vh).T + (np.abs(dh) * np.abs(oh)).sum(1, keepdims=True)) * scale
             for z, w in enumerate((ds, np.abs(ds), p * f, f)):
                 kk, qq = (kh, qh) if z == 0 else (np.abs(kh), np.abs(qh))
                 out["dQ"][z][b, :, h] += w @ kk
                 out["dK"][z][b, :, g] += w.T @ qq
-            out["dV"][0][b, :, g] += p.T @ dh
-            out["dV"][1][b, :, g] += p.T @ np.abs(dh)
+            out["dV"][0][b, :, g] += pv.T @ dh
+            out["dV"][1][b, :, g] += pv.T @ np.abs(dh)
     return out
 
 

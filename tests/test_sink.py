@@ -243,6 +243,28 @@ def test_bits_repeat_and_neighbours_stay(D):
         torch.testing.assert_close(r[2].float(), runs[0][2].float(), rtol=2 * U, atol=1e-3)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_sink", [0, 4])
+@pytest.mark.parametrize("down", [np.log(3), np.log(8), np.log(2000)])
+def test_where_p_saturates(D, n_sink, down):
+    """An lse lower than the forward's, as the call says it: dQ and dK take P as 65504 / 2^14 at most (from a
+    checkpoint 65504 / 2^8), dV as it is."""
+    B, H, Hkv, S, window = 1, 4, 2, 300, 70
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=46)
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    lse[:, :, 10:200:3] -= down
+    args = [np64(t) for t in (q, k, v, O)]
+    for grads, args, shift in (
+            (dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink), args, 14),
+            (dfa.dfa_attn_bwd_ckpt8(dfa.dfa_ckpt8_save(q, k, v, O), lse, do, Hkv, window, n_sink), [sink.ckpt8(t) for t in args], 8)):
+        ref = sink.attn_bwd(*args, np64(lse), np64(do), window, n_sink, most=65504 / 2 ** shift)
+        for got, name in zip(grads, ("dQ", "dK", "dV")):
+            r, terms, cancel, floor = ref[name]
+            close(got, r, ((1 if name == "dV" else 2) * U + F) * terms + F2 * cancel + 2.0 ** (-25 - shift) * floor
+                  + U * np.abs(r) + 1e-30, name)
+    dfa.dfa_check_errors()
+
+
 # ------------------------------------------------------------------------------------------------ checkpoints
 @pytest.mark.parametrize("B,H,Hkv,S,D", [(1, 1, 1, 1, 64), (1, 3, 1, 1, 128), (2, 4, 2, 129, 128), (1, 8, 8, 501, 64),
                                          (3, 6, 3, 77, 128)])
