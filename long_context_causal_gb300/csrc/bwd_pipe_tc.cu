@@ -187,7 +187,10 @@ __device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
 // to dQ as two bf16 numbers, dS and what its rounding lost (the rest), each an
 // MMA.  dV of its keys, the longest sums of all, takes P the same way: with P
 // rounded once an element of a sink's dV, whose terms cancelled, was off by half of
-// dV's rms (5013 tokens, causal, 1 sink; 0.02 of it now, at no cost).  FINE tiles have CTAs of their own, which run a second copy of the roles:
+// dV's rms (5013 tokens, causal, 1 sink; 0.02 of it now, at no cost).  And dK of its keys takes dS
+// with its rest (the worst element of a sink's dK, beside the result's rounding: 0.055 of dK's
+// rms without, 0.006 with it; 159 us from 156 there, no difference at 32K tokens).
+// FINE tiles have CTAs of their own, which run a second copy of the roles:
 // in one copy the extra code slowed every tile by 2%.  The rest's 32 KB of
 // shared memory come from the second dO slot (HD = 128, whose dO ring is then
 // one deep) or from the halves that HD = 64 leaves free in the K and V tiles.
@@ -482,7 +485,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
         const SDesc dQk = desc(sQ, 16), dQn = desc(sQ, 16384);
         const SDesc dOk = desc(sdO, 16), dOn = desc(sdO, 16384);
         const SDesc dSk = desc(sdS, 16), dSn = desc(sdS, 16384);
-        const SDesc dRn = desc(smem + kOffRest, kRestStep);
+        const SDesc dRn = desc(smem + kOffRest, kRestStep), dRk = desc(smem + kOffRest, 16);
         constexpr uint32_t kSlot = kTile >> 4, kRows16 = 2048 >> 4;
         auto kmaj = [](int kk) -> uint32_t { return (uint32_t)(((kk / 4) * 16384 + (kk % 4) * 32) >> 4); };
         uint32_t n = 0, kvi = 0;
@@ -562,6 +565,12 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
                         ss(tm + kColDKt, dSk + kmaj(kk), bq + kk * kRows16, idKM, kk > 0 ? 1u : acc0);
+                    if constexpr (FINE) {   // dK += (what dS^T's rounding lost) Q
+#pragma unroll
+                        for (int kk = 0; kk < BT / 16; ++kk)
+                            ss(tm + kColDKt, dRk + (uint32_t)(((kk / 4) * kRestStep + (kk % 4) * 32) >> 4),
+                               bq + kk * kRows16, idKM, 1u);
+                    }
                 }
                 commit(&q_empty[s]);
                 if (!more) {

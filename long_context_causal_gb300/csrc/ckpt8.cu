@@ -394,7 +394,7 @@ dfa_status launch_sink_finish(const SinkProblem& p, const SinkBwdPlan& plan, con
 }
 
 // The time of a plan is estimated in query tiles (about 2.4 us): an item costs
-// its tiles (FINE ones kFine each) and kItem more (loads, pipeline fill,
+// its tiles (FINE ones kFine each; 1.6 and 1.9 give the same times to 1%, 2.2 up to 7% more) and kItem more (loads, pipeline fill,
 // epilogue); a CTA has up to four items of one size in whole rounds, and more
 // or mixed ones within half an item of the mean; each slab, written and read
 // at the memory's rate, costs the GPU 0.013 of a tile on top of one for the

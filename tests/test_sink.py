@@ -244,6 +244,24 @@ def test_bits_repeat_and_neighbours_stay(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,window", [(3, 100), (6, 100), (40, 100), (200, 30), (1500, 2000)])
+def test_dk_of_the_sinks_tile(D, S, window):
+    """The same for dK, whose terms are dS q: P of dS is rounded to fp16 (half a step: 2^-11) and dS held in two bf16
+    numbers."""
+    B, H, Hkv, n_sink = 2, 4, 2, 1
+    q, k, v, do = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=38)
+    u = torch.randn(Hkv, D, device=DEV, generator=torch.Generator(DEV).manual_seed(39))
+    q += (0.25 * u.repeat_interleave(H // Hkv, 0)).bfloat16()
+    k[:, :n_sink] = (0.3 * k[:, :n_sink] + 1.5 * u).bfloat16()
+    O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+    dK = dfa.dfa_attn_bwd_sink(q, k, v, O, lse, do, window, n_sink)[1]
+    dfa.dfa_check_errors()
+    r, terms, cancel, floor = sink.attn_bwd(*(np64(t) for t in (q, k, v, O, lse, do)), window, n_sink)["dK"]
+    tol = (2.0 ** -11 + 2.0 ** -16 + F) * terms + F2 * cancel + 2.0 ** -39 * floor + U * np.abs(r) + 1e-30
+    close(dK[:, :128], r[:, :128], tol[:, :128], "dK")
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n_sink", [0, 4])
 @pytest.mark.parametrize("down", [np.log(3), np.log(8), np.log(2000)])
 def test_where_p_saturates(D, n_sink, down):
