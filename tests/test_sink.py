@@ -504,6 +504,29 @@ def test_captured_and_replayed():
     dfa.dfa_check_errors()
 
 
+def test_captured_on_a_stream_of_its_own():
+    """A stream that a captured one forks: what the calls allocate there belongs to the graph."""
+    W, N = 90, 2
+    sets = [make(1, 4, 2, 700, D, torch.bfloat16, device=DEV, seed=91) for D in (64, 128)]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        out = [step(*sets[0], W, N), step(*sets[1], W, N, stream=side)]
+        kept = dfa.dfa_attn_fwd_sink(*sets[1][:3], W, N, stream=side)[0]      # the other output is dropped in the capture
+        now.wait_stream(side)
+    for seed in (92, 93):
+        for tensors, D in zip(sets, (64, 128)):
+            for t, n in zip(tensors, make(1, 4, 2, 700, D, torch.bfloat16, device=DEV, seed=seed)):
+                t.copy_(n)
+        g.replay()
+        torch.cuda.synchronize()
+        for got, tensors in zip(out, sets):
+            same_step(got, step(*tensors, W, N))
+        assert torch.equal(kept, out[1][0])
+    dfa.dfa_check_errors()
+
+
 FIRST = """
 import torch
 from long_context_causal_gb300 import dfa
