@@ -236,6 +236,8 @@ dfa_status dfa_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
  *   window:    >= 1 tokens;  n_sink: 0 .. 128 tokens (more: UNSUPPORTED)
  * bf16 only (DFA_ERR_UNSUPPORTED for fp32), D in {64, 128}; tensors must be
  * finite (a NaN or infinity in K or V reaches queries that do not see it).
+ * Whole sequences only: packed batches (cu_seqlens) and chunk offsets have no
+ * windowed form.
  * The forward takes no workspace and is one kernel launch; the backward is
  * three launches.  Both may be captured in a CUDA graph; two graphs or calls
  * that can overlap need a backward workspace each.

@@ -199,21 +199,26 @@ __device__ __forceinline__ int cta_items(const SinkBwdPlan& p) {
 // half of each 32 KB unused; dQ^T stays a 128-row MMA whose upper 64 rows come
 // from whatever follows K's first half and are never read.  At 32K tokens, 32
 // heads of 8 kv heads and a window of 4096 the single-phase kernel of bwd_tc.cu
-// took 8.65 ms on the same items, the two phases alone 4.85, with what follows 2.89.
+// took 8.65 ms on the same items, the two phases alone 4.85, with what follows 3.07 to 3.13.
 //
-// What bounds the variant, on the same problem: shared memory.  A step of 128 x 128
-// at D = 128 reads 64 KB for each of the four products whose operands both lie there
-// (128 bytes per cycle: all of its bandwidth while they run) and 32 KB for dV,
-// writes 32 KB of dS and 64 KB of dQ, which are read once more, and takes in 64 KB
-// of Q and dO: 512 KB, 4100 cycles, and a step takes 3900 (2.05 us).  So what cut
-// that traffic or the LSU's part of it counted -- dQ leaving as bulk reductions of
-// blocks in shared memory (kBulk: 5.08 -> 4.21 ms, one dO slot instead of two for the
-// room) -- and shorter chains did not: P or dS handed over in parts, TMEM loads under
-// arithmetic, polling, other orders.  At D = 64 the MMA role matters too: it runs as
-// a converged warp of which one lane issues, so that descriptors sit in uniform
-// registers (3.69 -> 3.36 ms).  D = 128 takes 4.15 ms (1240 TFLOP/s, 65% of the cuBLAS
-// rate), of which 0.5 are the preparing and finishing kernels' memory traffic and
-// the ends of the lists.
+// What bounds the variant: no unit alone.  Counters of one launch at D = 128 (16384
+// tokens, 16 heads of 4 kv heads, window 4096, 4 sinks; 4550 cycles a step of 128 x 128
+// with the lists' ends): the tensor pipe is busy for 57% of them, the tensor cores'
+// reads of their operands in shared memory take 2350 cycles a step (52%), the LSU's
+// pipe, with dS, the staging of dQ and the side rows, 2450 (54%).  The two reads run side
+// by side (their sum exceeds the cycles; the banks move 385 KB out and 170 KB in a step,
+// under half of what they can).  At D = 64 the three are 45, 45 and 46%.  What remains is
+// the chain S -> P -> dS -> dQ -> its drain through single buffers, each link of which waits
+// on pipes that are busy half of the time.  What paid: less LSU traffic -- dQ leaves
+// as bulk reductions of blocks in shared memory (kBulk: 5.08 -> 4.21 ms at 32K tokens, 32 heads
+// of 8 kv heads, window 4096, one dO slot instead of two for the room).  What did not: P
+// or dS handed over in parts, TMEM loads under arithmetic, polling, other orders.  At
+// D = 64 the MMA role matters too: it runs as a converged warp of which one lane issues, so
+// that descriptors sit in uniform registers (3.69 -> 3.36 ms).  D = 128 takes 4.15 to
+// 4.17 ms back to back (1240 TFLOP/s, 65% of the cuBLAS rate; 4.5 on tensors that change
+// from call to call), of which 0.5 are the preparing and finishing kernels' memory
+// traffic and the ends of the lists.
+//
 // VARLEN: a packed batch (a.seq set).  SPLIT: split-kv items, a piece of
 // piece_tiles query tiles of a key tile's range (item value * n_split + piece);
 // their dK/dV go to fp32 accumulators by reduction.  The dense kernel is a
@@ -304,7 +309,7 @@ __device__ __forceinline__ void body(const CUtensorMap& tmQ, const CUtensorMap& 
     constexpr bool kBulk = SINK && !(FINE && HD == 128);  // dQ leaves through shared memory
     // kBulk: 16 KB for each drain warpgroup
     constexpr int kOffStage = HD == 128 ? kOffDO + kTile : kOffQ + 16384, kStageStep = HD == 128 ? 16384 : kTile;
-    // HD = 64: dQ^T has columns of its own, so dP^T of the next tile need not wait until it is read out (3.08
+    // HD = 64: dQ^T has columns of its own, so dP^T of the next tile need not wait until it is read out (3.07
     // instead of 3.36 ms).  dP^T stays behind dQ^T and dK: in front of them or between them, with a second
     // buffer for dS^T, it took 3.35 and 3.50 ms.
     constexpr bool kOwnDQ = HD == 64;

@@ -673,12 +673,13 @@ __device__ __forceinline__ float2 ds_pair(uint32_t p, float u0, float u1, float 
         : "r"(p), "f"(u0), "f"(u1), "f"(d0), "f"(d1));
     return r;
 }
-// What a pair loses in pack_bf16, packed: bf16(x - bf16(x)).
+// Two fp32 numbers packed to fp16x2; beyond 65504 they stay there.
 __device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// What a pair loses in pack_bf16 (`packed`), packed: bf16(x - bf16(x)).
 __device__ __forceinline__ uint32_t pack_rest(float2 x, uint32_t packed) {
     return pack_bf16(x.x - __uint_as_float(packed << 16), x.y - __uint_as_float(packed & 0xffff0000u));
 }

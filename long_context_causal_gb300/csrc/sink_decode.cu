@@ -3,9 +3,10 @@
 //
 // Sequence b holds n = kv_len[b] tokens; its query stands at position n - 1 and
 // sees key j iff j < n and (j > n - 1 - W or j < N).  Every visible key and
-// value is read once and used by the G query heads of its key/value head, a
-// few operations per byte: the kernel is bound by HBM, and what matters is to
-// keep every SM's loads in flight and to give every SM the same share.
+// value is read once for every 16 of the G query heads of its key/value head (once
+// in all up to G = 16) and used by all of those, a few operations per byte: the
+// kernel is bound by HBM, and what matters is to keep every SM's loads in flight
+// and to give every SM the same share.
 //
 // Split.  The visible keys of every (sequence, key/value head, block of 16
 // query heads) -- a segment -- are cut into tiles of 64, and all tiles of all
@@ -18,7 +19,8 @@
 // Few short segments (CLUSTER; rule at launch()): a cluster of eight CTAs takes a
 // segment, an eighth of its tiles each, and joins the parts through distributed
 // shared memory: one launch instead of two (1 sequence of 1501 tokens, 32 heads of 8
-// kv heads, window 1024: 5.6 us, by the two kernels 7.1; calls in a stream 8.2 and 9.6).
+// kv heads, window 1024: 5.6 us, by the two kernels 7.1; calls in a stream 7.9 to 8.7
+// and 9.6).
 //
 // Per CTA: one producer warp streams K and V tiles by TMA into a ring; eight
 // consumer warps in two groups take the tiles in turn, each warp 16 keys of
