@@ -147,6 +147,8 @@ def _on_its_stream(call):
         now = torch.cuda.current_stream()
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream))
+        if stream.device != now.device:          # entering it below would change the device under the tensors
+            raise ValueError(f"the stream is on {stream.device}, the current device is {now.device}")
         if stream.cuda_stream == now.cuda_stream:
             return call(*args, **kw)
         bound = sig.bind(*args, **kw)

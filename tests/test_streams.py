@@ -110,3 +110,22 @@ def test_a_call_on_the_current_stream_stays_as_it_was(monkeypatch):
     assert call(1) == (1,) and call(1, b=3, stream=None) == (1,) and call(5, 6, None) == (5,)
     assert seen == [(1, 2, None), (1, 3, None), (5, 6, None)]
     assert list(__import__("inspect").signature(call).parameters) == ["a", "b", "stream"]
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Before anything is allocated or launched (CPU, with stand-ins for the streams)."""
+    class Stream:
+        def __init__(self, device, cuda_stream):
+            self.device, self.cuda_stream = torch.device("cuda", device), cuda_stream
+
+    @dfa._on_its_stream
+    def call(a, stream=None):
+        return (a, stream)
+
+    now = Stream(0, 16)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now)
+    with pytest.raises(ValueError, match="cuda:1"):
+        call(1, Stream(1, 32))
+    same = Stream(0, 16)
+    assert call(1, stream=same) == (1, same)
