@@ -57,13 +57,12 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def _binding_command() -> list[str]:
-    """The host compiler's command against the torch that runs, without the output."""
+def _binding_command(cuda: str) -> list[str]:
+    """The host compiler's command against the torch that runs, without the output; cuda: the toolkit's folder."""
     import sysconfig
 
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
-    cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
@@ -73,11 +72,12 @@ def _binding_command() -> list[str]:
 
 
 def _binding_key() -> str:
-    """What the module is built against: it fits no other torch or Python."""
+    """What the module is built against: it fits no other torch or Python.  (The
+    toolkit, for whose runtime headers alone it is needed, may be gone since.)"""
     import sys
 
     import torch
-    return "\n".join([f"torch {torch.__version__}", f"python {sys.version}", *_binding_command()])
+    return "\n".join([f"torch {torch.__version__}", f"python {sys.version}", *_binding_command("")])
 
 
 def binding_up_to_date() -> bool:
@@ -93,7 +93,7 @@ def binding_up_to_date() -> bool:
 def build_binding() -> str:
     """The extension module, and beside the objects what it was built against."""
     tmp = BINDING_LIB + f".tmp{os.getpid()}"
-    r = subprocess.run(_binding_command() + ["-o", tmp], capture_output=True, text=True)
+    r = subprocess.run(_binding_command(os.path.dirname(os.path.dirname(_nvcc()))) + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(BINDING)}:\n{r.stdout}\n{r.stderr}")
     os.makedirs(BUILD, exist_ok=True)

@@ -22,7 +22,9 @@ def built(tmp_path, monkeypatch):
     return tmp_path
 
 
-def test_the_module_that_was_built_is_up_to_date(built):
+def test_the_module_that_was_built_is_up_to_date(built, monkeypatch):
+    assert build.binding_up_to_date()
+    monkeypatch.setattr(build, "_nvcc", lambda: pytest.fail("a built tree needs no compiler"))
     assert build.binding_up_to_date()
 
 
