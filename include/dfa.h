@@ -83,7 +83,8 @@ typedef enum { DFA_SCHED_BALANCED = 0, DFA_SCHED_UNBALANCED = 1, DFA_SCHED_SPLIT
  *   q:        [B, Lq, H, D] with element strides q_strides = {batch, seq, head}
  *   k, v:     [B, Lkv, H_kv, D] with element strides kv_strides (shared by k, v)
  *             (either stride array may be NULL for the dense layout; strides
- *             must be multiples of 8 elements so rows stay 16-byte aligned)
+ *             must be multiples of 8 elements so rows stay 16-byte aligned; bf16:
+ *             0, a broadcast, only for a dimension of one element)
  *   causal:   1 = mask kv_offset + j > q_offset + i; 0 = attend to the whole chunk
  *   O_partial: fp32 [B, Lq, H, D] dense, the normalised partial output
  *   lse:      fp32 [B, H, Lq] dense, natural-log log-sum-exp of the partial
@@ -267,7 +268,8 @@ dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const 
  * (j > n - 1 - window or j < n_sink).
  *   q, O:    [B, H, D] dense, bf16;  lse: fp32 [B, H]
  *   k, v:    [B, S_max, H_kv, D] with element strides kv_strides = {batch,
- *            token, head} (shared; NULL: dense), multiples of 8, D contiguous
+ *            token, head} (shared; NULL: dense), multiples of 8 (0, a
+ *            broadcast, only for a dimension of one element), D contiguous
  *   kv_len:  DEVICE int32 [B]; read when the kernels run, so a captured call
  *            follows the lengths.  0: O = 0, lse = -inf.  Values below 0 count
  *            as 0, above S_max as S_max.

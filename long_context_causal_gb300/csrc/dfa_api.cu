@@ -201,6 +201,14 @@ dfa_status check_ptrs(std::initializer_list<const void*> ps) {
     return DFA_OK;
 }
 
+// A dimension of stride 0 that holds more than one element (a broadcast one) has
+// no tensor map: the bf16 kernels cannot load it.
+dfa_status check_broadcast(int B, int L, int heads, int64_t sb, int64_t ss, int64_t sh) {
+    if ((B > 1 && sb == 0) || (L > 1 && ss == 0) || (heads > 1 && sh == 0))
+        return fail(DFA_ERR_INVALID_ARG, "a stride of 0 is for dimensions of one element (copy a broadcast tensor first)");
+    return DFA_OK;
+}
+
 dfa_status upload_list(const CachedList* c, void* dst, cudaStream_t s) {
     cudaError_t e = cudaMemcpyAsync(dst, c->host, c->count * sizeof(int32_t), cudaMemcpyHostToDevice, s);
     return e == cudaSuccess ? DFA_OK : fail(DFA_ERR_CUDA, "work-list upload: %s", cudaGetErrorString(e));
@@ -345,6 +353,9 @@ extern "C" dfa_status dfa_chunk_attn_fwd(const void* q, const void* k, const voi
     if (dt == DFA_F32) {
         st = simt_fwd(p, dt, q, k, v, O_partial, true, lse, s);
     } else {
+        if ((st = check_broadcast(B, Lq, H, p.q_sb, p.q_ss, p.q_sh)) ||
+            (Lkv > 0 && (st = check_broadcast(B, Lkv, H_kv, p.kv_sb, p.kv_ss, p.kv_sh))))
+            return st;
         st = tc_fwd(p, q, k, v, O_partial, true, lse, nullptr, s);
     }
     if (st == DFA_OK) count_launch(DFA_KERNEL_FWD);
@@ -1025,6 +1036,7 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
         p.kv_sb = kv_strides[0]; p.kv_ss = kv_strides[1]; p.kv_sh = kv_strides[2];
         for (int64_t x : {p.kv_sb, p.kv_ss, p.kv_sh})
             if (x < 0 || x % 8 != 0) return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+        if ((st = check_broadcast(B, S_max, H_kv, p.kv_sb, p.kv_ss, p.kv_sh))) return st;
     }
     if ((st = check_ws(workspace, ws_bytes, decode_workspace(p)))) return st;
     if ((st = check_ptrs({q, k, v, O}))) return st;

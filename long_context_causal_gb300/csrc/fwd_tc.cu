@@ -532,15 +532,17 @@ bool make_tmap_bshd(void* map, const void* base, int B, int L, int heads, int D,
     CUtensorMap* m = static_cast<CUtensorMap*>(map);
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(L > 0 ? L : 1), (cuuint64_t)(B > 0 ? B : 1)};
+    // no rows: a map of one, never loaded from
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(L > 0 ? L : 1), (cuuint64_t)(L > 0 && B > 0 ? B : 1)};
     cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)ss * 2, (cuuint64_t)sb * 2};
     cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     // A stride of a size-1 dimension is never used; keep it valid for the encoder.
-    if (heads == 1 && strides[0] == 0) strides[0] = 16;
-    if (strides[0] == 0) strides[0] = 16;
-    if (strides[1] == 0) strides[1] = 16;
-    if (strides[2] == 0) strides[2] = 16;
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] != 0) continue;
+        if (dims[i + 1] > 1) return false;      // broadcast
+        strides[i] = 16;
+    }
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

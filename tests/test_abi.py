@@ -46,6 +46,17 @@ def test_chunk_fwd_validation(kw, code):
     assert st == code and msg
 
 
+def s3(*x):
+    return (ctypes.c_int64 * 3)(*x)
+
+
+@pytest.mark.parametrize("kw", [dict(B=2, qs=s3(0, 256, 128)), dict(qs=s3(1 << 15, 0, 128)), dict(qs=s3(1 << 15, 256, 0)),
+                                dict(B=2, ks=s3(0, 128, 128)), dict(ks=s3(1 << 14, 0, 128)), dict(Hkv=2, ks=s3(1 << 15, 128, 0))])
+def test_chunk_fwd_refuses_broadcast_tensors(kw):
+    st, msg = chunk(**kw)
+    assert st == dfa.DFA_ERR_INVALID_ARG and "broadcast" in msg
+
+
 def test_empty_chunk_is_a_no_op():
     st, _ = chunk(Lq=0, q=None, O=None, lse=None)
     assert st == dfa.DFA_OK

@@ -262,3 +262,17 @@ def test_n_chunks_does_not_change_the_result():
     torch.cuda.synchronize()
     for O, l in outs[1:]:
         assert torch.equal(O, outs[0][0]) and torch.equal(l, outs[0][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_chunk_of_no_keys(dtype):
+    """Every row is empty, whatever the batch; strides of a dimension of one element are never used."""
+    q, k, v, _ = make(2, 4, 2, 130, 64, dtype, device="cuda", seed=5)
+    O, lse = dfa.dfa_chunk_attn_fwd(q, k[:, :0], v[:, :0])
+    assert (O == 0).all() and (lse == -torch.inf).all()
+    one = dfa.dfa_chunk_attn_fwd(q[:1, :, :1].contiguous(), k[:1, :, :1].contiguous(), v[:1, :, :1].contiguous())
+    flat = [t[0, :, 0].contiguous().as_strided((1, 130, 1, 64), (0, 64, 0, 1)) for t in (q, k, v)]
+    for a, b in zip(one, dfa.dfa_chunk_attn_fwd(*flat)):
+        assert torch.equal(a, b)
+    dfa.dfa_check_errors()

@@ -415,6 +415,19 @@ def test_decode_strided_cache_and_lengths_out_of_range():
     check_decode(O, lse, q, k, v, [0, 150, 200], 60, 3)
 
 
+def test_decode_strides_of_dimensions_of_one_element():
+    """They are never used and may be 0; a cache that a batch shares by a stride of 0 is refused."""
+    S, D = 150, 64
+    k, v, n = cache(1, S, 1, D, [140], 60, 3, 76)
+    q = torch.randn(1, 4, D, device=DEV, generator=torch.Generator(DEV).manual_seed(77)).bfloat16()
+    flat = [t[0, :, 0].as_strided((1, S, 1, D), (0, D, 0, 1)) for t in (k, v)]
+    O, lse = dfa.dfa_attn_decode_sink(q, *flat, n, 60, 3)
+    dfa.dfa_check_errors()
+    check_decode(O, lse, q, k, v, [140], 60, 3)
+    with pytest.raises(dfa.DfaError, match="broadcast"):
+        dfa.dfa_attn_decode_sink(q.expand(2, 4, D).contiguous(), k.expand(2, S, 1, D), v.expand(2, S, 1, D), n.repeat(2), 60, 3)
+
+
 def test_decode_follows_the_prompt_and_is_captured_once():
     """A prompt through the forward, then tokens one at a time through one
     captured call: each row is what the forward gives for the whole sequence."""

@@ -264,6 +264,11 @@ def test_decode_refusals(kw, code):
     assert decode(**kw) == code and dfa.dfa_last_error()
 
 
+@pytest.mark.parametrize("ks", [(0, 256, 128), (300 * 256, 0, 128), (300 * 256, 256, 0)])
+def test_decode_refuses_broadcast_caches(ks):
+    assert decode(ks=(ctypes.c_int64 * 3)(*ks)) == dfa.DFA_ERR_INVALID_ARG and "broadcast" in dfa.dfa_last_error()
+
+
 def test_decode_of_no_sequence_and_size_queries():
     assert decode(B=0, q=None, k=None, v=None, n=None, ws=None, wn=0) == dfa.DFA_OK
     assert dfa.dfa_attn_decode_sink_workspace_size(8193, 4, 2, 128) == 0
