@@ -621,7 +621,8 @@ def dfa_launch_count(kind: str | int) -> int:
 def dfa_copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torch.Tensor:
     """dst <- src, byte for byte, through the SMs (include/dfa.h: dfa_copy).
     Both dense, with the same byte count; each on the GPU or in pinned host
-    memory.  Asynchronous on `stream` (default: the current stream)."""
+    memory.  Asynchronous on `stream` (default: the current stream): both have to
+    stay until the stream has come past it."""
     for t, name in ((dst, "dst"), (src, "src")):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
