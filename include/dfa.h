@@ -285,6 +285,50 @@ dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa
                                 int n_sink, float scale, void* O, float* lse, void* workspace, size_t ws_bytes,
                                 void* stream);
 
+/* The same step that also gathers what its query drew from each key.  The mass of
+ * a key of key/value head g is the sum of the attention weights that the
+ * queries so far gave it, over the query heads of the group:
+ *   mass_out[b, g, j] = mass[b, g, j] + sum_h exp(s_hj - lse_h)   for j < n, the
+ *                       second term 0 for keys that the query does not see,
+ *   mass_out[b, g, j] = 0                                         for j >= n.
+ *   mass:     fp32 [B, H_kv, S_max], finite or not, read for j < n only; NULL: zero
+ *   mass_out: fp32 [B, H_kv, S_max]; may be `mass` itself, else it does not
+ *             overlap an input
+ *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as below
+ * Everything else as dfa_attn_decode_sink, O and lse with the same bits.  Two or
+ * three launches; the same bits on every call.  */
+size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink);
+dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
+                                int S_max, int D, const int64_t* kv_strides, const int32_t* kv_len, const float* mass,
+                                int window, int n_sink, float scale, void* O, float* lse, float* mass_out,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* Eviction: a cache cut down to the keys that matter.  Of the n = kv_len[b] (counted
+ * as above) keys of sequence b, each key/value head keeps all if n <= keep, else
+ * `keep` of them: the first n_first, the last n_recent, and of the others those
+ * with the greatest mass, the lower position where masses are equal (-0 is 0; a
+ * NaN stands below every number).  They move, in their order, to rows 0 .. of
+ * k_out and v_out.
+ *   k, v:     [B, S_max, H_kv, D] bf16 or fp32 with element strides kv_strides =
+ *             {batch, token, head} (shared; NULL: dense), D contiguous; rows and
+ *             pointers on 16 bytes (strides multiples of 8 bf16 or 4 fp32 elements);
+ *             a stride of 0 (a broadcast) is allowed
+ *   mass:     fp32 [B, H_kv, S_max], read for j < n only
+ *   k_out, v_out: [B, cap, H_kv, D], cap >= keep, strides out_strides (not 0 for a
+ *             dimension of several elements); rows behind the kept ones are left
+ *             as they were
+ *   len_out:  int32 [B], min(n, keep)
+ *   mass_out: fp32 [B, H_kv, cap], the kept keys' masses, 0 behind them
+ *   kept:     int32 [B, H_kv, keep], their positions in k and v, rising; -1 behind
+ * keep >= 1, n_first, n_recent >= 0, n_first + n_recent <= keep.  No output may
+ * overlap an input.  The heads of a sequence keep different positions, so a window
+ * counted in rows (the calls above) means the last rows that were kept.  D in {64, 128}.
+ * Two launches, no workspace; may be captured. */
+dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt, int B, int H_kv, int S_max, int D,
+                           const int64_t* kv_strides, const int32_t* kv_len, const float* mass, int keep, int n_first,
+                           int n_recent, int cap, const int64_t* out_strides, void* k_out, void* v_out,
+                           int32_t* len_out, float* mass_out, int32_t* kept, void* stream);
+
 /* 8-bit attention checkpoint: what a layer keeps for its backward besides lse
  * (DISTFLASHATTN §3.3 keeps the attention's output so that the forward runs
  * once) in half the memory.  Each group of 32 consecutive elements of the head
@@ -385,7 +429,9 @@ typedef enum {
     DFA_KERNEL_DELTA = 3,     /* Delta = rowsum(dO * O) preprocessing      */
     DFA_KERNEL_CONVERT = 4,   /* fp32 dQ accumulator -> output dtype       */
     DFA_KERNEL_COPY = 5,      /* dfa_copy                                  */
-    DFA_KERNEL_KINDS = 6
+    DFA_KERNEL_MASS = 6,      /* weights gathered per key                  */
+    DFA_KERNEL_EVICT = 7,     /* choice and moving of the keys that stay   */
+    DFA_KERNEL_KINDS = 8
 } dfa_kernel_kind;
 int64_t dfa_launch_count(dfa_kernel_kind kind);
 

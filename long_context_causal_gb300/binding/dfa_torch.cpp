@@ -41,6 +41,9 @@ struct Entry {
     decltype(&dfa_ckpt8_size) ckpt_bytes;
     decltype(&dfa_attn_bwd_ckpt8) bwd_ckpt;
     decltype(&dfa_attn_bwd_ckpt8_workspace_size) bwd_ckpt_bytes;
+    decltype(&dfa_attn_decode_mass) decode_mass;
+    decltype(&dfa_attn_decode_mass_workspace_size) decode_mass_bytes;
+    decltype(&dfa_cache_evict) evict;
 } g;
 
 struct ValueErr {
@@ -255,31 +258,115 @@ PyObject* bwd(PyObject* const* a) {
     return st ? PyLong_FromLong(st) : pack({std::move(dQ), std::move(dK), std::move(dV)});
 }
 
-PyObject* decode(PyObject* const* a) {
-    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+// A cache k, v [B, S_max, H_kv, D] of one stride set, D contiguous.
+struct Cache {
+    int B, S, Hkv, D;
+    int64_t strides[3];
+};
+Cache cache(const at::Tensor& k, const at::Tensor& v, const char* what) {
+    if (k.dim() != 4 || k.sizes() != v.sizes())
+        throw ValueErr{std::string(what) + " must be [B, S_max, H_kv, D], got " + shape_of(k) + ", " + shape_of(v)};
+    if (v.scalar_type() != k.scalar_type()) throw ValueErr{std::string(what) + " must have the same dtype"};
+    if (k.strides() != v.strides() || k.stride(3) != 1)
+        throw ValueErr{std::string(what) + " must share their strides, with the head dimension contiguous"};
+    return Cache{small(k.size(0)), small(k.size(1)), small(k.size(2)), small(k.size(3)), {k.stride(0), k.stride(1), k.stride(2)}};
+}
+// The tokens of a call over a cache: q [B, H, D] beside it.
+Cache cache_of(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v) {
     if (q.dim() != 3 || k.dim() != 4 || k.sizes() != v.sizes() || k.size(0) != q.size(0) || k.size(3) != q.size(2))
         throw ValueErr{"q must be [B, H, D] and k, v [B, S_max, H_kv, D], got " + shape_of(q) + ", " + shape_of(k) + ", " +
                        shape_of(v)};
     if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type())
         throw ValueErr{"q, k and v must have the same dtype"};
-    if (k.strides() != v.strides() || k.stride(3) != 1)
-        throw ValueErr{"k and v must share their strides, with the head dimension contiguous"};
+    const Cache c = cache(k, v, "k and v");
     if (!q.is_contiguous()) throw ValueErr{"q must be contiguous ([B, H, D] dense)"};
+    return c;
+}
+
+PyObject* decode(PyObject* const* a) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Cache c = cache_of(q, k, v);
     const int d = on_gpu({&q, &k, &v});
     const at::Device dev = q.device();
-    const int B = small(q.size(0)), H = small(q.size(1)), D = small(q.size(2)), S = small(k.size(1)), Hkv = small(k.size(2));
-    const at::Tensor len = given(a[3], "kv_len", {B}, at::kInt, dev);
+    const int H = small(q.size(1));
+    const at::Tensor len = given(a[3], "kv_len", {c.B}, at::kInt, dev);
     const Stream s = stream_of(a[10], d);
     at::Tensor O = output(a[7], "O", q.sizes(), q.scalar_type(), dev, s);
-    at::Tensor lse = output(a[8], "lse", {B, H}, at::kFloat, dev, s);
-    const at::Tensor ws = bytes(a[9], "workspace_buf", a[9] == Py_None ? g.decode_bytes(B, H, Hkv, D) : 0, dev, s);
+    at::Tensor lse = output(a[8], "lse", {c.B, H}, at::kFloat, dev, s);
+    const at::Tensor ws = bytes(a[9], "workspace_buf", a[9] == Py_None ? g.decode_bytes(c.B, H, c.Hkv, c.D) : 0, dev, s);
     hold(s, {&q, &k, &v, &len, &O, &lse, &ws});
-    const int64_t strides[3] = {k.stride(0), k.stride(1), k.stride(2)};
-    const dfa_status st = without_gil(g.decode, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), B, H, Hkv, S, D,
-                                      static_cast<const int64_t*>(strides), static_cast<const int32_t*>(len.data_ptr()),
-                                      number(a[4], "window"), number(a[5], "n_sink"), scale_of(a[6], D), O.data_ptr(),
+    const dfa_status st = without_gil(g.decode, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), c.B, H, c.Hkv, c.S, c.D,
+                                      &c.strides[0], static_cast<const int32_t*>(len.data_ptr()), number(a[4], "window"),
+                                      number(a[5], "n_sink"), scale_of(a[6], c.D), O.data_ptr(),
                                       static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
     return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
+}
+
+PyObject* decode_mass(PyObject* const* a) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Cache c = cache_of(q, k, v);
+    const int d = on_gpu({&q, &k, &v});
+    const at::Device dev = q.device();
+    const int H = small(q.size(1));
+    const at::Tensor len = given(a[3], "kv_len", {c.B}, at::kInt, dev);
+    const at::Tensor mass = a[4] == Py_None ? at::Tensor() : given(a[4], "mass", {c.B, c.Hkv, c.S}, at::kFloat, dev);
+    const int window = a[5] == Py_None ? std::max(c.S, 1) : number(a[5], "window"), n_sink = number(a[6], "n_sink");
+    const Stream s = stream_of(a[12], d);
+    at::Tensor O = output(a[8], "O", q.sizes(), q.scalar_type(), dev, s);
+    at::Tensor lse = output(a[9], "lse", {c.B, H}, at::kFloat, dev, s);
+    at::Tensor out = output(a[10], "mass_out", {c.B, c.Hkv, c.S}, at::kFloat, dev, s);
+    const at::Tensor ws = bytes(a[11], "workspace_buf",
+                                a[11] == Py_None ? g.decode_mass_bytes(c.B, H, c.Hkv, c.S, c.D, window, n_sink) : 0, dev, s);
+    hold(s, {&q, &k, &v, &len, &O, &lse, &out, &ws});
+    if (mass.defined()) hold(s, {&mass});
+    const dfa_status st = without_gil(g.decode_mass, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_of(q), c.B, H, c.Hkv, c.S,
+                                      c.D, &c.strides[0], static_cast<const int32_t*>(len.data_ptr()),
+                                      mass.defined() ? static_cast<const float*>(mass.data_ptr()) : nullptr, window, n_sink,
+                                      scale_of(a[7], c.D), O.data_ptr(), static_cast<float*>(lse.data_ptr()),
+                                      static_cast<float*>(out.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse), std::move(out)});
+}
+
+// A new cache for the keys that stay: the rows behind them are zero.
+at::Tensor new_cache(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev, const Stream& s) {
+    at::Tensor t = result(shape, type, dev, s);
+    const NoGil released;
+    if (!s.other) return t.zero_();
+    c10::cuda::CUDAStreamGuard guard(torch_stream(s, dev));
+    return t.zero_();
+}
+
+PyObject* evict(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+    const Cache c = cache(k, v, "k and v");
+    const dfa_dtype dt = dtype_of(k);
+    const int d = on_gpu({&k, &v});
+    const at::Device dev = k.device();
+    const auto type = k.scalar_type();
+    const at::Tensor len = given(a[2], "kv_len", {c.B}, at::kInt, dev);
+    const at::Tensor mass = given(a[3], "mass", {c.B, c.Hkv, c.S}, at::kFloat, dev);
+    const int keep = number(a[4], "keep"), n_first = number(a[5], "n_first"), n_recent = number(a[6], "n_recent");
+    if (keep < 1) throw ValueErr{"keep must be at least 1"};
+    if ((a[7] == Py_None) != (a[8] == Py_None)) throw ValueErr{"k_out and v_out are given together"};
+    const Stream s = stream_of(a[12], d);
+    const bool made = a[7] == Py_None;
+    at::Tensor ko = made ? new_cache({c.B, keep, c.Hkv, c.D}, type, dev, s) : tensor(a[7], "k_out");
+    at::Tensor vo = made ? new_cache({c.B, keep, c.Hkv, c.D}, type, dev, s) : tensor(a[8], "v_out");
+    const Cache o = cache(ko, vo, "k_out and v_out");
+    if (o.B != c.B || o.Hkv != c.Hkv || o.D != c.D || ko.scalar_type() != type || ko.device() != dev || vo.device() != dev)
+        throw ValueErr{"k_out and v_out must be caches of k's dtype, batch, heads and head dimension on " + dev.str() + ", got " +
+                       c10::toString(ko.scalar_type()) + " " + shape_of(ko) + " on " + ko.device().str()};
+    at::Tensor len_out = output(a[9], "len_out", {c.B}, at::kInt, dev, s);
+    at::Tensor mass_out = output(a[10], "mass_out", {c.B, c.Hkv, o.S}, at::kFloat, dev, s);
+    at::Tensor kept = output(a[11], "kept", {c.B, c.Hkv, keep}, at::kInt, dev, s);
+    hold(s, {&k, &v, &len, &mass, &ko, &vo, &len_out, &mass_out, &kept});
+    const dfa_status st = without_gil(g.evict, k.data_ptr(), v.data_ptr(), dt, c.B, c.Hkv, c.S, c.D, &c.strides[0],
+                                      static_cast<const int32_t*>(len.data_ptr()), static_cast<const float*>(mass.data_ptr()),
+                                      keep, n_first, n_recent, o.S, &o.strides[0], ko.data_ptr(), vo.data_ptr(),
+                                      static_cast<int32_t*>(len_out.data_ptr()), static_cast<float*>(mass_out.data_ptr()),
+                                      static_cast<int32_t*>(kept.data_ptr()), s.handle);
+    return st ? PyLong_FromLong(st)
+              : pack({std::move(ko), std::move(vo), std::move(len_out), std::move(mass_out), std::move(kept)});
 }
 
 PyObject* save(PyObject* const* a) {
@@ -365,12 +452,13 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // bind(address of each entry point, in the order of Entry)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[10];
-    if (n != 10) {
-        PyErr_SetString(PyExc_TypeError, "bind takes ten addresses");
+    constexpr int kEntries = sizeof(Entry) / sizeof(void*);
+    void* p[kEntries];
+    if (n != kEntries) {
+        PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kEntries);
         return nullptr;
     }
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -390,6 +478,8 @@ PyMethodDef methods[] = {{"bind", FAST(bind)},
                          {"ckpt8_save", FAST((call<save, 6>))},
                          {"ckpt8_restore", FAST((call<restore, 11>))},
                          {"bwd_ckpt8", FAST((call<bwd_ckpt, 12>))},
+                         {"decode_mass", FAST((call<decode_mass, 13>))},
+                         {"cache_evict", FAST((call<evict, 13>))},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dfa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

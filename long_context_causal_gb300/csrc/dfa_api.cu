@@ -1015,13 +1015,32 @@ DecodeProblem decode_problem(int B, int H, int Hkv, int S, int D, int window, in
 
 }  // namespace
 
-extern "C" size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D) {
-    const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
+static bool decode_sizes_ok(const DecodeProblem& p) {
     char keep[sizeof(g_msg)];
     memcpy(keep, g_msg, sizeof(g_msg));
     const bool ok = check_decode(DFA_BF16, p) == DFA_OK;
     memcpy(g_msg, keep, sizeof(g_msg));
-    return ok ? decode_workspace(p) : 0;
+    return ok;
+}
+
+extern "C" size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D) {
+    const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
+    return decode_sizes_ok(p) ? decode_workspace(p, false) : 0;
+}
+
+// Strides of a caller's cache, if given, in place of the dense ones.
+static dfa_status take_strides(DecodeProblem& p, const int64_t* kv_strides) {
+    if (!kv_strides) return DFA_OK;
+    p.kv_sb = kv_strides[0]; p.kv_ss = kv_strides[1]; p.kv_sh = kv_strides[2];
+    for (int64_t x : {p.kv_sb, p.kv_ss, p.kv_sh})
+        if (x < 0 || x % 8 != 0) return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+    return check_broadcast(p.B, p.S, p.Hkv, p.kv_sb, p.kv_ss, p.kv_sh);
+}
+
+static bool aligned4(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return false;
+    return true;
 }
 
 extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H,
@@ -1031,19 +1050,111 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
     g_msg[0] = 0;
     DecodeProblem p = decode_problem(B, H, H_kv, S_max, D, window, n_sink, scale);
     dfa_status st = check_decode(dt, p);
-    if (st || B == 0) return st;
-    if (kv_strides) {
-        p.kv_sb = kv_strides[0]; p.kv_ss = kv_strides[1]; p.kv_sh = kv_strides[2];
-        for (int64_t x : {p.kv_sb, p.kv_ss, p.kv_sh})
-            if (x < 0 || x % 8 != 0) return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
-        if ((st = check_broadcast(B, S_max, H_kv, p.kv_sb, p.kv_ss, p.kv_sh))) return st;
-    }
-    if ((st = check_ws(workspace, ws_bytes, decode_workspace(p)))) return st;
+    if (st || B == 0 || (st = take_strides(p, kv_strides))) return st;
+    if ((st = check_ws(workspace, ws_bytes, decode_workspace(p, false)))) return st;
     if ((st = check_ptrs({q, k, v, O}))) return st;
-    if (!kv_len || !lse || ((reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(lse)) & 3u))
-        return fail(DFA_ERR_INVALID_ARG, "kv_len and lse must be 4-byte aligned pointers");
+    if (!aligned4({kv_len, lse})) return fail(DFA_ERR_INVALID_ARG, "kv_len and lse must be 4-byte aligned pointers");
     p.window = std::min(window, S_max);
-    return sink_decode(p, q, k, v, kv_len, O, lse, workspace, static_cast<cudaStream_t>(stream));
+    return sink_decode(p, q, k, v, kv_len, O, lse, nullptr, nullptr, workspace, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- attention weights gathered per key, eviction
+namespace {
+
+// Bytes [at, at + bytes) of a tensor; with strides, from its first element's to its last one's end.
+struct Range {
+    const void* at;
+    size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+dfa_status check_apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range& o : outs)
+        for (const Range& i : ins)
+            if (overlap(o, i)) return fail(DFA_ERR_INVALID_ARG, "an output overlaps an input");
+    return DFA_OK;
+}
+size_t extent(int B, int L, int heads, int D, int64_t sb, int64_t ss, int64_t sh, int elt) {
+    if (!B || !L || !heads) return 0;
+    return (size_t)((B - 1) * sb + (L - 1) * ss + (heads - 1) * sh + D) * elt;
+}
+
+// The window holds at most the cache, so that sizes follow from what can be visible.
+DecodeProblem mass_problem(int B, int H, int Hkv, int S, int D, int window, int n_sink, float scale) {
+    DecodeProblem p = decode_problem(B, H, Hkv, S, D, window, n_sink, scale);
+    if (window > S) p.window = std::max(S, 1);
+    return p;
+}
+dfa_status check_mass(dfa_dtype dt, const DecodeProblem& p) {
+    dfa_status st = check_decode(dt, p);
+    if (st) return st;
+    if ((int64_t)p.B * p.Hkv * p.S > ((int64_t)1 << 37)) return fail(DFA_ERR_INVALID_ARG, "problem too large");
+    return DFA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink) {
+    const DecodeProblem p = mass_problem(B, H, H_kv, S_max, D, window, n_sink, 1.f);
+    return decode_sizes_ok(p) ? decode_workspace(p, true) : 0;
+}
+
+extern "C" dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H,
+                                           int H_kv, int S_max, int D, const int64_t* kv_strides,
+                                           const int32_t* kv_len, const float* mass, int window, int n_sink,
+                                           float scale, void* O, float* lse, float* mass_out, void* workspace,
+                                           size_t ws_bytes, void* stream) {
+    g_msg[0] = 0;
+    DecodeProblem p = mass_problem(B, H, H_kv, S_max, D, window, n_sink, scale);
+    dfa_status st = check_mass(dt, p);
+    if (st || B == 0 || (st = take_strides(p, kv_strides))) return st;
+    if ((st = check_ws(workspace, ws_bytes, decode_workspace(p, true)))) return st;
+    if ((st = check_ptrs({q, k, v, O}))) return st;
+    if (!aligned4({kv_len, lse, mass_out}) || (mass && !aligned4({mass})))
+        return fail(DFA_ERR_INVALID_ARG, "kv_len, lse, mass and mass_out must be 4-byte aligned pointers");
+    const size_t cache = extent(B, S_max, H_kv, D, p.kv_sb, p.kv_ss, p.kv_sh, 2), masses = sizeof(float) * (size_t)B * H_kv * S_max;
+    if ((st = check_apart({{mass_out, masses}}, {{k, cache}, {v, cache}, {q, 2 * (size_t)B * H * D}, {kv_len, sizeof(int) * (size_t)B}})))
+        return st;
+    if (mass && mass != mass_out && (st = check_apart({{mass_out, masses}}, {{mass, masses}}))) return st;
+    return sink_decode(p, q, k, v, kv_len, O, lse, mass, mass_out, workspace, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt, int B, int H_kv, int S_max, int D,
+                                      const int64_t* kv_strides, const int32_t* kv_len, const float* mass, int keep,
+                                      int n_first, int n_recent, int cap, const int64_t* out_strides, void* k_out,
+                                      void* v_out, int32_t* len_out, float* mass_out, int32_t* kept, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st;
+    if ((st = check_dtype(dt)) || (st = check_common(B, H_kv, H_kv, D, 1.f))) return st;
+    if (S_max < 1) return fail(DFA_ERR_INVALID_ARG, "the cache must have room for a token");
+    if (keep < 1 || n_first < 0 || n_recent < 0 || (int64_t)n_first + n_recent > keep)
+        return fail(DFA_ERR_INVALID_ARG, "keep=%d of which the first %d and the last %d: at least one, and no more of these than kept",
+                    keep, n_first, n_recent);
+    if (cap < keep) return fail(DFA_ERR_INVALID_ARG, "cap=%d: the new cache must have room for the %d kept keys", cap, keep);
+    if ((int64_t)B * H_kv > (1 << 24) || S_max > (1 << 30) || cap > (1 << 30) || (int64_t)B * H_kv * std::min(keep, S_max) > ((int64_t)1 << 34))
+        return fail(DFA_ERR_INVALID_ARG, "problem too large (%d x %d heads of %d tokens)", B, H_kv, S_max);
+    if (B == 0) return DFA_OK;
+    const int elt = dt == DFA_BF16 ? 2 : 4;
+    EvictProblem p{B, H_kv, S_max, D, elt, keep, cap, n_first, n_recent,
+                   (int64_t)S_max * H_kv * D, (int64_t)H_kv * D, D, (int64_t)cap * H_kv * D, (int64_t)H_kv * D, D};
+    if (kv_strides) p.in_sb = kv_strides[0], p.in_ss = kv_strides[1], p.in_sh = kv_strides[2];
+    if (out_strides) p.out_sb = out_strides[0], p.out_ss = out_strides[1], p.out_sh = out_strides[2];
+    for (int64_t x : {p.in_sb, p.in_ss, p.in_sh, p.out_sb, p.out_ss, p.out_sh})
+        if (x < 0 || x % (16 / elt) != 0)
+            return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of %d elements", 16 / elt);
+    if ((st = check_broadcast(B, cap, H_kv, p.out_sb, p.out_ss, p.out_sh))) return st;
+    if ((st = check_ptrs({k, v, k_out, v_out}))) return st;
+    if (!aligned4({kv_len, mass, len_out, mass_out, kept}))
+        return fail(DFA_ERR_INVALID_ARG, "kv_len, mass, len_out, mass_out and kept must be 4-byte aligned pointers");
+    if (k_out == v_out) return fail(DFA_ERR_INVALID_ARG, "k_out and v_out are the same memory");
+    const size_t rows = (size_t)B * H_kv, in = extent(B, S_max, H_kv, D, p.in_sb, p.in_ss, p.in_sh, elt),
+                 out = extent(B, cap, H_kv, D, p.out_sb, p.out_ss, p.out_sh, elt);
+    if ((st = check_apart({{k_out, out}, {v_out, out}, {len_out, 4 * (size_t)B}, {mass_out, 4 * rows * cap}, {kept, 4 * rows * keep}},
+                          {{k, in}, {v, in}, {kv_len, 4 * (size_t)B}, {mass, 4 * rows * S_max}})))
+        return st;
+    return cache_evict(p, k, v, kv_len, mass, k_out, v_out, len_out, mass_out, kept, static_cast<cudaStream_t>(stream));
 }
 
 // ---------------------------------------------------------------- 8-bit attention checkpoints

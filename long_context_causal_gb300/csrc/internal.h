@@ -163,9 +163,19 @@ struct DecodeProblem {
 };
 constexpr int kMaxDecodeBatch = 8192;   // the kernel sums the lengths up in shared memory
 int64_t decode_tiles(const DecodeProblem& p);      // at most, per (sequence, block of query heads)
-size_t decode_workspace(const DecodeProblem& p);
+size_t decode_workspace(const DecodeProblem& p, bool mass);
+// mass_out (may be null, or mass itself): mass plus the step's weights, [B, Hkv, S].
 dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
-                       void* O, float* lse, void* ws, cudaStream_t s);
+                       void* O, float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s);
+
+// Eviction from a cache (cache_evict.cu): strides in elements of elt bytes.
+struct EvictProblem {
+    int B, Hkv, S, D, elt;
+    int keep, cap, n_first, n_recent;
+    int64_t in_sb, in_ss, in_sh, out_sb, out_ss, out_sh;
+};
+dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, const int32_t* kv_len, const float* mass,
+                       void* k_out, void* v_out, int32_t* len_out, float* mass_out, int32_t* kept, cudaStream_t s);
 
 // 8-bit checkpoint sections, in bytes from the start of the buffer: int8
 // payloads of q, k, v, O and their exponent bytes (one for 32 elements).

@@ -80,6 +80,11 @@ struct Args {
     int* prefix;                  // [B + 1], for the joining kernel
     float* part;                  // [2 * n CTAs][MH][D + 2]: unnormalised O, max, sum
     int* err;
+    // MASS: the scores times log2 e of the visible keys, [B * H][stride] in the order of the tiles
+    float* score;
+    int stride;                   // 64 * the most tiles of a segment
+    const float* mass;            // [B, Hkv, S], null: zero
+    float* mass_out;              // [B, Hkv, S]; may be `mass`
 };
 
 // The visible keys of a sequence as tiles: the sinks' tiles, if the window has
@@ -118,6 +123,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Stores four consecutive scores of a head's row.
+__device__ __forceinline__ void store_scores(const Args& a, int64_t row, int at, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(a.score + row * a.stride + at) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
 // Cursor over a CTA's range of tiles.
 struct Cursor {
     int b, r, k;        // sequence, segment of the sequence, tile of the segment
@@ -150,7 +160,7 @@ __device__ __forceinline__ void next_segment(const Args& a, Cursor& c) {
     }
 }
 
-template <int D, bool CLUSTER>
+template <int D, bool CLUSTER, bool MASS>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
     using C = Cfg<D>;
@@ -319,6 +329,19 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         s[z][e] *= a.scale_log2;
                         if (8 * z + t + 4 * (e & 1) >= n) s[z][e] = -INFINITY;
                     }
+                if constexpr (MASS) {
+                    // keys 4 m + t of a head's 16 in lane t become 4 t .. 4 t + 3
+                    const int64_t row = (int64_t)c.b * a.H + h0 + g;
+                    const int at = k * KT + w16 + 4 * t;
+                    float lo[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
+                    quad_transpose(lo, lane);
+                    if (g < nh) store_scores(a, row, at, lo);
+                    if (nh > 8) {
+                        float hi[4] = {s[0][2], s[0][3], s[1][2], s[1][3]};
+                        quad_transpose(hi, lane);
+                        if (g + 8 < nh) store_scores(a, row + 8, at, hi);
+                    }
+                }
                 float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
                 float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
@@ -543,11 +566,46 @@ join_kernel(const Args a, int grid) {
     if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
+// mass_out = mass + the step's weights: each visible key's 2^(score - lse log2 e), summed
+// over the heads of its group in their order.  0 behind the sequence.
+constexpr int kMassThreads = 256;
+__global__ void __launch_bounds__(kMassThreads)
+mass_kernel(const Args a, int blocks) {
+    wait_for_previous_kernel();      // its lse, and the scores of the one before
+    const int r = blockIdx.x / blocks, b = r / a.Hkv, g = r % a.Hkv, j = blockIdx.x % blocks * kMassThreads + threadIdx.x;
+    if (j >= a.S) return;
+    const int64_t at = (int64_t)r * a.S + j;
+    const Seen x = seen(a, b);
+    float sum = 0.f;
+    if (j < x.n) {
+        sum = a.mass ? a.mass[at] : 0.f;
+        const int key = j >= x.lo ? x.sink_tiles * KT + j - x.lo : j;
+        if (j >= x.lo || j < a.n_sink) {
+            const int64_t row = (int64_t)b * a.H + g * a.G;
+            float w = 0.f;
+            for (int h = 0; h < a.G; ++h) w += ex2(a.score[(row + h) * a.stride + key] - a.lse[row + h] * kLog2e);
+            sum += w;
+        }
+    }
+    a.mass_out[at] = sum;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-template <int D>
+size_t prefix_bytes(const DecodeProblem& p) { return align256(sizeof(int) * ((size_t)p.B + 1)); }
+size_t part_bytes(const DecodeProblem& p) { return align256(sizeof(float) * 2 * (size_t)num_sms() * MH * (p.D + 2)); }
+
+dfa_status launch_mass(const Args& a, cudaStream_t s) {
+    const int blocks = (a.S + kMassThreads - 1) / kMassThreads;
+    const cudaError_t e = launch_overlapped(mass_kernel, dim3((unsigned)(a.B * a.Hkv * blocks)), kMassThreads, 0, s, a, blocks);
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode mass launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_MASS);
+    return DFA_OK;
+}
+
+template <int D, bool MASS>
 dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len, void* O,
-                  float* lse, void* ws, cudaStream_t s) {
+                  float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s) {
     using C = Cfg<D>;
     CUtensorMap mk, mv;
     if (!make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.kv_sb, p.kv_ss, p.kv_sh, KT) ||
@@ -562,16 +620,22 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     a.lse = lse;
     a.scale_log2 = p.scale * kLog2e;
     a.prefix = static_cast<int*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256(sizeof(int) * ((size_t)p.B + 1)));
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(p));
     a.err = device_error_flag();
+    if (MASS) {
+        a.score = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(p) + part_bytes(p));
+        a.stride = (int)(KT * decode_tiles(p));
+        a.mass = mass;
+        a.mass_out = mass_out;
+    }
     const int segments = p.B * a.Hkv * a.HB;
     const int64_t tiles = (int64_t)segments * decode_tiles(p);
     const int n = (int)std::min<int64_t>(num_sms(), tiles);
     const int smem = C::kOffPrefix + (int)sizeof(int) * (p.B + 1);
     static std::atomic<uint64_t> seen{0};
     static std::atomic<int> clusters{0};             // that run at a time
-    auto spread = decode_kernel<D, false>;
-    auto clustered = decode_kernel<D, true>;
+    auto spread = decode_kernel<D, false, MASS>;
+    auto clustered = decode_kernel<D, true, MASS>;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
@@ -601,7 +665,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mk, mv, a);
         if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
         count_launch(DFA_KERNEL_FWD);
-        return DFA_OK;
+        return MASS ? launch_mass(a, s) : DFA_OK;
     }
     spread<<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
@@ -611,7 +675,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_FWD);
     count_launch(DFA_KERNEL_MERGE);
-    return DFA_OK;
+    return MASS ? launch_mass(a, s) : DFA_OK;
 }
 
 }  // namespace
@@ -621,14 +685,17 @@ int64_t decode_tiles(const DecodeProblem& p) {
     return (keys + KT - 1) / KT + (p.window < p.S ? (p.n_sink + KT - 1) / KT : 0);
 }
 
-size_t decode_workspace(const DecodeProblem& p) {
-    return align256(align256(sizeof(int) * ((size_t)p.B + 1)) +
-                    sizeof(float) * 2 * (size_t)num_sms() * MH * (p.D + 2));
+size_t decode_workspace(const DecodeProblem& p, bool mass) {
+    return prefix_bytes(p) + part_bytes(p) + (mass ? sizeof(float) * (size_t)p.B * p.H * KT * decode_tiles(p) : 0);
 }
 
 dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
-                       void* O, float* lse, void* ws, cudaStream_t s) {
-    return p.D == 128 ? launch<128>(p, q, k, v, kv_len, O, lse, ws, s) : launch<64>(p, q, k, v, kv_len, O, lse, ws, s);
+                       void* O, float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s) {
+    if (mass_out)
+        return p.D == 128 ? launch<128, true>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s)
+                          : launch<64, true>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s);
+    return p.D == 128 ? launch<128, false>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s)
+                      : launch<64, false>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s);
 }
 
 }  // namespace dfa

@@ -27,7 +27,7 @@ HEADER = os.path.join(INCLUDE, "dfa.h")
 DFA_OK, DFA_ERR_INVALID_ARG, DFA_ERR_UNSUPPORTED, DFA_ERR_CUDA, DFA_ERR_TIMEOUT, DFA_ERR_WORKSPACE = range(6)
 DFA_F32, DFA_BF16 = 0, 1
 DFA_SCHED_BALANCED, DFA_SCHED_UNBALANCED, DFA_SCHED_SPLIT_KV = 0, 1, 2
-KERNEL_KINDS = {"fwd": 0, "bwd": 1, "merge": 2, "delta": 3, "convert": 4, "copy": 5}
+KERNEL_KINDS = {"fwd": 0, "bwd": 1, "merge": 2, "delta": 3, "convert": 4, "copy": 5, "mass": 6, "evict": 7}
 _SCHED = {"balanced": DFA_SCHED_BALANCED, "unbalanced": DFA_SCHED_UNBALANCED, "split_kv": DFA_SCHED_SPLIT_KV,
           DFA_SCHED_BALANCED: DFA_SCHED_BALANCED, DFA_SCHED_UNBALANCED: DFA_SCHED_UNBALANCED,
           DFA_SCHED_SPLIT_KV: DFA_SCHED_SPLIT_KV}
@@ -87,6 +87,11 @@ def _load() -> ctypes.CDLL:
         "dfa_attn_bwd_ckpt8_workspace_size": (sz, [i32] * 7),
         "dfa_attn_bwd_ckpt8": (i32, [vp, sz, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                      vp, vp, vp, vp, sz, vp]),
+        "dfa_attn_decode_mass_workspace_size": (sz, [i32] * 7),
+        "dfa_attn_decode_mass": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, p64, vp, vp, i32, i32, f32, vp, vp, vp,
+                                       vp, sz, vp]),
+        "dfa_cache_evict": (i32, [vp, vp, i32, i32, i32, i32, i32, p64, vp, vp, i32, i32, i32, i32, p64, vp, vp, vp, vp,
+                                  vp, vp]),
         "dfa_build_split_worklist": (i64, [i32, i32, i32, i32, i32, i32, p32, p32]),
         "dfa_debug_mma": (i32, [i32, vp, vp, vp, vp]),
         "dfa_debug_cta_trace": (i32, [vp, i32]),
@@ -502,7 +507,8 @@ class _Native:
         native.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
             "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
             "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
-            "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size")))
+            "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size", "dfa_attn_decode_mass",
+            "dfa_attn_decode_mass_workspace_size", "dfa_cache_evict")))
         vars(self).update((n, f) for n, f in vars(native).items() if not n.startswith("__"))
         return getattr(native, name)
 
@@ -544,6 +550,28 @@ def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: f
     (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
     GPU; returns (O [B,H,D], lse fp32 [B,H])."""
     return _result(_native.decode_sink(q, k, v, kv_len, window, n_sink, scale, O, lse, workspace_buf, stream))
+
+
+def dfa_attn_decode_mass_workspace_size(B, H, H_kv, S_max, D, window, n_sink) -> int:
+    return _lib.dfa_attn_decode_mass_workspace_size(B, H, H_kv, S_max, D, window, n_sink)
+
+
+def dfa_attn_decode_mass(q, k, v, kv_len, mass=None, window: int | None = None, n_sink: int = 0,
+                         scale: float | None = None, O=None, lse=None, mass_out=None, workspace_buf=None, stream=None):
+    """dfa_attn_decode_sink (window None: every key) that also adds the weights its
+    query gave each key to `mass` fp32 [B,H_kv,S_max] (None: zero): returns (O, lse,
+    mass_out), mass_out 0 behind each sequence; mass_out=mass adds in place."""
+    return _result(_native.decode_mass(q, k, v, kv_len, mass, window, n_sink, scale, O, lse, mass_out, workspace_buf, stream))
+
+
+def dfa_cache_evict(k, v, kv_len, mass, keep: int, n_first: int = 0, n_recent: int = 0, k_out=None, v_out=None,
+                    len_out=None, mass_out=None, kept=None, stream=None):
+    """The `keep` keys of each sequence and key/value head that stay (the first
+    n_first, the last n_recent, the heaviest of the others) moved in their order to
+    another cache k_out, v_out [B,cap,H_kv,D] (None: new ones with cap = keep, zero
+    behind the kept rows): returns (k_out, v_out, len_out int32 [B], mass_out fp32
+    [B,H_kv,cap], kept int32 [B,H_kv,keep], -1 behind)."""
+    return _result(_native.cache_evict(k, v, kv_len, mass, keep, n_first, n_recent, k_out, v_out, len_out, mass_out, kept, stream))
 
 
 def dfa_ckpt8_size(B, H, H_kv, S, D) -> int:

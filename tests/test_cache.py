@@ -1,0 +1,214 @@
+"""The calls over a long cache on the GPU, against the fp64 reference (oracle/cache.py).
+
+Tolerances count what is rounded.  fp32 sums of up to D = 128 products move a score
+by less than F / 2 = 2^-13 (scores here stay below 60), a log-sum-exp by as much; a
+weight exp(s - lse) by F times itself where lse is handed in, by 2 F where it is the
+call's own.  Weights are positive, so sums of them are off by no more, and by 2^-24
+per addition (at most 2^10 of these in a row in one sum here: F / 4).  O, as in the
+windowed tests: P is rounded to bf16 (U times the sum of P |v|) and the result once.
+What is kept, moved and counted is exact.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_causal_gb300 import dfa
+from oracle import cache, sink
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U, F = 2.0 ** -8, 2.0 ** -12
+NAN = float("nan")
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, ref, tol, what):
+    bad = ~(np.abs(np64(got) - ref) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, first at {np.argwhere(bad)[0]}, worst {np.nanmax(np.abs(np64(got) - ref) / (tol + 1e-30)):.3g} of the tolerance"
+
+
+def gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def rand(seed, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, device=DEV, generator=gen(seed)).to(dtype)
+
+
+def lens_of(lens):
+    return torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------------------------------------ single tokens with masses
+# (B, H, Hkv, S, D, window, n_sink, lens)
+STEP = [
+    (1, 1, 1, 1, 64, 1, 0, [1]), (2, 2, 1, 3, 128, 3, 0, [0, 2]), (1, 8, 2, 64, 128, 64, 0, [64]),
+    (2, 8, 8, 65, 64, 65, 0, [65, 64]), (3, 12, 4, 200, 128, 60, 3, [200, 61, 62]), (2, 16, 1, 300, 64, 100, 128, [300, 129]),
+    (1, 17, 1, 130, 128, 130, 0, [127]), (2, 40, 2, 500, 64, 77, 17, [500, 90]), (2, 33, 3, 257, 128, 16, 1, [257, 1]),
+    (1, 4, 4, 5000, 128, 5000, 0, [4999]), (1, 32, 8, 9000, 64, 9000, 0, [8577]), (6, 8, 2, 3001, 128, 1500, 4, [0, 1, 1500, 1501, 3001, 2222]),
+    (40, 8, 4, 700, 64, 700, 0, [i * 17 for i in range(40)]),
+]
+
+
+def poisoned(case, seed):
+    B, H, Hkv, S, D, window, n_sink, lens = case
+    q, k, v, m = rand(seed, B, H, D), rand(seed + 1, B, S, Hkv, D), rand(seed + 2, B, S, Hkv, D), rand(seed + 3, B, Hkv, S, dtype=torch.float32).abs()
+    k[:, ::7] *= 2
+    for b, n in enumerate(lens):       # what the query does not see may hold anything
+        j = torch.arange(S, device=DEV)
+        hidden = (j >= n) | ((j <= n - 1 - window) & (j >= n_sink))
+        k[b, hidden], v[b, hidden] = NAN, float("inf")
+        m[b, :, n:] = NAN
+    return q, k, v, lens_of(lens), m
+
+
+def check_step(got, case, q, k, v, m):
+    B, H, Hkv, S, D, window, n_sink, lens = case
+    O, lse, out = got
+    Or, lr, size = sink.decode(np64(q), np64(k), np64(v), lens, window, n_sink)
+    close(O, Or, (U + F) * size + U * np.abs(Or), "O")
+    empty = np.asarray(lens) == 0
+    assert (np64(lse)[empty] == -np.inf).all()
+    close(lse[~torch.from_numpy(empty)], lr[~empty], 2 * F, "lse")
+    w = cache.step_mass(np64(q), np64(k), lens, window, n_sink)
+    live = np.arange(S) < np.asarray(lens)[:, None, None]
+    before = np.zeros_like(w) if m is None else np.where(live, np64(m), 0.0)
+    close(out, before + w, 2 * F * w + 2.0 ** -23 * (before + w), "mass")
+    assert (np64(out)[~np.broadcast_to(live, w.shape)] == 0).all()
+
+
+@pytest.mark.parametrize("case", STEP, ids=lambda c: "B{}H{}kv{}S{}D{}w{}s{}".format(*c))
+def test_step_masses(case):
+    q, k, v, n, m = poisoned(case, 11)
+    window, n_sink = case[5:7]
+    got = dfa.dfa_attn_decode_mass(q, k, v, n, m, window, n_sink)
+    alone = dfa.dfa_attn_decode_mass(q, k, v, n, None, window, n_sink)
+    dfa.dfa_check_errors()
+    check_step(got, case, q, k, v, m)
+    check_step(alone, case, q, k, v, None)
+    # the plain step's O and lse, the same bits in place and again
+    O, lse = dfa.dfa_attn_decode_sink(q, k, v, n, window, n_sink)
+    into = m.clone()
+    again = dfa.dfa_attn_decode_mass(q, k, v, n, into, window, n_sink, mass_out=into)
+    assert again[2] is into or again[2].data_ptr() == into.data_ptr()
+    for a, b in ((got[0], O), (got[1], lse), (again[0], O), (again[1], lse), (again[2], got[2])):
+        assert torch.equal(a, b)
+
+
+def test_step_masses_strided_cache_and_lengths_out_of_range():
+    B, H, Hkv, S, D = 3, 4, 2, 200, 128
+    both = rand(21, B, Hkv, S, 2, D + 8)           # head-major, k and v interleaved
+    k, v = both[..., 0, :D].transpose(1, 2), both[..., 1, :D].transpose(1, 2)
+    q, m = rand(22, B, H, D), rand(23, B, Hkv, S, dtype=torch.float32)
+    got = dfa.dfa_attn_decode_mass(q, k, v, lens_of([-4, 150, 999]), m, 60, 3, scale=0.2)
+    dfa.dfa_check_errors()
+    Or, lr, size = sink.decode(np64(q), np64(k), np64(v), [0, 150, 200], 60, 3, 0.2)
+    close(got[0], Or, (U + F) * size + U * np.abs(Or), "O")
+    w = cache.step_mass(np64(q), np64(k), [0, 150, 200], 60, 3, 0.2)
+    want = np.where(np.arange(S) < np.array([0, 150, 200])[:, None, None], np64(m), 0.0) + w
+    close(got[2], want, 2 * F * w + 2.0 ** -23 * np.abs(want), "mass")
+
+
+def test_step_masses_of_a_cache_beyond_32_bits():
+    B, H, Hkv, S, D, W, N = 3, 16, 8, 1 << 20, 128, 700, 4
+    k, v = (torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(24 + i)) for i in range(2))
+    q, lens = rand(26, B, H, D), [S, 5, S - 1]
+    for window in (W, None):
+        got = dfa.dfa_attn_decode_mass(q, k, v, lens_of(lens), None, window, N)
+        dfa.dfa_check_errors()
+        # every head of a sequence gives away one
+        np.testing.assert_allclose(np64(got[2]).sum((1, 2)), H, rtol=4 * F)
+        for b, n in enumerate(lens):
+            idx = torch.arange(n, device=DEV)
+            idx = idx[(idx > n - 1 - W) | (idx < N)] if window else idx[-2000:]
+            s = torch.einsum("hd,jhd->hj", q[b].double(), k[b, idx].double().repeat_interleave(2, 1)) * D ** -0.5
+            w = torch.exp(s - got[1][b].double()[:, None]).reshape(Hkv, 2, -1).sum(1)
+            close(got[2][b][:, idx], np64(w), 2 * F * np64(w), "mass")
+
+
+# ------------------------------------------------------------------------------------------------ eviction
+# (B, Hkv, S, D, keep, cap, n_first, n_recent, lens)
+EVICT = [
+    (1, 1, 1, 64, 1, 1, 0, 0, [1]), (2, 3, 5, 128, 3, 4, 1, 1, [0, 5]), (2, 2, 33, 64, 32, 40, 4, 8, [33, 32]),
+    (1, 8, 501, 64, 128, 200, 4, 32, [501]), (3, 2, 1000, 128, 10, 10, 5, 5, [1000, 11, 10]), (2, 1, 1025, 64, 1024, 1024, 0, 0, [1025, 1024]),
+    (2, 4, 2500, 128, 700, 701, 0, 100, [2500, 2049]), (1, 2, 9000, 64, 4000, 4500, 3, 0, [8999]), (2, 2, 40000, 64, 1000, 1000, 4, 64, [40000, 1001]),
+    (1, 1, 70001, 128, 69999, 70001, 1, 1, [70001]), (1, 3, 131, 64, 300, 400, 7, 200, [131]), (5, 1, 64, 64, 1, 1, 0, 0, [64, 1, 0, 2, 63]),
+]
+EVICT_IDS = ["B{}kv{}S{}D{}k{}c{}f{}r{}".format(*c) for c in EVICT]
+
+
+def check_evict(got, k, v, m, lens, case, behind=0):
+    B, Hkv, S, D, keep, cap, n_first, n_recent, _ = case
+    ko, vo, lo, mo, kept = got
+    m = m.cpu().numpy()
+    assert lo.tolist() == [min(n, keep) for n in lens]
+    for b, n in enumerate(lens):
+        for g in range(Hkv):
+            j = cache.kept(m[b, g], n, keep, n_first, n_recent)
+            assert kept[b, g].tolist() == j.tolist() + [-1] * (keep - len(j)), (b, g)
+            at, r = torch.from_numpy(j).to(DEV), len(j)
+            assert torch.equal(ko[b, :r, g], k[b, at, g]) and torch.equal(vo[b, :r, g], v[b, at, g]), (b, g)
+            assert (ko[b, r:, g] == behind).all() and (vo[b, r:, g] == behind).all()
+            assert np.array_equal(mo[b, g].cpu().numpy()[:r], m[b, g, j], equal_nan=True) and (mo[b, g, r:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "few", "odd"])
+@pytest.mark.parametrize("case", EVICT, ids=EVICT_IDS)
+def test_evict(case, kind):
+    B, Hkv, S, D, keep, cap, n_first, n_recent, lens = case
+    k, v = rand(31, B, S, Hkv, D), rand(32, B, S, Hkv, D)
+    m = torch.exp(3 * rand(33, B, Hkv, S, dtype=torch.float32))
+    if kind == "ties":                   # most of the masses equal, the border among them
+        m = torch.where(m > 9, m, 0.0)
+    elif kind == "few":                  # a handful of values, whole and of both signs
+        m = (m * 2).clamp(max=6).round() - 3
+    elif kind == "odd":                  # what a mass should not be, and what no order may stumble over
+        for i, x in enumerate((NAN, float("inf"), -float("inf"), 0.0, -0.0, 1e-45, -1e-45, 3.4e38, -NAN)):
+            m[..., i::17] = x
+    for b, n in enumerate(lens):
+        m[b, :, n:] = float("inf")       # behind the sequence: not a key
+    ko, vo = (torch.full((B, cap, Hkv, D), 7, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    got = dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, n_first, n_recent, ko, vo)
+    check_evict(got, k, v, m, lens, case, 7)
+    again = dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, n_first, n_recent)
+    check_evict(again, k, v, m, lens, (B, Hkv, S, D, keep, keep, n_first, n_recent, lens))
+
+
+def test_evict_strides_types_and_lengths_out_of_range():
+    B, Hkv, S, D, keep, cap = 3, 2, 300, 128, 50, 60
+    lens = [0, 250, 300]
+    m = rand(41, B, Hkv, S, dtype=torch.float32)
+    n = lens_of([-7, 250, 1000])
+    both = rand(42, B, Hkv, S, 2, D + 8)                            # head-major, k and v interleaved
+    k, v = both[..., 0, :D].transpose(1, 2), both[..., 1, :D].transpose(1, 2)
+    out = torch.full((B, Hkv, cap, 2, D + 8), 7.0, device=DEV).bfloat16()
+    ko, vo = out[..., 0, :D].transpose(1, 2), out[..., 1, :D].transpose(1, 2)
+    case = (B, Hkv, S, D, keep, cap, 2, 9, lens)
+    check_evict(dfa.dfa_cache_evict(k, v, n, m, keep, 2, 9, ko, vo), k, v, m, lens, case, 7)
+    assert (out[..., D:] == 7).all()
+    k, v = rand(43, B, S, Hkv, D, dtype=torch.float32), rand(44, B, S, Hkv, D, dtype=torch.float32)
+    ko, vo = (torch.full((B, cap, Hkv, D), 7.0, device=DEV) for _ in range(2))
+    check_evict(dfa.dfa_cache_evict(k, v, n, m, keep, 2, 9, ko, vo), k, v, m, lens, case, 7)
+    shared = rand(45, 1, S, Hkv, D).expand(B, S, Hkv, D)            # one cache for the batch: a stride of 0
+    check_evict(dfa.dfa_cache_evict(shared, shared, n, m, keep, 2, 9), shared, shared, m, lens, (B, Hkv, S, D, keep, keep, 2, 9, lens))
+
+
+def test_evict_from_a_cache_beyond_32_bits():
+    B, Hkv, S, D, keep = 3, 8, (1 << 20) + 5, 128, 300
+    k, v = (torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(46 + i)) for i in range(2))
+    m = torch.rand(B, Hkv, S, device=DEV, generator=gen(48))
+    lens = [S, 17, S - 1]
+    ko, vo, lo, mo, kept = dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, 4, 16)
+    for b, n in enumerate(lens):
+        r = min(n, keep)
+        for g in range(Hkv):
+            at = kept[b, g, :r].long()
+            if n > keep:
+                top = torch.topk(m[b, g, 4:n - 16], keep - 20).indices + 4
+                want = torch.cat((torch.arange(4, device=DEV), top.sort().values, torch.arange(n - 16, n, device=DEV)))
+                assert torch.equal(m[b, g, at].sort().values, m[b, g, want].sort().values) and (at[1:] > at[:-1]).all()
+            assert torch.equal(ko[b, :r, g], k[b, at, g]) and torch.equal(vo[b, :r, g], v[b, at, g])
+            assert torch.equal(mo[b, g, :r], m[b, g, at])
