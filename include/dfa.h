@@ -285,9 +285,27 @@ dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa
                                 int n_sink, float scale, void* O, float* lse, void* workspace, size_t ws_bytes,
                                 void* stream);
 
-/* The same step that also gathers what its query drew from each key.  The mass of
- * a key of key/value head g is the sum of the attention weights that the
- * queries so far gave it, over the query heads of the group:
+/* Attention weights gathered per key: the mass of a key of key/value head g is the
+ * sum of the weights that queries gave it, over the query heads of the group.
+ * Over a prompt, from the forward's q, k and saved lse:
+ *   mass[b, g, j] = sum_h sum_{i >= S - n_last, i sees j} exp(s_ij - lse_i),
+ * i and j as in dfa_attn_fwd_sink with the same window and n_sink (window >= S,
+ * n_sink = 0: plain causal attention, after dfa_attn_fwd).  n_last >= 1 (above S: S):
+ * how many of the last queries count.  q, k [B, S, heads, D] dense, bf16; lse fp32
+ * [B, H, S], rows before S - n_last are not read; a row with lse = -inf counts for nothing.
+ *   mass:      fp32 [B, H_kv, S], 0 for keys that none of the queries sees; overlaps
+ *              no input
+ *   workspace: >= dfa_attn_mass_workspace_size() bytes, 16-byte aligned, contents
+ *              not preserved; calls that can overlap need one each
+ * bf16 only, D in {64, 128}.  Two launches; may be captured; the same bits on
+ * every call.  Keys may hold anything where no counted query sees them; a NaN in q
+ * or lse reaches the keys that its query sees. */
+size_t dfa_attn_mass_workspace_size(int B, int H, int H_kv, int S, int D);
+dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dtype dt, int B, int H, int H_kv, int S,
+                         int D, int window, int n_sink, int n_last, float scale, float* mass, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* The single-token step that adds its query's weights to the masses:
  *   mass_out[b, g, j] = mass[b, g, j] + sum_h exp(s_hj - lse_h)   for j < n, the
  *                       second term 0 for keys that the query does not see,
  *   mass_out[b, g, j] = 0                                         for j >= n.

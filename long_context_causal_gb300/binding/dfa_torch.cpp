@@ -44,6 +44,8 @@ struct Entry {
     decltype(&dfa_attn_decode_mass) decode_mass;
     decltype(&dfa_attn_decode_mass_workspace_size) decode_mass_bytes;
     decltype(&dfa_cache_evict) evict;
+    decltype(&dfa_attn_mass) mass;
+    decltype(&dfa_attn_mass_workspace_size) mass_bytes;
 } g;
 
 struct ValueErr {
@@ -302,6 +304,24 @@ PyObject* decode(PyObject* const* a) {
     return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
 }
 
+PyObject* mass(PyObject* const* a) {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+    const Sequence z = sequence(q, k, k);
+    const int d = on_gpu({&q, &k});
+    const at::Device dev = q.device();
+    const at::Tensor lse = given(a[2], "lse", {z.B, z.H, z.S}, at::kFloat, dev);
+    const int window = a[3] == Py_None ? std::max(z.S, 1) : number(a[3], "window"), n_sink = number(a[4], "n_sink"),
+              n_last = a[5] == Py_None ? std::max(z.S, 1) : number(a[5], "n_last");
+    const Stream s = stream_of(a[9], d);
+    at::Tensor out = output(a[7], "mass", {z.B, z.Hkv, z.S}, at::kFloat, dev, s);
+    const at::Tensor ws = bytes(a[8], "workspace_buf", a[8] == Py_None ? g.mass_bytes(z.B, z.H, z.Hkv, z.S, z.D) : 0, dev, s);
+    hold(s, {&q, &k, &lse, &out, &ws});
+    const dfa_status st = without_gil(g.mass, q.data_ptr(), k.data_ptr(), static_cast<const float*>(lse.data_ptr()), dtype_of(q),
+                                      z.B, z.H, z.Hkv, z.S, z.D, window, n_sink, n_last, scale_of(a[6], z.D),
+                                      static_cast<float*>(out.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    return st ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(out));
+}
+
 PyObject* decode_mass(PyObject* const* a) {
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
     const Cache c = cache_of(q, k, v);
@@ -478,6 +498,7 @@ PyMethodDef methods[] = {{"bind", FAST(bind)},
                          {"ckpt8_save", FAST((call<save, 6>))},
                          {"ckpt8_restore", FAST((call<restore, 11>))},
                          {"bwd_ckpt8", FAST((call<bwd_ckpt, 12>))},
+                         {"mass", FAST((call<mass, 10>))},
                          {"decode_mass", FAST((call<decode_mass, 13>))},
                          {"cache_evict", FAST((call<evict, 13>))},
                          {nullptr, nullptr, 0, nullptr}};

@@ -1096,6 +1096,27 @@ dfa_status check_mass(dfa_dtype dt, const DecodeProblem& p) {
 
 }  // namespace
 
+extern "C" size_t dfa_attn_mass_workspace_size(int B, int H, int H_kv, int S, int D) {
+    return sink_sizes_ok(B, H, H_kv, S, D, 1, 0) ? key_mass_workspace() : 0;
+}
+
+extern "C" dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dtype dt, int B, int H,
+                                    int H_kv, int S, int D, int window, int n_sink, int n_last, float scale,
+                                    float* mass, void* workspace, size_t ws_bytes, void* stream) {
+    g_msg[0] = 0;
+    dfa_status st = check_sink(dt, B, H, H_kv, S, D, window, n_sink, scale);
+    if (st || (st = check_sink_rows(B, H, S))) return st;
+    if (n_last < 1) return fail(DFA_ERR_INVALID_ARG, "n_last must be at least one query (got %d)", n_last);
+    if ((int64_t)B * S == 0) return DFA_OK;
+    if ((st = check_ws(workspace, ws_bytes, key_mass_workspace())) || (st = check_ptrs({q, k}))) return st;
+    if (!aligned4({lse, mass})) return fail(DFA_ERR_INVALID_ARG, "lse and mass must be 4-byte aligned pointers");
+    const size_t tokens = (size_t)B * S;
+    if ((st = check_apart({{mass, 4 * tokens * H_kv}}, {{q, 2 * tokens * H * D}, {k, 2 * tokens * H_kv * D}, {lse, 4 * tokens * H}})))
+        return st;
+    return tc_key_mass(sink_problem(B, H, H_kv, S, D, window, n_sink, scale), std::min(n_last, S), q, k, lse, mass, workspace,
+                       static_cast<cudaStream_t>(stream));
+}
+
 extern "C" size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink) {
     const DecodeProblem p = mass_problem(B, H, H_kv, S_max, D, window, n_sink, 1.f);
     return decode_sizes_ok(p) ? decode_workspace(p, true) : 0;

@@ -168,6 +168,11 @@ size_t decode_workspace(const DecodeProblem& p, bool mass);
 dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
                        void* O, float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s);
 
+// Weights gathered per key over the last n_last queries (key_mass.cu): mass [B, Hkv, S].
+size_t key_mass_workspace();
+dfa_status tc_key_mass(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,
+                       cudaStream_t s);
+
 // Eviction from a cache (cache_evict.cu): strides in elements of elt bytes.
 struct EvictProblem {
     int B, Hkv, S, D, elt;

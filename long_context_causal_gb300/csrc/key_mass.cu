@@ -1,0 +1,457 @@
+// key_mass.cu -- attention weight gathered per key over a prompt, for sm_103a.
+//
+// mass[b, g, j] = sum over the heads h of group g and the queries i >= S - n_last
+// that see key j of exp(scale <q_ih, k_j> - lse_ih), with the window and sinks of
+// sink_fwd_tc.cu: the column sums of the softmax that the forward never forms.
+//
+// One product per pair, S^T = K Q^T, keys in the rows: an accumulator row is a
+// key's, so a thread adds up its key's weights in a register and no sum crosses
+// threads.  A CTA holds a block of 512 keys (four tiles of 128) in shared memory
+// and sweeps the heads of the group and the tiles of 128 queries that see it; each
+// query tile is loaded once for the four key tiles (16 bytes a cycle, a quarter of
+// what one key tile at a time would ask of the L2).  TMEM holds the four tiles'
+// scores, one warpgroup for each: while a warpgroup forms its weights the tensor
+// cores run the other three products.
+//
+// Roles (640 threads, one CTA per SM): warp 0 TMA producer of K and Q, warp 1 MMA
+// issuer, warp 2 TMEM owner, warp 3 the queries' -lse log2 e (-inf for rows past
+// the end: weight 0), warps 4-19 four warpgroups.
+//
+// Split.  A block's sweep is a list of steps (head, query tile); the steps of all
+// blocks, in order, are dealt to the CTAs in equal contiguous ranges.  How many
+// steps lie before a block is a sum of three linear pieces, so a CTA finds its
+// first step without a table.  A block that one CTA sweeps whole is written there;
+// of the others each CTA leaves 512 sums, which a second kernel adds up in the
+// order of the steps.  No atomics: the same bits on every call.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dfa {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 640;
+constexpr int BT = 128;                    // keys or queries per tile
+constexpr int kTiles = 4;                  // key tiles per block
+constexpr int kBlock = kTiles * BT;
+constexpr int kNSlots = 4;                 // query tiles whose lse are at hand
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kTileBytes = BT * D * 2;
+    static constexpr int kQSlots = D == 128 ? 3 : 4;
+    static constexpr int kOffQ = kTiles * kTileBytes;
+    static constexpr int kOffN = kOffQ + kQSlots * kTileBytes;
+    static constexpr int kOffBar = kOffN + kNSlots * BT * 4;
+    static constexpr int kSmem = kOffBar + 256;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Args {
+    int H, Hkv, G, S;
+    int window, n_sink;    // window <= S; n_sink 0 when the window covers every key
+    int q0, n_qt;          // first query; tiles of 128 from it on
+    int n_kb;              // key blocks per (batch, kv head)
+    int64_t steps;         // of all blocks, one per (head of the group, query tile)
+    int e1, c0;            // block kb is seen by tiles [max(0, 4 kb - c0), min(n_qt, 4 kb + e1))
+    float scale_log2;
+    const float* lse;      // [B, H, S]
+    float* mass;           // [B, Hkv, S]
+    float* part;           // [2 * CTAs][kBlock]
+    int* err;
+};
+
+// sum over k < K of max(0, 4 k + c)
+__host__ __device__ inline int64_t ramp(int64_t K, int64_t c) {
+    const int64_t k0 = c > 0 ? 0 : -c / 4 + 1;          // the first k with 4 k + c > 0
+    return K > k0 ? (K - k0) * (c + 2 * (k0 + K - 1)) : 0;
+}
+// Query tiles that see the blocks before K, all counted.
+__host__ __device__ inline int64_t tiles_before(const Args& a, int64_t K) {
+    int64_t x = ramp(K, a.e1) - ramp(K, a.e1 - a.n_qt) - ramp(K, -a.c0);
+    if (K > 0 && a.n_sink > 0) x += a.n_qt - min(a.n_qt, max(a.e1, 0));     // all of them see block 0
+    return x;
+}
+// The tiles that see a block: [first, last).
+__host__ __device__ inline void tiles_of(const Args& a, int kb, int& first, int& last) {
+    first = max(0, 4 * kb - a.c0);
+    last = kb == 0 && a.n_sink > 0 ? a.n_qt : min(a.n_qt, 4 * kb + a.e1);
+}
+
+// Position in the list of steps: block kb of row r = b * Hkv + g, head h of the group, query tile t.
+struct Cursor {
+    int r, kb, h, t, first, last;
+    __device__ __forceinline__ void find(const Args& a, int64_t x) {
+        const int64_t per_row = tiles_before(a, a.n_kb) * a.G;
+        r = (int)(x / per_row);
+        x -= r * per_row;
+        int lo = 0, hi = a.n_kb - 1;                    // the last block that begins at or before x and is not empty
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (tiles_before(a, mid) * a.G <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        kb = lo;
+        tiles_of(a, kb, first, last);
+        const int at = (int)(x - tiles_before(a, kb) * a.G);
+        h = at / (last - first);
+        t = first + at % (last - first);
+    }
+    // To the next step; the caller knows that there is one.  True if it is another block's.
+    __device__ __forceinline__ bool next(const Args& a) {
+        if (++t < last) return false;
+        t = first;
+        if (++h < a.G) return false;
+        h = 0;
+        do {
+            if (++kb == a.n_kb) kb = 0, ++r;
+            tiles_of(a, kb, first, last);
+        } while (last <= first);
+        t = first;
+        return true;
+    }
+    __device__ __forceinline__ int row0(const Args& a) const { return a.q0 + t * BT; }
+    // Whether a key tile has a pair that is visible in this step.
+    __device__ __forceinline__ bool sees(const Args& a, int w) const {
+        const int k0 = kb * kBlock + w * BT, i0 = row0(a);
+        return k0 < a.S && min(i0 + BT, a.S) > k0 && (i0 - k0 < BT + a.window - 1 || k0 < a.n_sink);
+    }
+    // 32 columns each that hold queries
+    __device__ __forceinline__ int chunks(const Args& a) const { return min(4, (a.S - row0(a) + 31) / 32); }
+};
+
+// Weights of 32 queries for this thread's key: 2^(s c + n), n the queries' -lse log2 e;
+// see: the queries that see the key.
+__device__ __forceinline__ void add32(uint64_t (&acc)[2], const uint32_t (&u)[32], float c, const float* n) {
+    const uint64_t cc = pack_f32x2(c, c);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(n + e);
+        const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), cc, pack_f32x2(m.x, m.y)));
+        const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])), cc, pack_f32x2(m.z, m.w)));
+        acc[0] = add_f32x2(acc[0], pack_f32x2(ex2(x.x), ex2(x.y)));
+        acc[1] = add_f32x2(acc[1], pack_f32x2(ex2(y.x), ex2(y.y)));
+    }
+}
+__device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t see) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : 0xff800000u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const Args a) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {            // the swizzled tiles need a 1 KB aligned base
+        if (threadIdx.x == 0 && a.err) atomicExch(a.err, 2);
+        return;
+    }
+    uint8_t *sK = smem, *sQ = smem + C::kOffQ;
+    float* sN = reinterpret_cast<float*>(smem + C::kOffN);                // [kNSlots][128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* k_full = bars + 0;             // [kTiles]
+    uint64_t* k_empty = bars + 4;            // one for the block
+    uint64_t* s_full = bars + 5;             // [kTiles]
+    uint64_t* s_free = bars + 9;             // [kTiles]
+    uint64_t* q_full = bars + 13;            // [kQSlots]
+    uint64_t* q_empty = bars + 17;
+    uint64_t* n_full = bars + 21;            // [kNSlots]
+    uint64_t* n_empty = bars + 25;
+    uint64_t* done = bars + 29;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 31);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kTiles; ++w) {
+            mbar_init(&k_full[w], 1);
+            mbar_init(&s_full[w], 1);
+            mbar_init(&s_free[w], 4);
+        }
+        mbar_init(k_empty, 1);
+        for (int s = 0; s < C::kQSlots; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+        }
+        for (int s = 0; s < kNSlots; ++s) {
+            mbar_init(&n_full[s], 1);
+            mbar_init(&n_empty[s], 4 * kTiles);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t begin = a.steps * blockIdx.x / gridDim.x, end = a.steps * (blockIdx.x + 1) / gridDim.x;
+    const int n = (int)(end - begin);        // at least one: the grid is no larger than the list
+    Cursor c;
+    c.find(a, begin);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer of K and Q
+        uint32_t blocks = 0;
+        bool ok = true, fresh = true;
+        int i = 0;
+        for (; i < n && ok; ++i) {
+            if (fresh) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(k_empty, (blocks & 1) ^ 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                if (lane == 0) {
+                    for (int w = 0; w < kTiles; ++w) {
+                        const int k0 = c.kb * kBlock + w * BT;
+                        if (k0 >= a.S) {
+                            mbar_arrive(&k_full[w]);
+                            continue;
+                        }
+                        mbar_arrive_expect_tx(&k_full[w], C::kTileBytes);
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            tma_load_4d(sK + w * C::kTileBytes + blk * 16384, &tmK, &k_full[w], blk * 64, c.r % a.Hkv, k0,
+                                        c.r / a.Hkv);
+                    }
+                }
+                __syncwarp();
+                ++blocks;
+            }
+            const int slot = i % C::kQSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait_acc(&q_empty[slot], ((i / C::kQSlots) & 1) ^ 1, abort_flag, a.err, nullptr));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full[slot], C::kTileBytes);
+                for (int blk = 0; blk < D / 64; ++blk)
+                    tma_load_4d(sQ + slot * C::kTileBytes + blk * 16384, &tmQ, &q_full[slot], blk * 64,
+                                c.r % a.Hkv * a.G + c.h, c.row0(a), c.r / a.Hkv);
+            }
+            __syncwarp();
+            fresh = i + 1 < n && c.next(a);
+        }
+        if (!ok && lane == 0) {
+            // Aborted: let the copies already issued land before the CTA exits.
+            int dummy = 0;
+            if (blocks > 0)
+                for (int w = 0; w < kTiles; ++w) mbar_wait(&k_full[w], (blocks - 1) & 1, &dummy, nullptr);
+            for (int m = max(i - C::kQSlots, 0); m < i; ++m)
+                mbar_wait(&q_full[m % C::kQSlots], (m / C::kQSlots) & 1, &dummy, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (one lane of a converged warp)
+        const uint32_t lead = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);      // uniform
+        const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        constexpr uint64_t kStep = C::kTileBytes >> 4;
+        uint32_t blocks = 0, used[kTiles] = {0, 0, 0, 0};
+        bool ok = true, fresh = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && mbar_wait_issuer(bar, parity, abort_flag, a.err);
+            if (ok) tc_fence_after();
+            return ok;
+        };
+        for (int i = 0; i < n && ok; ++i) {
+            const int slot = i % C::kQSlots;
+            if (!wait(&q_full[slot], (i / C::kQSlots) & 1)) break;
+            const uint32_t id = idesc_bf16_f32(BT, 32 * c.chunks(a), false, false);
+#pragma unroll
+            for (int w = 0; w < kTiles; ++w) {
+                if (fresh && !wait(&k_full[w], blocks & 1)) break;
+                if (!c.sees(a, w)) continue;
+                if (!wait(&s_free[w], (used[w] & 1) ^ 1)) break;
+                ++used[w];
+                const uint64_t a0 = dK + w * kStep, b0 = dQ + slot * kStep;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                    mma_ss_lead(lead, tm + w * BT, a0 + off, b0 + off, id, kk > 0);
+                }
+                mma_commit_lead(lead, &s_full[w]);
+            }
+            if (!ok) break;
+            mma_commit_lead(lead, &q_empty[slot]);
+            if (fresh) ++blocks;
+            fresh = i + 1 < n && c.next(a);
+            if (fresh) mma_commit_lead(lead, k_empty);
+        }
+        // Drain: every MMA issued here has finished before TMEM is freed.
+        mma_commit_lead(lead, done);
+        int dummy = 0;
+        mbar_wait(done, 0, &dummy, a.err);
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ -lse log2 e of the queries
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int slot = i % kNSlots;
+            float x[4];
+            const float* lse = a.lse + ((int64_t)(c.r / a.Hkv) * a.H + c.r % a.Hkv * a.G + c.h) * a.S;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = c.row0(a) + e * 32 + lane;
+                const float l = row < a.S ? lse[row] : -INFINITY;
+                x[e] = l == -INFINITY ? l : -l * kLog2e;      // no such query, or one that sees nothing: weight 0
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait_acc(&n_empty[slot], ((i / kNSlots) & 1) ^ 1, abort_flag, a.err, nullptr));
+            if (!ok) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sN[slot * BT + e * 32 + lane] = x[e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&n_full[slot]);
+            if (i + 1 < n) c.next(a);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ weights: a warpgroup per key tile, a thread per key
+        const int w = (warp - 4) / 4, row = w * BT + (warp % 4) * 32 + lane;
+        const uint32_t tS = tmem + ((uint32_t)((warp % 4) * 32) << 16) + w * BT;
+        uint32_t used = 0;
+        bool from_start = c.h == 0 && c.t == c.first;
+        float total = 0.f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int slot = i % kNSlots;
+            const bool sees = c.sees(a, w);
+            ok = mbar_wait_acc(&n_full[slot], (i / kNSlots) & 1, abort_flag, a.err, nullptr);
+            if (sees) ok = ok && mbar_wait_acc(&s_full[w], used & 1, abort_flag, a.err, nullptr);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (sees) {
+                ++used;
+                tc_fence_after();
+                const float* nl = sN + slot * BT;
+                const int i0 = c.row0(a), key = c.kb * kBlock + row, k0 = c.kb * kBlock + w * BT, chunks = c.chunks(a);
+                uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
+                if (chunks == 4 && k0 + BT - 1 <= i0 && (i0 + BT - 1 - k0 < a.window)) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32_async(tS, x);
+                    tmem_wait_ld32(x);
+                    tmem_ld32_async(tS + 32, y);
+                    add32(acc, x, a.scale_log2, nl);
+                    tmem_wait_ld32(y);
+                    tmem_ld32_async(tS + 64, x);
+                    add32(acc, y, a.scale_log2, nl + 32);
+                    tmem_wait_ld32(x);
+                    tmem_ld32_async(tS + 96, y);
+                    add32(acc, x, a.scale_log2, nl + 64);
+                    tmem_wait_ld32(y);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[w]);
+                    add32(acc, y, a.scale_log2, nl + 96);
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < chunks; ++q) {
+                        uint32_t x[32];
+                        tmem_ld32(tS + q * 32, x);
+                        // query i sees key j iff j <= i and (i < j + window or j < n_sink)
+                        const int at = key - (i0 + q * 32);
+                        mask32(x, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
+                        add32(acc, x, a.scale_log2, nl + q * 32);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[w]);
+                }
+                total += sum_f32x2(add_f32x2(acc[0], acc[1]));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&n_empty[slot]);
+            const int r = c.r, key = c.kb * kBlock + row;
+            const bool last_step = c.h == a.G - 1 && c.t == c.last - 1;
+            if (last_step || i + 1 == n) {
+                if (last_step && from_start) {
+                    if (key < a.S) a.mass[(int64_t)r * a.S + key] = total;
+                } else {
+                    a.part[(int64_t)(2 * blockIdx.x + from_start) * kBlock + row] = total;
+                }
+                total = 0.f;
+                from_start = true;
+            }
+            if (i + 1 < n) c.next(a);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// A block per key block: what no query sees is 0, what several CTAs swept is added up.
+__global__ void __launch_bounds__(kBlock)
+join_kernel(const Args a, int grid) {
+    wait_for_previous_kernel();
+    const int r = blockIdx.x / a.n_kb, kb = blockIdx.x % a.n_kb, key = kb * kBlock + threadIdx.x;
+    int first, last;
+    tiles_of(a, kb, first, last);
+    float sum = 0.f;
+    if (last > first) {
+        const int64_t x0 = (r * tiles_before(a, a.n_kb) + tiles_before(a, kb)) * a.G, x1 = x0 + (int64_t)(last - first) * a.G - 1;
+        // the CTA that holds step x is the last one whose range begins at or before it
+        const int c0 = (int)(((x0 + 1) * grid - 1) / a.steps), c1 = (int)(((x1 + 1) * grid - 1) / a.steps);
+        if (c0 == c1) return;                  // written by the CTA itself
+        for (int c = c0; c <= c1; ++c) sum += a.part[(int64_t)(2 * c + (c == c0)) * kBlock + threadIdx.x];
+    }
+    if (key < a.S) a.mass[(int64_t)r * a.S + key] = sum;
+}
+
+template <int D>
+dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,
+                  cudaStream_t s) {
+    CUtensorMap mq, mk;
+    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, (int64_t)p.S * p.H * D, (int64_t)p.H * D, D) ||
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, (int64_t)p.S * p.Hkv * D, (int64_t)p.Hkv * D, D))
+        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+    Args a{};
+    a.H = p.H; a.Hkv = p.Hkv; a.G = p.H / p.Hkv; a.S = p.S;
+    a.window = p.window; a.n_sink = p.n_sink;
+    a.q0 = p.S - n_last;
+    a.n_qt = (n_last + BT - 1) / BT;
+    a.n_kb = (p.S + kBlock - 1) / kBlock;
+    a.c0 = (a.q0 + BT - 1) / BT;
+    // the last tile that sees key 512 kb + 511: the last t with q0 + 128 t <= that + window - 1
+    const int64_t x = (int64_t)kBlock - 2 + p.window - a.q0;
+    a.e1 = (int)(x >= 0 ? x / BT : -((-x + BT - 1) / BT)) + 1;
+    a.steps = (int64_t)p.B * p.Hkv * tiles_before(a, a.n_kb) * a.G;
+    a.scale_log2 = p.scale * kLog2e;
+    a.lse = lse; a.mass = mass;
+    a.part = static_cast<float*>(ws);
+    a.err = device_error_flag();
+    static std::atomic<uint64_t> seen{0};
+    auto kernel = key_mass_kernel<D>;
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "key_mass: kernel attributes");
+        mark_on_device(seen);
+    }
+    const int grid = (int)std::min<int64_t>(num_sms(), a.steps);
+    kernel<<<grid, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
+    e = launch_overlapped(join_kernel, dim3((unsigned)(p.B * p.Hkv * a.n_kb)), kBlock, 0, s, a, grid);
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass join launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_MASS, 2);
+    return DFA_OK;
+}
+
+}  // namespace
+
+size_t key_mass_workspace() { return sizeof(float) * 2 * (size_t)num_sms() * kBlock; }
+
+dfa_status tc_key_mass(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,
+                       cudaStream_t s) {
+    return p.D == 128 ? launch<128>(p, n_last, q, k, lse, mass, ws, s) : launch<64>(p, n_last, q, k, lse, mass, ws, s);
+}
+
+}  // namespace dfa

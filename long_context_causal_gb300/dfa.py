@@ -87,6 +87,8 @@ def _load() -> ctypes.CDLL:
         "dfa_attn_bwd_ckpt8_workspace_size": (sz, [i32] * 7),
         "dfa_attn_bwd_ckpt8": (i32, [vp, sz, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                      vp, vp, vp, vp, sz, vp]),
+        "dfa_attn_mass_workspace_size": (sz, [i32] * 5),
+        "dfa_attn_mass": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]),
         "dfa_attn_decode_mass_workspace_size": (sz, [i32] * 7),
         "dfa_attn_decode_mass": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, p64, vp, vp, i32, i32, f32, vp, vp, vp,
                                        vp, sz, vp]),
@@ -508,7 +510,7 @@ class _Native:
             "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
             "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
             "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size", "dfa_attn_decode_mass",
-            "dfa_attn_decode_mass_workspace_size", "dfa_cache_evict")))
+            "dfa_attn_decode_mass_workspace_size", "dfa_cache_evict", "dfa_attn_mass", "dfa_attn_mass_workspace_size")))
         vars(self).update((n, f) for n, f in vars(native).items() if not n.startswith("__"))
         return getattr(native, name)
 
@@ -550,6 +552,19 @@ def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: f
     (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
     GPU; returns (O [B,H,D], lse fp32 [B,H])."""
     return _result(_native.decode_sink(q, k, v, kv_len, window, n_sink, scale, O, lse, workspace_buf, stream))
+
+
+def dfa_attn_mass_workspace_size(B, H, H_kv, S, D) -> int:
+    return _lib.dfa_attn_mass_workspace_size(B, H, H_kv, S, D)
+
+
+def dfa_attn_mass(q, k, lse, window: int | None = None, n_sink: int = 0, n_last: int | None = None,
+                  scale: float | None = None, mass=None, workspace_buf=None, stream=None):
+    """Attention weight that each key drew from the last `n_last` queries (None: all)
+    of a sequence, over the heads of its group, from the forward's lse: q [B,S,H,D],
+    k [B,S,H_kv,D] bf16 dense, window and n_sink as in the forward (window None: plain
+    causal); returns mass fp32 [B,H_kv,S]."""
+    return _result(_native.mass(q, k, lse, window, n_sink, n_last, scale, mass, workspace_buf, stream))
 
 
 def dfa_attn_decode_mass_workspace_size(B, H, H_kv, S_max, D, window, n_sink) -> int:

@@ -42,6 +42,86 @@ def lens_of(lens):
     return torch.tensor(lens, dtype=torch.int32, device=DEV)
 
 
+# ------------------------------------------------------------------------------------------------ masses of a prompt
+# (B, H, Hkv, S, D, window, n_sink, n_last)
+MASS = [
+    (1, 1, 1, 1, 64, 1, 0, 1), (2, 2, 1, 2, 128, 1, 1, 2), (1, 4, 2, 31, 64, 31, 0, 7), (2, 4, 4, 127, 128, 127, 0, 127),
+    (1, 6, 2, 128, 64, 16, 4, 128), (3, 3, 3, 129, 128, 129, 0, 1), (2, 8, 2, 300, 64, 300, 0, 300), (1, 8, 1, 513, 128, 100, 128, 513),
+    (1, 4, 2, 700, 64, 1, 3, 700), (1, 2, 2, 1025, 128, 1025, 0, 64), (2, 6, 2, 1100, 64, 512, 17, 1099), (1, 5, 5, 1500, 128, 1500, 0, 1500),
+    (1, 8, 2, 2000, 64, 130, 1, 333), (1, 3, 1, 2500, 128, 700, 4, 2500), (1, 2, 1, 2600, 64, 2000, 0, 129), (1, 4, 2, 2048, 128, 128, 128, 2048),
+    (1, 1, 1, 4200, 64, 40, 9, 4200),
+]
+MASS_IDS = ["B{}H{}kv{}S{}D{}w{}s{}l{}".format(*c) for c in MASS]
+
+
+def prompt(case, seed):
+    B, H, Hkv, S, D, window, n_sink, n_last = case
+    q, k = rand(seed, B, S, H, D), rand(seed + 1, B, S, Hkv, D)
+    k[:, ::7] *= 2
+    lse = torch.from_numpy(sink.attn_fwd(np64(q), np64(k), np64(k), window, n_sink)[1]).float().to(DEV)
+    return q, k, lse
+
+
+def poison(case, q, k, lse):
+    """NaN in what no counted query needs: earlier queries and their lse, and the keys that none of the others sees."""
+    B, H, Hkv, S, D, window, n_sink, n_last = case
+    q, k, lse = q.clone(), k.clone(), lse.clone()
+    q[:, :S - n_last], lse[:, :, :S - n_last] = NAN, NAN
+    k[:, torch.from_numpy(~sink.visible(S, window, n_sink)[S - n_last:].any(0)).to(DEV)] = NAN
+    return q, k, lse
+
+
+@pytest.mark.parametrize("case", MASS, ids=MASS_IDS)
+def test_mass(case):
+    window, n_sink, n_last = case[5:]
+    q, k, lse = prompt(case, 51)
+    ref = cache.mass(np64(q), np64(k), np64(lse), window, n_sink, n_last)
+    bad = poison(case, q, k, lse)
+    ws = torch.full((dfa.dfa_attn_mass_workspace_size(*case[:5]),), 0xFF, dtype=torch.uint8, device=DEV)
+    got = dfa.dfa_attn_mass(*bad, window, n_sink, n_last, workspace_buf=ws)
+    dfa.dfa_check_errors()
+    # a score is a sum of D products, its weight off by F / 2 relative; the sums by a quarter of F
+    close(got, ref, F * ref, "mass")
+    assert torch.equal(got, dfa.dfa_attn_mass(q, k, lse, window, n_sink, n_last))
+
+
+def test_mass_what_it_must_not_trip_over():
+    """A row that sees nothing (lse = -inf) counts for nothing; a NaN query reaches the keys that it sees and no others;
+    weights far above and below one; a scale of the caller's."""
+    case = (1, 2, 1, 900, 64, 200, 3, 900)
+    q, k, lse = prompt(case, 53)
+    lse[0, 1, 700] = -float("inf")
+    got = dfa.dfa_attn_mass(q, k, lse, 200, 3)
+    ref = cache.mass(np64(q), np64(k), np.where(np64(lse) == -np.inf, np.inf, np64(lse)), 200, 3, 900)
+    close(got, ref, F * ref, "mass")
+    q[0, 500, 0] = NAN
+    with_nan, seen = dfa.dfa_attn_mass(q, k, lse, 200, 3)[0, 0], torch.from_numpy(sink.visible(900, 200, 3)[500]).to(DEV)
+    assert with_nan[seen].isnan().all() and torch.equal(with_nan[~seen], got[0, 0][~seen])
+    q, k, lse = prompt(case, 54)
+    got = dfa.dfa_attn_mass(q, k, lse - 40, 200, 3, scale=0.5)
+    ref = cache.mass(np64(q), np64(k), np64(lse) - 40, 200, 3, 900, 0.5)
+    close(got, ref, F * ref, "mass")
+
+
+def test_mass_of_many_heads_and_blocks():
+    """More blocks than SMs, most of them swept whole, and a few that many CTAs share: every query gives away one."""
+    from long_context_causal_gb300.inputs import make
+    for B, H, Hkv, S, D, window, n_sink in ((2, 8, 4, 30000, 64, 700, 5), (1, 4, 2, 20001, 128, 20001, 0), (70, 4, 4, 515, 64, 515, 0)):
+        q, k, v, _ = make(B, H, Hkv, S, D, torch.bfloat16, device=DEV, seed=55)
+        O, lse = dfa.dfa_attn_fwd_sink(q, k, v, window, n_sink)
+        for n_last in (S, 1000 if S > 1000 else 1):
+            got = dfa.dfa_attn_mass(q, k, lse, window, n_sink, n_last)
+            dfa.dfa_check_errors()
+            np.testing.assert_allclose(np64(got).sum((1, 2)), H * n_last, rtol=4 * F)
+            # keys of every block against the definition, all queries that see them
+            for j in list(range(0, S, S // 9 + 1)) + [0, S - 1]:
+                lo = max(j, S - n_last)
+                i = torch.arange(lo, max(lo, S if j < n_sink else min(j + window, S)), device=DEV)
+                s = torch.einsum("bihd,bhd->bhi", q[:, i].double(), k[:, j].double().repeat_interleave(H // Hkv, 1)) * D ** -0.5
+                w = torch.exp(s - lse[:, :, i].double()).sum(2).reshape(B, Hkv, -1).sum(2)
+                close(got[:, :, j], np64(w), 2 * F * np64(w), "mass")
+
+
 # ------------------------------------------------------------------------------------------------ single tokens with masses
 # (B, H, Hkv, S, D, window, n_sink, lens)
 STEP = [

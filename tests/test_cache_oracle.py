@@ -79,6 +79,30 @@ REFUSED = [(dict(dt=0), dfa.DFA_ERR_UNSUPPORTED), (dict(dt=5), dfa.DFA_ERR_INVAL
            (dict(n_sink=129), dfa.DFA_ERR_UNSUPPORTED)]
 
 
+def mass(**kw):
+    a = dict(q=FAR[0], k=FAR[1], lse=FAR[2], dt=1, B=2, H=4, Hkv=2, S=300, D=128, window=64, n_sink=4, n_last=300, scale=0.1, m=FAR[3],
+             ws=FAR[4], wn=1 << 40)
+    a.update(kw)
+    return lib.dfa_attn_mass(*(a[x] for x in ("q", "k", "lse", "dt", "B", "H", "Hkv", "S", "D", "window", "n_sink", "n_last", "scale",
+                                              "m", "ws", "wn")), None)
+
+
+@pytest.mark.parametrize("kw,code", REFUSED + [
+    (dict(S=-1), dfa.DFA_ERR_INVALID_ARG), (dict(n_last=0), dfa.DFA_ERR_INVALID_ARG), (dict(S=0, n_last=-3), dfa.DFA_ERR_INVALID_ARG),
+    (dict(B=1 << 14, H=1 << 10, Hkv=1), dfa.DFA_ERR_INVALID_ARG), (dict(q=MIS), dfa.DFA_ERR_INVALID_ARG), (dict(k=None), dfa.DFA_ERR_INVALID_ARG),
+    (dict(lse=A + 2), dfa.DFA_ERR_INVALID_ARG), (dict(m=None), dfa.DFA_ERR_INVALID_ARG), (dict(m=FAR[0]), dfa.DFA_ERR_INVALID_ARG),
+    (dict(m=FAR[2] + 4), dfa.DFA_ERR_INVALID_ARG), (dict(ws=None), dfa.DFA_ERR_WORKSPACE), (dict(ws=MIS), dfa.DFA_ERR_INVALID_ARG),
+    (dict(wn=dfa.dfa_attn_mass_workspace_size(2, 4, 2, 300, 128) - 1), dfa.DFA_ERR_WORKSPACE)])
+def test_mass_refusals(kw, code):
+    assert mass(**kw) == code and dfa.dfa_last_error()
+
+
+def test_mass_of_nothing_and_size_queries():
+    assert mass(B=0, q=None, k=None, lse=None, m=None, ws=None, wn=0) == dfa.DFA_OK
+    assert mass(S=0, q=None, k=None, lse=None, m=None, ws=None, wn=0) == dfa.DFA_OK
+    assert dfa.dfa_attn_mass_workspace_size(1, 4, 2, 300, 80) == 0 and dfa.dfa_attn_mass_workspace_size(1, 4, 3, 300, 64) == 0
+
+
 @pytest.mark.parametrize("kw,code", REFUSED + [
     (dict(S=0), dfa.DFA_ERR_INVALID_ARG), (dict(B=8193), dfa.DFA_ERR_UNSUPPORTED), (dict(n=None), dfa.DFA_ERR_INVALID_ARG),
     (dict(mo=None), dfa.DFA_ERR_INVALID_ARG), (dict(m=A + 2), dfa.DFA_ERR_INVALID_ARG), (dict(mo=A + 1), dfa.DFA_ERR_INVALID_ARG),
@@ -144,6 +168,12 @@ def test_the_binding_refuses_cache_tensors():
     for call in (lambda: dfa.dfa_attn_decode_mass(q, k, k, n), lambda: dfa.dfa_cache_evict(k, k, n, m, 4)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+    lse = t(2, 4, 8, dtype=torch.float32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfa.dfa_attn_mass(t(2, 8, 4, 64), k, lse)
+    for bad in ((q, k), (t(2, 8, 4, 64), k[:, :4]), (t(2, 8, 4, 128), k)):
+        with pytest.raises(ValueError, match="must be"):
+            dfa.dfa_attn_mass(*bad, lse)
     for bad in ((q[:1], k, k), (q, k[0], k[0]), (q, k, t(2, 8, 2, 128)), (t(2, 4, 128), k, k)):
         with pytest.raises(ValueError, match="must be"):
             dfa.dfa_attn_decode_mass(*bad, n)
