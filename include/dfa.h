@@ -285,6 +285,25 @@ dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa
                                 int n_sink, float scale, void* O, float* lse, void* workspace, size_t ws_bytes,
                                 void* stream);
 
+/* One new token for each sequence of a batch that shares its first P keys and
+ * values: the query of sequence b stands behind the prefix and its own n = kv_len[b]
+ * rows and sees all of both.  The prefix is read once per 256 queries of a key/value
+ * head (sequences x heads of the group), not once per sequence.
+ *   q, O:      [B, H, D] dense, bf16;  lse: fp32 [B, H]
+ *   k_prefix, v_prefix: [P, H_kv, D] with element strides prefix_strides = {token,
+ *              head} (shared; NULL: dense); P = 0: none (the pointers may be NULL)
+ *   k, v, kv_strides, kv_len: the sequences' own caches, as dfa_attn_decode_sink
+ *              (0 own rows: the prefix alone; none at all: O = 0, lse = -inf)
+ *   workspace: >= dfa_attn_decode_prefix_workspace_size() bytes, 16-byte aligned,
+ *              contents not preserved; calls that can overlap need one each
+ * Cache rows behind kv_len may hold anything.  bf16 only, D in {64, 128}, at most 8192
+ * sequences.  Two or three launches; may be captured; the same bits on every call. */
+size_t dfa_attn_decode_prefix_workspace_size(int B, int H, int H_kv, int P, int D);
+dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                                  dfa_dtype dt, int B, int H, int H_kv, int P, int S_max, int D,
+                                  const int64_t* prefix_strides, const int64_t* kv_strides, const int32_t* kv_len,
+                                  float scale, void* O, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* Attention weights gathered per key: the mass of a key of key/value head g is the
  * sum of the weights that queries gave it, over the query heads of the group.
  * Over a prompt, from the forward's q, k and saved lse:

@@ -46,6 +46,8 @@ struct Entry {
     decltype(&dfa_cache_evict) evict;
     decltype(&dfa_attn_mass) mass;
     decltype(&dfa_attn_mass_workspace_size) mass_bytes;
+    decltype(&dfa_attn_decode_prefix) decode_prefix;
+    decltype(&dfa_attn_decode_prefix_workspace_size) decode_prefix_bytes;
 } g;
 
 struct ValueErr {
@@ -304,6 +306,33 @@ PyObject* decode(PyObject* const* a) {
     return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
 }
 
+PyObject* decode_prefix(PyObject* const* a) {
+    const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_prefix"), &vp = tensor(a[2], "v_prefix"), &k = tensor(a[3], "k"),
+                     &v = tensor(a[4], "v");
+    const Cache c = cache_of(q, k, v);
+    if (kp.dim() != 3 || kp.sizes() != vp.sizes() || kp.size(1) != c.Hkv || kp.size(2) != c.D)
+        throw ValueErr{"k_prefix and v_prefix must be [P, H_kv, D] like k and v, got " + shape_of(kp) + ", " + shape_of(vp)};
+    if (kp.scalar_type() != q.scalar_type() || vp.scalar_type() != q.scalar_type())
+        throw ValueErr{"the prefix must have the dtype of q"};
+    if (kp.strides() != vp.strides() || kp.stride(2) != 1)
+        throw ValueErr{"k_prefix and v_prefix must share their strides, with the head dimension contiguous"};
+    const int d = on_gpu({&q, &kp, &vp, &k, &v});
+    const at::Device dev = q.device();
+    const int H = small(q.size(1)), P = small(kp.size(0));
+    const at::Tensor len = given(a[5], "kv_len", {c.B}, at::kInt, dev);
+    const Stream s = stream_of(a[10], d);
+    at::Tensor O = output(a[7], "O", q.sizes(), q.scalar_type(), dev, s);
+    at::Tensor lse = output(a[8], "lse", {c.B, H}, at::kFloat, dev, s);
+    const at::Tensor ws = bytes(a[9], "workspace_buf", a[9] == Py_None ? g.decode_prefix_bytes(c.B, H, c.Hkv, P, c.D) : 0, dev, s);
+    hold(s, {&q, &kp, &vp, &k, &v, &len, &O, &lse, &ws});
+    const int64_t strides[2] = {kp.stride(0), kp.stride(1)};
+    const dfa_status st = without_gil(g.decode_prefix, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                      dtype_of(q), c.B, H, c.Hkv, P, c.S, c.D, &strides[0], &c.strides[0],
+                                      static_cast<const int32_t*>(len.data_ptr()), scale_of(a[6], c.D), O.data_ptr(),
+                                      static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), s.handle);
+    return st ? PyLong_FromLong(st) : pack({std::move(O), std::move(lse)});
+}
+
 PyObject* mass(PyObject* const* a) {
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
     const Sequence z = sequence(q, k, k);
@@ -500,6 +529,7 @@ PyMethodDef methods[] = {{"bind", FAST(bind)},
                          {"bwd_ckpt8", FAST((call<bwd_ckpt, 12>))},
                          {"mass", FAST((call<mass, 10>))},
                          {"decode_mass", FAST((call<decode_mass, 13>))},
+                         {"decode_prefix", FAST((call<decode_prefix, 11>))},
                          {"cache_evict", FAST((call<evict, 13>))},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dfa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

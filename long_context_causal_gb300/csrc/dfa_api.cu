@@ -1058,6 +1058,41 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
     return sink_decode(p, q, k, v, kv_len, O, lse, nullptr, nullptr, workspace, static_cast<cudaStream_t>(stream));
 }
 
+static dfa_status check_prefix(dfa_dtype dt, const DecodeProblem& p, int P) {
+    dfa_status st = check_decode(dt, p);
+    if (st) return st;
+    if (P < 0) return fail(DFA_ERR_INVALID_ARG, "negative prefix length");
+    if (P > (1 << 30)) return fail(DFA_ERR_INVALID_ARG, "problem too large (prefix of %d tokens)", P);
+    return DFA_OK;
+}
+
+extern "C" size_t dfa_attn_decode_prefix_workspace_size(int B, int H, int H_kv, int P, int D) {
+    const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
+    return decode_sizes_ok(p) && P >= 0 && P <= (1 << 30) ? prefix_workspace(p, P) : 0;
+}
+
+extern "C" dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                                             const void* v, dfa_dtype dt, int B, int H, int H_kv, int P, int S_max, int D,
+                                             const int64_t* prefix_strides, const int64_t* kv_strides,
+                                             const int32_t* kv_len, float scale, void* O, float* lse, void* workspace,
+                                             size_t ws_bytes, void* stream) {
+    g_msg[0] = 0;
+    DecodeProblem p = decode_problem(B, H, H_kv, S_max, D, std::max(S_max, 1), 0, scale);
+    dfa_status st = check_prefix(dt, p, P);
+    if (st || B == 0 || (st = take_strides(p, kv_strides))) return st;
+    int64_t ss = (int64_t)H_kv * D, sh = D;
+    if (prefix_strides) {
+        ss = prefix_strides[0], sh = prefix_strides[1];
+        for (int64_t x : {ss, sh})
+            if (x < 0 || x % 8 != 0) return fail(DFA_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+        if ((st = check_broadcast(1, P, H_kv, 0, ss, sh))) return st;
+    }
+    if ((st = check_ws(workspace, ws_bytes, prefix_workspace(p, P)))) return st;
+    if ((st = check_ptrs({q, k, v, O})) || (P > 0 && (st = check_ptrs({k_prefix, v_prefix})))) return st;
+    if (!aligned4({kv_len, lse})) return fail(DFA_ERR_INVALID_ARG, "kv_len and lse must be 4-byte aligned pointers");
+    return prefix_decode(p, P, q, k_prefix, v_prefix, ss, sh, k, v, kv_len, O, lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- attention weights gathered per key, eviction
 namespace {
 

@@ -168,6 +168,25 @@ size_t decode_workspace(const DecodeProblem& p, bool mass);
 dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
                        void* O, float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s);
 
+// Single tokens behind a shared prefix.  The prefix's part (prefix_decode.cu): the
+// B G queries of a key/value head are rows, pairs of 128-row tiles of a head are
+// segments, and the key tiles of all segments are dealt to `grid` CTAs in equal
+// contiguous ranges.  Part (segment s, CTA c, z) is slab 2 (s + c) + z; z is the
+// row's tile of the pair, or where the pair has one tile both z hold a part of it.
+struct PrefixPlan {
+    int P, rows, row_stride;      // keys; rows per head; rows per slab
+    int n_pairs, n_kt, n_seg;     // segments per head, key tiles, segments
+    int grid, slabs;              // 0 without keys
+    int64_t steps;
+};
+PrefixPlan prefix_plan(int B, int G, int Hkv, int P, int sms);
+dfa_status tc_prefix(const DecodeProblem& p, const PrefixPlan& plan, const void* q, const void* kp, const void* vp, int64_t ss,
+                     int64_t sh, float* part, float2* stat, cudaStream_t s);
+// Both parts and their join (sink_decode.cu); ss, sh: the prefix's strides.
+size_t prefix_workspace(const DecodeProblem& p, int P);
+dfa_status prefix_decode(const DecodeProblem& p, int P, const void* q, const void* kp, const void* vp, int64_t ss, int64_t sh,
+                         const void* k, const void* v, const int32_t* kv_len, void* O, float* lse, void* ws, cudaStream_t s);
+
 // Weights gathered per key over the last n_last queries (key_mass.cu): mass [B, Hkv, S].
 size_t key_mass_workspace();
 dfa_status tc_key_mass(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,

@@ -297,6 +297,10 @@ __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cl
 // overlap that one's end (programmatic stream serialization).
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets a kernel that was launched to overlap this one start as soon as every CTA
+// has come here and there is room on an SM.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 // Allocates `ncols` TMEM columns (power of two >= 32); whole warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {

@@ -85,7 +85,10 @@ struct Args {
     int stride;                   // 64 * the most tiles of a segment
     const float* mass;            // [B, Hkv, S], null: zero
     float* mass_out;              // [B, Hkv, S]; may be `mass`
+    // PARTS: a segment that one CTA covers leaves its rows' parts here, [B * H][D + 2]
+    float* own;
 };
+enum Mode { kPlain, kMass, kParts };
 
 // The visible keys of a sequence as tiles: the sinks' tiles, if the window has
 // moved off them, then the window's.
@@ -160,7 +163,7 @@ __device__ __forceinline__ void next_segment(const Args& a, Cursor& c) {
     }
 }
 
-template <int D, bool CLUSTER, bool MASS>
+template <int D, bool CLUSTER, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
     using C = Cfg<D>;
@@ -226,7 +229,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
         const int total = prefix[a.B];
         const int n_ctas = min((int)gridDim.x, total);   // every one of them has a tile
-        if ((int)blockIdx.x >= n_ctas) return;
+        if ((int)blockIdx.x >= n_ctas) {
+            if (MODE == kParts && blockIdx.x == 0) wait_for_previous_kernel();
+            return;
+        }
         begin = (int)((int64_t)total * blockIdx.x / n_ctas);
         end = (int)((int64_t)total * (blockIdx.x + 1) / n_ctas);
         c = find(a, prefix, begin);
@@ -260,6 +266,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, &dummy, nullptr);
         }
         __syncwarp();
+        // PARTS: started beside the prefix's kernel.  What joins the parts waits for this
+        // one to end, and through its first CTA for that one.
+        if (MODE == kParts && blockIdx.x == 0) wait_for_previous_kernel();
         if constexpr (CLUSTER) {
             cluster_sync();
             cluster_sync();
@@ -329,7 +338,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         s[z][e] *= a.scale_log2;
                         if (8 * z + t + 4 * (e & 1) >= n) s[z][e] = -INFINITY;
                     }
-                if constexpr (MASS) {
+                if constexpr (MODE == kMass) {
                     // keys 4 m + t of a head's 16 in lane t become 4 t .. 4 t + 3
                     const int64_t row = (int64_t)c.b * a.H + h0 + g;
                     const int at = k * KT + w16 + 4 * t;
@@ -423,6 +432,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         if (!ok) break;
         const bool whole = k0 == 0 && k1 == c.s.tiles;
         float* part = a.part + (int64_t)(2 * blockIdx.x + (k0 == 0)) * MH * (D + 2);
+        if (MODE == kParts && whole) part = a.own + ((int64_t)c.b * a.H + h0) * (D + 2);
         for (int y = threadIdx.x; y < nh * (D / 4); y += kConsumers * 32) {
             const int h = y / (D / 4), d = y % (D / 4) * 4;
             float m = -INFINITY, l = 0.f;
@@ -443,7 +453,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 const bool second = y >= kConsumers * 32;
                 mine[second] = acc;
                 mine_ml[second] = make_float2(m, l);
-            } else if (whole) {
+            } else if (MODE != kParts && whole) {
                 const float inv = 1.f / l;
                 const int64_t row = (int64_t)c.b * a.H + h0 + h;
                 *reinterpret_cast<uint2*>(a.O + row * D + d) =
@@ -566,6 +576,85 @@ join_kernel(const Args a, int grid) {
     if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
+// Joins the parts of a shared prefix and of the sequences' own keys: D / 2 threads
+// per row (sequence, head), one per pair of dims, prefix first, in the order of the keys.
+constexpr int kPrefixThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kPrefixThreads)
+prefix_join_kernel(const Args a, int grid, const PrefixPlan p, const float* part, const float2* stat) {
+    wait_for_previous_kernel();
+    const int64_t row = (int64_t)blockIdx.x * (kPrefixThreads / (D / 2)) + threadIdx.x / (D / 2);
+    if (row >= (int64_t)a.B * a.H) return;
+    const int d = threadIdx.x % (D / 2) * 2, b = (int)(row / a.H), h = (int)(row % a.H), gq = h / a.G, gi = h % a.G;
+    float m = -INFINITY, l = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    auto add = [&](const float2 (&st)[kJoinAhead], const float2 (&v)[kJoinAhead]) {
+        float n = m;
+#pragma unroll
+        for (int e = 0; e < kJoinAhead; ++e) n = fmaxf(n, st[e].x);
+        if (n == -INFINITY) return;
+        const float f = ex2(m - n);
+        m = n;
+        l *= f;
+        acc.x *= f;
+        acc.y *= f;
+#pragma unroll
+        for (int e = 0; e < kJoinAhead; ++e) {
+            const float g = ex2(st[e].x - n);
+            l = fmaf(st[e].y, g, l);
+            acc.x = fmaf(v[e].x, g, acc.x);
+            acc.y = fmaf(v[e].y, g, acc.y);
+        }
+    };
+    if (p.grid > 0) {
+        const int at = b * a.G + gi, tile = at / 128, r = at % 128, s = gq * p.n_pairs + tile / 2;
+        const bool alone = (tile & ~1) * 128 + 128 >= p.rows;       // the pair has this tile only: two parts
+        const int64_t x0 = (int64_t)s * p.n_kt, x1 = x0 + p.n_kt - 1;
+        const int c0 = (int)(((x0 + 1) * p.grid - 1) / p.steps), c1 = (int)(((x1 + 1) * p.grid - 1) / p.steps);
+        const int n = (c1 - c0 + 1) << alone;
+        for (int y = 0; y < n; y += kJoinAhead) {
+            float2 st[kJoinAhead], v[kJoinAhead];
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e) {
+                st[e] = make_float2(-INFINITY, 0.f);
+                v[e] = make_float2(0.f, 0.f);
+                if (y + e < n) {
+                    const int64_t slab = alone ? 2 * (int64_t)(s + c0) + y + e : 2 * (int64_t)(s + c0 + y + e) + (tile & 1);
+                    const int64_t z = slab * p.row_stride + r;
+                    st[e] = stat[z];
+                    if (st[e].y > 0.f) v[e] = *reinterpret_cast<const float2*>(part + z * D + d);   // else nothing was written
+                }
+            }
+            add(st, v);
+        }
+    }
+    const int R = a.Hkv * a.HB, rb = gq * a.HB + gi / MH;
+    const int64_t total = a.prefix[a.B], n_ctas = min((int64_t)grid, total);
+    const int before = a.prefix[b], tiles = (a.prefix[b + 1] - before) / R;
+    if (tiles > 0) {
+        const int64_t first = before + (int64_t)rb * tiles, last = first + tiles - 1;
+        const int c0 = (int)(((first + 1) * n_ctas - 1) / total), c1 = (int)(((last + 1) * n_ctas - 1) / total);
+        for (int c = c0; c <= c1; c += kJoinAhead) {
+            float2 st[kJoinAhead], v[kJoinAhead];
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e) {
+                st[e] = make_float2(-INFINITY, 0.f);
+                v[e] = make_float2(0.f, 0.f);
+                if (c + e <= c1) {
+                    const float* z = c0 == c1 ? a.own + row * (D + 2)
+                                              : a.part + ((int64_t)(2 * (c + e) + (c + e == c0)) * MH + gi % MH) * (D + 2);
+                    st[e] = *reinterpret_cast<const float2*>(z + D);
+                    v[e] = *reinterpret_cast<const float2*>(z + d);
+                }
+            }
+            add(st, v);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no keys at all
+    *reinterpret_cast<uint32_t*>(a.O + row * D + d) = pack_bf16(acc.x * inv, acc.y * inv);
+    if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
 // mass_out = mass + the step's weights: each visible key's 2^(score - lse log2 e), summed
 // over the heads of its group in their order.  0 behind the sequence.
 constexpr int kMassThreads = 256;
@@ -593,6 +682,8 @@ mass_kernel(const Args a, int blocks) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t prefix_bytes(const DecodeProblem& p) { return align256(sizeof(int) * ((size_t)p.B + 1)); }
+size_t own_bytes(const DecodeProblem& p) { return align256(sizeof(float) * (size_t)p.B * p.H * (p.D + 2)); }
+size_t stat_bytes(const PrefixPlan& x) { return align256(sizeof(float2) * 2 * (size_t)x.slabs * x.row_stride); }
 size_t part_bytes(const DecodeProblem& p) { return align256(sizeof(float) * 2 * (size_t)num_sms() * MH * (p.D + 2)); }
 
 dfa_status launch_mass(const Args& a, cudaStream_t s) {
@@ -603,14 +694,8 @@ dfa_status launch_mass(const Args& a, cudaStream_t s) {
     return DFA_OK;
 }
 
-template <int D, bool MASS>
-dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len, void* O,
-                  float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s) {
-    using C = Cfg<D>;
-    CUtensorMap mk, mv;
-    if (!make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, p.kv_sb, p.kv_ss, p.kv_sh, KT) ||
-        !make_tmap_bshd(&mv, v, p.B, p.S, p.Hkv, D, p.kv_sb, p.kv_ss, p.kv_sh, KT))
-        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+template <int D>
+Args make_args(const DecodeProblem& p, const void* q, const int32_t* kv_len, void* O, float* lse, void* ws) {
     Args a{};
     a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.G = p.H / p.Hkv; a.HB = (a.G + MH - 1) / MH;
     a.S = p.S; a.window = p.window; a.n_sink = p.n_sink;
@@ -622,6 +707,76 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     a.prefix = static_cast<int*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(p));
     a.err = device_error_flag();
+    return a;
+}
+
+template <int D>
+dfa_status make_maps(const DecodeProblem& p, const void* k, const void* v, CUtensorMap* mk, CUtensorMap* mv) {
+    if (!make_tmap_bshd(mk, k, p.B, p.S, p.Hkv, D, p.kv_sb, p.kv_ss, p.kv_sh, KT) ||
+        !make_tmap_bshd(mv, v, p.B, p.S, p.Hkv, D, p.kv_sb, p.kv_ss, p.kv_sh, KT))
+        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+    return DFA_OK;
+}
+
+template <int D>
+constexpr int most_smem() {
+    constexpr int most = Cfg<D>::kOffPrefix + (int)sizeof(int) * (kMaxDecodeBatch + 1);
+    static_assert(most <= 232448, "shared memory");
+    return most;
+}
+
+// The prefix's part, the own keys' part beside it, and the join.
+template <int D>
+dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const void* kp, const void* vp, int64_t ss, int64_t sh,
+                         const void* k, const void* v, const int32_t* kv_len, void* O, float* lse, void* ws, cudaStream_t s) {
+    CUtensorMap mk, mv;
+    dfa_status st = make_maps<D>(p, k, v, &mk, &mv);
+    if (st) return st;
+    Args a = make_args<D>(p, q, kv_len, O, lse, ws);
+    const PrefixPlan plan = prefix_plan(p.B, a.G, p.Hkv, P, num_sms());
+    char* at = static_cast<char*>(ws) + prefix_bytes(p) + part_bytes(p);
+    a.own = reinterpret_cast<float*>(at);
+    at += own_bytes(p);
+    float2* stat = reinterpret_cast<float2*>(at);
+    float* part = reinterpret_cast<float*>(at + stat_bytes(plan));
+    auto own = decode_kernel<D, false, kParts>;
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem<D>()) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "decode: kernel attributes");
+        mark_on_device(seen);
+    }
+    if (plan.grid > 0 && (st = tc_prefix(p, plan, q, kp, vp, ss, sh, part, stat, s))) return st;
+    const int n = (int)std::min<int64_t>(num_sms(), (int64_t)p.B * a.Hkv * a.HB * decode_tiles(p));
+    const size_t smem = Cfg<D>::kOffPrefix + sizeof(int) * (p.B + 1);
+    cudaError_t e;
+    if (plan.grid > 0) {
+        // Beside the prefix's kernel, on SMs that it leaves or does not need: it starts when that one has, which is
+        // after all work before the call.
+        e = launch_overlapped(own, dim3((unsigned)n), kThreads, smem, s, mk, mv, a);
+    } else {
+        own<<<n, kThreads, smem, s>>>(mk, mv, a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+    constexpr int rows = kPrefixThreads / (D / 2);
+    e = launch_overlapped(prefix_join_kernel<D>, dim3((unsigned)(((int64_t)p.B * p.H + rows - 1) / rows)), kPrefixThreads, 0, s, a, n,
+                          plan, static_cast<const float*>(part), static_cast<const float2*>(stat));
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "prefix join launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_FWD);
+    count_launch(DFA_KERNEL_MERGE);
+    return DFA_OK;
+}
+
+template <int D, Mode MODE>
+dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len, void* O,
+                  float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s) {
+    using C = Cfg<D>;
+    constexpr bool MASS = MODE == kMass;
+    CUtensorMap mk, mv;
+    const dfa_status st = make_maps<D>(p, k, v, &mk, &mv);
+    if (st) return st;
+    Args a = make_args<D>(p, q, kv_len, O, lse, ws);
     if (MASS) {
         a.score = reinterpret_cast<float*>(static_cast<char*>(ws) + prefix_bytes(p) + part_bytes(p));
         a.stride = (int)(KT * decode_tiles(p));
@@ -634,8 +789,8 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     const int smem = C::kOffPrefix + (int)sizeof(int) * (p.B + 1);
     static std::atomic<uint64_t> seen{0};
     static std::atomic<int> clusters{0};             // that run at a time
-    auto spread = decode_kernel<D, false, MASS>;
-    auto clustered = decode_kernel<D, true, MASS>;
+    auto spread = decode_kernel<D, false, MODE>;
+    auto clustered = decode_kernel<D, true, MODE>;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
@@ -648,8 +803,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (first_on_device(seen)) {
-        constexpr int most = C::kOffPrefix + (int)sizeof(int) * (kMaxDecodeBatch + 1);
-        static_assert(most <= 232448, "shared memory");
+        constexpr int most = most_smem<D>();
         int k = 0;
         if (cudaFuncSetAttribute(spread, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
             cudaFuncSetAttribute(clustered, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
@@ -692,10 +846,21 @@ size_t decode_workspace(const DecodeProblem& p, bool mass) {
 dfa_status sink_decode(const DecodeProblem& p, const void* q, const void* k, const void* v, const int32_t* kv_len,
                        void* O, float* lse, const float* mass, float* mass_out, void* ws, cudaStream_t s) {
     if (mass_out)
-        return p.D == 128 ? launch<128, true>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s)
-                          : launch<64, true>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s);
-    return p.D == 128 ? launch<128, false>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s)
-                      : launch<64, false>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s);
+        return p.D == 128 ? launch<128, kMass>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s)
+                          : launch<64, kMass>(p, q, k, v, kv_len, O, lse, mass, mass_out, ws, s);
+    return p.D == 128 ? launch<128, kPlain>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s)
+                      : launch<64, kPlain>(p, q, k, v, kv_len, O, lse, nullptr, nullptr, ws, s);
+}
+
+size_t prefix_workspace(const DecodeProblem& p, int P) {
+    const PrefixPlan x = prefix_plan(p.B, p.H / p.Hkv, p.Hkv, P, num_sms());
+    return prefix_bytes(p) + part_bytes(p) + own_bytes(p) + stat_bytes(x) + sizeof(float) * 2 * (size_t)x.slabs * x.row_stride * p.D;
+}
+
+dfa_status prefix_decode(const DecodeProblem& p, int P, const void* q, const void* kp, const void* vp, int64_t ss, int64_t sh,
+                         const void* k, const void* v, const int32_t* kv_len, void* O, float* lse, void* ws, cudaStream_t s) {
+    return p.D == 128 ? launch_prefix<128>(p, P, q, kp, vp, ss, sh, k, v, kv_len, O, lse, ws, s)
+                      : launch_prefix<64>(p, P, q, kp, vp, ss, sh, k, v, kv_len, O, lse, ws, s);
 }
 
 }  // namespace dfa

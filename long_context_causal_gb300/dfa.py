@@ -87,6 +87,9 @@ def _load() -> ctypes.CDLL:
         "dfa_attn_bwd_ckpt8_workspace_size": (sz, [i32] * 7),
         "dfa_attn_bwd_ckpt8": (i32, [vp, sz, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                      vp, vp, vp, vp, sz, vp]),
+        "dfa_attn_decode_prefix_workspace_size": (sz, [i32] * 5),
+        "dfa_attn_decode_prefix": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, p64, p64, vp, f32, vp, vp,
+                                         vp, sz, vp]),
         "dfa_attn_mass_workspace_size": (sz, [i32] * 5),
         "dfa_attn_mass": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]),
         "dfa_attn_decode_mass_workspace_size": (sz, [i32] * 7),
@@ -510,7 +513,8 @@ class _Native:
             "dfa_attn_fwd_sink", "dfa_attn_bwd_sink", "dfa_attn_bwd_sink_workspace_size", "dfa_attn_decode_sink",
             "dfa_attn_decode_sink_workspace_size", "dfa_ckpt8_save", "dfa_ckpt8_restore", "dfa_ckpt8_size",
             "dfa_attn_bwd_ckpt8", "dfa_attn_bwd_ckpt8_workspace_size", "dfa_attn_decode_mass",
-            "dfa_attn_decode_mass_workspace_size", "dfa_cache_evict", "dfa_attn_mass", "dfa_attn_mass_workspace_size")))
+            "dfa_attn_decode_mass_workspace_size", "dfa_cache_evict", "dfa_attn_mass", "dfa_attn_mass_workspace_size",
+            "dfa_attn_decode_prefix", "dfa_attn_decode_prefix_workspace_size")))
         vars(self).update((n, f) for n, f in vars(native).items() if not n.startswith("__"))
         return getattr(native, name)
 
@@ -552,6 +556,19 @@ def dfa_attn_decode_sink(q, k, v, kv_len, window: int, n_sink: int = 0, scale: f
     (any strides that are multiples of 8, D contiguous), kv_len int32 [B] on the
     GPU; returns (O [B,H,D], lse fp32 [B,H])."""
     return _result(_native.decode_sink(q, k, v, kv_len, window, n_sink, scale, O, lse, workspace_buf, stream))
+
+
+def dfa_attn_decode_prefix_workspace_size(B, H, H_kv, P, D) -> int:
+    return _lib.dfa_attn_decode_prefix_workspace_size(B, H, H_kv, P, D)
+
+
+def dfa_attn_decode_prefix(q, k_prefix, v_prefix, k, v, kv_len, scale: float | None = None, O=None, lse=None,
+                           workspace_buf=None, stream=None):
+    """One new token per sequence of a batch that shares its first keys and values:
+    q [B,H,D], k_prefix, v_prefix [P,H_kv,D], the sequences' own caches k, v
+    [B,S_max,H_kv,D] (strides as in dfa_attn_decode_sink) with kv_len int32 [B] rows
+    each; returns (O [B,H,D], lse fp32 [B,H])."""
+    return _result(_native.decode_prefix(q, k_prefix, v_prefix, k, v, kv_len, scale, O, lse, workspace_buf, stream))
 
 
 def dfa_attn_mass_workspace_size(B, H, H_kv, S, D) -> int:

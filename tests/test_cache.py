@@ -209,6 +209,81 @@ def test_step_masses_of_a_cache_beyond_32_bits():
             close(got[2][b][:, idx], np64(w), 2 * F * np64(w), "mass")
 
 
+# ------------------------------------------------------------------------------------------------ a shared prefix
+# (B, H, Hkv, P, S, D, lens): one query tile of a head, two, three, many; few keys and many pieces; own rows from none on
+PREFIX = [
+    (1, 1, 1, 1, 1, 64, [0]), (2, 2, 1, 0, 3, 128, [0, 2]), (1, 4, 2, 5, 4, 128, [4]), (3, 12, 4, 127, 70, 64, [0, 1, 70]),
+    (4, 8, 8, 128, 64, 128, [64, 3, 0, 63]), (2, 34, 2, 300, 65, 64, [65, 0]), (4, 32, 8, 1000, 64, 128, [1, 17, 34, 50]),
+    (33, 4, 1, 129, 40, 128, [i for i in range(33)]), (64, 8, 2, 700, 33, 64, [33 - i % 34 for i in range(64)]),
+    (97, 4, 1, 1500, 20, 128, [i % 21 for i in range(97)]), (130, 6, 2, 257, 9, 64, [i % 10 for i in range(130)]),
+    (7, 40, 1, 4000, 600, 64, [600, 0, 599, 64, 65, 1, 300]), (2, 2, 1, 30000, 129, 128, [129, 0]), (200, 16, 4, 130, 5, 64, [i % 6 for i in range(200)]),
+]
+
+
+def check_prefix(got, q, kp, vp, k, v, lens, scale=None):
+    Or, lr, size = cache.decode_prefix(np64(q), np64(kp), np64(vp), np64(k), np64(v), lens, scale)
+    close(got[0], Or, (U + F) * size + U * np.abs(Or), "O")
+    empty = lr == -np.inf
+    assert (np64(got[1])[empty] == -np.inf).all() and (np64(got[0])[empty] == 0).all()
+    close(got[1][~torch.from_numpy(empty)], lr[~empty], 2 * F, "lse")
+
+
+@pytest.mark.parametrize("case", PREFIX, ids=lambda c: "B{}H{}kv{}P{}S{}D{}".format(*c))
+def test_prefix(case):
+    B, H, Hkv, P, S, D, lens = case
+    q, kp, vp, k, v = rand(61, B, H, D), rand(62, P, Hkv, D), rand(63, P, Hkv, D), rand(64, B, S, Hkv, D), rand(65, B, S, Hkv, D)
+    kp[P // 2::5] *= 3                     # maxima that rise along the keys
+    for b, n in enumerate(lens):
+        k[b, n:], v[b, n:] = NAN, float("inf")
+    ws = torch.full((dfa.dfa_attn_decode_prefix_workspace_size(B, H, Hkv, P, D),), 0xFF, dtype=torch.uint8, device=DEV)
+    got = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens), workspace_buf=ws)
+    dfa.dfa_check_errors()
+    check_prefix(got, q, kp, vp, k, v, lens)
+    again = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens))
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_prefix_strides_lengths_out_of_range_and_scale():
+    B, H, Hkv, P, S, D = 3, 4, 2, 200, 50, 128
+    both = rand(71, Hkv, P, 2, D + 8)               # head-major, k and v interleaved
+    kp, vp = both[..., 0, :D].transpose(0, 1), both[..., 1, :D].transpose(0, 1)
+    own = rand(72, B, Hkv, S, 2, D + 8)
+    k, v = own[..., 0, :D].transpose(1, 2), own[..., 1, :D].transpose(1, 2)
+    q = rand(73, B, H, D)
+    got = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of([-4, 20, 999]), scale=0.2)
+    dfa.dfa_check_errors()
+    check_prefix(got, q, kp, vp, k, v, [0, 20, 50], 0.2)
+
+
+def test_prefix_is_the_step_over_a_cache_that_holds_it():
+    B, H, Hkv, P, S, D = 12, 24, 3, 5000, 300, 128
+    lens = [25 * i for i in range(B)]
+    q, kp, vp, k, v = rand(74, B, H, D), rand(75, P, Hkv, D), rand(76, P, Hkv, D), rand(77, B, S, Hkv, D), rand(78, B, S, Hkv, D)
+    O, lse = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens))
+    kk, vv = (torch.cat((t.expand(B, P, Hkv, D), own), 1) for t, own in ((kp, k), (vp, v)))
+    want = dfa.dfa_attn_decode_sink(q, kk, vv, lens_of([P + n for n in lens]), P + S)
+    dfa.dfa_check_errors()
+    # both sides round P and the result; sum_j P |v_j| stays below 1.5
+    assert (O.float() - want[0].float()).abs().max() <= 2 * (U + F) * 1.5 + 2 * U
+    assert (lse - want[1]).abs().max() <= 4 * F
+
+
+def test_prefix_beyond_32_bits():
+    B, H, Hkv, P, S, D = 2, 16, 8, (1 << 21) + 77, 10, 128
+    kp, vp = (torch.empty(P, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(79 + i)) for i in range(2))
+    q, k, v = rand(81, B, H, D), rand(82, B, S, Hkv, D), rand(83, B, S, Hkv, D)
+    O, lse = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of([10, 0]))
+    dfa.dfa_check_errors()
+    s = [torch.einsum("hd,jd->hj", q[0, :2].double(), torch.cat((kp[:, 0], k[0, :, 0])).double()) * D ** -0.5,
+         torch.einsum("hd,jd->hj", q[1, -2:].double(), kp[:, -1].double()) * D ** -0.5]
+    vs = [torch.cat((vp[:, 0], v[0, :, 0])).double(), vp[:, -1].double()]
+    for b, hs in ((0, slice(0, 2)), (1, slice(H - 2, H))):
+        p = torch.softmax(s[b], -1)
+        size, ref = np64(p @ vs[b].abs()), np64(p @ vs[b])
+        close(O[b, hs], ref, (U + F) * size + U * np.abs(ref), "O")
+        close(lse[b, hs], np64(torch.logsumexp(s[b], -1)), 2 * F, "lse")
+
+
 # ------------------------------------------------------------------------------------------------ eviction
 # (B, Hkv, S, D, keep, cap, n_first, n_recent, lens)
 EVICT = [

@@ -126,6 +126,32 @@ def test_decode_mass_sizes():
     assert size(2, 4, 2, 1 << 20, 128, 64, 4) <= base + 4 * 2 * 4 * 64 * 4 + 4096
 
 
+def prefix(**kw):
+    a = dict(q=FAR[0], kp=FAR[1], vp=FAR[2], k=FAR[3], v=FAR[4], dt=1, B=2, H=4, Hkv=2, P=500, S=300, D=128, ps=None, ks=None, n=FAR[5],
+             scale=0.1, O=FAR[6], lse=FAR[7], ws=FAR[8], wn=1 << 40)
+    a.update(kw)
+    return lib.dfa_attn_decode_prefix(*(a[x] for x in ("q", "kp", "vp", "k", "v", "dt", "B", "H", "Hkv", "P", "S", "D", "ps", "ks", "n",
+                                                       "scale", "O", "lse", "ws", "wn")), None)
+
+
+@pytest.mark.parametrize("kw,code", [r for r in REFUSED if "window" not in r[0] and "n_sink" not in r[0]] + [
+    (dict(S=0), dfa.DFA_ERR_INVALID_ARG), (dict(P=-1), dfa.DFA_ERR_INVALID_ARG), (dict(P=(1 << 30) + 1), dfa.DFA_ERR_INVALID_ARG),
+    (dict(B=8193), dfa.DFA_ERR_UNSUPPORTED), (dict(kp=None), dfa.DFA_ERR_INVALID_ARG), (dict(vp=MIS), dfa.DFA_ERR_INVALID_ARG),
+    (dict(n=None), dfa.DFA_ERR_INVALID_ARG), (dict(lse=A + 2), dfa.DFA_ERR_INVALID_ARG), (dict(v=None), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ps=(ctypes.c_int64 * 2)(256, 12)), dfa.DFA_ERR_INVALID_ARG), (dict(ps=(ctypes.c_int64 * 2)(-256, 128)), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ps=(ctypes.c_int64 * 2)(0, 128)), dfa.DFA_ERR_INVALID_ARG), (dict(ps=(ctypes.c_int64 * 2)(256, 0)), dfa.DFA_ERR_INVALID_ARG),
+    (dict(ks=(ctypes.c_int64 * 3)(0, 256, 128)), dfa.DFA_ERR_INVALID_ARG), (dict(ws=None), dfa.DFA_ERR_WORKSPACE),
+    (dict(wn=dfa.dfa_attn_decode_prefix_workspace_size(2, 4, 2, 500, 128) - 1), dfa.DFA_ERR_WORKSPACE)])
+def test_prefix_refusals(kw, code):
+    assert prefix(**kw) == code and dfa.dfa_last_error()
+
+
+def test_prefix_of_no_sequence_and_size_queries():
+    size = dfa.dfa_attn_decode_prefix_workspace_size
+    assert prefix(B=0, q=None, kp=None, vp=None, k=None, v=None, n=None, O=None, lse=None, ws=None, wn=0) == dfa.DFA_OK
+    assert size(8193, 4, 2, 500, 128) == 0 and size(2, 4, 2, -1, 128) == 0 and size(2, 4, 2, 500, 96) == 0 and size(2, 4, 2, 0, 128) > 0
+
+
 def evict(**kw):
     a = dict(k=FAR[0], v=FAR[1], dt=1, B=2, Hkv=3, S=300, D=128, ks=None, n=FAR[2], m=FAR[3], keep=40, first=2, recent=8, cap=64,
              os=None, ko=FAR[4], vo=FAR[5], lo=FAR[6], mo=FAR[7], kept=FAR[8])
@@ -177,6 +203,13 @@ def test_the_binding_refuses_cache_tensors():
     for bad in ((q[:1], k, k), (q, k[0], k[0]), (q, k, t(2, 8, 2, 128)), (t(2, 4, 128), k, k)):
         with pytest.raises(ValueError, match="must be"):
             dfa.dfa_attn_decode_mass(*bad, n)
+    kp = t(9, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfa.dfa_attn_decode_prefix(q, kp, kp, k, k, n)
+    for bad in ((kp[0], kp[0]), (kp, kp[:4]), (kp[:, :1], kp[:, :1]), (t(9, 2, 128), t(9, 2, 128)), (kp.float(), kp.float()),
+                (kp, t(2, 9, 64).transpose(0, 1))):
+        with pytest.raises(ValueError, match="must"):
+            dfa.dfa_attn_decode_prefix(q, *bad, k, k, n)
     for other in (t(2, 8, 2, 128), k.float(), t(2, 2, 8, 64).transpose(1, 2)):
         with pytest.raises(ValueError, match="must"):
             dfa.dfa_cache_evict(k, other, n, m, 4)
