@@ -7,10 +7,10 @@
 //
 // select_kernel finds the border: masses become unsigned integers of the same
 // order, and a radix select of three digits (11, 11 and 10 bits) narrows down the
-// integer T of the last one that stays, and how many of those equal to T do.
-// Positions follow from counts: a warp owns a contiguous range of keys, counts
-// what it keeps, and after one scan over all warps of the row writes its keys'
-// positions in order.  A row is shared by a cluster of up to eight CTAs that add
+// integer T of the last one that stays, and how many of those equal to T do; it ends
+// early where a whole bin stays.  Positions follow from counts: a thread owns up to
+// 16 consecutive keys, which it holds in registers, counts what it keeps of them,
+// and after one scan over all threads of the row writes their positions in order.  A row is shared by a cluster of up to eight CTAs that add
 // their histograms and counts through distributed shared memory.
 //
 // copy_kernel moves the rows: bound by HBM (each kept row read and written once).
@@ -29,7 +29,6 @@ using namespace ptx;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
 
 struct Args {
     int Hkv, S, keep, cap, n_first, n_recent;
@@ -40,9 +39,11 @@ struct Args {
     int32_t* kept;                // [B, Hkv, keep]
 };
 
-// Unsigned integers in the order of the numbers; -0 is 0, NaN stands below all.
+// Unsigned integers in the order of the numbers; -0 is 0, NaN stands below all (1).
+// 0: no key that competes; kSure: stays in any case (above every number).
+constexpr uint32_t kSure = 0xffffffffu;
 __device__ __forceinline__ uint32_t ordered(float x) {
-    if (x != x) return 0;
+    if (x != x) return 1;
     const uint32_t u = __float_as_uint(x + 0.f);
     return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
@@ -53,8 +54,8 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank)
     return r;
 }
 
-// Inclusive sum over the threads before and including this one; all: of all threads.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* s_warp, uint32_t& all) {
+// Sum over the threads up to and including this one.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* s_warp) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -70,16 +71,57 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* s_warp, uin
         const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
-    all = __shfl_sync(0xffffffffu, w, 31);
     const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
     return x + (warp ? before : 0);
 }
 
+// A thread's keys at .. at + PER - 1 in their order; `at` is on 16 bytes and may be below 0.
+template <int PER>
+__device__ __forceinline__ void load(uint32_t (&u)[PER], const float* mass, int at, int n, int lo, int hi) {
+    float x[PER];
+#pragma unroll
+    for (int s = 0; s < PER; s += 4) {
+        if (at + s >= 0 && at + s + 3 < n) {
+            const float4 y = *reinterpret_cast<const float4*>(mass + at + s);
+            x[s] = y.x, x[s + 1] = y.y, x[s + 2] = y.z, x[s + 3] = y.w;
+        } else {
+#pragma unroll
+            for (int e = s; e < s + 4; ++e) x[e] = at + e >= 0 && at + e < n ? mass[at + e] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < PER; ++s) u[s] = ordered(x[s]);
+    if (at < lo || at + PER > hi) {
+#pragma unroll
+        for (int s = 0; s < PER; ++s)
+            if (at + s < lo || at + s >= hi) u[s] = 0;
+    }
+}
+// The keys that stay in any case, once the others have been counted.
+template <int PER>
+__device__ __forceinline__ void mark(uint32_t (&u)[PER], int at, int n, int lo, int hi) {
+    if (at < lo || at + PER > hi) {
+#pragma unroll
+        for (int s = 0; s < PER; ++s) {
+            const int j = at + s;
+            if (j >= 0 && j < n && (j < lo || j >= hi)) u[s] = kSure;
+        }
+    }
+}
+
+template <int LOG_C, int PER>
 __global__ void __launch_bounds__(kThreads, 1)
-select_kernel(const Args a, int log_c) {
-    __shared__ uint32_t hist[2][kBins];
-    __shared__ uint32_t s_scan[kWarps], s_count[kWarps + 1], s_found[2];
-    const int C = 1 << log_c, rank = blockIdx.x & (C - 1), row = blockIdx.x >> log_c, b = row / a.Hkv;
+select_kernel(const Args a) {
+    constexpr int C = 1 << LOG_C;
+    // Digits of 11 bits; where CTAs share a row, of 8, for all of them read all histograms.  Copies of a
+    // histogram, so that equal digits of a warp's keys wait less for one another.
+    constexpr int kBits = C == 1 ? 11 : 8, kBins = 1 << kBits, kCopies = C == 1 ? 2 : 8;
+    __shared__ union {
+        uint32_t hist[kCopies][kBins];
+        uint16_t list[kThreads * PER];       // what stays of a chunk
+    } sm;
+    __shared__ uint32_t folded[2][C > 1 ? kBins : 1], s_scan[kWarps], s_count[2], s_found[3];
+    const int rank = blockIdx.x % C, row = blockIdx.x / C, b = row / a.Hkv;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int n = min(max(a.kv_len[b], 0), a.S);
     const float* mass = a.mass + (int64_t)row * a.S;
@@ -99,91 +141,130 @@ select_kernel(const Args a, int log_c) {
         return;
     }
     const int lo = a.n_first, hi = n - a.n_recent;      // the keys that compete
-    const int want = a.keep - a.n_first - a.n_recent;   // so many of them stay; fewer than there are
-    // a warp's keys: 32 * steps from `from` on
-    const int steps = (n + 32 * C * kWarps - 1) / (32 * C * kWarps), from = (rank * kWarps + warp) * 32 * steps;
-    uint32_t T = 0xffffffffu;       // what stays is above T, or equal to it and among the first E of those
-    int E = 0;
-    if (want > 0) {
+    // Rows of more than C * kThreads * PER keys are read in chunks of that many, again in each pass.
+    constexpr int chunk = C * kThreads * PER;
+    const int shift = (int)(reinterpret_cast<uintptr_t>(mass) / 4 % 4);
+    const int from = (rank * kThreads + tid) * PER - shift, chunks = (n + shift + chunk - 1) / chunk;
+    uint32_t u[PER];
+    load(u, mass, from, n, lo, hi);
+    // What stays is above T, or equal to it and among the first E of those: the digits of T, from above.
+    uint32_t T = kSure - 1, E = a.keep - a.n_first - a.n_recent;
+    int at = from;
+    if (E > 0) {
         T = 0;
-        E = want;
-        int top = 32;
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            uint32_t* h = hist[pass & 1];
-            const int bits = pass == 2 ? 10 : 11, low = top - bits;
-            for (int i = tid; i < kBins; i += kThreads) h[i] = 0;
+        for (int pass = 0, top = 32; top > 0; ++pass) {
+            const int low = max(top - kBits, 0);
+            for (int i = tid; i < kCopies * kBins; i += kThreads) sm.hist[0][i] = 0;
             __syncthreads();
-            for (int s = 0; s < steps; ++s) {
-                const int j = from + s * 32 + lane;
-                if (j < lo || j >= hi) continue;
-                const uint32_t u = ordered(mass[j]);
-                if (top == 32 || u >> top == T >> top) atomicAdd(&h[u >> low & ((1u << bits) - 1)], 1u);
+            uint32_t* mine = sm.hist[lane % kCopies];
+#pragma unroll 1
+            for (int ch = 0; ch < chunks; ++ch) {
+                if (chunks > 1) load(u, mass, at = ch * chunk + from, n, lo, hi);
+                if (pass == 0) {
+#pragma unroll
+                    for (int s = 0; s < PER; ++s)
+                        if (u[s]) atomicAdd(&mine[u[s] >> (32 - kBits)], 1u);
+                } else {
+                    const uint32_t high = T >> top, digit = (1u << (top - low)) - 1;
+#pragma unroll
+                    for (int s = 0; s < PER; ++s)
+                        if (u[s] >> top == high) atomicAdd(&mine[u[s] >> low & digit], 1u);
+                }
             }
-            __syncwarp();
-            if (C > 1) cluster_sync();
-            else __syncthreads();
-            // bins in falling order, two of them a thread
-            uint32_t c[2] = {0, 0};
-            const int bin = kBins - 1 - 2 * tid;
-            for (int r = 0; r < C; ++r) {
-                c[0] += C > 1 ? ld_cluster_u32(&h[bin], r) : h[bin];
-                c[1] += C > 1 ? ld_cluster_u32(&h[bin - 1], r) : h[bin - 1];
+            __syncthreads();
+            // the bin that holds the E-th one from above, and how many of it stay
+            constexpr int kEach = C == 1 ? kBins / kThreads : 1;      // bins of a thread, in falling order
+            uint32_t c[kEach], sum = 0;
+            const int bin = kBins - 1 - kEach * tid;
+            if (C == 1) {
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    c[e] = 0;
+#pragma unroll
+                    for (int f = 0; f < kCopies; ++f) c[e] += sm.hist[f][bin - e];
+                    sum += c[e];
+                }
+            } else {
+                if (bin >= 0) {
+#pragma unroll
+                    for (int f = 0; f < kCopies; ++f) sum += sm.hist[f][bin];
+                    folded[pass & 1][bin] = sum;
+                }
+                __syncwarp();
+                cluster_sync();
+                sum = 0;
+                if (bin >= 0) {
+                    uint32_t part[C];
+#pragma unroll
+                    for (int r = 0; r < C; ++r) part[r] = ld_cluster_u32(&folded[pass & 1][bin], r);
+#pragma unroll
+                    for (int r = 0; r < C; ++r) sum += part[r];
+                }
+                c[0] = sum;
             }
-            uint32_t all;
-            const uint32_t upto = block_scan(c[0] + c[1], s_scan, all), before = upto - c[0] - c[1];
-            if (before < (uint32_t)E && upto >= (uint32_t)E) {
-                const bool second = before + c[0] < (uint32_t)E;
-                s_found[0] = bin - second;
-                s_found[1] = E - before - (second ? c[0] : 0);
+            uint32_t before = block_scan(sum, s_scan) - sum;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (before < E && before + c[e] >= E) {
+                    s_found[0] = bin - e;
+                    s_found[1] = E - before;
+                    s_found[2] = c[e];
+                }
+                before += c[e];
             }
             __syncthreads();
             T |= s_found[0] << low;
             E = s_found[1];
             top = low;
+            if (E == s_found[2]) {   // the whole bin stays: everything above its lower end
+                T -= 1;
+                E = 0;
+                break;
+            }
         }
     }
-    // what each warp keeps for certain (upper half), and its keys equal to T (lower half)
-    uint32_t sure = 0, equal = 0;
-    for (int s = 0; s < steps; ++s) {
-        const int j = from + s * 32 + lane;
-        const bool in = j < n, free = j >= lo && j < hi;
-        const uint32_t u = in ? ordered(mass[j]) : 0;
-        sure += __popc(__ballot_sync(0xffffffffu, in && (!free || u > T)));
-        equal += __popc(__ballot_sync(0xffffffffu, in && free && u == T));
-    }
-    if (E == 0) equal = 0;           // want = 0: none of them stays
-    // keys before this warp's: of the CTAs before, then of the warps before
-    uint32_t all;
-    const uint32_t upto_s = block_scan(lane == 0 ? sure : 0, s_scan, all);
-    if (tid == 0) s_count[0] = all;
-    const uint32_t upto_e = block_scan(lane == 0 ? equal : 0, s_scan, all);
-    if (tid == 0) s_count[1] = all;
-    uint32_t at_s = __shfl_sync(0xffffffffu, upto_s, 0) - sure, at_e = __shfl_sync(0xffffffffu, upto_e, 0) - equal;
-    if (C > 1) {
+    // Positions: what is above T (upper half of a count) and equal to it (lower half) before a key; both below 2^16 in a CTA.
+    uint32_t base_s = 0, base_e = 0;                 // in the chunks before
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+        if (chunks > 1) load(u, mass, at = ch * chunk + from, n, lo, hi);
+        mark(u, at, n, lo, hi);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int s = 0; s < PER; ++s) mine += u[s] > T ? 1u << 16 : u[s] == T ? 1u : 0u;
+        const uint32_t upto = block_scan(mine, s_scan);
+        if (tid == kThreads - 1) s_count[ch & 1] = upto;
         __syncwarp();
-        cluster_sync();
-        for (int r = 0; r < rank; ++r) {
-            at_s += ld_cluster_u32(&s_count[0], r);
-            at_e += ld_cluster_u32(&s_count[1], r);
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        uint32_t cta_s = base_s, cta_e = base_e, own = 0;      // before this CTA's keys; its counts
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            const uint32_t c = C > 1 ? ld_cluster_u32(&s_count[ch & 1], r) : s_count[ch & 1];
+            if (r < rank) cta_s += c >> 16, cta_e += c & 0xffffu;
+            if (r == rank) own = c;
+            base_s += c >> 16, base_e += c & 0xffffu;
         }
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int s = 0; s < steps; ++s) {
-        const int j = from + s * 32 + lane;
-        const bool in = j < n, free = j >= lo && j < hi;
-        const float x = in ? mass[j] : 0.f;
-        const uint32_t u = ordered(x);
-        const bool is_s = in && (!free || u > T), is_e = in && free && u == T && E > 0;
-        const uint32_t ms = __ballot_sync(0xffffffffu, is_s), me = __ballot_sync(0xffffffffu, is_e);
-        const uint32_t e = at_e + __popc(me & below);
-        if (is_s || (is_e && e < (uint32_t)E)) {
-            const int r = at_s + __popc(ms & below) + min(e, (uint32_t)E);
+        const int r0 = cta_s + min(cta_e, E), r1 = cta_s + (own >> 16) + min(cta_e + (own & 0xffffu), E);
+        uint32_t at_s = cta_s + ((upto - mine) >> 16), at_e = cta_e + ((upto - mine) & 0xffffu);
+        if (mine) {
+#pragma unroll
+            for (int s = 0; s < PER; ++s) {
+                const bool sure = u[s] > T, equal = u[s] == T;
+                if (sure || (equal && at_e < E)) sm.list[at_s + min(at_e, E) - r0] = (uint16_t)(tid * PER + s);
+                at_s += sure;
+                at_e += equal;
+            }
+        }
+        __syncthreads();
+        const int first = at - tid * PER;
+        for (int r = r0 + tid; r < r1; r += kThreads) {
+            const int j = first + sm.list[r - r0];
             kept[r] = j;
-            mass_out[r] = x;
+            mass_out[r] = mass[j];
         }
-        at_s += __popc(ms);
-        at_e += __popc(me);
+        if (chunks > 1) __syncthreads();
     }
     __syncwarp();
     if (C > 1) cluster_sync();       // no CTA leaves while another one may still read its counts
@@ -237,8 +318,13 @@ dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, cons
                        void* k_out, void* v_out, int32_t* len_out, float* mass_out, int32_t* kept, cudaStream_t s) {
     const Args a{p.Hkv, p.S, p.keep, p.cap, p.n_first, p.n_recent, kv_len, mass, len_out, mass_out, kept};
     const int rows = p.B * p.Hkv;
+    // A row to a CTA while its threads hold the keys: 8 x 8 rows of 16384 keys 53 us with the copy, by two CTAs each 59,
+    // by eight 107 (their barriers and 3.5 times as many CTAs as SMs); 8 rows of 131072 by one 99 (chunks), by four 61,
+    // by eight 42.  Rows of 501 keys with 4 keys a thread 10.3, 16 a thread 14.3.
     int log_c = 0;
-    while ((1 << log_c) < kMaxCluster && p.S > (kThreads * 2 << log_c)) ++log_c;
+    while ((1 << log_c) < kMaxCluster && p.S > (kThreads * 16 << log_c)) ++log_c;
+    void (*const kernels[])(const Args) = {select_kernel<0, 16>, select_kernel<1, 16>, select_kernel<2, 16>, select_kernel<3, 16>};
+    void (*const kernel)(const Args) = log_c == 0 && p.S <= kThreads * 4 ? select_kernel<0, 4> : kernels[log_c];
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -249,7 +335,7 @@ dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, cons
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a, log_c);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_EVICT);
     const int unit = 16 / p.elt;
