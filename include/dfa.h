@@ -332,8 +332,8 @@ dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dty
  *   mass_out: fp32 [B, H_kv, S_max]; may be `mass` itself, else it does not
  *             overlap an input
  *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as below
- * Everything else as dfa_attn_decode_sink, O and lse with the same bits.  Two or
- * three launches; the same bits on every call.  */
+ * Everything else as dfa_attn_decode_sink (whose O and lse may differ in the
+ * last bits: the keys are cut elsewhere).  Two launches; the same bits on every call. */
 size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink);
 dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
                                 int S_max, int D, const int64_t* kv_strides, const int32_t* kv_len, const float* mass,

@@ -180,6 +180,7 @@ struct PrefixPlan {
     int64_t steps;
 };
 PrefixPlan prefix_plan(int B, int G, int Hkv, int P, int sms);
+// The next launch (launch_overlapped) may start beside it.
 dfa_status tc_prefix(const DecodeProblem& p, const PrefixPlan& plan, const void* q, const void* kp, const void* vp, int64_t ss,
                      int64_t sh, float* part, float2* stat, cudaStream_t s);
 // Both parts and their join (sink_decode.cu); ss, sh: the prefix's strides.

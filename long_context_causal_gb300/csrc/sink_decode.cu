@@ -78,17 +78,24 @@ struct Args {
     float* lse;                   // [B, H]
     float scale_log2;
     int* prefix;                  // [B + 1], for the joining kernel
-    float* part;                  // [2 * n CTAs][MH][D + 2]: unnormalised O, max, sum
+    float* part;                  // [2 * n CTAs][MH][row_floats]: unnormalised O, max, sum
     int* err;
     // MASS: the scores times log2 e of the visible keys, [B * H][stride] in the order of the tiles
     float* score;
     int stride;                   // 64 * the most tiles of a segment
     const float* mass;            // [B, Hkv, S], null: zero
     float* mass_out;              // [B, Hkv, S]; may be `mass`
-    // PARTS: a segment that one CTA covers leaves its rows' parts here, [B * H][D + 2]
+    // PARTS: a segment that one CTA covers leaves its rows' parts here, [B * H][row_floats]
     float* own;
 };
 enum Mode { kPlain, kMass, kParts };
+// Units that a segment counts for beside its tiles when the tiles are dealt: it costs a CTA 2 us beside
+// 0.7 to 0.9 us per tile.  (The plain step deals tiles alone.)
+template <bool CLUSTER, Mode MODE>
+constexpr int kUnits = CLUSTER || MODE == kPlain ? 0 : 2;
+// Floats of a head's partial: unnormalised O, max, sum.
+template <int D, Mode MODE>
+constexpr int row_floats() { return MODE == kPlain ? D + 2 : D + 4; }
 
 // The visible keys of a sequence as tiles: the sinks' tiles, if the window has
 // moved off them, then the window's.
@@ -131,13 +138,15 @@ __device__ __forceinline__ void store_scores(const Args& a, int64_t row, int at,
     *reinterpret_cast<float4*>(a.score + row * a.stride + at) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// Cursor over a CTA's range of tiles.
+// Cursor over a CTA's range.  A segment counts for W units more than its tiles, which
+// stand before them: what its beginning and end cost a CTA.
 struct Cursor {
-    int b, r, k;        // sequence, segment of the sequence, tile of the segment
+    int b, r, v;        // sequence, segment of the sequence, unit of the segment
     Seen s;
 };
 
-// Finds tile x (0 <= x < total): prefix[b] <= x < prefix[b + 1].
+// Finds unit x (0 <= x < total): prefix[b] <= x < prefix[b + 1].
+template <int W>
 __device__ __forceinline__ Cursor find(const Args& a, const int* prefix, int x) {
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
@@ -149,13 +158,13 @@ __device__ __forceinline__ Cursor find(const Args& a, const int* prefix, int x) 
     c.b = lo;
     c.s = seen(a, lo);
     const int at = x - prefix[lo];
-    c.r = at / c.s.tiles;
-    c.k = at % c.s.tiles;
+    c.r = at / (c.s.tiles + W);
+    c.v = at % (c.s.tiles + W);
     return c;
 }
 // The segment after the cursor's (the caller knows that there is one).
 __device__ __forceinline__ void next_segment(const Args& a, Cursor& c) {
-    c.k = 0;
+    c.v = 0;
     if (++c.r == a.Hkv * a.HB) {
         c.r = 0;
         do c.s = seen(a, ++c.b);
@@ -167,6 +176,7 @@ template <int D, bool CLUSTER, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
     using C = Cfg<D>;
+    constexpr int W = kUnits<CLUSTER, MODE>, kRow = row_floats<D, MODE>();
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {            // the swizzled tiles need a 1 KB aligned base
         if (threadIdx.x == 0 && a.err) atomicExch(a.err, 2);
@@ -201,15 +211,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         c.b = segment / R;
         c.r = segment % R;
         c.s = seen(a, c.b);
-        begin = c.k = c.s.tiles * rank / kCluster;
+        begin = c.v = c.s.tiles * rank / kCluster;
         end = c.s.tiles * (rank + 1) / kCluster;
         __syncthreads();
     } else {
-        // Tiles before each sequence, all segments counted.
+        // Units before each sequence, all segments counted.
         int carry = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + (int)threadIdx.x;
-            int x = b < a.B ? seen(a, b).tiles * R : 0;
+            int x = b < a.B ? seen(a, b).tiles : 0;
+            x = x > 0 ? (x + W) * R : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -228,42 +239,52 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         if (blockIdx.x == 0)
             for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
         const int total = prefix[a.B];
-        const int n_ctas = min((int)gridDim.x, total);   // every one of them has a tile
+        const int n_ctas = min((int)gridDim.x, total);   // every one of them has a unit
         if ((int)blockIdx.x >= n_ctas) {
             if (MODE == kParts && blockIdx.x == 0) wait_for_previous_kernel();
             return;
         }
         begin = (int)((int64_t)total * blockIdx.x / n_ctas);
         end = (int)((int64_t)total * (blockIdx.x + 1) / n_ctas);
-        c = find(a, prefix, begin);
+        c = find<W>(a, prefix, begin);
     }
     if (warp == kConsumers) {
         // ------------------------------------------------------------ TMA producer
         bool ok = true;
-        int x = begin;
-        for (; x < end && ok; ++x) {
-            const int i = x - begin, slot = i % C::kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait_acc(&empty[slot], ((i / C::kStages) & 1) ^ 1, abort_flag, a.err, nullptr));
-            if (!ok) break;
-            int key, n;
-            tile_keys(c.s, a.n_sink, c.k, key, n);
-            if (lane == 0) {
-                uint8_t* dst = smem + slot * C::kStage;
-                const int g = c.r / a.HB;
-                mbar_arrive_expect_tx(&full[slot], C::kStage);
-                for (int blk = 0; blk < D / 64; ++blk) {
-                    tma_load_4d(dst + blk * KT * 128, &tmK, &full[slot], blk * 64, g, key, c.b);
-                    tma_load_4d(dst + C::kHalf + blk * KT * 128, &tmV, &full[slot], blk * 64, g, key, c.b);
+        int i = 0;
+        const uint64_t once = MODE == kMass ? l2_evict_first() : 0;
+        for (int x = begin; x < end && ok;) {
+            const int v1 = min(c.s.tiles + W, c.v + end - x), k1 = v1 - W;
+            for (int k = max(c.v - W, 0); k < k1; ++k, ++i) {
+                const int slot = i % C::kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(&empty[slot], ((i / C::kStages) & 1) ^ 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                int key, n;
+                tile_keys(c.s, a.n_sink, k, key, n);
+                if (lane == 0) {
+                    uint8_t* dst = smem + slot * C::kStage;
+                    const int g = c.r / a.HB;
+                    mbar_arrive_expect_tx(&full[slot], C::kStage);
+                    for (int blk = 0; blk < D / 64; ++blk) {
+                        if (MODE == kMass) {         // read once: the scores are to stay in the L2
+                            tma_load_4d_once(dst + blk * KT * 128, &tmK, &full[slot], blk * 64, g, key, c.b, once);
+                            tma_load_4d_once(dst + C::kHalf + blk * KT * 128, &tmV, &full[slot], blk * 64, g, key, c.b, once);
+                        } else {
+                            tma_load_4d(dst + blk * KT * 128, &tmK, &full[slot], blk * 64, g, key, c.b);
+                            tma_load_4d(dst + C::kHalf + blk * KT * 128, &tmV, &full[slot], blk * 64, g, key, c.b);
+                        }
+                    }
                 }
+                __syncwarp();
             }
-            __syncwarp();
-            if (++c.k == c.s.tiles && x + 1 < end) next_segment(a, c);
+            x += v1 - c.v;
+            if (x < end) next_segment(a, c);
         }
         if (!ok && lane == 0) {
             // Aborted: let the copies already issued land before the CTA exits.
             int dummy = 0;
-            for (int i = max(x - begin - C::kStages, 0); i < x - begin; ++i)
-                mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, &dummy, nullptr);
+            for (int m = max(i - C::kStages, 0); m < i; ++m)
+                mbar_wait(&full[m % C::kStages], (m / C::kStages) & 1, &dummy, nullptr);
         }
         __syncwarp();
         // PARTS: started beside the prefix's kernel.  What joins the parts waits for this
@@ -287,9 +308,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     float2 mine_ml[2];
     mine_ml[0] = mine_ml[1] = make_float2(-INFINITY, 0.f);
     mine[0] = mine[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int i = 0;
     for (int x = begin; x < end && ok;) {
         // One segment, or the part of it in this CTA's range.
-        const int k0 = c.k, k1 = min(c.s.tiles, k0 + end - x);
+        const int v1 = min(c.s.tiles + W, c.v + end - x), k0 = max(c.v - W, 0), k1 = v1 - W;
+        x += v1 - c.v;
+        if (k1 <= k0) {                      // nothing but what stands before the tiles (or an empty share)
+            if constexpr (CLUSTER) break;
+            if (x < end) next_segment(a, c);
+            continue;
+        }
         const int gq = c.r / a.HB, hb = c.r % a.HB;
         const int h0 = gq * a.G + hb * MH, nh = min(a.G - hb * MH, MH);
         uint4 qa[D / 32], qb[D / 32];        // dims [32 p + 8 t, + 8) of heads g and g + 8
@@ -306,8 +334,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads g, g + 8; l: this lane's columns
-        for (int k = k0; k < k1; ++k, ++x) {
-            const int i = x - begin;
+        for (int k = k0; k < k1; ++k, ++i) {
             if ((i & 1) != grp) continue;
             const int slot = i % C::kStages;
             ok = __all_sync(0xffffffffu, mbar_wait_acc(&full[slot], (i / C::kStages) & 1, abort_flag, a.err, nullptr));
@@ -431,8 +458,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         ok = named_bar_and(1, kConsumers * 32, ok);
         if (!ok) break;
         const bool whole = k0 == 0 && k1 == c.s.tiles;
-        float* part = a.part + (int64_t)(2 * blockIdx.x + (k0 == 0)) * MH * (D + 2);
-        if (MODE == kParts && whole) part = a.own + ((int64_t)c.b * a.H + h0) * (D + 2);
+        float* part = a.part + (int64_t)(2 * blockIdx.x + (k0 == 0)) * MH * kRow;
+        if (MODE == kParts && whole) part = a.own + ((int64_t)c.b * a.H + h0) * kRow;
         for (int y = threadIdx.x; y < nh * (D / 4); y += kConsumers * 32) {
             const int h = y / (D / 4), d = y % (D / 4) * 4;
             float m = -INFINITY, l = 0.f;
@@ -460,9 +487,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                     make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
                 if (d == 0) a.lse[row] = (m + __log2f(l)) * kLn2;
             } else {
-                *reinterpret_cast<float2*>(part + h * (D + 2) + d) = make_float2(acc.x, acc.y);
-                *reinterpret_cast<float2*>(part + h * (D + 2) + d + 2) = make_float2(acc.z, acc.w);
-                if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 2) + D) = make_float2(m, l);
+                *reinterpret_cast<float2*>(part + h * kRow + d) = make_float2(acc.x, acc.y);
+                *reinterpret_cast<float2*>(part + h * kRow + d + 2) = make_float2(acc.z, acc.w);
+                if (d == 0) *reinterpret_cast<float2*>(part + h * kRow + D) = make_float2(m, l);
             }
         }
         if constexpr (CLUSTER) break;
@@ -472,7 +499,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     if constexpr (CLUSTER) {
         // Parts [rank][head][D + 4] (unnormalised output, maximum, sum) in rank 0's ring, which it no longer needs.
         const int h0 = c.r / a.HB * a.G + c.r % a.HB * MH, nh = min(a.G - c.r % a.HB * MH, MH);
-        constexpr int kRow = D + 4;
+        constexpr int kRow = D + 4;          // unnormalised output, maximum, sum
         static_assert(kCluster * MH * kRow * 4 <= C::kOffMerge, "parts");
         __syncwarp();
         cluster_sync();
@@ -576,119 +603,211 @@ join_kernel(const Args a, int grid) {
     if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// Joins the parts of a shared prefix and of the sequences' own keys: D / 2 threads
-// per row (sequence, head), one per pair of dims, prefix first, in the order of the keys.
-constexpr int kPrefixThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kPrefixThreads)
-prefix_join_kernel(const Args a, int grid, const PrefixPlan p, const float* part, const float2* stat) {
-    wait_for_previous_kernel();
-    const int64_t row = (int64_t)blockIdx.x * (kPrefixThreads / (D / 2)) + threadIdx.x / (D / 2);
-    if (row >= (int64_t)a.B * a.H) return;
-    const int d = threadIdx.x % (D / 2) * 2, b = (int)(row / a.H), h = (int)(row % a.H), gq = h / a.G, gi = h % a.G;
-    float m = -INFINITY, l = 0.f;
-    float2 acc = make_float2(0.f, 0.f);
-    auto add = [&](const float2 (&st)[kJoinAhead], const float2 (&v)[kJoinAhead]) {
-        float n = m;
-#pragma unroll
-        for (int e = 0; e < kJoinAhead; ++e) n = fmaxf(n, st[e].x);
-        if (n == -INFINITY) return;
-        const float f = ex2(m - n);
-        m = n;
-        l *= f;
-        acc.x *= f;
-        acc.y *= f;
-#pragma unroll
-        for (int e = 0; e < kJoinAhead; ++e) {
-            const float g = ex2(st[e].x - n);
-            l = fmaf(st[e].y, g, l);
-            acc.x = fmaf(v[e].x, g, acc.x);
-            acc.y = fmaf(v[e].y, g, acc.y);
-        }
-    };
-    if (p.grid > 0) {
-        const int at = b * a.G + gi, tile = at / 128, r = at % 128, s = gq * p.n_pairs + tile / 2;
-        const bool alone = (tile & ~1) * 128 + 128 >= p.rows;       // the pair has this tile only: two parts
-        const int64_t x0 = (int64_t)s * p.n_kt, x1 = x0 + p.n_kt - 1;
-        const int c0 = (int)(((x0 + 1) * p.grid - 1) / p.steps), c1 = (int)(((x1 + 1) * p.grid - 1) / p.steps);
-        const int n = (c1 - c0 + 1) << alone;
-        for (int y = 0; y < n; y += kJoinAhead) {
-            float2 st[kJoinAhead], v[kJoinAhead];
-#pragma unroll
-            for (int e = 0; e < kJoinAhead; ++e) {
-                st[e] = make_float2(-INFINITY, 0.f);
-                v[e] = make_float2(0.f, 0.f);
-                if (y + e < n) {
-                    const int64_t slab = alone ? 2 * (int64_t)(s + c0) + y + e : 2 * (int64_t)(s + c0 + y + e) + (tile & 1);
-                    const int64_t z = slab * p.row_stride + r;
-                    st[e] = stat[z];
-                    if (st[e].y > 0.f) v[e] = *reinterpret_cast<const float2*>(part + z * D + d);   // else nothing was written
-                }
-            }
-            add(st, v);
-        }
+// The CTAs that hold units [x, x + n) of a list of `total` dealt to n_ctas in equal
+// ranges: the last ones whose ranges begin at or before them.
+__device__ __forceinline__ void ctas_of(int64_t x, int64_t n, int64_t total, int n_ctas, int& c0, int& c1) {
+    if (total < (1 << 23)) {             // 32 bits: n_ctas is below 2^9
+        c0 = (int)((((uint32_t)x + 1) * (uint32_t)n_ctas - 1) / (uint32_t)total);
+        c1 = (int)((((uint32_t)x + (uint32_t)n) * (uint32_t)n_ctas - 1) / (uint32_t)total);
+    } else {
+        c0 = (int)(((x + 1) * n_ctas - 1) / total);
+        c1 = (int)(((x + n) * n_ctas - 1) / total);
     }
-    const int R = a.Hkv * a.HB, rb = gq * a.HB + gi / MH;
-    const int64_t total = a.prefix[a.B], n_ctas = min((int64_t)grid, total);
-    const int before = a.prefix[b], tiles = (a.prefix[b + 1] - before) / R;
-    if (tiles > 0) {
-        const int64_t first = before + (int64_t)rb * tiles, last = first + tiles - 1;
-        const int c0 = (int)(((first + 1) * n_ctas - 1) / total), c1 = (int)(((last + 1) * n_ctas - 1) / total);
-        for (int c = c0; c <= c1; c += kJoinAhead) {
-            float2 st[kJoinAhead], v[kJoinAhead];
+}
+// Those of the tiles of a segment of sequence b; none: c1 < c0.
+__device__ __forceinline__ void own_ctas(const Args& a, int b, int r, int W, int grid, int& c0, int& c1) {
+    const int total = a.prefix[a.B], before = a.prefix[b], units = (a.prefix[b + 1] - before) / (a.Hkv * a.HB);
+    c0 = 0, c1 = -1;
+    if (units > 0) ctas_of((int64_t)before + (int64_t)r * units + W, units - W, total, min(grid, total), c0, c1);
+}
+
+// Parts of a row (sequence b, head h) joined by a warp: of the prefix, if there is
+// one, then of the own keys, in the order of the keys, 32 at a time: a lane reads a
+// part's maximum and sum, the warp adds the outputs up with the lanes' factors.
+template <int D, Mode MODE>
+__device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row, const PrefixPlan& p, const float* part, const float2* stat) {
+    constexpr int V = D / 32, kRow = row_floats<D, MODE>(), kAhead = 8;
+    const int lane = threadIdx.x % 32, b = (int)(row / a.H), h = (int)row - b * a.H, g = h / a.G, gi = h - g * a.G;
+    int c0, c1;
+    own_ctas(a, b, g * a.HB + gi / MH, kUnits<false, MODE>, grid, c0, c1);
+    if (MODE == kMass && c0 == c1) return;       // finished by the CTA itself
+    int n_prefix = 0, s = 0, tile = 0, pc0 = 0;
+    bool alone = false;
+    if (MODE == kParts && p.grid > 0) {
+        const int at = b * a.G + gi;
+        tile = at / 128;
+        s = g * p.n_pairs + tile / 2;
+        alone = (tile & ~1) * 128 + 128 >= p.rows;       // the pair has this tile only: two parts a piece
+        int pc1;
+        ctas_of((int64_t)s * p.n_kt, p.n_kt, p.steps, p.grid, pc0, pc1);
+        n_prefix = (pc1 - pc0 + 1) << alone;
+    }
+    const int n = n_prefix + c1 - c0 + 1;
+    float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
-            for (int e = 0; e < kJoinAhead; ++e) {
-                st[e] = make_float2(-INFINITY, 0.f);
-                v[e] = make_float2(0.f, 0.f);
-                if (c + e <= c1) {
-                    const float* z = c0 == c1 ? a.own + row * (D + 2)
-                                              : a.part + ((int64_t)(2 * (c + e) + (c + e == c0)) * MH + gi % MH) * (D + 2);
-                    st[e] = *reinterpret_cast<const float2*>(z + D);
-                    v[e] = *reinterpret_cast<const float2*>(z + d);
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int base = 0; base < n; base += 32) {
+        const int i = base + lane;
+        const float* src = nullptr;
+        float2 st = make_float2(-INFINITY, 0.f);
+        if (i < n_prefix) {
+            const int64_t slab = alone ? 2 * (int64_t)(s + pc0) + i : 2 * (int64_t)(s + pc0 + i) + (tile & 1);
+            const int64_t z = slab * p.row_stride + (b * a.G + gi) % 128;
+            st = stat[z];
+            src = part + z * D;
+        } else if (i < n) {
+            const int c = c0 + i - n_prefix;
+            src = c0 == c1 ? a.own + row * kRow : a.part + ((int64_t)(2 * c + (c == c0)) * MH + gi % MH) * kRow;
+            st = *reinterpret_cast<const float2*>(src + D);
+        }
+        float top = st.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        const float old = top == -INFINITY ? 1.f : ex2(m - top);
+        const float f = st.y > 0.f ? ex2(st.x - top) : 0.f;      // sum 0: no key in the part, nothing else was written
+        float sum = f * st.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        m = top;
+        l = fmaf(l, old, sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= old;
+        const int count = min(n - base, 32);
+        for (int e = 0; e < count; e += kAhead) {
+            float x[kAhead][V], w[kAhead];
+#pragma unroll
+            for (int z = 0; z < kAhead; ++z) {
+                const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), (e + z) & 31));
+                w[z] = e + z < count ? __shfl_sync(0xffffffffu, f, (e + z) & 31) : 0.f;
+                if (w[z] > 0.f) {
+                    if constexpr (V == 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(from + lane * 4);
+                        x[z][0] = y.x, x[z][1] = y.y, x[z][2] = y.z, x[z][3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2*>(from + lane * 2);
+                        x[z][0] = y.x, x[z][1] = y.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[z][v] = 0.f;
                 }
             }
-            add(st, v);
+#pragma unroll
+            for (int z = 0; z < kAhead; ++z)
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] = fmaf(w[z], x[z][v], acc[v]);
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no keys at all
-    *reinterpret_cast<uint32_t*>(a.O + row * D + d) = pack_bf16(acc.x * inv, acc.y * inv);
-    if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + row * D + lane * V);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else *dst = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// mass_out = mass + the step's weights: each visible key's 2^(score - lse log2 e), summed
-// over the heads of its group in their order.  0 behind the sequence.
-constexpr int kMassThreads = 256;
-__global__ void __launch_bounds__(kMassThreads)
-mass_kernel(const Args a, int blocks) {
-    wait_for_previous_kernel();      // its lse, and the scores of the one before
-    const int r = blockIdx.x / blocks, b = r / a.Hkv, g = r % a.Hkv, j = blockIdx.x % blocks * kMassThreads + threadIdx.x;
-    if (j >= a.S) return;
-    const int64_t at = (int64_t)r * a.S + j;
+// Joins the parts of a shared prefix and of the sequences' own keys, a warp per row.
+constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+prefix_join_kernel(const Args a, int grid, const PrefixPlan p, const float* part, const float2* stat) {
+    wait_for_previous_kernel();
+    const int64_t row = (int64_t)blockIdx.x * kFinishWarps + threadIdx.x / 32;
+    if (row < (int64_t)a.B * a.H) join_row<D, kParts>(a, grid, row, p, part, stat);
+}
+
+// The masses of a step, and the outputs of the segments that several CTAs share.
+//   mass_out = mass + each visible key's 2^(score - lse log2 e), summed over the heads
+//   of its group in their order; 0 behind the sequence.
+// Blocks [0, joins): a warp per row.  The others: 4096 keys of a (sequence, key/value
+// head) each, four of a thread at a time, once the block knows the heads' log-sum-exps:
+// of the rows that are still being joined it adds up the parts' sums itself.  grid 0: every row
+// has been finished.
+constexpr int kMassRounds = 4, kMassKeys = kMassRounds * 4 * kFinishThreads, kMassHeads = 32;
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+mass_kernel(const Args a, int grid, int joins, int blocks) {
+    wait_for_previous_kernel();
+    if ((int)blockIdx.x < joins) {
+        const int64_t row = (int64_t)blockIdx.x * kFinishWarps + threadIdx.x / 32;
+        if (row < (int64_t)a.B * a.H) join_row<D, kMass>(a, grid, row, PrefixPlan{}, nullptr, nullptr);
+        return;
+    }
+    constexpr int kRow = row_floats<D, kMass>();
+    __shared__ float s_lse[kMassHeads];              // times log2 e
+    const int id = blockIdx.x - joins, r = id / blocks, b = r / a.Hkv, g = r - b * a.Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int first = (id - r * blocks) * kMassKeys, end = min(first + kMassKeys, a.S);
     const Seen x = seen(a, b);
-    float sum = 0.f;
-    if (j < x.n) {
-        sum = a.mass ? a.mass[at] : 0.f;
-        const int key = j >= x.lo ? x.sink_tiles * KT + j - x.lo : j;
-        if (j >= x.lo || j < a.n_sink) {
-            const int64_t row = (int64_t)b * a.H + g * a.G;
-            float w = 0.f;
-            for (int h = 0; h < a.G; ++h) w += ex2(a.score[(row + h) * a.stride + key] - a.lse[row + h] * kLog2e);
-            sum += w;
+    const float* mass = a.mass + (int64_t)r * a.S;
+    float* out = a.mass_out + (int64_t)r * a.S;
+    for (int j = max(first, x.n) + threadIdx.x; j < end; j += kFinishThreads) out[j] = 0.f;
+    const int last = min(end, x.n);
+    if (first >= last) return;
+    for (int h0 = 0; h0 < a.G; h0 += kMassHeads) {
+        const int heads = min(a.G - h0, kMassHeads);
+        const int64_t row0 = (int64_t)b * a.H + g * a.G + h0;
+        __syncthreads();                             // the last heads' have been read
+        for (int h = warp; h < heads; h += kFinishWarps) {
+            int c0 = 0, c1 = 0;
+            if (grid > 0) own_ctas(a, b, g * a.HB + (h0 + h) / MH, kUnits<false, kMass>, grid, c0, c1);
+            float m, l = 1.f;
+            if (c0 == c1) {
+                m = a.lse[row0 + h] * kLog2e;
+            } else {
+                float2 st = make_float2(-INFINITY, 0.f);
+                for (int c = c0 + lane; c <= c1; c += 32) {
+                    const float2 y = *reinterpret_cast<const float2*>(a.part + ((int64_t)(2 * c + (c == c0)) * MH + (h0 + h) % MH) * kRow + D);
+                    const float t = fmaxf(st.x, y.x);
+                    st = make_float2(t, st.y * ex2(st.x - t) + y.y * ex2(y.x - t));
+                }
+                m = st.x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                l = st.y * ex2(st.x - m);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            }
+            if (lane == 0) s_lse[h] = m + __log2f(l);
+        }
+        __syncthreads();
+        const float* score = a.score + row0 * a.stride;
+        for (int j0 = first + threadIdx.x; j0 < last; j0 += 4 * kFinishThreads) {
+            float before[4], w[4] = {0.f, 0.f, 0.f, 0.f};
+            int key[4];                              // the key's place among the scores; -1: not seen
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + e * kFinishThreads;
+                before[e] = j >= last ? 0.f : h0 > 0 ? out[j] : a.mass ? mass[j] : 0.f;
+                key[e] = j >= last ? -1 : j >= x.lo ? x.sink_tiles * KT + j - x.lo : j < a.n_sink ? j : -1;
+            }
+#pragma unroll 4
+            for (int h = 0; h < heads; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (key[e] >= 0) w[e] += ex2(score[(int64_t)h * a.stride + key[e]] - s_lse[h]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + e * kFinishThreads;
+                if (j < last) out[j] = before[e] + w[e];
+            }
         }
     }
-    a.mass_out[at] = sum;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t prefix_bytes(const DecodeProblem& p) { return align256(sizeof(int) * ((size_t)p.B + 1)); }
-size_t own_bytes(const DecodeProblem& p) { return align256(sizeof(float) * (size_t)p.B * p.H * (p.D + 2)); }
+size_t own_bytes(const DecodeProblem& p) { return align256(sizeof(float) * (size_t)p.B * p.H * (p.D + 4)); }
 size_t stat_bytes(const PrefixPlan& x) { return align256(sizeof(float2) * 2 * (size_t)x.slabs * x.row_stride); }
-size_t part_bytes(const DecodeProblem& p) { return align256(sizeof(float) * 2 * (size_t)num_sms() * MH * (p.D + 2)); }
+size_t part_bytes(const DecodeProblem& p) { return align256(sizeof(float) * 2 * (size_t)num_sms() * MH * (p.D + 4)); }
 
-dfa_status launch_mass(const Args& a, cudaStream_t s) {
-    const int blocks = (a.S + kMassThreads - 1) / kMassThreads;
-    const cudaError_t e = launch_overlapped(mass_kernel, dim3((unsigned)(a.B * a.Hkv * blocks)), kMassThreads, 0, s, a, blocks);
+// grid: CTAs of the step's kernel, 0 if it has finished every row.
+template <int D>
+dfa_status launch_mass(const Args& a, int grid, cudaStream_t s) {
+    const int blocks = (a.S + kMassKeys - 1) / kMassKeys, joins = grid > 0 ? (int)(((int64_t)a.B * a.H + kFinishWarps - 1) / kFinishWarps) : 0;
+    const cudaError_t e = launch_overlapped(mass_kernel<D>, dim3((unsigned)(joins + a.B * a.Hkv * blocks)), kFinishThreads, 0, s, a, grid,
+                                            joins, blocks);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode mass launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_MASS);
     return DFA_OK;
@@ -746,8 +865,8 @@ dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const voi
             return fail(DFA_ERR_CUDA, "decode: kernel attributes");
         mark_on_device(seen);
     }
-    if (plan.grid > 0 && (st = tc_prefix(p, plan, q, kp, vp, ss, sh, part, stat, s))) return st;
     const int n = (int)std::min<int64_t>(num_sms(), (int64_t)p.B * a.Hkv * a.HB * decode_tiles(p));
+    if (plan.grid > 0 && (st = tc_prefix(p, plan, q, kp, vp, ss, sh, part, stat, s))) return st;
     const size_t smem = Cfg<D>::kOffPrefix + sizeof(int) * (p.B + 1);
     cudaError_t e;
     if (plan.grid > 0) {
@@ -759,9 +878,8 @@ dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const voi
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-    constexpr int rows = kPrefixThreads / (D / 2);
-    e = launch_overlapped(prefix_join_kernel<D>, dim3((unsigned)(((int64_t)p.B * p.H + rows - 1) / rows)), kPrefixThreads, 0, s, a, n,
-                          plan, static_cast<const float*>(part), static_cast<const float2*>(stat));
+    e = launch_overlapped(prefix_join_kernel<D>, dim3((unsigned)(((int64_t)p.B * p.H + kFinishWarps - 1) / kFinishWarps)), kFinishThreads,
+                          0, s, a, n, plan, static_cast<const float*>(part), static_cast<const float2*>(stat));
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "prefix join launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_FWD);
     count_launch(DFA_KERNEL_MERGE);
@@ -819,17 +937,18 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mk, mv, a);
         if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
         count_launch(DFA_KERNEL_FWD);
-        return MASS ? launch_mass(a, s) : DFA_OK;
+        return MASS ? launch_mass<D>(a, 0, s) : DFA_OK;
     }
     spread<<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_FWD);
+    if (MASS) return launch_mass<D>(a, n, s);
     e = launch_overlapped(join_kernel<D>, dim3(segments, (std::min(a.G, MH) * (D / 2) + kJoinThreads - 1) / kJoinThreads),
                           kJoinThreads, 0, s, a, n);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
-    count_launch(DFA_KERNEL_FWD);
     count_launch(DFA_KERNEL_MERGE);
-    return MASS ? launch_mass(a, s) : DFA_OK;
+    return DFA_OK;
 }
 
 }  // namespace
