@@ -316,8 +316,8 @@ dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const voi
  *              no input
  *   workspace: >= dfa_attn_mass_workspace_size() bytes, 16-byte aligned, contents
  *              not preserved; calls that can overlap need one each
- * bf16 only, D in {64, 128}.  Two launches; may be captured; the same bits on
- * every call.  Keys may hold anything where no counted query sees them; a NaN in q
+ * bf16 only, D in {64, 128}.  One or two launches; may be captured; the same bits
+ * on every call.  Keys may hold anything where no counted query sees them; a NaN in q
  * or lse reaches the keys that its query sees. */
 size_t dfa_attn_mass_workspace_size(int B, int H, int H_kv, int S, int D);
 dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dtype dt, int B, int H, int H_kv, int S,

@@ -40,7 +40,7 @@ using namespace ptx;
 
 constexpr int kThreads = 640;
 constexpr int BT = 128;                    // keys or queries per tile
-constexpr int kTiles = 4;                  // key tiles per block
+constexpr int kTiles = 4;                  // key tiles per block, and regions of TMEM
 constexpr int kBlock = kTiles * BT;
 constexpr int kNSlots = 4;                 // query tiles whose lse are at hand
 constexpr float kLog2e = 1.4426950408889634f;
@@ -406,6 +406,329 @@ join_kernel(const Args a, int grid) {
     if (key < a.S) a.mass[(int64_t)r * a.S + key] = sum;
 }
 
+// ---------------------------------------------------------------- few queries
+// An observation window: the last queries of a group's heads, each head's padded to a
+// multiple of 32, are at most 512 rows.  They stay in shared memory as the B operand,
+// in P groups of 128, and the tiles of 128 keys stream through a ring: every key is
+// read once and its mass is finished there, in one launch.  A tile's P products go to
+// P of the four TMEM regions, so 4 / P tiles are in work at a time; a warpgroup adds
+// up a region, and the P sums of a key meet in shared memory, in their order.  Bound by
+// HBM up to 256 rows (64 queries of 4 heads), above that by the exponentials.
+constexpr int kMostCols = 512;
+
+template <int D, int P>
+struct TailCfg {
+    static constexpr int kTileBytes = BT * D * 2;
+    static constexpr int kSlots = D == 128 ? 6 - P : 8;
+    static constexpr int kOffK = P * kTileBytes;
+    static constexpr int kOffN = kOffK + kSlots * kTileBytes;
+    static constexpr int kOffPart = kOffN + 2 * P * BT * 4;
+    static constexpr int kOffBar = kOffPart + 2 * kTiles * BT * 4;
+    static constexpr int kSmem = kOffBar + 512;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct TailArgs {
+    int H, Hkv, G, S;
+    int window, n_sink;
+    int q0, pad, cols;     // first query; rows of a head, of a group
+    int jt, sink;          // first key tile of the window; 1: tile 0 before it, for the sinks
+    int n_tiles;           // tiles of a row (batch, key/value head)
+    int rows;
+    float scale_log2;
+    const float* lse;
+    float* mass;
+    int* err;
+};
+
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, 1)
+tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const TailArgs a) {
+    using C = TailCfg<D, P>;
+    constexpr int kTeams = kTiles / P;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {            // the swizzled tiles need a 1 KB aligned base
+        if (threadIdx.x == 0 && a.err) atomicExch(a.err, 2);
+        return;
+    }
+    uint8_t *sQ = smem, *sK = smem + C::kOffK;
+    float* sN = reinterpret_cast<float*>(smem + C::kOffN);                // [2][P * 128]
+    float* sPart = reinterpret_cast<float*>(smem + C::kOffPart);          // [team][2][P][128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* q_full = bars + 0;
+    uint64_t* q_empty = bars + 1;
+    uint64_t* n_full = bars + 2;             // [2]
+    uint64_t* n_empty = bars + 4;            // [2]
+    uint64_t* s_full = bars + 6;             // [kTiles]
+    uint64_t* s_free = bars + 10;            // [kTiles]
+    uint64_t* done = bars + 14;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 16);
+    uint64_t* k_full = bars + 20;            // [kSlots]
+    uint64_t* k_empty = k_full + C::kSlots;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&n_full[i], 1);
+            mbar_init(&n_empty[i], 4 * kTiles);
+        }
+        for (int w = 0; w < kTiles; ++w) {
+            mbar_init(&s_full[w], 1);
+            mbar_init(&s_free[w], 4);
+        }
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t steps = (int64_t)a.rows * a.n_tiles, begin = steps * blockIdx.x / gridDim.x, end = steps * (blockIdx.x + 1) / gridDim.x;
+    const int n = (int)(end - begin);        // at least one: the grid is no larger than the list
+    int r = (int)(begin / a.n_tiles), k = (int)(begin - (int64_t)r * a.n_tiles);
+    // The tile's first key; to the next tile: true if it is another row's.
+    auto key0 = [&] { return (a.sink ? (k == 0 ? 0 : a.jt + k - 1) : a.jt + k) * BT; };
+    auto next = [&] {
+        if (++k < a.n_tiles) return false;
+        k = 0;
+        ++r;
+        return true;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer of Q and K
+        bool ok = true, fresh = true;
+        uint32_t row = 0;
+        int i = 0;
+        for (; i < n && ok; ++i) {
+            if (fresh) {
+                ok = __all_sync(0xffffffffu, mbar_wait_acc(q_empty, (row & 1) ^ 1, abort_flag, a.err, nullptr));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(a.cols * D * 2));
+                    for (int c = 0; c < a.cols; c += 32)
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            tma_load_4d(sQ + c / BT * C::kTileBytes + blk * 16384 + c % BT * 128, &tmQ, q_full, blk * 64,
+                                        r % a.Hkv * a.G + c / a.pad, a.q0 + c % a.pad, r / a.Hkv);
+                }
+                __syncwarp();
+                ++row;
+            }
+            const int slot = i % C::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait_acc(&k_empty[slot], ((i / C::kSlots) & 1) ^ 1, abort_flag, a.err, nullptr));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes);
+                for (int blk = 0; blk < D / 64; ++blk)
+                    tma_load_4d(sK + slot * C::kTileBytes + blk * 16384, &tmK, &k_full[slot], blk * 64, r % a.Hkv, key0(), r / a.Hkv);
+            }
+            __syncwarp();
+            fresh = i + 1 < n && next();
+        }
+        if (!ok && lane == 0) {
+            // Aborted: let the copies already issued land before the CTA exits.
+            int dummy = 0;
+            if (row > 0) mbar_wait(q_full, (row - 1) & 1, &dummy, nullptr);
+            for (int m = max(i - C::kSlots, 0); m < i; ++m) mbar_wait(&k_full[m % C::kSlots], (m / C::kSlots) & 1, &dummy, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (one lane of a converged warp)
+        const uint32_t lead = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);      // uniform
+        const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        constexpr uint64_t kStep = C::kTileBytes >> 4;
+        bool ok = true, fresh = true;
+        uint32_t row = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && mbar_wait_issuer(bar, parity, abort_flag, a.err);
+            if (ok) tc_fence_after();
+            return ok;
+        };
+        for (int i = 0; i < n && ok; ++i) {
+            const int slot = i % C::kSlots, team = i % kTeams;
+            if (fresh && !wait(q_full, row++ & 1)) break;
+            if (!wait(&k_full[slot], (i / C::kSlots) & 1)) break;
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const int w = team * P + q;
+                if (!wait(&s_free[w], ((i / kTeams) & 1) ^ 1)) break;
+                const int cols = min(a.cols - q * BT, BT);
+                if (cols > 0) {                  // 257 to 384 columns leave the last group without any
+                    const uint32_t id = idesc_bf16_f32(BT, cols, false, false);
+                    const uint64_t a0 = dK + slot * kStep, b0 = dQ + q * kStep;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+                        mma_ss_lead(lead, tm + w * BT, a0 + off, b0 + off, id, kk > 0);
+                    }
+                }
+                mma_commit_lead(lead, &s_full[w]);
+            }
+            if (!ok) break;
+            mma_commit_lead(lead, &k_empty[slot]);
+            fresh = i + 1 < n && next();
+            if (fresh) mma_commit_lead(lead, q_empty);
+        }
+        // Drain: every MMA issued here has finished before TMEM is freed.
+        mma_commit_lead(lead, done);
+        int dummy = 0;
+        mbar_wait(done, 0, &dummy, a.err);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ keys that no query sees
+        const int from = a.sink * BT, len = a.jt * BT - from;
+        const int z0 = (int)((int64_t)len * blockIdx.x / gridDim.x), z1 = (int)((int64_t)len * (blockIdx.x + 1) / gridDim.x);
+        for (int y = 0; y < a.rows; ++y)
+            for (int z = z0 + lane; z < z1; z += 32) a.mass[(int64_t)y * a.S + from + z] = 0.f;
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ -lse log2 e of the queries, once per row
+        const int last = (int)((end - 1) / a.n_tiles);
+        for (int row = 0; r <= last; ++r, ++row) {
+            if (!__all_sync(0xffffffffu, mbar_wait_acc(&n_empty[row & 1], ((row >> 1) & 1) ^ 1, abort_flag, a.err, nullptr))) break;
+            const float* lse = a.lse + ((int64_t)(r / a.Hkv) * a.H + r % a.Hkv * a.G) * a.S;
+#pragma unroll 4
+            for (int c = lane; c < a.cols; c += 32) {
+                const int i = a.q0 + c % a.pad;
+                const float l = i < a.S ? lse[(int64_t)(c / a.pad) * a.S + i] : -INFINITY;
+                sN[(row & 1) * P * BT + c] = l == -INFINITY ? l : -l * kLog2e;    // no such query, or one that sees nothing
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&n_full[row & 1]);
+        }
+    } else {
+        // ------------------------------------------------------------ weights: a warpgroup per region, a thread per key
+        const int w = (warp - 4) / 4, team = w / P, q = w % P, row = (warp % 4) * 32 + lane;
+        const uint32_t tS = tmem + ((uint32_t)((warp % 4) * 32) << 16) + w * BT;
+        const int chunks = max(min(a.cols - q * BT, BT), 0) / 32, per = a.pad / 32;     // of 32 columns: here, per head
+        float* part = sPart + team * 2 * P * BT;
+        bool ok = true, fresh = true;
+        int seen_rows = 0;
+        uint32_t used = 0;
+        for (int i = 0; i < n; ++i) {
+            // A warp whose wait gave up still comes to its team's next barrier: the others may be waiting there.
+            if (fresh) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_acc(&n_full[seen_rows & 1], (seen_rows >> 1) & 1, abort_flag, a.err, nullptr));
+                ++seen_rows;
+            }
+            if (i % kTeams == team) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_acc(&s_full[w], used & 1, abort_flag, a.err, nullptr));
+                float sum = 0.f;
+                const int k0 = key0(), key = k0 + row;
+                if (ok) {
+                    tc_fence_after();
+                    const float* nl = sN + ((seen_rows - 1) & 1) * P * BT + q * BT;
+                    uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
+                    if (chunks > 0 && k0 + BT - 1 <= a.q0 && a.S - 1 - k0 < a.window) {
+                        uint32_t x[32], y[32];
+                        tmem_ld32_async(tS, x);
+#pragma unroll 1
+                        for (int c = 0; c < chunks; c += 2) {
+                            tmem_wait_ld32(x);
+                            if (c + 1 < chunks) tmem_ld32_async(tS + c * 32 + 32, y);
+                            add32(acc, x, a.scale_log2, nl + c * 32);
+                            if (c + 1 < chunks) {
+                                tmem_wait_ld32(y);
+                                if (c + 2 < chunks) tmem_ld32_async(tS + c * 32 + 64, x);
+                                add32(acc, y, a.scale_log2, nl + c * 32 + 32);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < chunks; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(tS + c * 32, x);
+                            const int at = key - (a.q0 + (q * 4 + c) % per * 32);
+                            mask32(x, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
+                            add32(acc, x, a.scale_log2, nl + c * 32);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[w]);
+                    sum = sum_f32x2(add_f32x2(acc[0], acc[1]));
+                }
+                if constexpr (P > 1) {
+                    // the parts of two tiles in turn: a buffer is written again only behind the barrier that comes
+                    // after it was read
+                    float* buf = part + (used & 1) * P * BT;
+                    if (q > 0) buf[q * BT + row] = sum;
+                    ok = named_bar_and(1 + team, P * BT, ok);
+                    if (q == 0)
+#pragma unroll
+                        for (int z = 1; z < P; ++z) sum += buf[z * BT + row];
+                }
+                if (!ok) break;
+                if (q == 0 && key < a.S) a.mass[(int64_t)r * a.S + key] = sum;
+                ++used;
+            }
+            fresh = i + 1 < n && next();
+            if (fresh || i + 1 == n) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&n_empty[(seen_rows - 1) & 1]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <int D, int P>
+dfa_status launch_tail(const SinkProblem& p, const TailArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, cudaStream_t s) {
+    static std::atomic<uint64_t> seen{0};
+    auto kernel = tail_mass_kernel<D, P>;
+    constexpr int smem = TailCfg<D, P>::kSmem;
+    if (first_on_device(seen)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return fail(DFA_ERR_CUDA, "key_mass: kernel attributes");
+        mark_on_device(seen);
+    }
+    kernel<<<(int)std::min<int64_t>(num_sms(), (int64_t)a.rows * a.n_tiles), kThreads, smem, s>>>(mq, mk, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_MASS);
+    return DFA_OK;
+}
+
+template <int D>
+dfa_status launch_tail(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, cudaStream_t s) {
+    CUtensorMap mq, mk;
+    if (!make_tmap_bshd(&mq, q, p.B, p.S, p.H, D, (int64_t)p.S * p.H * D, (int64_t)p.H * D, D, 32) ||
+        !make_tmap_bshd(&mk, k, p.B, p.S, p.Hkv, D, (int64_t)p.S * p.Hkv * D, (int64_t)p.Hkv * D, D))
+        return fail(DFA_ERR_CUDA, "tensor map encoding failed");
+    TailArgs a{};
+    a.H = p.H; a.Hkv = p.Hkv; a.G = p.H / p.Hkv; a.S = p.S;
+    a.window = p.window; a.n_sink = p.n_sink;
+    a.q0 = p.S - n_last;
+    a.pad = (n_last + 31) / 32 * 32;
+    a.cols = a.G * a.pad;
+    a.jt = std::max(a.q0 - p.window + 1, 0) / BT;
+    a.sink = p.n_sink > 0 && a.jt > 0;
+    a.n_tiles = (p.S + BT - 1) / BT - a.jt + a.sink;
+    a.rows = p.B * p.Hkv;
+    a.scale_log2 = p.scale * kLog2e;
+    a.lse = lse; a.mass = mass;
+    a.err = device_error_flag();
+    if (a.cols <= BT) return launch_tail<D, 1>(p, a, mq, mk, s);
+    if (a.cols <= 2 * BT) return launch_tail<D, 2>(p, a, mq, mk, s);
+    return launch_tail<D, 4>(p, a, mq, mk, s);
+}
+
 template <int D>
 dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,
                   cudaStream_t s) {
@@ -451,6 +774,8 @@ size_t key_mass_workspace() { return sizeof(float) * 2 * (size_t)num_sms() * kBl
 
 dfa_status tc_key_mass(const SinkProblem& p, int n_last, const void* q, const void* k, const float* lse, float* mass, void* ws,
                        cudaStream_t s) {
+    if ((int64_t)(p.H / p.Hkv) * ((n_last + 31) / 32 * 32) <= kMostCols)
+        return p.D == 128 ? launch_tail<128>(p, n_last, q, k, lse, mass, s) : launch_tail<64>(p, n_last, q, k, lse, mass, s);
     return p.D == 128 ? launch<128>(p, n_last, q, k, lse, mass, ws, s) : launch<64>(p, n_last, q, k, lse, mass, ws, s);
 }
 

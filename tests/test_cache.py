@@ -49,7 +49,8 @@ MASS = [
     (1, 6, 2, 128, 64, 16, 4, 128), (3, 3, 3, 129, 128, 129, 0, 1), (2, 8, 2, 300, 64, 300, 0, 300), (1, 8, 1, 513, 128, 100, 128, 513),
     (1, 4, 2, 700, 64, 1, 3, 700), (1, 2, 2, 1025, 128, 1025, 0, 64), (2, 6, 2, 1100, 64, 512, 17, 1099), (1, 5, 5, 1500, 128, 1500, 0, 1500),
     (1, 8, 2, 2000, 64, 130, 1, 333), (1, 3, 1, 2500, 128, 700, 4, 2500), (1, 2, 1, 2600, 64, 2000, 0, 129), (1, 4, 2, 2048, 128, 128, 128, 2048),
-    (1, 1, 1, 4200, 64, 40, 9, 4200),
+    (1, 1, 1, 4200, 64, 40, 9, 4200), (2, 4, 1, 900, 128, 900, 0, 128), (1, 8, 1, 1300, 64, 300, 5, 64), (3, 2, 2, 640, 128, 100, 128, 512),
+    (1, 3, 1, 1000, 64, 1000, 0, 65), (2, 16, 1, 2100, 128, 64, 3, 1), (1, 12, 4, 3001, 64, 2000, 0, 33), (5, 4, 4, 130, 128, 130, 0, 2),
 ]
 MASS_IDS = ["B{}H{}kv{}S{}D{}w{}s{}l{}".format(*c) for c in MASS]
 
