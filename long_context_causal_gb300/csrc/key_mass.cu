@@ -125,22 +125,54 @@ struct Cursor {
         const int k0 = kb * kBlock + w * BT, i0 = row0(a);
         return k0 < a.S && min(i0 + BT, a.S) > k0 && (i0 - k0 < BT + a.window - 1 || k0 < a.n_sink);
     }
+    // The first query tile from t on that does not see a key tile whole (or has rows past the end); t if it is one.
+    __device__ __forceinline__ int whole_until(const Args& a, int w) const {
+        const int k0 = kb * kBlock + w * BT, i0 = row0(a);
+        if (i0 < k0 + BT - 1) return t;
+        // i0 + 127 - k0 < window and i0 + 128 <= S
+        return t + max(min(min(a.window - (i0 - k0), a.S - i0) / BT, last - t), 0);
+    }
     // 32 columns each that hold queries
     __device__ __forceinline__ int chunks(const Args& a) const { return min(4, (a.S - row0(a) + 31) / 32); }
 };
 
 // Weights of 32 queries for this thread's key: 2^(s c + n), n the queries' -lse log2 e;
 // see: the queries that see the key.
-__device__ __forceinline__ void add32(uint64_t (&acc)[2], const uint32_t (&u)[32], float c, const float* n) {
+__device__ __forceinline__ void add32(uint64_t (&acc)[4], const uint32_t (&u)[32], float c, const float* n) {
     const uint64_t cc = pack_f32x2(c, c);
+    uint64_t x[16];
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(n + e);
-        const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), cc, pack_f32x2(m.x, m.y)));
-        const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])), cc, pack_f32x2(m.z, m.w)));
-        acc[0] = add_f32x2(acc[0], pack_f32x2(ex2(x.x), ex2(x.y)));
-        acc[1] = add_f32x2(acc[1], pack_f32x2(ex2(y.x), ex2(y.y)));
+    for (int e = 0; e < 16; e += 2) {
+        const float4 m = *reinterpret_cast<const float4*>(n + 2 * e);
+        x[e] = fma_f32x2(pack_f32x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), cc, pack_f32x2(m.x, m.y));
+        x[e + 1] = fma_f32x2(pack_f32x2(__uint_as_float(u[2 * e + 2]), __uint_as_float(u[2 * e + 3])), cc, pack_f32x2(m.z, m.w));
     }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 y = unpack_f32x2(x[e]);
+        x[e] = pack_f32x2(ex2(y.x), ex2(y.y));
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e & 3] = add_f32x2(acc[e & 3], x[e]);
+}
+__device__ __forceinline__ float sum4(const uint64_t (&acc)[4]) {
+    return sum_f32x2(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
+}
+// Those of 128 queries, all of which see it: each piece's load runs under the arithmetic of the one before.
+__device__ __forceinline__ void add128(uint64_t (&acc)[4], uint32_t tS, float c, const float* n) {
+    uint32_t x[32], y[32];
+    tmem_ld32_async(tS, x);
+    tmem_wait_ld32(x);
+    tmem_ld32_async(tS + 32, y);
+    add32(acc, x, c, n);
+    tmem_wait_ld32(y);
+    tmem_ld32_async(tS + 64, x);
+    add32(acc, y, c, n + 32);
+    tmem_wait_ld32(x);
+    tmem_ld32_async(tS + 96, y);
+    add32(acc, x, c, n + 64);
+    tmem_wait_ld32(y);
+    add32(acc, y, c, n + 96);
 }
 __device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t see) {
 #pragma unroll
@@ -260,7 +292,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         uint32_t blocks = 0, used[kTiles] = {0, 0, 0, 0};
         bool ok = true, fresh = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && mbar_wait_issuer(bar, parity, abort_flag, a.err);
+            ok = ok && mbar_wait_spin(bar, parity, abort_flag, a.err);
             if (ok) tc_fence_after();
             return ok;
         };
@@ -322,18 +354,20 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         float total = 0.f;
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const int slot = i % kNSlots;
-            const bool sees = c.sees(a, w);
-            ok = mbar_wait_acc(&n_full[slot], (i / kNSlots) & 1, abort_flag, a.err, nullptr);
-            if (sees) ok = ok && mbar_wait_acc(&s_full[w], used & 1, abort_flag, a.err, nullptr);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (sees) {
-                ++used;
-                tc_fence_after();
-                const float* nl = sN + slot * BT;
-                const int i0 = c.row0(a), key = c.kb * kBlock + row, k0 = c.kb * kBlock + w * BT, chunks = c.chunks(a);
-                uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
-                if (chunks == 4 && k0 + BT - 1 <= i0 && (i0 + BT - 1 - k0 < a.window)) {
+            // Steps whose 128 queries see all keys of the tile, up to the head's last one or the first that does not.
+            const int whole = c.whole_until(a, w) - c.t;
+            if (whole > 0) {
+                const int end_i = min(i + whole, n);
+                c.t += end_i - i - 1;
+#pragma unroll 1
+                for (;; ++i) {
+                    const int slot = i % kNSlots;
+                    const float* nl = sN + slot * BT;
+                    ok = mbar_wait_acc(&n_full[slot], (i / kNSlots) & 1, abort_flag, a.err, nullptr) &&
+                         mbar_wait_acc(&s_full[w], used++ & 1, abort_flag, a.err, nullptr);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after();
+                    uint64_t acc[4] = {0, 0, 0, 0};
                     uint32_t x[32], y[32];
                     tmem_ld32_async(tS, x);
                     tmem_wait_ld32(x);
@@ -350,7 +384,24 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[w]);
                     add32(acc, y, a.scale_log2, nl + 96);
-                } else {
+                    total += sum4(acc);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&n_empty[slot]);
+                    if (i + 1 == end_i) break;
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
+            } else {
+                const int slot = i % kNSlots;
+                const bool sees = c.sees(a, w);
+                ok = mbar_wait_acc(&n_full[slot], (i / kNSlots) & 1, abort_flag, a.err, nullptr);
+                if (sees) ok = ok && mbar_wait_acc(&s_full[w], used & 1, abort_flag, a.err, nullptr);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (sees) {
+                    ++used;
+                    tc_fence_after();
+                    const float* nl = sN + slot * BT;
+                    const int i0 = c.row0(a), key = c.kb * kBlock + row, chunks = c.chunks(a);
+                    uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int q = 0; q < chunks; ++q) {
                         uint32_t x[32];
@@ -363,11 +414,11 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[w]);
+                    total += sum4(acc);
                 }
-                total += sum_f32x2(add_f32x2(acc[0], acc[1]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&n_empty[slot]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&n_empty[slot]);
             const int r = c.r, key = c.kb * kBlock + row;
             const bool last_step = c.h == a.G - 1 && c.t == c.last - 1;
             if (last_step || i + 1 == n) {
@@ -554,7 +605,7 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true, fresh = true;
         uint32_t row = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && mbar_wait_issuer(bar, parity, abort_flag, a.err);
+            ok = ok && mbar_wait_spin(bar, parity, abort_flag, a.err);
             if (ok) tc_fence_after();
             return ok;
         };
@@ -600,12 +651,15 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int row = 0; r <= last; ++r, ++row) {
             if (!__all_sync(0xffffffffu, mbar_wait_acc(&n_empty[row & 1], ((row >> 1) & 1) ^ 1, abort_flag, a.err, nullptr))) break;
             const float* lse = a.lse + ((int64_t)(r / a.Hkv) * a.H + r % a.Hkv * a.G) * a.S;
-#pragma unroll 4
-            for (int c = lane; c < a.cols; c += 32) {
-                const int i = a.q0 + c % a.pad;
-                const float l = i < a.S ? lse[(int64_t)(c / a.pad) * a.S + i] : -INFINITY;
-                sN[(row & 1) * P * BT + c] = l == -INFINITY ? l : -l * kLog2e;    // no such query, or one that sees nothing
+            float x[P * 4];
+#pragma unroll
+            for (int e = 0; e < P * 4; ++e) {
+                const int c = e * 32 + lane, h = e * 32 / a.pad, i = a.q0 + c - h * a.pad;   // 32 columns are one head's
+                const float l = c < a.cols && i < a.S ? lse[(int64_t)h * a.S + i] : -INFINITY;
+                x[e] = l == -INFINITY ? l : -l * kLog2e;      // no such query, or one that sees nothing
             }
+#pragma unroll
+            for (int e = 0; e < P * 4; ++e) sN[(row & 1) * P * BT + e * 32 + lane] = x[e];
             __syncwarp();
             if (lane == 0) mbar_arrive(&n_full[row & 1]);
         }
@@ -631,19 +685,16 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if (ok) {
                     tc_fence_after();
                     const float* nl = sN + ((seen_rows - 1) & 1) * P * BT + q * BT;
-                    uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
-                    if (chunks > 0 && k0 + BT - 1 <= a.q0 && a.S - 1 - k0 < a.window) {
-                        uint32_t x[32], y[32];
-                        tmem_ld32_async(tS, x);
+                    uint64_t acc[4] = {0, 0, 0, 0};
+                    if (k0 + BT - 1 <= a.q0 && a.S - 1 - k0 < a.window) {
+                        if (chunks == 4) {
+                            add128(acc, tS, a.scale_log2, nl);
+                        } else {
 #pragma unroll 1
-                        for (int c = 0; c < chunks; c += 2) {
-                            tmem_wait_ld32(x);
-                            if (c + 1 < chunks) tmem_ld32_async(tS + c * 32 + 32, y);
-                            add32(acc, x, a.scale_log2, nl + c * 32);
-                            if (c + 1 < chunks) {
-                                tmem_wait_ld32(y);
-                                if (c + 2 < chunks) tmem_ld32_async(tS + c * 32 + 64, x);
-                                add32(acc, y, a.scale_log2, nl + c * 32 + 32);
+                            for (int c = 0; c < chunks; ++c) {
+                                uint32_t x[32];
+                                tmem_ld32(tS + c * 32, x);
+                                add32(acc, x, a.scale_log2, nl + c * 32);
                             }
                         }
                     } else {
@@ -659,7 +710,7 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[w]);
-                    sum = sum_f32x2(add_f32x2(acc[0], acc[1]));
+                    sum = sum4(acc);
                 }
                 if constexpr (P > 1) {
                     // the parts of two tiles in turn: a buffer is written again only behind the barrier that comes
