@@ -109,10 +109,47 @@ __device__ __forceinline__ void mark(uint32_t (&u)[PER], int at, int n, int lo, 
     }
 }
 
-template <int LOG_C, int PER>
+struct CopyArgs {
+    int Hkv, S, keep, log_u;      // 16-byte units of a row: 2^log_u
+    const int32_t* kv_len;
+    const int32_t* kept;
+    const uint4 *k, *v;
+    uint4 *k_out, *v_out;
+    int64_t in_sb, in_ss, in_sh, out_sb, out_ss, out_sh;   // units
+};
+
+// Rows from(r) -> r of a (sequence, head)'s keys and values, r < rows, by the CTA.
+template <typename From>
+__device__ __forceinline__ void copy_rows(const CopyArgs& c, int b, int g, int rows, From from) {
+    constexpr int kAhead = 4;
+    const int units = rows << c.log_u;
+    for (int y = threadIdx.x; y < units; y += kAhead * kThreads) {
+        uint4 k[kAhead], v[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const int x = y + e * kThreads;
+            if (x >= units) break;
+            const int64_t at = b * c.in_sb + from(x >> c.log_u) * c.in_ss + g * c.in_sh + (x & ((1 << c.log_u) - 1));
+            k[e] = c.k[at];
+            v[e] = c.v[at];
+        }
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const int x = y + e * kThreads;
+            if (x >= units) break;
+            const int64_t at = b * c.out_sb + (x >> c.log_u) * c.out_ss + g * c.out_sh + (x & ((1 << c.log_u) - 1));
+            c.k_out[at] = k[e];
+            c.v_out[at] = v[e];
+        }
+    }
+}
+
+// MOVE: the rows are moved as well (one CTA per row, all its keys in one chunk).
+template <int LOG_C, int PER, bool MOVE>
 __global__ void __launch_bounds__(kThreads, 1)
-select_kernel(const Args a) {
+select_kernel(const Args a, const CopyArgs copy) {
     constexpr int C = 1 << LOG_C;
+    static_assert(!MOVE || C == 1, "one CTA per row");
     // Digits of 11 bits; where CTAs share a row, of 8, for all of them read all histograms.  Copies of a
     // histogram, so that equal digits of a warp's keys wait less for one another.
     constexpr int kBits = C == 1 ? 11 : 8, kBins = 1 << kBits, kCopies = C == 1 ? 2 : 8;
@@ -122,7 +159,7 @@ select_kernel(const Args a) {
     } sm;
     __shared__ uint32_t folded[2][C > 1 ? kBins : 1], s_scan[kWarps], s_count[2], s_found[3];
     const int rank = blockIdx.x % C, row = blockIdx.x / C, b = row / a.Hkv;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, lane = tid % 32;
     const int n = min(max(a.kv_len[b], 0), a.S);
     const float* mass = a.mass + (int64_t)row * a.S;
     float* mass_out = a.mass_out + (int64_t)row * a.cap;
@@ -138,6 +175,7 @@ select_kernel(const Args a) {
             mass_out[r] = mass[r];
             kept[r] = r;
         }
+        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, n, [](int r) -> int64_t { return r; });
         return;
     }
     const int lo = a.n_first, hi = n - a.n_recent;      // the keys that compete
@@ -264,20 +302,12 @@ select_kernel(const Args a) {
             kept[r] = j;
             mass_out[r] = mass[j];
         }
+        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, r1, [&](int r) -> int64_t { return first + sm.list[r]; });
         if (chunks > 1) __syncthreads();
     }
     __syncwarp();
     if (C > 1) cluster_sync();       // no CTA leaves while another one may still read its counts
 }
-
-struct CopyArgs {
-    int Hkv, S, keep, log_u;      // 16-byte units of a row: 2^log_u
-    const int32_t* kv_len;
-    const int32_t* kept;
-    const uint4 *k, *v;
-    uint4 *k_out, *v_out;
-    int64_t in_sb, in_ss, in_sh, out_sb, out_ss, out_sh;   // units
-};
 
 constexpr int kCopyThreads = 256, kCopyAhead = 4;
 // Block (x, b): units [x, x + 1) * kCopyThreads * kCopyAhead of sequence b's rows, heads
@@ -314,6 +344,9 @@ copy_kernel(const CopyArgs a, int blocks) {
 
 }  // namespace
 
+// Rows of up to this many 16-byte units (keys; the values as many) are moved by the CTA that chose them: one launch.
+constexpr int kMoveUnits = 4096;
+
 dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, const int32_t* kv_len, const float* mass,
                        void* k_out, void* v_out, int32_t* len_out, float* mass_out, int32_t* kept, cudaStream_t s) {
     const Args a{p.Hkv, p.S, p.keep, p.cap, p.n_first, p.n_recent, kv_len, mass, len_out, mass_out, kept};
@@ -323,21 +356,6 @@ dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, cons
     // by eight 42.  Rows of 501 keys with 4 keys a thread 10.3, 16 a thread 14.3.
     int log_c = 0;
     while ((1 << log_c) < kMaxCluster && p.S > (kThreads * 16 << log_c)) ++log_c;
-    void (*const kernels[])(const Args) = {select_kernel<0, 16>, select_kernel<1, 16>, select_kernel<2, 16>, select_kernel<3, 16>};
-    void (*const kernel)(const Args) = log_c == 0 && p.S <= kThreads * 4 ? select_kernel<0, 4> : kernels[log_c];
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1u << log_c;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)rows << log_c);
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));
-    count_launch(DFA_KERNEL_EVICT);
     const int unit = 16 / p.elt;
     CopyArgs c{};
     c.Hkv = p.Hkv; c.S = p.S; c.keep = p.keep;
@@ -348,7 +366,26 @@ dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, cons
     c.k_out = static_cast<uint4*>(k_out); c.v_out = static_cast<uint4*>(v_out);
     c.in_sb = p.in_sb / unit; c.in_ss = p.in_ss / unit; c.in_sh = p.in_sh / unit;
     c.out_sb = p.out_sb / unit; c.out_ss = p.out_ss / unit; c.out_sh = p.out_sh / unit;
-    const int64_t units = (int64_t)std::min(p.keep, p.S) * p.Hkv << c.log_u;
+    const int most = std::min(p.keep, p.S);
+    const bool small = p.S <= kThreads * 4, move = small && (most << c.log_u) <= kMoveUnits;
+    using Kernel = void (*)(const Args, const CopyArgs);
+    const Kernel kernels[] = {small ? (move ? Kernel(select_kernel<0, 4, true>) : Kernel(select_kernel<0, 4, false>)) : Kernel(select_kernel<0, 16, false>),
+                              select_kernel<1, 16, false>, select_kernel<2, 16, false>, select_kernel<3, 16, false>};
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1u << log_c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)rows << log_c);
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = log_c > 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[log_c], a, c);
+    if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));
+    count_launch(DFA_KERNEL_EVICT);
+    if (move) return DFA_OK;
+    const int64_t units = (int64_t)most * p.Hkv << c.log_u;
     const int blocks = (int)((units + kCopyThreads * kCopyAhead - 1) / (kCopyThreads * kCopyAhead));
     e = launch_overlapped(copy_kernel, dim3((unsigned)(p.B * blocks)), kCopyThreads, 0, s, c, blocks);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "evict copy launch: %s", cudaGetErrorString(e));

@@ -179,7 +179,10 @@ __device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t see) {
     for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : 0xff800000u;
 }
 
-template <int D>
+// CLUSTER: a block's steps are shared by a cluster of eight CTAs, an eighth each, whose sums
+// meet in the first one's shared memory: one launch.
+constexpr int kCluster = 8, kJoinSteps = 4;
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
 key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const Args a) {
     using C = Cfg<D>;
@@ -233,12 +236,27 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int64_t begin = a.steps * blockIdx.x / gridDim.x, end = a.steps * (blockIdx.x + 1) / gridDim.x;
-    const int n = (int)(end - begin);        // at least one: the grid is no larger than the list
     Cursor c;
-    c.find(a, begin);
+    int n, rank = 0;
+    float total = 0.f;                       // of a key's weights, in the threads that add them up
+    if constexpr (CLUSTER) {
+        rank = blockIdx.x % kCluster;
+        c.r = blockIdx.x / kCluster / a.n_kb;
+        c.kb = blockIdx.x / kCluster % a.n_kb;
+        tiles_of(a, c.kb, c.first, c.last);
+        const int per = max(c.last - c.first, 0), all = per * a.G, from = all * rank / kCluster;
+        n = all * (rank + 1) / kCluster - from;
+        c.h = per ? from / per : 0;
+        c.t = c.first + (per ? from % per : 0);
+    } else {
+        const int64_t begin = a.steps * blockIdx.x / gridDim.x, end = a.steps * (blockIdx.x + 1) / gridDim.x;
+        n = (int)(end - begin);              // at least one: the grid is no larger than the list
+        c.find(a, begin);
+    }
 
-    if (warp == 0) {
+    if (CLUSTER && n == 0) {
+        // nothing to sweep
+    } else if (warp == 0) {
         // ------------------------------------------------------------ TMA producer of K and Q
         uint32_t blocks = 0;
         bool ok = true, fresh = true;
@@ -351,7 +369,6 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint32_t tS = tmem + ((uint32_t)((warp % 4) * 32) << 16) + w * BT;
         uint32_t used = 0;
         bool from_start = c.h == 0 && c.t == c.first;
-        float total = 0.f;
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             // Steps whose 128 queries see all keys of the tile, up to the head's last one or the first that does not.
@@ -421,7 +438,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             const int r = c.r, key = c.kb * kBlock + row;
             const bool last_step = c.h == a.G - 1 && c.t == c.last - 1;
-            if (last_step || i + 1 == n) {
+            if (!CLUSTER && (last_step || i + 1 == n)) {
                 if (last_step && from_start) {
                     if (key < a.S) a.mass[(int64_t)r * a.S + key] = total;
                 } else {
@@ -437,6 +454,20 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, 512);
+    if constexpr (CLUSTER) {
+        // [rank][key] in the first CTA's key tiles, which nothing reads any more
+        __syncwarp();
+        cluster_sync();
+        const int at = threadIdx.x - 128;
+        if (at >= 0) st_cluster_f32(map_to_rank(smem_u32(smem) + (uint32_t)(rank * kBlock + at) * 4, 0), total);
+        __syncwarp();
+        cluster_sync();
+        const int key = c.kb * kBlock + at;
+        if (rank != 0 || at < 0 || key >= a.S) return;
+        float sum = 0.f;
+        for (int r = 0; r < kCluster; ++r) sum += reinterpret_cast<const float*>(smem)[r * kBlock + at];
+        a.mass[(int64_t)c.r * a.S + key] = sum;
+    }
 }
 
 // A block per key block: what no query sees is 0, what several CTAs swept is added up.
@@ -803,11 +834,41 @@ dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k
     a.part = static_cast<float*>(ws);
     a.err = device_error_flag();
     static std::atomic<uint64_t> seen{0};
-    auto kernel = key_mass_kernel<D>;
+    static std::atomic<int> clusters{0};             // that run at a time
+    auto kernel = key_mass_kernel<D, false>;
+    auto clustered = key_mass_kernel<D, true>;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)kCluster);
+    cfg.blockDim = dim3((unsigned)kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     if (first_on_device(seen)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
+        int k = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(clustered, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&k, clustered, &cfg) != cudaSuccess)
             return fail(DFA_ERR_CUDA, "key_mass: kernel attributes");
+        clusters.store(k);
         mark_on_device(seen);
+    }
+    // One round of clusters, if the longest of their shares is not longer than an equal share of all SMs and the second
+    // launch (kJoinSteps).
+    const int64_t segments = (int64_t)p.B * p.Hkv * a.n_kb;
+    int64_t longest = 0;
+    if (segments <= clusters.load())
+        for (int kb = 0; kb < a.n_kb; ++kb) longest = std::max(longest, (tiles_before(a, kb + 1) - tiles_before(a, kb)) * a.G);
+    if (segments <= clusters.load() && (longest + kCluster - 1) / kCluster <= (a.steps + num_sms() - 1) / num_sms() + kJoinSteps) {
+        cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * a.n_kb * kCluster));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mq, mk, a);
+        if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
+        count_launch(DFA_KERNEL_MASS);
+        return DFA_OK;
     }
     const int grid = (int)std::min<int64_t>(num_sms(), a.steps);
     kernel<<<grid, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, a);

@@ -297,6 +297,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 // Arrives on the mbarrier at `saddr` of CTA `rank`: what this thread, and those
 // of its warp before the last __syncwarp(), wrote is visible to a thread that
 // has waited there and called fence_cluster().

@@ -85,14 +85,19 @@ struct Args {
     int stride;                   // 64 * the most tiles of a segment
     const float* mass;            // [B, Hkv, S], null: zero
     float* mass_out;              // [B, Hkv, S]; may be `mass`
+    int fused;                    // CLUSTER: the scores stay in shared memory and the cluster forms the masses
     // PARTS: a segment that one CTA covers leaves its rows' parts here, [B * H][row_floats]
     float* own;
+    PrefixPlan p;                 // PARTS, SOLO: the prefix's parts
+    const float* p_part;
+    const float2* p_stat;
 };
-enum Mode { kPlain, kMass, kParts };
+// Plain; with masses; behind a prefix: leaving parts, or (SOLO) a CTA per segment, which adds the prefix's.
+enum Mode { kPlain, kMass, kParts, kSolo };
 // Units that a segment counts for beside its tiles when the tiles are dealt: it costs a CTA 2 us beside
 // 0.7 to 0.9 us per tile.  (The plain step deals tiles alone.)
 template <bool CLUSTER, Mode MODE>
-constexpr int kUnits = CLUSTER || MODE == kPlain ? 0 : 2;
+constexpr int kUnits = CLUSTER || MODE == kPlain || MODE == kSolo ? 0 : 2;
 // Floats of a head's partial: unnormalised O, max, sum.
 template <int D, Mode MODE>
 constexpr int row_floats() { return MODE == kPlain ? D + 2 : D + 4; }
@@ -133,9 +138,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Stores four consecutive scores of a head's row.
-__device__ __forceinline__ void store_scores(const Args& a, int64_t row, int at, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(a.score + row * a.stride + at) = make_float4(x[0], x[1], x[2], x[3]);
+// Floats of a head's scores in shared memory: eight tiles of a cluster's CTA, rows on different banks.
+constexpr int kScoreRow = kClusterTiles / kCluster * KT + 4;
+constexpr int kScoreBytes = MH * kScoreRow * 4;
+__device__ __forceinline__ void store4(float* at, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // Cursor over a CTA's range.  A segment counts for W units more than its tiles, which
@@ -172,6 +179,43 @@ __device__ __forceinline__ void next_segment(const Args& a, Cursor& c) {
     }
 }
 
+// The CTAs that hold units [x, x + n) of a list of `total` dealt to n_ctas in equal
+// ranges: the last ones whose ranges begin at or before them.
+__device__ __forceinline__ void ctas_of(int64_t x, int64_t n, int64_t total, int n_ctas, int& c0, int& c1) {
+    if (total < (1 << 23)) {             // 32 bits: n_ctas is below 2^9
+        c0 = (int)((((uint32_t)x + 1) * (uint32_t)n_ctas - 1) / (uint32_t)total);
+        c1 = (int)((((uint32_t)x + (uint32_t)n) * (uint32_t)n_ctas - 1) / (uint32_t)total);
+    } else {
+        c0 = (int)(((x + 1) * n_ctas - 1) / total);
+        c1 = (int)(((x + n) * n_ctas - 1) / total);
+    }
+}
+// Where the prefix's parts of the heads of a group are, in the order of the keys.
+struct PrefixParts {
+    int b, c0, count;             // sequence; first CTA, number of pieces
+    int s, z, r, n;               // of a head: segment, tile of the pair, row; parts
+    bool alone;
+    int g;
+    __device__ __forceinline__ PrefixParts(const Args& a, int sequence, int group) : b(sequence), c0(0), count(0), s(-1), n(0), g(group) {}
+    __device__ __forceinline__ void head(const Args& a, int gi) {
+        if (a.p.grid == 0) return;
+        const int at = b * a.G + gi, tile = at / 128, seg = g * a.p.n_pairs + tile / 2;
+        if (seg != s) {
+            s = seg;
+            int c1;
+            ctas_of((int64_t)s * a.p.n_kt, a.p.n_kt, a.p.steps, a.p.grid, c0, c1);
+            count = c1 - c0 + 1;
+        }
+        r = at % 128;
+        z = tile & 1;
+        alone = (tile & ~1) * 128 + 128 >= a.p.rows;         // the pair has this tile only: two parts a piece
+        n = count << alone;
+    }
+    __device__ __forceinline__ int64_t at(const Args& a, int i) const {
+        return (alone ? 2 * (int64_t)(s + c0) + i : 2 * (int64_t)(s + c0 + i) + z) * a.p.row_stride + r;
+    }
+};
+
 template <int D, bool CLUSTER, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
@@ -189,6 +233,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     uint64_t* empty = full + C::kStages;                               // [kStages]
     volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
     int* prefix = reinterpret_cast<int*>(smem + C::kOffPrefix);
+    float* s_score = reinterpret_cast<float*>(smem + C::kOffPrefix);   // CLUSTER, MASS: in its place
     int* s_scan = reinterpret_cast<int*>(smem + C::kOffBar + 192);     // [9]
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -213,6 +258,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         c.s = seen(a, c.b);
         begin = c.v = c.s.tiles * rank / kCluster;
         end = c.s.tiles * (rank + 1) / kCluster;
+        __syncthreads();
+    } else if constexpr (MODE == kSolo) {
+        c.b = blockIdx.x / R;
+        c.r = blockIdx.x % R;
+        c.s = seen(a, c.b);
+        begin = c.v = 0;
+        end = c.s.tiles;
         __syncthreads();
     } else {
         // Units before each sequence, all segments counted.
@@ -304,7 +356,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     const int g = lane / 4, t = lane % 4, grp = warp / 4, w16 = (warp % 4) * 16;
     const int rn = (g >> 1) | ((g & 1) << 2);
     bool ok = true;
-    float4 mine[2];                      // CLUSTER: this CTA's part of at most two groups of four dims
+    float4 mine[2];                      // CLUSTER, SOLO: this CTA's part of at most two groups of four dims
     float2 mine_ml[2];
     mine_ml[0] = mine_ml[1] = make_float2(-INFINITY, 0.f);
     mine[0] = mine[1] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -314,7 +366,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int v1 = min(c.s.tiles + W, c.v + end - x), k0 = max(c.v - W, 0), k1 = v1 - W;
         x += v1 - c.v;
         if (k1 <= k0) {                      // nothing but what stands before the tiles (or an empty share)
-            if constexpr (CLUSTER) break;
+            if constexpr (CLUSTER || MODE == kSolo) break;
             if (x < end) next_segment(a, c);
             continue;
         }
@@ -367,15 +419,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                     }
                 if constexpr (MODE == kMass) {
                     // keys 4 m + t of a head's 16 in lane t become 4 t .. 4 t + 3
-                    const int64_t row = (int64_t)c.b * a.H + h0 + g;
-                    const int at = k * KT + w16 + 4 * t;
+                    const bool here = CLUSTER && a.fused;
+                    float* to = here ? s_score + g * kScoreRow + i * KT : a.score + ((int64_t)c.b * a.H + h0 + g) * a.stride + k * KT;
+                    to += w16 + 4 * t;
                     float lo[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
                     quad_transpose(lo, lane);
-                    if (g < nh) store_scores(a, row, at, lo);
+                    if (g < nh) store4(to, lo);
                     if (nh > 8) {
                         float hi[4] = {s[0][2], s[0][3], s[1][2], s[1][3]};
                         quad_transpose(hi, lane);
-                        if (g + 8 < nh) store_scores(a, row + 8, at, hi);
+                        if (g + 8 < nh) store4(to + 8 * (here ? kScoreRow : a.stride), hi);
                     }
                 }
                 float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
@@ -476,7 +529,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            if constexpr (CLUSTER) {
+            if constexpr (CLUSTER || MODE == kSolo) {
                 const bool second = y >= kConsumers * 32;
                 mine[second] = acc;
                 mine_ml[second] = make_float2(m, l);
@@ -492,7 +545,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 if (d == 0) *reinterpret_cast<float2*>(part + h * kRow + D) = make_float2(m, l);
             }
         }
-        if constexpr (CLUSTER) break;
+        if constexpr (CLUSTER || MODE == kSolo) break;
         named_bar_sync(1, kConsumers * 32);  // the merge buffer is read before the next segment fills it
         if (x < end) next_segment(a, c);
     }
@@ -501,8 +554,38 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int h0 = c.r / a.HB * a.G + c.r % a.HB * MH, nh = min(a.G - c.r % a.HB * MH, MH);
         constexpr int kRow = D + 4;          // unnormalised output, maximum, sum
         static_assert(kCluster * MH * kRow * 4 <= C::kOffMerge, "parts");
+        const bool masses = MODE == kMass && a.fused;
+        // The masses of this CTA's keys so far, and their place; -1: none.
+        constexpr int kEach = kClusterTiles / kCluster * KT / (kConsumers * 32);
+        float before[kEach];
+        int64_t at[kEach];
+        if (masses) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int y = threadIdx.x + e * kConsumers * 32;
+                at[e] = -1;
+                before[e] = 0.f;
+                if (y >= (end - begin) * KT) continue;
+                int key, n;
+                tile_keys(c.s, a.n_sink, begin + y / KT, key, n);
+                if (y % KT >= n) continue;
+                at[e] = ((int64_t)c.b * a.Hkv + c.r) * a.S + key + y % KT;
+                if (a.mass) before[e] = a.mass[at[e]];
+            }
+        }
         __syncwarp();
         cluster_sync();
+        // Maxima and sums go to every CTA where each one forms the masses of its keys ([rank][head], in the merge buffer).
+        if (masses && (int)threadIdx.x < nh) {
+            const int h = threadIdx.x;
+            float m = -INFINITY, l = 0.f;
+            if (end > begin) {
+                for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, s_max[w * MH + h]);
+                for (int w = 0; w < kConsumers; ++w) l = fmaf(ex2(s_max[w * MH + h] - m), s_sum[w * MH + h], l);
+            }
+            for (int r = 0; r < kCluster; ++r)
+                st_cluster_v2(map_to_rank(smem_u32(smem) + C::kOffMerge + (uint32_t)(rank * MH + h) * 8, r), make_float2(m, l));
+        }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int y = threadIdx.x + z * kConsumers * 32, h = y / (D / 4), d = y % (D / 4) * 4;
@@ -513,6 +596,29 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         }
         __syncwarp();
         cluster_sync();
+        if (masses) {
+            if ((int)threadIdx.x < nh) {
+                const float2* st = reinterpret_cast<const float2*>(smem + C::kOffMerge) + threadIdx.x;
+                float m = -INFINITY, l = 0.f;
+                for (int r = 0; r < kCluster; ++r) m = fmaxf(m, st[r * MH].x);
+                for (int r = 0; r < kCluster; ++r) l += st[r * MH].y > 0.f ? ex2(st[r * MH].x - m) * st[r * MH].y : 0.f;
+                s_max[threadIdx.x] = m + __log2f(l);             // used where there is a key
+            }
+            named_bar_sync(1, kConsumers * 32);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (at[e] < 0) continue;
+                const float* score = s_score + threadIdx.x + e * kConsumers * 32;
+                float w = 0.f;
+                for (int h = 0; h < nh; ++h) w += ex2(score[h * kScoreRow] - s_max[h]);
+                a.mass_out[at[e]] = before[e] + w;
+            }
+            // the keys that the query does not see, an eighth of them each
+            const int64_t row = ((int64_t)c.b * a.Hkv + c.r) * a.S;
+            const int j1 = (int)((int64_t)a.S * (rank + 1) / kCluster);
+            for (int j = (int)((int64_t)a.S * rank / kCluster) + threadIdx.x; j < j1; j += kConsumers * 32)
+                if (j >= c.s.n || (j < c.s.lo && j >= a.n_sink)) a.mass_out[row + j] = a.mass && j < c.s.n ? a.mass[row + j] : 0.f;
+        }
         if (rank != 0) return;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
@@ -537,6 +643,57 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;          // no tiles: an empty sequence
             const int64_t row = (int64_t)c.b * a.H + h0 + h;
+            *reinterpret_cast<uint2*>(a.O + row * D + d) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        }
+    }
+    if constexpr (MODE == kSolo) {
+        if (!ok) return;
+        const int gq = c.r / a.HB, hb = c.r % a.HB, nh = min(a.G - hb * MH, MH);
+        PrefixParts pieces(a, c.b, gq);
+        wait_for_previous_kernel();          // the prefix's parts
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int y = threadIdx.x + z * kConsumers * 32, h = y / (D / 4), d = y % (D / 4) * 4;
+            if (h >= nh) continue;
+            float m = mine_ml[z].x, l = mine_ml[z].y;
+            float4 acc = mine[z];
+            pieces.head(a, hb * MH + h);
+            for (int e0 = 0; e0 < pieces.n; e0 += 4) {
+                float2 st[4];
+                float4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[e] = make_float2(-INFINITY, 0.f);
+                    v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (e0 + e < pieces.n) {
+                        const int64_t at = pieces.at(a, e0 + e);
+                        st[e] = a.p_stat[at];
+                        v[e] = *reinterpret_cast<const float4*>(a.p_part + at * D + d);
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, st[e].x);
+                if (top == -INFINITY) continue;
+                const float f = ex2(m - top);
+                m = top;
+                l *= f;
+                acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!(st[e].y > 0.f)) continue;              // nothing else was written
+                    const float w = ex2(st[e].x - top);
+                    l = fmaf(w, st[e].y, l);
+                    acc.x = fmaf(w, v[e].x, acc.x);
+                    acc.y = fmaf(w, v[e].y, acc.y);
+                    acc.z = fmaf(w, v[e].z, acc.z);
+                    acc.w = fmaf(w, v[e].w, acc.w);
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;          // no keys at all
+            const int64_t row = (int64_t)c.b * a.H + gq * a.G + hb * MH + h;
             *reinterpret_cast<uint2*>(a.O + row * D + d) =
                 make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
             if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
@@ -603,17 +760,6 @@ join_kernel(const Args a, int grid) {
     if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// The CTAs that hold units [x, x + n) of a list of `total` dealt to n_ctas in equal
-// ranges: the last ones whose ranges begin at or before them.
-__device__ __forceinline__ void ctas_of(int64_t x, int64_t n, int64_t total, int n_ctas, int& c0, int& c1) {
-    if (total < (1 << 23)) {             // 32 bits: n_ctas is below 2^9
-        c0 = (int)((((uint32_t)x + 1) * (uint32_t)n_ctas - 1) / (uint32_t)total);
-        c1 = (int)((((uint32_t)x + (uint32_t)n) * (uint32_t)n_ctas - 1) / (uint32_t)total);
-    } else {
-        c0 = (int)(((x + 1) * n_ctas - 1) / total);
-        c1 = (int)(((x + n) * n_ctas - 1) / total);
-    }
-}
 // Those of the tiles of a segment of sequence b; none: c1 < c0.
 __device__ __forceinline__ void own_ctas(const Args& a, int b, int r, int W, int grid, int& c0, int& c1) {
     const int total = a.prefix[a.B], before = a.prefix[b], units = (a.prefix[b + 1] - before) / (a.Hkv * a.HB);
@@ -625,23 +771,15 @@ __device__ __forceinline__ void own_ctas(const Args& a, int b, int r, int W, int
 // one, then of the own keys, in the order of the keys, 32 at a time: a lane reads a
 // part's maximum and sum, the warp adds the outputs up with the lanes' factors.
 template <int D, Mode MODE>
-__device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row, const PrefixPlan& p, const float* part, const float2* stat) {
+__device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row) {
     constexpr int V = D / 32, kRow = row_floats<D, MODE>(), kAhead = 8;
     const int lane = threadIdx.x % 32, b = (int)(row / a.H), h = (int)row - b * a.H, g = h / a.G, gi = h - g * a.G;
     int c0, c1;
     own_ctas(a, b, g * a.HB + gi / MH, kUnits<false, MODE>, grid, c0, c1);
     if (MODE == kMass && c0 == c1) return;       // finished by the CTA itself
-    int n_prefix = 0, s = 0, tile = 0, pc0 = 0;
-    bool alone = false;
-    if (MODE == kParts && p.grid > 0) {
-        const int at = b * a.G + gi;
-        tile = at / 128;
-        s = g * p.n_pairs + tile / 2;
-        alone = (tile & ~1) * 128 + 128 >= p.rows;       // the pair has this tile only: two parts a piece
-        int pc1;
-        ctas_of((int64_t)s * p.n_kt, p.n_kt, p.steps, p.grid, pc0, pc1);
-        n_prefix = (pc1 - pc0 + 1) << alone;
-    }
+    PrefixParts pieces(a, b, g);
+    if (MODE == kParts) pieces.head(a, gi);
+    const int n_prefix = pieces.n;
     const int n = n_prefix + c1 - c0 + 1;
     float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
@@ -651,10 +789,9 @@ __device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row, c
         const float* src = nullptr;
         float2 st = make_float2(-INFINITY, 0.f);
         if (i < n_prefix) {
-            const int64_t slab = alone ? 2 * (int64_t)(s + pc0) + i : 2 * (int64_t)(s + pc0 + i) + (tile & 1);
-            const int64_t z = slab * p.row_stride + (b * a.G + gi) % 128;
-            st = stat[z];
-            src = part + z * D;
+            const int64_t z = pieces.at(a, i);
+            st = a.p_stat[z];
+            src = a.p_part + z * D;
         } else if (i < n) {
             const int c = c0 + i - n_prefix;
             src = c0 == c1 ? a.own + row * kRow : a.part + ((int64_t)(2 * c + (c == c0)) * MH + gi % MH) * kRow;
@@ -710,10 +847,10 @@ __device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row, c
 constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
 template <int D>
 __global__ void __launch_bounds__(kFinishThreads)
-prefix_join_kernel(const Args a, int grid, const PrefixPlan p, const float* part, const float2* stat) {
+prefix_join_kernel(const Args a, int grid) {
     wait_for_previous_kernel();
     const int64_t row = (int64_t)blockIdx.x * kFinishWarps + threadIdx.x / 32;
-    if (row < (int64_t)a.B * a.H) join_row<D, kParts>(a, grid, row, p, part, stat);
+    if (row < (int64_t)a.B * a.H) join_row<D, kParts>(a, grid, row);
 }
 
 // The masses of a step, and the outputs of the segments that several CTAs share.
@@ -730,7 +867,7 @@ mass_kernel(const Args a, int grid, int joins, int blocks) {
     wait_for_previous_kernel();
     if ((int)blockIdx.x < joins) {
         const int64_t row = (int64_t)blockIdx.x * kFinishWarps + threadIdx.x / 32;
-        if (row < (int64_t)a.B * a.H) join_row<D, kMass>(a, grid, row, PrefixPlan{}, nullptr, nullptr);
+        if (row < (int64_t)a.B * a.H) join_row<D, kMass>(a, grid, row);
         return;
     }
     constexpr int kRow = row_floats<D, kMass>();
@@ -844,7 +981,8 @@ constexpr int most_smem() {
     return most;
 }
 
-// The prefix's part, the own keys' part beside it, and the join.
+// The prefix's part, the own keys' part beside it, and the join; or a CTA per segment of own keys that joins as well.
+constexpr int kSoloTiles = 4;
 template <int D>
 dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const void* kp, const void* vp, int64_t ss, int64_t sh,
                          const void* k, const void* v, const int32_t* kv_len, void* O, float* lse, void* ws, cudaStream_t s) {
@@ -858,28 +996,39 @@ dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const voi
     at += own_bytes(p);
     float2* stat = reinterpret_cast<float2*>(at);
     float* part = reinterpret_cast<float*>(at + stat_bytes(plan));
+    a.p = plan;
+    a.p_stat = stat;
+    a.p_part = part;
     auto own = decode_kernel<D, false, kParts>;
+    auto solo = decode_kernel<D, false, kSolo>;
     static std::atomic<uint64_t> seen{0};
     if (first_on_device(seen)) {
-        if (cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem<D>()) != cudaSuccess)
+        if (cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem<D>()) != cudaSuccess ||
+            cudaFuncSetAttribute(solo, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem<D>()) != cudaSuccess)
             return fail(DFA_ERR_CUDA, "decode: kernel attributes");
         mark_on_device(seen);
     }
-    const int n = (int)std::min<int64_t>(num_sms(), (int64_t)p.B * a.Hkv * a.HB * decode_tiles(p));
     if (plan.grid > 0 && (st = tc_prefix(p, plan, q, kp, vp, ss, sh, part, stat, s))) return st;
-    const size_t smem = Cfg<D>::kOffPrefix + sizeof(int) * (p.B + 1);
+    // Beside the prefix's kernel, on SMs that it leaves or does not need: it starts when that one has, which is after all
+    // work before the call.  Without a prefix it is launched as any other.
+    auto launch_own = [&](auto kernel, int grid, size_t smem) {
+        if (plan.grid > 0) return launch_overlapped(kernel, dim3((unsigned)grid), kThreads, smem, s, mk, mv, a);
+        kernel<<<grid, kThreads, smem, s>>>(mk, mv, a);
+        return cudaGetLastError();
+    };
+    const int64_t segments = (int64_t)p.B * a.Hkv * a.HB, tiles = decode_tiles(p);
     cudaError_t e;
-    if (plan.grid > 0) {
-        // Beside the prefix's kernel, on SMs that it leaves or does not need: it starts when that one has, which is
-        // after all work before the call.
-        e = launch_overlapped(own, dim3((unsigned)n), kThreads, smem, s, mk, mv, a);
-    } else {
-        own<<<n, kThreads, smem, s>>>(mk, mv, a);
-        e = cudaGetLastError();
+    if (tiles <= kSoloTiles && segments <= num_sms()) {
+        e = launch_own(solo, (int)segments, Cfg<D>::kOffPrefix + 16);
+        if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+        count_launch(DFA_KERNEL_FWD);
+        return DFA_OK;
     }
+    const int n = (int)std::min<int64_t>(num_sms(), segments * tiles);
+    e = launch_own(own, n, Cfg<D>::kOffPrefix + sizeof(int) * (p.B + 1));
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
     e = launch_overlapped(prefix_join_kernel<D>, dim3((unsigned)(((int64_t)p.B * p.H + kFinishWarps - 1) / kFinishWarps)), kFinishThreads,
-                          0, s, a, n, plan, static_cast<const float*>(part), static_cast<const float2*>(stat));
+                          0, s, a, n);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "prefix join launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_FWD);
     count_launch(DFA_KERNEL_MERGE);
@@ -916,7 +1065,10 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)kCluster);
     cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.dynamicSmemBytes = C::kOffPrefix + 16;
+    a.fused = MASS && a.HB == 1;             // the heads of a group in one segment
+    constexpr int cluster_smem = C::kOffPrefix + (MASS ? kScoreBytes : 16);
+    static_assert(cluster_smem <= 232448, "shared memory");
+    cfg.dynamicSmemBytes = cluster_smem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -924,7 +1076,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
         constexpr int most = most_smem<D>();
         int k = 0;
         if (cudaFuncSetAttribute(spread, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-            cudaFuncSetAttribute(clustered, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+            cudaFuncSetAttribute(clustered, cudaFuncAttributeMaxDynamicSharedMemorySize, std::max(most, cluster_smem)) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&k, clustered, &cfg) != cudaSuccess)
             return fail(DFA_ERR_CUDA, "decode: kernel attributes");
         clusters.store(k);
@@ -937,7 +1089,7 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mk, mv, a);
         if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
         count_launch(DFA_KERNEL_FWD);
-        return MASS ? launch_mass<D>(a, 0, s) : DFA_OK;
+        return MASS && !a.fused ? launch_mass<D>(a, 0, s) : DFA_OK;
     }
     spread<<<n, kThreads, smem, s>>>(mk, mv, a);
     cudaError_t e = cudaGetLastError();
