@@ -190,6 +190,14 @@ __device__ __forceinline__ void ctas_of(int64_t x, int64_t n, int64_t total, int
         c1 = (int)(((x + n) * n_ctas - 1) / total);
     }
 }
+// Brings a segment's queries (at most 16 rows) to the L1.
+template <int D>
+__device__ __forceinline__ void prefetch_rows(const Args& a, const Cursor& c, int lane) {
+    const int hb = c.r % a.HB, h0 = c.r / a.HB * a.G + hb * MH, nh = min(a.G - hb * MH, MH);
+    const char* rows = reinterpret_cast<const char*>(a.q + ((int64_t)c.b * a.H + h0) * D);
+    if (lane < nh * D * 2 / 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + lane * 128));
+}
+
 // Where the prefix's parts of the heads of a group are, in the order of the keys.
 struct PrefixParts {
     int b, c0, count;             // sequence; first CTA, number of pieces
@@ -330,7 +338,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 __syncwarp();
             }
             x += v1 - c.v;
-            if (x < end) next_segment(a, c);
+            if (x < end) {
+                next_segment(a, c);
+                // its queries are on their way while the consumers are still at the ring's tiles
+                if (MODE != kPlain) prefetch_rows<D>(a, c, lane);
+            }
         }
         if (!ok && lane == 0) {
             // Aborted: let the copies already issued land before the CTA exits.
