@@ -368,3 +368,275 @@ def test_evict_from_a_cache_beyond_32_bits():
                 assert torch.equal(m[b, g, at].sort().values, m[b, g, want].sort().values) and (at[1:] > at[:-1]).all()
             assert torch.equal(ko[b, :r, g], k[b, at, g]) and torch.equal(vo[b, :r, g], v[b, at, g])
             assert torch.equal(mo[b, g, :r], m[b, g, at])
+
+
+# ------------------------------------------------------------------------------------------------ together
+def test_a_prompt_evicted_continued_and_evicted_again():
+    """A prompt's forward, its masses, a smaller cache, tokens through one captured step that adds to the masses, the
+    cache cut down again: each step against the reference on what the cache holds then."""
+    B, H, Hkv, D, S, keep, cap = 2, 8, 2, 128, 900, 300, 340
+    q, k, v = rand(91, B, S + 60, H, D), rand(92, B, S + 60, Hkv, D), rand(93, B, S + 60, Hkv, D)
+    O, lse = dfa.dfa_attn_fwd(q[:, :S].contiguous(), k[:, :S].contiguous(), v[:, :S].contiguous())
+    m = dfa.dfa_attn_mass(q[:, :S].contiguous(), k[:, :S].contiguous(), lse)
+    close(m, cache.mass(np64(q[:, :S]), np64(k[:, :S]), np64(lse), S, 0, S), 2 * F * np64(m), "mass")
+    kc, vc = (torch.full((B, cap, Hkv, D), NAN, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    _, _, n, mc, kept = dfa.dfa_cache_evict(k[:, :S], v[:, :S], lens_of([S, S]), m, keep, 4, 50, kc, vc)
+    held = [[[int(j) for j in kept[b, g]] for g in range(Hkv)] for b in range(B)]
+    qt = torch.empty(B, H, D, dtype=torch.bfloat16, device=DEV)
+
+    def capture(kc, vc, n, mc):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = dfa.dfa_attn_decode_mass(qt, kc, vc, n, mc, mass_out=mc)
+        return graph, out
+
+    def follow(i, graph, out, kc, vc, n, mc):
+        at = n.clone()
+        for b in range(B):
+            kc[b, at[b]], vc[b, at[b]] = k[b, i], v[b, i]
+            for g in range(Hkv):
+                held[b][g].append(i)
+        qt.copy_(q[:, i])
+        n.add_(1)
+        before = np64(mc)
+        graph.replay()
+        for b in range(B):
+            for h in range(H):
+                g = h * Hkv // H
+                j = torch.tensor(held[b][g], device=DEV)
+                Or, lr, size = sink.decode(np64(qt[b:b + 1, h:h + 1]), np64(k[b:b + 1, j][:, :, g:g + 1]), np64(v[b:b + 1, j][:, :, g:g + 1]),
+                                           [len(j)], len(j), 0)
+                close(out[0][b:b + 1, h:h + 1], Or, (U + F) * size + U * np.abs(Or), "O")
+                close(out[1][b:b + 1, h:h + 1], lr, 2 * F, "lse")
+        np.testing.assert_allclose(np64(mc).sum((1, 2)) - before.sum((1, 2)), H, rtol=1e-2)
+        return int(n[0])
+
+    graph, out = capture(kc, vc, n, mc)
+    for i in range(S, S + 40):
+        last = follow(i, graph, out, kc, vc, n, mc)
+    assert last == cap
+    k2, v2 = (torch.full((B, cap, Hkv, D), NAN, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    masses = mc.clone()
+    _, _, n2, m2, kept2 = dfa.dfa_cache_evict(kc, vc, n, mc, 100, 4, 20, k2, v2)
+    for b in range(B):
+        for g in range(Hkv):
+            assert kept2[b, g].tolist() == cache.kept(masses[b, g].cpu().numpy(), cap, 100, 4, 20).tolist()
+            held[b][g] = [held[b][g][j] for j in kept2[b, g].tolist()]
+    graph2, out2 = capture(k2, v2, n2, m2)
+    for i in range(S + 40, S + 50):
+        follow(i, graph2, out2, k2, v2, n2, m2)
+    dfa.dfa_check_errors()
+
+
+def everything(stream=None, seed=101):
+    """One call of each kind: small ones that run in clusters or one CTA, large ones that are cut."""
+    got = []
+    for B, H, Hkv, S, D, window, N, last in ((1, 4, 2, 700, 64, 700, 0, 700), (2, 8, 4, 2600, 128, 900, 3, 2600), (1, 4, 2, 3000, 128, 3000, 0, 40)):
+        q, k, lse = rand(seed, B, S, H, D), rand(seed + 1, B, S, Hkv, D), rand(seed + 2, B, H, S, dtype=torch.float32) + 8
+        got.append(dfa.dfa_attn_mass(q, k, lse, window, N, last, stream=stream))
+    for B, H, Hkv, S, D, lens in ((1, 8, 4, 900, 128, [801]), (9, 16, 8, 2500, 64, [i * 300 for i in range(9)])):
+        q, k, v, m = rand(seed + 3, B, H, D), rand(seed + 4, B, S, Hkv, D), rand(seed + 5, B, S, Hkv, D), rand(seed + 6, B, Hkv, S, dtype=torch.float32).abs()
+        got += dfa.dfa_attn_decode_mass(q, k, v, lens_of(lens), m, stream=stream)
+        for keep in (64, 700):
+            got += dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, 2, 30, stream=stream)
+        for P in (0, 90, 2000):
+            kp, vp = rand(seed + 7, P, Hkv, D), rand(seed + 8, P, Hkv, D)
+            got += dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens), stream=stream)
+            got += dfa.dfa_attn_decode_prefix(q, kp, vp, k[:, :100].contiguous(), v[:, :100].contiguous(), lens_of(lens), stream=stream)
+    return got
+
+
+def same(a, b):
+    return len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_the_same_bits_on_every_call_and_from_a_graph(monkeypatch):
+    want = everything()
+    assert same(everything(), want)
+    # the inputs are made outside the graph: what makes them is not captured
+    made = {}
+    for name in ("rand", "lens_of"):
+        def once(*a, make=globals()[name], **kw):
+            key = str((make, a, kw))
+            if key not in made:
+                made[key] = make(*a, **kw)
+            return made[key]
+        monkeypatch.setitem(globals(), name, once)
+    everything()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = everything()
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, want)
+    dfa.dfa_check_errors()
+
+
+def test_calls_on_other_streams_and_from_threads():
+    import threading
+    want = [everything(seed=s) for s in (111, 131)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in want]
+    for _ in range(3):
+        got = []
+        for st, seed in zip(streams, (111, 131)):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(everything(seed=seed))
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want))
+    failed = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    assert same(everything(seed=(111, 131)[i % 2]), want[i % 2])
+        except BaseException as e:       # shown by the test, not lost with the thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    dfa.dfa_check_errors()
+    assert not failed, failed
+
+
+def test_a_call_on_another_stream_holds_its_tensors():
+    """Inputs dropped while the other stream has still to read them, outputs from memory that the current stream is about
+    to write."""
+    B, H, Hkv, S, D = 2, 8, 2, 1200, 128
+    s = torch.cuda.Stream()
+
+    def made():
+        return (rand(141, B, H, D), rand(142, 300, Hkv, D), rand(143, 300, Hkv, D), rand(144, B, S, Hkv, D), rand(145, B, S, Hkv, D),
+                lens_of([1200, 700]), rand(146, B, Hkv, S, dtype=torch.float32).abs(), rand(147, B, S, H, D), rand(148, B, H, S, dtype=torch.float32) + 8)
+
+    def calls(q, kp, vp, k, v, n, m, qs, lse, stream=None):
+        return [dfa.dfa_attn_mass(qs, k, lse, stream=stream)] + list(dfa.dfa_attn_decode_mass(q, k, v, n, m, stream=stream)) + \
+            list(dfa.dfa_cache_evict(k, v, n, m, 800, 3, 40, stream=stream)) + list(dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, n, stream=stream))
+
+    want = calls(*made())
+    for _ in range(3):
+        data = made()
+        torch.cuda.synchronize()
+        blocks = [torch.empty_like(t) for t in want]
+        torch.cuda._sleep(20000000)
+        for t in blocks:
+            t.fill_(7)
+        del blocks
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20000000)
+        got = calls(*data, stream=s)
+        sizes = [torch.empty_like(t, device="meta") for t in data]
+        del data
+        fill = [torch.full_like(t, 1, device=DEV) for t in sizes]
+        torch.cuda.synchronize()
+        assert same(got, want)
+        del fill
+    dfa.dfa_check_errors()
+
+
+FIRST = """
+import torch
+from long_context_causal_gb300 import dfa
+g = torch.Generator("cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+for D in (64, 128):
+    q, k, v, qs, kp, vp = r(2, 8, D), r(2, 600, 2, D), r(2, 600, 2, D), r(2, 600, 8, D), r(200, 2, D), r(200, 2, D)
+    n, m, lse = torch.full((2,), 555, dtype=torch.int32, device="cuda"), torch.rand(2, 2, 600, device="cuda"), torch.full((2, 8, 600), 9.0, device="cuda")
+    chain = lambda: (dfa.dfa_attn_mass(qs, k, lse), dfa.dfa_attn_mass(qs, k, lse, n_last=30)) + dfa.dfa_attn_decode_mass(q, k, v, n, m) + \\
+        dfa.dfa_cache_evict(k, v, n, m, 100) + dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, n)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, chain()))
+dfa.dfa_check_errors()
+"""
+
+
+def test_first_calls_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_mass_beyond_32_bits():
+    """2^31 elements in q: keys of the last head and the end of the sequence."""
+    B, H, Hkv, S, D, W, N = 1, 32, 8, 524288 + 77, 128, 300, 4
+    q, k = (torch.empty(B, S, h, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(151 + h)) for h in (H, Hkv))
+    lse = torch.rand(B, H, S, device=DEV, generator=gen(152)) + 6
+    for n_last in (S, 50):
+        m = dfa.dfa_attn_mass(q, k, lse, W, N, n_last)
+        dfa.dfa_check_errors()
+        for j in (S - 1, S - 60, S - 349, S - 700, 2):
+            i = torch.arange(max(j, S - n_last), S if j < N else max(min(j + W, S), max(j, S - n_last)), device=DEV)
+            s = torch.einsum("ihd,hd->hi", q[0, i].double(), k[0, j].double().repeat_interleave(H // Hkv, 0)) * D ** -0.5
+            w = torch.exp(s - lse[0][:, i].double()).sum(1).reshape(Hkv, -1).sum(1)
+            # sums of up to 2^12 tiles of 128: as many additions in fp32
+            close(m[0, :, j], np64(w), (F + 2.0 ** -12) * np64(w), "mass")
+
+
+def test_empty_batches_and_no_tokens():
+    H, Hkv, D = 4, 2, 64
+    t = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
+    for B, S in ((0, 50), (3, 0)):
+        assert dfa.dfa_attn_mass(t(B, S, H, D), t(B, S, Hkv, D), t(B, H, S, dtype=torch.float32)).shape == (B, Hkv, S)
+    q, k, n, m = t(0, H, D), t(0, 9, Hkv, D), t(0, dtype=torch.int32), t(0, Hkv, 9, dtype=torch.float32)
+    assert [x.shape for x in dfa.dfa_attn_decode_mass(q, k, k, n, m)] == [(0, H, D), (0, H), (0, Hkv, 9)]
+    assert [x.shape[0] for x in dfa.dfa_cache_evict(k, k, n, m, 4)] == [0] * 5
+    assert [x.shape for x in dfa.dfa_attn_decode_prefix(q, t(5, Hkv, D), t(5, Hkv, D), k, k, n)] == [(0, H, D), (0, H)]
+    with pytest.raises(dfa.DfaError, match="room"):
+        dfa.dfa_attn_decode_mass(t(2, H, D), t(2, 0, Hkv, D), t(2, 0, Hkv, D), t(2, dtype=torch.int32))
+    dfa.dfa_check_errors()
+
+
+def test_what_the_binding_refuses_on_the_gpu():
+    B, H, Hkv, S, D = 2, 4, 2, 40, 64
+    q, k, n, m = rand(1, B, H, D), rand(2, B, S, Hkv, D), lens_of([9, 9]), torch.zeros(B, Hkv, S, device=DEV)
+    with pytest.raises(dfa.DfaError, match="overlaps"):
+        dfa.dfa_cache_evict(k, k.clone(), n, m, 10, k_out=k[:, :20], v_out=k[:, 20:])
+    with pytest.raises(dfa.DfaError, match="overlaps"):
+        dfa.dfa_cache_evict(k, k, n, m, 10, len_out=n)
+    with pytest.raises(dfa.DfaError, match="same memory"):
+        x = k.clone()
+        dfa.dfa_cache_evict(k, k, n, m, 10, k_out=x, v_out=x)
+    with pytest.raises(ValueError, match="together"):
+        dfa.dfa_cache_evict(k, k, n, m, 10, k_out=k.clone())
+    with pytest.raises(ValueError, match="caches of k"):
+        dfa.dfa_cache_evict(k, k, n, m, 10, k_out=k.float(), v_out=k.float())
+    with pytest.raises(dfa.DfaError, match="cap"):
+        dfa.dfa_cache_evict(k, k, n, m, 10, k_out=rand(3, B, 9, Hkv, D), v_out=rand(4, B, 9, Hkv, D))
+    for bad in ((0, 0, 0), (10, 6, 5), (10, -1, 0)):
+        with pytest.raises((dfa.DfaError, ValueError)):
+            dfa.dfa_cache_evict(k, k, n, m, *bad)
+    with pytest.raises(ValueError, match="32-bit"):
+        dfa.dfa_cache_evict(k, k, n, m, 1 << 31)
+    with pytest.raises(ValueError, match="mass must be"):
+        dfa.dfa_attn_decode_mass(q, k, k, n, m[:, :, :-1].contiguous())
+    with pytest.raises(ValueError, match="kv_len must be"):
+        dfa.dfa_attn_decode_mass(q, k, k, n.long(), m)
+    with pytest.raises(dfa.DfaError):
+        dfa.dfa_attn_decode_mass(q.float(), k.float(), k.float(), n, m)
+    with pytest.raises(dfa.DfaError, match="broadcast"):
+        dfa.dfa_attn_decode_prefix(q, rand(5, 1, Hkv, D).expand(7, Hkv, D), rand(6, 1, Hkv, D).expand(7, Hkv, D), k, k, n)
+    with pytest.raises(ValueError, match="workspace"):
+        dfa.dfa_attn_decode_prefix(q, k[0], k[0], k, k, n, workspace_buf=torch.zeros(9, device=DEV))
+    with pytest.raises(dfa.DfaError, match="workspace"):
+        dfa.dfa_attn_mass(rand(7, B, S, H, D), k, torch.zeros(B, H, S, device=DEV), workspace_buf=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(dfa.DfaError, match="n_last"):
+        dfa.dfa_attn_mass(rand(7, B, S, H, D), k, torch.zeros(B, H, S, device=DEV), n_last=0)
+    assert dfa.dfa_attn_mass(rand(7, B, S, H, D), k, torch.zeros(B, H, S, device=DEV), n_last=1 << 30).shape == (B, Hkv, S)
+    dfa.dfa_check_errors()
