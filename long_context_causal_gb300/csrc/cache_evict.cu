@@ -160,6 +160,7 @@ select_kernel(const Args a, const CopyArgs copy) {
     __shared__ uint32_t folded[2][C > 1 ? kBins : 1], s_scan[kWarps], s_count[2], s_found[3];
     const int rank = blockIdx.x % C, row = blockIdx.x / C, b = row / a.Hkv;
     const int tid = threadIdx.x, lane = tid % 32;
+    wait_for_previous_kernel();
     const int n = min(max(a.kv_len[b], 0), a.S);
     const float* mass = a.mass + (int64_t)row * a.S;
     float* mass_out = a.mass_out + (int64_t)row * a.cap;
@@ -372,15 +373,17 @@ dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, cons
     const Kernel kernels[] = {small ? (move ? Kernel(select_kernel<0, 4, true>) : Kernel(select_kernel<0, 4, false>)) : Kernel(select_kernel<0, 16, false>),
                               select_kernel<1, 16, false>, select_kernel<2, 16, false>, select_kernel<3, 16, false>};
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1u << log_c;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1u << log_c;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)rows << log_c);
     cfg.blockDim = dim3((unsigned)kThreads);
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = log_c > 0;
+    cfg.numAttrs = 1 + (log_c > 0);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[log_c], a, c);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_EVICT);

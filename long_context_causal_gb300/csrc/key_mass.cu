@@ -235,6 +235,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous_kernel();
     const uint32_t tmem = *tmem_slot;
     Cursor c;
     int n, rank = 0;
@@ -578,6 +579,7 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous_kernel();
     const uint32_t tmem = *tmem_slot;
     const int64_t steps = (int64_t)a.rows * a.n_tiles, begin = steps * blockIdx.x / gridDim.x, end = steps * (blockIdx.x + 1) / gridDim.x;
     const int n = (int)(end - begin);        // at least one: the grid is no larger than the list
@@ -780,8 +782,7 @@ dfa_status launch_tail(const SinkProblem& p, const TailArgs& a, const CUtensorMa
             return fail(DFA_ERR_CUDA, "key_mass: kernel attributes");
         mark_on_device(seen);
     }
-    kernel<<<(int)std::min<int64_t>(num_sms(), (int64_t)a.rows * a.n_tiles), kThreads, smem, s>>>(mq, mk, a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(kernel, dim3((unsigned)std::min<int64_t>(num_sms(), (int64_t)a.rows * a.n_tiles)), kThreads, smem, s, mq, mk, a);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_MASS);
     return DFA_OK;
@@ -837,10 +838,12 @@ dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k
     static std::atomic<int> clusters{0};             // that run at a time
     auto kernel = key_mass_kernel<D, false>;
     auto clustered = key_mass_kernel<D, true>;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)kCluster);
     cfg.blockDim = dim3((unsigned)kThreads);
@@ -865,14 +868,14 @@ dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k
         for (int kb = 0; kb < a.n_kb; ++kb) longest = std::max(longest, (tiles_before(a, kb + 1) - tiles_before(a, kb)) * a.G);
     if (segments <= clusters.load() && (longest + kCluster - 1) / kCluster <= (a.steps + num_sms() - 1) / num_sms() + kJoinSteps) {
         cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * a.n_kb * kCluster));
+        cfg.numAttrs = 2;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mq, mk, a);
         if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
         count_launch(DFA_KERNEL_MASS);
         return DFA_OK;
     }
     const int grid = (int)std::min<int64_t>(num_sms(), a.steps);
-    kernel<<<grid, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_overlapped(kernel, dim3((unsigned)grid), kThreads, Cfg<D>::kSmem, s, mq, mk, a);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass launch: %s", cudaGetErrorString(e));
     e = launch_overlapped(join_kernel, dim3((unsigned)(p.B * p.Hkv * a.n_kb)), kBlock, 0, s, a, grid);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "key_mass join launch: %s", cudaGetErrorString(e));

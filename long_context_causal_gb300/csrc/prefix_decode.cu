@@ -104,7 +104,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     uint64_t* kv_empty = bars + 16 + C::kSlots;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    launch_dependents();                  // the sequences' own keys need nothing of this
     if (threadIdx.x == 0) {
         for (int w = 0; w < 2; ++w) {
             mbar_init(&q_full[w], 4);
@@ -130,6 +129,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous_kernel();
+    launch_dependents();                  // the sequences' own keys need nothing of this
     const uint32_t tmem = *tmem_slot;
     const int64_t steps = a.p.steps, begin = steps * blockIdx.x / gridDim.x, end = steps * (blockIdx.x + 1) / gridDim.x;
 
@@ -379,8 +380,7 @@ dfa_status launch(const DecodeProblem& p, const PrefixPlan& plan, const void* q,
             return fail(DFA_ERR_CUDA, "prefix: kernel attributes");
         mark_on_device(seen);
     }
-    kernel<<<plan.grid, kThreads, Cfg<D>::kSmem, s>>>(mk, mv, a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(kernel, dim3((unsigned)plan.grid), kThreads, Cfg<D>::kSmem, s, mk, mv, a);
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "prefix launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_FWD);
     return DFA_OK;

@@ -256,6 +256,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         tma_prefetch_desc(&tmV);
         prefix[0] = 0;
     }
+    if (MODE == kMass) wait_for_previous_kernel();
     Cursor c;
     int begin, end;
     const int R = a.Hkv * a.HB, rank = blockIdx.x % kCluster;
@@ -1070,10 +1071,12 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     static std::atomic<int> clusters{0};             // that run at a time
     auto spread = decode_kernel<D, false, MODE>;
     auto clustered = decode_kernel<D, true, MODE>;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)kCluster);
     cfg.blockDim = dim3((unsigned)kThreads);
@@ -1098,13 +1101,19 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
     // heads 8.2 us, spread over all SMs 8.9; 8192 keys 12.1 and 10.8; 262 keys 4.2 and 6.0.
     if (segments <= clusters.load() && decode_tiles(p) <= kClusterTiles) {
         cfg.gridDim = dim3((unsigned)(segments * kCluster));
+        if (MASS) cfg.numAttrs = 2;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, mk, mv, a);
         if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
         count_launch(DFA_KERNEL_FWD);
         return MASS && !a.fused ? launch_mass<D>(a, 0, s) : DFA_OK;
     }
-    spread<<<n, kThreads, smem, s>>>(mk, mv, a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (MASS) {
+        e = launch_overlapped(spread, dim3((unsigned)n), kThreads, (size_t)smem, s, mk, mv, a);
+    } else {
+        spread<<<n, kThreads, smem, s>>>(mk, mv, a);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return fail(DFA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
     count_launch(DFA_KERNEL_FWD);
     if (MASS) return launch_mass<D>(a, n, s);
