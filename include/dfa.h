@@ -333,7 +333,7 @@ dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dty
  *             overlap an input
  *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as below
  * Everything else as dfa_attn_decode_sink (whose O and lse may differ in the
- * last bits: the keys are cut elsewhere).  Two launches; the same bits on every call. */
+ * last bits: the keys are cut elsewhere).  One or two launches; the same bits on every call. */
 size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink);
 dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H, int H_kv,
                                 int S_max, int D, const int64_t* kv_strides, const int32_t* kv_len, const float* mass,
@@ -360,7 +360,7 @@ dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa
  * keep >= 1, n_first, n_recent >= 0, n_first + n_recent <= keep.  No output may
  * overlap an input.  The heads of a sequence keep different positions, so a window
  * counted in rows (the calls above) means the last rows that were kept.  D in {64, 128}.
- * Two launches, no workspace; may be captured. */
+ * One or two launches, no workspace; may be captured. */
 dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt, int B, int H_kv, int S_max, int D,
                            const int64_t* kv_strides, const int32_t* kv_len, const float* mass, int keep, int n_first,
                            int n_recent, int cap, const int64_t* out_strides, void* k_out, void* v_out,

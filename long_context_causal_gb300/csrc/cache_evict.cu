@@ -14,6 +14,12 @@
 // their histograms and counts through distributed shared memory.
 //
 // copy_kernel moves the rows: bound by HBM (each kept row read and written once).
+//
+// What it takes: 8 x 8 rows of up to 16384 keys to 4096, D = 128, 50.6 us a call (265 MB,
+// 5.2 TB/s, 77% of the copy rate): 36 the copy, 9 the choice on 64 of the SMs -- latency of
+// the dependent passes, 32 warps each with barriers between; one prompt of 131072 keys to
+// 16384 40 us (140 MB): 19 and 18, of which three digits' exchanges through distributed
+// shared memory are half.  The masses are read once while a row fits the threads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

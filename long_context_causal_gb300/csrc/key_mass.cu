@@ -13,6 +13,20 @@
 // scores, one warpgroup for each: while a warpgroup forms its weights the tensor
 // cores run the other three products.
 //
+// What bounds it: the warpgroups' arithmetic.  128 x 128 scores are 512 cycles of the
+// exponential unit and 512 of the tensor cores.  The arithmetic around the exponentials
+// alone lets a sub-partition do a tile's 32 rows in 632 cycles with four warps; in the
+// kernel a step of four tiles takes 3030 (tensor cores 66% busy, exponentials 66%, issue
+// slots 52%), set by the sub-partition that also has the issuing warp.  32K tokens, 32/8
+// heads, D = 128, window 4096, 4 sinks: 827 to 851 us (1210 to 1250 TFLOP/s); 2 x 5003
+// tokens causal, 16/2 heads, 80 to 83 us (1240).  With three quarters of the products left
+// out 720 us, without the loads of the queries' log-sum-exps 792, with half of the
+// exponentials 779: no unit alone.  Measured and not kept: two warpgroups that hold a
+// tile's 128 scores each 974 (too few warps to hide the latencies); scores loaded ahead
+// across a loop's end 1960 to 2080; the warpgroups' waits by polling 876, the issuing
+// warp's by suspending 878; a region handed back at half of the arithmetic instead of
+// three quarters 853; log-sum-exps loaded 8 bytes at a time instead of 16 no change.
+//
 // Roles (640 threads, one CTA per SM): warp 0 TMA producer of K and Q, warp 1 MMA
 // issuer, warp 2 TMEM owner, warp 3 the queries' -lse log2 e (-inf for rows past
 // the end: weight 0), warps 4-19 four warpgroups.
@@ -22,7 +36,10 @@
 // steps lie before a block is a sum of three linear pieces, so a CTA finds its
 // first step without a table.  A block that one CTA sweeps whole is written there;
 // of the others each CTA leaves 512 sums, which a second kernel adds up in the
-// order of the steps.  No atomics: the same bits on every call.
+// order of the steps.  No atomics: the same bits on every call.  With few blocks (rule at
+// launch()) a cluster shares a block's steps instead: 2 x 301 tokens 8.2 us, 10.2
+// with the second launch (6.0 since a call's first kernel is set up while the one before
+// it ends).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -495,8 +512,13 @@ join_kernel(const Args a, int grid) {
 // in P groups of 128, and the tiles of 128 keys stream through a ring: every key is
 // read once and its mass is finished there, in one launch.  A tile's P products go to
 // P of the four TMEM regions, so 4 / P tiles are in work at a time; a warpgroup adds
-// up a region, and the P sums of a key meet in shared memory, in their order.  Bound by
-// HBM up to 256 rows (64 queries of 4 heads), above that by the exponentials.
+// up a region, and the P sums of a key meet in shared memory, in their order.
+//
+// The last 64 queries of 32K tokens, 32/8 heads, D = 128: 19.4 us a call (68.7 MB at 3.5
+// TB/s, half of the copy rate; 42 by blocks of 512 keys as above).  A tile of keys takes
+// 1770 cycles where HBM would bring one in 1400: as above, the arithmetic of the weights
+// (1024 cycles of exponentials).  The 14 tiles of a CTA are 12.5 us of it, the rest passes
+// before the first tile's scores are there (64 KB of queries, then the keys) and at the end.
 constexpr int kMostCols = 512;
 
 template <int D, int P>

@@ -32,6 +32,27 @@
 // permuted alike in Q and K, and V's rows are paired with byte permutes, so no
 // transposing load is needed.  Each warp keeps its own running maximum and
 // sum in fp32; the probabilities are rounded to bf16 for the second product.
+//
+// With masses (kMass).  A key's weight needs its heads' log-sum-exps, which are known
+// at the end only: the consumers write the scores down, 4 bytes a head beside the 512
+// of a key and value (D = 128; 3% more at 4 heads a group), and the launch that joins
+// the outputs turns them into weights.  K and V are loaded to make room first, so the
+// scores are still in the L2 then: 32 sequences of up to 16384 keys, 32/8 heads, 178 us
+// a call (1.10 GB at 6140 GB/s, 91% of the copy rate), of which 165 are the cache and
+// 11 the masses; 195 before the cache policy and with 1024 keys a block, 219 with a
+// launch of its own for the masses and short sequences counted by their tiles alone.
+// In a cluster (one sequence of 1501 keys) the scores stay in shared memory and the CTA
+// that has them forms the weights: 6.3 us of GPU time, 9.3 by two launches.
+//
+// Behind a shared prefix (kParts, kSolo).  The same kernel over the sequences' own keys,
+// started beside prefix_decode.cu's and leaving fp32 parts, which prefix_join_kernel adds
+// to the prefix's: 128 sequences of up to 1024 own keys, 64/8 heads, behind 16384: 117 us
+// a call (prefix 48, own keys 52 at 5.1 TB/s, join 10).  A segment costs a CTA 2 us beside
+// its tiles (queries, the eight warps' states made one), so short sequences count for more
+// than their keys when the tiles are dealt: with tiles alone the CTA of the shortest ones
+// ran 123 us, the others 46.  Where the own keys are few (at most four tiles, a segment per
+// SM at most) a CTA takes a segment and adds the prefix's parts itself: 4 sequences behind
+// 1000 keys 9.1 us of GPU time, 10.7 with the launch that joins.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -859,7 +880,7 @@ __device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row) {
 // Joins the parts of a shared prefix and of the sequences' own keys, a warp per row.
 constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
+__global__ void __launch_bounds__(kFinishThreads, 4)
 prefix_join_kernel(const Args a, int grid) {
     wait_for_previous_kernel();
     const int64_t row = (int64_t)blockIdx.x * kFinishWarps + threadIdx.x / 32;
