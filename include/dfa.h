@@ -297,7 +297,7 @@ dfa_status dfa_attn_decode_sink(const void* q, const void* k, const void* v, dfa
  *   workspace: >= dfa_attn_decode_prefix_workspace_size() bytes, 16-byte aligned,
  *              contents not preserved; calls that can overlap need one each
  * Cache rows behind kv_len may hold anything.  bf16 only, D in {64, 128}, at most 8192
- * sequences.  Two or three launches; may be captured; the same bits on every call. */
+ * sequences.  One to three launches; may be captured; the same bits on every call. */
 size_t dfa_attn_decode_prefix_workspace_size(int B, int H, int H_kv, int P, int D);
 dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
                                   dfa_dtype dt, int B, int H, int H_kv, int P, int S_max, int D,
@@ -358,7 +358,7 @@ dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa
  *   mass_out: fp32 [B, H_kv, cap], the kept keys' masses, 0 behind them
  *   kept:     int32 [B, H_kv, keep], their positions in k and v, rising; -1 behind
  * keep >= 1, n_first, n_recent >= 0, n_first + n_recent <= keep.  No output may
- * overlap an input.  The heads of a sequence keep different positions, so a window
+ * overlap an input (from its first element to the end of its last one).  The heads of a sequence keep different positions, so a window
  * counted in rows (the calls above) means the last rows that were kept.  D in {64, 128}.
  * One or two launches, no workspace; may be captured. */
 dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt, int B, int H_kv, int S_max, int D,

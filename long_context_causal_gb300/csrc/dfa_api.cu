@@ -999,13 +999,14 @@ extern "C" dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void
 
 namespace {
 
+int64_t decode_segments(const DecodeProblem& p) { return (int64_t)p.B * p.Hkv * ((p.H / p.Hkv + 15) / 16); }
+
 dfa_status check_decode(dfa_dtype dt, const DecodeProblem& p) {
     dfa_status st = check_sink(dt, p.B, p.H, p.Hkv, p.S, p.D, p.window, p.n_sink, p.scale);
     if (st) return st;
     if (p.S < 1) return fail(DFA_ERR_INVALID_ARG, "the cache must have room for a token");
     if (p.B > kMaxDecodeBatch) return fail(DFA_ERR_UNSUPPORTED, "%d sequences: at most %d at once", p.B, kMaxDecodeBatch);
-    const int64_t blocks = (p.H / p.Hkv + 15) / 16;
-    if (p.B * p.Hkv * blocks * decode_tiles(p) > (1 << 30)) return fail(DFA_ERR_INVALID_ARG, "problem too large");
+    if (decode_segments(p) * decode_tiles(p) > (1 << 30)) return fail(DFA_ERR_INVALID_ARG, "problem too large");
     return DFA_OK;
 }
 
@@ -1015,17 +1016,26 @@ DecodeProblem decode_problem(int B, int H, int Hkv, int S, int D, int window, in
 
 }  // namespace
 
-static bool decode_sizes_ok(const DecodeProblem& p) {
+// Of the calls whose segments count for more than their tiles when the tiles are dealt (32-bit sums).
+static dfa_status check_units(dfa_dtype dt, const DecodeProblem& p) {
+    dfa_status st = check_decode(dt, p);
+    if (st) return st;
+    if (decode_segments(p) * (decode_tiles(p) + kDecodeUnits) > (1 << 30) || (int64_t)p.B * p.H > (1 << 28))
+        return fail(DFA_ERR_INVALID_ARG, "problem too large");
+    return DFA_OK;
+}
+
+static bool decode_sizes_ok(const DecodeProblem& p, dfa_status (*check)(dfa_dtype, const DecodeProblem&)) {
     char keep[sizeof(g_msg)];
     memcpy(keep, g_msg, sizeof(g_msg));
-    const bool ok = check_decode(DFA_BF16, p) == DFA_OK;
+    const bool ok = check(DFA_BF16, p) == DFA_OK;
     memcpy(g_msg, keep, sizeof(g_msg));
     return ok;
 }
 
 extern "C" size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D) {
     const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
-    return decode_sizes_ok(p) ? decode_workspace(p, false) : 0;
+    return decode_sizes_ok(p, check_decode) ? decode_workspace(p, false) : 0;
 }
 
 // Strides of a caller's cache, if given, in place of the dense ones.
@@ -1059,7 +1069,7 @@ extern "C" dfa_status dfa_attn_decode_sink(const void* q, const void* k, const v
 }
 
 static dfa_status check_prefix(dfa_dtype dt, const DecodeProblem& p, int P) {
-    dfa_status st = check_decode(dt, p);
+    dfa_status st = check_units(dt, p);
     if (st) return st;
     if (P < 0) return fail(DFA_ERR_INVALID_ARG, "negative prefix length");
     if (P > (1 << 30)) return fail(DFA_ERR_INVALID_ARG, "problem too large (prefix of %d tokens)", P);
@@ -1068,7 +1078,7 @@ static dfa_status check_prefix(dfa_dtype dt, const DecodeProblem& p, int P) {
 
 extern "C" size_t dfa_attn_decode_prefix_workspace_size(int B, int H, int H_kv, int P, int D) {
     const DecodeProblem p = decode_problem(B, H, H_kv, 1, D, 1, 0, 1.f);
-    return decode_sizes_ok(p) && P >= 0 && P <= (1 << 30) ? prefix_workspace(p, P) : 0;
+    return decode_sizes_ok(p, check_units) && P >= 0 && P <= (1 << 30) ? prefix_workspace(p, P) : 0;
 }
 
 extern "C" dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
@@ -1123,7 +1133,7 @@ DecodeProblem mass_problem(int B, int H, int Hkv, int S, int D, int window, int 
     return p;
 }
 dfa_status check_mass(dfa_dtype dt, const DecodeProblem& p) {
-    dfa_status st = check_decode(dt, p);
+    dfa_status st = check_units(dt, p);
     if (st) return st;
     if ((int64_t)p.B * p.Hkv * p.S > ((int64_t)1 << 37)) return fail(DFA_ERR_INVALID_ARG, "problem too large");
     return DFA_OK;
@@ -1154,7 +1164,7 @@ extern "C" dfa_status dfa_attn_mass(const void* q, const void* k, const float* l
 
 extern "C" size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink) {
     const DecodeProblem p = mass_problem(B, H, H_kv, S_max, D, window, n_sink, 1.f);
-    return decode_sizes_ok(p) ? decode_workspace(p, true) : 0;
+    return decode_sizes_ok(p, check_units) ? decode_workspace(p, true) : 0;
 }
 
 extern "C" dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa_dtype dt, int B, int H,

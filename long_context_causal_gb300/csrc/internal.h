@@ -162,6 +162,7 @@ struct DecodeProblem {
     float scale;
 };
 constexpr int kMaxDecodeBatch = 8192;   // the kernel sums the lengths up in shared memory
+constexpr int kDecodeUnits = 2;         // what a segment counts for beside its tiles (with masses, behind a prefix)
 int64_t decode_tiles(const DecodeProblem& p);      // at most, per (sequence, block of query heads)
 size_t decode_workspace(const DecodeProblem& p, bool mass);
 // mass_out (may be null, or mass itself): mass plus the step's weights, [B, Hkv, S].

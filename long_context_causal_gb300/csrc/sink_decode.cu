@@ -59,6 +59,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -118,7 +119,7 @@ enum Mode { kPlain, kMass, kParts, kSolo };
 // Units that a segment counts for beside its tiles when the tiles are dealt: it costs a CTA 2 us beside
 // 0.7 to 0.9 us per tile.  (The plain step deals tiles alone.)
 template <bool CLUSTER, Mode MODE>
-constexpr int kUnits = CLUSTER || MODE == kPlain || MODE == kSolo ? 0 : 2;
+constexpr int kUnits = CLUSTER || MODE == kPlain || MODE == kSolo ? 0 : kDecodeUnits;
 // Floats of a head's partial: unnormalised O, max, sum.
 template <int D, Mode MODE>
 constexpr int row_floats() { return MODE == kPlain ? D + 2 : D + 4; }
@@ -419,7 +420,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         float o[D / 8][4];
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads g, g + 8; l: this lane's columns
+        // heads g, g + 8; l: this lane's columns.  The maxima begin at the lowest number, so that a score that is
+        // -inf in 32 bits counts for nothing wherever it stands.
+        float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
         for (int k = k0; k < k1; ++k, ++i) {
             if ((i & 1) != grp) continue;
             const int slot = i % C::kStages;
@@ -472,7 +475,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
                 if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-                    const float y0 = fmaxf(m0, x0), y1 = fmaxf(m1, x1);   // finite: key 0 of the 16 is visible
+                    const float y0 = fmaxf(m0, x0), y1 = fmaxf(m1, x1);
                     const float a0 = ex2(m0 - y0), a1 = ex2(m1 - y1);     // 0 at first
                     m0 = y0; m1 = y1;
                     l0 *= a0; l1 *= a1;
@@ -555,7 +558,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
-                const float f = ex2(s_max[w * MH + h] - m);      // a warp without keys: max -inf, factor 0
+                const float f = ex2(s_max[w * MH + h] - m);      // a warp without keys: sum and outputs 0
                 const float4 v = *reinterpret_cast<const float4*>(s_merge + (w * MH + h) * D + d);
                 l = fmaf(f, s_sum[w * MH + h], l);
                 acc.x = fmaf(f, v.x, acc.x);
@@ -635,7 +638,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 const float2* st = reinterpret_cast<const float2*>(smem + C::kOffMerge) + threadIdx.x;
                 float m = -INFINITY, l = 0.f;
                 for (int r = 0; r < kCluster; ++r) m = fmaxf(m, st[r * MH].x);
-                for (int r = 0; r < kCluster; ++r) l += st[r * MH].y > 0.f ? ex2(st[r * MH].x - m) * st[r * MH].y : 0.f;
+                for (int r = 0; r < kCluster; ++r) l += st[r * MH].y == 0.f ? 0.f : ex2(st[r * MH].x - m) * st[r * MH].y;   // a NaN stays
                 s_max[threadIdx.x] = m + __log2f(l);             // used where there is a key
             }
             named_bar_sync(1, kConsumers * 32);
@@ -710,15 +713,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 float top = m;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, st[e].x);
-                if (top == -INFINITY) continue;
-                const float f = ex2(m - top);
+                const float base = top == -INFINITY ? 0.f : top;
+                const float f = ex2(m - base);
                 m = top;
                 l *= f;
                 acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (!(st[e].y > 0.f)) continue;              // nothing else was written
-                    const float w = ex2(st[e].x - top);
+                    if (st[e].y == 0.f) continue;                // nothing else was written
+                    const float w = ex2(st[e].x - base);
                     l = fmaf(w, st[e].y, l);
                     acc.x = fmaf(w, v[e].x, acc.x);
                     acc.y = fmaf(w, v[e].y, acc.y);

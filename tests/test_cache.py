@@ -210,6 +210,31 @@ def test_step_masses_of_a_cache_beyond_32_bits():
             close(got[2][b][:, idx], np64(w), 2 * F * np64(w), "mass")
 
 
+def test_step_masses_of_nans_and_scores_below_32_bits():
+    """Visible keys whose score is -inf in 32 bits draw nothing, whole tiles of them too; a NaN score reaches all
+    that its head's softmax touches and nothing else.  One launch, a cluster and a second one, all SMs."""
+    for case in ((1, 4, 2, 700, 64, 700, 0, [700]), (1, 40, 2, 700, 128, 300, 9, [650]), (3, 8, 2, 6000, 128, 6000, 0, [6000, 64, 5000])):
+        B, H, Hkv, S, D, window, n_sink, lens = case
+        q, k, v, n, m = poisoned(case, 15)
+        q[:, :, 0], k[:, :, :, 0] = 2.0 ** 100, 0
+        for b in range(B):
+            for lo, hi in ((0, 16), (lens[b] - 200, lens[b] - 70), (lens[b] - 3, lens[b] - 1)):
+                k[b, max(lo, 0):max(hi, 0), :, 0] = -2.0 ** 100
+        got = dfa.dfa_attn_decode_mass(q, k, v, n, m, window, n_sink)
+        dfa.dfa_check_errors()
+        check_step(got, case, q, k, v, m)
+        j, G = lens[0] - 5, H // Hkv
+        k[0, j, 1, 3] = NAN
+        O, lse, out = dfa.dfa_attn_decode_mass(q, k, v, n, m, window, n_sink)
+        dfa.dfa_check_errors()
+        seen = torch.arange(S, device=DEV)
+        seen = (seen < lens[0]) & ((seen >= lens[0] - window) | (seen < n_sink))
+        assert O[0, G:].isnan().all() and lse[0, G:].isnan().all() and out[0, 1, seen].isnan().all()
+        for a, b in ((O[0, :G], got[0][0, :G]), (lse[0, :G], got[1][0, :G]), (out[0, 0], got[2][0, 0]), (out[0, 1, ~seen], got[2][0, 1, ~seen]),
+                     (O[1:], got[0][1:]), (out[1:], got[2][1:])):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------------ a shared prefix
 # (B, H, Hkv, P, S, D, lens): one query tile of a head, two, three, many; few keys and many pieces; own rows from none on
 PREFIX = [
@@ -267,6 +292,31 @@ def test_prefix_is_the_step_over_a_cache_that_holds_it():
     # both sides round P and the result; sum_j P |v_j| stays below 1.5
     assert (O.float() - want[0].float()).abs().max() <= 2 * (U + F) * 1.5 + 2 * U
     assert (lse - want[1]).abs().max() <= 4 * F
+
+
+def test_prefix_of_nans_and_scores_below_32_bits():
+    """As of the step: in the prefix and among the own keys; a CTA per segment, and parts that are joined."""
+    for B, H, Hkv, P, S, D, lens in ((3, 8, 2, 500, 20, 64, [20, 0, 7]), (5, 12, 4, 700, 400, 128, [400, 0, 64, 7, 399])):
+        q, kp, vp, k, v = rand(91, B, H, D), rand(92, P, Hkv, D), rand(93, P, Hkv, D), rand(94, B, S, Hkv, D), rand(95, B, S, Hkv, D)
+        q[:, :, 0], kp[:, :, 0], k[:, :, :, 0] = 2.0 ** 100, 0, 0
+        kp[:200, :, 0], k[:, :17, :, 0], k[:, 70:210, :, 0] = -2.0 ** 100, -2.0 ** 100, -2.0 ** 100
+        n, G = lens_of(lens), H // Hkv
+        got = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, n)
+        dfa.dfa_check_errors()
+        check_prefix(got, q, kp, vp, k, v, lens)
+        bad = kp.clone()
+        bad[P - 100, 1, 5] = NAN
+        O, lse = dfa.dfa_attn_decode_prefix(q, bad, vp, k, v, n)
+        assert O[:, G:2 * G].isnan().all() and lse[:, G:2 * G].isnan().all()
+        others = torch.tensor([h for h in range(H) if h // G != 1], device=DEV)
+        assert torch.equal(O[:, others], got[0][:, others]) and torch.equal(lse[:, others], got[1][:, others])
+        bad = q.clone()
+        bad[1, 0, 5] = NAN                     # of the sequence without own keys
+        O, lse = dfa.dfa_attn_decode_prefix(bad, kp, vp, k, v, n)
+        dfa.dfa_check_errors()
+        assert O[1, 0].isnan().all() and lse[1, 0].isnan()
+        O[1, 0], lse[1, 0] = got[0][1, 0], got[1][1, 0]
+        assert torch.equal(O, got[0]) and torch.equal(lse, got[1])
 
 
 def test_prefix_beyond_32_bits():

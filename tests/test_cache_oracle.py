@@ -126,6 +126,14 @@ def test_decode_mass_sizes():
     assert size(2, 4, 2, 1 << 20, 128, 64, 4) <= base + 4 * 2 * 4 * 64 * 4 + 4096
 
 
+def test_sizes_whose_tiles_32_bits_do_not_count():
+    """A segment counts for two units more than its tiles: 2^30 of one tile are 3 * 2^30 units."""
+    big = dict(B=8192, H=1 << 17, Hkv=1 << 17, S=64)
+    assert dfa.dfa_attn_decode_mass_workspace_size(8192, 1 << 17, 1 << 17, 64, 128, 64, 0) == 0
+    assert dfa.dfa_attn_decode_prefix_workspace_size(8192, 1 << 17, 1 << 17, 64, 128) == 0
+    assert decode_mass(**big) == dfa.DFA_ERR_INVALID_ARG and prefix(**big) == dfa.DFA_ERR_INVALID_ARG
+
+
 def prefix(**kw):
     a = dict(q=FAR[0], kp=FAR[1], vp=FAR[2], k=FAR[3], v=FAR[4], dt=1, B=2, H=4, Hkv=2, P=500, S=300, D=128, ps=None, ks=None, n=FAR[5],
              scale=0.1, O=FAR[6], lse=FAR[7], ws=FAR[8], wn=1 << 40)
