@@ -68,7 +68,7 @@ def _binding_command(cuda: str) -> list[str]:
     return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] +
             ["-isystem" + i for i in include] + [BINDING, "-L" + os.path.join(root, "lib")] +
-            ["-l" + x for x in ("torch_python", "torch", "torch_cpu", "c10", "c10_cuda")])
+            ["-l" + x for x in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda")])
 
 
 def _binding_key() -> str:

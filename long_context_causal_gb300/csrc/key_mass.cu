@@ -38,7 +38,7 @@
 // of the others each CTA leaves 512 sums, which a second kernel adds up in the
 // order of the steps.  No atomics: the same bits on every call.  With few blocks (rule at
 // launch()) a cluster shares a block's steps instead: 2 x 301 tokens 8.2 us, 10.2
-// with the second launch (6.0 since a call's first kernel is set up while the one before
+// with the second launch (5.4 since a call's first kernel is set up while the one before
 // it ends).
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -593,6 +593,31 @@ def test_a_call_on_another_stream_holds_its_tensors():
     dfa.dfa_check_errors()
 
 
+def test_workspaces_go_back_and_outputs_are_ordinary_tensors():
+    """Calls leave no memory behind, refused ones and those on another stream neither; in inference mode the outputs are
+    what torch makes there."""
+    want, s = everything(), torch.cuda.Stream()
+    q, k = rand(1, 2, 4, 64), rand(2, 2, 40, 2, 64)
+    n, m = lens_of([9, 9]), torch.zeros(2, 2, 40, device=DEV)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(3):
+        got = everything()
+        assert same(got, want)
+        del got
+        with pytest.raises(dfa.DfaError):
+            dfa.dfa_attn_decode_mass(q, k, k, n, m, window=0)
+        del _
+        dfa.dfa_attn_decode_prefix(q, k[0], k[0], k, k, n, stream=s)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == before
+    with torch.inference_mode():
+        got = everything()
+        assert all(t.is_inference() for t in got) and same(got, want)
+    assert not any(t.is_inference() or t.requires_grad for t in want)
+    dfa.dfa_check_errors()
+
+
 FIRST = """
 import torch
 from long_context_causal_gb300 import dfa
