@@ -342,20 +342,24 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             const int r4 = r & ~3, left = min(a.p.row_stride, a.p.rows - (c.row0 + tile * BM)) - r4;
             float4* dst = reinterpret_cast<float4*>(a.part + (slab * a.p.row_stride + r4) * D) + (lane & 3);
 #pragma unroll 1
-            for (int e = 0; e < D / 16; ++e) {
-                uint32_t u[16];
-                tmem_ld16_async(tO + e * 16, u);
-                tmem_wait_ld16(u);
-                uint32_t o[4][4];                         // [word][16 bytes of the row's 64]
+            for (int e0 = 0; e0 < D / 16; e0 += 4) {
+                uint32_t u[4][16];
 #pragma unroll
-                for (int f = 0; f < 16; ++f) o[f % 4][f / 4] = u[f];
+                for (int e = 0; e < 4; ++e) tmem_ld16_async(tO + (e0 + e) * 16, u[e]);
 #pragma unroll
-                for (int f = 0; f < 4; ++f) quad_transpose(o[f], lane);
+                for (int e = 0; e < 4; ++e) {
+                    tmem_wait_ld16(u[e]);
+                    uint32_t o[4][4];                     // [word][16 bytes of the row's 64]
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    if (f < left)
-                        dst[f * (D / 4) + e * 4] = make_float4(__uint_as_float(o[0][f]), __uint_as_float(o[1][f]),
-                                                               __uint_as_float(o[2][f]), __uint_as_float(o[3][f]));
+                    for (int f = 0; f < 16; ++f) o[f % 4][f / 4] = u[e][f];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) quad_transpose(o[f], lane);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        if (f < left)
+                            dst[f * (D / 4) + (e0 + e) * 4] = make_float4(__uint_as_float(o[0][f]), __uint_as_float(o[1][f]),
+                                                                          __uint_as_float(o[2][f]), __uint_as_float(o[3][f]));
+                }
             }
             tc_fence_before();
         }

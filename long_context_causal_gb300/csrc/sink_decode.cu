@@ -52,7 +52,8 @@
 // than their keys when the tiles are dealt: with tiles alone the CTA of the shortest ones
 // ran 123 us, the others 46.  Where the own keys are few (at most four tiles, a segment per
 // SM at most) a CTA takes a segment and adds the prefix's parts itself: 4 sequences behind
-// 1000 keys 9.1 us of GPU time, 10.7 with the launch that joins.
+// 1000 keys 7.5 us of GPU time; 10.7 with the launch that joins, 9.0 with a part's place
+// worked out once the prefix is there and four parts asked for at a time.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -688,38 +689,52 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     if constexpr (MODE == kSolo) {
         if (!ok) return;
         const int gq = c.r / a.HB, hb = c.r % a.HB, nh = min(a.G - hb * MH, MH);
+        // Where the parts are is known before they are there.
         PrefixParts pieces(a, c.b, gq);
+        int parts[2];
+        int64_t first[2], step[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int h = (threadIdx.x + z * kConsumers * 32) / (D / 4);
+            parts[z] = 0;
+            if (h >= nh) continue;
+            pieces.head(a, hb * MH + h);
+            parts[z] = pieces.n;
+            first[z] = pieces.at(a, 0);
+            step[z] = pieces.at(a, 1) - first[z];
+        }
         wait_for_previous_kernel();          // the prefix's parts
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int y = threadIdx.x + z * kConsumers * 32, h = y / (D / 4), d = y % (D / 4) * 4;
             if (h >= nh) continue;
+            constexpr int kAhead = 8;
             float m = mine_ml[z].x, l = mine_ml[z].y;
             float4 acc = mine[z];
-            pieces.head(a, hb * MH + h);
-            for (int e0 = 0; e0 < pieces.n; e0 += 4) {
-                float2 st[4];
-                float4 v[4];
+#pragma unroll 1
+            for (int e0 = 0; e0 < parts[z]; e0 += kAhead) {
+                float2 st[kAhead];
+                float4 v[kAhead];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < kAhead; ++e) {
                     st[e] = make_float2(-INFINITY, 0.f);
                     v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (e0 + e < pieces.n) {
-                        const int64_t at = pieces.at(a, e0 + e);
+                    if (e0 + e < parts[z]) {
+                        const int64_t at = first[z] + (e0 + e) * step[z];
                         st[e] = a.p_stat[at];
                         v[e] = *reinterpret_cast<const float4*>(a.p_part + at * D + d);
                     }
                 }
                 float top = m;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, st[e].x);
+                for (int e = 0; e < kAhead; ++e) top = fmaxf(top, st[e].x);
                 const float base = top == -INFINITY ? 0.f : top;
                 const float f = ex2(m - base);
                 m = top;
                 l *= f;
                 acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < kAhead; ++e) {
                     if (st[e].y == 0.f) continue;                // nothing else was written
                     const float w = ex2(st[e].x - base);
                     l = fmaf(w, st[e].y, l);
