@@ -3,22 +3,23 @@
 // Of the n = kv_len[b] keys of a sequence and key/value head, `keep` stay: the
 // first n_first, the last n_recent, and of the others those with the greatest
 // mass, ties to the lowest position.  They move, in their order, to the front of
-// another cache.  Two launches.
+// another cache.  Two launches, or one where the rows are short (kMoveUnits).
 //
 // select_kernel finds the border: masses become unsigned integers of the same
-// order, and a radix select of three digits (11, 11 and 10 bits) narrows down the
-// integer T of the last one that stays, and how many of those equal to T do; it ends
-// early where a whole bin stays.  Positions follow from counts: a thread owns up to
+// order, and a radix select (digits of 11, 11 and 10 bits, or four of 8) narrows down
+// the integer T of the last one that stays, and how many of those equal to T do; it
+// ends early where a whole bin stays.  Positions follow from counts: a thread owns up to
 // 16 consecutive keys, which it holds in registers, counts what it keeps of them,
-// and after one scan over all threads of the row writes their positions in order.  A row is shared by a cluster of up to eight CTAs that add
-// their histograms and counts through distributed shared memory.
+// and after one scan over all threads of the row writes their positions in order.  A
+// long row is shared by a cluster of up to eight CTAs that add their histograms and
+// counts through distributed shared memory.
 //
 // copy_kernel moves the rows: bound by HBM (each kept row read and written once).
 //
-// What it takes: 8 x 8 rows of up to 16384 keys to 4096, D = 128, 50.6 us a call (265 MB,
-// 5.2 TB/s, 77% of the copy rate): 36 the copy, 9 the choice on 64 of the SMs -- latency of
+// What it takes: 8 x 8 rows of up to 16384 keys to 4096, D = 128, 50.3 us a call (265 MB,
+// 5.3 TB/s, 78% of the copy rate): 36 the copy, 9 the choice on 64 of the SMs -- latency of
 // the dependent passes, 32 warps each with barriers between; one prompt of 131072 keys to
-// 16384 40 us (140 MB): 19 and 18, of which three digits' exchanges through distributed
+// 16384 37.4 us (140 MB): 19 and 15, of which three digits' exchanges through distributed
 // shared memory are half.  The masses are read once while a row fits the threads.
 #include <cuda_runtime.h>
 
@@ -156,14 +157,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 select_kernel(const Args a, const CopyArgs copy) {
     constexpr int C = 1 << LOG_C;
     static_assert(!MOVE || C == 1, "one CTA per row");
-    // Digits of 11 bits; where CTAs share a row, of 8, for all of them read all histograms.  Copies of a
-    // histogram, so that equal digits of a warp's keys wait less for one another.
-    constexpr int kBits = C == 1 ? 11 : 8, kBins = 1 << kBits, kCopies = C == 1 ? 2 : 8;
+    // Digits of 11 bits; where CTAs share a row, of 8, for all of them read all histograms (131072 keys: 9 bits the same,
+    // 10 bits 1.3 us more; one CTA with 12 bits 0.6 us more).  One histogram per CTA: equal digits of a warp are added up
+    // by the shared memory, copies of it only share its banks (8 of them: 2 us more).  A pass counts in one while it
+    // clears the next one's; the one before may still be read by other CTAs.
+    constexpr int kBits = C == 1 ? 11 : 8, kBins = 1 << kBits, kBufs = C == 1 ? 2 : 3;
     __shared__ union {
-        uint32_t hist[kCopies][kBins];
+        uint32_t hist[kBufs][kBins];
         uint16_t list[kThreads * PER];       // what stays of a chunk
     } sm;
-    __shared__ uint32_t folded[2][C > 1 ? kBins : 1], s_scan[kWarps], s_count[2], s_found[3];
+    __shared__ uint32_t s_scan[kWarps], s_count[2], s_found[3];
     const int rank = blockIdx.x % C, row = blockIdx.x / C, b = row / a.Hkv;
     const int tid = threadIdx.x, lane = tid % 32;
     wait_for_previous_kernel();
@@ -197,12 +200,12 @@ select_kernel(const Args a, const CopyArgs copy) {
     int at = from;
     if (E > 0) {
         T = 0;
+        for (int i = tid; i < kBins; i += kThreads) sm.hist[0][i] = 0;
+        __syncthreads();
 #pragma unroll 1
         for (int pass = 0, top = 32; top > 0; ++pass) {
             const int low = max(top - kBits, 0);
-            for (int i = tid; i < kCopies * kBins; i += kThreads) sm.hist[0][i] = 0;
-            __syncthreads();
-            uint32_t* mine = sm.hist[lane % kCopies];
+            uint32_t* mine = sm.hist[pass % kBufs];
 #pragma unroll 1
             for (int ch = 0; ch < chunks; ++ch) {
                 if (chunks > 1) load(u, mass, at = ch * chunk + from, n, lo, hi);
@@ -217,37 +220,30 @@ select_kernel(const Args a, const CopyArgs copy) {
                         if (u[s] >> top == high) atomicAdd(&mine[u[s] >> low & digit], 1u);
                 }
             }
-            __syncthreads();
+            for (int i = tid; i < kBins; i += kThreads) sm.hist[(pass + 1) % kBufs][i] = 0;
+            __syncwarp();
+            if (C > 1) cluster_sync();
+            else __syncthreads();
             // the bin that holds the E-th one from above, and how many of it stay
-            constexpr int kEach = C == 1 ? kBins / kThreads : 1;      // bins of a thread, in falling order
+            constexpr int kEach = kBins > kThreads ? kBins / kThreads : 1;      // bins of a thread, in falling order
             uint32_t c[kEach], sum = 0;
             const int bin = kBins - 1 - kEach * tid;
-            if (C == 1) {
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    c[e] = 0;
-#pragma unroll
-                    for (int f = 0; f < kCopies; ++f) c[e] += sm.hist[f][bin - e];
-                    sum += c[e];
-                }
-            } else {
-                if (bin >= 0) {
-#pragma unroll
-                    for (int f = 0; f < kCopies; ++f) sum += sm.hist[f][bin];
-                    folded[pass & 1][bin] = sum;
-                }
-                __syncwarp();
-                cluster_sync();
-                sum = 0;
-                if (bin >= 0) {
+            for (int e = 0; e < kEach; ++e) {
+                c[e] = 0;
+                if (bin < 0) continue;
+                if constexpr (C == 1) {
+                    c[e] = mine[bin - e];
+                } else {
                     uint32_t part[C];
 #pragma unroll
-                    for (int r = 0; r < C; ++r) part[r] = ld_cluster_u32(&folded[pass & 1][bin], r);
+                    for (int r = 0; r < C; ++r) part[r] = ld_cluster_u32(&mine[bin - e], r);
 #pragma unroll
-                    for (int r = 0; r < C; ++r) sum += part[r];
+                    for (int r = 0; r < C; ++r) c[e] += part[r];
                 }
-                c[0] = sum;
             }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) sum += c[e];
             uint32_t before = block_scan(sum, s_scan) - sum;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
@@ -283,13 +279,17 @@ select_kernel(const Args a, const CopyArgs copy) {
         __syncwarp();
         if (C > 1) cluster_sync();
         else __syncthreads();
-        uint32_t cta_s = base_s, cta_e = base_e, own = 0;      // before this CTA's keys; its counts
+        uint32_t cta_s = base_s, cta_e = base_e, own = s_count[ch & 1];    // before this CTA's keys; its counts
+        if constexpr (C > 1) {
+            const uint32_t theirs = ld_cluster_u32(&s_count[ch & 1], lane % C);      // all at once
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            const uint32_t c = C > 1 ? ld_cluster_u32(&s_count[ch & 1], r) : s_count[ch & 1];
-            if (r < rank) cta_s += c >> 16, cta_e += c & 0xffffu;
-            if (r == rank) own = c;
-            base_s += c >> 16, base_e += c & 0xffffu;
+            for (int r = 0; r < C; ++r) {
+                const uint32_t c = __shfl_sync(0xffffffffu, theirs, r);
+                if (r < rank) cta_s += c >> 16, cta_e += c & 0xffffu;
+                base_s += c >> 16, base_e += c & 0xffffu;
+            }
+        } else {
+            base_s += own >> 16, base_e += own & 0xffffu;
         }
         const int r0 = cta_s + min(cta_e, E), r1 = cta_s + (own >> 16) + min(cta_e + (own & 0xffffu), E);
         uint32_t at_s = cta_s + ((upto - mine) >> 16), at_e = cta_e + ((upto - mine) & 0xffffu);
