@@ -125,12 +125,12 @@ struct CopyArgs {
     int64_t in_sb, in_ss, in_sh, out_sb, out_ss, out_sh;   // units
 };
 
-// Rows from(r) -> r of a (sequence, head)'s keys and values, r < rows, by the CTA.
+// Rows from(r) -> r of a (sequence, head)'s keys and values, r0 <= r < r1, by the CTA.
 template <typename From>
-__device__ __forceinline__ void copy_rows(const CopyArgs& c, int b, int g, int rows, From from) {
+__device__ __forceinline__ void copy_rows(const CopyArgs& c, int b, int g, int r0, int r1, From from) {
     constexpr int kAhead = 4;
-    const int units = rows << c.log_u;
-    for (int y = threadIdx.x; y < units; y += kAhead * kThreads) {
+    const int units = r1 << c.log_u;
+    for (int y = (r0 << c.log_u) + threadIdx.x; y < units; y += kAhead * kThreads) {
         uint4 k[kAhead], v[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
@@ -151,7 +151,7 @@ __device__ __forceinline__ void copy_rows(const CopyArgs& c, int b, int g, int r
     }
 }
 
-// MOVE: the rows are moved as well (one CTA per row, all its keys in one chunk).
+// MOVE: the rows are moved as well, those of each chunk behind its choice (one CTA per row).
 template <int LOG_C, int PER, bool MOVE>
 __global__ void __launch_bounds__(kThreads, 1)
 select_kernel(const Args a, const CopyArgs copy) {
@@ -185,7 +185,7 @@ select_kernel(const Args a, const CopyArgs copy) {
             mass_out[r] = mass[r];
             kept[r] = r;
         }
-        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, n, [](int r) -> int64_t { return r; });
+        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, 0, n, [](int r) -> int64_t { return r; });
         return;
     }
     const int lo = a.n_first, hi = n - a.n_recent;      // the keys that compete
@@ -309,7 +309,7 @@ select_kernel(const Args a, const CopyArgs copy) {
             kept[r] = j;
             mass_out[r] = mass[j];
         }
-        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, r1, [&](int r) -> int64_t { return first + sm.list[r]; });
+        if constexpr (MOVE) copy_rows(copy, b, row - b * a.Hkv, r0, r1, [&](int r) -> int64_t { return first + sm.list[r - r0]; });
         if (chunks > 1) __syncthreads();
     }
     __syncwarp();

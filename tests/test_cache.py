@@ -383,6 +383,25 @@ def test_evict(case, kind):
     check_evict(again, k, v, m, lens, (B, Hkv, S, D, keep, keep, n_first, n_recent, lens))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("S", [4093, 4094, 4095, 4096, 4097])
+def test_evict_rows_that_do_not_begin_on_16_bytes(S, dtype):
+    """The masses of a row are read 16 bytes at a time and a CTA's threads hold 4096 keys at once: rows that begin
+    off 16 bytes, those of odd lengths and of a mass that is a slice, spill into a second turn.  Moved in one launch
+    (few kept) and in two."""
+    Hkv, D = 3, 64
+    lens = [S, S - 1, S - 3]
+    k, v = rand(35, 3, S, Hkv, D, dtype=dtype), rand(36, 3, S, Hkv, D, dtype=dtype)
+    flat = torch.exp(3 * rand(37, 3 * Hkv * S + 3, dtype=torch.float32))
+    for off in range(4):
+        m = flat[off:off + 3 * Hkv * S].view(3, Hkv, S)
+        for keep, n_first, n_recent in ((1, 0, 0), (64, 0, 63), (256, 0, 0), (200, 199, 0), (513, 0, 9)):
+            ko, vo = (torch.full((3, keep + 1, Hkv, D), 7, dtype=dtype, device=DEV) for _ in range(2))
+            got = dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, n_first, n_recent, ko, vo)
+            dfa.dfa_check_errors()
+            check_evict(got, k, v, m, lens, (3, Hkv, S, D, keep, keep + 1, n_first, n_recent, lens), 7)
+
+
 def test_evict_strides_types_and_lengths_out_of_range():
     B, Hkv, S, D, keep, cap = 3, 2, 300, 128, 50, 60
     lens = [0, 250, 300]
