@@ -154,8 +154,10 @@ struct Cursor {
 };
 
 // Weights of 32 queries for this thread's key: 2^(s c + n), n the queries' -lse log2 e;
-// see: the queries that see the key.
-__device__ __forceinline__ void add32(uint64_t (&acc)[4], const uint32_t (&u)[32], float c, const float* n) {
+// see: the queries that see the key.  The others' weights are 0 whatever their scores and n are (a NaN
+// among them): the mask comes behind both.
+template <bool MASKED = false>
+__device__ __forceinline__ void add32(uint64_t (&acc)[4], const uint32_t (&u)[32], float c, const float* n, uint32_t see = 0xffffffffu) {
     const uint64_t cc = pack_f32x2(c, c);
     uint64_t x[16];
 #pragma unroll
@@ -166,7 +168,11 @@ __device__ __forceinline__ void add32(uint64_t (&acc)[4], const uint32_t (&u)[32
     }
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        const float2 y = unpack_f32x2(x[e]);
+        float2 y = unpack_f32x2(x[e]);
+        if (MASKED) {
+            y.x = see >> (2 * e) & 1 ? y.x : -INFINITY;
+            y.y = see >> (2 * e + 1) & 1 ? y.y : -INFINITY;
+        }
         x[e] = pack_f32x2(ex2(y.x), ex2(y.y));
     }
 #pragma unroll
@@ -191,11 +197,6 @@ __device__ __forceinline__ void add128(uint64_t (&acc)[4], uint32_t tS, float c,
     tmem_wait_ld32(y);
     add32(acc, y, c, n + 96);
 }
-__device__ __forceinline__ void mask32(uint32_t (&u)[32], uint32_t see) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? u[e] : 0xff800000u;
-}
-
 // CLUSTER: a block's steps are shared by a cluster of eight CTAs, an eighth each, whose sums
 // meet in the first one's shared memory: one launch.
 constexpr int kCluster = 8, kJoinSteps = 4;
@@ -443,8 +444,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         tmem_ld32(tS + q * 32, x);
                         // query i sees key j iff j <= i and (i < j + window or j < n_sink)
                         const int at = key - (i0 + q * 32);
-                        mask32(x, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
-                        add32(acc, x, a.scale_log2, nl + q * 32);
+                        add32<true>(acc, x, a.scale_log2, nl + q * 32, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -760,8 +760,7 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             uint32_t x[32];
                             tmem_ld32(tS + c * 32, x);
                             const int at = key - (a.q0 + (q * 4 + c) % per * 32);
-                            mask32(x, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
-                            add32(acc, x, a.scale_log2, nl + c * 32);
+                            add32<true>(acc, x, a.scale_log2, nl + c * 32, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
                         }
                     }
                     tc_fence_before();

@@ -104,6 +104,35 @@ def test_mass_what_it_must_not_trip_over():
     close(got, ref, F * ref, "mass")
 
 
+# (B, H, Hkv, S, D, window, n_sink, n_last): by a cluster per block, by all SMs, by the kernels of few queries (their
+# groups of 128 columns: 1, 2, 4)
+@pytest.mark.parametrize("case", [(1, 2, 1, 900, 64, 200, 3, 900), (2, 8, 2, 6000, 128, 1500, 5, 6000), (1, 2, 2, 5000, 64, 5000, 0, 3000),
+                                  (1, 2, 1, 900, 128, 200, 3, 50), (2, 4, 1, 1500, 64, 300, 0, 64), (1, 8, 2, 700, 128, 700, 0, 100)],
+                         ids=lambda c: "B{}H{}kv{}S{}D{}w{}s{}l{}".format(*c))
+def test_mass_of_a_nan_query_reaches_the_keys_it_sees(case):
+    """With the log-sum-exp that the windowed forward gives for it; one lower than 32 bits times log2 e hold likewise."""
+    B, H, Hkv, S, D, window, n_sink, n_last = case
+    q, k = rand(57, B, S, H, D), rand(58, B, S, Hkv, D)
+    _, lse = dfa.dfa_attn_fwd_sink(q, k, k, window, n_sink)
+    want = dfa.dfa_attn_mass(q, k, lse, window, n_sink, n_last)
+    for i in (S - 1, S - n_last // 2, S - n_last):
+        bad = q.clone()
+        bad[0, i, 0, 5] = NAN
+        _, lse_bad = dfa.dfa_attn_fwd_sink(bad, k, k, window, n_sink)
+        assert lse_bad[0, 0, i].isnan() and lse_bad.isnan().sum() == 1
+        low = lse.clone()
+        low[0, 0, i] = -3.4e38
+        seen = torch.zeros(B, Hkv, S, dtype=torch.bool, device=DEV)
+        seen[0, 0] = torch.arange(S, device=DEV) <= i
+        seen[0, 0, n_sink:max(i - window + 1, n_sink)] = False
+        for got, there in ((dfa.dfa_attn_mass(bad, k, lse_bad, window, n_sink, n_last), torch.isnan),
+                           (dfa.dfa_attn_mass(q, k, lse_bad, window, n_sink, n_last), torch.isnan),
+                           (dfa.dfa_attn_mass(q, k, low, window, n_sink, n_last), torch.isposinf)):
+            assert torch.equal(there(got), seen), i
+            assert torch.equal(got[~seen], want[~seen])
+    dfa.dfa_check_errors()
+
+
 def test_mass_of_many_heads_and_blocks():
     """More blocks than SMs, most of them swept whole, and a few that many CTAs share: every query gives away one."""
     from long_context_causal_gb300.inputs import make
