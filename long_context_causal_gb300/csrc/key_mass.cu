@@ -178,6 +178,11 @@ __device__ __forceinline__ void add32(uint64_t (&acc)[4], const uint32_t (&u)[32
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e & 3] = add_f32x2(acc[e & 3], x[e]);
 }
+// Bit e: query i0 + e sees key j, i.e. j <= i and (i < j + window or j < n_sink).  Rows past the end are zeros and
+// see nothing: times a key's infinity they would be NaN.
+__device__ __forceinline__ uint32_t see32(int key, int i0, int S, int window, int n_sink) {
+    return ~low_bits(key - i0) & low_bits(S - i0) & (key < n_sink ? 0xffffffffu : low_bits(key - i0 + window));
+}
 __device__ __forceinline__ float sum4(const uint64_t (&acc)[4]) {
     return sum_f32x2(add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3])));
 }
@@ -442,9 +447,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int q = 0; q < chunks; ++q) {
                         uint32_t x[32];
                         tmem_ld32(tS + q * 32, x);
-                        // query i sees key j iff j <= i and (i < j + window or j < n_sink)
-                        const int at = key - (i0 + q * 32);
-                        add32<true>(acc, x, a.scale_log2, nl + q * 32, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
+                        add32<true>(acc, x, a.scale_log2, nl + q * 32, see32(key, i0 + q * 32, a.S, a.window, a.n_sink));
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -743,24 +746,17 @@ tail_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     tc_fence_after();
                     const float* nl = sN + ((seen_rows - 1) & 1) * P * BT + q * BT;
                     uint64_t acc[4] = {0, 0, 0, 0};
-                    if (k0 + BT - 1 <= a.q0 && a.S - 1 - k0 < a.window) {
-                        if (chunks == 4) {
-                            add128(acc, tS, a.scale_log2, nl);
-                        } else {
-#pragma unroll 1
-                            for (int c = 0; c < chunks; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32(tS + c * 32, x);
-                                add32(acc, x, a.scale_log2, nl + c * 32);
-                            }
-                        }
+                    const bool whole = k0 + BT - 1 <= a.q0 && a.S - 1 - k0 < a.window;      // every query sees all keys
+                    if (whole && chunks == 4 && a.q0 + a.pad == a.S) {
+                        add128(acc, tS, a.scale_log2, nl);
                     } else {
 #pragma unroll 1
                         for (int c = 0; c < chunks; ++c) {
+                            const int i0 = a.q0 + (q * 4 + c) % per * 32;
                             uint32_t x[32];
                             tmem_ld32(tS + c * 32, x);
-                            const int at = key - (a.q0 + (q * 4 + c) % per * 32);
-                            add32<true>(acc, x, a.scale_log2, nl + c * 32, ~low_bits(at) & (key < a.n_sink ? 0xffffffffu : low_bits(at + a.window)));
+                            if (whole && i0 + 32 <= a.S) add32(acc, x, a.scale_log2, nl + c * 32);
+                            else add32<true>(acc, x, a.scale_log2, nl + c * 32, see32(key, i0, a.S, a.window, a.n_sink));
                         }
                     }
                     tc_fence_before();

@@ -133,6 +133,24 @@ def test_mass_of_a_nan_query_reaches_the_keys_it_sees(case):
     dfa.dfa_check_errors()
 
 
+@pytest.mark.parametrize("case", [(1, 2, 1, 900, 64, 200, 3, 900), (2, 8, 2, 6001, 128, 1500, 5, 6001), (1, 2, 1, 900, 128, 200, 3, 50),
+                                  (2, 4, 1, 1507, 64, 300, 0, 61), (1, 8, 2, 700, 128, 700, 0, 100), (1, 16, 1, 1300, 128, 1300, 0, 20)],
+                         ids=lambda c: "B{}H{}kv{}S{}D{}w{}s{}l{}".format(*c))
+def test_mass_of_keys_whose_scores_are_below_32_bits(case):
+    """Keys with an infinity and a score of -inf draw nothing.  Tiles of queries that end behind the sequence have rows of
+    zeros there, whose products with such a key are NaN."""
+    B, H, Hkv, S, D, window, n_sink, n_last = case
+    q, k, lse = rand(59, B, S, H, D), rand(60, B, S, Hkv, D), rand(61, B, H, S, dtype=torch.float32) + 8
+    q[..., 3] = q[..., 3].abs() + 1
+    want = dfa.dfa_attn_mass(q, k, lse, window, n_sink, n_last)
+    far = torch.zeros(S, dtype=torch.bool, device=DEV)
+    far[[0, S // 2, S - 300, S - 130, S - 3, S - 1]] = True
+    k[:, far, :, 3] = -float("inf")
+    got = dfa.dfa_attn_mass(q, k, lse, window, n_sink, n_last)
+    dfa.dfa_check_errors()
+    assert (got[..., far] == 0).all() and torch.equal(got[..., ~far], want[..., ~far])
+
+
 def test_mass_of_many_heads_and_blocks():
     """More blocks than SMs, most of them swept whole, and a few that many CTAs share: every query gives away one."""
     from long_context_causal_gb300.inputs import make
