@@ -276,7 +276,8 @@ dfa_status dfa_attn_bwd_sink(const void* q, const void* k, const void* v, const 
  *   workspace: >= dfa_attn_decode_sink_workspace_size() bytes, 16-byte
  *            aligned, contents not preserved; calls that can overlap need one
  *            each
- * Cache rows that the query does not see may hold anything, NaN included.
+ * Cache rows that the query does not see may hold anything, NaN included.  A key
+ * whose score is -inf in 32 bits draws nothing; a head that has no other: O = 0, lse = -inf.
  * bf16 only, D in {64, 128}, n_sink <= 128, at most 8192 sequences
  * (UNSUPPORTED otherwise).  One or two launches; the same bits on every call. */
 size_t dfa_attn_decode_sink_workspace_size(int B, int H, int H_kv, int D);

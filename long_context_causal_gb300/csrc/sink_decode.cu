@@ -161,6 +161,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// What a head's weights relative to 2^m, whose sum is l, make of its output and its log-sum-exp (times log2 e).  l = 0:
+// there is no key, or the scores are -inf in 32 bits one and all; nothing is drawn then, O = 0 and lse = -inf, however
+// the keys were cut.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.f ? -INFINITY : m + __log2f(l); }
+// What a key's score is taken from for its weight: 2^(-inf - 0) is 0, 2^(-inf + inf) is not.
+__device__ __forceinline__ float weight_base(float lse) { return lse == -INFINITY ? 0.f : lse; }
+
 // Floats of a head's scores in shared memory: eight tiles of a cluster's CTA, rows on different banks.
 constexpr int kScoreRow = kClusterTiles / kCluster * KT + 4;
 constexpr int kScoreBytes = MH * kScoreRow * 4;
@@ -572,11 +580,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 mine[second] = acc;
                 mine_ml[second] = make_float2(m, l);
             } else if (MODE != kParts && whole) {
-                const float inv = 1.f / l;
+                const float inv = reciprocal(l);
                 const int64_t row = (int64_t)c.b * a.H + h0 + h;
                 *reinterpret_cast<uint2*>(a.O + row * D + d) =
                     make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                if (d == 0) a.lse[row] = (m + __log2f(l)) * kLn2;
+                if (d == 0) a.lse[row] = log2_sum(m, l) * kLn2;
             } else {
                 *reinterpret_cast<float2*>(part + h * kRow + d) = make_float2(acc.x, acc.y);
                 *reinterpret_cast<float2*>(part + h * kRow + d + 2) = make_float2(acc.z, acc.w);
@@ -640,7 +648,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 float m = -INFINITY, l = 0.f;
                 for (int r = 0; r < kCluster; ++r) m = fmaxf(m, st[r * MH].x);
                 for (int r = 0; r < kCluster; ++r) l += st[r * MH].y == 0.f ? 0.f : ex2(st[r * MH].x - m) * st[r * MH].y;   // a NaN stays
-                s_max[threadIdx.x] = m + __log2f(l);             // used where there is a key
+                s_max[threadIdx.x] = weight_base(log2_sum(m, l));
             }
             named_bar_sync(1, kConsumers * 32);
 #pragma unroll
@@ -679,11 +687,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;          // no tiles: an empty sequence
+            const float inv = reciprocal(l);
             const int64_t row = (int64_t)c.b * a.H + h0 + h;
             *reinterpret_cast<uint2*>(a.O + row * D + d) =
                 make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-            if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+            if (d == 0) a.lse[row] = log2_sum(m, l) * kLn2;
         }
     }
     if constexpr (MODE == kSolo) {
@@ -744,11 +752,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                     acc.w = fmaf(w, v[e].w, acc.w);
                 }
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;          // no keys at all
+            const float inv = reciprocal(l);
             const int64_t row = (int64_t)c.b * a.H + gq * a.G + hb * MH + h;
             *reinterpret_cast<uint2*>(a.O + row * D + d) =
                 make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-            if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+            if (d == 0) a.lse[row] = log2_sum(m, l) * kLn2;
         }
     }
 }
@@ -807,9 +815,9 @@ join_kernel(const Args a, int grid) {
         }
     }
     const int64_t row = (int64_t)b * a.H + h0 + h;
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no tiles: an empty sequence
+    const float inv = reciprocal(l);
     *reinterpret_cast<uint32_t*>(a.O + row * D + d) = pack_bf16(acc.x * inv, acc.y * inv);
-    if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (d == 0) a.lse[row] = log2_sum(m, l) * kLn2;
 }
 
 // Those of the tiles of a segment of sequence b; none: c1 < c0.
@@ -888,11 +896,11 @@ __device__ __forceinline__ void join_row(const Args& a, int grid, int64_t row) {
                 for (int v = 0; v < V; ++v) acc[v] = fmaf(w[z], x[z][v], acc[v]);
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no keys at all
+    const float inv = reciprocal(l);
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + row * D + lane * V);
     if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
     else *dst = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (lane == 0) a.lse[row] = log2_sum(m, l) * kLn2;
 }
 
 // Joins the parts of a shared prefix and of the sequences' own keys, a warp per row.
@@ -956,7 +964,7 @@ mass_kernel(const Args a, int grid, int joins, int blocks) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             }
-            if (lane == 0) s_lse[h] = m + __log2f(l);
+            if (lane == 0) s_lse[h] = weight_base(log2_sum(m, l));
         }
         __syncthreads();
         const float* score = a.score + row0 * a.stride;

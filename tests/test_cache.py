@@ -282,6 +282,45 @@ def test_step_masses_of_nans_and_scores_below_32_bits():
             assert torch.equal(a, b)
 
 
+# segments of one CTA each, by a cluster, cut by several CTAs, in two blocks of heads
+@pytest.mark.parametrize("case", [(90, 8, 4, 60, 64, 60, 0, [1 + i % 60 for i in range(90)]), (1, 4, 2, 700, 128, 200, 3, [640]),
+                                  (3, 8, 2, 6000, 128, 6000, 0, [6000, 64, 5000]), (1, 20, 1, 500, 64, 500, 0, [431]),
+                                  (40, 34, 2, 400, 128, 300, 5, [10 * i for i in range(40)])], ids=lambda c: "B{}H{}kv{}S{}D{}".format(*c))
+def test_step_of_a_head_whose_scores_are_all_below_32_bits(case):
+    """It draws nothing: O = 0, lse = -inf and no weight, whoever has its keys; the other heads' results stay."""
+    B, H, Hkv, S, D, window, n_sink, lens = case
+    q, k, v, n, m = poisoned(case, 16)
+    q[:, :, 0], k[..., 0] = 0, -2.0 ** 100
+    whole = dfa.dfa_attn_decode_mass(q, k, v, n, m, window, n_sink)
+    steps = dfa.dfa_attn_decode_sink(q, k, v, n, window, n_sink)
+    check_step(whole, case, q, k, v, m)
+    q[:, 1, 0] = 2.0 ** 100
+    others = [h for h in range(H) if h != 1]
+    for (O, lse), ref in ((dfa.dfa_attn_decode_mass(q, k, v, n, m, window, n_sink)[:2], whole), (dfa.dfa_attn_decode_sink(q, k, v, n, window, n_sink), steps)):
+        dfa.dfa_check_errors()
+        assert (O[:, 1] == 0).all() and (lse[:, 1] == -np.inf).all()
+        assert torch.equal(O[:, others], ref[0][:, others]) and torch.equal(lse[:, others], ref[1][:, others])
+    got = dfa.dfa_attn_decode_mass(q, k, v, n, None, window, n_sink)[2]
+    q[:, 1, 0], k[..., 0] = 0, 0                       # the weights of the other heads
+    w = cache.step_mass(np64(q), np64(k), lens, window, n_sink)
+    w[:, :1] -= cache.step_mass(np64(q[:, 1:2]), np64(k[:, :, :1]), lens, window, n_sink)
+    close(got, w, 2 * F * w + 1e-15, "mass")           # w is a difference of fp64 numbers of at most 1 per head and key
+
+
+def test_prefix_of_a_head_whose_scores_are_all_below_32_bits():
+    for B, H, Hkv, P, S, D, lens in ((3, 8, 2, 500, 20, 64, [20, 0, 7]), (5, 12, 4, 700, 400, 128, [400, 0, 64, 7, 399]), (2, 4, 2, 0, 30, 64, [30, 1])):
+        q, kp, vp, k, v = rand(96, B, H, D), rand(97, P, Hkv, D), rand(98, P, Hkv, D), rand(99, B, S, Hkv, D), rand(100, B, S, Hkv, D)
+        q[:, :, 0], kp[:, :, 0], k[..., 0] = 0, -2.0 ** 100, -2.0 ** 100
+        want = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens))
+        check_prefix(want, q, kp, vp, k, v, lens)
+        q[:, 1, 0] = 2.0 ** 100
+        O, lse = dfa.dfa_attn_decode_prefix(q, kp, vp, k, v, lens_of(lens))
+        dfa.dfa_check_errors()
+        assert (O[:, 1] == 0).all() and (lse[:, 1] == -np.inf).all()
+        others = [h for h in range(H) if h != 1]
+        assert torch.equal(O[:, others], want[0][:, others]) and torch.equal(lse[:, others], want[1][:, others])
+
+
 # ------------------------------------------------------------------------------------------------ a shared prefix
 # (B, H, Hkv, P, S, D, lens): one query tile of a head, two, three, many; few keys and many pieces; own rows from none on
 PREFIX = [
