@@ -359,8 +359,10 @@ dfa_status dfa_attn_decode_mass(const void* q, const void* k, const void* v, dfa
  *   mass_out: fp32 [B, H_kv, cap], the kept keys' masses, 0 behind them
  *   kept:     int32 [B, H_kv, keep], their positions in k and v, rising; -1 behind
  * keep >= 1, n_first, n_recent >= 0, n_first + n_recent <= keep.  No output may
- * overlap an input (from its first element to the end of its last one).  The heads of a sequence keep different positions, so a window
- * counted in rows (the calls above) means the last rows that were kept.  D in {64, 128}.
+ * overlap an input (from its first element to the end of its last one), nor another
+ * output; k_out and v_out may interleave in one buffer, without a common element.  The
+ * heads of a sequence keep different positions, so a window counted in rows (the calls
+ * above) means the last rows that were kept.  D in {64, 128}.
  * One or two launches, no workspace; may be captured. */
 dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt, int B, int H_kv, int S_max, int D,
                            const int64_t* kv_strides, const int32_t* kv_len, const float* mass, int keep, int n_first,

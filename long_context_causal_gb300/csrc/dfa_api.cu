@@ -1121,6 +1121,33 @@ dfa_status check_apart(std::initializer_list<Range> outs, std::initializer_list<
             if (overlap(o, i)) return fail(DFA_ERR_INVALID_ARG, "an output overlaps an input");
     return DFA_OK;
 }
+dfa_status check_apart(std::initializer_list<Range> outs) {
+    for (const Range* o = outs.begin(); o != outs.end(); ++o)
+        for (const Range* i = outs.begin(); i != o; ++i)
+            if (overlap(*o, *i)) return fail(DFA_ERR_INVALID_ARG, "an output overlaps another one");
+    return DFA_OK;
+}
+
+// Whether two tensors of these sizes and strides (n dimensions, the strides rising), t elements apart, with runs of D
+// elements share one: t = sum c_i stride_i + less than D in size, |c_i| < size_i.  A dimension has few c_i in reach of
+// what the smaller ones can add; `steps` counts them, for strides where that is not so (true then).
+struct Dim {
+    int64_t size, stride;
+};
+bool share(int64_t t, const Dim* d, int n, int D, int& steps) {
+    if (n == 0) return std::abs(t) < D;
+    const Dim& x = d[n - 1];
+    if (x.size <= 1) return share(t, d, n - 1, D, steps);
+    int64_t reach = D - 1;
+    for (int i = 0; i + 1 < n; ++i) reach += (d[i].size - 1) * d[i].stride;
+    const int64_t c0 = std::max(1 - x.size, (t - reach) / x.stride - 1), c1 = std::min(x.size - 1, (t + reach) / x.stride + 1);
+    for (int64_t c = c0; c <= c1; ++c) {
+        const int64_t left = t - c * x.stride;
+        if (std::abs(left) > reach) continue;
+        if (--steps < 0 || share(left, d, n - 1, D, steps)) return true;
+    }
+    return false;
+}
 size_t extent(int B, int L, int heads, int D, int64_t sb, int64_t ss, int64_t sh, int elt) {
     if (!B || !L || !heads) return 0;
     return (size_t)((B - 1) * sb + (L - 1) * ss + (heads - 1) * sh + D) * elt;
@@ -1214,12 +1241,20 @@ extern "C" dfa_status dfa_cache_evict(const void* k, const void* v, dfa_dtype dt
     if ((st = check_ptrs({k, v, k_out, v_out}))) return st;
     if (!aligned4({kv_len, mass, len_out, mass_out, kept}))
         return fail(DFA_ERR_INVALID_ARG, "kv_len, mass, len_out, mass_out and kept must be 4-byte aligned pointers");
-    if (k_out == v_out) return fail(DFA_ERR_INVALID_ARG, "k_out and v_out are the same memory");
     const size_t rows = (size_t)B * H_kv, in = extent(B, S_max, H_kv, D, p.in_sb, p.in_ss, p.in_sh, elt),
                  out = extent(B, cap, H_kv, D, p.out_sb, p.out_ss, p.out_sh, elt);
     if ((st = check_apart({{k_out, out}, {v_out, out}, {len_out, 4 * (size_t)B}, {mass_out, 4 * rows * cap}, {kept, 4 * rows * keep}},
                           {{k, in}, {v, in}, {kv_len, 4 * (size_t)B}, {mass, 4 * rows * S_max}})))
         return st;
+    const Range ko{k_out, out}, vo{v_out, out}, lo{len_out, 4 * (size_t)B}, mo{mass_out, 4 * rows * cap}, at{kept, 4 * rows * keep};
+    if ((st = check_apart({ko, lo, mo, at})) || (st = check_apart({vo, lo, mo, at}))) return st;
+    if (overlap(ko, vo)) {           // side by side in one buffer, as two slices of it
+        Dim d[] = {{B, p.out_sb}, {cap, p.out_ss}, {H_kv, p.out_sh}};
+        std::sort(std::begin(d), std::end(d), [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+        int steps = 1 << 12;
+        if (share((static_cast<const char*>(v_out) - static_cast<const char*>(k_out)) / elt, d, 3, D, steps))
+            return fail(DFA_ERR_INVALID_ARG, "k_out and v_out share the same memory");
+    }
     return cache_evict(p, k, v, kv_len, mass, k_out, v_out, len_out, mass_out, kept, static_cast<cudaStream_t>(stream));
 }
 

@@ -507,6 +507,28 @@ def test_evict_strides_types_and_lengths_out_of_range():
     check_evict(dfa.dfa_cache_evict(shared, shared, n, m, keep, 2, 9), shared, shared, m, lens, (B, Hkv, S, D, keep, keep, 2, 9, lens))
 
 
+def test_evict_into_two_slices_of_one_buffer():
+    """k_out and v_out side by side, whatever dimension they share; none of these has a common element."""
+    B, Hkv, S, D, keep, cap = 2, 2, 200, 64, 30, 32
+    k, v, m = rand(49, B, S, Hkv, D), rand(50, B, S, Hkv, D), rand(51, B, Hkv, S, dtype=torch.float32)
+    lens = [200, 20]
+    pool = lambda *s: torch.full(s, 7, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    pairs = [(x[:, :cap], x[:, cap:]) for x in [pool(B, 2 * cap, Hkv, D)]] + [(x[:, ::2], x[:, 1::2]) for x in [pool(B, 2 * cap, Hkv, D)]] + \
+        [(x[:, :, ::2], x[:, :, 1::2]) for x in [pool(B, cap, 2 * Hkv, D)]] + [(x[..., :D], x[..., D:]) for x in [pool(B, cap, Hkv, 2 * D)]] + \
+        [(x[:B], x[B:]) for x in [pool(2 * B, cap, Hkv, D)]] + [(x[::2], x[1::2]) for x in [pool(2 * B, cap, Hkv, D)]] + \
+        [(x[:, 0:2 * cap:2], x[:, 5:5 + 2 * cap:2]) for x in [pool(B, 2 * cap + 5, Hkv, D)]] + \
+        [(x[:, 1].permute(1, 2, 0, 3), x[:, 0].permute(1, 2, 0, 3)) for x in [pool(Hkv, 2, B, cap, D)]]
+    for ko, vo in pairs:
+        got = dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, 2, 3, ko, vo)
+        check_evict(got, k, v, m, lens, (B, Hkv, S, D, keep, cap, 2, 3, lens), 7)
+    x = pool(B, 2 * cap, Hkv, D)
+    for ko, vo in ((x[:, :cap], x[:, cap - 1:-1]), (x[:, ::2], x[:, ::2]), (x[:, 4:4 + cap], x[:, 1:1 + cap])):
+        with pytest.raises(dfa.DfaError, match="same memory"):
+            dfa.dfa_cache_evict(k, v, lens_of(lens), m, keep, 2, 3, ko, vo)
+    assert (x == 7).all()
+    dfa.dfa_check_errors()
+
+
 def test_evict_from_a_cache_beyond_32_bits():
     B, Hkv, S, D, keep = 3, 8, (1 << 20) + 5, 128, 300
     k, v = (torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(46 + i)) for i in range(2))

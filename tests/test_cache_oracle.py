@@ -187,6 +187,13 @@ CACHE = 2 * 2 * 300 * 3 * 128        # bytes of k
     (dict(lo=A + 2), dfa.DFA_ERR_INVALID_ARG), (dict(m=None), dfa.DFA_ERR_INVALID_ARG), (dict(vo=FAR[4]), dfa.DFA_ERR_INVALID_ARG),
     (dict(ko=FAR[0]), dfa.DFA_ERR_INVALID_ARG), (dict(vo=FAR[0] + CACHE - 16), dfa.DFA_ERR_INVALID_ARG),
     (dict(lo=FAR[2]), dfa.DFA_ERR_INVALID_ARG), (dict(mo=FAR[3]), dfa.DFA_ERR_INVALID_ARG), (dict(kept=FAR[3]), dfa.DFA_ERR_INVALID_ARG),
+    # outputs among each other: small ones; slices of one buffer a row, a head, a few elements or a sequence apart
+    (dict(kept=FAR[7] + 8), dfa.DFA_ERR_INVALID_ARG), (dict(lo=FAR[8] + 4 * 2 * 3 * 40 - 4), dfa.DFA_ERR_INVALID_ARG), (dict(lo=FAR[7]), dfa.DFA_ERR_INVALID_ARG),
+    (dict(mo=FAR[4]), dfa.DFA_ERR_INVALID_ARG), (dict(kept=FAR[5] + 64), dfa.DFA_ERR_INVALID_ARG), (dict(lo=FAR[5] + 4), dfa.DFA_ERR_INVALID_ARG),
+    *[(dict(vo=FAR[4] + 2 * d), dfa.DFA_ERR_INVALID_ARG) for d in (8, 128, 384, 10 * 384, 64 * 384)],
+    *[(dict(ko=FAR[5] + 2 * d, vo=FAR[5], os=s3(130 * 400, 400, 128)), dfa.DFA_ERR_INVALID_ARG) for d in (16, 120, 63 * 400, 130 * 400 + 63 * 400 + 256 + 120)],
+    (dict(vo=FAR[4] + 2 * 3 * 800, os=s3(64 * 400, 400, 128), B=1, cap=128), dfa.DFA_ERR_INVALID_ARG),
+    (dict(vo=FAR[4] + 2 * (1 << 16), os=s3(8, 8, 8), Hkv=64, cap=1 << 20, S=64, B=64), dfa.DFA_ERR_INVALID_ARG),
 ])
 def test_evict_refusals(kw, code):
     assert evict(**kw) == code and dfa.dfa_last_error()
