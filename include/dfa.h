@@ -331,7 +331,8 @@ dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dty
  *   mass_out[b, g, j] = 0                                         for j >= n.
  *   mass:     fp32 [B, H_kv, S_max], finite or not, read for j < n only; NULL: zero
  *   mass_out: fp32 [B, H_kv, S_max]; may be `mass` itself, else it does not
- *             overlap an input
+ *             overlap an input.  O, lse and mass_out do not overlap one another, nor
+ *             O and lse `mass`
  *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as below
  * Everything else as dfa_attn_decode_sink (whose O and lse may differ in the
  * last bits: the keys are cut elsewhere).  One or two launches; the same bits on every call. */

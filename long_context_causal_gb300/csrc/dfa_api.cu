@@ -1210,7 +1210,9 @@ extern "C" dfa_status dfa_attn_decode_mass(const void* q, const void* k, const v
     const size_t cache = extent(B, S_max, H_kv, D, p.kv_sb, p.kv_ss, p.kv_sh, 2), masses = sizeof(float) * (size_t)B * H_kv * S_max;
     if ((st = check_apart({{mass_out, masses}}, {{k, cache}, {v, cache}, {q, 2 * (size_t)B * H * D}, {kv_len, sizeof(int) * (size_t)B}})))
         return st;
-    if (mass && mass != mass_out && (st = check_apart({{mass_out, masses}}, {{mass, masses}}))) return st;
+    const Range out_O{O, 2 * (size_t)B * H * D}, out_lse{lse, sizeof(float) * (size_t)B * H};
+    if ((st = check_apart({{mass_out, masses}, out_O, out_lse}))) return st;
+    if (mass && mass != mass_out && (st = check_apart({{mass_out, masses}, out_O, out_lse}, {{mass, masses}}))) return st;
     return sink_decode(p, q, k, v, kv_len, O, lse, mass, mass_out, workspace, static_cast<cudaStream_t>(stream));
 }
 

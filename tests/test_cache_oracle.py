@@ -111,6 +111,9 @@ def test_mass_of_nothing_and_size_queries():
     (dict(ks=(ctypes.c_int64 * 3)(0, 256, 128)), dfa.DFA_ERR_INVALID_ARG),
     (dict(mo=FAR[4] + 4), dfa.DFA_ERR_INVALID_ARG), (dict(mo=FAR[1] + 2 * 2 * 300 * 256 - 4), dfa.DFA_ERR_INVALID_ARG),
     (dict(mo=FAR[3] + 4), dfa.DFA_ERR_INVALID_ARG), (dict(ws=None), dfa.DFA_ERR_WORKSPACE), (dict(ws=MIS), dfa.DFA_ERR_INVALID_ARG),
+    (dict(lse=FAR[7] + 4), dfa.DFA_ERR_INVALID_ARG), (dict(lse=FAR[7] + 4 * 2 * 2 * 300 - 4, m=None), dfa.DFA_ERR_INVALID_ARG),
+    (dict(O=FAR[7]), dfa.DFA_ERR_INVALID_ARG), (dict(mo=FAR[5] + 2 * 2 * 4 * 128 - 4), dfa.DFA_ERR_INVALID_ARG),
+    (dict(lse=FAR[5] + 8), dfa.DFA_ERR_INVALID_ARG), (dict(lse=FAR[4] + 8), dfa.DFA_ERR_INVALID_ARG), (dict(O=FAR[4] + 16), dfa.DFA_ERR_INVALID_ARG),
     (dict(wn=dfa.dfa_attn_decode_mass_workspace_size(2, 4, 2, 300, 128, 64, 4) - 1), dfa.DFA_ERR_WORKSPACE)])
 def test_decode_mass_refusals(kw, code):
     assert decode_mass(**kw) == code and dfa.dfa_last_error()
