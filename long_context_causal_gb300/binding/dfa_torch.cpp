@@ -144,6 +144,14 @@ Stream stream_of(PyObject* o, int dev) {
         n = o;
         Py_INCREF(n);
     } else {
+        // A handle says nothing of its device; a stream object does, and the tensors are on the current one.
+        PyObject* at = PyObject_GetAttrString(o, "device_index");
+        if (!at) PyErr_Clear();
+        const long index = at ? PyLong_AsLong(at) : dev;
+        Py_XDECREF(at);
+        if (index == -1 && PyErr_Occurred()) throw Raised{};
+        if (index != dev)
+            throw ValueErr{"the stream is on cuda:" + std::to_string(index) + ", the current device is cuda:" + std::to_string(dev)};
         n = PyObject_GetAttrString(o, "cuda_stream");
         if (!n) throw Raised{};
     }

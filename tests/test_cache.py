@@ -842,3 +842,31 @@ def test_what_the_binding_refuses_on_the_gpu():
         dfa.dfa_attn_mass(rand(7, B, S, H, D), k, torch.zeros(B, H, S, device=DEV), n_last=0)
     assert dfa.dfa_attn_mass(rand(7, B, S, H, D), k, torch.zeros(B, H, S, device=DEV), n_last=1 << 30).shape == (B, Hkv, S)
     dfa.dfa_check_errors()
+
+
+def test_a_stream_of_another_device_is_refused_by_the_binding():
+    """By every call that it marshals, before anything is allocated or launched (a stand-in: there may be one device)."""
+    class Elsewhere:
+        device_index, cuda_stream = torch.cuda.current_device() + 1, torch.cuda.current_stream().cuda_stream
+
+    class Here:
+        device_index, cuda_stream = torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+
+    B, H, Hkv, S, D = 2, 4, 2, 40, 64
+    q, k, n, m, qs, lse = rand(1, B, H, D), rand(2, B, S, Hkv, D), lens_of([9, 9]), torch.zeros(B, Hkv, S, device=DEV), rand(3, B, S, H, D), torch.zeros(B, H, S, device=DEV)
+    kept = dfa.dfa_ckpt8_save(qs, k, k, qs)
+    calls = [lambda s: dfa.dfa_attn_mass(qs, k, lse, stream=s), lambda s: dfa.dfa_attn_decode_mass(q, k, k, n, m, stream=s),
+             lambda s: dfa.dfa_cache_evict(k, k, n, m, 10, stream=s), lambda s: dfa.dfa_attn_decode_prefix(q, k[0], k[0], k, k, n, stream=s),
+             lambda s: dfa.dfa_attn_decode_sink(q, k, k, n, 8, stream=s), lambda s: dfa.dfa_attn_fwd_sink(qs, k, k, 8, stream=s),
+             lambda s: dfa.dfa_attn_bwd_sink(qs, k, k, qs, lse, qs, 8, stream=s), lambda s: dfa.dfa_ckpt8_save(qs, k, k, qs, stream=s),
+             lambda s: dfa.dfa_ckpt8_restore(kept, B, S, H, Hkv, D, stream=s), lambda s: dfa.dfa_attn_bwd_ckpt8(kept, lse, qs, Hkv, 8, stream=s)]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for call in calls:
+        with pytest.raises(ValueError, match="the stream is on cuda:"):
+            call(Elsewhere)
+    assert torch.cuda.memory_allocated() == before
+    for s in (Here, torch.cuda.current_stream(), Here.cuda_stream, torch.cuda.Stream()):
+        assert torch.equal(calls[0](s), calls[0](None))
+        torch.cuda.synchronize()
+    dfa.dfa_check_errors()
