@@ -488,6 +488,20 @@ def test_evict_rows_that_do_not_begin_on_16_bytes(S, dtype):
             check_evict(got, k, v, m, lens, (3, Hkv, S, D, keep, keep + 1, n_first, n_recent, lens), 7)
 
 
+@pytest.mark.parametrize("S", [16384, 32767, 65536, 131071, 131073])
+def test_evict_long_rows_that_do_not_begin_on_16_bytes(S):
+    """The same where a CTA, two, four or eight of a cluster hold a row but for the keys that its misalignment pushes out."""
+    Hkv, D, keep = 2, 64, 700
+    k, v = rand(38, 1, S, Hkv, D), rand(39, 1, S, Hkv, D)
+    flat = torch.exp(3 * rand(40, Hkv * S + 3, dtype=torch.float32)).clamp(max=50)      # the border among equal ones
+    for off in (0, 1, 3):
+        m = flat[off:off + Hkv * S].view(1, Hkv, S)
+        ko, vo = (torch.full((1, keep, Hkv, D), 7, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        got = dfa.dfa_cache_evict(k, v, lens_of([S]), m, keep, 2, 9, ko, vo)
+        dfa.dfa_check_errors()
+        check_evict(got, k, v, m, [S], (1, Hkv, S, D, keep, keep, 2, 9, [S]), 7)
+
+
 def test_evict_strides_types_and_lengths_out_of_range():
     B, Hkv, S, D, keep, cap = 3, 2, 300, 128, 50, 60
     lens = [0, 250, 300]
