@@ -312,7 +312,8 @@ dfa_status dfa_attn_decode_prefix(const void* q, const void* k_prefix, const voi
  * i and j as in dfa_attn_fwd_sink with the same window and n_sink (window >= S,
  * n_sink = 0: plain causal attention, after dfa_attn_fwd).  n_last >= 1 (above S: S):
  * how many of the last queries count.  q, k [B, S, heads, D] dense, bf16; lse fp32
- * [B, H, S], rows before S - n_last are not read; a row with lse = -inf counts for nothing.
+ * [B, H, S], rows before S - n_last are not read; a row with lse = -inf counts for nothing
+ * (where its scores are neither NaN nor +inf).
  *   mass:      fp32 [B, H_kv, S], 0 for keys that none of the queries sees; overlaps
  *              no input
  *   workspace: >= dfa_attn_mass_workspace_size() bytes, 16-byte aligned, contents
@@ -333,7 +334,9 @@ dfa_status dfa_attn_mass(const void* q, const void* k, const float* lse, dfa_dty
  *   mass_out: fp32 [B, H_kv, S_max]; may be `mass` itself, else it does not
  *             overlap an input.  O, lse and mass_out do not overlap one another, nor
  *             O and lse `mass`
- *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as below
+ *   workspace: >= dfa_attn_decode_mass_workspace_size() bytes, as above; it holds the
+ *             scores, 4 bytes for each query head and each of the S_max keys (of those a
+ *             window and its sinks can cover): 1 GB for 32 sequences, 64 heads, 128K keys
  * Everything else as dfa_attn_decode_sink (whose O and lse may differ in the
  * last bits: the keys are cut elsewhere).  One or two launches; the same bits on every call. */
 size_t dfa_attn_decode_mass_workspace_size(int B, int H, int H_kv, int S_max, int D, int window, int n_sink);

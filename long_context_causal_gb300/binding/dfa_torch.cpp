@@ -167,7 +167,9 @@ c10::cuda::CUDAStream torch_stream(const Stream& s, const at::Device& dev) {
 
 // A new tensor is owned by the stream the call runs on: the allocator hands out
 // its memory again only behind the call's kernels, and took it from no work that
-// another stream has still to do.
+// another stream has still to do.  Made below torch's dispatcher: its modes do not see
+// the tensor, and its filling of new memory under deterministic algorithms does not take
+// place; every element is written by the call (or zeroed, new_cache()).
 at::Tensor allocate(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev, const Stream& s) {
     const NoGil released;
     if (!s.other) return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));

@@ -16,11 +16,11 @@
 //
 // copy_kernel moves the rows: bound by HBM (each kept row read and written once).
 //
-// What it takes: 8 x 8 rows of up to 16384 keys to 4096, D = 128, 50.3 us a call (265 MB,
-// 5.3 TB/s, 78% of the copy rate): 36 the copy, 9 the choice on 64 of the SMs -- latency of
-// the dependent passes, 32 warps each with barriers between; one prompt of 131072 keys to
-// 16384 37.4 us (140 MB): 19 and 15, of which three digits' exchanges through distributed
-// shared memory are half.  The masses are read once while a row fits the threads.
+// What it takes: 8 x 8 rows of up to 16384 keys to 4096, D = 128, 50.3 to 50.5 us a call (265 MB,
+// 5.3 TB/s, 78% of the copy rate; D = 64 32.7, 4.1 TB/s): 36 the copy, 9 the choice on 64 of the
+// SMs -- latency of the dependent passes, 32 warps each with barriers between; one prompt of 131072
+// keys to 16384 36.9 to 38.0 us (140 MB; D = 64 29): 19 and 15, of which three digits' exchanges
+// through distributed shared memory are half.  The masses are read once while a row fits the threads.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -352,15 +352,19 @@ copy_kernel(const CopyArgs a, int blocks) {
 }  // namespace
 
 // Rows of up to this many 16-byte units (keys; the values as many) are moved by the CTA that chose them: one launch.
+// GPU time in one launch and in two: 2048 units a row, 8 rows of 501 keys 7.0 and 7.2 us, 256 rows of 4000 14.4 and
+// 15.1; 4096 units 9.0 and 8.2, 17.8 and 18.9; 8192 units, 8 rows of 4000 11.6 and 8.2, 256 of them 30.4 and 31.3.
 constexpr int kMoveUnits = 4096;
 
 dfa_status cache_evict(const EvictProblem& p, const void* k, const void* v, const int32_t* kv_len, const float* mass,
                        void* k_out, void* v_out, int32_t* len_out, float* mass_out, int32_t* kept, cudaStream_t s) {
     const Args a{p.Hkv, p.S, p.keep, p.cap, p.n_first, p.n_recent, kv_len, mass, len_out, mass_out, kept};
     const int rows = p.B * p.Hkv;
-    // A row to a CTA while its threads hold the keys: 8 x 8 rows of 16384 keys 53 us with the copy, by two CTAs each 59,
-    // by eight 107 (their barriers and 3.5 times as many CTAs as SMs); 8 rows of 131072 by one 99 (chunks), by four 61,
-    // by eight 42.  Rows of 501 keys with 4 keys a thread 10.3, 16 a thread 14.3.
+    // A row to a CTA while its threads hold the keys, GPU time with the copy: 8 x 8 rows of up to 16384 keys 50.1 us, by
+    // two CTAs each 53.7, by eight 95 (their barriers and 3.5 times as many CTAs as SMs); 8 rows of 16384 12.7 and 17.3.
+    // Longer rows by as many as hold them: 8 rows of 32768 by one 25.3 (chunks), by two 17.6, by eight 19.4; of 131072 by
+    // one 83, by four 50, by eight 34.7.  Four keys a thread while that holds a row: 501 keys, two launches 7.5, 16 a
+    // thread 11.2.
     int log_c = 0;
     while ((1 << log_c) < kMaxCluster && p.S > (kThreads * 16 << log_c)) ++log_c;
     const int unit = 16 / p.elt;

@@ -18,8 +18,10 @@
 // alone lets a sub-partition do a tile's 32 rows in 632 cycles with four warps; in the
 // kernel a step of four tiles takes 3030 (tensor cores 66% busy, exponentials 66%, issue
 // slots 52%), set by the sub-partition that also has the issuing warp.  32K tokens, 32/8
-// heads, D = 128, window 4096, 4 sinks: 827 to 851 us (1210 to 1250 TFLOP/s); 2 x 5003
-// tokens causal, 16/2 heads, 80 to 83 us (1240).  With three quarters of the products left
+// heads, D = 128, window 4096, 4 sinks: 827 to 862 us (1200 to 1250 TFLOP/s); 2 x 5003
+// tokens causal, 16/2 heads, 80 to 83 us (1240).  At D = 64 the products are half and the
+// exponentials the same: 721 and 75 us, exponentials 70% busy, tensor cores 35%, issue slots
+// 55% (the exponentials alone would take 400 and 40 us at the highest clock).  With three quarters of the products left
 // out 720 us, without the loads of the queries' log-sum-exps 792, with half of the
 // exponentials 779: no unit alone.  Measured and not kept: two warpgroups that hold a
 // tile's 128 scores each 974 (too few warps to hide the latencies); scores loaded ahead
@@ -37,9 +39,7 @@
 // first step without a table.  A block that one CTA sweeps whole is written there;
 // of the others each CTA leaves 512 sums, which a second kernel adds up in the
 // order of the steps.  No atomics: the same bits on every call.  With few blocks (rule at
-// launch()) a cluster shares a block's steps instead: 2 x 301 tokens 8.2 us, 10.2
-// with the second launch (5.4 since a call's first kernel is set up while the one before
-// it ends).
+// launch()) a cluster shares a block's steps instead, in one launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -517,8 +517,8 @@ join_kernel(const Args a, int grid) {
 // P of the four TMEM regions, so 4 / P tiles are in work at a time; a warpgroup adds
 // up a region, and the P sums of a key meet in shared memory, in their order.
 //
-// The last 64 queries of 32K tokens, 32/8 heads, D = 128: 19.4 us a call (68.7 MB at 3.5
-// TB/s, half of the copy rate; 42 by blocks of 512 keys as above).  A tile of keys takes
+// The last 64 queries of 32K tokens, 32/8 heads, D = 128: 19.4 to 20.1 us a call (68.7 MB at 3.4
+// to 3.5 TB/s, half of the copy rate; 42 by blocks of 512 keys as above; D = 64 18.7).  A tile of keys takes
 // 1770 cycles where HBM would bring one in 1400: as above, the arithmetic of the weights
 // (1024 cycles of exponentials).  The 14 tiles of a CTA are 12.5 us of it, 4 us pass
 // until the first tile of keys is there.  Measured and not kept: the queries by plain loads
@@ -880,7 +880,9 @@ dfa_status launch(const SinkProblem& p, int n_last, const void* q, const void* k
         mark_on_device(seen);
     }
     // One round of clusters, if the longest of their shares is not longer than an equal share of all SMs and the second
-    // launch (kJoinSteps).
+    // launch (kJoinSteps).  GPU time by clusters and by all SMs: 2 x 301 tokens, 8/4 heads, 6.0 and 7.7 us (D = 64 5.5 and
+    // 7.3); 700 tokens, 8/8 heads, 8.9 both; 1000 tokens, 8/2 heads, the longest shares that the rule lets through, 11.3
+    // and 10.3; 2000 tokens, left to all SMs, 16.9 and 14.0.
     const int64_t segments = (int64_t)p.B * p.Hkv * a.n_kb;
     int64_t longest = 0;
     if (segments <= clusters.load())

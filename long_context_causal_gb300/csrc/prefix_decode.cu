@@ -21,7 +21,8 @@
 // the softmax chain as in the forward.  48 sequences of 4 heads a group (192 rows) behind
 // 32768 keys, 8 kv heads, D = 128: 28 to 30 us (134 MB, 4.6 TB/s); 128 sequences of 8 heads
 // a group (1024 rows) behind 16384: 48 us (1430 TFLOP/s; tensor cores 47% busy under cold
-// caches).  Waits of the issuing warp by polling: 1% slower on both.
+// caches; at D = 64 29%, as busy as the exponentials: the chain of product, softmax, product).
+// Waits of the issuing warp by polling: 1% slower on both.
 //
 // The kernel of the own keys is let go at once (launch_dependents) and takes the SMs as
 // this one leaves them.
@@ -407,7 +408,10 @@ PrefixPlan prefix_plan(int B, int G, int Hkv, int P, int sms) {
     p.n_kt = (P + BN - 1) / BN;
     p.n_seg = Hkv * p.n_pairs;
     p.steps = (int64_t)p.n_seg * p.n_kt;
-    // A multiple of the segments where that uses most SMs: no CTA has two pieces then.
+    // A multiple of the segments where that uses nine tenths of the SMs: no CTA has two pieces then.  Calls with it and
+    // with all SMs: 10 segments on 150 CTAs 35.3 and 38.9 us (16384 keys, 128 rows a head; D = 64 22.4 and 25.6), 12 on 144
+    // 41.3 and 46.1 (30.2 and 31.8), 24 on 144 39.9 and 41.5 (25.5 and 27.1), 4 on 144 42.2 both (34.1 and 33.8).  Fewer SMs
+    // may pay or not: 32 segments on 128 78.7 and 81.7 us, at D = 64 64.2 and 61.6.
     p.grid = (int)std::min<int64_t>(sms, p.steps);
     const int even = sms / p.n_seg * p.n_seg;
     if (p.steps > even && even * 10 >= sms * 9) p.grid = even;

@@ -37,12 +37,12 @@
 // at the end only: the consumers write the scores down, 4 bytes a head beside the 512
 // of a key and value (D = 128; 3% more at 4 heads a group), and the launch that joins
 // the outputs turns them into weights.  K and V are loaded to make room first, so the
-// scores are still in the L2 then: 32 sequences of up to 16384 keys, 32/8 heads, 178 us
-// a call (1.10 GB at 6140 GB/s, 91% of the copy rate), of which 165 are the cache and
+// scores are still in the L2 then: 32 sequences of up to 16384 keys, 32/8 heads, 178 to 183 us
+// a call (1.10 GB at 6000 to 6140 GB/s, 91% of the copy rate; D = 64 136, 4.1 TB/s), of which 165 are the cache and
 // 11 the masses; 195 before the cache policy and with 1024 keys a block, 219 with a
 // launch of its own for the masses and short sequences counted by their tiles alone.
 // In a cluster (one sequence of 1501 keys) the scores stay in shared memory and the CTA
-// that has them forms the weights: 6.3 us of GPU time, 9.3 by two launches.
+// that has them forms the weights: 6.3 to 6.5 us of GPU time, 8.9 to 9.3 by two launches.
 //
 // Behind a shared prefix (kParts, kSolo).  The same kernel over the sequences' own keys,
 // started beside prefix_decode.cu's and leaving fp32 parts, which prefix_join_kernel adds
@@ -52,7 +52,7 @@
 // than their keys when the tiles are dealt: with tiles alone the CTA of the shortest ones
 // ran 123 us, the others 46.  Where the own keys are few (at most four tiles, a segment per
 // SM at most) a CTA takes a segment and adds the prefix's parts itself: 4 sequences behind
-// 1000 keys 7.5 us of GPU time; 10.7 with the launch that joins, 9.0 with a part's place
+// 1000 keys 7.5 to 7.8 us of GPU time; 10.7 with the launch that joins, 9.0 with a part's place
 // worked out once the prefix is there and four parts asked for at a time.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -1042,6 +1042,10 @@ constexpr int most_smem() {
 }
 
 // The prefix's part, the own keys' part beside it, and the join; or a CTA per segment of own keys that joins as well.
+// The second while the caches have room for at most four tiles (the host does not know the lengths) and an SM takes a
+// segment at most.  GPU time by it and by the first, 4 sequences, 32/8 heads, behind 1000 keys: 64 own keys 7.7 and 10.5
+// us, 256 7.7 and 12.3; 16 sequences of 256 11.4 and 16.1; behind 16000 19.3 and 26.8; D = 64 6.8 and 9.6, 6.8 and 11.3.
+// With more room the second was still ahead, by less for each tile: 4 x 512 own keys 8.6 and 13.7, 4 x 1024 12.1 and 14.8.
 constexpr int kSoloTiles = 4;
 template <int D>
 dfa_status launch_prefix(const DecodeProblem& p, int P, const void* q, const void* kp, const void* vp, int64_t ss, int64_t sh,
@@ -1145,7 +1149,8 @@ dfa_status launch(const DecodeProblem& p, const void* q, const void* k, const vo
         mark_on_device(seen);
     }
     // One round of clusters, each with tiles enough for its share of the SMs: 4096 keys of 8 kv
-    // heads 8.2 us, spread over all SMs 8.9; 8192 keys 12.1 and 10.8; 262 keys 4.2 and 6.0.
+    // heads 8.2 us, spread over all SMs 8.9; 8192 keys 12.1 and 10.8; 262 keys 4.2 and 6.0.  With masses, GPU time: 262
+    // keys 5.4 and 7.7, 1501 6.5 and 8.9, 4096 9.1 and 11.9 (D = 64 7.6 and 13.7); 4096 of one kv head 8.8 and 12.6.
     if (segments <= clusters.load() && decode_tiles(p) <= kClusterTiles) {
         cfg.gridDim = dim3((unsigned)(segments * kCluster));
         if (MASS) cfg.numAttrs = 2;
